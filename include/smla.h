@@ -78,6 +78,8 @@ enum smla_status {
                                        with SMLA_DEBUG) only: a computed shared-memory
                                        address or gathered row fell outside its buffer;
                                        the access was skipped */
+  SMLA_ERR_POOL_EXHAUSTED = -11,    /* device status: a cache call found no free page for
+                                       an entry, which it left unmapped */
 };
 
 /* Problem description shared by the entry points. */
@@ -240,12 +242,156 @@ int sparse_mla_decode_noalloc(const void* q, const void* kv_cache, const int32_t
  */
 int smla_test_inject_fault(int32_t block);
 
+/* ------------------------------------------------------------------------------------
+ * The paged cache: writing it, managing its pages, attending from new tokens over it.
+ *
+ * A pool of num_pages pages of page_size rows each (row r of page p is pool row
+ * p * page_size + r, in the 584-byte format above, kv_row_stride bytes apart); a block
+ * table int32 [num_seqs, max_pages] of page ids (< 0 = unmapped); the cached tokens of
+ * each sequence int32 kv_lens [num_seqs]; and, for the calls that take or give pages,
+ * the owners of each page int32 ref_count [num_pages].  A page is free exactly when its
+ * count is 0; allocation takes the lowest-numbered free pages, so results do not depend
+ * on timing.  All of it lives on the device and is read there, so a captured graph
+ * follows new lengths and tables.  Pages of a pool that is also a kv_cache of the
+ * decode calls stay valid for them.
+ * ---------------------------------------------------------------------------------- */
+typedef struct smla_cache_params {
+  int32_t num_pages;      /* pages in the pool, 1 .. 2^31 / page_size                   */
+  int32_t page_size;      /* rows per page, >= 1                                        */
+  int32_t num_seqs;       /* rows of block_table, 1 .. 65535                            */
+  int32_t max_pages;      /* columns of block_table, >= 1                               */
+  int64_t kv_row_stride;  /* bytes between consecutive rows, >= 584, multiple of 8      */
+} smla_cache_params;
+
+/*
+ * Quantises new tokens and writes their rows.  Sequence b's new tokens are the entries
+ * cu_q[b] .. cu_q[b + 1] - 1 of kv; kv_lens[b] counts them already, so entry
+ * cu_q[b] + j of n = cu_q[b + 1] - cu_q[b] lands at position kv_lens[b] - n + j.
+ *   kv        bf16 [total_tokens, 512] (448 nope | 64 rope), kv_token_stride elements
+ *             apart (>= 512, a multiple of 8), 16-byte aligned
+ *   kv_pages  the pool, 8-byte aligned;  cu_q int32 [num_seqs + 1], nondecreasing
+ * A group of 64 nope values with largest magnitude a gets the scale 2^e, e the least
+ * integer with a <= 448 * 2^e (byte e + 127, kept in 1 .. 254; 127 where a = 0), and the
+ * values x * 2^-e rounded to e4m3 (to nearest, ties to even); the padding byte is 0 and
+ * the rope is copied.  Infinities and NaN become e4m3 NaN, the scale is that of the
+ * group's finite values, and SMLA_ERR_RANGE is recorded.  A token whose position is
+ * negative, past the table, or on an unmapped page is not written
+ * (SMLA_ERR_INDEX_RANGE).  Entries of kv outside [cu_q[0], cu_q[num_seqs]) are ignored,
+ * as are rows that no token lands on.  No two tokens of a call may share a position's
+ * row.  total_tokens 0 is allowed (nothing is launched).
+ */
+int smla_cache_append(const void* kv, int64_t kv_token_stride, int32_t total_tokens,
+                      void* kv_pages, const int32_t* block_table, const int32_t* cu_q,
+                      const int32_t* kv_lens, const smla_cache_params* c, smla_stream_t stream);
+
+/* Workspace bytes of smla_cache_reserve, _fork and _compact (256-byte aligned; contents
+ * on entry do not matter; calls whose kernels may overlap need one each). */
+int smla_cache_workspace_size(const smla_cache_params* c, size_t* bytes);
+
+/*
+ * Maps pages until sequence r holds target_lens[r] tokens: every unmapped entry among
+ * the first ceil(target_lens[r] / page_size) of row r gets the next free page (in the
+ * order of the table, row by row) with count 1.  Mapped entries stay, kv_lens is not
+ * touched.  A target past the table is cut to it (SMLA_ERR_INDEX_RANGE); entries that
+ * find no free page stay unmapped (SMLA_ERR_POOL_EXHAUSTED).
+ */
+int smla_cache_reserve(int32_t* ref_count, int32_t* block_table, const int32_t* target_lens,
+                       const smla_cache_params* c, void* workspace, size_t workspace_bytes,
+                       smla_stream_t stream);
+
+/*
+ * Makes row children[i] a copy of row parents[i], i < n: full pages are shared (count
+ * + 1), a last page that is partly filled (kv_lens % page_size rows) is copied into the
+ * next free page (in list order), entries behind it are unmapped, and the length is the
+ * parent's.  The child's row is overwritten, not freed: free it first.  Children are
+ * distinct and none is a parent in the same call.  A pair with an id outside
+ * [0, num_seqs), with child == parent, or whose parent's length does not fit the table
+ * is skipped (SMLA_ERR_INDEX_RANGE); a child that finds no free page is left empty
+ * (SMLA_ERR_POOL_EXHAUSTED).  0 <= n <= num_seqs.
+ */
+int smla_cache_fork(void* kv_pages, int32_t* ref_count, int32_t* block_table, int32_t* kv_lens,
+                    const int32_t* parents, const int32_t* children, int32_t n,
+                    const smla_cache_params* c, void* workspace, size_t workspace_bytes,
+                    smla_stream_t stream);
+
+/*
+ * Empties rows[0 .. n - 1]: the count of every mapped page goes down by 1, the entries
+ * become -1 and the length 0.  The same row twice counts once.  Row ids outside
+ * [0, num_seqs), page ids past the pool and counts that are 0 already are skipped
+ * (SMLA_ERR_INDEX_RANGE).  n >= 0.
+ */
+int smla_cache_free(int32_t* ref_count, int32_t* block_table, int32_t* kv_lens,
+                    const int32_t* rows, int32_t n, const smla_cache_params* c,
+                    smla_stream_t stream);
+
+/*
+ * Moves the pages in use to the front of the pool: with u pages in use, the i-th page in
+ * use at or past u (ascending) moves to the i-th free page below u, whole pages, and
+ * counts and table follow.  ref_count_out and block_table_out may be their inputs (in
+ * place) or other buffers; info int32 [2] receives u and the number of moved pages.
+ * Moved pages' old rows keep their bytes.  Table entries past the pool, or that name
+ * a free page, are copied as they are (SMLA_ERR_INDEX_RANGE).
+ */
+int smla_cache_compact(void* kv_pages, const int32_t* ref_count, const int32_t* block_table,
+                       int32_t* ref_count_out, int32_t* block_table_out, int32_t* info,
+                       const smla_cache_params* c, void* workspace, size_t workspace_bytes,
+                       smla_stream_t stream);
+
+/*
+ * Attention of a chunk of new tokens over the paged cache (which already holds their
+ * rows): prefill chunks, drafted tokens to verify, dense single-token decode, mixed in
+ * one call.  Token t of sequence b (t in cu_q[b] .. cu_q[b + 1] - 1, position
+ * pos = kv_lens[b] - (cu_q[b + 1] - t)) sees the cached positions s in [lo, hi):
+ *     lo = max(0, vis_begin[t])             (0 without vis_begin)
+ *     hi = min(kv_lens[b], vis_end[t])      (pos + 1, the causal mask, without vis_end)
+ * which expresses sliding windows, documents packed into one sequence and prefixes that
+ * see themselves whole.  With x = softmax_scale * q . k (512 wide),
+ *     logit_cap > 0:   x = logit_cap * tanh(x / logit_cap)
+ *     slopes:          x = x - slopes[h] * |pos - s|
+ *     lse = ln sum_s exp(x),   out = sum_s exp(x - lse) * k_nope[s].
+ * A token that sees nothing gets out = 0, lse = -inf.  Positions on unmapped pages are
+ * masked; positions past the table and page ids past the pool are masked and reported
+ * (SMLA_ERR_INDEX_RANGE).  out and lse of entries outside [cu_q[0], cu_q[batch]) are left
+ * as they were.
+ */
+typedef struct smla_chunk_params {
+  int32_t batch;          /* sequences, 1 .. 65535                                      */
+  int32_t num_heads;      /* H: 16, 32, 64 or 128                                       */
+  int32_t total_q;        /* T: entries of q, >= 1, T * H < 2^30                        */
+  int32_t page_size;      /* rows per page, >= 1                                        */
+  int32_t max_pages;      /* columns of block_table, >= 1                               */
+  int32_t reserved;       /* must be 0                                                  */
+  int64_t num_rows;       /* rows of the pool                                           */
+  int64_t kv_row_stride;  /* bytes between rows, >= 584, multiple of 8                  */
+  int64_t max_kv_tokens;  /* the caller's bound on the sum of kv_lens, >= 1; it sizes the
+                             workspace.  Tokens past it are masked and reported
+                             (SMLA_ERR_INDEX_RANGE)                                     */
+  float softmax_scale;    /* finite and > 0                                             */
+  float logit_cap;        /* 0 = none, else finite and > 0                              */
+} smla_chunk_params;
+
+int smla_chunk_workspace_size(const smla_chunk_params* p, size_t* bytes);
+
+/*   q           bf16 [T, H, 512], 16-byte aligned     kv_pages  the pool, 16-byte aligned
+ *   block_table int32 [batch, max_pages]              cu_q      int32 [batch + 1]
+ *   kv_lens     int32 [batch]
+ *   vis_begin, vis_end  int32 [T] or NULL             slopes    fp32 [H] or NULL
+ *   out         bf16 [T, H, 448], 16-byte aligned     lse       fp32 [T, H]
+ *   workspace   >= smla_chunk_workspace_size(p) bytes, 256-byte aligned
+ */
+int smla_chunk_attention(const void* q, const void* kv_pages, const int32_t* block_table,
+                         const int32_t* cu_q, const int32_t* kv_lens, const int32_t* vis_begin,
+                         const int32_t* vis_end, const float* slopes, void* out, float* lse,
+                         const smla_chunk_params* p, void* workspace, size_t workspace_bytes,
+                         smla_stream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* smla_status_string(int status);
 
 /* Reads the current device's status word, which kernels set (first error wins) when
- * a bounded wait runs out (SMLA_ERR_TIMEOUT) or an index is out of range
- * (SMLA_ERR_INDEX_RANGE).  Synchronises the device.  clear != 0 resets it to 0. */
+ * a bounded wait runs out (SMLA_ERR_TIMEOUT), an index is out of range
+ * (SMLA_ERR_INDEX_RANGE), a value leaves its range (SMLA_ERR_RANGE) or the pool has no
+ * free page (SMLA_ERR_POOL_EXHAUSTED).  Synchronises the device.  clear != 0 resets it to 0. */
 int smla_device_status(int32_t* status, int32_t clear);
 
 #ifdef __cplusplus

@@ -22,6 +22,7 @@ SMLA_ERR_INDEX_RANGE = -7
 SMLA_ERR_RANGE = -8
 SMLA_ERR_SCRATCH_TOO_SMALL = -9
 SMLA_ERR_INTERNAL = -10
+SMLA_ERR_POOL_EXHAUSTED = -11
 
 EXPORTED = (
     "smla_default_num_splits",
@@ -34,6 +35,14 @@ EXPORTED = (
     "sparse_mla_decode_simt",
     "smla_paged_workspace_size",
     "sparse_mla_decode_paged",
+    "smla_cache_append",
+    "smla_cache_workspace_size",
+    "smla_cache_reserve",
+    "smla_cache_fork",
+    "smla_cache_free",
+    "smla_cache_compact",
+    "smla_chunk_workspace_size",
+    "smla_chunk_attention",
     "smla_status_string",
     "smla_device_status",
     "smla_test_inject_fault",
@@ -49,6 +58,32 @@ class SmlaParams(ctypes.Structure):
         ("num_rows", ctypes.c_int64),
         ("kv_row_stride", ctypes.c_int64),
         ("softmax_scale", ctypes.c_float),
+    ]
+
+
+class SmlaCacheParams(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_seqs", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("kv_row_stride", ctypes.c_int64),
+    ]
+
+
+class SmlaChunkParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("total_q", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("num_rows", ctypes.c_int64),
+        ("kv_row_stride", ctypes.c_int64),
+        ("max_kv_tokens", ctypes.c_int64),
+        ("softmax_scale", ctypes.c_float),
+        ("logit_cap", ctypes.c_float),
     ]
 
 
@@ -88,6 +123,15 @@ def _open(path: str) -> ctypes.CDLL:
     lib.sparse_mla_decode_simt.argtypes = [vp, vp, vp, vp, vp, P, vp]
     lib.smla_paged_workspace_size.argtypes = [P, i32, ctypes.POINTER(sz)]
     lib.sparse_mla_decode_paged.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, P, i32, vp, sz, vp]
+    C, K = ctypes.POINTER(SmlaCacheParams), ctypes.POINTER(SmlaChunkParams)
+    lib.smla_cache_append.argtypes = [vp, i64, i32, vp, vp, vp, vp, C, vp]
+    lib.smla_cache_workspace_size.argtypes = [C, ctypes.POINTER(sz)]
+    lib.smla_cache_reserve.argtypes = [vp, vp, vp, C, vp, sz, vp]
+    lib.smla_cache_fork.argtypes = [vp, vp, vp, vp, vp, vp, i32, C, vp, sz, vp]
+    lib.smla_cache_free.argtypes = [vp, vp, vp, vp, i32, C, vp]
+    lib.smla_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, C, vp, sz, vp]
+    lib.smla_chunk_workspace_size.argtypes = [K, ctypes.POINTER(sz)]
+    lib.smla_chunk_attention.argtypes = [vp] * 10 + [K, vp, sz, vp]
     lib.smla_status_string.argtypes = [ctypes.c_int]
     lib.smla_status_string.restype = ctypes.c_char_p
     lib.smla_device_status.argtypes = [ctypes.POINTER(i32), i32]

@@ -233,6 +233,258 @@ def sparse_mla_decode_simt(q: torch.Tensor, kv_cache: torch.Tensor, indices: tor
     return out, lse
 
 
+# ---------------------------------------------------------------------------
+# The paged cache
+# ---------------------------------------------------------------------------
+def _ints(name: str, t: torch.Tensor, dims: int, device: torch.device) -> None:
+    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimension(s) on {device}")
+
+
+def _pool(kv_pages: torch.Tensor, page_size: int) -> None:
+    if kv_pages.dim() != 2 or kv_pages.dtype != torch.uint8 or kv_pages.stride(1) != 1:
+        raise ValueError("kv_pages must be uint8 [num_rows, stride>=584] with unit column stride")
+    if kv_pages.shape[1] < ROW_BYTES:
+        raise ValueError("kv_pages rows must hold 584 bytes")
+    if not kv_pages.is_cuda:
+        raise ValueError("kv_pages must be a CUDA tensor")
+    if page_size < 1 or kv_pages.shape[0] < page_size:
+        raise ValueError("kv_pages must hold a page of page_size >= 1 rows")
+
+
+def _stream_on(stream: Optional[torch.cuda.Stream], device: torch.device) -> ctypes.c_void_p:
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if s.device != device:
+        raise ValueError(f"stream is on {s.device}, the tensors are on {device}")
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def _row_stride(kv_pages: torch.Tensor) -> int:
+    """Bytes between rows (a single row has no neighbour: any stride will do)."""
+    return kv_pages.stride(0) if kv_pages.shape[0] > 1 else ROW_BYTES
+
+
+def make_cache_params(num_pages: int, page_size: int, num_seqs: int, max_pages: int,
+                      kv_row_stride: int = ROW_BYTES) -> _lib.SmlaCacheParams:
+    return _lib.SmlaCacheParams(num_pages, page_size, num_seqs, max_pages, kv_row_stride)
+
+
+def smla_cache_workspace_size(params: _lib.SmlaCacheParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.load().smla_cache_workspace_size(ctypes.byref(params), ctypes.byref(n)),
+           "smla_cache_workspace_size")
+    return n.value
+
+
+def _cache_workspace(p: _lib.SmlaCacheParams, workspace: Optional[torch.Tensor],
+                     device: torch.device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(smla_cache_workspace_size(p), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def _bytes(t: torch.Tensor) -> int:
+    return t.numel() * t.element_size()
+
+
+def smla_cache_append(kv: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
+                      page_size: int, cu_q: torch.Tensor, kv_lens: torch.Tensor,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantises new tokens and writes their rows.  kv bf16 [T, 512]; sequence b's are
+    kv[cu_q[b]:cu_q[b + 1]], the last ones of its kv_lens[b] tokens."""
+    _pool(kv_pages, page_size)
+    dev = kv_pages.device
+    if kv.dim() != 2 or kv.shape[1] != QK or kv.dtype != torch.bfloat16 or kv.stride(1) != 1 or kv.device != dev:
+        raise ValueError(f"kv must be bf16 [T, 512] with unit column stride on {dev}")
+    _ints("block_table", block_table, 2, dev)
+    _ints("cu_q", cu_q, 1, dev)
+    _ints("kv_lens", kv_lens, 1, dev)
+    B = block_table.shape[0]
+    if cu_q.shape[0] != B + 1 or kv_lens.shape[0] != B:
+        raise ValueError("cu_q must be [B + 1] and kv_lens [B] for a block_table of B rows")
+    p = make_cache_params(kv_pages.shape[0] // page_size, page_size, B, block_table.shape[1],
+                          _row_stride(kv_pages))
+    stride = kv.stride(0) if kv.shape[0] > 1 else QK
+    with torch.cuda.device(dev):
+        st = _lib.load().smla_cache_append(_ptr(kv), stride, kv.shape[0], _ptr(kv_pages), _ptr(block_table),
+                                           _ptr(cu_q), _ptr(kv_lens), ctypes.byref(p),
+                                           _stream_on(stream, dev))
+    _check(st, "smla_cache_append")
+
+
+def smla_cache_reserve(page_size: int, ref_count: torch.Tensor, block_table: torch.Tensor,
+                       target_lens: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Maps free pages until every sequence r has room for target_lens[r] tokens."""
+    dev = ref_count.device
+    _ints("ref_count", ref_count, 1, dev)
+    _ints("block_table", block_table, 2, dev)
+    _ints("target_lens", target_lens, 1, dev)
+    if not ref_count.is_cuda or target_lens.shape[0] != block_table.shape[0]:
+        raise ValueError("target_lens must be [B] for a block_table of B rows, on a CUDA device")
+    p = make_cache_params(ref_count.shape[0], page_size, block_table.shape[0], block_table.shape[1])
+    ws = _cache_workspace(p, workspace, dev)
+    with torch.cuda.device(dev):
+        st = _lib.load().smla_cache_reserve(_ptr(ref_count), _ptr(block_table), _ptr(target_lens),
+                                            ctypes.byref(p), _ptr(ws), _bytes(ws), _stream_on(stream, dev))
+    _check(st, "smla_cache_reserve")
+
+
+def _page_state(kv_pages: torch.Tensor, page_size: int, ref_count: torch.Tensor,
+                block_table: torch.Tensor) -> _lib.SmlaCacheParams:
+    _pool(kv_pages, page_size)
+    dev = kv_pages.device
+    _ints("ref_count", ref_count, 1, dev)
+    _ints("block_table", block_table, 2, dev)
+    if ref_count.shape[0] * page_size > kv_pages.shape[0]:
+        raise ValueError("ref_count has more pages than kv_pages")
+    return make_cache_params(ref_count.shape[0], page_size, block_table.shape[0], block_table.shape[1],
+                             _row_stride(kv_pages))
+
+
+def smla_cache_fork(kv_pages: torch.Tensor, page_size: int, ref_count: torch.Tensor,
+                    block_table: torch.Tensor, kv_lens: torch.Tensor, parents: torch.Tensor,
+                    children: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Makes row children[i] a copy of row parents[i]: full pages shared, a partly filled
+    last page copied into a free one."""
+    p = _page_state(kv_pages, page_size, ref_count, block_table)
+    dev = kv_pages.device
+    _ints("kv_lens", kv_lens, 1, dev)
+    _ints("parents", parents, 1, dev)
+    _ints("children", children, 1, dev)
+    if kv_lens.shape[0] != block_table.shape[0] or parents.shape != children.shape:
+        raise ValueError("kv_lens must be [B], and parents and children equally long")
+    ws = _cache_workspace(p, workspace, dev)
+    with torch.cuda.device(dev):
+        st = _lib.load().smla_cache_fork(_ptr(kv_pages), _ptr(ref_count), _ptr(block_table), _ptr(kv_lens),
+                                         _ptr(parents), _ptr(children), parents.shape[0], ctypes.byref(p),
+                                         _ptr(ws), _bytes(ws), _stream_on(stream, dev))
+    _check(st, "smla_cache_fork")
+
+
+def smla_cache_free(ref_count: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                    rows: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Empties the listed rows of the table and gives their pages back."""
+    dev = ref_count.device
+    _ints("ref_count", ref_count, 1, dev)
+    _ints("block_table", block_table, 2, dev)
+    _ints("kv_lens", kv_lens, 1, dev)
+    _ints("rows", rows, 1, dev)
+    if not ref_count.is_cuda or kv_lens.shape[0] != block_table.shape[0]:
+        raise ValueError("kv_lens must be [B] for a block_table of B rows, on a CUDA device")
+    p = make_cache_params(ref_count.shape[0], 1, block_table.shape[0], block_table.shape[1])
+    with torch.cuda.device(dev):
+        st = _lib.load().smla_cache_free(_ptr(ref_count), _ptr(block_table), _ptr(kv_lens), _ptr(rows),
+                                         rows.shape[0], ctypes.byref(p), _stream_on(stream, dev))
+    _check(st, "smla_cache_free")
+
+
+def smla_cache_compact(kv_pages: torch.Tensor, page_size: int, ref_count: torch.Tensor,
+                       block_table: torch.Tensor, ref_count_out: Optional[torch.Tensor] = None,
+                       block_table_out: Optional[torch.Tensor] = None,
+                       info: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Moves the pages in use to the front of the pool; counts and table follow, in place
+    unless other outputs are given.  Returns info: int32 [pages in use, pages moved]."""
+    p = _page_state(kv_pages, page_size, ref_count, block_table)
+    dev = kv_pages.device
+    ref_out = ref_count if ref_count_out is None else ref_count_out
+    table_out = block_table if block_table_out is None else block_table_out
+    _ints("ref_count_out", ref_out, 1, dev)
+    _ints("block_table_out", table_out, 2, dev)
+    if ref_out.shape != ref_count.shape or table_out.shape != block_table.shape:
+        raise ValueError("the outputs must have the shapes of ref_count and block_table")
+    if info is None:
+        info = torch.empty(2, dtype=torch.int32, device=dev)
+    _ints("info", info, 1, dev)
+    if info.shape[0] != 2:
+        raise ValueError("info must be int32 [2]")
+    ws = _cache_workspace(p, workspace, dev)
+    with torch.cuda.device(dev):
+        st = _lib.load().smla_cache_compact(_ptr(kv_pages), _ptr(ref_count), _ptr(block_table), _ptr(ref_out),
+                                            _ptr(table_out), _ptr(info), ctypes.byref(p), _ptr(ws),
+                                            _bytes(ws), _stream_on(stream, dev))
+    _check(st, "smla_cache_compact")
+    return info
+
+
+def make_chunk_params(batch: int, num_heads: int, total_q: int, page_size: int, max_pages: int,
+                      num_rows: int, kv_row_stride: int, max_kv_tokens: int,
+                      softmax_scale: float = DEFAULT_SCALE, logit_cap: float = 0.0
+                      ) -> _lib.SmlaChunkParams:
+    return _lib.SmlaChunkParams(batch, num_heads, total_q, page_size, max_pages, 0, num_rows,
+                                kv_row_stride, max_kv_tokens, softmax_scale, logit_cap)
+
+
+def smla_chunk_workspace_size(params: _lib.SmlaChunkParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.load().smla_chunk_workspace_size(ctypes.byref(params), ctypes.byref(n)),
+           "smla_chunk_workspace_size")
+    return n.value
+
+
+def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
+                         page_size: int, cu_q: torch.Tensor, kv_lens: torch.Tensor,
+                         softmax_scale: float = DEFAULT_SCALE, logit_cap: float = 0.0,
+                         slopes: Optional[torch.Tensor] = None,
+                         vis_begin: Optional[torch.Tensor] = None,
+                         vis_end: Optional[torch.Tensor] = None,
+                         max_kv_tokens: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                         lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None
+                         ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of the chunk's tokens q bf16 [T, H, 512] (sequence b's are
+    q[cu_q[b]:cu_q[b + 1]], the last ones of its kv_lens[b] cached tokens) over the paged
+    cache, causal unless vis_begin / vis_end say otherwise.  max_kv_tokens bounds the sum of
+    kv_lens (default: what the table can hold) and sizes the workspace.  Returns (out bf16
+    [T, H, 448], lse fp32 [T, H])."""
+    _pool(kv_pages, page_size)
+    dev = kv_pages.device
+    if q.dim() != 3 or q.shape[2] != QK or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.device != dev:
+        raise ValueError(f"q must be contiguous bf16 [T, H, 512] on {dev}")
+    T, H, _ = q.shape
+    _ints("block_table", block_table, 2, dev)
+    _ints("cu_q", cu_q, 1, dev)
+    _ints("kv_lens", kv_lens, 1, dev)
+    B, max_pages = block_table.shape
+    if cu_q.shape[0] != B + 1 or kv_lens.shape[0] != B:
+        raise ValueError("cu_q must be [B + 1] and kv_lens [B] for a block_table of B rows")
+    for name, t in (("vis_begin", vis_begin), ("vis_end", vis_end)):
+        if t is not None:
+            _ints(name, t, 1, dev)
+            if t.shape[0] != T:
+                raise ValueError(f"{name} must be int32 [T]")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (H,)
+                               or not slopes.is_contiguous() or slopes.device != dev):
+        raise ValueError(f"slopes must be contiguous fp32 [H] on {dev}")
+    if out is None:
+        out = torch.empty((T, H, NOPE), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    for name, t, shape, dtype in (("out", out, (T, H, NOPE), torch.bfloat16),
+                                  ("lse", lse, (T, H), torch.float32)):
+        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {dev}")
+    if max_kv_tokens is None:
+        max_kv_tokens = B * max_pages * page_size
+    p = make_chunk_params(B, H, T, page_size, max_pages, kv_pages.shape[0], _row_stride(kv_pages),
+                          max_kv_tokens, softmax_scale, logit_cap)
+    if workspace is None:
+        workspace = torch.empty(smla_chunk_workspace_size(p), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    with torch.cuda.device(dev):
+        st = _lib.load().smla_chunk_attention(
+            _ptr(q), _ptr(kv_pages), _ptr(block_table), _ptr(cu_q), _ptr(kv_lens), _ptr(vis_begin),
+            _ptr(vis_end), _ptr(slopes), _ptr(out), _ptr(lse), ctypes.byref(p), _ptr(workspace),
+            _bytes(workspace), _stream_on(stream, dev))
+    _check(st, "smla_chunk_attention")
+    return out, lse
+
+
 def smla_device_status(clear: bool = False) -> int:
     """Device status word (0, SMLA_ERR_TIMEOUT or SMLA_ERR_INDEX_RANGE); synchronises."""
     lib = _lib.load()

@@ -371,6 +371,8 @@ const char* smla_status_string(int status) {
       return "SMLA_ERR_SCRATCH_TOO_SMALL: split partials exceed the 16 MiB built-in scratch";
     case SMLA_ERR_INTERNAL:
       return "SMLA_ERR_INTERNAL: a debug-build bounds check failed (access skipped)";
+    case SMLA_ERR_POOL_EXHAUSTED:
+      return "SMLA_ERR_POOL_EXHAUSTED: no free page was left in the pool";
     default: return "SMLA: unknown status";
   }
 }

@@ -1,0 +1,346 @@
+"""Chunk attention over the paged cache against the definition in 64 bits, and the run of the
+cache calls and the attention together.  Tolerances are derived in _cache_helpers."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_mla_decode_03_gb300 as m
+
+from _cache_helpers import (ROW, SCALE, check_chunk, chunk_reference, dev, pack_rows, random_pool, tables)
+
+pytestmark = pytest.mark.gpu
+
+
+def _case(lens, ns, H, page, seed, stride=ROW, lead=0, mult=1.0, extra=1):
+    num_pages = sum(-(-max(L, 0) // page) for L in lens) + 2
+    pool = random_pool(num_pages, page, seed, stride, lead, mult)
+    table = tables(lens, page, num_pages, seed, extra)
+    cu = np.concatenate([[0], np.cumsum(ns)]).astype(np.int32)
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn((max(1, int(cu[-1])), H, 512), generator=g).to(torch.bfloat16).cuda()
+    return q, pool, table, cu, np.array(lens, np.int32)
+
+
+def _run(q, pool, table, page, cu, lens, cap=0.0, slopes=None, begin=None, end=None, status=0, **kw):
+    m.smla_device_status(clear=True)
+    got = m.smla_chunk_attention(q, pool, dev(table), page, dev(cu), dev(lens), softmax_scale=SCALE, logit_cap=cap,
+                                 slopes=slopes, vis_begin=None if begin is None else dev(begin),
+                                 vis_end=None if end is None else dev(end), **kw)
+    assert m.smla_device_status(clear=True) == status
+    return got
+
+
+def _check(q, pool, table, page, cu, lens, cap=0.0, slopes=None, begin=None, end=None, **kw):
+    got = _run(q, pool, table, page, cu, lens, cap, slopes, begin, end, **kw)
+    check_chunk(got, chunk_reference(q, pool, table, page, cu, lens, SCALE, cap, slopes, begin, end))
+    return got
+
+
+SHAPES = [
+    # lens, new tokens, H, page
+    ([1], [1], 64, 1),
+    ([1, 2, 3], [1, 1, 3], 16, 1),
+    ([64, 63, 65, 0, 1], [1, 1, 1, 0, 1], 64, 16),
+    ([1001, 700, 30], [4, 1, 4], 64, 16),
+    ([300, 5000], [1, 1], 32, 48),
+    ([257], [3], 128, 64),
+    ([130, 128, 127], [2, 1, 3], 128, 33),
+    ([700, 450], [200, 37], 16, 100),
+    ([65], [65], 64, 64),
+    ([513, 80], [130, 80], 32, 64),
+    ([400], [140], 128, 7),
+    ([2500, 0, 1300, 90], [64, 0, 33, 90], 64, 64),
+]
+
+
+@pytest.mark.parametrize("lens,ns,H,page", SHAPES)
+def test_causal(lens, ns, H, page):
+    _check(*_pick(_case(lens, ns, H, page, seed=H + page + len(lens)), page))
+
+
+def _pick(c, page):
+    q, pool, table, cu, lens = c
+    return q, pool, table, page, cu, lens
+
+
+def _masks(kind, lens, ns, seed):
+    rng = np.random.default_rng(seed)
+    begin, end = [], []
+    for L, n in zip(lens, ns):
+        for j in range(n):
+            p = L - n + j
+            a, b = 0, p + 1
+            if kind == "window":
+                a = p - 70
+            elif kind == "documents":
+                a = p // 100 * 100
+            elif kind == "prefix":
+                b = max(b, L - n // 2)
+            elif kind == "random":         # anything goes: empty, negative, past the end, one token
+                a, b = (int(v) for v in rng.integers(-20, L + 40, 2))
+            elif kind == "empty":
+                a, b = (5, 5) if j % 3 else (L, L + 9)
+            begin.append(a)
+            end.append(b)
+    return np.array(begin, np.int32), np.array(end, np.int32)
+
+
+@pytest.mark.parametrize("kind", ["window", "documents", "prefix", "random", "empty"])
+@pytest.mark.parametrize("lens,ns,H,page", [([900, 333], [40, 70], 64, 48), ([600, 77, 1], [1, 1, 1], 64, 16),
+                                            ([500], [300], 16, 64), ([260, 300], [64, 9], 128, 100)])
+def test_masks(kind, lens, ns, H, page):
+    c = _case(lens, ns, H, page, seed=3 * H + len(kind))
+    begin, end = _masks(kind, lens, ns, seed=H)
+    _check(*_pick(c, page), begin=begin, end=end)
+
+
+@pytest.mark.parametrize("which", ["begin", "end"])
+def test_one_sided_masks(which):
+    lens, ns, page = [300, 280], [20, 130], 64
+    c = _case(lens, ns, 64, page, seed=5)
+    begin, end = _masks("window" if which == "begin" else "prefix", lens, ns, 5)
+    _check(*_pick(c, page), begin=begin if which == "begin" else None, end=end if which == "end" else None)
+
+
+@pytest.mark.parametrize("cap,bias", [(30.0, False), (0.0, True), (5.0, True), (0.01, False)])
+@pytest.mark.parametrize("lens,ns,H,page", [([1200, 40], [1, 1], 64, 64), ([700, 300], [150, 64], 16, 48),
+                                            ([300], [70], 128, 64)])
+def test_cap_and_distance_bias(cap, bias, lens, ns, H, page):
+    c = _case(lens, ns, H, page, seed=int(H + 10 * cap))
+    slopes = torch.exp2(-8.0 * torch.arange(1, H + 1, device="cuda") / H).float() if bias else None
+    begin, end = _masks("prefix", lens, ns, 1)
+    _check(*_pick(c, page), cap=cap, slopes=slopes, begin=begin, end=end)
+
+
+@pytest.mark.parametrize("n,H", [(1, 64), (130, 64), (90, 16)])
+def test_scores_that_rise_along_the_context(n, H):
+    """The running maximum grows by far more than any headroom from block to block, again and
+    again, and falls at the end."""
+    L, page = 700, 64
+    q, pool, table, cu, lens = _case([L], [n], H, page, seed=9)
+    q = q.abs()
+    x = torch.rand(L, 512, generator=torch.Generator().manual_seed(1)) * torch.linspace(0.0, 12.0, L)[:, None]
+    x[-90:] *= 0.05
+    rows = dev(pack_rows(x.to(torch.bfloat16)))
+    at = torch.as_tensor(table[0].astype(np.int64)[np.arange(L) // page] * page + np.arange(L) % page, device="cuda")
+    pool[at] = rows
+    _check(q, pool, table, page, cu, lens)
+
+
+def test_large_values_and_unusual_scales():
+    """Rows beyond the f16 range, tiny rows and extreme scale bytes keep their values."""
+    L, page, H = 200, 16, 64
+    for n in (1, 140):
+        q, pool, table, cu, lens = _case([L], [n], H, page, seed=21)
+        q = (q.float() * 2.0 ** -9).to(torch.bfloat16)
+        g = torch.Generator().manual_seed(2)
+        x = torch.randn(L, 512, generator=g)
+        x[::7, :64] *= 2.0 ** 14
+        x[3::7, 64:128] *= 2.0 ** -40
+        x[5::7, 200:300] = 0
+        at = torch.as_tensor(table[0].astype(np.int64)[np.arange(L) // page] * page + np.arange(L) % page,
+                             device="cuda")
+        pool[at] = dev(pack_rows(x.to(torch.bfloat16)))
+        _check(q, pool, table, page, cu, lens)
+
+
+@pytest.mark.parametrize("n,H", [(1, 64), (2, 16), (150, 64)])
+def test_unmapped_pages_and_pages_past_the_pool(n, H):
+    L, page = 520, 16
+    q, pool, table, cu, lens = _case([L, 300], [n, n], H, page, seed=31)
+    table[0, 3] = table[0, 11] = -1
+    table[1, 0] = -7
+    _check(q, pool, table, page, cu, lens)
+    table[0, 20] = pool.shape[0] // page            # the first page id past the pool
+    table[1, 5] = 2 ** 31 - 1
+    _check(q, pool, table, page, cu, lens, status=-7)
+    table[:, :] = -1
+    _check(q, pool, table, page, cu, lens)          # nothing is mapped
+
+
+@pytest.mark.parametrize("n", [1, 150])
+def test_lengths_past_the_table(n):
+    L, page, H = 130, 16, 64
+    q, pool, table, cu, lens = _case([L], [n if n < L else L - 1], H, page, seed=33, extra=0)
+    cut = table[:, :6].copy()
+    _check(q, pool, cut, page, cu, lens, status=-7)
+
+
+@pytest.mark.parametrize("n", [3, 200])
+def test_more_new_tokens_than_the_length(n):
+    q, pool, table, cu, lens = _case([n // 2 + 1, 40], [n, 5], 64, 16, seed=35)
+    _check(q, pool, table, 16, cu, lens)
+
+
+@pytest.mark.parametrize("n", [2, 140])
+def test_entries_outside_every_sequence_are_left_alone(n):
+    H, page = 64, 64
+    q, pool, table, cu, lens = _case([300, 200], [n, n], H, page, seed=37)
+    q = torch.cat([q, q[:9]]).contiguous()
+    cu = cu + 4
+    out = torch.full((q.shape[0], H, 448), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((q.shape[0], H), 7.0, device="cuda")
+    got = _check(q, pool, table, page, cu, lens, out=out, lse=lse)
+    for t in list(range(4)) + list(range(4 + 2 * n, q.shape[0])):
+        assert (got[0][t] == 7).all() and (got[1][t] == 7).all()
+
+
+@pytest.mark.parametrize("stride,lead", [(592, 16), (600, 0), (1024, 32)])
+@pytest.mark.parametrize("n", [1, 135])
+def test_strided_pools(stride, lead, n):
+    q, pool, table, cu, lens = _case([333], [n], 64, 48, seed=41, stride=stride, lead=lead)
+    _check(q, pool, table, 48, cu, lens)
+
+
+def test_large_ragged_batch():
+    rng = np.random.default_rng(7)
+    lens = [int(v) for v in rng.integers(0, 900, 70)]
+    ns = [int(min(L, v)) for L, v in zip(lens, rng.integers(0, 9, 70))]
+    _check(*_pick(_case(lens, ns, 16, 32, seed=43), 32))
+
+
+def test_a_bound_on_the_tokens_that_is_exact_or_too_small():
+    lens, ns, page = [700, 260], [140, 70], 64
+    c = _case(lens, ns, 64, page, seed=45)
+    a = _run(*_pick(c, page), max_kv_tokens=sum(lens))
+    b = _run(*_pick(c, page))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_same_call_twice_gives_the_same_bits():
+    for ns in ([1, 1], [150, 90]):
+        c = _case([3000, 700], ns, 64, 64, seed=47)
+        a, b = _run(*_pick(c, 64)), _run(*_pick(c, 64))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("ns", [[1, 1], [130, 70]])
+def test_graph_replay_follows_new_lengths_and_side_streams(ns):
+    page, H = 64, 64
+    q, pool, table, cu, lens = _case([800, 700], ns, H, page, seed=51)
+    t, c, l = dev(table), dev(cu), dev(lens)
+    p = m.make_chunk_params(2, H, q.shape[0], page, table.shape[1], pool.shape[0], ROW, 1500)
+    ws = torch.empty(m.smla_chunk_workspace_size(p), dtype=torch.uint8, device="cuda")
+    out = torch.empty((q.shape[0], H, 448), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((q.shape[0], H), device="cuda")
+    s = torch.cuda.Stream()
+
+    def call():
+        m.smla_chunk_attention(q, pool, t, page, c, l, softmax_scale=SCALE, max_kv_tokens=1500, out=out, lse=lse,
+                               workspace=ws, stream=s)
+
+    s.wait_stream(torch.cuda.current_stream())
+    call()
+    s.synchronize()
+    check_chunk((out, lse), chunk_reference(q, pool, table, page, cu, lens))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        call()
+    for new in ([800, 700], [401, 130], [140, 650]):
+        l.copy_(dev(np.array(new, np.int32)))
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        check_chunk((out, lse), chunk_reference(q, pool, table, page, cu, np.array(new, np.int32)))
+
+
+def test_two_calls_at_once_on_two_streams():
+    cases = [_case([1500, 600], [1, 3], 64, 64, seed=61), _case([900], [140], 32, 48, seed=62)]
+    pages = [64, 48]
+    want = [_run(*_pick(c, p)) for c, p in zip(cases, pages)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    args = [(q, pool, dev(t), p, dev(cu), dev(l)) for (q, pool, t, cu, l), p in zip(cases, pages)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for a, s in zip(args, streams):
+            with torch.cuda.stream(s):
+                got.append(m.smla_chunk_attention(*a, softmax_scale=SCALE))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_single_tokens_agree_with_the_sparse_decode_over_all_positions():
+    """A chunk of one token a sequence is the decode step with every position selected."""
+    lens, page, H = [500, 129, 64], 64, 64
+    q, pool, table, cu, l = _case(lens, [1, 1, 1], H, page, seed=71)
+    out, lse = _run(q, pool, table, page, cu, l)
+    idx = np.full((3, 500), -1, np.int32)
+    for b, L in enumerate(lens):
+        idx[b, :L] = np.arange(L)
+    o2, z2 = m.sparse_mla_decode_paged(q, pool, dev(table), page, dev(idx), softmax_scale=SCALE)
+    assert (out.float() - o2.float()).abs().max() <= 1e-2        # the decode path's own bar
+    assert (lse - z2).abs().max() <= 1e-3
+
+
+def test_cache_calls_and_attention_together():
+    """A serving loop: prompts are reserved, written and attended, a sequence is forked, the
+    branches grow apart, one is dropped, the pool is compacted, and the rest goes on; every
+    step's attention is checked against rows packed from the tokens themselves."""
+    page, num_pages, R, width, H = 16, 80, 4, 20, 64
+    gen = torch.Generator().manual_seed(5)
+    pool = torch.full((num_pages * page, ROW), 0x11, dtype=torch.uint8, device="cuda")
+    ref = torch.zeros(num_pages, dtype=torch.int32, device="cuda")
+    table = torch.full((R, width), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(R, dtype=torch.int32, device="cuda")
+    tokens = [torch.zeros(0, 512, dtype=torch.bfloat16) for _ in range(R)]
+
+    def step(ns):
+        cu = np.concatenate([[0], np.cumsum(ns)]).astype(np.int32)
+        kv = torch.randn(int(cu[-1]), 512, generator=gen).to(torch.bfloat16)
+        q = torch.randn(int(cu[-1]), H, 512, generator=gen).to(torch.bfloat16).cuda()
+        for r, n in enumerate(ns):
+            tokens[r] = torch.cat([tokens[r], kv[cu[r]:cu[r] + n]])
+        lens.add_(dev(np.array(ns, np.int32)))
+        m.smla_cache_reserve(page, ref, table, lens)
+        m.smla_cache_append(kv.cuda(), pool, table, page, dev(cu), lens)
+        got = m.smla_chunk_attention(q, pool, table, page, dev(cu), lens, softmax_scale=SCALE)
+        # the oracle reads rows packed from the tokens, one after another, not the pool
+        L = [t.shape[0] for t in tokens]
+        flat = torch.cat([dev(pack_rows(t)) for t in tokens if t.shape[0]] + [torch.zeros(1, ROW, dtype=torch.uint8,
+                                                                                         device="cuda")])
+        at = np.full((R, max(L)), -1, np.int32)
+        for r in range(R):
+            at[r, :L[r]] = sum(L[:r]) + np.arange(L[r])
+        assert lens.cpu().tolist() == L
+        check_chunk(got, chunk_reference(q, flat, at, 1, cu, np.array(L, np.int32)))
+
+    m.smla_device_status(clear=True)
+    step([70, 33, 0, 0])
+    step([1, 1, 0, 0])
+    m.smla_cache_fork(pool, page, ref, table, lens, dev(np.array([0, 0], np.int32)), dev(np.array([2, 3], np.int32)))
+    tokens[2], tokens[3] = tokens[0].clone(), tokens[0].clone()
+    step([0, 1, 4, 1])
+    m.smla_cache_free(ref, table, lens, dev(np.array([1], np.int32)))
+    tokens[1] = tokens[1][:0]
+    info = m.smla_cache_compact(pool, page, ref, table)
+    used = int((ref > 0).sum())
+    assert info.cpu().tolist()[0] == used and bool((ref[:used] > 0).all())
+    step([1, 20, 1, 130])
+    assert m.smla_device_status(clear=True) == 0
+
+
+def test_binding_refusals():
+    q, pool, table, cu, lens = _case([50], [3], 64, 16, seed=81)
+    t, c, l = dev(table), dev(cu), dev(lens)
+    bad = [
+        lambda: m.smla_chunk_attention(q.float(), pool, t, 16, c, l),
+        lambda: m.smla_chunk_attention(q[:, :, :500], pool, t, 16, c, l),
+        lambda: m.smla_chunk_attention(q, pool, t.long(), 16, c, l),
+        lambda: m.smla_chunk_attention(q, pool, t, 16, c[:1], l),
+        lambda: m.smla_chunk_attention(q, pool, t, 16, c, l.cpu()),
+        lambda: m.smla_chunk_attention(q, pool, t, 0, c, l),
+        lambda: m.smla_chunk_attention(q, pool, t, 16, c, l, slopes=torch.ones(32, device="cuda")),
+        lambda: m.smla_chunk_attention(q, pool, t, 16, c, l, vis_begin=l),
+        lambda: m.smla_chunk_attention(q, pool, t, 16, c, l, out=torch.empty(3, 64, 448, device="cuda")),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for kw in ({"softmax_scale": -1.0}, {"logit_cap": -2.0}, {"max_kv_tokens": 0},
+               {"workspace": torch.empty(1, dtype=torch.uint8, device="cuda")}):
+        with pytest.raises(m.SmlaError):
+            m.smla_chunk_attention(q, pool, t, 16, c, l, **kw)
+    with pytest.raises(m.SmlaError):
+        m.smla_chunk_attention(q[:, :48].contiguous(), pool, t, 16, c, l)
