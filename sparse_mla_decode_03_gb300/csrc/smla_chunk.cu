@@ -8,135 +8,294 @@
 #include <cstdint>
 
 #include "../../include/smla.h"
+#include "smla_chunk.h"
 #include "smla_internal.h"
 #include "smla_ptx.cuh"
 
 namespace smla {
 namespace {
 
-struct ChunkArgs {
-  const uint16_t* q;
-  const uint8_t* pool;
-  const int32_t *table, *cu_q, *kv_lens, *vis_begin, *vis_end;
-  const float* slopes;
-  __nv_bfloat16* out;
-  float* lse;
-  int B, H, T, page_size, max_pages;
-  int64_t num_rows, stride;
-  float scale, cap;
-  int* status;
-};
-
-__device__ __forceinline__ float e4m3_value(uint32_t byte) {
-  uint32_t h2;
-  const uint16_t in = static_cast<uint16_t>(byte);
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(in));
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xffffu)));
-}
 __device__ __forceinline__ float ue8m0_value(uint32_t e) {
   return __uint_as_float(e == 0u ? 0x00400000u : (e == 255u ? 0x7fffffffu : (e << 23)));
 }
 
-// One CTA per (token, head), element-wise fp32: four warps take the visible positions in
-// turn, each with its own online softmax, merged at the end.
-__global__ void __launch_bounds__(128) chunk_plain_kernel(const ChunkArgs a) {
-  __shared__ float qs[kQkDim];
-  __shared__ float wm[4], wl[4];
-  __shared__ float wacc[4][kNope];
+// ---------------------------------------------------------------------------
+// Plan
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+
+// Exclusive sum over the CTA; *total gets the sum.
+__device__ long long block_sum(long long v, long long* total, long long* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    long long w = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  *total = warp_sums[31];
+  return s - v + (warp > 0 ? warp_sums[warp - 1] : 0);
+}
+
+// One CTA.  tile_rows: (token, head) rows of a tile; workers: shares of the line.
+__global__ void __launch_bounds__(kPlanThreads, 1)
+    plan_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows, int workers, int min_share) {
+  __shared__ long long sums[32];
   grid_dep_wait();
   grid_dep_launch();
-  const int h = blockIdx.y, t = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (t < a.cu_q[0] || t >= a.cu_q[a.B]) return;
-  int b = 0;
-  for (int hi = a.B; hi - b > 1;) {
-    const int mid = (b + hi) / 2;
-    if (a.cu_q[mid] <= t) b = mid;
-    else hi = mid;
+  const int tokens_of_tile = tile_rows / a.H;
+  long long tiles = 0, blocks = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    int n = 0, len = 0;
+    if (b < a.B) {
+      const int first = min(max(a.cu_q[b], 0), a.T);
+      n = min(max(a.cu_q[b + 1], first), a.T) - first;
+      len = max(a.kv_lens[b], 0);
+    }
+    const int nt = (n + tokens_of_tile - 1) / tokens_of_tile;
+    // a sequence without cached tokens keeps one block (of zeros) for its tiles to read
+    const int nb = n > 0 ? max(1, (len + kChunkBlk - 1) / kChunkBlk) : 0;
+    long long t_all, b_all;
+    const long long t0 = tiles + block_sum(nt, &t_all, sums);
+    const long long s0 = blocks + block_sum(nb, &b_all, sums);
+    if (b < a.B) {
+      const long long left = p.cap_blocks - s0;
+      if (nb > left) {
+        len = left > 0 ? static_cast<int>(left) * kChunkBlk : 0;
+        atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
+      }
+      p.tile_base[b] = static_cast<int>(t0);
+      p.seq_base[b] = static_cast<int>(min(s0, static_cast<long long>(p.cap_blocks)));
+      p.seq_len[b] = len;
+    }
+    tiles += t_all;
+    blocks += b_all;
   }
-  const int len = a.kv_lens[b];
-  const int pos = len - (a.cu_q[b + 1] - t);
-  const int lo = a.vis_begin ? max(0, a.vis_begin[t]) : 0;
-  const int hi = a.vis_end ? min(len, a.vis_end[t]) : pos + 1;
-  const uint16_t* qrow = a.q + (static_cast<int64_t>(t) * a.H + h) * kQkDim;
-  for (int c = threadIdx.x; c < kQkDim; c += blockDim.x)
-    qs[c] = __uint_as_float(static_cast<uint32_t>(qrow[c]) << 16);
+  if (threadIdx.x == 0) {
+    p.tile_base[a.B] = static_cast<int>(tiles);
+    p.seq_base[a.B] = static_cast<int>(min(blocks, static_cast<long long>(p.cap_blocks)));
+  }
   __syncthreads();
-  float m = -INFINITY, l = 0.f;
-  float acc[16];
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int s = lo + warp; s < hi; s += 4) {
-    const int page = s / a.page_size;
-    if (page >= a.max_pages) {
-      if (lane == 0) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
-      continue;
+  long long line = 0;
+  for (int t0 = 0; t0 < static_cast<int>(tiles); t0 += kPlanThreads) {
+    const int t = t0 + static_cast<int>(threadIdx.x);
+    int4 tile = make_int4(0, 0, 0, 0);
+    int n = 0;
+    if (t < tiles) {
+      const int b = find_last_le(p.tile_base, a.B + 1, t);
+      const int first = min(max(a.cu_q[b], 0), a.T), last = min(max(a.cu_q[b + 1], first), a.T);
+      const int tok = first + (t - p.tile_base[b]) * tokens_of_tile;
+      const int count = min(tokens_of_tile, last - tok);
+      int low = 0x7fffffff, high = 0;
+      for (int j = 0; j < count; ++j) {
+        int lo, hi, pos;
+        visible(a, b, tok + j, p.seq_len[b], &lo, &hi, &pos);
+        if (hi > lo) {
+          low = min(low, lo);
+          high = max(high, hi);
+        }
+      }
+      const int blk = high > 0 ? low / kChunkBlk : 0;
+      n = high > 0 ? (high - 1) / kChunkBlk + 1 - blk : 1;
+      tile = make_int4(b, tok, count, blk);
     }
-    const int phys = a.table[static_cast<int64_t>(b) * a.max_pages + page];
-    if (phys < 0) continue;
-    const int64_t r = static_cast<int64_t>(phys) * a.page_size + s % a.page_size;
-    if (r >= a.num_rows) {
-      if (lane == 0) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
-      continue;
+    long long all;
+    const long long at = line + block_sum(n, &all, sums);
+    if (t < tiles) {
+      p.tile[t] = tile;
+      p.cum[t] = static_cast<int>(min(at, 0x7fffffffll));
     }
-    const uint8_t* row = a.pool + r * a.stride;
-    float v[16];
-    float dot = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int w = lane + 32 * j;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[4 * j + e] = 0.f;
-      if (w < kNope / 4) {
-        const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(row) + w);
-        const float sc = ue8m0_value(__ldg(row + kNope + (4 * w) / 64));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[4 * j + e] = e4m3_value((word >> (8 * e)) & 0xffu) * sc;
-          dot = fmaf(qs[4 * w + e], v[4 * j + e], dot);
+    line += all;
+  }
+  if (threadIdx.x == 0) {
+    p.cum[tiles] = static_cast<int>(line);
+    p.head[0] = static_cast<int>(tiles);
+    p.head[1] = static_cast<int>(line);
+    p.head[2] = max(min_share, static_cast<int>((line + workers - 1) / workers));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Expanded copy: the rows of each sequence in the order of its positions, bf16.  The e4m3
+// values times their powers of two are exact in bf16.  A warp writes 8 of a block's rows;
+// lane l < 28 holds columns 16 l .. 16 l + 15, lanes 28..31 the rope.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t expand_pair(uint32_t two, float scale) {
+  uint32_t h2;
+  const uint16_t in = static_cast<uint16_t>(two);
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(in));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y * scale), "f"(f.x * scale));
+  return r;
+}
+__device__ __forceinline__ bool not_finite(uint32_t bf16x2) {
+  return (bf16x2 & 0x7f80u) == 0x7f80u || (bf16x2 & 0x7f800000u) == 0x7f800000u;
+}
+
+__global__ void __launch_bounds__(256) expand_kernel(const ChunkArgs a, const ChunkPlan p) {
+  __shared__ uint32_t mapped[8], odd[8];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int total = p.seq_base[a.B];
+  for (int g = blockIdx.x; g <= total; g += gridDim.x) {
+    // block `total` stands behind the copy: zeros, for the sequences that found no room
+    const int64_t out_blk = g < total ? g : p.cap_blocks;
+    int b = 0, s0 = 0, len = 0;
+    if (g < total) {
+      b = find_last_le(p.seq_base, a.B + 1, g);
+      s0 = (g - p.seq_base[b]) * kChunkBlk;
+      len = p.seq_len[b];
+    }
+    // lane j < 8: the pool row of position s0 + 8 warp + j
+    long long row = -1;
+    const int s = s0 + 8 * warp + lane;
+    if (lane < 8 && s < len) {
+      const int page = s / a.page_size;
+      if (page >= a.max_pages) {
+        atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
+      } else {
+        const int phys = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + page);
+        if (phys >= 0) {
+          row = static_cast<long long>(phys) * a.page_size + (s - page * a.page_size);
+          if (row >= a.num_rows) {
+            row = -1;
+            atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
+          }
         }
       }
     }
-    const uint32_t rw = __ldg(reinterpret_cast<const uint32_t*>(row + 456) + lane);
-    dot = fmaf(qs[kNope + 2 * lane], __uint_as_float(rw << 16), dot);
-    dot = fmaf(qs[kNope + 2 * lane + 1], __uint_as_float(rw & 0xffff0000u), dot);
+    const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
+    uint32_t poison = 0;
+    uint2 in[8][2];
+    uint2 more[8][2];
+    uint32_t sc[8];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    float x = dot * a.scale;
-    if (a.cap > 0.f) x = a.cap * tanhf(x / a.cap);
-    if (a.slopes) x -= a.slopes[h] * fabsf(static_cast<float>(pos - s));
-    const float m_new = fmaxf(m, x);
-    const float f = expf(m - m_new), p = expf(x - m_new);
-    l = l * f + p;
+    for (int j = 0; j < 8; ++j) {
+      const long long r = __shfl_sync(0xffffffffu, row, j);
+      in[j][0] = in[j][1] = more[j][0] = more[j][1] = make_uint2(0u, 0u);
+      sc[j] = 127;
+      if (r >= 0) {
+        const uint8_t* src = a.pool + r * a.stride;
+        const uint2* w = reinterpret_cast<const uint2*>(src + (lane < 28 ? 16 * lane : 456 + 32 * (lane - 28)));
+        in[j][0] = __ldg(w);
+        in[j][1] = __ldg(w + 1);
+        if (lane >= 28) {
+          more[j][0] = __ldg(w + 2);
+          more[j][1] = __ldg(w + 3);
+        } else {
+          sc[j] = __ldg(src + kNope + lane / 4);
+        }
+      }
+    }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = acc[i] * f + p * v[i];
-    m = m_new;
-  }
-  if (lane == 0) {
-    wm[warp] = m;
-    wl[warp] = l;
-  }
+    for (int j = 0; j < 8; ++j) {
+      uint32_t o[8];
+      if (lane < 28) {
+        const float f = ue8m0_value(sc[j]);
+        const uint32_t w[4] = {in[j][0].x, in[j][0].y, in[j][1].x, in[j][1].y};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int w = lane + 32 * j;
-    if (w < kNope / 4) {
+        for (int k = 0; k < 4; ++k) {
+          o[2 * k] = expand_pair(w[k] & 0xffffu, f);
+          o[2 * k + 1] = expand_pair(w[k] >> 16, f);
+        }
+      } else {
+        o[0] = in[j][0].x; o[1] = in[j][0].y; o[2] = in[j][1].x; o[3] = in[j][1].y;
+        o[4] = more[j][0].x; o[5] = more[j][0].y; o[6] = more[j][1].x; o[7] = more[j][1].y;
+      }
+      bool bad = false;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) wacc[warp][4 * w + e] = acc[4 * j + e];
+      for (int k = 0; k < 8; ++k) bad |= not_finite(o[k]);
+      if (__any_sync(0xffffffffu, bad)) {
+        poison |= 1u << j;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = 0;
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.kv + (out_blk * kChunkBlk + 8 * warp + j) * kQkDim + 16 * lane);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+    __syncthreads();
+    if (lane == 0) {
+      mapped[warp] = have;
+      odd[warp] = poison;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      unsigned long long x = 0, y = 0;
+      for (int w = 0; w < 8; ++w) {
+        x |= static_cast<unsigned long long>(mapped[w] & 0xffu) << (8 * w);
+        y |= static_cast<unsigned long long>(odd[w]) << (8 * w);
+      }
+      p.seen[out_blk] = make_ulonglong2(x, y);
     }
   }
-  __syncthreads();
-  const float M = fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3]));
-  float L = 0.f, fw[4];
+}
+
+// ---------------------------------------------------------------------------
+// Merge: the partial results of the tiles that a share's border cuts.  Grid (row groups of
+// 8, borders): border c lies between workers c and c + 1 and serves its tile if it is the
+// first border inside.  A warp a row.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int per = p.head[2], total = p.head[1], tiles = p.head[0];
+  const int c1 = blockIdx.y + 1;
+  const int64_t border = static_cast<int64_t>(c1) * per;
+  if (border >= total) return;
+  const int x = static_cast<int>(border);
+  const int t = find_last_le(p.cum, tiles + 1, x);
+  const int begin = p.cum[t], end = p.cum[t + 1];
+  if (begin == x || begin / per + 1 != c1) return;
+  const int4 tile = p.tile[t];
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= tile.z * a.H) return;
+  const int first = c1 - 1, last = (end - 1) / per;
+  // slot of worker c: its share begins inside the tile (0), or the tile inside its share (1)
+  auto slot = [&](int c) { return 2 * c + (begin < c * per ? 0 : 1); };
+  float top = -INFINITY;
+  for (int c = first + lane; c <= last; c += 32) top = fmaxf(top, p.lse_part[slot(c) * tile_rows + row]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    fw[i] = wm[i] == -INFINITY ? 0.f : expf(wm[i] - M);
-    L += wl[i] * fw[i];
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float shift = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+  float2 acc[7];
+#pragma unroll
+  for (int k = 0; k < 7; ++k) acc[k] = make_float2(0.f, 0.f);
+  for (int c = first; c <= last; ++c) {
+    const int64_t at = static_cast<int64_t>(slot(c)) * tile_rows + row;
+    const float w = expf(p.lse_part[at] - shift);
+    sum += w;
+    const float2* o = reinterpret_cast<const float2*>(p.o_part + at * kNope) + lane;
+#pragma unroll
+    for (int k = 0; k < 7; ++k) {
+      const float2 v = o[32 * k];
+      acc[k].x = fmaf(w, v.x, acc[k].x);
+      acc[k].y = fmaf(w, v.y, acc[k].y);
+    }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  __nv_bfloat16* orow = a.out + (static_cast<int64_t>(t) * a.H + h) * kNope;
-  for (int c = threadIdx.x; c < kNope; c += blockDim.x)
-    orow[c] = __float2bfloat16_rn((wacc[0][c] * fw[0] + wacc[1][c] * fw[1] + wacc[2][c] * fw[2] +
-                                   wacc[3][c] * fw[3]) * inv);
-  if (threadIdx.x == 0) a.lse[static_cast<int64_t>(t) * a.H + h] = L > 0.f ? M + logf(L) : -INFINITY;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t orow = static_cast<int64_t>(tile.y) * a.H + row;
+  __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + orow * kNope) + lane;
+#pragma unroll
+  for (int k = 0; k < 7; ++k) out[32 * k] = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
+  if (lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : shift + logf(sum);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -151,9 +310,58 @@ int check_chunk(const smla_chunk_params* p) {
   if (!(std::isfinite(p->logit_cap) && p->logit_cap >= 0.f)) return SMLA_ERR_INVALID_ARG;
   if (p->num_heads != 16 && p->num_heads != 32 && p->num_heads != 64 && p->num_heads != 128)
     return SMLA_ERR_UNSUPPORTED_SHAPE;
-  if (p->batch > 65535 || static_cast<int64_t>(p->total_q) * p->num_heads >= (int64_t{1} << 30))
+  if (p->batch > 65535 || p->max_kv_tokens > (int64_t{1} << 30) || static_cast<int64_t>(p->total_q) * p->num_heads >= (int64_t{1} << 30))
     return SMLA_ERR_UNSUPPORTED_SHAPE;
   return SMLA_OK;
+}
+
+// Pairs of SMs of the GPU that this library is for: the workers that a workspace has
+// room for.
+constexpr int kMaxPairs = 76;
+constexpr int kMinShare = 4;     // blocks: a share pays for its query tile and its partial result
+
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// The workspace of a call; base may be null to size it.
+size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* q = base + at;
+    at += round256(bytes);
+    return q;
+  };
+  const size_t B = p->batch;
+  const size_t tiles = (static_cast<size_t>(p->total_q) * p->num_heads + kPairRows - 1) / kPairRows + B;
+  const int64_t cap = (p->max_kv_tokens + kChunkBlk - 1) / kChunkBlk + p->batch;
+  plan->cap_blocks = cap;
+  plan->head = reinterpret_cast<int32_t*>(take(256));
+  plan->tile = reinterpret_cast<int4*>(take(16 * tiles));
+  plan->cum = reinterpret_cast<int32_t*>(take(4 * (tiles + 1)));
+  plan->tile_base = reinterpret_cast<int32_t*>(take(4 * (B + 1)));
+  plan->seq_base = reinterpret_cast<int32_t*>(take(4 * (B + 1)));
+  plan->seq_len = reinterpret_cast<int32_t*>(take(4 * B));
+  plan->lse_part = reinterpret_cast<float*>(take(size_t{4} * 2 * kMaxPairs * kPairRows));
+  plan->o_part = reinterpret_cast<float*>(take(size_t{4} * 2 * kMaxPairs * kPairRows * kNope));
+  plan->seen = reinterpret_cast<ulonglong2*>(take(16 * static_cast<size_t>(cap + 1)));
+  plan->kv = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(cap + 1) * kChunkBlk * kQkDim * 2));
+  return at;
+}
+
+cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_t s) {
+  int workers = 0;
+  cudaError_t e = pair_workers(&workers);
+  if (e != cudaSuccess) return e;
+  if (workers > kMaxPairs) workers = kMaxPairs;
+  e = launch_programmatic(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, p, kPairRows, workers, kMinShare);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = p.cap_blocks + 1;
+  e = launch_programmatic(expand_kernel, dim3(static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8)), dim3(256),
+                          0, s, a, p);
+  if (e != cudaSuccess) return e;
+  e = launch_chunk_pair(a, p, workers, s);
+  if (e != cudaSuccess) return e;
+  if (workers < 2) return cudaSuccess;
+  return launch_programmatic(merge_kernel, dim3(kPairRows / 8, workers - 1), dim3(256), 0, s, a, p, kPairRows);
 }
 
 }  // namespace
@@ -167,7 +375,8 @@ int smla_chunk_workspace_size(const smla_chunk_params* p, size_t* bytes) {
   const int st = check_chunk(p);
   if (st != SMLA_OK) return st;
   if (bytes == nullptr) return SMLA_ERR_INVALID_ARG;
-  *bytes = 256;
+  ChunkPlan plan;
+  *bytes = lay_out(p, nullptr, &plan);
   return SMLA_OK;
 }
 
@@ -198,8 +407,9 @@ int smla_chunk_attention(const void* q, const void* kv_pages, const int32_t* blo
                        static_cast<__nv_bfloat16*>(out), lse, p->batch, p->num_heads, p->total_q,
                        p->page_size, p->max_pages, p->num_rows, p->kv_row_stride, p->softmax_scale,
                        p->logit_cap, status};
-  const cudaError_t e = launch_programmatic(chunk_plain_kernel, dim3(p->total_q, p->num_heads), dim3(128), 0,
-                                            reinterpret_cast<cudaStream_t>(stream), a);
+  ChunkPlan plan;
+  lay_out(p, static_cast<char*>(workspace), &plan);
+  const cudaError_t e = launch_pair_path(a, plan, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 

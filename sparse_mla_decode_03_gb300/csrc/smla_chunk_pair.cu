@@ -1,0 +1,512 @@
+// Chunk attention on pairs of SMs: the kernel for many query rows.
+//
+// The (token, head) rows of a sequence are cut into tiles of 256; all heads share K and V
+// (k = the 512-wide row, v = its first 448 columns), so a tile is a plain matrix problem:
+// S = Q K^T (256 x 64 x 512 a block of 64 positions), O += P V (256 x 448 x 64).
+//
+// What bounds it.  The tensor core needs 1,920 cycles a block (4,096 multiply-adds a
+// cycle and SM), and shared memory feeds it 128 bytes a cycle: with one SM on 128 rows,
+// Q alone (128 KB a block) would take as long as its product, and the same block of K and
+// V would be read by every SM.  A pair (tcgen05 cta_group::2) works on 256 rows: each SM
+// keeps half of the rows (Q, S, P, O) and brings half of the other operand, 32 of the 64
+// positions for K and half of the columns for V.  That is 80 KB of Q and K for 1,024
+// cycles of the first product (1,280 cycles of shared memory) and 60 KB of P and V for 896
+// of the second: together about 2,400 cycles a block with the incoming copies.
+// Tensor memory is full: O takes 448 columns, S the other 64.  So there is one S; the
+// softmax takes it into registers at once and P goes through shared memory, which
+// lets the scores of block i + 1 run while the softmax of block i does.
+//
+// K and V are read from an expanded copy (bf16 rows, the e4m3 values times their
+// powers of two: exact), which a kernel before this one writes once a call: 1.6 KB moved a
+// position, against 960 multiply-adds for each of its query rows.
+//
+// Warps of a CTA: 0..3 softmax and results (a thread a row), 4 tensor copies (one lane), 5
+// in the leading CTA issues the products (one lane).  Every wait is bounded.
+#include <cstring>
+#include <mutex>
+
+#include "smla_chunk.h"
+#include "smla_ptx.cuh"
+
+namespace smla {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kStages = 5;
+constexpr int kStage = 16384;      // K: 32 positions x 256 columns; V: 64 positions x 128 columns
+constexpr int kQBytes = 128 * 1024;
+constexpr int kRingOff = kQBytes;
+constexpr int kPOff = kRingOff + kStages * kStage;
+constexpr int kBarOff = kPOff + 128 * 128;
+constexpr int kSmem = kBarOff + 512 + 1024;
+constexpr uint32_t kColS = 448;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994530942f;
+// The running maximum is raised only when a score passes it by 2^8: the weights stay
+// exact in 32 bits (and in bf16's exponent range), and most blocks rescale nothing.
+constexpr float kHeadroom = 8.f;
+constexpr long long kWaitLimit = 2000000000ll;     // SM clocks, ~1 s
+
+// FULL: a stage's copies have landed in both CTAs (the leader's counts); EMPTY: the
+// products that read a stage are done; QFULL / QEMPTY: the same of Q; SFULL: the scores
+// of a block are in tensor memory; SEMPTY: both CTAs' softmax have taken them (leader);
+// PFULL: both have written P (leader); PV: the value product of a block is done; OEMPTY:
+// both have taken O (leader).
+enum Bar : int { FULL = 0, EMPTY = FULL + kStages, QFULL = EMPTY + kStages, QEMPTY, SFULL, SEMPTY, PFULL, PV, OEMPTY, kBars };
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const float* v) {
+  tmem_st16(taddr, v);
+  tmem_st16(taddr + 16, v + 16);
+}
+
+// A wait that gives up on its limit or when another role has.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* stop, int* status) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_cluster(bar, parity)) {
+    if (*stop) return false;
+    if (clock64() - t0 > kWaitLimit) {
+      *stop = 1;
+      atomicCAS(status, 0, SMLA_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// The same for a whole warp: one verdict for its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop, int* status) {
+  return __all_sync(0xffffffffu, wait(bar, parity, stop, status));
+}
+
+template <bool MODS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    pair_kernel(const ChunkArgs a, const ChunkPlan plan, const __grid_constant__ Maps maps) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int worker = blockIdx.x >> 1;
+  auto bar = [&](int i) { return sbase + kBarOff + 8u * static_cast<uint32_t>(i); };
+  volatile uint32_t* taddr = reinterpret_cast<volatile uint32_t*>(smem + kBarOff + 8 * kBars);
+  volatile int* stop = reinterpret_cast<volatile int*>(smem + kBarOff + 8 * kBars + 8);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBars; ++i)
+      mbar_init(bar(i), i == SEMPTY || i == PFULL || i == OEMPTY ? 8 : 1);
+    *stop = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc_pair(sbase + kBarOff + 8 * kBars, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive_wait();
+  tc_fence_after();
+  const uint32_t tmem = *taddr;
+  grid_dep_wait();
+  grid_dep_launch();
+
+  const int total = plan.head[1], per = plan.head[2], tiles = plan.head[0];
+  const int x0 = min(total, worker * per), x1 = min(total, x0 + per);
+  const int t_first = x0 < x1 ? find_last_le(plan.cum, tiles + 1, x0) : 0;
+  const int rows_of_token = a.H;
+
+  if (warp == 4) {
+    // ---------------- tensor copies ----------------
+    if (lane == 0) {
+      uint32_t n = 0;            // stages filled
+      uint32_t nq = 0;
+      bool ok = true;
+      const uint32_t full0 = dsmem_addr(bar(FULL), 0), qfull = dsmem_addr(bar(QFULL), 0);
+      auto stage = [&](uint32_t* dst) {       // the next free stage
+        const uint32_t s = n % kStages, use = n / kStages;
+        if (use > 0) ok = ok && wait(bar(EMPTY + s), (use - 1) & 1, stop, a.status);
+        if (!ok) return 0u;
+        if (rank == 0) mbar_arrive_expect_tx(bar(FULL + s), 2 * kStage);
+        *dst = sbase + kRingOff + s * kStage;
+        ++n;
+        return full0 + 8 * s;
+      };
+      for (int x = x0, t = t_first; ok && x < x1; ++t) {
+        const int4 tile = plan.tile[t];
+        const int begin = plan.cum[t], end = min(x1, plan.cum[t + 1]);
+        const int nb = end - x;
+        const int row0 = (plan.seq_base[tile.x] + tile.w + (x - begin)) * kChunkBlk;
+        if (nq > 0) ok = wait(bar(QEMPTY), (nq - 1) & 1, stop, a.status);
+        if (!ok) break;
+        ++nq;
+        if (rank == 0) mbar_arrive_expect_tx(bar(QFULL), 2 * kQBytes);
+        for (int c = 0; c < 8; ++c)
+          tma_load_2d_pair(sbase + c * 16384, &maps.q, 64 * c, tile.y * rows_of_token + 128 * rank, qfull);
+        for (int i = 0; ok && i <= nb; ++i) {
+          if (i < nb) {
+            for (int h = 0; ok && h < 2; ++h) {
+              uint32_t dst;
+              const uint32_t f = stage(&dst);
+              if (!ok) break;
+              for (int c = 0; c < 4; ++c)
+                tma_load_2d_pair(dst + c * 4096, &maps.k, 256 * h + 64 * c, row0 + i * kChunkBlk + 32 * rank, f);
+            }
+          }
+          if (i > 0) {
+            for (int h = 0; ok && h < 2; ++h) {
+              uint32_t dst;
+              const uint32_t f = stage(&dst);
+              if (!ok) break;
+              // columns 0..255 in halves of 128; 256..447 in halves of 96 (and 32 not read)
+              const int col = h == 0 ? 128 * rank : 256 + 96 * rank;
+              for (int c = 0; c < 2; ++c)
+                tma_load_2d_pair(dst + c * 8192, &maps.v, col + 64 * c, row0 + (i - 1) * kChunkBlk, f);
+            }
+          }
+        }
+        x = end;
+      }
+      if (!ok) {   // copies in flight land within microseconds: 1 ms before shared memory goes
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
+        }
+      }
+    }
+  } else if (warp == 5) {
+    // ---------------- products ----------------
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t kIdQK = idesc_bf16(256, 64, false, false);
+      constexpr uint32_t kIdV0 = idesc_bf16(256, 256, false, true);
+      constexpr uint32_t kIdV1 = idesc_bf16(256, 192, false, true);
+      const uint64_t dq = smem_desc(sbase, 16, 1024, SWZ_128B);
+      const uint64_t dk = smem_desc(sbase + kRingOff, 16, 1024, SWZ_128B);
+      const uint64_t dv = smem_desc(sbase + kRingOff, 8192, 1024, SWZ_128B);
+      const uint64_t dp = smem_desc(sbase + kPOff, 16, 1024, SWZ_128B);
+      uint32_t n = 0, nq = 0, ns = 0, np = 0;      // stages, tiles, scores and value products so far
+      bool ok = true;
+      auto full = [&](uint32_t* s) {
+        *s = n % kStages;
+        ok = ok && wait(bar(FULL + *s), (n / kStages) & 1, stop, a.status);
+        tc_fence_after();
+        ++n;
+      };
+      for (int x = x0, t = t_first; ok && x < x1; ++t) {
+        const int end = min(x1, plan.cum[t + 1]);
+        const int nb = end - x;
+        ok = wait(bar(QFULL), nq & 1, stop, a.status);
+        for (int i = 0; ok && i <= nb; ++i) {
+          if (i < nb) {
+            if (ns > 0) ok = wait(bar(SEMPTY), (ns - 1) & 1, stop, a.status);
+            for (int h = 0; ok && h < 2; ++h) {
+              uint32_t s;
+              full(&s);
+              if (!ok) break;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_f16_ss_pair(tmem + kColS, dq + (((4 * h + c) * 16384 + k * 32) >> 4),
+                                  dk + ((s * kStage + c * 4096 + k * 32) >> 4), kIdQK, (h | c | k) != 0);
+              mma_commit_pair(bar(EMPTY + s));
+            }
+            if (!ok) break;
+            mma_commit_pair(bar(SFULL));
+            ++ns;
+            if (i == nb - 1) mma_commit_pair(bar(QEMPTY));
+          }
+          if (i > 0) {
+            ok = wait(bar(PFULL), np & 1, stop, a.status);
+            if (ok && i == 1 && nq > 0) ok = wait(bar(OEMPTY), (nq - 1) & 1, stop, a.status);
+            for (int h = 0; ok && h < 2; ++h) {
+              uint32_t s;
+              full(&s);
+              if (!ok) break;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_f16_ss_pair(tmem + 256 * h, dp + ((k * 32) >> 4), dv + ((s * kStage + k * 2048) >> 4),
+                                h == 0 ? kIdV0 : kIdV1, i > 1 || k > 0);
+              mma_commit_pair(bar(EMPTY + s));
+            }
+            if (!ok) break;
+            mma_commit_pair(bar(PV));
+            ++np;
+          }
+        }
+        ++nq;
+        x = end;
+      }
+      if (!ok) {   // let issued products drain before tensor memory is freed
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
+        }
+      }
+    }
+  } else {
+    // ---------------- softmax and results: thread = row ----------------
+    const int r = threadIdx.x;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tS = tmem + kColS + lanes, tO = tmem + lanes;
+    const uint32_t sempty = dsmem_addr(bar(SEMPTY), 0), pfull = dsmem_addr(bar(PFULL), 0),
+                   oempty = dsmem_addr(bar(OEMPTY), 0);
+    const uint32_t prow = sbase + kPOff + r * 128;
+    const float scale2 = a.scale * kLog2e;
+    uint32_t ns = 0, np = 0;
+    bool ok = true;
+    for (int x = x0, t = t_first; ok && x < x1; ++t) {
+      const int4 tile = plan.tile[t];
+      const int begin = plan.cum[t], after = plan.cum[t + 1], end = min(x1, after);
+      const int nb = end - x;
+      const int b = tile.x, base = plan.seq_base[b], blk = tile.w + (x - begin);
+      const int row = static_cast<int>(rank) * 128 + r;
+      const int tok = row / rows_of_token, head = row % rows_of_token;
+      const bool mine = tok < tile.z;
+      int lo = 0, hi = 0, pos = 0;
+      if (mine) visible(a, b, tile.y + tok, plan.seq_len[b], &lo, &hi, &pos);
+      const float slope2 = MODS && a.slopes != nullptr ? a.slopes[head] * kLog2e : 0.f;
+      // l sums the weights for the lse, lr their bf16 roundings, which the value product
+      // uses: normalised by lr, a rounding moves out by its weight times v - out only
+      float m = -INFINITY, l = 0.f, lr = 0.f;
+      for (int i = 0; ok && i < nb; ++i) {
+        const ulonglong2 rows = plan.seen[base + blk + i];
+        ok = warp_wait(bar(SFULL), ns & 1, stop, a.status);
+        ++ns;
+        if (!ok) break;
+        tc_fence_after();
+        float v[64];
+        tmem_ld32(tS, v);
+        tmem_ld32(tS + 32, v + 32);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(sempty);
+        const int s0 = (blk + i) * kChunkBlk;
+        if constexpr (MODS) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            float y = v[c];
+            if (a.cap > 0.f) {
+              // cap tanh(z), z = scale x / cap, tanh(z) = 1 - 2 / (1 + e^(2 z))
+              const float e = exp2_fast(y * (2.f * scale2 / a.cap));
+              y = a.cap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
+            } else {
+              y *= scale2;
+            }
+            v[c] = y - slope2 * fabsf(static_cast<float>(pos - (s0 + c)));
+          }
+        }
+        // positions of the block that the row sees
+        const int c0 = max(0, lo - s0), c1 = min(64, hi - s0);
+        unsigned long long seen = rows.x;
+        if (c0 > 0 || c1 < 64)
+          seen = c1 > c0 ? rows.x & (~0ull << c0) & (~0ull >> (64 - c1)) : 0ull;
+        if (__any_sync(0xffffffffu, seen != ~0ull)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!((seen >> c) & 1)) v[c] = -INFINITY;
+        }
+        float top = fmaxf(v[0], v[1]);
+#pragma unroll
+        for (int c = 2; c < 64; ++c) top = fmaxf(top, v[c]);
+        if constexpr (!MODS) top *= scale2;
+        float alpha = 1.f;
+        if (top > m + kHeadroom || (m == -INFINITY && top > m)) {
+          alpha = exp2_fast(m - top);     // 0 while m is -inf
+          m = top;
+          l *= alpha;
+          lr *= alpha;
+        }
+        const float shift = m == -INFINITY ? 0.f : m;
+        uint32_t p[32];
+        float sum0 = 0.f, sum1 = 0.f, rsum0 = 0.f, rsum1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float e0 = exp2_fast(MODS ? v[c] - shift : fmaf(v[c], scale2, -shift));
+          const float e1 = exp2_fast(MODS ? v[c + 1] - shift : fmaf(v[c + 1], scale2, -shift));
+          sum0 += e0;
+          sum1 += e1;
+          p[c / 2] = pack_bf16(e0, e1);
+          rsum0 += __uint_as_float(p[c / 2] << 16);
+          rsum1 += __uint_as_float(p[c / 2] & 0xffff0000u);
+        }
+        l += sum0 + sum1;
+        lr += rsum0 + rsum1;
+        // the copy holds zeros for a row with NaN or infinities, which would reach every row
+        // of the tile through the value product; the rows that see it become NaN here
+        if (seen & rows.y) l = lr = __uint_as_float(0x7fffffffu);
+        // the value product before this one is done: P may be written, O rescaled
+        if (i > 0) {
+          ok = warp_wait(bar(PV), (np - 1) & 1, stop, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < kNope; c += 32) {
+              float o[32];
+              tmem_ld32(tO + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= alpha;
+              tmem_store32(tO + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(prow + ((u ^ (r & 7)) << 4)), "r"(p[4 * u]),
+                       "r"(p[4 * u + 1]), "r"(p[4 * u + 2]), "r"(p[4 * u + 3])
+                       : "memory");
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(pfull);
+        ++np;
+      }
+      if (!ok) break;
+      ok = warp_wait(bar(PV), (np - 1) & 1, stop, a.status);
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / lr;       // NaN stays NaN
+      const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      const bool whole = begin >= x0 && after <= x1;
+      const int64_t orow = static_cast<int64_t>(tile.y) * rows_of_token + row;
+      const int slot = 2 * worker + (begin < x0 ? 0 : 1);
+      __nv_bfloat16* od = a.out + orow * kNope;
+      float* pd = plan.o_part + (static_cast<int64_t>(slot) * kPairRows + row) * kNope;
+#pragma unroll 1
+      for (int c = 0; c < kNope; c += 32) {
+        float o[32];
+        tmem_ld32(tO + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] *= inv;
+        if (mine) {
+          if (whole) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4*>(od + c + k) =
+                  make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
+                             pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(pd + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(oempty);
+      if (mine) {
+        if (whole) a.lse[orow] = lse;
+        else plan.lse_part[slot * kPairRows + row] = lse;
+      }
+      x = end;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive_wait();       // neither CTA's shared or tensor memory goes while the other uses it
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+std::mutex g_mu;
+
+template <bool MODS>
+cudaError_t configure(int dev) {
+  static bool done[64] = {};
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (done[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(pair_kernel<MODS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
+
+cudaError_t encode(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
+  const EncodeTiledFn fn = encode_tiled();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dim[2] = {kQkDim, static_cast<cuuint64_t>(rows)};
+  const cuuint64_t pitch[1] = {kQkDim * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t step[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dim, pitch, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <bool MODS>
+cudaError_t launch(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = configure<MODS>(dev);
+  if (e != cudaSuccess) return e;
+  Maps maps;
+  std::memset(static_cast<void*>(&maps), 0, sizeof(maps));
+  const int64_t kv_rows = (p.cap_blocks + 1) * kChunkBlk;
+  e = encode(&maps.q, a.q, static_cast<int64_t>(a.T) * a.H, 128);
+  if (e == cudaSuccess) e = encode(&maps.k, p.kv, kv_rows, 32);
+  if (e == cudaSuccess) e = encode(&maps.v, p.kv, kv_rows, 64);
+  if (e != cudaSuccess) return e;
+  return launch_programmatic(pair_kernel<MODS>, dim3(2 * workers), dim3(kThreads), kSmem, stream, a, p, maps);
+}
+
+}  // namespace
+
+// Pairs that the current device holds at once: asked once a device.
+cudaError_t pair_workers(int* workers) {
+  static int known[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = configure<false>(dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (known[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, pair_kernel<false>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorNotSupported;
+    known[dev] = n;
+  }
+  *workers = known[dev];
+  return cudaSuccess;
+}
+
+cudaError_t launch_chunk_pair(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStream_t stream) {
+  return a.cap > 0.f || a.slopes != nullptr ? launch<true>(a, p, workers, stream)
+                                            : launch<false>(a, p, workers, stream);
+}
+
+}  // namespace smla

@@ -1594,22 +1594,6 @@ cudaError_t configure(int dev) {
   return cudaSuccess;
 }
 
-// cuTensorMapEncodeTiled from the driver, looked up once through the runtime (the
-// library does not link against the driver library).
-using EncodeTiledFn = decltype(&cuTensorMapEncodeTiled);
-EncodeTiledFn encode_tiled() {
-  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
-}
-
 // The tensor maps of a launch: the gather maps of a cache of num_rows (>= 1) rows,
 // `stride` bytes apart (a multiple of 8, >= 584), starting at the 16-byte aligned kv
 // (elements of 8 bytes, boxes of one 74-word window), and the map of the 16-byte
