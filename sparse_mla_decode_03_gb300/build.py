@@ -24,7 +24,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v
          "-I", os.path.join(ROOT, "include")]
 SOURCES = ["smla_decode.cu", "smla_combine.cu", "smla_api.cu", "smla_noalloc.cu", "smla_simt.cu",
            "smla_paged.cu", "smla_cache.cu", "smla_chunk.cu",
-           "smla_chunk_pair.cu"]
+           "smla_chunk_pair.cu", "smla_chunk_single.cu"]
 
 
 def nvcc() -> str:

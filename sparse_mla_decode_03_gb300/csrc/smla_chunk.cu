@@ -56,7 +56,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   __shared__ long long sums[32];
   grid_dep_wait();
   grid_dep_launch();
-  const int tokens_of_tile = tile_rows / a.H;
   long long tiles = 0, blocks = 0;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + static_cast<int>(threadIdx.x);
@@ -66,7 +65,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
       n = min(max(a.cu_q[b + 1], first), a.T) - first;
       len = max(a.kv_lens[b], 0);
     }
-    const int nt = (n + tokens_of_tile - 1) / tokens_of_tile;
+    const int nt = (n * a.H + tile_rows - 1) / tile_rows;      // total_q * H < 2^30
     // a sequence without cached tokens keeps one block (of zeros) for its tiles to read
     const int nb = n > 0 ? max(1, (len + kChunkBlk - 1) / kChunkBlk) : 0;
     long long t_all, b_all;
@@ -98,12 +97,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     if (t < tiles) {
       const int b = find_last_le(p.tile_base, a.B + 1, t);
       const int first = min(max(a.cu_q[b], 0), a.T), last = min(max(a.cu_q[b + 1], first), a.T);
-      const int tok = first + (t - p.tile_base[b]) * tokens_of_tile;
-      const int count = min(tokens_of_tile, last - tok);
+      const int row = first * a.H + (t - p.tile_base[b]) * tile_rows;
+      const int rows = min(tile_rows, last * a.H - row);
       int low = 0x7fffffff, high = 0;
-      for (int j = 0; j < count; ++j) {
+      for (int tok = row / a.H; tok <= (row + rows - 1) / a.H; ++tok) {
         int lo, hi, pos;
-        visible(a, b, tok + j, p.seq_len[b], &lo, &hi, &pos);
+        visible(a, b, tok, p.seq_len[b], &lo, &hi, &pos);
         if (hi > lo) {
           low = min(low, lo);
           high = max(high, hi);
@@ -111,7 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
       }
       const int blk = high > 0 ? low / kChunkBlk : 0;
       n = high > 0 ? (high - 1) / kChunkBlk + 1 - blk : 1;
-      tile = make_int4(b, tok, count, blk);
+      tile = make_int4(b, row, rows, blk);
     }
     long long all;
     const long long at = line + block_sum(n, &all, sums);
@@ -265,7 +264,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const Chu
   if (begin == x || begin / per + 1 != c1) return;
   const int4 tile = p.tile[t];
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= tile.z * a.H) return;
+  if (row >= tile.z) return;
   const int first = c1 - 1, last = (end - 1) / per;
   // slot of worker c: its share begins inside the tile (0), or the tile inside its share (1)
   auto slot = [&](int c) { return 2 * c + (begin < c * per ? 0 : 1); };
@@ -291,7 +290,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const Chu
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t orow = static_cast<int64_t>(tile.y) * a.H + row;
+  const int64_t orow = static_cast<int64_t>(tile.y) + row;
   __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + orow * kNope) + lane;
 #pragma unroll
   for (int k = 0; k < 7; ++k) out[32 * k] = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
@@ -315,9 +314,10 @@ int check_chunk(const smla_chunk_params* p) {
   return SMLA_OK;
 }
 
-// Pairs of SMs of the GPU that this library is for: the workers that a workspace has
-// room for.
-constexpr int kMaxPairs = 76;
+// SMs of the GPU that this library is for: the workers that a workspace has room for (a
+// pair of SMs with 256 rows each needs twice what two SMs with 64 do).
+constexpr int kMaxSms = 152;
+constexpr int kMaxPairs = kMaxSms / 2;
 constexpr int kMinShare = 4;     // blocks: a share pays for its query tile and its partial result
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -331,7 +331,7 @@ size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
     return q;
   };
   const size_t B = p->batch;
-  const size_t tiles = (static_cast<size_t>(p->total_q) * p->num_heads + kPairRows - 1) / kPairRows + B;
+  const size_t tiles = (static_cast<size_t>(p->total_q) * p->num_heads + kSingleRows - 1) / kSingleRows + B;
   const int64_t cap = (p->max_kv_tokens + kChunkBlk - 1) / kChunkBlk + p->batch;
   plan->cap_blocks = cap;
   plan->head = reinterpret_cast<int32_t*>(take(256));
@@ -347,6 +347,11 @@ size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
   return at;
 }
 
+cudaError_t launch_merge(const ChunkArgs& a, const ChunkPlan& p, int rows, int workers, cudaStream_t s) {
+  if (workers < 2) return cudaSuccess;
+  return launch_programmatic(merge_kernel, dim3(rows / 8, workers - 1), dim3(256), 0, s, a, p, rows);
+}
+
 cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_t s) {
   int workers = 0;
   cudaError_t e = pair_workers(&workers);
@@ -355,13 +360,24 @@ cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_
   e = launch_programmatic(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, p, kPairRows, workers, kMinShare);
   if (e != cudaSuccess) return e;
   const int64_t blocks = p.cap_blocks + 1;
-  e = launch_programmatic(expand_kernel, dim3(static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8)), dim3(256),
-                          0, s, a, p);
+  e = launch_programmatic(expand_kernel, dim3(static_cast<unsigned>(blocks < kMaxSms * 8 ? blocks : kMaxSms * 8)),
+                          dim3(256), 0, s, a, p);
   if (e != cudaSuccess) return e;
   e = launch_chunk_pair(a, p, workers, s);
-  if (e != cudaSuccess) return e;
-  if (workers < 2) return cudaSuccess;
-  return launch_programmatic(merge_kernel, dim3(kPairRows / 8, workers - 1), dim3(256), 0, s, a, p, kPairRows);
+  return e == cudaSuccess ? launch_merge(a, p, kPairRows, workers, s) : e;
+}
+
+cudaError_t launch_single_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_t s) {
+  const int workers = kMaxSms;
+  cudaError_t e = launch_programmatic(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, p, kSingleRows, workers,
+                                      kMinShare);
+  if (e == cudaSuccess) e = launch_chunk_single(a, p, workers, s);
+  return e == cudaSuccess ? launch_merge(a, p, kSingleRows, workers, s) : e;
+}
+
+// Which kernel: pairs once a sequence brings a full tile of 256 rows on average.
+bool use_pairs(const smla_chunk_params* p) {
+  return static_cast<int64_t>(p->total_q) * p->num_heads >= static_cast<int64_t>(kPairRows) * p->batch;
 }
 
 }  // namespace
@@ -409,7 +425,8 @@ int smla_chunk_attention(const void* q, const void* kv_pages, const int32_t* blo
                        p->logit_cap, status};
   ChunkPlan plan;
   lay_out(p, static_cast<char*>(workspace), &plan);
-  const cudaError_t e = launch_pair_path(a, plan, reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = use_pairs(p) ? launch_pair_path(a, plan, s) : launch_single_path(a, plan, s);
   return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 

@@ -32,7 +32,7 @@ struct ChunkArgs {
 // the others leave partial results that the merge joins.
 struct ChunkPlan {
   int32_t* head;         // [0] tiles, [1] blocks on the line, [2] blocks a share
-  int4* tile;            // sequence, first token, tokens, first block
+  int4* tile;            // sequence, first row (token * H + head), rows, first block
   int32_t* cum;          // [tiles + 1] start of each tile on the line
   int32_t* tile_base;    // [B + 1] first tile of each sequence
   int32_t* seq_base;     // [B + 1] first block of each sequence in the expanded copy
@@ -67,5 +67,12 @@ __device__ __forceinline__ void visible(const ChunkArgs& a, int b, int t, int le
 constexpr int kPairRows = 256;
 cudaError_t pair_workers(int* workers);
 cudaError_t launch_chunk_pair(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStream_t stream);
+
+// Single kernel: tiles of 64 rows on one SM each, which expands the rows itself.
+constexpr int kSingleRows = 64;
+cudaError_t launch_chunk_single(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStream_t stream);
+
+// The tensor map of `rows` rows of 512 bf16, in boxes of 64 columns, 128-byte swizzle.
+cudaError_t encode_rows(CUtensorMap* map, const void* base, int64_t rows, int box_rows);
 
 }  // namespace smla

@@ -26,6 +26,7 @@
 #include <mutex>
 
 #include "smla_chunk.h"
+#include "smla_chunk_rows.cuh"
 #include "smla_ptx.cuh"
 
 namespace smla {
@@ -40,13 +41,6 @@ constexpr int kPOff = kRingOff + kStages * kStage;
 constexpr int kBarOff = kPOff + 128 * 128;
 constexpr int kSmem = kBarOff + 512 + 1024;
 constexpr uint32_t kColS = 448;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.69314718055994530942f;
-// The running maximum is raised only when a score passes it by 2^8: the weights stay
-// exact in 32 bits (and in bf16's exponent range), and most blocks rescale nothing.
-constexpr float kHeadroom = 8.f;
-constexpr long long kWaitLimit = 2000000000ll;     // SM clocks, ~1 s
-
 // FULL: a stage's copies have landed in both CTAs (the leader's counts); EMPTY: the
 // products that read a stage are done; QFULL / QEMPTY: the same of Q; SFULL: the scores
 // of a block are in tensor memory; SEMPTY: both CTAs' softmax have taken them (leader);
@@ -57,41 +51,6 @@ enum Bar : int { FULL = 0, EMPTY = FULL + kStages, QFULL = EMPTY + kStages, QEMP
 struct Maps {
   CUtensorMap q, k, v;
 };
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ void tmem_store32(uint32_t taddr, const float* v) {
-  tmem_st16(taddr, v);
-  tmem_st16(taddr + 16, v + 16);
-}
-
-// A wait that gives up on its limit or when another role has.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* stop, int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*stop) return false;
-    if (clock64() - t0 > kWaitLimit) {
-      *stop = 1;
-      atomicCAS(status, 0, SMLA_ERR_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-
-// The same for a whole warp: one verdict for its lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop, int* status) {
-  return __all_sync(0xffffffffu, wait(bar, parity, stop, status));
-}
 
 template <bool MODS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -128,7 +87,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int total = plan.head[1], per = plan.head[2], tiles = plan.head[0];
   const int x0 = min(total, worker * per), x1 = min(total, x0 + per);
   const int t_first = x0 < x1 ? find_last_le(plan.cum, tiles + 1, x0) : 0;
-  const int rows_of_token = a.H;
 
   if (warp == 4) {
     // ---------------- tensor copies ----------------
@@ -156,7 +114,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++nq;
         if (rank == 0) mbar_arrive_expect_tx(bar(QFULL), 2 * kQBytes);
         for (int c = 0; c < 8; ++c)
-          tma_load_2d_pair(sbase + c * 16384, &maps.q, 64 * c, tile.y * rows_of_token + 128 * rank, qfull);
+          tma_load_2d_pair(sbase + c * 16384, &maps.q, 64 * c, tile.y + 128 * rank, qfull);
         for (int i = 0; ok && i <= nb; ++i) {
           if (i < nb) {
             for (int h = 0; ok && h < 2; ++h) {
@@ -278,23 +236,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t sempty = dsmem_addr(bar(SEMPTY), 0), pfull = dsmem_addr(bar(PFULL), 0),
                    oempty = dsmem_addr(bar(OEMPTY), 0);
     const uint32_t prow = sbase + kPOff + r * 128;
-    const float scale2 = a.scale * kLog2e;
     uint32_t ns = 0, np = 0;
     bool ok = true;
     for (int x = x0, t = t_first; ok && x < x1; ++t) {
       const int4 tile = plan.tile[t];
       const int begin = plan.cum[t], after = plan.cum[t + 1], end = min(x1, after);
       const int nb = end - x;
-      const int b = tile.x, base = plan.seq_base[b], blk = tile.w + (x - begin);
+      const int base = plan.seq_base[tile.x], blk = tile.w + (x - begin);
       const int row = static_cast<int>(rank) * 128 + r;
-      const int tok = row / rows_of_token, head = row % rows_of_token;
-      const bool mine = tok < tile.z;
-      int lo = 0, hi = 0, pos = 0;
-      if (mine) visible(a, b, tile.y + tok, plan.seq_len[b], &lo, &hi, &pos);
-      const float slope2 = MODS && a.slopes != nullptr ? a.slopes[head] * kLog2e : 0.f;
-      // l sums the weights for the lse, lr their bf16 roundings, which the value product
-      // uses: normalised by lr, a rounding moves out by its weight times v - out only
-      float m = -INFINITY, l = 0.f, lr = 0.f;
+      const bool mine = row < tile.z;
+      RowState<MODS> st(a, plan, tile, row, mine);
       for (int i = 0; ok && i < nb; ++i) {
         const ulonglong2 rows = plan.seen[base + blk + i];
         ok = warp_wait(bar(SFULL), ns & 1, stop, a.status);
@@ -308,83 +259,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(sempty);
-        const int s0 = (blk + i) * kChunkBlk;
-        if constexpr (MODS) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            float y = v[c];
-            if (a.cap > 0.f) {
-              // cap tanh(z), z = scale x / cap, tanh(z) = 1 - 2 / (1 + e^(2 z))
-              const float e = exp2_fast(y * (2.f * scale2 / a.cap));
-              y = a.cap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
-            } else {
-              y *= scale2;
-            }
-            v[c] = y - slope2 * fabsf(static_cast<float>(pos - (s0 + c)));
-          }
-        }
-        // positions of the block that the row sees
-        const int c0 = max(0, lo - s0), c1 = min(64, hi - s0);
-        unsigned long long seen = rows.x;
-        if (c0 > 0 || c1 < 64)
-          seen = c1 > c0 ? rows.x & (~0ull << c0) & (~0ull >> (64 - c1)) : 0ull;
-        if (__any_sync(0xffffffffu, seen != ~0ull)) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!((seen >> c) & 1)) v[c] = -INFINITY;
-        }
-        float top = fmaxf(v[0], v[1]);
-#pragma unroll
-        for (int c = 2; c < 64; ++c) top = fmaxf(top, v[c]);
-        if constexpr (!MODS) top *= scale2;
-        float alpha = 1.f;
-        if (top > m + kHeadroom || (m == -INFINITY && top > m)) {
-          alpha = exp2_fast(m - top);     // 0 while m is -inf
-          m = top;
-          l *= alpha;
-          lr *= alpha;
-        }
-        const float shift = m == -INFINITY ? 0.f : m;
         uint32_t p[32];
-        float sum0 = 0.f, sum1 = 0.f, rsum0 = 0.f, rsum1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          const float e0 = exp2_fast(MODS ? v[c] - shift : fmaf(v[c], scale2, -shift));
-          const float e1 = exp2_fast(MODS ? v[c + 1] - shift : fmaf(v[c + 1], scale2, -shift));
-          sum0 += e0;
-          sum1 += e1;
-          p[c / 2] = pack_bf16(e0, e1);
-          rsum0 += __uint_as_float(p[c / 2] << 16);
-          rsum1 += __uint_as_float(p[c / 2] & 0xffff0000u);
-        }
-        l += sum0 + sum1;
-        lr += rsum0 + rsum1;
-        // the copy holds zeros for a row with NaN or infinities, which would reach every row
-        // of the tile through the value product; the rows that see it become NaN here
-        if (seen & rows.y) l = lr = __uint_as_float(0x7fffffffu);
+        const float alpha = st.weights(v, (blk + i) * kChunkBlk, rows, p);
         // the value product before this one is done: P may be written, O rescaled
         if (i > 0) {
           ok = warp_wait(bar(PV), (np - 1) & 1, stop, a.status);
           if (!ok) break;
           tc_fence_after();
-          if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-            for (int c = 0; c < kNope; c += 32) {
-              float o[32];
-              tmem_ld32(tO + c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= alpha;
-              tmem_store32(tO + c, o);
-            }
-            tmem_wait_st();
-          }
+          rescale_rows(tO, alpha);
         }
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(prow + ((u ^ (r & 7)) << 4)), "r"(p[4 * u]),
-                       "r"(p[4 * u + 1]), "r"(p[4 * u + 2]), "r"(p[4 * u + 3])
-                       : "memory");
+        store_weights(sbase + kPOff, r, p);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -395,41 +279,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = warp_wait(bar(PV), (np - 1) & 1, stop, a.status);
       if (!ok) break;
       tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / lr;       // NaN stays NaN
-      const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      const bool whole = begin >= x0 && after <= x1;
-      const int64_t orow = static_cast<int64_t>(tile.y) * rows_of_token + row;
-      const int slot = 2 * worker + (begin < x0 ? 0 : 1);
-      __nv_bfloat16* od = a.out + orow * kNope;
-      float* pd = plan.o_part + (static_cast<int64_t>(slot) * kPairRows + row) * kNope;
-#pragma unroll 1
-      for (int c = 0; c < kNope; c += 32) {
-        float o[32];
-        tmem_ld32(tO + c, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] *= inv;
-        if (mine) {
-          if (whole) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 8)
-              *reinterpret_cast<uint4*>(od + c + k) =
-                  make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
-                             pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(pd + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-          }
-        }
-      }
+      store_rows<kPairRows>(a, plan, st, tO, tile, row, mine, begin >= x0 && after <= x1,
+                            2 * worker + (begin < x0 ? 0 : 1));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(oempty);
-      if (mine) {
-        if (whole) a.lse[orow] = lse;
-        else plan.lse_part[slot * kPairRows + row] = lse;
-      }
       x = end;
     }
   }
@@ -455,7 +309,26 @@ cudaError_t configure(int dev) {
   return e;
 }
 
-cudaError_t encode(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
+template <bool MODS>
+cudaError_t launch(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = configure<MODS>(dev);
+  if (e != cudaSuccess) return e;
+  Maps maps;
+  std::memset(static_cast<void*>(&maps), 0, sizeof(maps));
+  const int64_t kv_rows = (p.cap_blocks + 1) * kChunkBlk;
+  e = encode_rows(&maps.q, a.q, static_cast<int64_t>(a.T) * a.H, 128);
+  if (e == cudaSuccess) e = encode_rows(&maps.k, p.kv, kv_rows, 32);
+  if (e == cudaSuccess) e = encode_rows(&maps.v, p.kv, kv_rows, 64);
+  if (e != cudaSuccess) return e;
+  return launch_programmatic(pair_kernel<MODS>, dim3(2 * workers), dim3(kThreads), kSmem, stream, a, p, maps);
+}
+
+}  // namespace
+
+cudaError_t encode_rows(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
   const EncodeTiledFn fn = encode_tiled();
   if (fn == nullptr) return cudaErrorNotSupported;
   const cuuint64_t dim[2] = {kQkDim, static_cast<cuuint64_t>(rows)};
@@ -467,25 +340,6 @@ cudaError_t encode(CUtensorMap* m, const void* base, int64_t rows, int box_rows)
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
-
-template <bool MODS>
-cudaError_t launch(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStream_t stream) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  e = configure<MODS>(dev);
-  if (e != cudaSuccess) return e;
-  Maps maps;
-  std::memset(static_cast<void*>(&maps), 0, sizeof(maps));
-  const int64_t kv_rows = (p.cap_blocks + 1) * kChunkBlk;
-  e = encode(&maps.q, a.q, static_cast<int64_t>(a.T) * a.H, 128);
-  if (e == cudaSuccess) e = encode(&maps.k, p.kv, kv_rows, 32);
-  if (e == cudaSuccess) e = encode(&maps.v, p.kv, kv_rows, 64);
-  if (e != cudaSuccess) return e;
-  return launch_programmatic(pair_kernel<MODS>, dim3(2 * workers), dim3(kThreads), kSmem, stream, a, p, maps);
-}
-
-}  // namespace
 
 // Pairs that the current device holds at once: asked once a device.
 cudaError_t pair_workers(int* workers) {

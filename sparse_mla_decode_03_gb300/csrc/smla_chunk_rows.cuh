@@ -1,0 +1,187 @@
+// What a thread of the chunk attention does with its (token, head) row: the weights of a
+// block of 64 positions from its scores, and the row's result.  Shared by the kernels that
+// differ in how they bring scores and value products about.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "smla_chunk.h"
+#include "smla_ptx.cuh"
+
+namespace smla {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994530942f;
+// The running maximum is raised only when a score passes it by 2^8: sums stay well inside
+// 32 bits, a weight's bf16 rounding is relative, and most blocks rescale nothing.
+constexpr float kHeadroom = 8.f;
+constexpr long long kWaitLimit = 2000000000ll;     // SM clocks, ~1 s
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A wait that gives up on its limit or when another role has.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* stop, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*stop) return false;
+    if (clock64() - t0 > kWaitLimit) {
+      *stop = 1;
+      atomicCAS(status, 0, SMLA_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+// The same for a whole warp: one verdict for its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop, int* status) {
+  return __all_sync(0xffffffffu, wait(bar, parity, stop, status));
+}
+
+// MODS: scores may be capped or biased by distance.
+template <bool MODS>
+struct RowState {
+  // l sums the weights for the lse, lr their bf16 roundings, which the value product uses:
+  // normalised by lr, a rounding moves out by its weight times v - out only
+  float m = -INFINITY, l = 0.f, lr = 0.f;
+  int lo = 0, hi = 0, pos = 0;       // visible positions, own position
+  float scale2, cap, slope2 = 0.f;
+
+  __device__ __forceinline__ RowState(const ChunkArgs& a, const ChunkPlan& plan, const int4& tile, int row,
+                                      bool mine)
+      : scale2(a.scale * kLog2e), cap(a.cap) {
+    if (!mine) return;
+    const int tok = (tile.y + row) / a.H;
+    visible(a, tile.x, tok, plan.seq_len[tile.x], &lo, &hi, &pos);
+    if (MODS && a.slopes != nullptr) slope2 = a.slopes[tile.y + row - tok * a.H] * kLog2e;
+  }
+
+  // The row's scores v of the block that starts at position s0 -> its weights p (bf16
+  // pairs).  rows: the block's mapped positions, and those whose row is not finite.
+  // Returns the factor by which earlier results of the row shrink.
+  __device__ __forceinline__ float weights(float (&v)[64], int s0, const ulonglong2& rows, uint32_t (&p)[32]) {
+    if constexpr (MODS) {
+#pragma unroll
+      for (int c = 0; c < 64; ++c) {
+        float y = v[c];
+        if (cap > 0.f) {
+          // cap tanh(z), z = scale x / cap, tanh(z) = 1 - 2 / (1 + e^(2 z))
+          const float e = exp2_fast(y * (2.f * scale2 / cap));
+          y = cap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
+        } else {
+          y *= scale2;
+        }
+        v[c] = y - slope2 * fabsf(static_cast<float>(pos - (s0 + c)));
+      }
+    }
+    const int c0 = max(0, lo - s0), c1 = min(64, hi - s0);
+    unsigned long long seen = rows.x;
+    if (c0 > 0 || c1 < 64) seen = c1 > c0 ? rows.x & (~0ull << c0) & (~0ull >> (64 - c1)) : 0ull;
+    if (__any_sync(0xffffffffu, seen != ~0ull)) {
+#pragma unroll
+      for (int c = 0; c < 64; ++c)
+        if (!((seen >> c) & 1)) v[c] = -INFINITY;
+    }
+    float top = fmaxf(v[0], v[1]);
+#pragma unroll
+    for (int c = 2; c < 64; ++c) top = fmaxf(top, v[c]);
+    if constexpr (!MODS) top *= scale2;
+    float alpha = 1.f;
+    if (top > m + kHeadroom || (m == -INFINITY && top > m)) {
+      alpha = exp2_fast(m - top);     // 0 while m is -inf
+      m = top;
+      l *= alpha;
+      lr *= alpha;
+    }
+    const float shift = m == -INFINITY ? 0.f : m;
+    float sum0 = 0.f, sum1 = 0.f, rsum0 = 0.f, rsum1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < 64; c += 2) {
+      const float e0 = exp2_fast(MODS ? v[c] - shift : fmaf(v[c], scale2, -shift));
+      const float e1 = exp2_fast(MODS ? v[c + 1] - shift : fmaf(v[c + 1], scale2, -shift));
+      sum0 += e0;
+      sum1 += e1;
+      p[c / 2] = pack_bf16(e0, e1);
+      rsum0 += __uint_as_float(p[c / 2] << 16);
+      rsum1 += __uint_as_float(p[c / 2] & 0xffff0000u);
+    }
+    l += sum0 + sum1;
+    lr += rsum0 + rsum1;
+    // a row with NaN or infinities is held as zeros, since it would reach every row of the
+    // tile through the value product; the rows that see it become NaN here
+    if (seen & rows.y) l = lr = __uint_as_float(0x7fffffffu);
+    return alpha;
+  }
+};
+
+// Row r's weights into the 128-byte rows of P (K-major, 128-byte swizzle).
+__device__ __forceinline__ void store_weights(uint32_t p_base, int r, const uint32_t (&p)[32]) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p_base + r * 128 + ((u ^ (r & 7)) << 4)),
+                 "r"(p[4 * u]), "r"(p[4 * u + 1]), "r"(p[4 * u + 2]), "r"(p[4 * u + 3])
+                 : "memory");
+}
+
+// The warp's rows of O times alpha, unless it is 1 for all of them.
+__device__ __forceinline__ void rescale_rows(uint32_t tO, float alpha) {
+  if (!__any_sync(0xffffffffu, alpha != 1.f)) return;
+#pragma unroll 1
+  for (int c = 0; c < kNope; c += 32) {
+    float o[32];
+    tmem_ld32(tO + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) o[k] *= alpha;
+    tmem_st16(tO + c, o);
+    tmem_st16(tO + c + 16, o + 16);
+  }
+  tmem_wait_st();
+}
+
+// The row's result: final (`whole`), or partial into `slot`.  Whole warp.
+template <int TILE_ROWS, bool MODS>
+__device__ __forceinline__ void store_rows(const ChunkArgs& a, const ChunkPlan& plan, const RowState<MODS>& st,
+                                           uint32_t tO, const int4& tile, int row, bool mine, bool whole, int slot) {
+  const float inv = st.l == 0.f ? 0.f : 1.f / st.lr;         // NaN stays NaN
+  const float lse = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
+  const int64_t orow = static_cast<int64_t>(tile.y) + row;
+  const int64_t prow = static_cast<int64_t>(slot) * TILE_ROWS + row;
+  __nv_bfloat16* od = a.out + orow * kNope;
+  float* pd = plan.o_part + prow * kNope;
+#pragma unroll 1
+  for (int c = 0; c < kNope; c += 32) {
+    float o[32];
+    tmem_ld32(tO + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) o[k] *= inv;
+    if (mine) {
+      if (whole) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 8)
+          *reinterpret_cast<uint4*>(od + c + k) =
+              make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]), pack_bf16(o[k + 4], o[k + 5]),
+                         pack_bf16(o[k + 6], o[k + 7]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; k += 4)
+          *reinterpret_cast<float4*>(pd + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+      }
+    }
+  }
+  if (mine) {
+    if (whole) a.lse[orow] = lse;
+    else plan.lse_part[prow] = lse;
+  }
+}
+
+}  // namespace smla
