@@ -279,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = warp_wait(bar(PV), (np - 1) & 1, stop, a.status);
       if (!ok) break;
       tc_fence_after();
-      store_rows<kPairRows>(a, plan, st, tO, tile, row, mine, begin >= x0 && after <= x1,
+      store_rows<kPairRows>(a, plan, inverse_sum(st.l, st.lr), lse_of(st.m, st.l), tO, tile, row, mine, begin >= x0 && after <= x1,
                             2 * worker + (begin < x0 ? 0 : 1));
       tc_fence_before();
       __syncwarp();

@@ -46,6 +46,32 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, wait(bar, parity, stop, status));
 }
 
+// What may be done to a score x = q . k besides the scale: a cap and a distance bias (both
+// in units of log2).
+struct ScoreMods {
+  float scale2, cap2, inner;     // scale, cap and 2 scale / cap; cap2 0: none
+  __device__ __forceinline__ explicit ScoreMods(const ChunkArgs& a)
+      : scale2(a.scale * kLog2e), cap2(a.cap * kLog2e), inner(a.cap > 0.f ? 2.f * a.scale * kLog2e / a.cap : 0.f) {}
+  // away: distance to the position
+  __device__ __forceinline__ float operator()(float x, float slope2, float away) const {
+    float y;
+    if (cap2 > 0.f) {
+      // cap tanh(z), z = scale x / cap, tanh(z) = 1 - 2 / (1 + e^(2 z))
+      y = cap2 - __fdividef(2.f * cap2, 1.f + exp2_fast(x * inner));
+    } else {
+      y = x * scale2;
+    }
+    return fmaf(-slope2, fabsf(away), y);
+  }
+};
+
+// The positions of the 64 from s0 on, of those in `mapped`, that lie in [lo, hi).
+__device__ __forceinline__ unsigned long long seen_of(unsigned long long mapped, int s0, int lo, int hi) {
+  const int c0 = max(0, lo - s0), c1 = min(64, hi - s0);
+  if (c0 <= 0 && c1 >= 64) return mapped;
+  return c1 > c0 ? mapped & (~0ull << c0) & (~0ull >> (64 - c1)) : 0ull;
+}
+
 // MODS: scores may be capped or biased by distance.
 template <bool MODS>
 struct RowState {
@@ -53,11 +79,12 @@ struct RowState {
   // normalised by lr, a rounding moves out by its weight times v - out only
   float m = -INFINITY, l = 0.f, lr = 0.f;
   int lo = 0, hi = 0, pos = 0;       // visible positions, own position
-  float scale2, cap, slope2 = 0.f;
+  ScoreMods mods;
+  float slope2 = 0.f;
 
   __device__ __forceinline__ RowState(const ChunkArgs& a, const ChunkPlan& plan, const int4& tile, int row,
                                       bool mine)
-      : scale2(a.scale * kLog2e), cap(a.cap) {
+      : mods(a) {
     if (!mine) return;
     const int tok = (tile.y + row) / a.H;
     visible(a, tile.x, tok, plan.seq_len[tile.x], &lo, &hi, &pos);
@@ -68,23 +95,13 @@ struct RowState {
   // pairs).  rows: the block's mapped positions, and those whose row is not finite.
   // Returns the factor by which earlier results of the row shrink.
   __device__ __forceinline__ float weights(float (&v)[64], int s0, const ulonglong2& rows, uint32_t (&p)[32]) {
+    const float scale2 = mods.scale2;
     if constexpr (MODS) {
+      const float from = static_cast<float>(pos - s0);
 #pragma unroll
-      for (int c = 0; c < 64; ++c) {
-        float y = v[c];
-        if (cap > 0.f) {
-          // cap tanh(z), z = scale x / cap, tanh(z) = 1 - 2 / (1 + e^(2 z))
-          const float e = exp2_fast(y * (2.f * scale2 / cap));
-          y = cap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
-        } else {
-          y *= scale2;
-        }
-        v[c] = y - slope2 * fabsf(static_cast<float>(pos - (s0 + c)));
-      }
+      for (int c = 0; c < 64; ++c) v[c] = mods(v[c], slope2, from - static_cast<float>(c));
     }
-    const int c0 = max(0, lo - s0), c1 = min(64, hi - s0);
-    unsigned long long seen = rows.x;
-    if (c0 > 0 || c1 < 64) seen = c1 > c0 ? rows.x & (~0ull << c0) & (~0ull >> (64 - c1)) : 0ull;
+    const unsigned long long seen = seen_of(rows.x, s0, lo, hi);
     if (__any_sync(0xffffffffu, seen != ~0ull)) {
 #pragma unroll
       for (int c = 0; c < 64; ++c)
@@ -147,12 +164,11 @@ __device__ __forceinline__ void rescale_rows(uint32_t tO, float alpha) {
   tmem_wait_st();
 }
 
-// The row's result: final (`whole`), or partial into `slot`.  Whole warp.
-template <int TILE_ROWS, bool MODS>
-__device__ __forceinline__ void store_rows(const ChunkArgs& a, const ChunkPlan& plan, const RowState<MODS>& st,
+// A row's result: final (`whole`), or partial into `slot`.  inv: 1 / sum of the weights.
+// Whole warp; a lane whose row is not `mine` only keeps step.
+template <int TILE_ROWS>
+__device__ __forceinline__ void store_rows(const ChunkArgs& a, const ChunkPlan& plan, float inv, float lse,
                                            uint32_t tO, const int4& tile, int row, bool mine, bool whole, int slot) {
-  const float inv = st.l == 0.f ? 0.f : 1.f / st.lr;         // NaN stays NaN
-  const float lse = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
   const int64_t orow = static_cast<int64_t>(tile.y) + row;
   const int64_t prow = static_cast<int64_t>(slot) * TILE_ROWS + row;
   __nv_bfloat16* od = a.out + orow * kNope;
@@ -183,5 +199,10 @@ __device__ __forceinline__ void store_rows(const ChunkArgs& a, const ChunkPlan& 
     else plan.lse_part[prow] = lse;
   }
 }
+
+// 1 / sum and lse of a row with maximum m, sum l and sum of rounded weights lr; a row that
+// saw nothing gives 0 and -inf, NaN stays NaN.
+__device__ __forceinline__ float inverse_sum(float l, float lr) { return l == 0.f ? 0.f : 1.f / lr; }
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
 
 }  // namespace smla

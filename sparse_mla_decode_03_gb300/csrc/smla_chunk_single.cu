@@ -16,13 +16,14 @@
 //
 // Expansion without conversions: an e4m3 byte's exponent and mantissa, shifted into bf16's
 // fields, are its value times 2^-120 (subnormals included), and one bf16 product by
-// 2^(scale byte - 7) puts both powers right, exactly.  Rows with NaN or with scale bytes
-// past 134 take a slower path.
+// 2^(scale byte - 7) puts both powers right, exactly.  The shifts act on four bytes at
+// once: the integer pipe is the expansion's bound.  Rows with NaN or with scale bytes past
+// 134 take a slower path.
 //
 // Warps of a CTA: 0..3 softmax and results (lanes 0..15: 64 rows lie in 16 tensor-memory
-// lanes of each quarter), 4..11 expand (8 rows of each block; the next block's bytes are in
-// flight in registers, the one after next's page ids too), 12 loads Q and issues the
-// products.  Every wait is bounded.
+// lanes of each quarter), 4..19 expand (4 rows of each block; the next block's bytes are in
+// flight in registers, the page ids of the one after next too), 20 issues the products,
+// scores or value product, whichever is ready, 21 loads Q.  Every wait is bounded.
 #include <cstring>
 #include <mutex>
 
@@ -34,16 +35,23 @@ namespace smla {
 namespace {
 
 constexpr int kExpandWarp0 = 4;
-constexpr int kExpandWarps = 8;
-constexpr int kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;
+constexpr int kExpandWarps = 16;
+constexpr int kMmaWarp = 20;
+constexpr int kQWarp = 21;
+constexpr int kThreads = 24 * 32;
+// Registers (setmaxnreg): what the launch gives is split among the warpgroups.
+constexpr int kLaunchRegs = 80;
+constexpr int kRegsSoft = 88, kRegsExpand = 88, kRegsMma = 40;
+static_assert(kRegsSoft * 128 + kRegsExpand * 512 + kRegsMma * 128 <= kLaunchRegs * kThreads, "register split");
+static_assert(kRegsSoft >= kLaunchRegs && kRegsExpand >= kLaunchRegs && kRegsMma <= kLaunchRegs,
+              "the direction that each role's setmaxnreg takes");
 constexpr int kSlab = 64 * 128;            // 64 columns of 64 rows
 constexpr int kBuf = 8 * kSlab;            // an expanded block
 constexpr int kQOff = 0;
 constexpr int kBufOff = 8 * kSlab;
 constexpr int kPOff = kBufOff + 2 * kBuf;
 constexpr int kBarOff = kPOff + kSlab;
-constexpr int kMaskOff = kBarOff + 256;    // mapped and poisoned positions: [2 buffers][2][8 bytes]
+constexpr int kMaskOff = kBarOff + 256;    // mapped and poisoned positions: [2 buffers][16 half bytes][2]
 constexpr int kSmem = kMaskOff + 64 + 1024;
 constexpr uint32_t kColS = 448;
 
@@ -52,44 +60,61 @@ constexpr uint32_t kColS = 448;
 // PFULL: weights written; PV: value product done; OEMPTY: results taken.
 enum Bar : int { FULL = 0, EMPTY = 2, QFULL = 4, QEMPTY, SFULL, SEMPTY, PFULL, PV, OEMPTY, kBars };
 
-// A position on the line, walked block by block.
+// A row of the blocks on the line, walked block by block: page and row in it follow by
+// additions, divided out at a tile's start only.
 struct Cursor {
   int x, x1, t, next;     // next: where tile t ends
-  int b, blk, len;
-  __device__ __forceinline__ void load(const ChunkPlan& p) {
+  int b, left;            // sequence, and its positions from the row's on
+  int page, off;
+  __device__ __forceinline__ void load(const ChunkPlan& p, int row, int page_size) {
     const int4 tile = p.tile[t];
     next = p.cum[t + 1];
     b = tile.x;
-    blk = tile.w + (x - p.cum[t]);
-    len = p.seq_len[b];
+    const int pos = (tile.w + (x - p.cum[t])) * kChunkBlk + row;
+    left = p.seq_len[b] - pos;
+    page = pos / page_size;
+    off = pos - page * page_size;
   }
-  __device__ __forceinline__ void step(const ChunkPlan& p) {
+  // pages, rest: 64 / page_size and 64 % page_size
+  __device__ __forceinline__ void step(const ChunkPlan& p, int row, int page_size, int pages, int rest) {
     ++x;
-    ++blk;
-    if (x < x1 && x == next) {
+    if (x == next && x < x1) {
       ++t;
-      load(p);
+      load(p, row, page_size);
+      return;
+    }
+    left -= kChunkBlk;
+    page += pages;
+    off += rest;
+    if (off >= page_size) {
+      off -= page_size;
+      ++page;
     }
   }
 };
 
-// Two e4m3 bytes (in bits 8..15 and 24..31) as bf16 times 2^-120, times m.
-__device__ __forceinline__ uint32_t expand2(uint32_t t, uint32_t m) {
-  const uint32_t v = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(m));
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
 }
-__device__ __forceinline__ uint32_t spread(uint32_t w, uint32_t sel) {
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "r"(sel));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+// Four e4m3 bytes -> four bf16, times m.  High bytes: sign and the exponent's upper three
+// bits; low bytes: its last bit and the mantissa.
+__device__ __forceinline__ uint2 expand4(uint32_t w, uint32_t m) {
+  const uint32_t high = (w & 0x80808080u) | ((w >> 4) & 0x07070707u);
+  const uint32_t low = (w << 4) & 0xf0f0f0f0u;
+  return make_uint2(mul_bf16x2(prmt(low, high, 0x5140), m), mul_bf16x2(prmt(low, high, 0x7362), m));
 }
 __device__ __forceinline__ uint4 expand8(uint2 w, uint32_t m) {
-  return make_uint4(expand2(spread(w.x, 0x1404), m), expand2(spread(w.x, 0x3424), m),
-                    expand2(spread(w.y, 0x1404), m), expand2(spread(w.y, 0x3424), m));
+  const uint2 a = expand4(w.x, m), b = expand4(w.y, m);
+  return make_uint4(a.x, a.y, b.x, b.y);
 }
-// Any e4m3 NaN among four bytes.
+// Any e4m3 NaN among four bytes: a byte of 0x7f carries into its bit 7.
 __device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
 
 // 8 bytes with any scale byte, in 32 bits; out of line: unusual rows only.
@@ -114,17 +139,128 @@ __device__ __forceinline__ bool not_finite(uint32_t v) {
 __device__ __forceinline__ void sts(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ void sts8(uint32_t addr, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ void sts4(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint2 ldg_once(const uint8_t* p) {
   uint2 v;
   asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
 
-// The bytes of one row that a lane holds: lane q of a row's 8 has words q + 8 g of the nope
-// part (columns 64 g + 8 q .. + 7 of group g), the scale word, and 16 bytes of the rope.
-struct RowBytes {
-  uint2 w[7], sc, r0, r1;
+// The 8-byte words of a row that a lane holds: l, l + 32 and l + 64.  Words 0..55 are the
+// nope part (word w: columns 8 (w % 8) .. + 7 of group w / 8), 56 the scales, 57..72 the rope.
+struct RowWords {
+  uint2 a, b, c;
 };
+
+// Two rows a thread: the 16 rows of a warp with their 64 scores of a block, as the
+// 16-lane tensor-memory load deals them out: lane 4 g + q has columns 8 j + 2 q and + 1 of
+// rows g (v[4 j], v[4 j + 1]) and g + 8 (v[4 j + 2], v[4 j + 3]).  Sums stay per thread
+// until the end, the maximum is the row's.
+template <bool MODS>
+struct TwoRows {
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
+  int lo[2] = {0, 0}, hi[2] = {0, 0}, pos[2] = {0, 0};
+  float slope2[2] = {0.f, 0.f};
+  ScoreMods mods;
+
+  __device__ __forceinline__ TwoRows(const ChunkArgs& a, const ChunkPlan& plan, const int4& tile, int row0)
+      : mods(a) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = row0 + 8 * i;
+      if (row >= tile.z) continue;
+      const int tok = (tile.y + row) / a.H;
+      visible(a, tile.x, tok, plan.seq_len[tile.x], &lo[i], &hi[i], &pos[i]);
+      if (MODS && a.slopes != nullptr) slope2[i] = a.slopes[tile.y + row - tok * a.H] * kLog2e;
+    }
+  }
+
+  __device__ __forceinline__ void weights(float (&v)[32], int s0, const ulonglong2& rows, uint32_t (&p)[16],
+                                          float (&alpha)[2]) {
+    const int col = 2 * (threadIdx.x & 3);
+    const float scale2 = mods.scale2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (MODS) {
+        const float from = static_cast<float>(pos[i] - s0 - col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[4 * j + 2 * i] = mods(v[4 * j + 2 * i], slope2[i], from - static_cast<float>(8 * j));
+          v[4 * j + 2 * i + 1] = mods(v[4 * j + 2 * i + 1], slope2[i], from - static_cast<float>(8 * j + 1));
+        }
+      }
+      const unsigned long long seen = seen_of(rows.x, s0, lo[i], hi[i]);
+      if (__any_sync(0xffffffffu, seen != ~0ull)) {
+        const unsigned long long at = seen >> col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (!((at >> (8 * j)) & 1)) v[4 * j + 2 * i] = -INFINITY;
+          if (!((at >> (8 * j)) & 2)) v[4 * j + 2 * i + 1] = -INFINITY;
+        }
+      }
+      float top = fmaxf(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+      for (int j = 1; j < 8; ++j) top = fmaxf(top, fmaxf(v[4 * j + 2 * i], v[4 * j + 2 * i + 1]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      if constexpr (!MODS) top *= scale2;
+      alpha[i] = 1.f;
+      if (top > m[i] + kHeadroom || (m[i] == -INFINITY && top > m[i])) {
+        alpha[i] = exp2_fast(m[i] - top);     // 0 while m is -inf
+        m[i] = top;
+        l[i] *= alpha[i];
+        lr[i] *= alpha[i];
+      }
+      const float shift = m[i] == -INFINITY ? 0.f : m[i];
+      float sum0 = 0.f, sum1 = 0.f, rsum0 = 0.f, rsum1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x0 = v[4 * j + 2 * i], x1 = v[4 * j + 2 * i + 1];
+        const float e0 = exp2_fast(MODS ? x0 - shift : fmaf(x0, scale2, -shift));
+        const float e1 = exp2_fast(MODS ? x1 - shift : fmaf(x1, scale2, -shift));
+        sum0 += e0;
+        sum1 += e1;
+        p[2 * j + i] = pack_bf16(e0, e1);
+        rsum0 += __uint_as_float(p[2 * j + i] << 16);
+        rsum1 += __uint_as_float(p[2 * j + i] & 0xffff0000u);
+      }
+      l[i] += sum0 + sum1;
+      lr[i] += rsum0 + rsum1;
+      // a row of the cache that is not finite is held as zeros; who sees it becomes NaN
+      if (seen & rows.y) l[i] = lr[i] = __uint_as_float(0x7fffffffu);
+    }
+  }
+};
+
+// x[0] of lane 4 g for row g < 8, x[1] for row g + 8, to lane = row.
+__device__ __forceinline__ float to_row(const float (&x)[2]) {
+  const int src = (threadIdx.x & 7) * 4;
+  const float a = __shfl_sync(0xffffffffu, x[0], src), b = __shfl_sync(0xffffffffu, x[1], src);
+  return (threadIdx.x & 8) ? b : a;
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+template <int I>
+struct Index {
+  static constexpr int value = I;
+};
+// The low halves of 16 bytes side by side.
+__device__ __forceinline__ unsigned long long sixteen_halves(unsigned long long low, unsigned long long high) {
+  auto eight = [](unsigned long long x) {
+    x = (x | (x >> 4)) & 0x00ff00ff00ff00ffull;
+    x = (x | (x >> 8)) & 0x0000ffff0000ffffull;
+    return (x | (x >> 16)) & 0x00000000ffffffffull;
+  };
+  return eight(low) | (eight(high) << 32);
+}
 
 template <bool MODS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -163,222 +299,248 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int t_first = x0 < x1 ? find_last_le(plan.cum, tiles + 1, x0) : 0;
 
   if (warp >= kExpandWarp0 && warp < kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsExpand) : "memory");
     // ---------------- expand ----------------
-    const int w8 = warp - kExpandWarp0, q = lane & 7;
-    const int row0 = 8 * w8 + (lane >> 3);          // and row0 + 4
+    // Rows 4 w16 .. + 3 of each block.  Lane j's cursor follows row j % 4; the warp reads a
+    // row at once, 256 consecutive bytes a load.
+    const int w16 = warp - kExpandWarp0;
+    const int mine = 4 * w16 + (lane & 3);
     if (x0 < x1) {
-      // page ids of the two rows of the cursor's block: -1 = no row there
-      auto pages = [&](const Cursor& c, int (&id)[2]) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int s = c.blk * kChunkBlk + row0 + 4 * j;
-          id[j] = -1;
-          if (c.x < c.x1 && s < c.len) {
-            const int page = s / a.page_size;
-            if (page < a.max_pages) id[j] = __ldg(a.table + static_cast<int64_t>(c.b) * a.max_pages + page);
-            else if (q == 0) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
-          }
-        }
+      const int pages_step = kChunkBlk / a.page_size, rest = kChunkBlk % a.page_size;
+      // page id of the cursor's row, -1 = no row there
+      auto lookup = [&](const Cursor& c) {
+        if (c.x >= c.x1 || c.left <= 0) return -1;
+        if (c.page < a.max_pages) return __ldg(a.table + static_cast<int64_t>(c.b) * a.max_pages + c.page);
+        atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
+        return -1;
       };
-      // the bytes of those rows; have: bit j set where row j is mapped
-      auto fetch = [&](const Cursor& c, const int (&id)[2], RowBytes (&d)[2], uint32_t& have) {
-        have = 0;
+      // the rows' bytes; returns which of the four are mapped
+      auto fetch = [&](int id, int off, RowWords (&d)[4]) {
+        const long long r = static_cast<long long>(id) * a.page_size + off;
+        const bool there = id >= 0 && r < a.num_rows;
+        if (id >= 0 && !there) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
+        const uint32_t have = __ballot_sync(0xffffffffu, there) & 15u;
+        const long long at = r * a.stride;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          long long row = -1;
-          if (id[j] >= 0) {
-            const int s = c.blk * kChunkBlk + row0 + 4 * j;
-            row = static_cast<long long>(id[j]) * a.page_size + s % a.page_size;
-            if (row >= a.num_rows) {
-              row = -1;
-              if (q == 0) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
-            }
-          }
-          if (row >= 0) {
-            have |= 1u << j;
-            const uint8_t* src = a.pool + row * a.stride;
-#pragma unroll
-            for (int g = 0; g < 7; ++g) d[j].w[g] = ldg_once(src + 64 * g + 8 * q);
-            d[j].sc = ldg_once(src + kNope);
-            d[j].r0 = ldg_once(src + 456 + 16 * q);
-            d[j].r1 = ldg_once(src + 456 + 16 * q + 8);
-          } else {
-#pragma unroll
-            for (int g = 0; g < 7; ++g) d[j].w[g] = make_uint2(0u, 0u);
-            d[j].sc = make_uint2(0x7f7f7f7fu, 0x007f7f7fu);
-            d[j].r0 = d[j].r1 = make_uint2(0u, 0u);
+        for (int j = 0; j < 4; ++j) {
+          const uint8_t* src = a.pool + __shfl_sync(0xffffffffu, at, j) + 8 * lane;
+          d[j].a = d[j].b = d[j].c = make_uint2(0u, 0u);
+          if ((have >> j) & 1) {
+            d[j].a = ldg_once(src);
+            d[j].b = ldg_once(src + 256);
+            if (lane < 9) d[j].c = ldg_once(src + 512);
           }
         }
+        return have;
       };
       Cursor at;                     // the block whose page ids are fetched next
       at.x = x0;
       at.x1 = x1;
       at.t = t_first;
-      at.load(plan);
-      Cursor c1 = at;                // the block whose bytes are fetched next
-      int id[2];
-      RowBytes cur[2], nxt[2];
-      uint32_t have, have_next = 0;
-      pages(at, id);
-      fetch(c1, id, cur, have);
-      at.step(plan);
-      c1 = at;
-      pages(at, id);
+      at.load(plan, mine, a.page_size);
+      RowWords words[2][4];
+      uint32_t have[2];
+      have[0] = fetch(lookup(at), at.off, words[0]);
+      at.step(plan, mine, a.page_size, pages_step, rest);
+      int id = lookup(at), off = at.off;
+      const int count = x1 - x0;
       bool ok = true;
-      for (int n = 0; ok && n < x1 - x0; ++n) {
-        fetch(c1, id, nxt, have_next);
-        at.step(plan);
-        c1 = at;
-        pages(at, id);
-        const int buf = n & 1;
-        if (n >= 2) ok = warp_wait(bar(EMPTY + buf), ((n >> 1) - 1) & 1, stop, a.status);
-        if (!ok) break;
-        uint32_t poison = 0;
+      // word b of this lane: nope, scales (lane 24) or rope; how its NaN are found
+      const uint32_t mb = lane < 24 ? 0x7f7f7f7fu : lane > 24 ? 0x7f807f80u : 0u;
+      const uint32_t ab = lane < 24 ? 0x01010101u : 0x00800080u;
+      const uint32_t tb = lane < 24 ? 0x80808080u : 0x80008000u;
+      const int sh = 8 * (lane >> 3);
+      const uint32_t dst_nope = sbase + kBufOff + (lane >> 3) * kSlab;
+      const int rope_b = lane - 25, rope_c = lane + 7;         // rope word of words b and c
+      // block n: words[B] are its rows', buffer B is its buffer
+      auto block = [&](int n, auto which) {
+        constexpr int B = decltype(which)::value;
+        have[B ^ 1] = fetch(id, off, words[B ^ 1]);
+        at.step(plan, mine, a.page_size, pages_step, rest);
+        id = lookup(at);
+        off = at.off;
+        if (n >= 2) ok = warp_wait(bar(EMPTY + B), ((n >> 1) - 1) & 1, stop, a.status);
+        if (!ok) return;
+        // anything that the fast path does not cover: NaN, infinite rope values, scale bytes
+        // past 134
+        uint32_t na = 0, nb = 0, nc = 0, top = 0;
+        uint32_t sx[4], sy[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const RowBytes& d = cur[j];
-          const int row = row0 + 4 * j;
-          const uint32_t dst = sbase + kBufOff + buf * kBuf + row * 128 + ((q ^ (row & 7)) << 4);
-          uint32_t odd = 0;
+        for (int j = 0; j < 4; ++j) {
+          const RowWords& d = words[B][j];
+          sx[j] = __shfl_sync(0xffffffffu, d.b.x, 24);
+          sy[j] = __shfl_sync(0xffffffffu, d.b.y, 24);
+          na |= nan_bits(d.a.x) | nan_bits(d.a.y);
+          nb |= ((d.b.x & mb) + ab) | ((d.b.y & mb) + ab);
+          nc |= ((d.c.x & 0x7f807f80u) + 0x00800080u) | ((d.c.y & 0x7f807f80u) + 0x00800080u);
+          sx[j] = (sx[j] >> sh) & 0xffu;
+          sy[j] = (sy[j] >> sh) & 0xffu;         // lanes 24..31: the padding byte, not used
+          top = max(top, max(sx[j], lane < 24 ? sy[j] : 0u));
+        }
+        const bool odd = (na & 0x80808080u) | (nb & tb) | (nc & 0x80008000u) | (top > 134u ? 1u : 0u);
+        const bool usual = !__any_sync(0xffffffffu, odd);
+        uint32_t dropped = 0;
 #pragma unroll
-          for (int g = 0; g < 7; ++g) odd |= nan_bits(d.w[g].x) | nan_bits(d.w[g].y);
-          odd &= 0x80808080u;
-          // scale bytes past 134: + 121 carries into bit 8 of a 16-bit lane
-          odd |= (((d.sc.x & 0x00ff00ffu) + 0x00790079u) | (((d.sc.x >> 8) & 0x00ff00ffu) + 0x00790079u) |
-                  ((d.sc.y & 0x00ff00ffu) + 0x00790079u) | (((d.sc.y >> 8) & 0x000000ffu) + 0x00000079u)) & 0x01000100u;
-          odd |= (not_finite(d.r0.x) | not_finite(d.r0.y) | not_finite(d.r1.x) | not_finite(d.r1.y)) ? 1u : 0u;
-          if (__any_sync(0xffffffffu, odd != 0)) {
-            uint4 o[8];
-            bool bad = false;
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              o[g] = g < 7 ? expand8_any(d.w[g], ((g < 4 ? d.sc.x : d.sc.y) >> (8 * (g & 3))) & 0xffu)
-                           : make_uint4(d.r0.x, d.r0.y, d.r1.x, d.r1.y);
-              bad |= not_finite(o[g].x) | not_finite(o[g].y) | not_finite(o[g].z) | not_finite(o[g].w);
-            }
-            // the 8 lanes of a row agree: zeros for a row that is not finite
-            const bool drop = (__ballot_sync(0xffffffffu, bad) >> (lane & 24)) & 0xffu;
-            poison |= drop ? 1u << j : 0u;
-#pragma unroll
-            for (int g = 0; g < 8; ++g) sts(dst + g * kSlab, drop ? make_uint4(0u, 0u, 0u, 0u) : o[g]);
+        for (int j = 0; j < 4; ++j) {
+          const RowWords& d = words[B][j];
+          const int row = 4 * w16 + j;
+          const uint32_t line = row * 128 + B * kBuf;
+          const uint32_t dn = dst_nope + line + (((lane & 7) ^ (row & 7)) << 4);
+          const uint32_t dr = sbase + kBufOff + 7 * kSlab + line;
+          auto rope = [&](int w) { return dr + (((w >> 1) ^ (row & 7)) << 4) + 8 * (w & 1); };
+          if (usual) {
+            // 2^(s - 7) as two bf16
+            sts(dn, expand8(d.a, ((sx[j] + 120u) << 7) * 0x00010001u));
+            if (lane < 24) sts(dn + 4 * kSlab, expand8(d.b, ((sy[j] + 120u) << 7) * 0x00010001u));
+            if (lane > 24) sts8(rope(rope_b), d.b);
+            if (lane < 9) sts8(rope(rope_c), d.c);
           } else {
-#pragma unroll
-            for (int g = 0; g < 7; ++g) {
-              // 2^(s - 7) as two bf16
-              const uint32_t s = ((g < 4 ? d.sc.x : d.sc.y) >> (8 * (g & 3))) & 0xffu;
-              sts(dst + g * kSlab, expand8(d.w[g], ((s + 120u) << 7) * 0x00010001u));
-            }
-            sts(dst + 7 * kSlab, make_uint4(d.r0.x, d.r0.y, d.r1.x, d.r1.y));
+            const uint4 o = expand8_any(d.a, sx[j]);
+            uint4 o2 = lane < 24 ? expand8_any(d.b, sy[j]) : make_uint4(0u, 0u, 0u, 0u);
+            if (lane > 24) o2 = make_uint4(d.b.x, d.b.y, 0u, 0u);
+            const bool bad = not_finite(o.x) | not_finite(o.y) | not_finite(o.z) | not_finite(o.w) |
+                             not_finite(o2.x) | not_finite(o2.y) | not_finite(o2.z) | not_finite(o2.w) |
+                             not_finite(d.c.x) | not_finite(d.c.y);
+            const bool drop = __any_sync(0xffffffffu, bad);       // zeros for a row that is not finite
+            dropped |= drop ? 1u << j : 0u;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            sts(dn, drop ? zero : o);
+            if (lane < 24) sts(dn + 4 * kSlab, drop ? zero : o2);
+            if (lane > 24) sts8(rope(rope_b), drop ? make_uint2(0u, 0u) : d.b);
+            if (lane < 9) sts8(rope(rope_c), drop ? make_uint2(0u, 0u) : d.c);
           }
         }
-        // row 8 w8 + i (i < 4): lane 8 i, bit 0; i >= 4: lane 8 (i - 4), bit 1
-        const uint32_t m0 = __ballot_sync(0xffffffffu, have & 1), m1 = __ballot_sync(0xffffffffu, have & 2);
-        const uint32_t p0 = __ballot_sync(0xffffffffu, poison & 1), p1 = __ballot_sync(0xffffffffu, poison & 2);
         if (lane == 0) {
-          auto pick = [](uint32_t lo, uint32_t hi) {
-            uint32_t v = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v |= ((lo >> (8 * i)) & 1u) << i | ((hi >> (8 * i)) & 1u) << (4 + i);
-            return static_cast<uint8_t>(v);
-          };
-          masks[buf * 16 + w8] = pick(m0, m1);
-          masks[buf * 16 + 8 + w8] = pick(p0, p1);
+          masks[B * 32 + w16] = static_cast<uint8_t>(have[B]);
+          masks[B * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(FULL + buf));
-#pragma unroll
-        for (int j = 0; j < 2; ++j) cur[j] = nxt[j];
-        have = have_next;
+        if (lane == 0) mbar_arrive(bar(FULL + B));
+      };
+      for (int n = 0; ok && n < count; n += 2) {
+        block(n, Index<0>());
+        if (ok && n + 1 < count) block(n + 1, Index<1>());
       }
     }
-  } else if (warp == kMmaWarp) {
-    // ---------------- Q and products ----------------
-    // The whole warp walks the schedule, one elected lane issues (descriptors stay uniform).
-    constexpr uint32_t kIdQK = idesc_bf16(64, 64, false, false);
-    constexpr uint32_t kIdV0 = idesc_bf16(64, 256, false, true);
-    constexpr uint32_t kIdV1 = idesc_bf16(64, 192, false, true);
-    const uint64_t d0 = smem_desc(sbase, 16, 1024, SWZ_128B), dv = smem_desc(sbase, kSlab, 1024, SWZ_128B);
-    const uint32_t hi = static_cast<uint32_t>(d0 >> 32);
-    const uint32_t lq = static_cast<uint32_t>(d0), lk = lq + (kBufOff >> 4), lp = lq + (kPOff >> 4);
-    const uint32_t lv = static_cast<uint32_t>(dv) + (kBufOff >> 4);
-    uint32_t n = 0, nv = 0, nq = 0;      // scores, value products and tiles so far
-    bool ok = true;
-    for (int x = x0, t = t_first; ok && x < x1; ++t) {
-      const int end = min(x1, plan.cum[t + 1]);
-      const int nb = end - x;
-      const int row0 = plan.tile[t].y;
-      if (nq > 0) ok = warp_wait(bar(QEMPTY), (nq - 1) & 1, stop, a.status);
-      if (!ok) break;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(bar(QFULL), 8 * kSlab);
-        for (int c = 0; c < 8; ++c) tma_load_2d(sbase + kQOff + c * kSlab, &qmap, 64 * c, row0, bar(QFULL));
-      }
-      __syncwarp();
-      ok = warp_wait(bar(QFULL), nq & 1, stop, a.status);
-      for (int i = 0; ok && i <= nb; ++i) {
-        if (i < nb) {
-          ok = warp_wait(bar(FULL + (n & 1)), (n >> 1) & 1, stop, a.status);
-          if (ok && n > 0) ok = warp_wait(bar(SEMPTY), (n - 1) & 1, stop, a.status);
-          if (!ok) break;
+  } else if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma) : "memory");
+    if (warp == kMmaWarp) {
+      // ---------------- products ----------------
+      // Scores of block n or the value product of block v, whichever is ready, so that a
+      // late block does not hold up the one before it.  The whole warp walks, one elected
+      // lane issues (descriptors stay uniform).
+      constexpr uint32_t kIdQK = idesc_bf16(64, 64, false, false);
+      constexpr uint32_t kIdV0 = idesc_bf16(64, 256, false, true);
+      constexpr uint32_t kIdV1 = idesc_bf16(64, 192, false, true);
+      const uint64_t d0 = smem_desc(sbase, 16, 1024, SWZ_128B), dv = smem_desc(sbase, kSlab, 1024, SWZ_128B);
+      const uint32_t hi = static_cast<uint32_t>(d0 >> 32);
+      const uint32_t lq = static_cast<uint32_t>(d0), lk = lq + (kBufOff >> 4), lp = lq + (kPOff >> 4);
+      const uint32_t lv = static_cast<uint32_t>(dv) + (kBufOff >> 4);
+      const int count = x1 - x0;
+      int n = 0, v = 0;                                 // scores and value products so far
+      int tn = t_first, tv = t_first;                   // their tiles
+      int n0 = 0, v0 = 0;                               // first block of those tiles
+      int n1 = count > 0 ? min(x1, plan.cum[tn + 1]) - x0 : 0, v1 = n1;   // behind their last
+      uint32_t kn = 0, kv = 0;                          // how many tiles before them
+      bool ok = true;
+      long long idle = clock64();
+      auto ready = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar(i), parity & 1)); };
+      while (ok && v < count) {
+        if (v < n && ready(PFULL, v) && (v > v0 || kv == 0 || ready(OEMPTY, kv - 1))) {
+          tc_fence_after();
+          const uint32_t lb = lv + (v & 1) * (kBuf >> 4);
+          const uint32_t old = v > v0 ? 1u : 0u;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t acc = k > 0 ? 1u : old;
+              mma_f16_ss_hl(tmem, lp + ((k * 32) >> 4), hi, lb + ((k * 2048) >> 4), hi, kIdV0, acc);
+              mma_f16_ss_hl(tmem + 256, lp + ((k * 32) >> 4), hi, lb + ((4 * kSlab + k * 2048) >> 4), hi, kIdV1, acc);
+            }
+            mma_commit(bar(EMPTY + (v & 1)));
+            mma_commit(bar(PV));
+          }
+          __syncwarp();
+          if (++v == v1 && v < count) {
+            ++tv;
+            ++kv;
+            v0 = v;
+            v1 = min(x1, plan.cum[tv + 1]) - x0;
+          }
+          idle = clock64();
+        } else if (n < count && n <= v + 1 && ready(FULL + (n & 1), n >> 1) && (n == 0 || ready(SEMPTY, n - 1)) &&
+                   (n > n0 || ready(QFULL, kn))) {
           tc_fence_after();
           const uint32_t lb = lk + (n & 1) * (kBuf >> 4);
           if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 8; ++c)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_f16_ss_hl(tmem + kColS, lq + ((c * kSlab + k * 32) >> 4), hi, lb + ((c * kSlab + k * 32) >> 4), hi,
                               kIdQK, c + k > 0 ? 1u : 0u);
             mma_commit(bar(SFULL));
-            if (i == nb - 1) mma_commit(bar(QEMPTY));
+            if (n + 1 == n1) mma_commit(bar(QEMPTY));
           }
           __syncwarp();
-          ++n;
-        }
-        if (i > 0) {
-          ok = warp_wait(bar(PFULL), nv & 1, stop, a.status);
-          if (ok && i == 1 && nq > 0) ok = warp_wait(bar(OEMPTY), (nq - 1) & 1, stop, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t lb = lv + (nv & 1) * (kBuf >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t acc = k > 0 ? 1u : (i > 1 ? 1u : 0u);
-              mma_f16_ss_hl(tmem, lp + ((k * 32) >> 4), hi, lb + ((k * 2048) >> 4), hi, kIdV0, acc);
-              mma_f16_ss_hl(tmem + 256, lp + ((k * 32) >> 4), hi, lb + ((4 * kSlab + k * 2048) >> 4), hi, kIdV1, acc);
-            }
-            mma_commit(bar(EMPTY + (nv & 1)));
-            mma_commit(bar(PV));
+          if (++n == n1 && n < count) {
+            ++tn;
+            ++kn;
+            n0 = n;
+            n1 = min(x1, plan.cum[tn + 1]) - x0;
           }
-          __syncwarp();
-          ++nv;
+          idle = clock64();
+        } else if (__any_sync(0xffffffffu, *stop || clock64() - idle > kWaitLimit)) {
+          if (lane == 0 && !*stop) {
+            *stop = 1;
+            atomicCAS(a.status, 0, SMLA_ERR_TIMEOUT);
+          }
+          ok = false;
         }
       }
-      ++nq;
-      x = end;
-    }
-    if (!ok) {   // copies and products in flight end within microseconds: 1 ms before they lose their memory
-      const long long t0 = clock64();
-      while (clock64() - t0 < 2000000) {
+      if (!ok) {   // products in flight end within microseconds: 1 ms before they lose their memory
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
+        }
       }
+    } else if (warp == kQWarp) {
+      // ---------------- Q ----------------
+      bool ok = true;
+      uint32_t k = 0;
+      for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
+        if (k > 0) ok = warp_wait(bar(QEMPTY), (k - 1) & 1, stop, a.status);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar(QFULL), 8 * kSlab);
+          for (int c = 0; c < 8; ++c)
+            tma_load_2d(sbase + kQOff + c * kSlab, &qmap, 64 * c, plan.tile[t].y, bar(QFULL));
+        }
+        __syncwarp();
+        x = min(x1, plan.cum[t + 1]);
+      }
+      // the last copy has landed before the CTA may end
+      if (k > 0) warp_wait(bar(QFULL), (k - 1) & 1, stop, a.status);
     }
   } else if (warp < kExpandWarp0) {
-    // ---------------- softmax and results: lane < 16 = row 16 warp + lane ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft) : "memory");
+    // ---------------- softmax and results ----------------
+    // Rows 16 warp .. + 15: two rows and a quarter of their scores a thread for the weights,
+    // lane = row for O.
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t tS = tmem + kColS + lanes, tO = tmem + lanes;
-    const int row = 16 * warp + (lane & 15);
+    const int g = lane >> 2;
+    // P: rows 16 warp + g and + 8 (the same row modulo 8), columns 2 (lane % 4) .. of unit j
+    const uint32_t p0 = sbase + kPOff + (16 * warp + g) * 128 + 4 * (lane & 3), p1 = p0 + 8 * 128;
     uint32_t n = 0;
     bool ok = true;
     for (int x = x0, t = t_first; ok && x < x1; ++t) {
       const int4 tile = plan.tile[t];
       const int begin = plan.cum[t], after = plan.cum[t + 1], end = min(x1, after);
       const int nb = end - x, blk = tile.w + (x - begin);
-      const bool mine = lane < 16 && row < tile.z;
-      // lanes 16..31 follow lanes 0..15 on scores of no row; rows past the tile stay whatever
-      // they are (a product's rows do not mix), so a warp without rows only keeps step
-      RowState<MODS> st(a, plan, tile, row, row < tile.z);
+      // rows past the tile stay whatever they are (a product's rows do not mix), so a warp
+      // without rows only keeps step
+      TwoRows<MODS> st(a, plan, tile, 16 * warp + g);
       const bool idle = 16 * warp >= tile.z;
       for (int i = 0; ok && i < nb; ++i, ++n) {
         ok = warp_wait(bar(SFULL), n & 1, stop, a.status);
@@ -392,26 +554,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after();
-        float v[64];
-        tmem_ld32(tS, v);
-        tmem_ld32(tS + 32, v + 32);
+        float v[32];
+        tmem_ld_16x64(tS, v);
         const volatile unsigned long long* mk =
-            reinterpret_cast<const volatile unsigned long long*>(smem + kMaskOff + (n & 1) * 16);
-        const ulonglong2 rows = make_ulonglong2(mk[0], mk[1]);
+            reinterpret_cast<const volatile unsigned long long*>(smem + kMaskOff + (n & 1) * 32);
+        const unsigned long long m0 = mk[0], m1 = mk[1], d0 = mk[2], d1 = mk[3];
+        ulonglong2 rows = make_ulonglong2(~0ull, 0ull);
+        if ((m0 & m1) != 0x0f0f0f0f0f0f0f0full || (d0 | d1) != 0)
+          rows = make_ulonglong2(sixteen_halves(m0, m1), sixteen_halves(d0, d1));
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(SEMPTY));
-        uint32_t p[32];
-        const float shrink = st.weights(v, (blk + i) * kChunkBlk, rows, p);
-        const float alpha = lane < 16 ? shrink : 1.f;
+        uint32_t p[16];
+        float alpha[2];
+        st.weights(v, (blk + i) * kChunkBlk, rows, p, alpha);
         if (i > 0) {
           ok = warp_wait(bar(PV), (n - 1) & 1, stop, a.status);
           if (!ok) break;
           tc_fence_after();
-          rescale_rows(tO, alpha);
+          if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+            const float f = to_row(alpha);
+            rescale_rows(tO, lane < 16 ? f : 1.f);
+          }
         }
-        if (lane < 16) store_weights(sbase + kPOff, row, p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sts4(p0 + ((j ^ g) << 4), p[2 * j]);
+          sts4(p1 + ((j ^ g) << 4), p[2 * j + 1]);
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -421,8 +592,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(bar(PV), (n - 1) & 1, stop, a.status);
       if (!ok) break;
       tc_fence_after();
-      store_rows<kSingleRows>(a, plan, st, tO, tile, row, mine, begin >= x0 && after <= x1,
-                              2 * worker + (begin < x0 ? 0 : 1));
+      if (!idle) {
+        float inv[2], lse[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float l = quad_sum(st.l[i]), lr = quad_sum(st.lr[i]);
+          inv[i] = inverse_sum(l, lr);
+          lse[i] = lse_of(st.m[i], l);
+        }
+        const int row = 16 * warp + (lane & 15);
+        store_rows<kSingleRows>(a, plan, to_row(inv), to_row(lse), tO, tile, row, lane < 16 && row < tile.z,
+                                begin >= x0 && after <= x1, 2 * worker + (begin < x0 ? 0 : 1));
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(OEMPTY));
@@ -451,6 +632,12 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStre
     if (!done[dev]) {
       e = cudaFuncSetAttribute(single_kernel<MODS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
+      // the register split assumes the launch's share: a build that differs is refused,
+      // since its increase would never be granted
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, single_kernel<MODS>);
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
       done[dev] = true;
     }
   }
