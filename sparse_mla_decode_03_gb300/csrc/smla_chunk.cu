@@ -50,20 +50,26 @@ __device__ long long block_sum(long long v, long long* total, long long* warp_su
   return s - v + (warp > 0 ? warp_sums[warp - 1] : 0);
 }
 
-// One CTA.  tile_rows: (token, head) rows of a tile; workers: shares of the line.
+// One CTA of kPlanThreads.  tile_rows: (token, head) rows of a tile; workers: shares of the
+// line.  Latency is all that counts here (a few dependent loads and block-wide sums), so
+// what the tiles need of their sequences stays in shared memory for the usual batch.
+constexpr int kPlanSeqs = 1024;    // sequences whose plan fits in shared memory
 __global__ void __launch_bounds__(kPlanThreads, 1)
     plan_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows, int workers, int min_share) {
   __shared__ long long sums[32];
+  __shared__ int32_t s_tile[kPlanSeqs + 1], s_first[kPlanSeqs], s_last[kPlanSeqs], s_len[kPlanSeqs];
   grid_dep_wait();
   grid_dep_launch();
+  const bool small = a.B <= kPlanSeqs;
   long long tiles = 0, blocks = 0;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + static_cast<int>(threadIdx.x);
-    int n = 0, len = 0;
+    int n = 0, len = 0, first = 0;
     if (b < a.B) {
-      const int first = min(max(a.cu_q[b], 0), a.T);
-      n = min(max(a.cu_q[b + 1], first), a.T) - first;
+      const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
       len = max(a.kv_lens[b], 0);
+      first = min(max(c0, 0), a.T);
+      n = min(max(c1, first), a.T) - first;
     }
     const int nt = (n * a.H + tile_rows - 1) / tile_rows;      // total_q * H < 2^30
     // a sequence without cached tokens keeps one block (of zeros) for its tiles to read
@@ -80,6 +86,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
       p.tile_base[b] = static_cast<int>(t0);
       p.seq_base[b] = static_cast<int>(min(s0, static_cast<long long>(p.cap_blocks)));
       p.seq_len[b] = len;
+      if (small) {
+        s_tile[b] = static_cast<int>(t0);
+        s_first[b] = first;
+        s_last[b] = first + n;
+        s_len[b] = len;
+      }
     }
     tiles += t_all;
     blocks += b_all;
@@ -87,6 +99,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   if (threadIdx.x == 0) {
     p.tile_base[a.B] = static_cast<int>(tiles);
     p.seq_base[a.B] = static_cast<int>(min(blocks, static_cast<long long>(p.cap_blocks)));
+    if (small) s_tile[a.B] = static_cast<int>(tiles);
   }
   __syncthreads();
   long long line = 0;
@@ -95,14 +108,26 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     int4 tile = make_int4(0, 0, 0, 0);
     int n = 0;
     if (t < tiles) {
-      const int b = find_last_le(p.tile_base, a.B + 1, t);
-      const int first = min(max(a.cu_q[b], 0), a.T), last = min(max(a.cu_q[b + 1], first), a.T);
-      const int row = first * a.H + (t - p.tile_base[b]) * tile_rows;
+      int b, first, last, len, base;
+      if (small) {
+        b = find_last_le(s_tile, a.B + 1, t);
+        first = s_first[b];
+        last = s_last[b];
+        len = s_len[b];
+        base = s_tile[b];
+      } else {
+        b = find_last_le(p.tile_base, a.B + 1, t);
+        first = min(max(a.cu_q[b], 0), a.T);
+        last = min(max(a.cu_q[b + 1], first), a.T);
+        len = p.seq_len[b];
+        base = p.tile_base[b];
+      }
+      const int row = first * a.H + (t - base) * tile_rows;
       const int rows = min(tile_rows, last * a.H - row);
       int low = 0x7fffffff, high = 0;
       for (int tok = row / a.H; tok <= (row + rows - 1) / a.H; ++tok) {
         int lo, hi, pos;
-        visible(a, b, tok, p.seq_len[b], &lo, &hi, &pos);
+        visible(a, b, tok, len, &lo, &hi, &pos);
         if (hi > lo) {
           low = min(low, lo);
           high = max(high, hi);
@@ -120,11 +145,23 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     }
     line += all;
   }
+  if (line > (1 << 30)) {     // far past any call that ends within hours: positions on the line stay ints
+    line = 0;
+    tiles = 0;
+    if (threadIdx.x == 0) atomicCAS(a.status, 0, SMLA_ERR_UNSUPPORTED_SHAPE);
+  }
+  const int per = max(min_share, static_cast<int>((line + workers - 1) / workers));
   if (threadIdx.x == 0) {
     p.cum[tiles] = static_cast<int>(line);
     p.head[0] = static_cast<int>(tiles);
     p.head[1] = static_cast<int>(line);
-    p.head[2] = max(min_share, static_cast<int>((line + workers - 1) / workers));
+    p.head[2] = per;
+  }
+  __syncthreads();
+  // the tile at the start of each share, so that nobody else has to search
+  for (int c = threadIdx.x; c < workers; c += kPlanThreads) {
+    const long long x = static_cast<long long>(c) * per;
+    p.start[c] = x < line ? find_last_le(p.cum, static_cast<int>(tiles) + 1, static_cast<int>(x)) : -1;
   }
 }
 
@@ -247,29 +284,36 @@ __global__ void __launch_bounds__(256) expand_kernel(const ChunkArgs a, const Ch
 }
 
 // ---------------------------------------------------------------------------
-// Merge: the partial results of the tiles that a share's border cuts.  Grid (row groups of
-// 8, borders): border c lies between workers c and c + 1 and serves its tile if it is the
-// first border inside.  A warp a row.
+// Merge: the partial results of the tiles that a share's border cuts.  Grid (row groups,
+// borders): border c lies between workers c - 1 and c and serves its tile if it is the
+// first border inside.  A row is joined by ROW_WARPS warps, each taking every
+// ROW_WARPS-th partial result: a long context over one tile of few rows has as many partial
+// results as there are workers, and one warp reading them in turn would be all latency.
 // ---------------------------------------------------------------------------
+template <int ROW_WARPS>
 __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows) {
+  constexpr int kRows = 8 / ROW_WARPS;          // rows of a CTA
+  __shared__ float2 part[8][kNope / 2 + 2];     // each warp's sum over its partial results
+  __shared__ float weight[8];
   grid_dep_wait();
   grid_dep_launch();
-  const int per = p.head[2], total = p.head[1], tiles = p.head[0];
   const int c1 = blockIdx.y + 1;
-  const int64_t border = static_cast<int64_t>(c1) * per;
-  if (border >= total) return;
-  const int x = static_cast<int>(border);
-  const int t = find_last_le(p.cum, tiles + 1, x);
+  const int t = p.start[c1];
+  if (t < 0) return;
+  const int per = p.head[2];
   const int begin = p.cum[t], end = p.cum[t + 1];
-  if (begin == x || begin / per + 1 != c1) return;
+  if (begin >= c1 * per || begin / per + 1 != c1) return;
   const int4 tile = p.tile[t];
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= tile.z) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kRows + warp / ROW_WARPS;
+  if (blockIdx.x * kRows >= tile.z) return;
   const int first = c1 - 1, last = (end - 1) / per;
   // slot of worker c: its share begins inside the tile (0), or the tile inside its share (1)
-  auto slot = [&](int c) { return 2 * c + (begin < c * per ? 0 : 1); };
+  auto at = [&](int c) { return static_cast<int64_t>(2 * c + (begin < c * per ? 0 : 1)) * tile_rows + row; };
+  const bool live = row < tile.z;
   float top = -INFINITY;
-  for (int c = first + lane; c <= last; c += 32) top = fmaxf(top, p.lse_part[slot(c) * tile_rows + row]);
+  if (live)
+    for (int c = first + lane; c <= last; c += 32) top = fmaxf(top, p.lse_part[at(c)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float shift = top == -INFINITY ? 0.f : top;
@@ -277,18 +321,38 @@ __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const Chu
   float2 acc[7];
 #pragma unroll
   for (int k = 0; k < 7; ++k) acc[k] = make_float2(0.f, 0.f);
-  for (int c = first; c <= last; ++c) {
-    const int64_t at = static_cast<int64_t>(slot(c)) * tile_rows + row;
-    const float w = expf(p.lse_part[at] - shift);
-    sum += w;
-    const float2* o = reinterpret_cast<const float2*>(p.o_part + at * kNope) + lane;
+  if (live) {
+#pragma unroll 2
+    for (int c = first + warp % ROW_WARPS; c <= last; c += ROW_WARPS) {
+      const float w = expf(p.lse_part[at(c)] - shift);
+      sum += w;
+      const float2* o = reinterpret_cast<const float2*>(p.o_part + at(c) * kNope) + lane;
 #pragma unroll
-    for (int k = 0; k < 7; ++k) {
-      const float2 v = o[32 * k];
-      acc[k].x = fmaf(w, v.x, acc[k].x);
-      acc[k].y = fmaf(w, v.y, acc[k].y);
+      for (int k = 0; k < 7; ++k) {
+        const float2 v = o[32 * k];
+        acc[k].x = fmaf(w, v.x, acc[k].x);
+        acc[k].y = fmaf(w, v.y, acc[k].y);
+      }
     }
   }
+  if constexpr (ROW_WARPS > 1) {
+#pragma unroll
+    for (int k = 0; k < 7; ++k) part[warp][lane + 32 * k] = acc[k];
+    if (lane == 0) weight[warp] = sum;
+    __syncthreads();
+    if (warp % ROW_WARPS != 0) return;
+#pragma unroll
+    for (int w = 1; w < ROW_WARPS; ++w) {       // in a fixed order: the same bits every time
+      sum += weight[warp + w];
+#pragma unroll
+      for (int k = 0; k < 7; ++k) {
+        const float2 v = part[warp + w][lane + 32 * k];
+        acc[k].x += v.x;
+        acc[k].y += v.y;
+      }
+    }
+  }
+  if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t orow = static_cast<int64_t>(tile.y) + row;
   __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + orow * kNope) + lane;
@@ -340,6 +404,7 @@ size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
   plan->tile_base = reinterpret_cast<int32_t*>(take(4 * (B + 1)));
   plan->seq_base = reinterpret_cast<int32_t*>(take(4 * (B + 1)));
   plan->seq_len = reinterpret_cast<int32_t*>(take(4 * B));
+  plan->start = reinterpret_cast<int32_t*>(take(4 * kMaxSms));
   plan->lse_part = reinterpret_cast<float*>(take(size_t{4} * 2 * kMaxPairs * kPairRows));
   plan->o_part = reinterpret_cast<float*>(take(size_t{4} * 2 * kMaxPairs * kPairRows * kNope));
   plan->seen = reinterpret_cast<ulonglong2*>(take(16 * static_cast<size_t>(cap + 1)));
@@ -349,7 +414,11 @@ size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
 
 cudaError_t launch_merge(const ChunkArgs& a, const ChunkPlan& p, int rows, int workers, cudaStream_t s) {
   if (workers < 2) return cudaSuccess;
-  return launch_programmatic(merge_kernel, dim3(rows / 8, workers - 1), dim3(256), 0, s, a, p, rows);
+  // few tiles (no more than workers): many partial results a row
+  const int64_t tiles = (static_cast<int64_t>(a.T) * a.H + rows - 1) / rows + a.B;
+  if (tiles * 4 <= workers)
+    return launch_programmatic(merge_kernel<8>, dim3(rows, workers - 1), dim3(256), 0, s, a, p, rows);
+  return launch_programmatic(merge_kernel<2>, dim3(rows / 4, workers - 1), dim3(256), 0, s, a, p, rows);
 }
 
 cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_t s) {

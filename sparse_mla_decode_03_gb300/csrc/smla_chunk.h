@@ -34,6 +34,7 @@ struct ChunkPlan {
   int32_t* head;         // [0] tiles, [1] blocks on the line, [2] blocks a share
   int4* tile;            // sequence, first row (token * H + head), rows, first block
   int32_t* cum;          // [tiles + 1] start of each tile on the line
+  int32_t* start;        // [workers] the tile at the start of each share, -1 behind the line
   int32_t* tile_base;    // [B + 1] first tile of each sequence
   int32_t* seq_base;     // [B + 1] first block of each sequence in the expanded copy
   int32_t* seq_len;      // [B] positions of each sequence that can be seen

@@ -84,9 +84,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   grid_dep_launch();
 
-  const int total = plan.head[1], per = plan.head[2], tiles = plan.head[0];
-  const int x0 = min(total, worker * per), x1 = min(total, x0 + per);
-  const int t_first = x0 < x1 ? find_last_le(plan.cum, tiles + 1, x0) : 0;
+  const int total = plan.head[1], per = plan.head[2];
+  const int t_first = plan.start[worker];
+  const int x0 = t_first >= 0 ? worker * per : total, x1 = min(total, x0 + per);
 
   if (warp == 4) {
     // ---------------- tensor copies ----------------
