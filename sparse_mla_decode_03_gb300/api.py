@@ -6,6 +6,7 @@ stream to the C entry point of the same name (include/smla.h) and raises
 CUDA kernels; there is no Python or CPU fallback."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import Optional, Tuple
@@ -259,6 +260,14 @@ def _stream_on(stream: Optional[torch.cuda.Stream], device: torch.device) -> cty
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(device: torch.device):
+    """The device as the current one for a call (no switch where it is already)."""
+    return _SAME if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+_SAME = contextlib.nullcontext()
+
+
 def _row_stride(kv_pages: torch.Tensor) -> int:
     """Bytes between rows (a single row has no neighbour: any stride will do)."""
     return kv_pages.stride(0) if kv_pages.shape[0] > 1 else ROW_BYTES
@@ -307,7 +316,7 @@ def smla_cache_append(kv: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
     p = make_cache_params(kv_pages.shape[0] // page_size, page_size, B, block_table.shape[1],
                           _row_stride(kv_pages))
     stride = kv.stride(0) if kv.shape[0] > 1 else QK
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = _lib.load().smla_cache_append(_ptr(kv), stride, kv.shape[0], _ptr(kv_pages), _ptr(block_table),
                                            _ptr(cu_q), _ptr(kv_lens), ctypes.byref(p),
                                            _stream_on(stream, dev))
@@ -326,7 +335,7 @@ def smla_cache_reserve(page_size: int, ref_count: torch.Tensor, block_table: tor
         raise ValueError("target_lens must be [B] for a block_table of B rows, on a CUDA device")
     p = make_cache_params(ref_count.shape[0], page_size, block_table.shape[0], block_table.shape[1])
     ws = _cache_workspace(p, workspace, dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = _lib.load().smla_cache_reserve(_ptr(ref_count), _ptr(block_table), _ptr(target_lens),
                                             ctypes.byref(p), _ptr(ws), _bytes(ws), _stream_on(stream, dev))
     _check(st, "smla_cache_reserve")
@@ -358,7 +367,7 @@ def smla_cache_fork(kv_pages: torch.Tensor, page_size: int, ref_count: torch.Ten
     if kv_lens.shape[0] != block_table.shape[0] or parents.shape != children.shape:
         raise ValueError("kv_lens must be [B], and parents and children equally long")
     ws = _cache_workspace(p, workspace, dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = _lib.load().smla_cache_fork(_ptr(kv_pages), _ptr(ref_count), _ptr(block_table), _ptr(kv_lens),
                                          _ptr(parents), _ptr(children), parents.shape[0], ctypes.byref(p),
                                          _ptr(ws), _bytes(ws), _stream_on(stream, dev))
@@ -376,7 +385,7 @@ def smla_cache_free(ref_count: torch.Tensor, block_table: torch.Tensor, kv_lens:
     if not ref_count.is_cuda or kv_lens.shape[0] != block_table.shape[0]:
         raise ValueError("kv_lens must be [B] for a block_table of B rows, on a CUDA device")
     p = make_cache_params(ref_count.shape[0], 1, block_table.shape[0], block_table.shape[1])
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = _lib.load().smla_cache_free(_ptr(ref_count), _ptr(block_table), _ptr(kv_lens), _ptr(rows),
                                          rows.shape[0], ctypes.byref(p), _stream_on(stream, dev))
     _check(st, "smla_cache_free")
@@ -403,7 +412,7 @@ def smla_cache_compact(kv_pages: torch.Tensor, page_size: int, ref_count: torch.
     if info.shape[0] != 2:
         raise ValueError("info must be int32 [2]")
     ws = _cache_workspace(p, workspace, dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = _lib.load().smla_cache_compact(_ptr(kv_pages), _ptr(ref_count), _ptr(block_table), _ptr(ref_out),
                                             _ptr(table_out), _ptr(info), ctypes.byref(p), _ptr(ws),
                                             _bytes(ws), _stream_on(stream, dev))
@@ -476,7 +485,7 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
         workspace = torch.empty(smla_chunk_workspace_size(p), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = _lib.load().smla_chunk_attention(
             _ptr(q), _ptr(kv_pages), _ptr(block_table), _ptr(cu_q), _ptr(kv_lens), _ptr(vis_begin),
             _ptr(vis_end), _ptr(slopes), _ptr(out), _ptr(lse), ctypes.byref(p), _ptr(workspace),

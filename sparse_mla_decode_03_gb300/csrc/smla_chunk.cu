@@ -50,47 +50,64 @@ __device__ long long block_sum(long long v, long long* total, long long* warp_su
   return s - v + (warp > 0 ? warp_sums[warp - 1] : 0);
 }
 
-// One CTA of kPlanThreads.  tile_rows: (token, head) rows of a tile; workers: shares of the
-// line.  Latency is all that counts here (a few dependent loads and block-wide sums), so
-// what the tiles need of their sequences stays in shared memory for the usual batch.
-constexpr int kPlanSeqs = 1024;    // sequences whose plan fits in shared memory
-__global__ void __launch_bounds__(kPlanThreads, 1)
-    plan_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows, int workers, int min_share) {
-  __shared__ long long sums[32];
-  __shared__ int32_t s_tile[kPlanSeqs + 1], s_first[kPlanSeqs], s_last[kPlanSeqs], s_len[kPlanSeqs];
-  grid_dep_wait();
-  grid_dep_launch();
-  const bool small = a.B <= kPlanSeqs;
+// What a sequence brings: its entries of q, clamped to it, and its blocks.
+struct Sequence {
+  int first, n, len, blocks;
+};
+__device__ __forceinline__ Sequence sequence(const ChunkArgs& a, int b) {
+  Sequence s = {0, 0, 0, 0};
+  if (b >= a.B) return s;
+  const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
+  s.len = max(a.kv_lens[b], 0);
+  s.first = min(max(c0, 0), a.T);
+  s.n = min(max(c1, s.first), a.T) - s.first;
+  // one without cached tokens keeps one block (of zeros) for its tiles to read
+  if (s.n > 0) s.blocks = max(1, (s.len + kChunkBlk - 1) / kChunkBlk);
+  return s;
+}
+// Its first block in the expanded copy, given the blocks before it, and how many positions
+// of it find room there.
+__device__ __forceinline__ int seq_base(const ChunkPlan& p, long long before) {
+  return static_cast<int>(min(before, static_cast<long long>(p.cap_blocks)));
+}
+__device__ __forceinline__ int seq_len(const ChunkPlan& p, const Sequence& s, long long before) {
+  const long long left = p.cap_blocks - before;
+  return s.blocks <= left ? s.len : left > 0 ? static_cast<int>(left) * kChunkBlk : 0;
+}
+
+constexpr int kPlanSeqs = 1024;    // sequences and tiles whose plan fits in shared memory
+constexpr int kPlanTiles = 2048;
+struct PlanShared {
+  long long sums[32];
+  int32_t tile[kPlanSeqs + 1], first[kPlanSeqs], last[kPlanSeqs], len[kPlanSeqs];
+  int32_t cum[kPlanTiles + 1];
+};
+
+// By one CTA of kPlanThreads.  tile_rows: (token, head) rows of a tile; workers: shares of
+// the line.  Latency is all that counts here (a few dependent loads and block-wide sums), so
+// what the tiles need of their sequences, and the line, stay in shared memory in usual calls.
+__device__ void make_plan(const ChunkArgs& a, const ChunkPlan& p, int tile_rows, int workers, int min_share,
+                          PlanShared& sh) {
+  const bool few = a.B <= kPlanSeqs;
   long long tiles = 0, blocks = 0;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + static_cast<int>(threadIdx.x);
-    int n = 0, len = 0, first = 0;
-    if (b < a.B) {
-      const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
-      len = max(a.kv_lens[b], 0);
-      first = min(max(c0, 0), a.T);
-      n = min(max(c1, first), a.T) - first;
-    }
-    const int nt = (n * a.H + tile_rows - 1) / tile_rows;      // total_q * H < 2^30
-    // a sequence without cached tokens keeps one block (of zeros) for its tiles to read
-    const int nb = n > 0 ? max(1, (len + kChunkBlk - 1) / kChunkBlk) : 0;
+    const Sequence s = sequence(a, b);
+    const int nt = (s.n * a.H + tile_rows - 1) / tile_rows;      // total_q * H < 2^30
     long long t_all, b_all;
-    const long long t0 = tiles + block_sum(nt, &t_all, sums);
-    const long long s0 = blocks + block_sum(nb, &b_all, sums);
+    const long long t0 = tiles + block_sum(nt, &t_all, sh.sums);
+    const long long s0 = blocks + block_sum(s.blocks, &b_all, sh.sums);
     if (b < a.B) {
-      const long long left = p.cap_blocks - s0;
-      if (nb > left) {
-        len = left > 0 ? static_cast<int>(left) * kChunkBlk : 0;
-        atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
-      }
+      const int len = seq_len(p, s, s0);
+      if (len != s.len) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
       p.tile_base[b] = static_cast<int>(t0);
-      p.seq_base[b] = static_cast<int>(min(s0, static_cast<long long>(p.cap_blocks)));
+      p.seq_base[b] = seq_base(p, s0);
       p.seq_len[b] = len;
-      if (small) {
-        s_tile[b] = static_cast<int>(t0);
-        s_first[b] = first;
-        s_last[b] = first + n;
-        s_len[b] = len;
+      if (few) {
+        sh.tile[b] = static_cast<int>(t0);
+        sh.first[b] = s.first;
+        sh.last[b] = s.first + s.n;
+        sh.len[b] = len;
       }
     }
     tiles += t_all;
@@ -98,10 +115,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   }
   if (threadIdx.x == 0) {
     p.tile_base[a.B] = static_cast<int>(tiles);
-    p.seq_base[a.B] = static_cast<int>(min(blocks, static_cast<long long>(p.cap_blocks)));
-    if (small) s_tile[a.B] = static_cast<int>(tiles);
+    p.seq_base[a.B] = seq_base(p, blocks);
+    if (few) sh.tile[a.B] = static_cast<int>(tiles);
   }
   __syncthreads();
+  const bool short_line = tiles <= kPlanTiles;
   long long line = 0;
   for (int t0 = 0; t0 < static_cast<int>(tiles); t0 += kPlanThreads) {
     const int t = t0 + static_cast<int>(threadIdx.x);
@@ -109,16 +127,17 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     int n = 0;
     if (t < tiles) {
       int b, first, last, len, base;
-      if (small) {
-        b = find_last_le(s_tile, a.B + 1, t);
-        first = s_first[b];
-        last = s_last[b];
-        len = s_len[b];
-        base = s_tile[b];
+      if (few) {
+        b = find_last_le(sh.tile, a.B + 1, t);
+        first = sh.first[b];
+        last = sh.last[b];
+        len = sh.len[b];
+        base = sh.tile[b];
       } else {
         b = find_last_le(p.tile_base, a.B + 1, t);
-        first = min(max(a.cu_q[b], 0), a.T);
-        last = min(max(a.cu_q[b + 1], first), a.T);
+        const Sequence s = sequence(a, b);
+        first = s.first;
+        last = s.first + s.n;
         len = p.seq_len[b];
         base = p.tile_base[b];
       }
@@ -138,10 +157,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
       tile = make_int4(b, row, rows, blk);
     }
     long long all;
-    const long long at = line + block_sum(n, &all, sums);
+    const long long at = line + block_sum(n, &all, sh.sums);
     if (t < tiles) {
+      const int cum = static_cast<int>(min(at, 0x7fffffffll));
       p.tile[t] = tile;
-      p.cum[t] = static_cast<int>(min(at, 0x7fffffffll));
+      p.cum[t] = cum;
+      if (short_line) sh.cum[t] = cum;
     }
     line += all;
   }
@@ -153,16 +174,45 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   const int per = max(min_share, static_cast<int>((line + workers - 1) / workers));
   if (threadIdx.x == 0) {
     p.cum[tiles] = static_cast<int>(line);
+    if (short_line) sh.cum[tiles] = static_cast<int>(line);
+  }
+  __syncthreads();
+  // the tile at the start of each share, so that nobody else has to search, and the cut
+  // tiles, found at the first share that begins inside each
+  const int32_t* cum = short_line ? sh.cum : p.cum;
+  const int c = static_cast<int>(threadIdx.x);
+  bool cut = false;
+  int4 piece = make_int4(0, 0, 0, 0);
+  if (c < workers) {
+    const long long x = static_cast<long long>(c) * per;
+    const int t = x < line ? find_last_le(cum, static_cast<int>(tiles) + 1, static_cast<int>(x)) : -1;
+    p.start[c] = t;
+    if (t >= 0) {
+      const int begin = cum[t];
+      cut = begin < x && begin / per + 1 == c;
+      if (cut) {
+        const int4 tile = p.tile[t];
+        piece = make_int4(tile.y, tile.z, c - 1, (cum[t + 1] - 1) / per);
+      }
+    }
+  }
+  long long cuts;
+  const long long k = block_sum(cut ? 1 : 0, &cuts, sh.sums);
+  if (cut) p.cut[k] = piece;
+  if (threadIdx.x == 0) {
     p.head[0] = static_cast<int>(tiles);
     p.head[1] = static_cast<int>(line);
     p.head[2] = per;
+    p.head[3] = static_cast<int>(cuts);
   }
-  __syncthreads();
-  // the tile at the start of each share, so that nobody else has to search
-  for (int c = threadIdx.x; c < workers; c += kPlanThreads) {
-    const long long x = static_cast<long long>(c) * per;
-    p.start[c] = x < line ? find_last_le(p.cum, static_cast<int>(tiles) + 1, static_cast<int>(x)) : -1;
-  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1)
+    plan_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows, int workers, int min_share) {
+  __shared__ PlanShared sh;
+  grid_dep_wait();
+  grid_dep_launch();
+  make_plan(a, p, tile_rows, workers, min_share, sh);
 }
 
 // ---------------------------------------------------------------------------
@@ -183,110 +233,141 @@ __device__ __forceinline__ bool not_finite(uint32_t bf16x2) {
   return (bf16x2 & 0x7f80u) == 0x7f80u || (bf16x2 & 0x7f800000u) == 0x7f800000u;
 }
 
-__global__ void __launch_bounds__(256) expand_kernel(const ChunkArgs a, const ChunkPlan p) {
-  __shared__ uint32_t mapped[8], odd[8];
+// CTA 0 makes the plan meanwhile; the others find the sequences' places by themselves (the
+// same sums over the batch), so that one launch does both.
+constexpr int kExpandRows = 2;     // rows of a block that a warp expands at once: 32 warps, 64 rows
+__global__ void __launch_bounds__(kPlanThreads, 1)
+    expand_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows, int workers, int min_share) {
+  __shared__ PlanShared sh;
+  __shared__ uint32_t mapped[32], odd[32];
   grid_dep_wait();
   grid_dep_launch();
+  if (blockIdx.x == 0) {
+    make_plan(a, p, tile_rows, workers, min_share, sh);
+    return;
+  }
+  // sh.first: first block of each sequence, sh.last: its visible positions; in rounds of
+  // kPlanSeqs sequences
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int total = p.seq_base[a.B];
-  for (int g = blockIdx.x; g <= total; g += gridDim.x) {
-    // block `total` stands behind the copy: zeros, for the sequences that found no room
-    const int64_t out_blk = g < total ? g : p.cap_blocks;
-    int b = 0, s0 = 0, len = 0;
-    if (g < total) {
-      b = find_last_le(p.seq_base, a.B + 1, g);
-      s0 = (g - p.seq_base[b]) * kChunkBlk;
-      len = p.seq_len[b];
-    }
-    // lane j < 8: the pool row of position s0 + 8 warp + j
-    long long row = -1;
-    const int s = s0 + 8 * warp + lane;
-    if (lane < 8 && s < len) {
-      const int page = s / a.page_size;
-      if (page >= a.max_pages) {
-        atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
-      } else {
-        const int phys = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + page);
-        if (phys >= 0) {
-          row = static_cast<long long>(phys) * a.page_size + (s - page * a.page_size);
-          if (row >= a.num_rows) {
-            row = -1;
-            atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
+  long long blocks = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanSeqs) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    const Sequence s = sequence(a, b);
+    long long all;
+    const long long s0 = blocks + block_sum(s.blocks, &all, sh.sums);
+    sh.first[threadIdx.x] = seq_base(p, s0);
+    sh.last[threadIdx.x] = seq_len(p, s, s0);
+    const int begin = seq_base(p, blocks), end = seq_base(p, blocks + all);
+    blocks += all;
+    __syncthreads();
+    const int seqs = min(kPlanSeqs, a.B - b0);
+    // blocks [begin, end) in turn; with the last round also the one behind the copy: zeros,
+    // for the sequences that found no room
+    const int stop = b0 + kPlanSeqs >= a.B ? end + 1 : end;
+    const int step = gridDim.x - 1;
+    int g = begin + (static_cast<int>(blockIdx.x) - 1 - begin % step + step) % step;
+    for (; g < stop; g += step) {
+      const bool real = g < end;
+      const int64_t out_blk = real ? g : p.cap_blocks;
+      int i = 0, s0 = 0, len = 0;
+      if (real) {
+        // the last sequence that begins at or before g and has blocks
+        i = find_last_le(sh.first, seqs, g);
+        s0 = (g - sh.first[i]) * kChunkBlk;
+        len = sh.last[i];
+      }
+      // lane j < kExpandRows: the pool row of position s0 + kExpandRows warp + j
+      long long row = -1;
+      const int pos = s0 + kExpandRows * warp + lane;
+      if (lane < kExpandRows && pos < len) {
+        const int page = pos / a.page_size;
+        if (page >= a.max_pages) {
+          atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
+        } else {
+          const int phys = __ldg(a.table + static_cast<int64_t>(b0 + i) * a.max_pages + page);
+          if (phys >= 0) {
+            row = static_cast<long long>(phys) * a.page_size + (pos - page * a.page_size);
+            if (row >= a.num_rows) {
+              row = -1;
+              atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
+            }
           }
         }
       }
-    }
-    const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
-    uint32_t poison = 0;
-    uint2 in[8][2];
-    uint2 more[8][2];
-    uint32_t sc[8];
+      const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
+      uint32_t poison = 0;
+      uint2 in[kExpandRows][4];
+      uint32_t sc[kExpandRows];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const long long r = __shfl_sync(0xffffffffu, row, j);
-      in[j][0] = in[j][1] = more[j][0] = more[j][1] = make_uint2(0u, 0u);
-      sc[j] = 127;
-      if (r >= 0) {
-        const uint8_t* src = a.pool + r * a.stride;
-        const uint2* w = reinterpret_cast<const uint2*>(src + (lane < 28 ? 16 * lane : 456 + 32 * (lane - 28)));
-        in[j][0] = __ldg(w);
-        in[j][1] = __ldg(w + 1);
-        if (lane >= 28) {
-          more[j][0] = __ldg(w + 2);
-          more[j][1] = __ldg(w + 3);
+      for (int j = 0; j < kExpandRows; ++j) {
+        const long long r = __shfl_sync(0xffffffffu, row, j);
+        in[j][0] = in[j][1] = in[j][2] = in[j][3] = make_uint2(0u, 0u);
+        sc[j] = 127;
+        if (r >= 0) {
+          const uint8_t* src = a.pool + r * a.stride;
+          const uint2* w = reinterpret_cast<const uint2*>(src + (lane < 28 ? 16 * lane : 456 + 32 * (lane - 28)));
+          in[j][0] = __ldg(w);
+          in[j][1] = __ldg(w + 1);
+          if (lane >= 28) {
+            in[j][2] = __ldg(w + 2);
+            in[j][3] = __ldg(w + 3);
+          } else {
+            sc[j] = __ldg(src + kNope + lane / 4);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kExpandRows; ++j) {
+        uint32_t o[8];
+        if (lane < 28) {
+          const float f = ue8m0_value(sc[j]);
+          const uint32_t w[4] = {in[j][0].x, in[j][0].y, in[j][1].x, in[j][1].y};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o[2 * k] = expand_pair(w[k] & 0xffffu, f);
+            o[2 * k + 1] = expand_pair(w[k] >> 16, f);
+          }
         } else {
-          sc[j] = __ldg(src + kNope + lane / 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o[2 * k] = in[j][k].x;
+            o[2 * k + 1] = in[j][k].y;
+          }
         }
-      }
-    }
+        bool bad = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t o[8];
-      if (lane < 28) {
-        const float f = ue8m0_value(sc[j]);
-        const uint32_t w[4] = {in[j][0].x, in[j][0].y, in[j][1].x, in[j][1].y};
+        for (int k = 0; k < 8; ++k) bad |= not_finite(o[k]);
+        if (__any_sync(0xffffffffu, bad)) {
+          poison |= 1u << j;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          o[2 * k] = expand_pair(w[k] & 0xffffu, f);
-          o[2 * k + 1] = expand_pair(w[k] >> 16, f);
+          for (int k = 0; k < 8; ++k) o[k] = 0;
         }
-      } else {
-        o[0] = in[j][0].x; o[1] = in[j][0].y; o[2] = in[j][1].x; o[3] = in[j][1].y;
-        o[4] = more[j][0].x; o[5] = more[j][0].y; o[6] = more[j][1].x; o[7] = more[j][1].y;
+        uint4* dst = reinterpret_cast<uint4*>(p.kv + (out_blk * kChunkBlk + kExpandRows * warp + j) * kQkDim + 16 * lane);
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      bool bad = false;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) bad |= not_finite(o[k]);
-      if (__any_sync(0xffffffffu, bad)) {
-        poison |= 1u << j;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = 0;
+      if (lane == 0) {
+        mapped[warp] = have & ((1u << kExpandRows) - 1u);
+        odd[warp] = poison;
       }
-      uint4* dst = reinterpret_cast<uint4*>(p.kv + (out_blk * kChunkBlk + 8 * warp + j) * kQkDim + 16 * lane);
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    }
-    __syncthreads();
-    if (lane == 0) {
-      mapped[warp] = have;
-      odd[warp] = poison;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      unsigned long long x = 0, y = 0;
-      for (int w = 0; w < 8; ++w) {
-        x |= static_cast<unsigned long long>(mapped[w] & 0xffu) << (8 * w);
-        y |= static_cast<unsigned long long>(odd[w]) << (8 * w);
+      __syncthreads();
+      if (warp == 0) {
+        // warp w's bits at kExpandRows w: the lower 16 warps make the low words
+        const uint32_t m = mapped[lane] << (kExpandRows * (lane & 15)), q = odd[lane] << (kExpandRows * (lane & 15));
+        const uint32_t m0 = __reduce_or_sync(0xffffffffu, lane < 16 ? m : 0u), m1 = __reduce_or_sync(0xffffffffu, lane < 16 ? 0u : m);
+        const uint32_t q0 = __reduce_or_sync(0xffffffffu, lane < 16 ? q : 0u), q1 = __reduce_or_sync(0xffffffffu, lane < 16 ? 0u : q);
+        if (lane == 0)
+          p.seen[out_blk] = make_ulonglong2(m0 | static_cast<unsigned long long>(m1) << 32,
+                                            q0 | static_cast<unsigned long long>(q1) << 32);
       }
-      p.seen[out_blk] = make_ulonglong2(x, y);
+      __syncthreads();
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Merge: the partial results of the tiles that a share's border cuts.  Grid (row groups,
-// borders): border c lies between workers c - 1 and c and serves its tile if it is the
-// first border inside.  A row is joined by ROW_WARPS warps, each taking every
+// Merge: the partial results of the tiles that a share's border cuts.  Grid (row groups, cut
+// tiles).  A row is joined by ROW_WARPS warps, each taking every
 // ROW_WARPS-th partial result: a long context over one tile of few rows has as many partial
 // results as there are workers, and one warp reading them in turn would be all latency.
 // ---------------------------------------------------------------------------
@@ -297,20 +378,16 @@ __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const Chu
   __shared__ float weight[8];
   grid_dep_wait();
   grid_dep_launch();
-  const int c1 = blockIdx.y + 1;
-  const int t = p.start[c1];
-  if (t < 0) return;
-  const int per = p.head[2];
-  const int begin = p.cum[t], end = p.cum[t + 1];
-  if (begin >= c1 * per || begin / per + 1 != c1) return;
-  const int4 tile = p.tile[t];
+  const int cuts = p.head[3];
+  const int4 cut = p.cut[blockIdx.y];     // first row of the tile, rows, first and last worker
+  if (static_cast<int>(blockIdx.y) >= cuts) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x * kRows + warp / ROW_WARPS;
-  if (blockIdx.x * kRows >= tile.z) return;
-  const int first = c1 - 1, last = (end - 1) / per;
+  if (static_cast<int>(blockIdx.x) * kRows >= cut.y) return;
+  const int first = cut.z, last = cut.w;
   // slot of worker c: its share begins inside the tile (0), or the tile inside its share (1)
-  auto at = [&](int c) { return static_cast<int64_t>(2 * c + (begin < c * per ? 0 : 1)) * tile_rows + row; };
-  const bool live = row < tile.z;
+  auto at = [&](int c) { return static_cast<int64_t>(2 * c + (c == first ? 1 : 0)) * tile_rows + row; };
+  const bool live = row < cut.y;
   float top = -INFINITY;
   if (live)
     for (int c = first + lane; c <= last; c += 32) top = fmaxf(top, p.lse_part[at(c)]);
@@ -354,7 +431,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const Chu
   }
   if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t orow = static_cast<int64_t>(tile.y) + row;
+  const int64_t orow = static_cast<int64_t>(cut.x) + row;
   __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + orow * kNope) + lane;
 #pragma unroll
   for (int k = 0; k < 7; ++k) out[32 * k] = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
@@ -405,6 +482,7 @@ size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
   plan->seq_base = reinterpret_cast<int32_t*>(take(4 * (B + 1)));
   plan->seq_len = reinterpret_cast<int32_t*>(take(4 * B));
   plan->start = reinterpret_cast<int32_t*>(take(4 * kMaxSms));
+  plan->cut = reinterpret_cast<int4*>(take(16 * kMaxSms));
   plan->lse_part = reinterpret_cast<float*>(take(size_t{4} * 2 * kMaxPairs * kPairRows));
   plan->o_part = reinterpret_cast<float*>(take(size_t{4} * 2 * kMaxPairs * kPairRows * kNope));
   plan->seen = reinterpret_cast<ulonglong2*>(take(16 * static_cast<size_t>(cap + 1)));
@@ -414,11 +492,12 @@ size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
 
 cudaError_t launch_merge(const ChunkArgs& a, const ChunkPlan& p, int rows, int workers, cudaStream_t s) {
   if (workers < 2) return cudaSuccess;
-  // few tiles (no more than workers): many partial results a row
+  // few tiles: many partial results a row
   const int64_t tiles = (static_cast<int64_t>(a.T) * a.H + rows - 1) / rows + a.B;
+  const unsigned cuts = static_cast<unsigned>(tiles < workers - 1 ? tiles : workers - 1);
   if (tiles * 4 <= workers)
-    return launch_programmatic(merge_kernel<8>, dim3(rows, workers - 1), dim3(256), 0, s, a, p, rows);
-  return launch_programmatic(merge_kernel<2>, dim3(rows / 4, workers - 1), dim3(256), 0, s, a, p, rows);
+    return launch_programmatic(merge_kernel<8>, dim3(rows, cuts), dim3(256), 0, s, a, p, rows);
+  return launch_programmatic(merge_kernel<2>, dim3(rows / 4, cuts), dim3(256), 0, s, a, p, rows);
 }
 
 cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_t s) {
@@ -426,11 +505,9 @@ cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_
   cudaError_t e = pair_workers(&workers);
   if (e != cudaSuccess) return e;
   if (workers > kMaxPairs) workers = kMaxPairs;
-  e = launch_programmatic(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, p, kPairRows, workers, kMinShare);
-  if (e != cudaSuccess) return e;
   const int64_t blocks = p.cap_blocks + 1;
-  e = launch_programmatic(expand_kernel, dim3(static_cast<unsigned>(blocks < kMaxSms * 8 ? blocks : kMaxSms * 8)),
-                          dim3(256), 0, s, a, p);
+  const unsigned grid = 1 + static_cast<unsigned>(blocks < kMaxSms - 1 ? blocks : kMaxSms - 1);
+  e = launch_programmatic(expand_kernel, dim3(grid), dim3(kPlanThreads), 0, s, a, p, kPairRows, workers, kMinShare);
   if (e != cudaSuccess) return e;
   e = launch_chunk_pair(a, p, workers, s);
   return e == cudaSuccess ? launch_merge(a, p, kPairRows, workers, s) : e;

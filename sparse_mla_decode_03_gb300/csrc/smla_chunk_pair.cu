@@ -108,7 +108,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int4 tile = plan.tile[t];
         const int begin = plan.cum[t], end = min(x1, plan.cum[t + 1]);
         const int nb = end - x;
-        const int row0 = (plan.seq_base[tile.x] + tile.w + (x - begin)) * kChunkBlk;
+        // the last block first: scores that a distance bias shapes fall along the way, and
+        // the running maximum seldom rises
+        const int row0 = (plan.seq_base[tile.x] + tile.w + (end - 1 - begin)) * kChunkBlk;
         if (nq > 0) ok = wait(bar(QEMPTY), (nq - 1) & 1, stop, a.status);
         if (!ok) break;
         ++nq;
@@ -122,7 +124,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const uint32_t f = stage(&dst);
               if (!ok) break;
               for (int c = 0; c < 4; ++c)
-                tma_load_2d_pair(dst + c * 4096, &maps.k, 256 * h + 64 * c, row0 + i * kChunkBlk + 32 * rank, f);
+                tma_load_2d_pair(dst + c * 4096, &maps.k, 256 * h + 64 * c, row0 - i * kChunkBlk + 32 * rank, f);
             }
           }
           if (i > 0) {
@@ -133,7 +135,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               // columns 0..255 in halves of 128; 256..447 in halves of 96 (and 32 not read)
               const int col = h == 0 ? 128 * rank : 256 + 96 * rank;
               for (int c = 0; c < 2; ++c)
-                tma_load_2d_pair(dst + c * 8192, &maps.v, col + 64 * c, row0 + (i - 1) * kChunkBlk, f);
+                tma_load_2d_pair(dst + c * 8192, &maps.v, col + 64 * c, row0 - (i - 1) * kChunkBlk, f);
             }
           }
         }
@@ -242,12 +244,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int4 tile = plan.tile[t];
       const int begin = plan.cum[t], after = plan.cum[t + 1], end = min(x1, after);
       const int nb = end - x;
-      const int base = plan.seq_base[tile.x], blk = tile.w + (x - begin);
+      const int base = plan.seq_base[tile.x], blk = tile.w + (end - 1 - begin);     // the first block
       const int row = static_cast<int>(rank) * 128 + r;
-      const bool mine = row < tile.z;
-      RowState<MODS> st(a, plan, tile, row, mine);
+      RowState<MODS> st(a, plan, tile, row, row < tile.z);
       for (int i = 0; ok && i < nb; ++i) {
-        const ulonglong2 rows = plan.seen[base + blk + i];
+        const ulonglong2 rows = plan.seen[base + blk - i];
         ok = warp_wait(bar(SFULL), ns & 1, stop, a.status);
         ++ns;
         if (!ok) break;
@@ -260,7 +261,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(sempty);
         uint32_t p[32];
-        const float alpha = st.weights(v, (blk + i) * kChunkBlk, rows, p);
+        const float alpha = st.weights(v, (blk - i) * kChunkBlk, rows, p);
         // the value product before this one is done: P may be written, O rescaled
         if (i > 0) {
           ok = warp_wait(bar(PV), (np - 1) & 1, stop, a.status);
@@ -279,8 +280,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = warp_wait(bar(PV), (np - 1) & 1, stop, a.status);
       if (!ok) break;
       tc_fence_after();
-      store_rows<kPairRows>(a, plan, inverse_sum(st.l, st.lr), lse_of(st.m, st.l), tO, tile, row, mine, begin >= x0 && after <= x1,
-                            2 * worker + (begin < x0 ? 0 : 1));
+      store_rows<kPairRows, 32>(a, plan, inverse_sum(st.l, st.lr), lse_of(st.m, st.l), tO, tile,
+                                static_cast<int>(rank) * 128 + 32 * warp, begin >= x0 && after <= x1,
+                                2 * worker + (begin < x0 ? 0 : 1), sbase + kPOff + warp * 32 * 128);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(oempty);

@@ -60,8 +60,10 @@ constexpr uint32_t kColS = 448;
 // PFULL: weights written; PV: value product done; OEMPTY: results taken.
 enum Bar : int { FULL = 0, EMPTY = 2, QFULL = 4, QEMPTY, SFULL, SEMPTY, PFULL, PV, OEMPTY, kBars };
 
-// A row of the blocks on the line, walked block by block: page and row in it follow by
-// additions, divided out at a tile's start only.
+// A row of the blocks on the line, walked tile by tile and each tile's share from its last
+// block to its first (scores that a distance bias shapes then fall along the way, and the
+// running maximum seldom rises): page and row in it follow by subtractions, divided out at a
+// tile's start only.
 struct Cursor {
   int x, x1, t, next;     // next: where tile t ends
   int b, left;            // sequence, and its positions from the row's on
@@ -70,7 +72,7 @@ struct Cursor {
     const int4 tile = p.tile[t];
     next = p.cum[t + 1];
     b = tile.x;
-    const int pos = (tile.w + (x - p.cum[t])) * kChunkBlk + row;
+    const int pos = (tile.w + (min(x1, next) - 1 - p.cum[t])) * kChunkBlk + row;
     left = p.seq_len[b] - pos;
     page = pos / page_size;
     off = pos - page * page_size;
@@ -83,12 +85,12 @@ struct Cursor {
       load(p, row, page_size);
       return;
     }
-    left -= kChunkBlk;
-    page += pages;
-    off += rest;
-    if (off >= page_size) {
-      off -= page_size;
-      ++page;
+    left += kChunkBlk;
+    page -= pages;
+    off -= rest;
+    if (off < 0) {
+      off += page_size;
+      --page;
     }
   }
 };
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int x = x0, t = t_first; ok && x < x1; ++t) {
       const int4 tile = plan.tile[t];
       const int begin = plan.cum[t], after = plan.cum[t + 1], end = min(x1, after);
-      const int nb = end - x, blk = tile.w + (x - begin);
+      const int nb = end - x, blk = tile.w + (end - 1 - begin);     // the first block
       // rows past the tile stay whatever they are (a product's rows do not mix), so a warp
       // without rows only keeps step
       TwoRows<MODS> st(a, plan, tile, 16 * warp + g);
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(SEMPTY));
         uint32_t p[16];
         float alpha[2];
-        st.weights(v, (blk + i) * kChunkBlk, rows, p, alpha);
+        st.weights(v, (blk - i) * kChunkBlk, rows, p, alpha);
         if (i > 0) {
           ok = warp_wait(bar(PV), (n - 1) & 1, stop, a.status);
           if (!ok) break;
@@ -599,9 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           inv[i] = inverse_sum(l, lr);
           lse[i] = lse_of(st.m[i], l);
         }
-        const int row = 16 * warp + (lane & 15);
-        store_rows<kSingleRows>(a, plan, to_row(inv), to_row(lse), tO, tile, row, lane < 16 && row < tile.z,
-                                begin >= x0 && after <= x1, 2 * worker + (begin < x0 ? 0 : 1));
+        store_rows<kSingleRows, 16>(a, plan, to_row(inv), to_row(lse), tO, tile, 16 * warp, begin >= x0 && after <= x1,
+                                    2 * worker + (begin < x0 ? 0 : 1), sbase + kPOff + warp * 16 * 128);
       }
       tc_fence_before();
       __syncwarp();
