@@ -21,9 +21,8 @@
 // 134 take a slower path.
 //
 // Warps of a CTA: 0..3 softmax and results (lanes 0..15: 64 rows lie in 16 tensor-memory
-// lanes of each quarter), 4..19 expand (4 rows of each block; the next block's bytes are in
-// flight in registers, the page ids of the one after next too), 20 issues the products,
-// scores or value product, whichever is ready, 21 loads Q.  Every wait is bounded.
+// lanes of each quarter), 4..19 expand (two sets in turn), 20 issues the scores, 21 the value
+// products, 22 loads Q.  Every wait is bounded.
 #include <cstring>
 #include <mutex>
 
@@ -35,9 +34,11 @@ namespace smla {
 namespace {
 
 constexpr int kExpandWarp0 = 4;
-constexpr int kExpandWarps = 16;
+constexpr int kSetWarps = 8;               // a set of expanding warps; two sets take turns
+constexpr int kRows = 64 / kSetWarps;      // of a block, a warp
 constexpr int kMmaWarp = 20;
-constexpr int kQWarp = 21;
+constexpr int kPvWarp = 21;
+constexpr int kQWarp = 22;
 constexpr int kThreads = 24 * 32;
 // Registers (setmaxnreg): what the launch gives is split among the warpgroups.
 constexpr int kLaunchRegs = 80;
@@ -51,14 +52,15 @@ constexpr int kQOff = 0;
 constexpr int kBufOff = 8 * kSlab;
 constexpr int kPOff = kBufOff + 2 * kBuf;
 constexpr int kBarOff = kPOff + kSlab;
-constexpr int kMaskOff = kBarOff + 256;    // mapped and poisoned positions: [2 buffers][16 half bytes][2]
-constexpr int kSmem = kMaskOff + 64 + 1024;
+constexpr int kMaskOff = kBarOff + 256;    // mapped rows and rows that are not finite: [2 buffers][2][8 bytes]
+constexpr int kSmem = kMaskOff + 32 + 1024;
 constexpr uint32_t kColS = 448;
 
-// FULL / EMPTY: block buffer filled / its value product done; QFULL / QEMPTY: Q loaded /
-// its last scores done; SFULL / SEMPTY: scores in tensor memory / taken by the softmax;
-// PFULL: weights written; PV: value product done; OEMPTY: results taken.
-enum Bar : int { FULL = 0, EMPTY = 2, QFULL = 4, QEMPTY, SFULL, SEMPTY, PFULL, PV, OEMPTY, kBars };
+// FULL / EMPTY: half of a block buffer (columns 0..255, the rest) filled / its value product
+// done, two buffers; QFULL / QEMPTY: Q loaded / its last scores done; SFULL / SEMPTY: scores
+// in tensor memory / taken by the softmax; PFULL: weights written; PV: value product done;
+// OEMPTY: results taken.
+enum Bar : int { FULL = 0, EMPTY = 4, QFULL = 8, QEMPTY, SFULL, SEMPTY, PFULL, PV, OEMPTY, kBars };
 
 // A row of the blocks on the line, walked tile by tile and each tile's share from its last
 // block to its first (scores that a distance bias shapes then fall along the way, and the
@@ -116,6 +118,8 @@ __device__ __forceinline__ uint4 expand8(uint2 w, uint32_t m) {
   const uint2 a = expand4(w.x, m), b = expand4(w.y, m);
   return make_uint4(a.x, a.y, b.x, b.y);
 }
+// Bits 15 and 31: an infinite or NaN bf16.
+__device__ __forceinline__ uint32_t rope_bits(uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; }
 // Any e4m3 NaN among four bytes: a byte of 0x7f carries into its bit 7.
 __device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
 
@@ -141,22 +145,35 @@ __device__ __forceinline__ bool not_finite(uint32_t v) {
 __device__ __forceinline__ void sts(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-__device__ __forceinline__ void sts8(uint32_t addr, uint2 v) {
-  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
-}
 __device__ __forceinline__ void sts4(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ uint2 ldg_once(const uint8_t* p) {
+// Predicated forms, so that lanes with and without a word do not part ways.
+__device__ __forceinline__ void sts_if(bool p, uint32_t addr, uint4 v) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t@q st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n\t}\n" ::"r"(addr),
+               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(p ? 1 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void sts8_if(bool p, uint32_t addr, uint2 v) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %3, 0;\n\t@q st.shared.v2.u32 [%0], {%1,%2};\n\t}\n" ::"r"(addr), "r"(v.x),
+               "r"(v.y), "r"(p ? 1 : 0)
+               : "memory");
+}
+// 8 bytes of the pool (read-only here, once), or `none`.
+__device__ __forceinline__ uint2 ldg_if(bool p, const uint8_t* src, uint32_t none) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %3, 0;\n\tmov.b32 %0, %4;\n\tmov.b32 %1, %4;\n\t"
+      "@q ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n\t}\n"
+      : "=&r"(v.x), "=&r"(v.y)
+      : "l"(src), "r"(p ? 1 : 0), "r"(none));
   return v;
 }
 
-// The 8-byte words of a row that a lane holds: l, l + 32 and l + 64.  Words 0..55 are the
-// nope part (word w: columns 8 (w % 8) .. + 7 of group w / 8), 56 the scales, 57..72 the rope.
+// The 8-byte words of 8 rows that a lane l holds.  Words 0..55 of a row are the nope part
+// (word w: columns 8 (w % 8) .. + 7 of group w / 8), 56 the scales, 57..72 the rope.
+// a[j], b[j]: words l and l + 32 of row j; c[k]: word 64 + l % 9 of row 3 k + l / 9.
 struct RowWords {
-  uint2 a, b, c;
+  uint2 a[8], b[8], c[3];
 };
 
 // Two rows a thread: the 16 rows of a warp with their 64 scores of a block, as the
@@ -250,20 +267,13 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-template <int I>
-struct Index {
-  static constexpr int value = I;
-};
-// The low halves of 16 bytes side by side.
-__device__ __forceinline__ unsigned long long sixteen_halves(unsigned long long low, unsigned long long high) {
-  auto eight = [](unsigned long long x) {
-    x = (x | (x >> 4)) & 0x00ff00ff00ff00ffull;
-    x = (x | (x >> 8)) & 0x0000ffff0000ffffull;
-    return (x | (x >> 16)) & 0x00000000ffffffffull;
-  };
-  return eight(low) | (eight(high) << 32);
+// After a wait has run out: products in flight end within microseconds, 1 ms before they lose
+// their memory.
+__device__ __forceinline__ void drain() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < 2000000) {
+  }
 }
-
 template <bool MODS>
 __global__ void __launch_bounds__(kThreads, 1)
     single_kernel(const ChunkArgs a, const ChunkPlan plan, const __grid_constant__ CUtensorMap qmap) {
@@ -280,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i)
-      mbar_init(bar(i), i < EMPTY ? kExpandWarps : i == SEMPTY || i == PFULL || i == OEMPTY ? 4 : 1);
+      mbar_init(bar(i), i < EMPTY ? kSetWarps : i == SEMPTY || i == PFULL || i == OEMPTY ? 4 : 1);
     *stop = 0;
     fence_mbar_init();
   }
@@ -302,10 +312,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kExpandWarp0 && warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsExpand) : "memory");
     // ---------------- expand ----------------
-    // Rows 4 w16 .. + 3 of each block.  Lane j's cursor follows row j % 4; the warp reads a
-    // row at once, 256 consecutive bytes a load.
-    const int w16 = warp - kExpandWarp0;
-    const int mine = 4 * w16 + (lane & 3);
+    // Set B takes blocks B, B + 2, ..., which go to buffer B: while one set expands, the
+    // other's loads are in flight (they may hold no more bytes than the small L1 that the
+    // shared memory leaves, so a set that did both in turn left it empty half of the time).
+    // Rows 8 w .. + 7 of a block are warp w's; lane j's cursor follows row j % 8; the warp
+    // reads a row at once, 256 consecutive bytes a load.
+    const int w8 = (warp - kExpandWarp0) % kSetWarps;
+    const int B = (warp - kExpandWarp0) / kSetWarps;
+    const int mine = kRows * w8 + (lane & (kRows - 1));
+    const int c_row = lane / 9, c_word = lane % 9;       // of words c
     if (x0 < x1) {
       const int pages_step = kChunkBlk / a.page_size, rest = kChunkBlk % a.page_size;
       // page id of the cursor's row, -1 = no row there
@@ -315,22 +330,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
         return -1;
       };
-      // the rows' bytes; returns which of the four are mapped
-      auto fetch = [&](int id, int off, RowWords (&d)[4]) {
+      // the rows' bytes; returns which of them are mapped
+      long long at_now = -1;         // byte offset of the lane's row of that block, -1: not there
+      auto fetch = [&](int id, int off, RowWords& d) {
         const long long r = static_cast<long long>(id) * a.page_size + off;
         const bool there = id >= 0 && r < a.num_rows;
         if (id >= 0 && !there) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
-        const uint32_t have = __ballot_sync(0xffffffffu, there) & 15u;
-        const long long at = r * a.stride;
+        const uint32_t have = __ballot_sync(0xffffffffu, there) & ((1u << kRows) - 1u);
+        // a row that is not there: zeros (and scale bytes of 0: zeros too)
+        at_now = there ? r * a.stride : -1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint8_t* src = a.pool + __shfl_sync(0xffffffffu, at, j) + 8 * lane;
-          d[j].a = d[j].b = d[j].c = make_uint2(0u, 0u);
-          if ((have >> j) & 1) {
-            d[j].a = ldg_once(src);
-            d[j].b = ldg_once(src + 256);
-            if (lane < 9) d[j].c = ldg_once(src + 512);
-          }
+        for (int j = 0; j < kRows; ++j) {
+          const long long o = __shfl_sync(0xffffffffu, at_now, j);
+          const uint8_t* src = a.pool + o + 8 * lane;
+          d.a[j] = ldg_if(o >= 0, src, 0u);
+          d.b[j] = ldg_if(o >= 0, src + 256, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const long long o = __shfl_sync(0xffffffffu, at_now, 3 * k + c_row);
+          d.c[k] = ldg_if(o >= 0 && 3 * k + c_row < kRows && lane < 27, a.pool + o + 512 + 8 * c_word, 0u);
         }
         return have;
       };
@@ -339,12 +358,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       at.x1 = x1;
       at.t = t_first;
       at.load(plan, mine, a.page_size);
-      RowWords words[2][4];
-      uint32_t have[2];
-      have[0] = fetch(lookup(at), at.off, words[0]);
-      at.step(plan, mine, a.page_size, pages_step, rest);
-      int id = lookup(at), off = at.off;
+      RowWords d;
       const int count = x1 - x0;
+      auto step = [&]() { at.step(plan, mine, a.page_size, pages_step, rest); };
+      if (B == 1) step();
+      uint32_t have = fetch(lookup(at), at.off, d);
+      step();
+      step();
+      int id = lookup(at), off = at.off;
       bool ok = true;
       // word b of this lane: nope, scales (lane 24) or rope; how its NaN are found
       const uint32_t mb = lane < 24 ? 0x7f7f7f7fu : lane > 24 ? 0x7f807f80u : 0u;
@@ -352,159 +373,192 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tb = lane < 24 ? 0x80808080u : 0x80008000u;
       const int sh = 8 * (lane >> 3);
       const uint32_t dst_nope = sbase + kBufOff + (lane >> 3) * kSlab;
-      const int rope_b = lane - 25, rope_c = lane + 7;         // rope word of words b and c
-      // block n: words[B] are its rows', buffer B is its buffer
-      auto block = [&](int n, auto which) {
-        constexpr int B = decltype(which)::value;
-        have[B ^ 1] = fetch(id, off, words[B ^ 1]);
-        at.step(plan, mine, a.page_size, pages_step, rest);
-        id = lookup(at);
-        off = at.off;
-        if (n >= 2) ok = warp_wait(bar(EMPTY + B), ((n >> 1) - 1) & 1, stop, a.status);
-        if (!ok) return;
+      for (int n = B; n < count; n += 2) {
+        // this lane's groups' scale bytes of row j (lanes 24 .. 31: no second group)
+        auto scale_a = [&](int j) { return (__shfl_sync(0xffffffffu, d.b[j].x, 24) >> sh) & 0xffu; };
+        auto scale_b = [&](int j) {
+          const uint32_t s = (__shfl_sync(0xffffffffu, d.b[j].y, 24) >> sh) & 0xffu;
+          return lane < 24 ? s : 0u;
+        };
         // anything that the fast path does not cover: NaN, infinite rope values, scale bytes
         // past 134
         uint32_t na = 0, nb = 0, nc = 0, top = 0;
-        uint32_t sx[4], sy[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const RowWords& d = words[B][j];
-          sx[j] = __shfl_sync(0xffffffffu, d.b.x, 24);
-          sy[j] = __shfl_sync(0xffffffffu, d.b.y, 24);
-          na |= nan_bits(d.a.x) | nan_bits(d.a.y);
-          nb |= ((d.b.x & mb) + ab) | ((d.b.y & mb) + ab);
-          nc |= ((d.c.x & 0x7f807f80u) + 0x00800080u) | ((d.c.y & 0x7f807f80u) + 0x00800080u);
-          sx[j] = (sx[j] >> sh) & 0xffu;
-          sy[j] = (sy[j] >> sh) & 0xffu;         // lanes 24..31: the padding byte, not used
-          top = max(top, max(sx[j], lane < 24 ? sy[j] : 0u));
+        for (int j = 0; j < kRows; ++j) {
+          na |= nan_bits(d.a[j].x) | nan_bits(d.a[j].y);
+          nb |= ((d.b[j].x & mb) + ab) | ((d.b[j].y & mb) + ab);
+          top = max(top, max(scale_a(j), scale_b(j)));
         }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) nc |= rope_bits(d.c[k].x) | rope_bits(d.c[k].y);
         const bool odd = (na & 0x80808080u) | (nb & tb) | (nc & 0x80008000u) | (top > 134u ? 1u : 0u);
         const bool usual = !__any_sync(0xffffffffu, odd);
-        uint32_t dropped = 0;
+        uint32_t dropped = 0;        // rows that are not finite: held as zeros
+        // The unusual path reads its rows again, one by one: kept in registers for it, they
+        // would make the usual path spill.
+        auto again = [&](int j, int byte) {      // 8 bytes of row j, zeros where it is not there
+          const long long o = __shfl_sync(0xffffffffu, at_now, j);
+          return ldg_if(o >= 0, a.pool + o + byte, 0u);
+        };
+        if (!usual) {
+#pragma unroll 1
+          for (int j = 0; j < kRows; ++j) {
+            const uint2 wa = again(j, 8 * lane), wb = again(j, 256 + 8 * lane), wc = again(j, 512 + 8 * min(lane, 8));
+            const uint32_t sx = __shfl_sync(0xffffffffu, wb.x, 24), sy = __shfl_sync(0xffffffffu, wb.y, 24);
+            const uint32_t s = max((sx >> sh) & 0xffu, lane < 24 ? (sy >> sh) & 0xffu : 0u);
+            const bool bad = ((nan_bits(wa.x) | nan_bits(wa.y)) & 0x80808080u) |
+                             ((((wb.x & mb) + ab) | ((wb.y & mb) + ab)) & tb) |
+                             ((rope_bits(wc.x) | rope_bits(wc.y)) & 0x80008000u) | (s > kMaxScaleByte ? 1u : 0u);
+            dropped |= __any_sync(0xffffffffu, bad) ? 1u << j : 0u;
+          }
+        }
+        const uint32_t parity = ((n >> 1) - 1) & 1;
+        if (n >= 2) ok = warp_wait(bar(EMPTY + 2 * B), parity, stop, a.status);
+        if (!ok) break;
+        const uint32_t dn = dst_nope + kRows * w8 * 128 + B * kBuf;
+        auto unit = [&](int j) { return j * 128 + (((lane & 7) ^ j) << 4); };    // the lane's unit of row j
+        if (usual) {
+          // two rows at a time, their conversions interleaved; times 2^(s - 7) as two bf16
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const RowWords& d = words[B][j];
-          const int row = 4 * w16 + j;
-          const uint32_t line = row * 128 + B * kBuf;
-          const uint32_t dn = dst_nope + line + (((lane & 7) ^ (row & 7)) << 4);
-          const uint32_t dr = sbase + kBufOff + 7 * kSlab + line;
-          auto rope = [&](int w) { return dr + (((w >> 1) ^ (row & 7)) << 4) + 8 * (w & 1); };
-          if (usual) {
-            // 2^(s - 7) as two bf16
-            sts(dn, expand8(d.a, ((sx[j] + 120u) << 7) * 0x00010001u));
-            if (lane < 24) sts(dn + 4 * kSlab, expand8(d.b, ((sy[j] + 120u) << 7) * 0x00010001u));
-            if (lane > 24) sts8(rope(rope_b), d.b);
-            if (lane < 9) sts8(rope(rope_c), d.c);
-          } else {
-            const uint4 o = expand8_any(d.a, sx[j]);
-            uint4 o2 = lane < 24 ? expand8_any(d.b, sy[j]) : make_uint4(0u, 0u, 0u, 0u);
-            if (lane > 24) o2 = make_uint4(d.b.x, d.b.y, 0u, 0u);
-            const bool bad = not_finite(o.x) | not_finite(o.y) | not_finite(o.z) | not_finite(o.w) |
-                             not_finite(o2.x) | not_finite(o2.y) | not_finite(o2.z) | not_finite(o2.w) |
-                             not_finite(d.c.x) | not_finite(d.c.y);
-            const bool drop = __any_sync(0xffffffffu, bad);       // zeros for a row that is not finite
-            dropped |= drop ? 1u << j : 0u;
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            sts(dn, drop ? zero : o);
-            if (lane < 24) sts(dn + 4 * kSlab, drop ? zero : o2);
-            if (lane > 24) sts8(rope(rope_b), drop ? make_uint2(0u, 0u) : d.b);
-            if (lane < 9) sts8(rope(rope_c), drop ? make_uint2(0u, 0u) : d.c);
+          for (int j0 = 0; j0 < kRows; j0 += 2) {
+            uint4 o[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              o[j] = expand8(d.a[j0 + j], ((scale_a(j0 + j) + 120u) << 7) * 0x00010001u);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) sts(dn + unit(j0 + j), o[j]);
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < kRows; ++j) {
+            const uint2 wa = again(j, 8 * lane);
+            const uint32_t s = (again(j, kNope).x >> sh) & 0xffu;
+            sts(dn + unit(j), (dropped >> j) & 1 ? make_uint4(0u, 0u, 0u, 0u) : expand8_any(wa, s));
           }
         }
         if (lane == 0) {
-          masks[B * 32 + w16] = static_cast<uint8_t>(have[B]);
-          masks[B * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
+          masks[B * 16 + w8] = static_cast<uint8_t>(have);
+          masks[B * 16 + 8 + w8] = static_cast<uint8_t>(dropped);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(FULL + B));
-      };
-      for (int n = 0; ok && n < count; n += 2) {
-        block(n, Index<0>());
-        if (ok && n + 1 < count) block(n + 1, Index<1>());
+        if (lane == 0) mbar_arrive(bar(FULL + 2 * B));
+        if (n >= 2) ok = warp_wait(bar(EMPTY + 2 * B + 1), parity, stop, a.status);
+        if (!ok) break;
+        // the rope: word w of row j
+        const uint32_t dr = sbase + kBufOff + 7 * kSlab + kRows * w8 * 128 + B * kBuf;
+        auto rope = [&](int j, int w) { return dr + j * 128 + (((w >> 1) ^ j) << 4) + 8 * (w & 1); };
+        if (usual) {
+#pragma unroll
+          for (int j0 = 0; j0 < kRows; j0 += 2) {
+            uint4 o[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              o[j] = expand8(d.b[j0 + j], ((scale_b(j0 + j) + 120u) << 7) * 0x00010001u);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              sts_if(lane < 24, dn + 4 * kSlab + unit(j0 + j), o[j]);
+              sts8_if(lane > 24, rope(j0 + j, (lane - 25) & 15), d.b[j0 + j]);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < kRows; ++j) {
+            const uint2 wb = again(j, 256 + 8 * lane);
+            const uint32_t s = (again(j, kNope).y >> sh) & 0xffu;
+            const bool drop = (dropped >> j) & 1;
+            sts_if(lane < 24, dn + 4 * kSlab + unit(j), drop ? make_uint4(0u, 0u, 0u, 0u) : expand8_any(wb, s));
+            sts8_if(lane > 24, rope(j, (lane - 25) & 15), drop ? make_uint2(0u, 0u) : wb);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const int j = 3 * k + c_row;
+          sts8_if(j < kRows && lane < 27, rope(j & 7, 7 + c_word), (dropped >> j) & 1 ? make_uint2(0u, 0u) : d.c[k]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(FULL + 2 * B + 1));
+        // block n + 2's bytes, and the page ids of the one after it
+        have = fetch(id, off, d);
+        step();
+        step();
+        id = lookup(at);
+        off = at.off;
       }
     }
   } else if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma) : "memory");
+    // The whole warp walks its schedule, one elected lane issues (descriptors stay uniform).
+    // Two warps, so that a value product that is ready does not wait for a block that is
+    // not, nor the other way round.
+    const uint64_t d0 = smem_desc(sbase, 16, 1024, SWZ_128B), dv = smem_desc(sbase, kSlab, 1024, SWZ_128B);
+    const uint32_t hi = static_cast<uint32_t>(d0 >> 32);
     if (warp == kMmaWarp) {
-      // ---------------- products ----------------
-      // Scores of block n or the value product of block v, whichever is ready, so that a
-      // late block does not hold up the one before it.  The whole warp walks, one elected
-      // lane issues (descriptors stay uniform).
+      // ---------------- scores ----------------
       constexpr uint32_t kIdQK = idesc_bf16(64, 64, false, false);
-      constexpr uint32_t kIdV0 = idesc_bf16(64, 256, false, true);
-      constexpr uint32_t kIdV1 = idesc_bf16(64, 192, false, true);
-      const uint64_t d0 = smem_desc(sbase, 16, 1024, SWZ_128B), dv = smem_desc(sbase, kSlab, 1024, SWZ_128B);
-      const uint32_t hi = static_cast<uint32_t>(d0 >> 32);
-      const uint32_t lq = static_cast<uint32_t>(d0), lk = lq + (kBufOff >> 4), lp = lq + (kPOff >> 4);
-      const uint32_t lv = static_cast<uint32_t>(dv) + (kBufOff >> 4);
-      const int count = x1 - x0;
-      int n = 0, v = 0;                                 // scores and value products so far
-      int tn = t_first, tv = t_first;                   // their tiles
-      int n0 = 0, v0 = 0;                               // first block of those tiles
-      int n1 = count > 0 ? min(x1, plan.cum[tn + 1]) - x0 : 0, v1 = n1;   // behind their last
-      uint32_t kn = 0, kv = 0;                          // how many tiles before them
+      const uint32_t lq = static_cast<uint32_t>(d0), lk = lq + (kBufOff >> 4);
+      uint32_t n = 0, k = 0;               // blocks and tiles so far
       bool ok = true;
-      long long idle = clock64();
-      auto ready = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar(i), parity & 1)); };
-      while (ok && v < count) {
-        if (v < n && ready(PFULL, v) && (v > v0 || kv == 0 || ready(OEMPTY, kv - 1))) {
-          tc_fence_after();
-          const uint32_t lb = lv + (v & 1) * (kBuf >> 4);
-          const uint32_t old = v > v0 ? 1u : 0u;
-          if (elect_one()) {
+      for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
+        const int end = min(x1, plan.cum[t + 1]);
+        ok = warp_wait(bar(QFULL), k & 1, stop, a.status);
+        for (; ok && x < end; ++x, ++n) {
+          if (n > 0) ok = warp_wait(bar(SEMPTY), (n - 1) & 1, stop, a.status);
+          for (int h = 0; ok && h < 2; ++h) {
+            ok = warp_wait(bar(FULL + 2 * (n & 1) + h), (n >> 1) & 1, stop, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t la = lq + h * ((4 * kSlab) >> 4), lb = lk + (n & 1) * (kBuf >> 4) + h * ((4 * kSlab) >> 4);
+            if (elect_one()) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t acc = k > 0 ? 1u : old;
-              mma_f16_ss_hl(tmem, lp + ((k * 32) >> 4), hi, lb + ((k * 2048) >> 4), hi, kIdV0, acc);
-              mma_f16_ss_hl(tmem + 256, lp + ((k * 32) >> 4), hi, lb + ((4 * kSlab + k * 2048) >> 4), hi, kIdV1, acc);
+                for (int i = 0; i < 4; ++i)
+                  mma_f16_ss_hl(tmem + kColS, la + ((c * kSlab + i * 32) >> 4), hi, lb + ((c * kSlab + i * 32) >> 4), hi,
+                                kIdQK, c + i > 0 ? 1u : static_cast<uint32_t>(h));
+              if (h == 1) {
+                mma_commit(bar(SFULL));
+                if (x + 1 == end) mma_commit(bar(QEMPTY));
+              }
             }
-            mma_commit(bar(EMPTY + (v & 1)));
+            __syncwarp();
+          }
+        }
+      }
+      if (!ok) drain();
+    } else if (warp == kPvWarp) {
+      // ---------------- value products ----------------
+      constexpr uint32_t kIdV0 = idesc_bf16(64, 256, false, true), kIdV1 = idesc_bf16(64, 192, false, true);
+      const uint32_t lp = static_cast<uint32_t>(d0) + (kPOff >> 4), lv = static_cast<uint32_t>(dv) + (kBufOff >> 4);
+      uint32_t n = 0, k = 0;
+      bool ok = true;
+      for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
+        const int end = min(x1, plan.cum[t + 1]);
+        uint32_t old = 0;                  // the tile's first product overwrites O
+        for (; ok && x < end; ++x, ++n, old = 1) {
+          ok = warp_wait(bar(PFULL), n & 1, stop, a.status);
+          if (ok && old == 0 && k > 0) ok = warp_wait(bar(OEMPTY), (k - 1) & 1, stop, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t lb = lv + (n & 1) * (kBuf >> 4);
+          if (elect_one()) {
+            // columns 0..255 first: the next block's may be written while 256..447 follow
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_f16_ss_hl(tmem, lp + ((i * 32) >> 4), hi, lb + ((i * 2048) >> 4), hi, kIdV0, i > 0 ? 1u : old);
+            mma_commit(bar(EMPTY + 2 * (n & 1)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_f16_ss_hl(tmem + 256, lp + ((i * 32) >> 4), hi, lb + ((4 * kSlab + i * 2048) >> 4), hi, kIdV1,
+                            i > 0 ? 1u : old);
+            mma_commit(bar(EMPTY + 2 * (n & 1) + 1));
             mma_commit(bar(PV));
           }
           __syncwarp();
-          if (++v == v1 && v < count) {
-            ++tv;
-            ++kv;
-            v0 = v;
-            v1 = min(x1, plan.cum[tv + 1]) - x0;
-          }
-          idle = clock64();
-        } else if (n < count && n <= v + 1 && ready(FULL + (n & 1), n >> 1) && (n == 0 || ready(SEMPTY, n - 1)) &&
-                   (n > n0 || ready(QFULL, kn))) {
-          tc_fence_after();
-          const uint32_t lb = lk + (n & 1) * (kBuf >> 4);
-          if (elect_one()) {
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f16_ss_hl(tmem + kColS, lq + ((c * kSlab + k * 32) >> 4), hi, lb + ((c * kSlab + k * 32) >> 4), hi,
-                              kIdQK, c + k > 0 ? 1u : 0u);
-            mma_commit(bar(SFULL));
-            if (n + 1 == n1) mma_commit(bar(QEMPTY));
-          }
-          __syncwarp();
-          if (++n == n1 && n < count) {
-            ++tn;
-            ++kn;
-            n0 = n;
-            n1 = min(x1, plan.cum[tn + 1]) - x0;
-          }
-          idle = clock64();
-        } else if (__any_sync(0xffffffffu, *stop || clock64() - idle > kWaitLimit)) {
-          if (lane == 0 && !*stop) {
-            *stop = 1;
-            atomicCAS(a.status, 0, SMLA_ERR_TIMEOUT);
-          }
-          ok = false;
         }
       }
-      if (!ok) {   // products in flight end within microseconds: 1 ms before they lose their memory
-        const long long t0 = clock64();
-        while (clock64() - t0 < 2000000) {
-        }
-      }
+      if (!ok) drain();
     } else if (warp == kQWarp) {
       // ---------------- Q ----------------
       bool ok = true;
@@ -545,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool idle = 16 * warp >= tile.z;
       for (int i = 0; ok && i < nb; ++i, ++n) {
         ok = warp_wait(bar(SFULL), n & 1, stop, a.status);
-        if (ok) ok = warp_wait(bar(FULL + (n & 1)), (n >> 1) & 1, stop, a.status);   // the masks' writers
+        if (ok) ok = warp_wait(bar(FULL + 2 * (n & 1)), (n >> 1) & 1, stop, a.status);   // the masks' writers
         if (!ok) break;
         if (idle) {
           if (lane == 0) mbar_arrive(bar(SEMPTY));
@@ -558,11 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[32];
         tmem_ld_16x64(tS, v);
         const volatile unsigned long long* mk =
-            reinterpret_cast<const volatile unsigned long long*>(smem + kMaskOff + (n & 1) * 32);
-        const unsigned long long m0 = mk[0], m1 = mk[1], d0 = mk[2], d1 = mk[3];
-        ulonglong2 rows = make_ulonglong2(~0ull, 0ull);
-        if ((m0 & m1) != 0x0f0f0f0f0f0f0f0full || (d0 | d1) != 0)
-          rows = make_ulonglong2(sixteen_halves(m0, m1), sixteen_halves(d0, d1));
+            reinterpret_cast<const volatile unsigned long long*>(smem + kMaskOff + (n & 1) * 16);
+        const ulonglong2 rows = make_ulonglong2(mk[0], mk[1]);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
