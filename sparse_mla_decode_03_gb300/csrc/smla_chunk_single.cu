@@ -199,59 +199,77 @@ struct TwoRows {
     }
   }
 
+  // The two rows side by side: the weights are on the way from scores to value product, and
+  // one row after the other is twice the latency.
   __device__ __forceinline__ void weights(float (&v)[32], int s0, const ulonglong2& rows, uint32_t (&p)[16],
                                           float (&alpha)[2]) {
     const int col = 2 * (threadIdx.x & 3);
     const float scale2 = mods.scale2;
+    if constexpr (MODS) {
+      const float from0 = static_cast<float>(pos[0] - s0 - col), from1 = static_cast<float>(pos[1] - s0 - col);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          v[4 * j + e] = mods(v[4 * j + e], slope2[0], from0 - static_cast<float>(8 * j + e));
+          v[4 * j + 2 + e] = mods(v[4 * j + 2 + e], slope2[1], from1 - static_cast<float>(8 * j + e));
+        }
+    }
+    const unsigned long long seen0 = seen_of(rows.x, s0, lo[0], hi[0]), seen1 = seen_of(rows.x, s0, lo[1], hi[1]);
+    if (__any_sync(0xffffffffu, (seen0 & seen1) != ~0ull)) {
+      const unsigned long long at0 = seen0 >> col, at1 = seen1 >> col;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (!((at0 >> (8 * j + e)) & 1)) v[4 * j + e] = -INFINITY;
+          if (!((at1 >> (8 * j + e)) & 1)) v[4 * j + 2 + e] = -INFINITY;
+        }
+    }
+    float t[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int j = 1; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] = fmaxf(t[e], v[4 * j + e]);
+    float top[2] = {fmaxf(t[0], t[1]), fmaxf(t[2], t[3])}, shift[2];
+#pragma unroll
+    for (int x = 1; x <= 2; x *= 2) {
+      const float u0 = __shfl_xor_sync(0xffffffffu, top[0], x), u1 = __shfl_xor_sync(0xffffffffu, top[1], x);
+      top[0] = fmaxf(top[0], u0);
+      top[1] = fmaxf(top[1], u1);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if constexpr (MODS) {
-        const float from = static_cast<float>(pos[i] - s0 - col);
+      if constexpr (!MODS) top[i] *= scale2;
+      const bool raise = top[i] > m[i] + kHeadroom || (m[i] == -INFINITY && top[i] > m[i]);
+      alpha[i] = raise ? exp2_fast(m[i] - top[i]) : 1.f;      // 0 while m is -inf
+      m[i] = raise ? top[i] : m[i];
+      shift[i] = m[i] == -INFINITY ? 0.f : m[i];
+    }
+    float sum[4] = {0.f, 0.f, 0.f, 0.f}, rsum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[4 * j + 2 * i] = mods(v[4 * j + 2 * i], slope2[i], from - static_cast<float>(8 * j));
-          v[4 * j + 2 * i + 1] = mods(v[4 * j + 2 * i + 1], slope2[i], from - static_cast<float>(8 * j + 1));
-        }
-      }
-      const unsigned long long seen = seen_of(rows.x, s0, lo[i], hi[i]);
-      if (__any_sync(0xffffffffu, seen != ~0ull)) {
-        const unsigned long long at = seen >> col;
+    for (int j = 0; j < 8; ++j) {
+      float e[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (!((at >> (8 * j)) & 1)) v[4 * j + 2 * i] = -INFINITY;
-          if (!((at >> (8 * j)) & 2)) v[4 * j + 2 * i + 1] = -INFINITY;
-        }
+      for (int k = 0; k < 4; ++k) {
+        const float x = v[4 * j + k];
+        e[k] = exp2_fast(MODS ? x - shift[k / 2] : fmaf(x, scale2, -shift[k / 2]));
+        sum[k] += e[k];
       }
-      float top = fmaxf(v[2 * i], v[2 * i + 1]);
 #pragma unroll
-      for (int j = 1; j < 8; ++j) top = fmaxf(top, fmaxf(v[4 * j + 2 * i], v[4 * j + 2 * i + 1]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      if constexpr (!MODS) top *= scale2;
-      alpha[i] = 1.f;
-      if (top > m[i] + kHeadroom || (m[i] == -INFINITY && top > m[i])) {
-        alpha[i] = exp2_fast(m[i] - top);     // 0 while m is -inf
-        m[i] = top;
-        l[i] *= alpha[i];
-        lr[i] *= alpha[i];
+      for (int i = 0; i < 2; ++i) {
+        p[2 * j + i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+        rsum[2 * i] += __uint_as_float(p[2 * j + i] << 16);
+        rsum[2 * i + 1] += __uint_as_float(p[2 * j + i] & 0xffff0000u);
       }
-      const float shift = m[i] == -INFINITY ? 0.f : m[i];
-      float sum0 = 0.f, sum1 = 0.f, rsum0 = 0.f, rsum1 = 0.f;
+    }
+    // a row of the cache that is not finite is held as zeros; who sees it becomes NaN
+    const bool odd0 = (seen0 & rows.y) != 0, odd1 = (seen1 & rows.y) != 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x0 = v[4 * j + 2 * i], x1 = v[4 * j + 2 * i + 1];
-        const float e0 = exp2_fast(MODS ? x0 - shift : fmaf(x0, scale2, -shift));
-        const float e1 = exp2_fast(MODS ? x1 - shift : fmaf(x1, scale2, -shift));
-        sum0 += e0;
-        sum1 += e1;
-        p[2 * j + i] = pack_bf16(e0, e1);
-        rsum0 += __uint_as_float(p[2 * j + i] << 16);
-        rsum1 += __uint_as_float(p[2 * j + i] & 0xffff0000u);
-      }
-      l[i] += sum0 + sum1;
-      lr[i] += rsum0 + rsum1;
-      // a row of the cache that is not finite is held as zeros; who sees it becomes NaN
-      if (seen & rows.y) l[i] = lr[i] = __uint_as_float(0x7fffffffu);
+    for (int i = 0; i < 2; ++i) {
+      const bool odd = i == 0 ? odd0 : odd1;
+      l[i] = odd ? __uint_as_float(0x7fffffffu) : fmaf(l[i], alpha[i], sum[2 * i] + sum[2 * i + 1]);
+      lr[i] = odd ? __uint_as_float(0x7fffffffu) : fmaf(lr[i], alpha[i], rsum[2 * i] + rsum[2 * i + 1]);
     }
   }
 };
@@ -598,8 +616,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       TwoRows<MODS> st(a, plan, tile, 16 * warp + g);
       const bool idle = 16 * warp >= tile.z;
       for (int i = 0; ok && i < nb; ++i, ++n) {
+        ok = warp_wait(bar(FULL + 2 * (n & 1)), (n >> 1) & 1, stop, a.status);     // the masks' writers
+        if (!ok) break;
+        const volatile unsigned long long* mk =
+            reinterpret_cast<const volatile unsigned long long*>(smem + kMaskOff + (n & 1) * 16);
+        const ulonglong2 rows = make_ulonglong2(mk[0], mk[1]);
         ok = warp_wait(bar(SFULL), n & 1, stop, a.status);
-        if (ok) ok = warp_wait(bar(FULL + 2 * (n & 1)), (n >> 1) & 1, stop, a.status);   // the masks' writers
         if (!ok) break;
         if (idle) {
           if (lane == 0) mbar_arrive(bar(SEMPTY));
@@ -611,9 +633,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         float v[32];
         tmem_ld_16x64(tS, v);
-        const volatile unsigned long long* mk =
-            reinterpret_cast<const volatile unsigned long long*>(smem + kMaskOff + (n & 1) * 16);
-        const ulonglong2 rows = make_ulonglong2(mk[0], mk[1]);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
