@@ -253,11 +253,18 @@ def _pool(kv_pages: torch.Tensor, page_size: int) -> None:
         raise ValueError("kv_pages must hold a page of page_size >= 1 rows")
 
 
-def _stream_on(stream: Optional[torch.cuda.Stream], device: torch.device) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if s.device != device:
-        raise ValueError(f"stream is on {s.device}, the tensors are on {device}")
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream_on(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
+    """The handle of `stream`, or of the device's current stream (its raw handle: a Stream
+    object costs more than a small launch)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    return stream.cuda_stream
+
+
+def _adr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _on(device: torch.device):
@@ -317,8 +324,8 @@ def smla_cache_append(kv: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
                           _row_stride(kv_pages))
     stride = kv.stride(0) if kv.shape[0] > 1 else QK
     with _on(dev):
-        st = _lib.load().smla_cache_append(_ptr(kv), stride, kv.shape[0], _ptr(kv_pages), _ptr(block_table),
-                                           _ptr(cu_q), _ptr(kv_lens), ctypes.byref(p),
+        st = _lib.load().smla_cache_append(_adr(kv), stride, kv.shape[0], _adr(kv_pages), _adr(block_table),
+                                           _adr(cu_q), _adr(kv_lens), ctypes.byref(p),
                                            _stream_on(stream, dev))
     _check(st, "smla_cache_append")
 
@@ -336,8 +343,8 @@ def smla_cache_reserve(page_size: int, ref_count: torch.Tensor, block_table: tor
     p = make_cache_params(ref_count.shape[0], page_size, block_table.shape[0], block_table.shape[1])
     ws = _cache_workspace(p, workspace, dev)
     with _on(dev):
-        st = _lib.load().smla_cache_reserve(_ptr(ref_count), _ptr(block_table), _ptr(target_lens),
-                                            ctypes.byref(p), _ptr(ws), _bytes(ws), _stream_on(stream, dev))
+        st = _lib.load().smla_cache_reserve(_adr(ref_count), _adr(block_table), _adr(target_lens),
+                                            ctypes.byref(p), _adr(ws), _bytes(ws), _stream_on(stream, dev))
     _check(st, "smla_cache_reserve")
 
 
@@ -368,9 +375,9 @@ def smla_cache_fork(kv_pages: torch.Tensor, page_size: int, ref_count: torch.Ten
         raise ValueError("kv_lens must be [B], and parents and children equally long")
     ws = _cache_workspace(p, workspace, dev)
     with _on(dev):
-        st = _lib.load().smla_cache_fork(_ptr(kv_pages), _ptr(ref_count), _ptr(block_table), _ptr(kv_lens),
-                                         _ptr(parents), _ptr(children), parents.shape[0], ctypes.byref(p),
-                                         _ptr(ws), _bytes(ws), _stream_on(stream, dev))
+        st = _lib.load().smla_cache_fork(_adr(kv_pages), _adr(ref_count), _adr(block_table), _adr(kv_lens),
+                                         _adr(parents), _adr(children), parents.shape[0], ctypes.byref(p),
+                                         _adr(ws), _bytes(ws), _stream_on(stream, dev))
     _check(st, "smla_cache_fork")
 
 
@@ -386,7 +393,7 @@ def smla_cache_free(ref_count: torch.Tensor, block_table: torch.Tensor, kv_lens:
         raise ValueError("kv_lens must be [B] for a block_table of B rows, on a CUDA device")
     p = make_cache_params(ref_count.shape[0], 1, block_table.shape[0], block_table.shape[1])
     with _on(dev):
-        st = _lib.load().smla_cache_free(_ptr(ref_count), _ptr(block_table), _ptr(kv_lens), _ptr(rows),
+        st = _lib.load().smla_cache_free(_adr(ref_count), _adr(block_table), _adr(kv_lens), _adr(rows),
                                          rows.shape[0], ctypes.byref(p), _stream_on(stream, dev))
     _check(st, "smla_cache_free")
 
@@ -413,8 +420,8 @@ def smla_cache_compact(kv_pages: torch.Tensor, page_size: int, ref_count: torch.
         raise ValueError("info must be int32 [2]")
     ws = _cache_workspace(p, workspace, dev)
     with _on(dev):
-        st = _lib.load().smla_cache_compact(_ptr(kv_pages), _ptr(ref_count), _ptr(block_table), _ptr(ref_out),
-                                            _ptr(table_out), _ptr(info), ctypes.byref(p), _ptr(ws),
+        st = _lib.load().smla_cache_compact(_adr(kv_pages), _adr(ref_count), _adr(block_table), _adr(ref_out),
+                                            _adr(table_out), _adr(info), ctypes.byref(p), _adr(ws),
                                             _bytes(ws), _stream_on(stream, dev))
     _check(st, "smla_cache_compact")
     return info
@@ -487,8 +494,8 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     with _on(dev):
         st = _lib.load().smla_chunk_attention(
-            _ptr(q), _ptr(kv_pages), _ptr(block_table), _ptr(cu_q), _ptr(kv_lens), _ptr(vis_begin),
-            _ptr(vis_end), _ptr(slopes), _ptr(out), _ptr(lse), ctypes.byref(p), _ptr(workspace),
+            _adr(q), _adr(kv_pages), _adr(block_table), _adr(cu_q), _adr(kv_lens), _adr(vis_begin),
+            _adr(vis_end), _adr(slopes), _adr(out), _adr(lse), ctypes.byref(p), _adr(workspace),
             _bytes(workspace), _stream_on(stream, dev))
     _check(st, "smla_chunk_attention")
     return out, lse

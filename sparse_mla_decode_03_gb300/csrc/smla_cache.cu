@@ -56,59 +56,65 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu_q, int B, int t) {
   return lo;
 }
 
-// One warp a token.  Lane l < 28 holds nope columns 16 l .. 16 l + 15 (four lanes a
-// scale group), lanes 28..31 the rope.
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= a.total) return;
-  const uint4* src = a.kv + t * a.token_units + 2 * lane;
-  const uint4 u0 = __ldg(src), u1 = __ldg(src + 1);
+// The row of token t, or null (reported) if it has no place; null too outside every sequence.
+__device__ __forceinline__ uint8_t* row_of(const AppendArgs& a, int t) {
   const int b = sequence_of(a.cu_q, a.B, t);
-  if (b < 0) return;
+  if (b < 0) return nullptr;
   const int64_t pos = static_cast<int64_t>(__ldg(a.kv_lens + b)) - (__ldg(a.cu_q + b + 1) - t);
-  int64_t row = -1;
   if (pos >= 0) {   // below 2^31: kv_lens is an int32
     const uint32_t at = static_cast<uint32_t>(pos), page = at / static_cast<uint32_t>(a.page_size);
     if (page < static_cast<uint32_t>(a.max_pages)) {
       const int phys = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + page);
       if (phys >= 0 && phys < a.num_pages)
-        row = static_cast<int64_t>(phys) * a.page_size + (at - page * a.page_size);
+        return a.pool + (static_cast<int64_t>(phys) * a.page_size + (at - page * a.page_size)) * a.stride;
     }
   }
-  if (row < 0) {
-    if (lane == 0) report(a.status, SMLA_ERR_INDEX_RANGE);
-    return;
-  }
-  uint8_t* dst = a.pool + row * a.stride;
-  const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-  float x[16];
-  float top = 0.f;
-  bool bad = false;
+  if ((threadIdx.x & 31) == 0) report(a.status, SMLA_ERR_INDEX_RANGE);
+  return nullptr;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// One token of a warp.  Lane l < 28 holds nope columns 16 l .. 16 l + 15 (four lanes a scale
+// group), lanes 28..31 the rope.  The row is put together in shared memory (stage: 73 words)
+// and leaves in consecutive words.
+__device__ __forceinline__ void write_row(const AppendArgs& a, uint8_t* dst, const uint4& u0, const uint4& u1,
+                                          uint2* stage) {
+  const int lane = threadIdx.x & 31;
+  uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+  // largest magnitude as bf16 bits, two columns at a time (magnitudes compare as integers)
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 8; ++i) m = max_u16x2(m, w[i] & 0x7fff7fffu);
+  uint32_t top = max(m >> 16, m & 0xffffu);
+  if (__any_sync(0xffffffffu, lane < 28 && top >= 0x7f80u)) {
+    // infinity and NaN are stored as NaN and do not count
+    top = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float m = fabsf(x[i]);
-    if (m < INFINITY) {
-      top = fmaxf(top, m);
-    } else {
-      bad = true;
-      x[i] = __uint_as_float(0x7fffffffu);   // infinity and NaN are stored as NaN
+    for (int i = 0; i < 8; ++i) {
+      uint32_t h[2] = {w[i] & 0xffffu, w[i] >> 16};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if ((h[k] & 0x7fffu) >= 0x7f80u) {
+          h[k] = 0x7fffu;
+          if (lane < 28) report(a.status, SMLA_ERR_RANGE);
+        } else {
+          top = max(top, h[k] & 0x7fffu);
+        }
+      }
+      w[i] = h[0] | h[1] << 16;
     }
   }
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   // 448 = 1.75 * 2^8, so the least e with top <= 448 * 2^e follows from top's exponent
   // and whether its mantissa exceeds 1.75: exact, no logarithm.
-  const uint32_t tb = __float_as_uint(top);
-  int byte = static_cast<int>(tb >> 23) - 8 + ((tb & 0x7fffffu) > 0x600000u ? 1 : 0);
-  byte = top == 0.f ? 127 : min(max(byte, 1), 254);
+  int byte = static_cast<int>(top >> 7) - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+  byte = top == 0 ? 127 : min(max(byte, 1), 254);
   // 2^(127 - byte) as a float (byte 254: the subnormal 2^-127)
   const float inv = __uint_as_float(byte < 254 ? static_cast<uint32_t>(254 - byte) << 23 : 0x00400000u);
   if (lane < 28) {
@@ -116,38 +122,63 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint16_t lo, hi;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[4 * i + 1] * inv), "f"(x[4 * i] * inv));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[4 * i + 3] * inv), "f"(x[4 * i + 2] * inv));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+          : "=h"(lo)
+          : "f"(__uint_as_float(w[2 * i] & 0xffff0000u) * inv), "f"(__uint_as_float(w[2 * i] << 16) * inv));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+          : "=h"(hi)
+          : "f"(__uint_as_float(w[2 * i + 1] & 0xffff0000u) * inv), "f"(__uint_as_float(w[2 * i + 1] << 16) * inv));
       o[i] = lo | (static_cast<uint32_t>(hi) << 16);
     }
-    uint2* d = reinterpret_cast<uint2*>(dst + 16 * lane);
-    d[0] = make_uint2(o[0], o[1]);
-    d[1] = make_uint2(o[2], o[3]);
-    if (bad) report(a.status, SMLA_ERR_RANGE);
+    stage[2 * lane] = make_uint2(o[0], o[1]);
+    stage[2 * lane + 1] = make_uint2(o[2], o[3]);
+    if ((lane & 3) == 0) reinterpret_cast<uint8_t*>(stage)[kNope + lane / 4] = static_cast<uint8_t>(byte);
   } else {
-    uint2* d = reinterpret_cast<uint2*>(dst + 456 + 32 * (lane - 28));
+    uint2* d = stage + 57 + 4 * (lane - 28);
     d[0] = make_uint2(u0.x, u0.y);
     d[1] = make_uint2(u0.z, u0.w);
     d[2] = make_uint2(u1.x, u1.y);
     d[3] = make_uint2(u1.z, u1.w);
+    if (lane == 28) reinterpret_cast<uint8_t*>(stage)[kNope + 7] = 0;      // the padding
   }
-  // the 7 scale bytes and the padding as one 8-byte word
-  uint32_t slo = 0, shi = 0;
-#pragma unroll
-  for (int g = 0; g < 7; ++g) {
-    const uint32_t v = static_cast<uint32_t>(__shfl_sync(0xffffffffu, byte, 4 * g));
-    if (g < 4) slo |= v << (8 * g);
-    else shi |= v << (8 * (g - 4));
-  }
-  if (lane == 0) *reinterpret_cast<uint2*>(dst + kNope) = make_uint2(slo, shi);
+  __syncwarp();
+  uint2* d = reinterpret_cast<uint2*>(dst);
+  d[lane] = stage[lane];
+  d[lane + 32] = stage[lane + 32];
+  if (lane < 9) d[lane + 64] = stage[lane + 64];
+  __syncwarp();
 }
+
+// N tokens a warp, all loads first: the bytes in flight are what bounds a long prompt.
+template <int N>
+__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * N;
+  if (t0 >= a.total) return;
+  __shared__ uint2 stage[8][76];
+  uint4 u[N][2];
+  uint8_t* dst[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint4* src = a.kv + min(t0 + k, a.total - 1) * a.token_units + 2 * (threadIdx.x & 31);
+    u[k][0] = __ldcs(src);
+    u[k][1] = __ldcs(src + 1);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) dst[k] = t0 + k < a.total ? row_of(a, t0 + k) : nullptr;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (dst[k] != nullptr) write_row(a, dst[k], u[k][0], u[k][1], stage[threadIdx.x >> 5]);
+}
+constexpr int kAppendTokens = 2;      // a warp, once every SM has that many warps' worth
 
 // ---------------------------------------------------------------------------
 // Ranking across the planning cluster
 // ---------------------------------------------------------------------------
 struct PlanShared {
   int warp[32];
-  int counts[2][kPlanCtas];   // one count of every CTA of the cluster, two in turn
+  int2 counts[2][kPlanCtas];   // counts of every CTA of the cluster, two slots in turn
 };
 
 // Exclusive sum of v over the CTA's threads; *total gets the sum.  All threads call.
@@ -176,62 +207,75 @@ __device__ int block_rank(int v, int* total, PlanShared* sh) {
   return s - v + (warp > 0 ? sh->warp[warp - 1] : 0);
 }
 
-// Shares this CTA's count with the cluster (slot 0 or 1; a slot may be used again after
-// another share): *before = sum of the lower ranks', returns the sum of all.  Orders
-// the cluster's memory accesses as a barrier does.
-__device__ int cluster_share(int mine, int slot, int* before, PlanShared* sh) {
+// Shares this CTA's two counts with the cluster (a slot may be used again after another
+// share): *before = sums of the lower ranks', returns the sums of all.  Orders the
+// cluster's memory accesses as a barrier does.
+__device__ int2 cluster_share(int2 mine, int slot, int2* before, PlanShared* sh) {
   cg::cluster_group cl = cg::this_cluster();
   const int rank = static_cast<int>(cl.block_rank());
   if (threadIdx.x < kPlanCtas) cl.map_shared_rank(sh, threadIdx.x)->counts[slot][rank] = mine;
   cl.sync();
-  int all = 0, low = 0;
+  int2 all = make_int2(0, 0), low = make_int2(0, 0);
 #pragma unroll
   for (int r = 0; r < kPlanCtas; ++r) {
-    const int c = sh->counts[slot][r];
-    all += c;
-    if (r < rank) low += c;
+    const int2 c = sh->counts[slot][r];
+    all.x += c.x;
+    all.y += c.y;
+    if (r < rank) {
+      low.x += c.x;
+      low.y += c.y;
+    }
   }
   *before = low;
   return all;
 }
 
-__device__ __forceinline__ void slice(int n, int* first, int* last) {
+// This CTA's part [first, last) of n things, and within it the thread's part, a run of a
+// multiple of 4: ranks then need one block-wide sum, whatever the length.
+struct Part {
+  int first, last, run0, run1;
+};
+__device__ __forceinline__ Part part_of(int n) {
   const int rank = static_cast<int>(cg::this_cluster().block_rank());
   const int per = ((n + kPlanCtas - 1) / kPlanCtas + 3) & ~3;
-  *first = min(n, rank * per);
-  *last = min(n, *first + per);
+  Part p;
+  p.first = static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(rank) * per));
+  p.last = min(n, p.first + per);
+  const int run = ((p.last - p.first + kPlanThreads - 1) / kPlanThreads + 3) & ~3;
+  p.run0 = min(p.last, p.first + static_cast<int>(threadIdx.x) * run);
+  p.run1 = min(p.last, p.run0 + run);
+  return p;
 }
-
-// Free pages (in use: inv) of [first, last), this CTA's total.
-__device__ int count_pages(const int32_t* ref, int first, int last, bool used, PlanShared* sh) {
-  int c = 0;
-  for (int p = first + threadIdx.x; p < last; p += kPlanThreads) c += (__ldcg(ref + p) > 0) == used;
-  int total;
-  block_rank(c, &total, sh);
-  return total;
-}
-
-// Gives the `want` lowest free pages (fewer where there are not so many) a count of 1
-// and lists them, ascending, in `list`.  Returns how many are listed.  Whole cluster.
-__device__ int take_free(int32_t* ref, int num_pages, int want, int32_t* list, int slot, PlanShared* sh) {
-  int first, last, before;
-  slice(num_pages, &first, &last);
-  const int mine = want > 0 ? count_pages(ref, first, last, false, sh) : 0;
-  const int all = cluster_share(mine, slot, &before, sh);
-  const int end = min(want, all);
-  for (int at = first; at < last && before < end; at += kPlanThreads) {
-    const int p = at + static_cast<int>(threadIdx.x);
-    const bool free = p < last && __ldcg(ref + p) <= 0;
-    int total;
-    const int r = before + block_rank(free ? 1 : 0, &total, sh);
-    if (free && r < end) {
-      list[r] = p;
-      ref[p] = 1;
-    }
-    before += total;
+// f(page, count) for the pages of the thread's run.
+template <class F>
+__device__ __forceinline__ void each_page(const int32_t* ref, const Part& p, F f) {
+  for (int q = p.run0; q < p.run1; q += 4) {
+    int c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = q + k < p.run1 ? __ldcg(ref + q + k) : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (q + k < p.run1) f(q + k, c[k]);
   }
-  cg::this_cluster().sync();
-  return end;
+}
+__device__ __forceinline__ int count_free(const int32_t* ref, const Part& p) {
+  int n = 0;
+  each_page(ref, p, [&](int, int c) { n += c <= 0; });
+  return n;
+}
+// Gives the `want` lowest free pages (or all) a count of 1 and lists them, ascending.
+// rank: free pages before the thread's run.
+__device__ __forceinline__ void take_free(int32_t* ref, const Part& p, int rank, int want, int32_t* list) {
+  if (rank >= want) return;
+  each_page(ref, p, [&](int page, int c) {
+    if (c <= 0) {
+      if (rank < want) {
+        list[rank] = page;
+        ref[page] = 1;
+      }
+      ++rank;
+    }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -239,59 +283,57 @@ __device__ int take_free(int32_t* ref, int num_pages, int want, int32_t* list, i
 // ---------------------------------------------------------------------------
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
     reserve_kernel(int32_t* ref, int32_t* table, const int32_t* target, int rows, int max_pages,
-                   int page_size, int num_pages, int32_t* list, int32_t* row_base, int* status) {
+                   int page_size, int num_pages, int32_t* list, int* status) {
   __shared__ PlanShared sh;
   cg::this_cluster().sync();   // every CTA has started: its shared memory may be written
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int first, last;
-  slice(rows, &first, &last);
-  auto entries = [&](int r) {      // entries of row r that the target needs
-    const int len = __ldg(target + r);
-    const int64_t need = len > 0 ? (static_cast<int64_t>(len) + page_size - 1) / page_size : 0;
-    if (need > max_pages) {
-      if (lane == 0) report(status, SMLA_ERR_INDEX_RANGE);
-      return max_pages;
+  // The table row after row: each CTA a part, each thread a run of it, so that a rank is the
+  // entries before the run plus those in it.
+  const Part pp = part_of(num_pages);
+  const int64_t entries = static_cast<int64_t>(rows) * max_pages;
+  const int64_t per = (entries + kPlanCtas - 1) / kPlanCtas;
+  const int64_t first = min(entries, cg::this_cluster().block_rank() * per), last = min(entries, first + per);
+  const int64_t run = (last - first + kPlanThreads - 1) / kPlanThreads;
+  const int64_t run0 = min(last, first + threadIdx.x * run), run1 = min(last, run0 + run);
+  // f(entry) for the unmapped entries of the run that the targets need
+  auto each_open = [&](auto f) {
+    int r = static_cast<int>(run0 / max_pages), c = static_cast<int>(run0 - static_cast<int64_t>(r) * max_pages);
+    int64_t i = run0;
+    while (i < run1) {
+      const int len = __ldg(target + r);
+      int need = len > 0 ? (len - 1) / page_size + 1 : 0;
+      if (need > max_pages) {
+        if (c == 0) report(status, SMLA_ERR_INDEX_RANGE);
+        need = max_pages;
+      }
+      const int64_t row_end = min(run1, i - c + max_pages), stop = min(run1, i - c + need);
+      int32_t* e = table;
+#pragma unroll 4
+      for (; i < stop; ++i)
+        if (__ldcg(e + i) < 0) f(i);
+      i = row_end;
+      ++r;
+      c = 0;
     }
-    return static_cast<int>(need);
   };
-  // unmapped entries of each row of the slice, then their exclusive sums
-  int mine = 0;
-  for (int r = first + warp; r < last; r += 32) {
-    const int need = entries(r);
-    const int32_t* e = table + static_cast<int64_t>(r) * max_pages;
-    int c = 0;
-    for (int i = lane; i < need; i += 32) c += e[i] < 0;
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0) row_base[r] = c;
-  }
-  __syncthreads();
-  for (int at = first; at < last; at += kPlanThreads) {
-    const int r = at + static_cast<int>(threadIdx.x);
-    const int c = r < last ? row_base[r] : 0;
-    int total;
-    const int base = mine + block_rank(c, &total, &sh);
-    if (r < last) row_base[r] = base;
-    mine += total;
-  }
-  int before;
-  const int want = cluster_share(mine, 0, &before, &sh);
-  const int got = take_free(ref, num_pages, want, list, 1, &sh);
-  if (want > got && threadIdx.x == 0) report(status, SMLA_ERR_POOL_EXHAUSTED);
-  for (int r = first + warp; r < last; r += 32) {
-    const int need = entries(r);
-    int32_t* e = table + static_cast<int64_t>(r) * max_pages;
-    int rank = before + row_base[r];
-    for (int i0 = 0; i0 < need; i0 += 32) {
-      const int i = i0 + lane;
-      const bool open = i < need && e[i] < 0;
-      const uint32_t mask = __ballot_sync(0xffffffffu, open);
-      const int k = rank + __popc(mask & ((1u << lane) - 1u));
-      if (open && k < got) e[i] = list[k];
-      rank += __popc(mask);
-    }
-  }
+  int free_total, need_total, mine = 0;
+  const int free_rank = block_rank(count_free(ref, pp), &free_total, &sh);
+  each_open([&](int64_t) { ++mine; });
+  const int need_rank = block_rank(mine, &need_total, &sh);
+  int2 low;
+  const int2 all = cluster_share(make_int2(need_total, free_total), 0, &low, &sh);
+  const int got = min(all.x, all.y);
+  take_free(ref, pp, low.y + free_rank, got, list);
+  if (all.x > got && blockIdx.x == 0 && threadIdx.x == 0) report(status, SMLA_ERR_POOL_EXHAUSTED);
+  if (got == 0) return;
+  cg::this_cluster().sync();
+  int k = low.x + need_rank;
+  if (mine > 0 && k < got)
+    each_open([&](int64_t i) {
+      if (k < got) table[i] = __ldcg(list + k);
+      ++k;
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -322,40 +364,65 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   cg::this_cluster().sync();   // every CTA has started: its shared memory may be written
   grid_dep_wait();
   grid_dep_launch();
-  int first, last, before;
-  slice(a.n, &first, &last);
-  int mine = 0;
-  for (int at = first; at < last; at += kPlanThreads) {
-    const int i = at + static_cast<int>(threadIdx.x);
-    const int len = i < last ? fork_length(a, i) : 0;
-    int total;
-    block_rank(len > 0 && len % a.page_size != 0 ? 1 : 0, &total, &sh);
-    mine += total;
+  const Part ip = part_of(a.n), pp = part_of(a.num_pages);
+  int free_total, need_total, mine = 0;
+  const int free_rank = block_rank(count_free(a.ref, pp), &free_total, &sh);
+  for (int i = ip.run0; i < ip.run1; ++i) {
+    const int len = fork_length(a, i);
+    mine += len > 0 && len % a.page_size != 0;
   }
-  const int want = cluster_share(mine, 0, &before, &sh);
-  const int got = take_free(a.ref, a.num_pages, want, a.list, 1, &sh);
-  for (int at = first; at < last; at += kPlanThreads) {
-    const int i = at + static_cast<int>(threadIdx.x);
-    const int len = i < last ? fork_length(a, i) : 0;
-    const bool need = len > 0 && len % a.page_size != 0;
-    int total;
-    const int k = before + block_rank(need ? 1 : 0, &total, &sh);
-    before += total;
-    if (i < last) {
-      int f = len < 0 ? kSkip : kNotNeeded;
-      if (need) f = k < got ? a.list[k] : kNoPage;
-      if (f == kSkip) report(a.status, SMLA_ERR_INDEX_RANGE);
-      if (f == kNoPage) report(a.status, SMLA_ERR_POOL_EXHAUSTED);
-      a.fresh[i] = f;
+  const int need_rank = block_rank(mine, &need_total, &sh);
+  int2 low;
+  const int2 all = cluster_share(make_int2(need_total, free_total), 0, &low, &sh);
+  const int got = min(all.x, all.y);
+  take_free(a.ref, pp, low.y + free_rank, got, a.list);
+  cg::this_cluster().sync();
+  int k = low.x + need_rank;
+  for (int i = ip.run0; i < ip.run1; ++i) {
+    const int len = fork_length(a, i);
+    int f = len < 0 ? kSkip : kNotNeeded;
+    if (len > 0 && len % a.page_size != 0) {
+      f = k < got ? __ldcg(a.list + k) : kNoPage;
+      ++k;
     }
+    if (f == kSkip) report(a.status, SMLA_ERR_INDEX_RANGE);
+    if (f == kNoPage) report(a.status, SMLA_ERR_POOL_EXHAUSTED);
+    a.fresh[i] = f;
   }
 }
 
-// Copies `words` 8-byte words from src to dst by the CTA's threads.
+// Copies rows from .. from + rows - 1 of the pool to to .. by the CTA's threads.  Rows that
+// follow one another without a gap go as 16-byte words where both ends allow it, four of a
+// thread's in flight.
 __device__ __forceinline__ void copy_rows(uint8_t* pool, int64_t stride, int64_t from, int64_t to,
                                           int rows) {
   const uint8_t* s = pool + from * stride;
   uint8_t* d = pool + to * stride;
+  if (stride == kRowBytes) {
+    // 16-byte aligned parts: both start on one, or both 8 bytes behind one
+    const bool same = ((reinterpret_cast<uintptr_t>(s) ^ reinterpret_cast<uintptr_t>(d)) & 8) == 0;
+    if (same) {
+      const int bytes = rows * kRowBytes;
+      const int head = static_cast<int>(reinterpret_cast<uintptr_t>(s) & 8);
+      const int units = (bytes - head) / 16, tail = bytes - head - 16 * units;
+      if (threadIdx.x == 0 && head) *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(s);
+      if (threadIdx.x == 1 && tail)
+        *reinterpret_cast<uint2*>(d + bytes - 8) = *reinterpret_cast<const uint2*>(s + bytes - 8);
+      const uint4* s4 = reinterpret_cast<const uint4*>(s + head);
+      uint4* d4 = reinterpret_cast<uint4*>(d + head);
+      const int step = blockDim.x;
+      for (int w = threadIdx.x; w < units; w += 4 * step) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (w + k * step < units) v[k] = __ldcs(s4 + w + k * step);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (w + k * step < units) __stcs(d4 + w + k * step, v[k]);
+      }
+      return;
+    }
+  }
   for (int w = threadIdx.x; w < rows * (kRowBytes / 8); w += blockDim.x) {
     const int64_t off = (w / (kRowBytes / 8)) * stride + 8 * (w % (kRowBytes / 8));
     *reinterpret_cast<uint2*>(d + off) = *reinterpret_cast<const uint2*>(s + off);
@@ -446,66 +513,50 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   cg::this_cluster().sync();   // every CTA has started: its shared memory may be written
   grid_dep_wait();
   grid_dep_launch();
-  int first, last, before;
-  slice(a.num_pages, &first, &last);
-  const int in_use = count_pages(a.ref, first, last, true, &sh);
-  const int used = cluster_share(in_use, 0, &before, &sh);
-  // Pages in use below this slice: `before`.  Holes are the free pages below `used`,
-  // movers the pages in use at or past it; their ranks follow from `before` alone:
-  // free pages below page p = p - (in use below p).
-  int below = before;
-  for (int at = first; at < last; at += kPlanThreads) {
-    const int p = at + static_cast<int>(threadIdx.x);
-    const bool u = p < last && __ldcg(a.ref + p) > 0;
-    int total;
-    const int r = below + block_rank(u ? 1 : 0, &total, &sh);   // pages in use below p
-    below += total;
-    if (p < last) {
-      if (p < used) {
-        if (!u) a.holes[p - r] = p;
-      } else {
-        // a mover's rank is r minus the pages in use below `used`, taken off below
-        a.rank_of[p] = u ? r : -1;
-      }
+  const Part pp = part_of(a.num_pages);
+  int mine = 0, total;
+  each_page(a.ref, pp, [&](int, int c) { mine += c > 0; });
+  const int rank = block_rank(mine, &total, &sh);
+  int2 low;
+  const int used = cluster_share(make_int2(total, 0), 0, &low, &sh).x;
+  // Holes are the free pages below `used`, movers the pages in use at or past it.  With r
+  // pages in use below page p, p - r free ones are: a hole's rank; a mover's is r less the
+  // pages in use below `used`, which the second share counts.
+  int r = low.x + rank, kept_here = 0;
+  each_page(a.ref, pp, [&](int p, int c) {
+    if (p < used) {
+      if (c <= 0) a.holes[p - r] = p;
+      else ++kept_here;
+    } else {
+      a.rank_of[p] = c > 0 ? r : -1;
     }
-  }
-  // pages in use below page `used` (the rank of the first mover)
-  int low = 0;
-  if (used > first && used <= last) {
-    int c = 0;
-    for (int p = first + threadIdx.x; p < used; p += kPlanThreads) c += __ldcg(a.ref + p) > 0;
-    int total;
-    block_rank(c, &total, &sh);
-    low = before + total;
-  }
-  int unused;
-  const int kept = used > 0 ? cluster_share(low, 1, &unused, &sh) : (cg::this_cluster().sync(), 0);
+    r += c > 0;
+  });
+  block_rank(kept_here, &total, &sh);
+  const int kept = cluster_share(make_int2(total, 0), 1, &low, &sh).x;
   const int moved = used - kept;
   // counts: each thread of a move reads and writes both of its pages' counts itself, so
   // ref_out may be ref
-  for (int at = first; at < last; at += kPlanThreads) {
-    const int p = at + static_cast<int>(threadIdx.x);
-    if (p >= last) continue;
-    const int c = a.ref[p];
+  each_page(a.ref, pp, [&](int p, int c) {
     if (p < used) {
       if (c > 0) a.ref_out[p] = c;
     } else if (c > 0) {
-      const int k = a.rank_of[p] - kept;
+      const int k = __ldcg(a.rank_of + p) - kept;
       a.movers[k] = p;
-      a.ref_out[a.holes[k]] = c;
+      a.ref_out[__ldcg(a.holes + k)] = c;
       a.ref_out[p] = 0;
     } else {
       a.ref_out[p] = c;
     }
-  }
+  });
   const int64_t step = static_cast<int64_t>(kPlanCtas) * kPlanThreads;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x; i < a.entries; i += step) {
     int v = a.table[i];
     if (v >= a.num_pages) {
       report(a.status, SMLA_ERR_INDEX_RANGE);
     } else if (v >= used) {
-      const int r = a.rank_of[v];
-      if (r >= 0) v = a.holes[r - kept];
+      const int r = __ldcg(a.rank_of + v);
+      if (r >= 0) v = __ldcg(a.holes + (r - kept));
       else report(a.status, SMLA_ERR_INDEX_RANGE);
     }
     a.table_out[i] = v;
@@ -517,7 +568,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 }
 
 // Moves the listed pages: a CTA takes chunks of kMoveRows rows in turn.
-constexpr int kMoveRows = 16;
+constexpr int kMoveRows = 28;      // 16,352 bytes: four 16-byte words a thread
 __global__ void __launch_bounds__(256) compact_move_kernel(const CompactArgs a) {
   grid_dep_wait();
   grid_dep_launch();
@@ -593,8 +644,12 @@ int smla_cache_append(const void* kv, int64_t kv_token_stride, int32_t total_tok
   const AppendArgs a = {static_cast<const uint4*>(kv), kv_token_stride / 8, total_tokens,
                         static_cast<uint8_t*>(kv_pages), block_table, cu_q, kv_lens, c->num_seqs,
                         c->max_pages, c->page_size, c->num_pages, c->kv_row_stride, status};
-  return done(launch_programmatic(append_kernel, dim3((total_tokens - 1) / 8 + 1), dim3(256), 0,
-                                  reinterpret_cast<cudaStream_t>(stream), a));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // few tokens: one a warp, the shortest way
+  if (total_tokens <= 152 * 64)
+    return done(launch_programmatic(append_kernel<1>, dim3((total_tokens - 1) / 8 + 1), dim3(256), 0, s, a));
+  return done(launch_programmatic(append_kernel<kAppendTokens>, dim3((total_tokens - 1) / (8 * kAppendTokens) + 1),
+                                  dim3(256), 0, s, a));
 }
 
 int smla_cache_workspace_size(const smla_cache_params* c, size_t* bytes) {
@@ -620,8 +675,7 @@ int smla_cache_reserve(int32_t* ref_count, int32_t* block_table, const int32_t* 
   return done(launch_programmatic(reserve_kernel, dim3(kPlanCtas), dim3(kPlanThreads), 0,
                                   reinterpret_cast<cudaStream_t>(stream), ref_count, block_table,
                                   target_lens, c->num_seqs, c->max_pages, c->page_size, c->num_pages,
-                                  reinterpret_cast<int32_t*>(ws),
-                                  reinterpret_cast<int32_t*>(ws + 3 * list_bytes(c)), status));
+                                  reinterpret_cast<int32_t*>(ws), status));
 }
 
 int smla_cache_fork(void* kv_pages, int32_t* ref_count, int32_t* block_table, int32_t* kv_lens,
