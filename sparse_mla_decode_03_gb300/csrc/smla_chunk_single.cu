@@ -21,7 +21,7 @@
 // 134 take a slower path.
 //
 // Warps of a CTA: 0..3 softmax and results (lanes 0..15: 64 rows lie in 16 tensor-memory
-// lanes of each quarter), 4..19 expand (two sets in turn), 20 issues the scores, 21 the value
+// lanes of each quarter), 4..19 expand, 20 issues the scores, 21 the value
 // products, 22 loads Q.  Every wait is bounded.
 #include <cstring>
 #include <mutex>
@@ -34,8 +34,8 @@ namespace smla {
 namespace {
 
 constexpr int kExpandWarp0 = 4;
-constexpr int kSetWarps = 8;               // a set of expanding warps; two sets take turns
-constexpr int kRows = 64 / kSetWarps;      // of a block, a warp
+constexpr int kExpandWarps = 16;
+constexpr int kRows = 64 / kExpandWarps;   // of a block, a warp
 constexpr int kMmaWarp = 20;
 constexpr int kPvWarp = 21;
 constexpr int kQWarp = 22;
@@ -52,8 +52,8 @@ constexpr int kQOff = 0;
 constexpr int kBufOff = 8 * kSlab;
 constexpr int kPOff = kBufOff + 2 * kBuf;
 constexpr int kBarOff = kPOff + kSlab;
-constexpr int kMaskOff = kBarOff + 256;    // mapped rows and rows that are not finite: [2 buffers][2][8 bytes]
-constexpr int kSmem = kMaskOff + 32 + 1024;
+constexpr int kMaskOff = kBarOff + 256;    // [2 buffers][mapped, not finite][16 half bytes]
+constexpr int kSmem = kMaskOff + 64 + 1024;
 constexpr uint32_t kColS = 448;
 
 // FULL / EMPTY: half of a block buffer (columns 0..255, the rest) filled / its value product
@@ -169,11 +169,12 @@ __device__ __forceinline__ uint2 ldg_if(bool p, const uint8_t* src, uint32_t non
   return v;
 }
 
-// The 8-byte words of 8 rows that a lane l holds.  Words 0..55 of a row are the nope part
-// (word w: columns 8 (w % 8) .. + 7 of group w / 8), 56 the scales, 57..72 the rope.
+// The 8-byte words of its warp's rows that a lane l holds.  Words 0..55 of a row are the nope
+// part (word w: columns 8 (w % 8) .. + 7 of group w / 8), 56 the scales, 57..72 the rope.
 // a[j], b[j]: words l and l + 32 of row j; c[k]: word 64 + l % 9 of row 3 k + l / 9.
+constexpr int kTails = (kRows + 2) / 3;
 struct RowWords {
-  uint2 a[8], b[8], c[3];
+  uint2 a[kRows], b[kRows], c[kTails];
 };
 
 // Two rows a thread: the 16 rows of a warp with their 64 scores of a block, as the
@@ -285,6 +286,15 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
+// The low halves of 16 bytes side by side.
+__device__ __forceinline__ unsigned long long halves(unsigned long long low, unsigned long long high) {
+  auto eight = [](unsigned long long x) {
+    x = (x | (x >> 4)) & 0x00ff00ff00ff00ffull;
+    x = (x | (x >> 8)) & 0x0000ffff0000ffffull;
+    return (x | (x >> 16)) & 0x00000000ffffffffull;
+  };
+  return eight(low) | (eight(high) << 32);
+}
 // After a wait has run out: products in flight end within microseconds, 1 ms before they lose
 // their memory.
 __device__ __forceinline__ void drain() {
@@ -308,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i)
-      mbar_init(bar(i), i < EMPTY ? kSetWarps : i == SEMPTY || i == PFULL || i == OEMPTY ? 4 : 1);
+      mbar_init(bar(i), i < EMPTY ? kExpandWarps : i == SEMPTY || i == PFULL || i == OEMPTY ? 4 : 1);
     *stop = 0;
     fence_mbar_init();
   }
@@ -330,14 +340,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kExpandWarp0 && warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsExpand) : "memory");
     // ---------------- expand ----------------
-    // Set B takes blocks B, B + 2, ..., which go to buffer B: while one set expands, the
-    // other's loads are in flight (they may hold no more bytes than the small L1 that the
-    // shared memory leaves, so a set that did both in turn left it empty half of the time).
-    // Rows 8 w .. + 7 of a block are warp w's; lane j's cursor follows row j % 8; the warp
-    // reads a row at once, 256 consecutive bytes a load.
-    const int w8 = (warp - kExpandWarp0) % kSetWarps;
-    const int B = (warp - kExpandWarp0) / kSetWarps;
-    const int mine = kRows * w8 + (lane & (kRows - 1));
+    // Rows 4 w .. + 3 of a block are warp w's; lane j's cursor follows row j % 4; the warp
+    // reads a row at once, 256 consecutive bytes a load.  All warps expand a block together,
+    // since that lies between a value product and the scores of the block after next; the
+    // next block's bytes are on their way meanwhile.
+    const int w16 = warp - kExpandWarp0;
+    const int mine = kRows * w16 + (lane & (kRows - 1));
     const int c_row = lane / 9, c_word = lane % 9;       // of words c
     if (x0 < x1) {
       const int pages_step = kChunkBlk / a.page_size, rest = kChunkBlk % a.page_size;
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           d.b[j] = ldg_if(o >= 0, src + 256, 0u);
         }
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
+        for (int k = 0; k < kTails; ++k) {
           const long long o = __shfl_sync(0xffffffffu, at_now, 3 * k + c_row);
           d.c[k] = ldg_if(o >= 0 && 3 * k + c_row < kRows && lane < 27, a.pool + o + 512 + 8 * c_word, 0u);
         }
@@ -378,11 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       at.load(plan, mine, a.page_size);
       RowWords d;
       const int count = x1 - x0;
-      auto step = [&]() { at.step(plan, mine, a.page_size, pages_step, rest); };
-      if (B == 1) step();
       uint32_t have = fetch(lookup(at), at.off, d);
-      step();
-      step();
+      at.step(plan, mine, a.page_size, pages_step, rest);
       int id = lookup(at), off = at.off;
       bool ok = true;
       // word b of this lane: nope, scales (lane 24) or rope; how its NaN are found
@@ -391,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tb = lane < 24 ? 0x80808080u : 0x80008000u;
       const int sh = 8 * (lane >> 3);
       const uint32_t dst_nope = sbase + kBufOff + (lane >> 3) * kSlab;
-      for (int n = B; n < count; n += 2) {
+      for (int n = 0; n < count; ++n) {
+        const int B = n & 1;
         // this lane's groups' scale bytes of row j (lanes 24 .. 31: no second group)
         auto scale_a = [&](int j) { return (__shfl_sync(0xffffffffu, d.b[j].x, 24) >> sh) & 0xffu; };
         auto scale_b = [&](int j) {
@@ -408,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           top = max(top, max(scale_a(j), scale_b(j)));
         }
 #pragma unroll
-        for (int k = 0; k < 3; ++k) nc |= rope_bits(d.c[k].x) | rope_bits(d.c[k].y);
+        for (int k = 0; k < kTails; ++k) nc |= rope_bits(d.c[k].x) | rope_bits(d.c[k].y);
         const bool odd = (na & 0x80808080u) | (nb & tb) | (nc & 0x80008000u) | (top > 134u ? 1u : 0u);
         const bool usual = !__any_sync(0xffffffffu, odd);
         uint32_t dropped = 0;        // rows that are not finite: held as zeros
@@ -433,8 +439,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t parity = ((n >> 1) - 1) & 1;
         if (n >= 2) ok = warp_wait(bar(EMPTY + 2 * B), parity, stop, a.status);
         if (!ok) break;
-        const uint32_t dn = dst_nope + kRows * w8 * 128 + B * kBuf;
-        auto unit = [&](int j) { return j * 128 + (((lane & 7) ^ j) << 4); };    // the lane's unit of row j
+        const uint32_t dn = dst_nope + kRows * w16 * 128 + B * kBuf;
+        const int r7 = (kRows * w16) & 7;                 // the warp's first row modulo 8
+        auto unit = [&](int j) { return j * 128 + (((lane & 7) ^ (r7 + j)) << 4); };    // the lane's unit of row j
         if (usual) {
           // two rows at a time, their conversions interleaved; times 2^(s - 7) as two bf16
 #pragma unroll
@@ -455,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (lane == 0) {
-          masks[B * 16 + w8] = static_cast<uint8_t>(have);
-          masks[B * 16 + 8 + w8] = static_cast<uint8_t>(dropped);
+          masks[B * 32 + w16] = static_cast<uint8_t>(have);
+          masks[B * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -464,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n >= 2) ok = warp_wait(bar(EMPTY + 2 * B + 1), parity, stop, a.status);
         if (!ok) break;
         // the rope: word w of row j
-        const uint32_t dr = sbase + kBufOff + 7 * kSlab + kRows * w8 * 128 + B * kBuf;
-        auto rope = [&](int j, int w) { return dr + j * 128 + (((w >> 1) ^ j) << 4) + 8 * (w & 1); };
+        const uint32_t dr = sbase + kBufOff + 7 * kSlab + kRows * w16 * 128 + B * kBuf;
+        auto rope = [&](int j, int w) { return dr + j * 128 + (((w >> 1) ^ (r7 + j)) << 4) + 8 * (w & 1); };
         if (usual) {
 #pragma unroll
           for (int j0 = 0; j0 < kRows; j0 += 2) {
@@ -490,17 +497,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
+        for (int k = 0; k < kTails; ++k) {
           const int j = 3 * k + c_row;
-          sts8_if(j < kRows && lane < 27, rope(j & 7, 7 + c_word), (dropped >> j) & 1 ? make_uint2(0u, 0u) : d.c[k]);
+          sts8_if(j < kRows && lane < 27, rope(j & (kRows - 1), 7 + c_word), (dropped >> j) & 1 ? make_uint2(0u, 0u) : d.c[k]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(FULL + 2 * B + 1));
-        // block n + 2's bytes, and the page ids of the one after it
+        // the next block's bytes, and the page ids of the one after it
         have = fetch(id, off, d);
-        step();
-        step();
+        at.step(plan, mine, a.page_size, pages_step, rest);
         id = lookup(at);
         off = at.off;
       }
@@ -619,8 +625,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(bar(FULL + 2 * (n & 1)), (n >> 1) & 1, stop, a.status);     // the masks' writers
         if (!ok) break;
         const volatile unsigned long long* mk =
-            reinterpret_cast<const volatile unsigned long long*>(smem + kMaskOff + (n & 1) * 16);
-        const ulonglong2 rows = make_ulonglong2(mk[0], mk[1]);
+            reinterpret_cast<const volatile unsigned long long*>(smem + kMaskOff + (n & 1) * 32);
+        const unsigned long long m0 = mk[0], m1 = mk[1], d0 = mk[2], d1 = mk[3];
+        ulonglong2 rows = make_ulonglong2(~0ull, 0ull);
+        if (__any_sync(0xffffffffu, (m0 & m1) != 0x0f0f0f0f0f0f0f0full || (d0 | d1) != 0))
+          rows = make_ulonglong2(halves(m0, m1), halves(d0, d1));
         ok = warp_wait(bar(SFULL), n & 1, stop, a.status);
         if (!ok) break;
         if (idle) {
