@@ -20,9 +20,9 @@
 // once: the integer pipe is the expansion's bound.  Rows with NaN or with scale bytes past
 // 134 take a slower path.
 //
-// Warps of a CTA: 0..3 softmax and results (lanes 0..15: 64 rows lie in 16 tensor-memory
-// lanes of each quarter), 4..19 expand, 20 issues the scores, 21 the value
-// products, 22 loads Q.  Every wait is bounded.
+// Warps of a CTA: 0..7 softmax and results (64 rows lie in 16 tensor-memory lanes of each
+// quarter, which two warps share by columns), 8..23 expand, 24 issues the scores, 25 the
+// value products, 26 loads Q.  Every wait is bounded.
 #include <cstring>
 #include <mutex>
 
@@ -33,17 +33,18 @@
 namespace smla {
 namespace {
 
-constexpr int kExpandWarp0 = 4;
+constexpr int kSoftWarps = 8;              // two for each quarter of tensor memory
+constexpr int kExpandWarp0 = 8;
 constexpr int kExpandWarps = 16;
 constexpr int kRows = 64 / kExpandWarps;   // of a block, a warp
-constexpr int kMmaWarp = 20;
-constexpr int kPvWarp = 21;
-constexpr int kQWarp = 22;
-constexpr int kThreads = 24 * 32;
+constexpr int kMmaWarp = 24;
+constexpr int kPvWarp = 25;
+constexpr int kQWarp = 26;
+constexpr int kThreads = 28 * 32;
 // Registers (setmaxnreg): what the launch gives is split among the warpgroups.
-constexpr int kLaunchRegs = 80;
-constexpr int kRegsSoft = 88, kRegsExpand = 88, kRegsMma = 40;
-static_assert(kRegsSoft * 128 + kRegsExpand * 512 + kRegsMma * 128 <= kLaunchRegs * kThreads, "register split");
+constexpr int kLaunchRegs = 72;
+constexpr int kRegsSoft = 80, kRegsExpand = 72, kRegsMma = 56;
+static_assert(kRegsSoft * 256 + kRegsExpand * 512 + kRegsMma * 128 <= kLaunchRegs * kThreads, "register split");
 static_assert(kRegsSoft >= kLaunchRegs && kRegsExpand >= kLaunchRegs && kRegsMma <= kLaunchRegs,
               "the direction that each role's setmaxnreg takes");
 constexpr int kSlab = 64 * 128;            // 64 columns of 64 rows
@@ -53,7 +54,8 @@ constexpr int kBufOff = 8 * kSlab;
 constexpr int kPOff = kBufOff + 2 * kBuf;
 constexpr int kBarOff = kPOff + kSlab;
 constexpr int kMaskOff = kBarOff + 256;    // [2 buffers][mapped, not finite][16 half bytes]
-constexpr int kSmem = kMaskOff + 64 + 1024;
+constexpr int kMaxOff = kMaskOff + 64;      // float [2 blocks][2 halves][64 rows]: largest scores; later sums
+constexpr int kSmem = kMaxOff + 1024 + 1024;
 constexpr uint32_t kColS = 448;
 
 // FULL / EMPTY: half of a block buffer (columns 0..255, the rest) filled / its value product
@@ -177,10 +179,10 @@ struct RowWords {
   uint2 a[kRows], b[kRows], c[kTails];
 };
 
-// Two rows a thread: the 16 rows of a warp with their 64 scores of a block, as the
-// 16-lane tensor-memory load deals them out: lane 4 g + q has columns 8 j + 2 q and + 1 of
-// rows g (v[4 j], v[4 j + 1]) and g + 8 (v[4 j + 2], v[4 j + 3]).  Sums stay per thread
-// until the end, the maximum is the row's.
+// Two rows a thread: the 16 rows of a quarter with 32 of their 64 scores of a block, as the
+// 16-lane tensor-memory load deals them out: lane 4 g + q has columns 8 j + 2 q and + 1 (of
+// the warp's half) of rows g (v[4 j], v[4 j + 1]) and g + 8 (v[4 j + 2], v[4 j + 3]).  Sums
+// stay per thread until the end; the maximum is the row's, of both halves.
 template <bool MODS>
 struct TwoRows {
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
@@ -200,16 +202,17 @@ struct TwoRows {
     }
   }
 
-  // The two rows side by side: the weights are on the way from scores to value product, and
-  // one row after the other is twice the latency.
-  __device__ __forceinline__ void weights(float (&v)[32], int s0, const ulonglong2& rows, uint32_t (&p)[16],
-                                          float (&alpha)[2]) {
-    const int col = 2 * (threadIdx.x & 3);
+  // The two rows side by side, and half of the columns a warp: the weights are on the way
+  // from scores to value product.  most: this block's [2 halves][64 rows] of shared memory.
+  __device__ __forceinline__ void weights(float (&v)[16], int s0, const ulonglong2& rows, volatile float* most,
+                                          uint32_t (&p)[8], float (&alpha)[2]) {
+    const int half = threadIdx.x >> 7, quarter = (threadIdx.x >> 5) & 3, g = (threadIdx.x >> 2) & 7;
+    const int col = 32 * half + 2 * (threadIdx.x & 3);
     const float scale2 = mods.scale2;
     if constexpr (MODS) {
       const float from0 = static_cast<float>(pos[0] - s0 - col), from1 = static_cast<float>(pos[1] - s0 - col);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           v[4 * j + e] = mods(v[4 * j + e], slope2[0], from0 - static_cast<float>(8 * j + e));
@@ -218,9 +221,9 @@ struct TwoRows {
     }
     const unsigned long long seen0 = seen_of(rows.x, s0, lo[0], hi[0]), seen1 = seen_of(rows.x, s0, lo[1], hi[1]);
     if (__any_sync(0xffffffffu, (seen0 & seen1) != ~0ull)) {
-      const unsigned long long at0 = seen0 >> col, at1 = seen1 >> col;
+      const uint32_t at0 = static_cast<uint32_t>(seen0 >> col), at1 = static_cast<uint32_t>(seen1 >> col);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           if (!((at0 >> (8 * j + e)) & 1)) v[4 * j + e] = -INFINITY;
@@ -229,7 +232,7 @@ struct TwoRows {
     }
     float t[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int j = 1; j < 8; ++j)
+    for (int j = 1; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) t[e] = fmaxf(t[e], v[4 * j + e]);
     float top[2] = {fmaxf(t[0], t[1]), fmaxf(t[2], t[3])}, shift[2];
@@ -239,6 +242,15 @@ struct TwoRows {
       top[0] = fmaxf(top[0], u0);
       top[1] = fmaxf(top[1], u1);
     }
+    // the other half's maximum (the quarter's two warps meet)
+    const int row = 16 * quarter + g;
+    if ((threadIdx.x & 3) == 0) {
+      most[64 * half + row] = top[0];
+      most[64 * half + row + 8] = top[1];
+    }
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+    top[0] = fmaxf(top[0], most[64 * (half ^ 1) + row]);
+    top[1] = fmaxf(top[1], most[64 * (half ^ 1) + row + 8]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if constexpr (!MODS) top[i] *= scale2;
@@ -249,7 +261,7 @@ struct TwoRows {
     }
     float sum[4] = {0.f, 0.f, 0.f, 0.f}, rsum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       float e[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -318,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i)
-      mbar_init(bar(i), i < EMPTY ? kExpandWarps : i == SEMPTY || i == PFULL || i == OEMPTY ? 4 : 1);
+      mbar_init(bar(i), i < EMPTY ? kExpandWarps : i == SEMPTY || i == PFULL || i == OEMPTY ? kSoftWarps : 1);
     *stop = 0;
     fence_mbar_init();
   }
@@ -604,13 +616,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kExpandWarp0) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft) : "memory");
     // ---------------- softmax and results ----------------
-    // Rows 16 warp .. + 15: two rows and a quarter of their scores a thread for the weights,
-    // lane = row for O.
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t tS = tmem + kColS + lanes, tO = tmem + lanes;
+    // Warps w and w + 4: rows 16 w .. + 15, columns 0..31 and 32..63 of a block; two rows and
+    // 8 of their scores a thread for the weights, lane = row for O, of which each warp has
+    // half of the columns.
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + kColS + 32 * half + lanes, tO = tmem + lanes;
     const int g = lane >> 2;
-    // P: rows 16 warp + g and + 8 (the same row modulo 8), columns 2 (lane % 4) .. of unit j
-    const uint32_t p0 = sbase + kPOff + (16 * warp + g) * 128 + 4 * (lane & 3), p1 = p0 + 8 * 128;
+    volatile float* most = reinterpret_cast<volatile float*>(smem + kMaxOff);
+    // P: rows 16 quarter + g and + 8 (the same row modulo 8), columns 2 (lane % 4) .. of unit j
+    const uint32_t p0 = sbase + kPOff + (16 * quarter + g) * 128 + 4 * (lane & 3), p1 = p0 + 8 * 128;
     uint32_t n = 0;
     bool ok = true;
     for (int x = x0, t = t_first; ok && x < x1; ++t) {
@@ -619,8 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nb = end - x, blk = tile.w + (end - 1 - begin);     // the first block
       // rows past the tile stay whatever they are (a product's rows do not mix), so a warp
       // without rows only keeps step
-      TwoRows<MODS> st(a, plan, tile, 16 * warp + g);
-      const bool idle = 16 * warp >= tile.z;
+      TwoRows<MODS> st(a, plan, tile, 16 * quarter + g);
+      const bool idle = 16 * quarter >= tile.z;
       for (int i = 0; ok && i < nb; ++i, ++n) {
         ok = warp_wait(bar(FULL + 2 * (n & 1)), (n >> 1) & 1, stop, a.status);     // the masks' writers
         if (!ok) break;
@@ -640,28 +655,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after();
-        float v[32];
-        tmem_ld_16x64(tS, v);
+        float v[16];
+        tmem_ld_16x32(tS, v);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(SEMPTY));
-        uint32_t p[16];
+        uint32_t p[8];
         float alpha[2];
-        st.weights(v, (blk - i) * kChunkBlk, rows, p, alpha);
+        st.weights(v, (blk - i) * kChunkBlk, rows, most + (n & 1) * 128, p, alpha);
         if (i > 0) {
           ok = warp_wait(bar(PV), (n - 1) & 1, stop, a.status);
           if (!ok) break;
           tc_fence_after();
           if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
             const float f = to_row(alpha);
-            rescale_rows(tO, lane < 16 ? f : 1.f);
+            rescale_rows(tO, lane < 16 ? f : 1.f, 224 * half, 224);
           }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          sts4(p0 + ((j ^ g) << 4), p[2 * j]);
-          sts4(p1 + ((j ^ g) << 4), p[2 * j + 1]);
+        for (int j = 0; j < 4; ++j) {
+          sts4(p0 + (((j + 4 * half) ^ g) << 4), p[2 * j]);
+          sts4(p1 + (((j + 4 * half) ^ g) << 4), p[2 * j + 1]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -673,15 +688,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (!idle) {
-        float inv[2], lse[2];
+        // the sums of both halves, through the maxima's places (their readers of the last
+        // blocks are done: each warp's arrivals for P came after its reads)
+        float l[2], lr[2], inv[2], lse[2];
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float l = quad_sum(st.l[i]), lr = quad_sum(st.lr[i]);
-          inv[i] = inverse_sum(l, lr);
-          lse[i] = lse_of(st.m[i], l);
+          l[i] = quad_sum(st.l[i]);
+          lr[i] = quad_sum(st.lr[i]);
+          if ((lane & 3) == 0) {
+            most[64 * half + 16 * quarter + g + 8 * i] = l[i];
+            most[128 + 64 * half + 16 * quarter + g + 8 * i] = lr[i];
+          }
         }
-        store_rows<kSingleRows, 16>(a, plan, to_row(inv), to_row(lse), tO, tile, 16 * warp, begin >= x0 && after <= x1,
-                                    2 * worker + (begin < x0 ? 0 : 1), sbase + kPOff + warp * 16 * 128);
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // in the same order in both warps
+          const float o = most[64 * (half ^ 1) + 16 * quarter + g + 8 * i], orr = most[128 + 64 * (half ^ 1) + 16 * quarter + g + 8 * i];
+          const float ls = half == 0 ? l[i] + o : o + l[i], lrs = half == 0 ? lr[i] + orr : orr + lr[i];
+          inv[i] = inverse_sum(ls, lrs);
+          lse[i] = lse_of(st.m[i], ls);
+        }
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");     // read before the next tile's maxima
+        store_rows<kSingleRows, 16, 64>(a, plan, to_row(inv), to_row(lse), tO, tile, 16 * quarter,
+                                        begin >= x0 && after <= x1, 2 * worker + (begin < x0 ? 0 : 1),
+                                        sbase + kPOff + quarter * 2048 + half * 1024, 224 * half, 224);
       }
       tc_fence_before();
       __syncwarp();
