@@ -284,3 +284,46 @@ def test_page_calls_replayed_from_a_graph_follow_the_state():
         model.fork(pr, ch)
         model.reserve([tg] * R)
         check_pages(model, r, t, l)
+
+
+def test_a_row_listed_twice_and_calls_on_a_side_stream():
+    page, num_pages = 8, 64
+    ref, table, lens = _state(num_pages, page, 5, 4, [30, 17, 8, 0, 0], 12)
+    s = torch.cuda.Stream()
+    r, t, l = dev(ref), dev(table), dev(lens)
+    pool = random_pool(num_pages, page, 12)
+    want = pool.cpu().numpy().copy()
+    model = PageModel(ref, table, lens, page)
+    s.wait_stream(torch.cuda.current_stream())
+    m.smla_cache_free(r, t, l, dev(np.array([2, 2, 2], np.int32)), stream=s)
+    model.free([2])
+    m.smla_cache_fork(pool, page, r, t, l, dev(np.array([0, 0], np.int32)), dev(np.array([3, 4], np.int32)), stream=s)
+    model.fork([0, 0], [3, 4])
+    m.smla_cache_reserve(page, r, t, dev(np.array([32, 17, 9, 32, 31], np.int32)), stream=s)
+    model.reserve([32, 17, 9, 32, 31])
+    m.smla_cache_compact(pool, page, r, t, stream=s)
+    model.compact()
+    s.synchronize()
+    check_pages(model, r, t, l)
+    for a, b, rows in model.copies:
+        want[b * page:b * page + rows] = want[a * page:a * page + rows]
+    assert np.array_equal(pool.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("stride,lead", [(ROW, 8), (600, 0), (1024, 16)])
+def test_compact_of_strided_and_odd_pools(stride, lead):
+    """Pages that start 8 bytes off a 16-byte boundary, and bytes between rows that stay."""
+    page, num_pages = 7, 60
+    pool = random_pool(num_pages, page, 14, stride, lead)
+    before = pool.cpu().numpy().copy()
+    rng = np.random.default_rng(14)
+    ref = (rng.random(num_pages) < 0.5).astype(np.int32)
+    table = np.flatnonzero(ref).astype(np.int32)[None, :].copy()
+    model = PageModel(ref, table, [0], page)
+    n, k = model.compact()
+    r, t = dev(ref), dev(table)
+    assert m.smla_cache_compact(pool, page, r, t).cpu().tolist() == [n, k]
+    check_pages(model, r, t, None)
+    for s, d, _ in model.copies:
+        before[d * page:(d + 1) * page, :ROW] = before[s * page:(s + 1) * page, :ROW]
+    assert np.array_equal(pool.cpu().numpy(), before)

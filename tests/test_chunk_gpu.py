@@ -344,3 +344,124 @@ def test_binding_refusals():
             m.smla_chunk_attention(q, pool, t, 16, c, l, **kw)
     with pytest.raises(m.SmlaError):
         m.smla_chunk_attention(q[:, :48].contiguous(), pool, t, 16, c, l)
+
+
+@pytest.mark.parametrize("n,H", [(1, 64), (3, 16), (70, 64), (150, 16)])
+def test_rows_that_are_not_finite_reach_only_who_sees_them(n, H):
+    """NaN and infinities in the cache: a token that sees such a row gets NaN, every other is
+    what it is without it (masked, causal later or in a page's unused tail)."""
+    L, page = 300, 48
+    q, pool, table, cu, lens = _case([L], [n], H, page, seed=91)
+    row = lambda p: int(table[0, p // page]) * page + p % page      # noqa: E731
+    pool[row(40), 7] = 0x7F                       # e4m3 NaN
+    pool[row(41), 450] = 0xFF                     # a NaN scale
+    pool[row(42), 449] = 250                      # a scale past bf16
+    pool[row(130), 500:502] = torch.tensor([0x80, 0x7F], dtype=torch.uint8)      # an infinite rope value
+    tail = int(table[0, -2]) * page + page - 1    # behind the last token of the last page
+    pool[tail] = 0xFF
+    begin = np.array([(0, 43, 131, 200)[j % 4] for j in range(n)], np.int32)
+    end = np.array([L - n + j + 1 if j % 3 else 35 for j in range(n)], np.int32)
+    out, lse = _run(q, pool, table, page, cu, lens, begin=begin, end=end)
+    clean = pool.clone()
+    for p in (40, 41, 42, 130):
+        clean[row(p)] = 0
+    ref = chunk_reference(q, clean, table, page, cu, lens, begin=begin, end=end)
+    sees = torch.tensor([any(b <= p < e for p in (40, 41, 42, 130)) for b, e in zip(begin, end)], device="cuda")
+    assert torch.isnan(out[sees].float()).all() and torch.isnan(lse[sees]).all()
+    ref[0][sees] = ref[1][sees] = float("nan")    # (not compared)
+    check_chunk((out, lse), ref)
+
+
+@pytest.mark.parametrize("n,H", [(2, 64), (100, 64)])
+def test_query_rows_that_are_not_finite_stay_alone(n, H):
+    q, pool, table, cu, lens = _case([200], [n], H, 64, seed=93)
+    ref = chunk_reference(q, pool, table, 64, cu, lens)
+    q[1, 5, 100] = float("nan")
+    q[0, 3, 500] = float("inf")
+    out, lse = _run(q, pool, table, 64, cu, lens)
+    for t, h in ((1, 5), (0, 3)):
+        assert torch.isnan(out[t, h].float()).all() and torch.isnan(lse[t, h])
+        out[t, h], lse[t, h] = ref[0][t, h].to(torch.bfloat16), ref[1][t, h].float()
+    check_chunk((out, lse), ref)
+
+
+@pytest.mark.parametrize("n", [1, 140])
+def test_tokens_past_the_bound_are_masked_and_reported(n):
+    """max_kv_tokens too small: the first sequences keep their tokens, later ones what is left,
+    counted in blocks of 64 with one to spare for every sequence."""
+    lens, page = [320, 640, 256], 64
+    q, pool, table, cu, l = _case(lens, [n] * 3, 64, page, seed=95)
+    got = _run(q, pool, table, page, cu, l, max_kv_tokens=448, status=-7)       # 7 + 3 blocks: 5, 5, 0
+    cut = table.copy()
+    cut[1, 5:] = -1
+    cut[2] = -1
+    check_chunk(got, chunk_reference(q, pool, cut, page, cu, l))
+
+
+@pytest.mark.parametrize("n,H", [(1, 16), (17, 16)])
+def test_more_sequences_than_the_plan_keeps_on_chip(n, H):
+    rng = np.random.default_rng(3)
+    lens = [int(v) for v in rng.integers(0, 70, 2100)]
+    ns = [min(L, int(v)) for L, v in zip(lens, rng.integers(0, n + 1, 2100))]
+    lens[5] = 300
+    q, pool, table, cu, l = _case(lens, ns, H, 16, seed=97)
+    out, lse = _run(q, pool, table, 16, cu, l)
+    pick = [0, 5, 1023, 1024, 1025, 2047, 2048, 2099] + [int(v) for v in rng.integers(0, 2100, 60)]
+    for b in pick:                                  # each against the definition by itself
+        if ns[b] == 0:
+            continue
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        ref = chunk_reference(q[rows], pool, table[b:b + 1], 16, [0, ns[b]], [lens[b]])
+        check_chunk((out[rows], lse[rows]), ref)
+
+
+@pytest.mark.parametrize("n", [1, 130])
+def test_a_pool_past_four_gigabytes(n):
+    """Row offsets past 32 bits: the pages in use are the last of the pool."""
+    page, H, L = 64, 64, 500
+    num_pages = (1 << 32) // (ROW * page) + 70
+    pool = torch.zeros(num_pages * page, ROW, dtype=torch.uint8, device="cuda")
+    small = random_pool(10, page, 99)
+    pool[-10 * page:] = small
+    table = (num_pages - 10 + np.random.default_rng(1).permutation(10)[None, :9]).astype(np.int32)
+    lens = np.array([L], np.int32)
+    cu = np.array([0, n], np.int32)
+    q = torch.randn(n, H, 512, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    kv = torch.randn(n, 512, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    m.smla_cache_append(kv.cuda(), pool, dev(table), page, dev(cu), dev(lens))
+    assert (pool[:-10 * page].view(-1)[::4097] == 0).all()
+    got = _run(q, pool, table, page, cu, lens)
+    low = table - (num_pages - 10)
+    check_chunk(got, chunk_reference(q, pool[-10 * page:], low, page, cu, lens))
+    at = torch.as_tensor(low[0].astype(np.int64)[np.arange(L - n, L) // page] * page + np.arange(L - n, L) % page)
+    assert np.array_equal(pool[-10 * page:].cpu().numpy()[at.numpy()], pack_rows(kv))
+
+
+def test_single_row_pools_and_single_positions():
+    """One page of one row, one token: the smallest cache there is."""
+    q, pool, table, cu, lens = _case([1], [1], 128, 1, seed=101)
+    one = pool[int(table[0, 0]):int(table[0, 0]) + 1]
+    _check(q, one, np.zeros((1, 1), np.int32), 1, cu, lens)
+
+
+def test_no_sequence_has_new_tokens():
+    q, pool, table, cu, lens = _case([50, 20], [0, 0], 64, 16, seed=103)
+    out = torch.full((1, 64, 448), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((1, 64), 3.0, device="cuda")
+    _run(q, pool, table, 16, cu, lens, out=out, lse=lse)
+    assert (out == 3).all() and (lse == 3).all()
+
+
+@pytest.mark.parametrize("ns", [[1, 1], [140, 60]])
+def test_calls_that_follow_one_another_share_a_workspace(ns):
+    """Calls of different shapes in one stream, one workspace, no waiting between them."""
+    a = _case([900, 400], ns, 64, 64, seed=105)
+    b = _case([300], [5], 16, 64, seed=106)
+    want = [_run(*_pick(a, 64)), _run(*_pick(b, 64))]
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    args = [(x[0], x[1], dev(x[2]), 64, dev(x[3]), dev(x[4])) for x in (a, b)]
+    for _ in range(4):
+        got = [m.smla_chunk_attention(*x, softmax_scale=SCALE, workspace=ws) for x in args]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
