@@ -361,9 +361,9 @@ typedef struct smla_chunk_params {
   int32_t page_size;      /* rows per page, >= 1                                        */
   int32_t max_pages;      /* columns of block_table, >= 1                               */
   int32_t reserved;       /* must be 0                                                  */
-  int64_t num_rows;       /* rows of the pool                                           */
-  int64_t kv_row_stride;  /* bytes between rows, >= 584, multiple of 8                  */
-  int64_t max_kv_tokens;  /* the caller's bound on the sum of kv_lens, >= 1; it sizes the
+  int64_t num_rows;       /* rows of the pool, 1 .. 2^31                                */
+  int64_t kv_row_stride;  /* bytes between rows, >= 584, multiple of 8, < 2^31          */
+  int64_t max_kv_tokens;  /* 1 .. 2^30: the caller's bound on the sum of kv_lens; it sizes the
                              workspace.  Tokens past it are masked and reported
                              (SMLA_ERR_INDEX_RANGE)                                     */
   float softmax_scale;    /* finite and > 0                                             */

@@ -450,7 +450,8 @@ int check_chunk(const smla_chunk_params* p) {
   if (!(std::isfinite(p->logit_cap) && p->logit_cap >= 0.f)) return SMLA_ERR_INVALID_ARG;
   if (p->num_heads != 16 && p->num_heads != 32 && p->num_heads != 64 && p->num_heads != 128)
     return SMLA_ERR_UNSUPPORTED_SHAPE;
-  if (p->batch > 65535 || p->max_kv_tokens > (int64_t{1} << 30) || static_cast<int64_t>(p->total_q) * p->num_heads >= (int64_t{1} << 30))
+  if (p->batch > 65535 || p->max_kv_tokens > (int64_t{1} << 30) || p->num_rows > (int64_t{1} << 31) ||
+      p->kv_row_stride >= (int64_t{1} << 31) || static_cast<int64_t>(p->total_q) * p->num_heads >= (int64_t{1} << 30))
     return SMLA_ERR_UNSUPPORTED_SHAPE;
   return SMLA_OK;
 }

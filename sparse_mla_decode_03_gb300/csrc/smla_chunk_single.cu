@@ -161,13 +161,10 @@ __device__ __forceinline__ void sts8_if(bool p, uint32_t addr, uint2 v) {
                "r"(v.y), "r"(p ? 1 : 0)
                : "memory");
 }
-// 8 bytes of the pool (read-only here, once), or `none`.
-__device__ __forceinline__ uint2 ldg_if(bool p, const uint8_t* src, uint32_t none) {
+// 8 bytes of the pool (read-only here, once).
+__device__ __forceinline__ uint2 ldg_once(const uint8_t* src) {
   uint2 v;
-  asm("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %3, 0;\n\tmov.b32 %0, %4;\n\tmov.b32 %1, %4;\n\t"
-      "@q ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n\t}\n"
-      : "=&r"(v.x), "=&r"(v.y)
-      : "l"(src), "r"(p ? 1 : 0), "r"(none));
+  asm("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(src));
   return v;
 }
 
@@ -361,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int c_row = lane / 9, c_word = lane % 9;       // of words c
     if (x0 < x1) {
       const int pages_step = kChunkBlk / a.page_size, rest = kChunkBlk % a.page_size;
+      const uint32_t stride = static_cast<uint32_t>(a.stride);
       // page id of the cursor's row, -1 = no row there
       auto lookup = [&](const Cursor& c) {
         if (c.x >= c.x1 || c.left <= 0) return -1;
@@ -368,26 +366,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
         return -1;
       };
-      // the rows' bytes; returns which of them are mapped
-      long long at_now = -1;         // byte offset of the lane's row of that block, -1: not there
+      // the rows' bytes; returns which of them are mapped.  In the place of a row that is not
+      // there the pool's first is read: its position is masked, and what it holds does not
+      // matter (a row that is not finite is held as zeros).  Rows of a pool that fits the
+      // GPU number far below 2^32.
+      uint32_t row_now = 0;
       auto fetch = [&](int id, int off, RowWords& d) {
         const long long r = static_cast<long long>(id) * a.page_size + off;
         const bool there = id >= 0 && r < a.num_rows;
         if (id >= 0 && !there) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
         const uint32_t have = __ballot_sync(0xffffffffu, there) & ((1u << kRows) - 1u);
-        // a row that is not there: zeros (and scale bytes of 0: zeros too)
-        at_now = there ? r * a.stride : -1;
+        row_now = there ? static_cast<uint32_t>(r) : 0u;
+        const uint8_t* base = a.pool + 8 * lane;
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
-          const long long o = __shfl_sync(0xffffffffu, at_now, j);
-          const uint8_t* src = a.pool + o + 8 * lane;
-          d.a[j] = ldg_if(o >= 0, src, 0u);
-          d.b[j] = ldg_if(o >= 0, src + 256, 0u);
+          const uint8_t* src = base + static_cast<uint64_t>(__shfl_sync(0xffffffffu, row_now, j)) * stride;
+          d.a[j] = ldg_once(src);
+          d.b[j] = ldg_once(src + 256);
         }
 #pragma unroll
         for (int k = 0; k < kTails; ++k) {
-          const long long o = __shfl_sync(0xffffffffu, at_now, 3 * k + c_row);
-          d.c[k] = ldg_if(o >= 0 && 3 * k + c_row < kRows && lane < 27, a.pool + o + 512 + 8 * c_word, 0u);
+          const int j = min(3 * k + c_row, kRows - 1);        // lanes with no such row: any
+          d.c[k] = ldg_once(a.pool + static_cast<uint64_t>(__shfl_sync(0xffffffffu, row_now, j)) * stride + 512 + 8 * c_word);
         }
         return have;
       };
@@ -407,15 +407,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ab = lane < 24 ? 0x01010101u : 0x00800080u;
       const uint32_t tb = lane < 24 ? 0x80808080u : 0x80008000u;
       const int sh = 8 * (lane >> 3);
+      const uint32_t pick = 0x4040u + 0x0101u * static_cast<uint32_t>(lane >> 3);   // (byte, 0, byte, 0)
+      const uint32_t pick_b = lane < 24 ? pick : 0x4444u;
       const uint32_t dst_nope = sbase + kBufOff + (lane >> 3) * kSlab;
       for (int n = 0; n < count; ++n) {
         const int B = n & 1;
-        // this lane's groups' scale bytes of row j (lanes 24 .. 31: no second group)
-        auto scale_a = [&](int j) { return (__shfl_sync(0xffffffffu, d.b[j].x, 24) >> sh) & 0xffu; };
-        auto scale_b = [&](int j) {
-          const uint32_t s = (__shfl_sync(0xffffffffu, d.b[j].y, 24) >> sh) & 0xffu;
-          return lane < 24 ? s : 0u;
-        };
+        // 2^(s - 7) as two bf16 of this lane's groups (s: their scale bytes) of each row; lanes
+        // 24 .. 31 have no second group
+        auto power = [](uint32_t twice) { return twice * 128u + 0x3c003c00u; };
+        uint32_t ma[kRows], mx[kRows];
         // anything that the fast path does not cover: NaN, infinite rope values, scale bytes
         // past 134
         uint32_t na = 0, nb = 0, nc = 0, top = 0;
@@ -423,18 +423,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < kRows; ++j) {
           na |= nan_bits(d.a[j].x) | nan_bits(d.a[j].y);
           nb |= ((d.b[j].x & mb) + ab) | ((d.b[j].y & mb) + ab);
-          top = max(top, max(scale_a(j), scale_b(j)));
+          const uint32_t sa = prmt(__shfl_sync(0xffffffffu, d.b[j].x, 24), 0, pick);
+          const uint32_t sb = prmt(__shfl_sync(0xffffffffu, d.b[j].y, 24), 0, pick_b);
+          top = max(top, max(sa, sb));
+          ma[j] = power(sa);
+          mx[j] = power(sb);
         }
 #pragma unroll
         for (int k = 0; k < kTails; ++k) nc |= rope_bits(d.c[k].x) | rope_bits(d.c[k].y);
-        const bool odd = (na & 0x80808080u) | (nb & tb) | (nc & 0x80008000u) | (top > 134u ? 1u : 0u);
+        const bool odd = (na & 0x80808080u) | (nb & tb) | (nc & 0x80008000u) | (top > 0x00860086u ? 1u : 0u);
         const bool usual = !__any_sync(0xffffffffu, odd);
         uint32_t dropped = 0;        // rows that are not finite: held as zeros
         // The unusual path reads its rows again, one by one: kept in registers for it, they
         // would make the usual path spill.
-        auto again = [&](int j, int byte) {      // 8 bytes of row j, zeros where it is not there
-          const long long o = __shfl_sync(0xffffffffu, at_now, j);
-          return ldg_if(o >= 0, a.pool + o + byte, 0u);
+        auto again = [&](int j, int byte) {      // 8 bytes of row j
+          return ldg_once(a.pool + static_cast<uint64_t>(__shfl_sync(0xffffffffu, row_now, j)) * stride + byte);
         };
         if (!usual) {
 #pragma unroll 1
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 o[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              o[j] = expand8(d.a[j0 + j], ((scale_a(j0 + j) + 120u) << 7) * 0x00010001u);
+              o[j] = expand8(d.a[j0 + j], ma[j0 + j]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) sts(dn + unit(j0 + j), o[j]);
           }
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 o[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              o[j] = expand8(d.b[j0 + j], ((scale_b(j0 + j) + 120u) << 7) * 0x00010001u);
+              o[j] = expand8(d.b[j0 + j], mx[j0 + j]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               sts_if(lane < 24, dn + 4 * kSlab + unit(j0 + j), o[j]);

@@ -90,6 +90,7 @@ def test_cache_pointers(lib):
     ({"total_q": 0}, INV), ({"total_q": 1 << 24}, SHAPE), ({"page_size": 0}, INV), ({"max_pages": 0}, INV),
     ({"reserved": 1}, INV), ({"num_rows": 0}, INV), ({"kv_row_stride": 576}, INV), ({"kv_row_stride": 590}, INV),
     ({"max_kv_tokens": 0}, INV), ({"softmax_scale": 0.0}, INV), ({"softmax_scale": float("nan")}, INV),
+    ({"num_rows": (1 << 31) + 1}, SHAPE), ({"kv_row_stride": 1 << 31}, SHAPE), ({"max_kv_tokens": (1 << 30) + 1}, SHAPE),
     ({"logit_cap": -1.0}, INV), ({"logit_cap": float("inf")}, INV),
 ])
 def test_chunk_params(lib, over, code):
