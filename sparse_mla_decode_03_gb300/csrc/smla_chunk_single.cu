@@ -51,18 +51,22 @@ constexpr int kSlab = 64 * 128;            // 64 columns of 64 rows
 constexpr int kBuf = 8 * kSlab;            // an expanded block
 constexpr int kQOff = 0;
 constexpr int kBufOff = 8 * kSlab;
-constexpr int kPOff = kBufOff + 2 * kBuf;
-constexpr int kBarOff = kPOff + kSlab;
+// P of a block takes the place of its rope, which the scores are done with; the buffer is
+// filled again only after the value product.  Without 8 KB for P the CTA stays below the
+// 196 KB step of the shared-memory carve-out, which leaves the loads 60 KB of L1, not 28.
+constexpr int kPOff = kBufOff + 7 * kSlab;     // + kBuf for the second buffer
+constexpr int kBarOff = kBufOff + 2 * kBuf;
 constexpr int kMaskOff = kBarOff + 256;    // [2 buffers][mapped, not finite][16 half bytes]
 constexpr int kMaxOff = kMaskOff + 64;      // float [2 blocks][2 halves][64 rows]: largest scores; later sums
 constexpr int kSmem = kMaxOff + 1024 + 1024;
+static_assert(kSmem <= 195 * 1024, "the carve-out step, less what the system takes");
 constexpr uint32_t kColS = 448;
 
 // FULL / EMPTY: half of a block buffer (columns 0..255, the rest) filled / its value product
 // done, two buffers; QFULL / QEMPTY: Q loaded / its last scores done; SFULL / SEMPTY: scores
-// in tensor memory / taken by the softmax; PFULL: weights written; PV: value product done;
-// OEMPTY: results taken.
-enum Bar : int { FULL = 0, EMPTY = 4, QFULL = 8, QEMPTY, SFULL, SEMPTY, PFULL, PV, OEMPTY, kBars };
+// in tensor memory / taken by the softmax; PFULL: weights written (one for each buffer: a
+// quarter may be a block ahead of another); OEMPTY: results taken.
+enum Bar : int { FULL = 0, EMPTY = 4, PFULL = 8, QFULL = 10, QEMPTY, SFULL, SEMPTY, OEMPTY, kBars };
 
 // A row of the blocks on the line, walked tile by tile and each tile's share from its last
 // block to its first (scores that a distance bias shapes then fall along the way, and the
@@ -284,6 +288,41 @@ struct TwoRows {
   }
 };
 
+// Half of the columns of rows row and row + 8 of the tile, as the 16-lane load deals them
+// out: final (`whole`), or partial into `slot`.  Four lanes write 32 consecutive bytes of a
+// partial row (16 of a final one).
+__device__ __forceinline__ void store_result(const ChunkArgs& a, const ChunkPlan& plan, const float (&inv)[2],
+                                             const float (&lse)[2], uint32_t tO, const int4& tile, int row,
+                                             bool whole, int slot, int half) {
+  const int q = threadIdx.x & 3;
+  const int64_t orow = static_cast<int64_t>(tile.y) + row, prow = static_cast<int64_t>(slot) * kSingleRows + row;
+#pragma unroll 1
+  for (int c = 224 * half; c < 224 * half + 224; c += 32) {
+    float o[16];
+    tmem_ld_16x32(tO + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (row + 8 * i >= tile.z) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = o[4 * j + 2 * i] * inv[i], y = o[4 * j + 2 * i + 1] * inv[i];
+        const int col = c + 8 * j + 2 * q;
+        if (whole) *reinterpret_cast<uint32_t*>(a.out + (orow + 8 * i) * kNope + col) = pack_bf16(x, y);
+        else *reinterpret_cast<float2*>(plan.o_part + (prow + 8 * i) * kNope + col) = make_float2(x, y);
+      }
+    }
+  }
+  if (half == 0 && q == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (row + 8 * i >= tile.z) continue;
+      if (whole) a.lse[orow + 8 * i] = lse[i];
+      else plan.lse_part[prow + 8 * i] = lse[i];
+    }
+  }
+}
+
 // x[0] of lane 4 g for row g < 8, x[1] for row g + 8, to lane = row.
 __device__ __forceinline__ float to_row(const float (&x)[2]) {
   const int src = (threadIdx.x & 7) * 4;
@@ -327,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i)
-      mbar_init(bar(i), i < EMPTY ? kExpandWarps : i == SEMPTY || i == PFULL || i == OEMPTY ? kSoftWarps : 1);
+      mbar_init(bar(i), i < EMPTY ? kExpandWarps : i == SEMPTY || i == PFULL || i == PFULL + 1 || i == OEMPTY ? kSoftWarps : 1);
     *stop = 0;
     fence_mbar_init();
   }
@@ -576,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int end = min(x1, plan.cum[t + 1]);
         uint32_t old = 0;                  // the tile's first product overwrites O
         for (; ok && x < end; ++x, ++n, old = 1) {
-          ok = warp_wait(bar(PFULL), n & 1, stop, a.status);
+          ok = warp_wait(bar(PFULL + (n & 1)), (n >> 1) & 1, stop, a.status);
           if (ok && old == 0 && k > 0) ok = warp_wait(bar(OEMPTY), (k - 1) & 1, stop, a.status);
           if (!ok) break;
           tc_fence_after();
@@ -585,14 +624,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // columns 0..255 first: the next block's may be written while 256..447 follow
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_f16_ss_hl(tmem, lp + ((i * 32) >> 4), hi, lb + ((i * 2048) >> 4), hi, kIdV0, i > 0 ? 1u : old);
+              mma_f16_ss_hl(tmem, lp + (n & 1) * (kBuf >> 4) + ((i * 32) >> 4), hi, lb + ((i * 2048) >> 4), hi, kIdV0, i > 0 ? 1u : old);
             mma_commit(bar(EMPTY + 2 * (n & 1)));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_f16_ss_hl(tmem + 256, lp + ((i * 32) >> 4), hi, lb + ((4 * kSlab + i * 2048) >> 4), hi, kIdV1,
+              mma_f16_ss_hl(tmem + 256, lp + (n & 1) * (kBuf >> 4) + ((i * 32) >> 4), hi, lb + ((4 * kSlab + i * 2048) >> 4), hi, kIdV1,
                             i > 0 ? 1u : old);
             mma_commit(bar(EMPTY + 2 * (n & 1) + 1));
-            mma_commit(bar(PV));
           }
           __syncwarp();
         }
@@ -651,10 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(bar(SFULL), n & 1, stop, a.status);
         if (!ok) break;
         if (idle) {
-          if (lane == 0) mbar_arrive(bar(SEMPTY));
-          if (i > 0) ok = warp_wait(bar(PV), (n - 1) & 1, stop, a.status);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive(bar(PFULL));
+          if (lane == 0) {
+            mbar_arrive(bar(SEMPTY));
+            mbar_arrive(bar(PFULL + (n & 1)));
+          }
           continue;
         }
         tc_fence_after();
@@ -667,27 +705,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t p[8];
         float alpha[2];
         st.weights(v, (blk - i) * kChunkBlk, rows, most + (n & 1) * 128, p, alpha);
-        if (i > 0) {
-          ok = warp_wait(bar(PV), (n - 1) & 1, stop, a.status);
+        // O may be rescaled once the value product before this one is done
+        if (i > 0 && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+          ok = warp_wait(bar(EMPTY + 2 * ((n - 1) & 1) + 1), ((n - 1) >> 1) & 1, stop, a.status);
           if (!ok) break;
           tc_fence_after();
-          if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-            const float f = to_row(alpha);
-            rescale_rows(tO, lane < 16 ? f : 1.f, 224 * half, 224);
-          }
+          const float f = to_row(alpha);
+          rescale_rows(tO, lane < 16 ? f : 1.f, 224 * half, 224);
         }
+        const uint32_t pb = (n & 1) * kBuf;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          sts4(p0 + (((j + 4 * half) ^ g) << 4), p[2 * j]);
-          sts4(p1 + (((j + 4 * half) ^ g) << 4), p[2 * j + 1]);
+          sts4(p0 + pb + (((j + 4 * half) ^ g) << 4), p[2 * j]);
+          sts4(p1 + pb + (((j + 4 * half) ^ g) << 4), p[2 * j + 1]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(PFULL));
+        if (lane == 0) mbar_arrive(bar(PFULL + (n & 1)));
       }
       if (!ok) break;
-      ok = warp_wait(bar(PV), (n - 1) & 1, stop, a.status);
+      ok = warp_wait(bar(EMPTY + 2 * ((n - 1) & 1) + 1), ((n - 1) >> 1) & 1, stop, a.status);
       if (!ok) break;
       tc_fence_after();
       if (!idle) {
@@ -714,9 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           lse[i] = lse_of(st.m[i], ls);
         }
         asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");     // read before the next tile's maxima
-        store_rows<kSingleRows, 16, 64>(a, plan, to_row(inv), to_row(lse), tO, tile, 16 * quarter,
-                                        begin >= x0 && after <= x1, 2 * worker + (begin < x0 ? 0 : 1),
-                                        sbase + kPOff + quarter * 2048 + half * 1024, 224 * half, 224);
+        store_result(a, plan, inv, lse, tO, tile, 16 * quarter + g, begin >= x0 && after <= x1,
+                     2 * worker + (begin < x0 ? 0 : 1), half);
       }
       tc_fence_before();
       __syncwarp();
