@@ -280,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = warp_wait(bar(PV), (np - 1) & 1, stop, a.status);
       if (!ok) break;
       tc_fence_after();
-      store_rows<kPairRows, 32, 128>(a, plan, inverse_sum(st.l, st.lr), lse_of(st.m, st.l), tO, tile,
+      store_rows<kPairRows>(a, plan, inverse_sum(st.l, st.lr), lse_of(st.m, st.l), tO, tile,
                                 static_cast<int>(rank) * 128 + 32 * warp, begin >= x0 && after <= x1,
                                 2 * worker + (begin < x0 ? 0 : 1), sbase + kPOff + warp * 32 * 128);
       tc_fence_before();

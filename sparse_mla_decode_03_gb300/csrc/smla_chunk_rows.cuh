@@ -169,34 +169,31 @@ __device__ __forceinline__ void rescale_rows(uint32_t tO, float alpha, int first
 __device__ __forceinline__ float inverse_sum(float l, float lr) { return l == 0.f ? 0.f : 1.f / lr; }
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
 
-// `count` columns of the results of a warp's rows row0 .. + ROWS - 1 of the tile (lane =
-// row): final (`whole`), or partial into `slot`.  inv: 1 / sum of the lane's row.  They pass
-// through ROWS * WIDTH bytes of shared memory, so that consecutive lanes write WIDTH
-// consecutive bytes of a row: written by the lane that holds it, 16 bytes of 32 rows at a
-// time, a tile took 14 us.
-template <int TILE_ROWS, int ROWS, int WIDTH>
+// The results of a warp's rows row0 .. + 31 of the tile (lane = row): final (`whole`), or
+// partial into `slot`.  inv: 1 / sum of the lane's row.  They pass through 4 KB of shared
+// memory (`stage`), so that consecutive lanes write 128 consecutive bytes of a row: written
+// by the lane that holds it, 16 bytes of 32 rows at a time, a tile took 14 us.
+template <int TILE_ROWS>
 __device__ __forceinline__ void store_rows(const ChunkArgs& a, const ChunkPlan& plan, float inv, float lse,
                                            uint32_t tO, const int4& tile, int row0, bool whole, int slot,
-                                           uint32_t stage, int first = 0, int count = kNope) {
-  constexpr int kUnits = WIDTH / 16;               // 16-byte units of a staged row
+                                           uint32_t stage) {
   const int lane = threadIdx.x & 31;
   const int64_t orow = static_cast<int64_t>(tile.y) + row0;
   const int64_t prow = static_cast<int64_t>(slot) * TILE_ROWS + row0;
-  const int live = min(ROWS, tile.z - row0);       // rows of the warp that the tile has
-  // unit u of row r, so that 8 rows' same units and a row's units lie in different banks
-  auto place = [&](int r, int u) { return stage + r * WIDTH + ((u ^ ((r * kUnits / 8) & (kUnits - 1))) << 4); };
+  const int live = min(32, tile.z - row0);         // rows of the warp that the tile has
+  // 16-byte unit u of row r, so that 8 rows' same units and a row's units lie in different banks
+  auto place = [&](int r, int u) { return stage + r * 128 + ((u ^ (r & 7)) << 4); };
   auto put = [&](int u, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    if (lane < ROWS)
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(place(lane, u)), "r"(x), "r"(y), "r"(z), "r"(w)
-                   : "memory");
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(place(lane, u)), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
   };
   // the staged bytes of each row to base + row * pitch
   auto flush = [&](char* base, int64_t pitch) {
     __syncwarp();
-    const int unit = lane % kUnits;
+    const int unit = lane & 7;
 #pragma unroll
-    for (int i = 0; i < ROWS * kUnits / 32; ++i) {
-      const int r = i * (32 / kUnits) + lane / kUnits;
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + lane / 8;
       uint4 v;
       asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                    : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
@@ -207,35 +204,29 @@ __device__ __forceinline__ void store_rows(const ChunkArgs& a, const ChunkPlan& 
     __syncwarp();
   };
 #pragma unroll 1
-  for (int c = first; c < first + count; c += 32) {
+  for (int c = 0; c < kNope; c += 32) {
     float o[32];
     tmem_ld32(tO + c, o);
     tmem_wait_ld();
 #pragma unroll
     for (int k = 0; k < 32; ++k) o[k] *= inv;
     if (whole) {
-      // 64 bytes a row: one or half of a staged row
-      const int u0 = WIDTH == 128 ? (c / 32 % 2) * 4 : 0;
+      // 64 bytes a row: half of a staged row
+      const int u0 = (c / 32 % 2) * 4;
 #pragma unroll
       for (int k = 0; k < 32; k += 8)
         put(u0 + k / 8, pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]), pack_bf16(o[k + 4], o[k + 5]),
             pack_bf16(o[k + 6], o[k + 7]));
-      if (WIDTH == 64) flush(reinterpret_cast<char*>(a.out + orow * kNope + c), kNope * 2);
-      else if (u0 == 4) flush(reinterpret_cast<char*>(a.out + orow * kNope + c - 32), kNope * 2);
+      if (u0 == 4) flush(reinterpret_cast<char*>(a.out + orow * kNope + c - 32), kNope * 2);
     } else {
       // 128 bytes a row
 #pragma unroll
-      for (int h = 0; h < 128 / WIDTH; ++h) {
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-          const int k = (h * kUnits + u) * 4;
-          put(u, __float_as_uint(o[k]), __float_as_uint(o[k + 1]), __float_as_uint(o[k + 2]), __float_as_uint(o[k + 3]));
-        }
-        flush(reinterpret_cast<char*>(plan.o_part + prow * kNope + c + h * (WIDTH / 4)), kNope * 4);
-      }
+      for (int k = 0; k < 32; k += 4)
+        put(k / 4, __float_as_uint(o[k]), __float_as_uint(o[k + 1]), __float_as_uint(o[k + 2]), __float_as_uint(o[k + 3]));
+      flush(reinterpret_cast<char*>(plan.o_part + prow * kNope + c), kNope * 4);
     }
   }
-  if (lane < live && first == 0) {
+  if (lane < live) {
     if (whole) a.lse[orow + lane] = lse;
     else plan.lse_part[prow + lane] = lse;
   }
