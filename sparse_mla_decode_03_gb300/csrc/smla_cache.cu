@@ -348,6 +348,14 @@ __device__ __forceinline__ int fork_length(const ForkArgs& a, int i) {
   return len < 0 || len > static_cast<int64_t>(a.max_pages) * a.page_size ? -1 : len;
 }
 
+// Whether the child of a parent of `len` tokens gets a page of its own: the last one is partly
+// filled, and mapped (an entry that names no page of the pool is copied as it is).
+__device__ __forceinline__ bool fork_takes(const ForkArgs& a, int i, int len) {
+  if (len <= 0 || len % a.page_size == 0) return false;
+  const int page = a.table[static_cast<int64_t>(__ldg(a.parents + i)) * a.max_pages + len / a.page_size];
+  return page >= 0 && page < a.num_pages;
+}
+
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
     fork_plan_kernel(const ForkArgs a) {
   __shared__ PlanShared sh;
@@ -358,8 +366,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   int free_total, need_total, mine = 0;
   const int free_rank = block_rank(count_free(a.ref, pp), &free_total, &sh);
   for (int i = ip.run0; i < ip.run1; ++i) {
-    const int len = fork_length(a, i);
-    mine += len > 0 && len % a.page_size != 0;
+    mine += fork_takes(a, i, fork_length(a, i));
   }
   const int need_rank = block_rank(mine, &need_total, &sh);
   int2 low;
@@ -371,7 +378,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   for (int i = ip.run0; i < ip.run1; ++i) {
     const int len = fork_length(a, i);
     int f = len < 0 ? kSkip : kNotNeeded;
-    if (len > 0 && len % a.page_size != 0) {
+    if (fork_takes(a, i, len)) {
       f = k < got ? __ldcg(a.list + k) : kNoPage;
       ++k;
     }
@@ -438,15 +445,16 @@ __global__ void __launch_bounds__(256) fork_apply_kernel(const ForkArgs a) {
       int v = -1;
       if (e < full) {
         v = src[e];
-        if (v >= 0 && v < a.num_pages) atomicAdd(a.ref + v, 1);
       } else if (e == full && rem > 0) {
-        v = fresh;
+        v = fresh >= 0 ? fresh : src[e];
       }
+      if (v >= a.num_pages) report(a.status, SMLA_ERR_INDEX_RANGE);
+      else if (v >= 0 && e < full) atomicAdd(a.ref + v, 1);
       dst[e] = v;
     }
     if (threadIdx.x == 0) a.kv_lens[c] = len;
   }
-  if (rem == 0) return;
+  if (fresh < 0 || rem == 0) return;
   const int from = src[full];
   if (from < 0 || from >= a.num_pages) return;
   for (int r0 = blockIdx.y * kForkRows; r0 < rem; r0 += gridDim.y * kForkRows) {

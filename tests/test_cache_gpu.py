@@ -327,3 +327,21 @@ def test_compact_of_strided_and_odd_pools(stride, lead):
     for s, d, _ in model.copies:
         before[d * page:(d + 1) * page, :ROW] = before[s * page:(s + 1) * page, :ROW]
     assert np.array_equal(pool.cpu().numpy(), before)
+
+
+def test_fork_of_a_parent_whose_last_page_is_not_mapped():
+    page = 8
+    pool = random_pool(6, page, 40)
+    before = pool.clone()
+    # parents: an unmapped last page (and a hole), a page past the pool, an ordinary one
+    table = dev(np.array([[2, -1, -1], [4, 99, -1], [3, 5, -1], [-1] * 3, [-1] * 3, [-1] * 3], dtype=np.int32))
+    lens = dev(np.array([19, 11, 12, 0, 0, 0], dtype=np.int32))
+    ref = dev(np.array([0, 0, 1, 1, 1, 1], dtype=np.int32))
+    m.smla_cache_fork(pool, page, ref, table, lens, dev(np.array([0, 1, 2], dtype=np.int32)),
+                      dev(np.array([3, 4, 5], dtype=np.int32)))
+    assert m.smla_device_status(clear=True) == -7     # page 99
+    assert table.cpu().tolist()[3:] == [[2, -1, -1], [4, 99, -1], [3, 0, -1]]
+    assert lens.cpu().tolist()[3:] == [19, 11, 12]
+    assert ref.cpu().tolist() == [1, 0, 2, 2, 2, 1]               # one page taken, for the ordinary one
+    assert torch.equal(pool[:4, :ROW], before[5 * page:5 * page + 4, :ROW])
+    assert torch.equal(pool[4:], before[4:])
