@@ -303,7 +303,8 @@ int smla_cache_reserve(int32_t* ref_count, int32_t* block_table, const int32_t* 
  * Makes row children[i] a copy of row parents[i], i < n: full pages are shared (count
  * + 1), a last page that is partly filled (kv_lens % page_size rows) is copied into the
  * next free page (in list order), entries behind it are unmapped, and the length is the
- * parent's.  The child's row is overwritten, not freed: free it first.  Children are
+ * parent's.  Entries that name no page of the pool are copied as they are (those past it:
+ * SMLA_ERR_INDEX_RANGE).  The child's row is overwritten, not freed: free it first.  Children are
  * distinct and none is a parent in the same call.  A pair with an id outside
  * [0, num_seqs), with child == parent, or whose parent's length does not fit the table
  * is skipped (SMLA_ERR_INDEX_RANGE); a child that finds no free page is left empty
@@ -330,7 +331,8 @@ int smla_cache_free(int32_t* ref_count, int32_t* block_table, int32_t* kv_lens,
  * counts and table follow.  ref_count_out and block_table_out may be their inputs (in
  * place) or other buffers; info int32 [2] receives u and the number of moved pages.
  * Moved pages' old rows keep their bytes.  Table entries past the pool, or that name
- * a free page, are copied as they are (SMLA_ERR_INDEX_RANGE).
+ * a free page, are copied as they are (SMLA_ERR_INDEX_RANGE).  Each output is its input's
+ * own buffer or one that overlaps none of the others.
  */
 int smla_cache_compact(void* kv_pages, const int32_t* ref_count, const int32_t* block_table,
                        int32_t* ref_count_out, int32_t* block_table_out, int32_t* info,
@@ -353,6 +355,24 @@ int smla_cache_compact(void* kv_pages, const int32_t* ref_count, const int32_t* 
  * masked; positions past the table and page ids past the pool are masked and reported
  * (SMLA_ERR_INDEX_RANGE).  out and lse of entries outside [cu_q[0], cu_q[batch]) are left
  * as they were.
+ *
+ * A cached row with a NaN, an infinite rope value or a scale byte above 246 (values past
+ * bf16) counts as not finite: tokens that see it get NaN in out and lse, all others are not
+ * touched by it.  The attention weights are rounded to bf16 for the value product (and the
+ * result divided by the sum of the rounded ones); everything else is held in 32 bits.  The
+ * same call gives the same bits every time.
+ *
+ * cu_q is nondecreasing; one that lists more query rows than q has, and a call with more than
+ * 2^30 blocks to go through (64 positions times 64 or 256 query rows each: hours of work),
+ * writes nothing and is reported (SMLA_ERR_INDEX_RANGE, SMLA_ERR_UNSUPPORTED_SHAPE).
+ *
+ * Two kernels.  From 256 query rows (tokens times heads) a sequence on average, pairs of SMs
+ * work on 256 rows each over a bf16 copy of the cached rows, which the call makes in the
+ * workspace (1,040 bytes a token of max_kv_tokens); below, single SMs work on 64 rows each and
+ * expand the rows themselves.  Either way the work is cut evenly over the GPU and partial
+ * results are joined.  Calls whose kernels may overlap (two streams, two graphs) need a
+ * workspace each; calls that follow one another in a stream may share one.  As with the
+ * decode calls, one eager call on the device comes before a capture.
  */
 typedef struct smla_chunk_params {
   int32_t batch;          /* sequences, 1 .. 65535                                      */

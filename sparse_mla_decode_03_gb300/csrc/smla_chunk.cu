@@ -119,6 +119,11 @@ __device__ void make_plan(const ChunkArgs& a, const ChunkPlan& p, int tile_rows,
     if (few) sh.tile[a.B] = static_cast<int>(tiles);
   }
   __syncthreads();
+  // a cu_q that decreases somewhere may list more tiles than the workspace has room for
+  if (tiles > (static_cast<long long>(a.T) * a.H + tile_rows - 1) / tile_rows + a.B) {
+    tiles = 0;
+    if (threadIdx.x == 0) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
+  }
   const bool short_line = tiles <= kPlanTiles;
   long long line = 0;
   for (int t0 = 0; t0 < static_cast<int>(tiles); t0 += kPlanThreads) {

@@ -237,7 +237,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + kColS + lanes, tO = tmem + lanes;
     const uint32_t sempty = dsmem_addr(bar(SEMPTY), 0), pfull = dsmem_addr(bar(PFULL), 0),
                    oempty = dsmem_addr(bar(OEMPTY), 0);
-    const uint32_t prow = sbase + kPOff + r * 128;
     uint32_t ns = 0, np = 0;
     bool ok = true;
     for (int x = x0, t = t_first; ok && x < x1; ++t) {

@@ -149,6 +149,7 @@ __device__ __forceinline__ void store_weights(uint32_t p_base, int r, const uint
 }
 
 // `count` columns of the warp's rows of O times alpha, unless it is 1 for all of them.
+// O is rescaled only where a row's maximum rises by more than kHeadroom, so seldom.
 __device__ __forceinline__ void rescale_rows(uint32_t tO, float alpha, int first = 0, int count = kNope) {
   if (!__any_sync(0xffffffffu, alpha != 1.f)) return;
 #pragma unroll 1

@@ -145,9 +145,6 @@ __device__ __noinline__ uint4 expand8_any(uint2 w, uint32_t s) {
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-__device__ __forceinline__ bool not_finite(uint32_t v) {
-  return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
-}
 __device__ __forceinline__ void sts(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }

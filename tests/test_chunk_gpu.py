@@ -465,3 +465,19 @@ def test_calls_that_follow_one_another_share_a_workspace(ns):
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+@pytest.mark.parametrize("T", [6, 150])
+def test_offsets_that_decrease_are_refused_on_the_device(T):
+    """Sequences that list the same entries over and over bring more tiles than a workspace holds."""
+    H, page, B = 64, 16, 33
+    pool = random_pool(8, page, 61)
+    table = dev(np.tile(np.arange(8, dtype=np.int32), (B, 1)))
+    cu = np.zeros(B + 1, dtype=np.int32)
+    cu[1::2] = T
+    q = torch.randn((T, H, 512), device="cuda").to(torch.bfloat16)
+    out = torch.full((T, H, 448), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, H), 7.0, dtype=torch.float32, device="cuda")
+    m.smla_chunk_attention(q, pool, table, page, dev(cu), dev(np.full(B, 128, dtype=np.int32)), out=out, lse=lse)
+    assert m.smla_device_status(clear=True) == -7
+    assert bool((out == 7).all()) and bool((lse == 7).all())
