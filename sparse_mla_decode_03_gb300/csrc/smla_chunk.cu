@@ -376,10 +376,23 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 // ROW_WARPS-th partial result: a long context over one tile of few rows has as many partial
 // results as there are workers, and one warp reading them in turn would be all latency.
 // ---------------------------------------------------------------------------
+struct Part {             // a lane's share of a partial result: float4 lane + 28 k of 112
+  float4 v[4];
+};
+__device__ __forceinline__ void add_scaled(Part& x, float w, const Part& y) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x.v[k].x = fmaf(w, y.v[k].x, x.v[k].x);
+    x.v[k].y = fmaf(w, y.v[k].y, x.v[k].y);
+    x.v[k].z = fmaf(w, y.v[k].z, x.v[k].z);
+    x.v[k].w = fmaf(w, y.v[k].w, x.v[k].w);
+  }
+}
 template <int ROW_WARPS>
 __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows) {
   constexpr int kRows = 8 / ROW_WARPS;          // rows of a CTA
-  __shared__ float2 part[8][kNope / 2 + 2];     // each warp's sum over its partial results
+  constexpr int kLanes = 28;                    // of 16 bytes: 4 x 28 are a row
+  __shared__ float4 part[ROW_WARPS > 1 ? 8 : 1][4][kLanes];     // each warp's sum over its partial results
   __shared__ float weight[8];
   grid_dep_wait();
   grid_dep_launch();
@@ -393,53 +406,62 @@ __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const Chu
   // slot of worker c: its share begins inside the tile (0), or the tile inside its share (1)
   auto at = [&](int c) { return static_cast<int64_t>(2 * c + (c == first ? 1 : 0)) * tile_rows + row; };
   const bool live = row < cut.y;
-  float top = -INFINITY;
+  auto load = [&](int c, Part& x) {
+    const float4* o = reinterpret_cast<const float4*>(p.o_part + at(c) * kNope) + lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      x.v[k] = live && lane < kLanes && c <= last ? __ldcg(o + kLanes * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  // two partial results are on their way while the weights are worked out
+  const int c0 = first + warp % ROW_WARPS;
+  Part x0, x1, acc = {};
+  load(c0, x0);
+  load(c0 + ROW_WARPS, x1);
+  const float mine = live && first + lane <= last ? p.lse_part[at(first + lane)] : -INFINITY;
+  float top = mine;
   if (live)
-    for (int c = first + lane; c <= last; c += 32) top = fmaxf(top, p.lse_part[at(c)]);
+    for (int c = first + 32 + lane; c <= last; c += 32) top = fmaxf(top, p.lse_part[at(c)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float shift = top == -INFINITY ? 0.f : top;
   float sum = 0.f;
-  float2 acc[7];
-#pragma unroll
-  for (int k = 0; k < 7; ++k) acc[k] = make_float2(0.f, 0.f);
-  if (live) {
-#pragma unroll 2
-    for (int c = first + warp % ROW_WARPS; c <= last; c += ROW_WARPS) {
-      const float w = expf(p.lse_part[at(c)] - shift);
-      sum += w;
-      const float2* o = reinterpret_cast<const float2*>(p.o_part + at(c) * kNope) + lane;
-#pragma unroll
-      for (int k = 0; k < 7; ++k) {
-        const float2 v = o[32 * k];
-        acc[k].x = fmaf(w, v.x, acc[k].x);
-        acc[k].y = fmaf(w, v.y, acc[k].y);
-      }
-    }
+  for (int c = c0; c <= last; c += 2 * ROW_WARPS) {
+    const int c1 = c + ROW_WARPS;
+    const float z0 = __shfl_sync(0xffffffffu, mine, (c - first) & 31), z1 = __shfl_sync(0xffffffffu, mine, (c1 - first) & 31);
+    const float w0 = live ? expf((c - first < 32 ? z0 : p.lse_part[at(c)]) - shift) : 0.f;
+    const float w1 = live && c1 <= last ? expf((c1 - first < 32 ? z1 : p.lse_part[at(c1)]) - shift) : 0.f;
+    add_scaled(acc, w0, x0);
+    add_scaled(acc, w1, x1);
+    sum += w0;
+    sum += w1;
+    load(c + 2 * ROW_WARPS, x0);
+    load(c1 + 2 * ROW_WARPS, x1);
   }
   if constexpr (ROW_WARPS > 1) {
 #pragma unroll
-    for (int k = 0; k < 7; ++k) part[warp][lane + 32 * k] = acc[k];
+    for (int k = 0; k < 4; ++k)
+      if (lane < kLanes) part[warp][k][lane] = acc.v[k];
     if (lane == 0) weight[warp] = sum;
     __syncthreads();
     if (warp % ROW_WARPS != 0) return;
 #pragma unroll
     for (int w = 1; w < ROW_WARPS; ++w) {       // in a fixed order: the same bits every time
       sum += weight[warp + w];
+      Part x;
 #pragma unroll
-      for (int k = 0; k < 7; ++k) {
-        const float2 v = part[warp + w][lane + 32 * k];
-        acc[k].x += v.x;
-        acc[k].y += v.y;
-      }
+      for (int k = 0; k < 4; ++k) x.v[k] = part[warp + w][k][min(lane, kLanes - 1)];
+      add_scaled(acc, 1.f, x);
     }
   }
   if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t orow = static_cast<int64_t>(cut.x) + row;
-  __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + orow * kNope) + lane;
+  uint2* out = reinterpret_cast<uint2*>(a.out + orow * kNope) + lane;
+  if (lane < kLanes) {
 #pragma unroll
-  for (int k = 0; k < 7; ++k) out[32 * k] = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
+    for (int k = 0; k < 4; ++k)
+      out[kLanes * k] = make_uint2(pack_bf16(acc.v[k].x * inv, acc.v[k].y * inv), pack_bf16(acc.v[k].z * inv, acc.v[k].w * inv));
+  }
   if (lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : shift + logf(sum);
 }
 
@@ -505,7 +527,7 @@ cudaError_t launch_merge(const ChunkArgs& a, const ChunkPlan& p, int rows, int w
   const unsigned cuts = static_cast<unsigned>(tiles < workers - 1 ? tiles : workers - 1);
   if (tiles * 4 <= workers)
     return launch_programmatic(merge_kernel<8>, dim3(rows, cuts), dim3(256), 0, s, a, p, rows);
-  return launch_programmatic(merge_kernel<2>, dim3(rows / 4, cuts), dim3(256), 0, s, a, p, rows);
+  return launch_programmatic(merge_kernel<1>, dim3(rows / 8, cuts), dim3(256), 0, s, a, p, rows);
 }
 
 cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_t s) {

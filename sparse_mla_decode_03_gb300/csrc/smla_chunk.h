@@ -50,6 +50,12 @@ struct ChunkPlan {
   int64_t cap_blocks;    // blocks of the expanded copy, not counting one of zeros behind
 };
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 __device__ __forceinline__ int find_last_le(const int32_t* a, int n, int x) {   // a[0] <= x
   int lo = 0;
   for (int hi = n; hi - lo > 1;) {
