@@ -20,7 +20,9 @@ __device__ __forceinline__ float ue8m0_value(uint32_t e) {
 }
 
 // ---------------------------------------------------------------------------
-// Plan
+// Plan: one CTA, 6 us cold (a launch, three dependent loads, block-wide sums), within the
+// expansion's launch where there is one.  Equal shares of the block line, whatever the lengths
+// and masks: no SM waits for the longest sequence.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 
@@ -222,8 +224,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 
 // ---------------------------------------------------------------------------
 // Expanded copy: the rows of each sequence in the order of its positions, bf16.  The e4m3
-// values times their powers of two are exact in bf16.  A warp writes 8 of a block's rows;
-// lane l < 28 holds columns 16 l .. 16 l + 15, lanes 28..31 the rope.
+// values times their powers of two are exact in bf16.  A CTA takes a block of 64 rows, a warp
+// two of them; lane l < 28 holds columns 16 l .. 16 l + 15, lanes 28..31 the rope.  Bound by
+// the launch and one trip to memory: 7.5 us for 8,192 rows (1.6 KB each), 11 us for 21,007.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t expand_pair(uint32_t two, float scale) {
   uint32_t h2;
@@ -375,6 +378,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 // tiles).  A row is joined by ROW_WARPS warps, each taking every
 // ROW_WARPS-th partial result: a long context over one tile of few rows has as many partial
 // results as there are workers, and one warp reading them in turn would be all latency.
+// Bound by latency and L2 (the parts were written just before): 16 us for the 75 tiles of 256
+// rows that 76 pairs cut (69 MB), 8 us behind single tokens.  Rows of few tiles: 8 warps each
+// (15 us with 2 for two tiles of 76 parts, 8 with 8); else one warp each, as the parts are two
+// or three.
 // ---------------------------------------------------------------------------
 struct Part {             // a lane's share of a partial result: float4 lane + 28 k of 112
   float4 v[4];
@@ -522,7 +529,7 @@ size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
 
 cudaError_t launch_merge(const ChunkArgs& a, const ChunkPlan& p, int rows, int workers, cudaStream_t s) {
   if (workers < 2) return cudaSuccess;
-  // few tiles: many partial results a row
+  // few tiles: many partial results a row (see the kernel)
   const int64_t tiles = (static_cast<int64_t>(a.T) * a.H + rows - 1) / rows + a.B;
   const unsigned cuts = static_cast<unsigned>(tiles < workers - 1 ? tiles : workers - 1);
   if (tiles * 4 <= workers)
@@ -551,7 +558,9 @@ cudaError_t launch_single_path(const ChunkArgs& a, const ChunkPlan& p, cudaStrea
   return e == cudaSuccess ? launch_merge(a, p, kSingleRows, workers, s) : e;
 }
 
-// Which kernel: pairs once a sequence brings a full tile of 256 rows on average.
+// Which kernel: pairs once a sequence brings a full tile of 256 rows on average.  Single against
+// pairs, 16 sequences of 16,000 and 64 heads: 1 token 90 and 184 us, 2 tokens 126 and 161, 4
+// tokens 214 and 160; 16 tokens of 16 heads over 8,000 93 and 88; 1 token of 128 heads 60 and 70.
 bool use_pairs(const smla_chunk_params* p) {
   return static_cast<int64_t>(p->total_q) * p->num_heads >= static_cast<int64_t>(kPairRows) * p->batch;
 }

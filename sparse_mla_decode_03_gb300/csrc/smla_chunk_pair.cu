@@ -20,8 +20,14 @@
 // powers of two: exact), which a kernel before this one writes once a call: 1.6 KB moved a
 // position, against 960 multiply-adds for each of its query rows.
 //
+// Measured: 1,024 tokens of 128 heads behind 15,360 positions in 2.22 ms with plan, expansion
+// and merge, 1.80 PFLOP/s (93 % of the measured matrix rate); 512 tokens of 64 heads in 8,192
+// positions 278 of 311 us, tensor pipe 78 % busy, the tensor core's shared-memory reads 69 %.
+// The issuing warp walks its schedule as one and elects a lane for the products alone: issued
+// by a branch of one lane they took 87 cycles each, against 45 to 64.
+//
 // Warps of a CTA: 0..3 softmax and results (a thread a row), 4 tensor copies (one lane), 5
-// in the leading CTA issues the products (one lane).  Every wait is bounded.
+// in the leading CTA issues the products.  Every wait is bounded.
 #include <cstring>
 #include <mutex>
 

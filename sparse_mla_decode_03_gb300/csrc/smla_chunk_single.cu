@@ -7,12 +7,19 @@
 // 512 a block of 64 positions), O += P V (64 x 448 x 64), K and V from one expanded block in
 // shared memory.
 //
-// What bounds it.  64 positions are 37 KB of the cache: 1,630 cycles at the measured
-// bandwidth with all SMs reading.  The products take at least 45 cycles each at 64 x 64 x 16
-// (measured; 32 of them) and half of the tensor rate at 64 rows (900 cycles for the value
-// product): about 2,350 cycles a block.  Shared memory moves 64 KB of Q, 64 KB of K, 72 KB
-// of V and P and 64 KB of expanded rows, 2,060 cycles.  So a block of one or two SMs' worth
-// of rows is bound by the tensor core at small tiles, within 1.5 of the cache's bandwidth.
+// What bounds it: the chain that each block goes through, not one unit.  64 positions are 37 KB
+// of the cache, 1,630 cycles at the copy rate with all SMs reading.  The products take 2,350
+// (32 of 64 x 64 x 16 at their measured minimum of 45 cycles; the value product runs at half
+// of the tensor rate with 64 rows: 900), the expansion about 1,600 of the integer pipe, the
+// softmax about 800.  Expansion, scores, softmax and value product of a block follow one
+// another, and the scores and O fill tensor memory, so two blocks in two buffers overlap in
+// part only: about 5,100 cycles a block.  32 single tokens of 64 heads over 8,192 positions
+// take 76 us (153 MB: 2.0 TB/s, 30 % of the copy rate; tensor pipe 40 % busy, integer pipe
+// 53 %), with plan and merge 85 us; two tokens of 16 heads over 131,072 take 68 and 77 us.
+// Measured and not kept: f16 operands (96 us against 93 then), two sets of 8 expanding warps
+// (93..105), the next block's rows read before this one's expansion (110: spills), through
+// shared memory (92 against 85: past the carve-out step) or half a row earlier (87), one lane
+// polling for its warp (107).
 //
 // Expansion without conversions: an e4m3 byte's exponent and mantissa, shifted into bf16's
 // fields, are its value times 2^-120 (subnormals included), and one bf16 product by
@@ -53,7 +60,8 @@ constexpr int kQOff = 0;
 constexpr int kBufOff = 8 * kSlab;
 // P of a block takes the place of its rope, which the scores are done with; the buffer is
 // filled again only after the value product.  Without 8 KB for P the CTA stays below the
-// 196 KB step of the shared-memory carve-out, which leaves the loads 60 KB of L1, not 28.
+// 196 KB step of the shared-memory carve-out, which leaves the loads 60 KB of L1, not 28 (93 ->
+// 85 us).
 constexpr int kPOff = kBufOff + 7 * kSlab;     // + kBuf for the second buffer
 constexpr int kBarOff = kBufOff + 2 * kBuf;
 constexpr int kMaskOff = kBarOff + 256;    // [2 buffers][mapped, not finite][16 half bytes]
