@@ -25,6 +25,15 @@ __device__ __forceinline__ float ue8m0_value(uint32_t e) {
 // and masks: no SM waits for the longest sequence.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
+// Least blocks of a share, which pays for its query tile and its partial result: 4 x 4 tokens of
+// 1,001: 33.0, 29.3, 31.6 and 35.9 us with 1, 2, 4 and 8.
+constexpr int kMinShare = 2;
+// A border within this many blocks of a tile's end moves there (by a quarter of a share at
+// most): a piece of a tile costs its 256 rows of Q and 458 KB of partial results, which leave an SM
+// at 28 bytes a cycle, as much as four blocks.  Seven ragged sequences of 16 heads: 68.0, 65.3,
+// 59.5, 59.4 and 59.5 us with 0, 1, 2, 3 and 6; three of 700 tokens in a window 156, 153, 151,
+// 147 and 146; single tokens do not mind.
+constexpr int kSnap = 3;
 
 // Exclusive sum over the CTA; *total gets the sum.
 __device__ long long block_sum(long long v, long long* total, long long* warp_sums) {
@@ -88,7 +97,7 @@ struct PlanShared {
 // By one CTA of kPlanThreads.  tile_rows: (token, head) rows of a tile; workers: shares of
 // the line.  Latency is all that counts here (a few dependent loads and block-wide sums), so
 // what the tiles need of their sequences, and the line, stay in shared memory in usual calls.
-__device__ void make_plan(const ChunkArgs& a, const ChunkPlan& p, int tile_rows, int workers, int min_share,
+__device__ void make_plan(const ChunkArgs& a, const ChunkPlan& p, int tile_rows, int workers,
                           PlanShared& sh) {
   const bool few = a.B <= kPlanSeqs;
   long long tiles = 0, blocks = 0;
@@ -178,29 +187,38 @@ __device__ void make_plan(const ChunkArgs& a, const ChunkPlan& p, int tile_rows,
     tiles = 0;
     if (threadIdx.x == 0) atomicCAS(a.status, 0, SMLA_ERR_UNSUPPORTED_SHAPE);
   }
-  const int per = max(min_share, static_cast<int>((line + workers - 1) / workers));
+  const int per = max(kMinShare, static_cast<int>((line + workers - 1) / workers));
   if (threadIdx.x == 0) {
     p.cum[tiles] = static_cast<int>(line);
     if (short_line) sh.cum[tiles] = static_cast<int>(line);
   }
   __syncthreads();
-  // the tile at the start of each share, so that nobody else has to search, and the cut
-  // tiles, found at the first share that begins inside each
+  // where each share begins, and the tile there, so that nobody else has to search
   const int32_t* cum = short_line ? sh.cum : p.cum;
-  const int c = static_cast<int>(threadIdx.x);
+  const int c = static_cast<int>(threadIdx.x), snap = min(kSnap, per / 4);
+  int32_t* border = sh.first;
+  int t = -1;
+  if (c <= workers) {
+    int x = static_cast<int>(min(static_cast<long long>(c) * per, line));
+    if (x < line) {
+      t = find_last_le(cum, static_cast<int>(tiles) + 1, x);
+      if (x - cum[t] <= snap) x = cum[t];
+      else if (cum[t + 1] - x <= snap) x = cum[++t];
+      if (x == line) t = -1;
+    }
+    border[c] = x;
+    p.begin[c] = x;
+    if (c < workers) p.start[c] = t;
+  }
+  __syncthreads();
+  // the cut tiles, found at the first share that begins inside each
   bool cut = false;
   int4 piece = make_int4(0, 0, 0, 0);
-  if (c < workers) {
-    const long long x = static_cast<long long>(c) * per;
-    const int t = x < line ? find_last_le(cum, static_cast<int>(tiles) + 1, static_cast<int>(x)) : -1;
-    p.start[c] = t;
-    if (t >= 0) {
-      const int begin = cum[t];
-      cut = begin < x && begin / per + 1 == c;
-      if (cut) {
-        const int4 tile = p.tile[t];
-        piece = make_int4(tile.y, tile.z, c - 1, (cum[t + 1] - 1) / per);
-      }
+  if (c > 0 && c < workers && t >= 0) {
+    cut = cum[t] < border[c] && border[c - 1] <= cum[t];
+    if (cut) {
+      const int4 tile = p.tile[t];
+      piece = make_int4(tile.y, tile.z, c - 1, find_last_le(border, workers + 1, cum[t + 1] - 1));
     }
   }
   long long cuts;
@@ -209,17 +227,16 @@ __device__ void make_plan(const ChunkArgs& a, const ChunkPlan& p, int tile_rows,
   if (threadIdx.x == 0) {
     p.head[0] = static_cast<int>(tiles);
     p.head[1] = static_cast<int>(line);
-    p.head[2] = per;
-    p.head[3] = static_cast<int>(cuts);
+    p.head[2] = static_cast<int>(cuts);
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1)
-    plan_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows, int workers, int min_share) {
+    plan_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows, int workers) {
   __shared__ PlanShared sh;
   grid_dep_wait();
   grid_dep_launch();
-  make_plan(a, p, tile_rows, workers, min_share, sh);
+  make_plan(a, p, tile_rows, workers, sh);
 }
 
 // ---------------------------------------------------------------------------
@@ -245,13 +262,13 @@ __device__ __forceinline__ bool not_finite(uint32_t bf16x2) {
 // same sums over the batch), so that one launch does both.
 constexpr int kExpandRows = 2;     // rows of a block that a warp expands at once: 32 warps, 64 rows
 __global__ void __launch_bounds__(kPlanThreads, 1)
-    expand_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows, int workers, int min_share) {
+    expand_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows, int workers) {
   __shared__ PlanShared sh;
   __shared__ uint32_t mapped[32], odd[32];
   grid_dep_wait();
   grid_dep_launch();
   if (blockIdx.x == 0) {
-    make_plan(a, p, tile_rows, workers, min_share, sh);
+    make_plan(a, p, tile_rows, workers, sh);
     return;
   }
   // sh.first: first block of each sequence, sh.last: its visible positions; in rounds of
@@ -403,7 +420,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const Chu
   __shared__ float weight[8];
   grid_dep_wait();
   grid_dep_launch();
-  const int cuts = p.head[3];
+  const int cuts = p.head[2];
   const int4 cut = p.cut[blockIdx.y];     // first row of the tile, rows, first and last worker
   if (static_cast<int>(blockIdx.y) >= cuts) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -494,10 +511,6 @@ int check_chunk(const smla_chunk_params* p) {
 // pair of SMs with 256 rows each needs twice what two SMs with 64 do).
 constexpr int kMaxSms = 152;
 constexpr int kMaxPairs = kMaxSms / 2;
-// Blocks: a share pays for its query tile and its partial result.  4 x 4 tokens of 1001: 33.0,
-// 29.3, 31.6 and 35.9 us with 1, 2, 4 and 8.
-constexpr int kMinShare = 2;
-
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // The workspace of a call; base may be null to size it.
@@ -519,6 +532,7 @@ size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
   plan->seq_base = reinterpret_cast<int32_t*>(take(4 * (B + 1)));
   plan->seq_len = reinterpret_cast<int32_t*>(take(4 * B));
   plan->start = reinterpret_cast<int32_t*>(take(4 * kMaxSms));
+  plan->begin = reinterpret_cast<int32_t*>(take(4 * (kMaxSms + 1)));
   plan->cut = reinterpret_cast<int4*>(take(16 * kMaxSms));
   plan->lse_part = reinterpret_cast<float*>(take(size_t{4} * 2 * kMaxPairs * kPairRows));
   plan->o_part = reinterpret_cast<float*>(take(size_t{4} * 2 * kMaxPairs * kPairRows * kNope));
@@ -544,7 +558,7 @@ cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_
   if (workers > kMaxPairs) workers = kMaxPairs;
   const int64_t blocks = p.cap_blocks + 1;
   const unsigned grid = 1 + static_cast<unsigned>(blocks < kMaxSms - 1 ? blocks : kMaxSms - 1);
-  e = launch_programmatic(expand_kernel, dim3(grid), dim3(kPlanThreads), 0, s, a, p, kPairRows, workers, kMinShare);
+  e = launch_programmatic(expand_kernel, dim3(grid), dim3(kPlanThreads), 0, s, a, p, kPairRows, workers);
   if (e != cudaSuccess) return e;
   e = launch_chunk_pair(a, p, workers, s);
   return e == cudaSuccess ? launch_merge(a, p, kPairRows, workers, s) : e;
@@ -552,8 +566,7 @@ cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_
 
 cudaError_t launch_single_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_t s) {
   const int workers = kMaxSms;
-  cudaError_t e = launch_programmatic(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, p, kSingleRows, workers,
-                                      kMinShare);
+  cudaError_t e = launch_programmatic(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, p, kSingleRows, workers);
   if (e == cudaSuccess) e = launch_chunk_single(a, p, workers, s);
   return e == cudaSuccess ? launch_merge(a, p, kSingleRows, workers, s) : e;
 }

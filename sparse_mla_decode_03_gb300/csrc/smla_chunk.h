@@ -34,10 +34,11 @@ struct ChunkArgs {
 // equal shares, one a worker.  A tile that lies in one share is finished by its worker;
 // the others leave partial results that the merge joins.
 struct ChunkPlan {
-  int32_t* head;         // [0] tiles, [1] blocks on the line, [2] blocks a share, [3] cut tiles
+  int32_t* head;         // [0] tiles, [1] blocks on the line, [2] cut tiles
   int4* tile;            // sequence, first row (token * H + head), rows, first block
   int32_t* cum;          // [tiles + 1] start of each tile on the line
   int32_t* start;        // [workers] the tile at the start of each share, -1 behind the line
+  int32_t* begin;        // [workers + 1] where each share starts on the line
   int4* cut;             // [cut tiles] first row, rows, first and last worker
   int32_t* tile_base;    // [B + 1] first tile of each sequence
   int32_t* seq_base;     // [B + 1] first block of each sequence in the expanded copy

@@ -90,9 +90,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   grid_dep_launch();
 
-  const int total = plan.head[1], per = plan.head[2];
-  const int t_first = plan.start[worker];
-  const int x0 = t_first >= 0 ? worker * per : total, x1 = min(total, x0 + per);
+  const int t_first = plan.start[worker], x0 = plan.begin[worker], x1 = plan.begin[worker + 1];
 
   if (warp == 4) {
     // ---------------- tensor copies ----------------

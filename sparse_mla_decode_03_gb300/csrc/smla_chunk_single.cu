@@ -386,9 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   grid_dep_launch();
 
-  const int total = plan.head[1], per = plan.head[2];
-  const int t_first = plan.start[worker];
-  const int x0 = t_first >= 0 ? worker * per : total, x1 = min(total, x0 + per);
+  const int t_first = plan.start[worker], x0 = plan.begin[worker], x1 = plan.begin[worker + 1];
 
   if (warp >= kExpandWarp0 && warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsExpand) : "memory");
