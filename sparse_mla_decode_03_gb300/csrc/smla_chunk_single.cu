@@ -217,13 +217,10 @@ struct TwoRows {
     const float scale2 = mods.scale2;
     if constexpr (MODS) {
       const float from0 = static_cast<float>(pos[0] - s0 - col), from1 = static_cast<float>(pos[1] - s0 - col);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          v[4 * j + e] = mods(v[4 * j + e], slope2[0], from0 - static_cast<float>(8 * j + e));
-          v[4 * j + 2 + e] = mods(v[4 * j + 2 + e], slope2[1], from1 - static_cast<float>(8 * j + e));
-        }
+      mods(v, [&](int k) {
+        const float c = static_cast<float>(8 * (k / 4) + k % 2);
+        return k % 4 < 2 ? make_float2(slope2[0], from0 - c) : make_float2(slope2[1], from1 - c);
+      });
     }
     const unsigned long long seen0 = seen_of(rows.x, s0, lo[0], hi[0]), seen1 = seen_of(rows.x, s0, lo[1], hi[1]);
     if (__any_sync(0xffffffffu, (seen0 & seen1) != ~0ull)) {

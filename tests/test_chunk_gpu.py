@@ -481,3 +481,30 @@ def test_offsets_that_decrease_are_refused_on_the_device(T):
     m.smla_chunk_attention(q, pool, table, page, dev(cu), dev(np.full(B, 128, dtype=np.int32)), out=out, lse=lse)
     assert m.smla_device_status(clear=True) == -7
     assert bool((out == 7).all()) and bool((lse == 7).all())
+
+
+@pytest.mark.parametrize("cap", [5.0, 30.0, 1000.0])
+@pytest.mark.parametrize("B,n", [(64, 1), (2, 32)])
+def test_capped_scores_keep_their_digits(B, n, cap):
+    """Tokens that see one position, whose score is one exact product: lse is the capped score.
+    Relative error: 9e-9 of the series, or past z = 1/4 the exponential form, 1 - 2 / (1 + e): two
+    steps of 2^-23 each of the exponential and of the quotient, which are 0.47 e and 0.75 there, over
+    tanh(1/4) = 0.245: 5 * 2^-22; a dozen 32-bit roundings of 2^-24 and the conversions to and from
+    log2: below 2^-19 together."""
+    H, page = 16, 4
+    rows = torch.zeros((B * page, ROW), dtype=torch.uint8, device="cuda")
+    rows[:, 448:455] = 127
+    rows[:, 0] = 0x38                                       # e4m3 1.0
+    lens = np.full(B, n, dtype=np.int32)
+    table = np.arange(B, dtype=np.int32)[:, None].repeat(-(-n // page), axis=1)
+    cu = (np.arange(B + 1) * n).astype(np.int32)
+    x = torch.cat([torch.logspace(-3, 2, B * n * H // 2), -torch.logspace(-3, 2, B * n * H // 2)])
+    q = torch.zeros((B * n, H, 512), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = x.view(B * n, H).to(torch.bfloat16).cuda()
+    m.smla_device_status(clear=True)
+    out, lse = m.smla_chunk_attention(q, rows, dev(table), page, dev(cu), dev(lens), softmax_scale=1.0, logit_cap=cap,
+                                      vis_begin=dev(np.zeros(B * n, np.int32)), vis_end=dev(np.ones(B * n, np.int32)))
+    assert m.smla_device_status(clear=True) == 0
+    want = cap * torch.tanh(q[:, :, 0].double() / cap)
+    assert ((lse.double() - want).abs() <= 2.0 ** -19 * want.abs()).all()
+    assert torch.equal(out[:, :, 0].float(), torch.ones_like(lse)) and not out[:, :, 1:].any()
