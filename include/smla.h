@@ -384,7 +384,7 @@ typedef struct smla_chunk_params {
   int64_t num_rows;       /* rows of the pool, 1 .. 2^31                                */
   int64_t kv_row_stride;  /* bytes between rows, >= 584, multiple of 8, < 2^31          */
   int64_t max_kv_tokens;  /* 1 .. 2^30: the caller's bound on the sum of kv_lens; it sizes the
-                             workspace.  Tokens past it are masked and reported
+                             workspace of pairs of SMs (see above).  Tokens past it are masked and reported
                              (SMLA_ERR_INDEX_RANGE)                                     */
   float softmax_scale;    /* finite and > 0                                             */
   float logit_cap;        /* 0 = none, else finite and > 0                              */

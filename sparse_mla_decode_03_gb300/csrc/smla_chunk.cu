@@ -507,11 +507,17 @@ int check_chunk(const smla_chunk_params* p) {
   return SMLA_OK;
 }
 
-// SMs of the GPU that this library is for: the workers that a workspace has room for (a
-// pair of SMs with 256 rows each needs twice what two SMs with 64 do).
+// SMs of the GPU that this library is for: the workers that a workspace has room for.
 constexpr int kMaxSms = 152;
 constexpr int kMaxPairs = kMaxSms / 2;
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// Which kernel: pairs once a sequence brings a full tile of 256 rows on average.  Single against
+// pairs, 16 sequences of 16,000 and 64 heads: 1 token 90 and 184 us, 2 tokens 126 and 161, 4
+// tokens 214 and 160; 16 tokens of 16 heads over 8,000 93 and 88; 1 token of 128 heads 60 and 70.
+bool use_pairs(const smla_chunk_params* p) {
+  return static_cast<int64_t>(p->total_q) * p->num_heads >= static_cast<int64_t>(kPairRows) * p->batch;
+}
 
 // The workspace of a call; base may be null to size it.
 size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
@@ -534,10 +540,13 @@ size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
   plan->start = reinterpret_cast<int32_t*>(take(4 * kMaxSms));
   plan->begin = reinterpret_cast<int32_t*>(take(4 * (kMaxSms + 1)));
   plan->cut = reinterpret_cast<int4*>(take(16 * kMaxSms));
-  plan->lse_part = reinterpret_cast<float*>(take(size_t{4} * 2 * kMaxPairs * kPairRows));
-  plan->o_part = reinterpret_cast<float*>(take(size_t{4} * 2 * kMaxPairs * kPairRows * kNope));
-  plan->seen = reinterpret_cast<ulonglong2*>(take(16 * static_cast<size_t>(cap + 1)));
-  plan->kv = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(cap + 1) * kChunkBlk * kQkDim * 2));
+  const size_t parts = use_pairs(p) ? 2 * kMaxPairs * kPairRows : 2 * kMaxSms * kSingleRows;
+  plan->lse_part = reinterpret_cast<float*>(take(4 * parts));
+  plan->o_part = reinterpret_cast<float*>(take(4 * parts * kNope));
+  // the expanded copy, which only pairs read
+  const size_t copies = use_pairs(p) ? static_cast<size_t>(cap + 1) : 0;
+  plan->seen = reinterpret_cast<ulonglong2*>(take(16 * copies));
+  plan->kv = reinterpret_cast<uint16_t*>(take(copies * kChunkBlk * kQkDim * 2));
   return at;
 }
 
@@ -571,12 +580,6 @@ cudaError_t launch_single_path(const ChunkArgs& a, const ChunkPlan& p, cudaStrea
   return e == cudaSuccess ? launch_merge(a, p, kSingleRows, workers, s) : e;
 }
 
-// Which kernel: pairs once a sequence brings a full tile of 256 rows on average.  Single against
-// pairs, 16 sequences of 16,000 and 64 heads: 1 token 90 and 184 us, 2 tokens 126 and 161, 4
-// tokens 214 and 160; 16 tokens of 16 heads over 8,000 93 and 88; 1 token of 128 heads 60 and 70.
-bool use_pairs(const smla_chunk_params* p) {
-  return static_cast<int64_t>(p->total_q) * p->num_heads >= static_cast<int64_t>(kPairRows) * p->batch;
-}
 
 }  // namespace
 }  // namespace smla

@@ -128,3 +128,15 @@ def test_binding_checks():
                                                 i1[:2])):
         with pytest.raises(ValueError):
             call()
+
+
+def test_chunk_workspace_of_single_tokens_holds_no_copy_of_the_cache(lib):
+    def need(**over):
+        n = ctypes.c_size_t()
+        assert lib.smla_chunk_workspace_size(_chunk(**over), ctypes.byref(n)) == 0
+        return n.value
+
+    few = dict(batch=4, num_heads=64, total_q=15)           # 240 rows a sequence on average
+    many = dict(batch=4, num_heads=64, total_q=16)
+    assert need(**few, max_kv_tokens=1 << 30) == need(**few, max_kv_tokens=1)
+    assert need(**many, max_kv_tokens=65 * 64) - need(**many, max_kv_tokens=64) == 64 * (64 * 1024 + 16)
