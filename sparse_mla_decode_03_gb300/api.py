@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
@@ -292,10 +293,16 @@ def smla_cache_workspace_size(params: _lib.SmlaCacheParams) -> int:
     return n.value
 
 
+@functools.lru_cache(maxsize=256)
+def _cache_bytes(num_pages: int, num_seqs: int) -> int:
+    """What smla_cache_workspace_size says: a matter of these two sizes alone."""
+    return smla_cache_workspace_size(make_cache_params(num_pages, 1, num_seqs, 1))
+
+
 def _cache_workspace(p: _lib.SmlaCacheParams, workspace: Optional[torch.Tensor],
                      device: torch.device) -> torch.Tensor:
     if workspace is None:
-        return torch.empty(smla_cache_workspace_size(p), dtype=torch.uint8, device=device)
+        return torch.empty(_cache_bytes(p.num_pages, p.num_seqs), dtype=torch.uint8, device=device)
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace
@@ -442,6 +449,12 @@ def smla_chunk_workspace_size(params: _lib.SmlaChunkParams) -> int:
     return n.value
 
 
+@functools.lru_cache(maxsize=1024)
+def _chunk_bytes(batch: int, num_heads: int, total_q: int, max_kv_tokens: int) -> int:
+    """What smla_chunk_workspace_size says: a matter of these sizes alone."""
+    return smla_chunk_workspace_size(make_chunk_params(batch, num_heads, total_q, 1, 1, 1, ROW_BYTES, max_kv_tokens))
+
+
 def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
                          page_size: int, cu_q: torch.Tensor, kv_lens: torch.Tensor,
                          softmax_scale: float = DEFAULT_SCALE, logit_cap: float = 0.0,
@@ -478,18 +491,18 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
         raise ValueError(f"slopes must be contiguous fp32 [H] on {dev}")
     if out is None:
         out = torch.empty((T, H, NOPE), dtype=torch.bfloat16, device=dev)
+    elif out.shape != (T, H, NOPE) or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be contiguous bf16 [{T}, {H}, {NOPE}] on {dev}")
     if lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    for name, t, shape, dtype in (("out", out, (T, H, NOPE), torch.bfloat16),
-                                  ("lse", lse, (T, H), torch.float32)):
-        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {dev}")
+    elif lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
+        raise ValueError(f"lse must be contiguous fp32 [{T}, {H}] on {dev}")
     if max_kv_tokens is None:
         max_kv_tokens = B * max_pages * page_size
     p = make_chunk_params(B, H, T, page_size, max_pages, kv_pages.shape[0], _row_stride(kv_pages),
                           max_kv_tokens, softmax_scale, logit_cap)
     if workspace is None:
-        workspace = torch.empty(smla_chunk_workspace_size(p), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(_chunk_bytes(B, H, T, max_kv_tokens), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     with _on(dev):
