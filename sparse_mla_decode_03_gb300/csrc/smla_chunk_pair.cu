@@ -22,7 +22,7 @@
 //
 // Measured: 1,024 tokens of 128 heads behind 15,360 positions in 2.22 ms with plan, expansion
 // and merge, 1.80 PFLOP/s (93 % of the measured matrix rate); 512 tokens of 64 heads in 8,192
-// positions 278 of 309 us, tensor pipe 78 % busy, the tensor core's shared-memory reads 69 %.
+// positions 278 of 310 us, tensor pipe 78 % busy, the tensor core's shared-memory reads 69 %.
 // The issuing warp walks its schedule as one and elects a lane for the products alone: issued
 // by a branch of one lane they took 87 cycles each, against 45 to 64.
 //
