@@ -668,8 +668,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // P: rows 16 quarter + g and + 8 (the same row modulo 8), columns 2 (lane % 4) .. of unit j
     const uint32_t p0 = sbase + kPOff + (16 * quarter + g) * 128 + 4 * (lane & 3), p1 = p0 + 8 * 128;
     uint32_t n = 0;
+    int x = x0, t = t_first, i = 0, held = 0;
     bool ok = true;
-    for (int x = x0, t = t_first; ok && x < x1; ++t) {
+    for (; ok && x < x1; ++t) {
       const int4 tile = plan.tile[t];
       const int begin = plan.cum[t], after = plan.cum[t + 1], end = min(x1, after);
       const int nb = end - x, blk = tile.w + (end - 1 - begin);     // the first block
@@ -677,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // without rows only keeps step
       TwoRows<MODS> st(a, plan, tile, 16 * quarter + g);
       const bool idle = 16 * quarter >= tile.z;
-      for (int i = 0; ok && i < nb; ++i, ++n) {
+      for (i = 0; ok && i < nb; ++i, ++n) {
         ok = warp_wait(bar(FULL + 2 * (n & 1)), (n >> 1) & 1, stop, a.status);     // the masks' writers
         if (!ok) break;
         const volatile unsigned long long* mk =
@@ -708,7 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O may be rescaled once the value product before this one is done
         if (i > 0 && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
           ok = warp_wait(bar(EMPTY + 2 * ((n - 1) & 1) + 1), ((n - 1) >> 1) & 1, stop, a.status);
-          if (!ok) break;
+          if (!ok) {
+            held = 1;
+            break;
+          }
           tc_fence_after();
           const float f = to_row(alpha);
           rescale_rows(tO, lane < 16 ? f : 1.f, 224 * half, 224);
@@ -760,6 +764,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(OEMPTY));
       x = end;
     }
+    // A wait has run out.  The quarter's other warp may have come further: both hold all
+    // meetings of the schedule, one a block and three a tile, so that neither waits for good.
+    if (!ok)
+      for (; x < x1; ++t, i = 0, held = 0) {
+        const int end = min(x1, plan.cum[t + 1]);
+        if (16 * quarter < plan.tile[t].z)
+          for (int k = end - x + 3 - i - held; k > 0; --k) asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+        x = end;
+      }
   }
   tc_fence_before();
   __syncthreads();
