@@ -236,7 +236,10 @@ int sparse_mla_decode_noalloc(const void* q, const void* kv_cache, const int32_t
  * wait for that block then runs out, the CTA records SMLA_ERR_TIMEOUT in the device
  * status word (smla_device_status), every role leaves through its bounded waits and
  * the epilogue, and the launch completes without a fault; its outputs are undefined.
- * CTAs whose split has no such block are unaffected.  block = -1 switches the hook
+ * CTAs whose split has no such block are unaffected.  In the kernels of
+ * smla_chunk_attention one warp withholds the same signal (single SMs) or that of the
+ * block's weights (pairs) for that block of each SM's share, and the waits keep their
+ * limit of about 1 s.  block = -1 switches the hook
  * off.  Returns SMLA_OK, or SMLA_ERR_INVALID_ARG for block < -1.  Not for use in
  * production; calls made while it is on are not thread-safe with respect to it.
  */

@@ -623,7 +623,7 @@ int smla_chunk_attention(const void* q, const void* kv_pages, const int32_t* blo
                        block_table, cu_q, kv_lens, vis_begin, vis_end, slopes,
                        static_cast<__nv_bfloat16*>(out), lse, p->batch, p->num_heads, p->total_q,
                        p->page_size, p->max_pages, p->num_rows, p->kv_row_stride, p->softmax_scale,
-                       p->logit_cap, status};
+                       p->logit_cap, status, fault_block()};
   ChunkPlan plan;
   lay_out(p, static_cast<char*>(workspace), &plan);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -27,6 +27,7 @@ struct ChunkArgs {
   int64_t num_rows, stride;
   float scale, cap;
   int* status;
+  int fault_block;       // test hook: the block of each share that one warp does not report (-1: none)
 };
 
 // The plan of a call: the (token, head) rows of each sequence cut into tiles, each tile's

@@ -276,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(pfull);
+        if (lane == 0 && !(warp == 0 && np == static_cast<uint32_t>(a.fault_block))) mbar_arrive_cluster(pfull);
         ++np;
       }
       if (!ok) break;

@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(FULL + 2 * B));
+        if (lane == 0 && !(n == a.fault_block && w16 == 0)) mbar_arrive(bar(FULL + 2 * B));
         if (n >= 2) ok = warp_wait(bar(EMPTY + 2 * B + 1), parity, stop, a.status);
         if (!ok) break;
         // the rope: word w of row j

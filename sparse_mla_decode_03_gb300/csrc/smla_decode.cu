@@ -1793,6 +1793,7 @@ cudaError_t fused_clusters(int H, int S, int* clusters) {
 }
 
 void set_fault_block(int block) { g_fault_block.store(block, std::memory_order_relaxed); }
+int fault_block() { return g_fault_block.load(std::memory_order_relaxed); }
 
 cudaError_t status_word_address(int** ptr) {
   return cudaGetSymbolAddress(reinterpret_cast<void**>(ptr), g_smla_status);

@@ -101,6 +101,7 @@ int launch_step(const void* q, const void* kv_cache, const int32_t* indices, voi
 // Test hook of smla_test_inject_fault: block index at which one converter warp of
 // every CTA of later decode launches withholds its "block filled" arrival (-1: off).
 void set_fault_block(int block);
+int fault_block();
 
 // Device address of the status word (kernels in other translation units record
 // their errors through it; device variables are not shared across them).

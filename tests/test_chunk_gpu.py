@@ -508,3 +508,22 @@ def test_capped_scores_keep_their_digits(B, n, cap):
     want = cap * torch.tanh(q[:, :, 0].double() / cap)
     assert ((lse.double() - want).abs() <= 2.0 ** -19 * want.abs()).all()
     assert torch.equal(out[:, :, 0].float(), torch.ones_like(lse)) and not out[:, :, 1:].any()
+
+
+@pytest.mark.parametrize("ns,H", [([1, 1], 64), ([40, 30], 16)])
+@pytest.mark.parametrize("block", [0, 1])
+def test_a_wait_that_runs_out_reports_and_the_next_call_is_right(ns, H, block):
+    """One warp keeps a signal back (nothing faults): the waits for it end after about a second, the
+    call returns, and the next one on the same context is right."""
+    page = 16
+    q, pool, table, cu, lens = _case([3000, 20000], ns, H, page, 77)
+    lib = m._lib.load()
+    m.smla_device_status(clear=True)
+    assert lib.smla_test_inject_fault(block) == 0
+    try:
+        m.smla_chunk_attention(q, pool, dev(table), page, dev(cu), dev(lens))
+        torch.cuda.synchronize()
+        assert m.smla_device_status(clear=True) == m._lib.SMLA_ERR_TIMEOUT
+    finally:
+        assert lib.smla_test_inject_fault(-1) == 0
+    _check(q, pool, table, page, cu, lens)
