@@ -8,7 +8,7 @@
 // CTA's slice of the pages or table each), so a call is one launch, plus one wide launch
 // where rows of the cache move.  Page calls are bound by launches and by the trips to memory
 // and cluster barriers of a plan: free 4 us, fork 9 + 5 (512 children 9 + 8), reserve 6 (of
-// 576 rows and 32,768 pages 13), compaction's plan 7 (32,768 pages 12).
+// 576 rows and 32,768 pages 13), compaction's plan 7 (32,768 pages 10).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -551,31 +551,32 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       a.ref_out[p] = c;
     }
   });
-  const int64_t step = static_cast<int64_t>(kPlanCtas) * kPlanThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x; i < a.entries; i += step) {
-    int v = a.table[i];
-    if (v >= a.num_pages) {
-      report(a.status, SMLA_ERR_INDEX_RANGE);
-    } else if (v >= used) {
-      const int r = __ldcg(a.rank_of + v);
-      if (r >= 0) v = __ldcg(a.holes + (r - kept));
-      else report(a.status, SMLA_ERR_INDEX_RANGE);
-    }
-    a.table_out[i] = v;
-  }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.info[0] = used;
     a.info[1] = moved;
   }
 }
 
-// Moves the listed pages: a CTA takes chunks of kMoveRows rows in turn.  Bound by memory: 7,889
-// pages of 64 rows, 37 KB each in and out, in 89 us, 6.6 TB/s (98 % of the measured copy rate).
+// Rewrites the table and moves the listed pages: a CTA takes chunks of kMoveRows rows in turn.  Bound by memory: 7,889
+// pages of 64 rows, 37 KB each in and out, in 87 us, the measured copy rate.
 constexpr int kMoveRows = 28;      // 16,352 bytes: four 16-byte words a thread
 __global__ void __launch_bounds__(256) compact_move_kernel(const CompactArgs a) {
   grid_dep_wait();
   grid_dep_launch();
-  const int moved = a.info[1];
+  const int used = a.info[0], moved = a.info[1], kept = used - moved;
+  // the table, each entry by itself
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.entries; i += step) {
+    int v = a.table[i];
+    if (v >= a.num_pages) {
+      report(a.status, SMLA_ERR_INDEX_RANGE);
+    } else if (v >= used) {
+      const int r = a.rank_of[v];
+      if (r >= 0) v = a.holes[r - kept];
+      else report(a.status, SMLA_ERR_INDEX_RANGE);
+    }
+    a.table_out[i] = v;
+  }
   const int per = (a.page_size + kMoveRows - 1) / kMoveRows;
   const int64_t chunks = static_cast<int64_t>(moved) * per;
   for (int64_t i = blockIdx.x; i < chunks; i += gridDim.x) {
