@@ -3,7 +3,11 @@
 Every function forwards device pointers of torch tensors and the current CUDA
 stream to the C entry point of the same name (include/smla.h) and raises
 ``SmlaError`` on a non-zero status.  All computation happens in the library's
-CUDA kernels; there is no Python or CPU fallback."""
+CUDA kernels; there is no Python or CPU fallback.
+
+With ``stream=`` another stream than the current one, what a call allocates is that stream's
+memory, and arguments may be dropped as soon as the call returns.  That the inputs are ready on
+that stream, and that results are read after it, stays with the caller."""
 from __future__ import annotations
 
 import contextlib
@@ -37,6 +41,33 @@ def _check(status: int, where: str) -> None:
 def _stream(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+_SAME = contextlib.nullcontext()
+
+
+def _side(stream: Optional[torch.cuda.Stream], device: torch.device) -> Optional[torch.cuda.Stream]:
+    """`stream`, if it is another than the device's current one."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index):
+        return None
+    return stream
+
+
+def _memory_of(side: Optional[torch.cuda.Stream]):
+    """Where a call that runs on `side` allocates: there, so that its results and workspace are not
+    handed out, before or after it, to work of the current stream that does not wait for it."""
+    return _SAME if side is None else torch.cuda.stream(side)
+
+
+def _keep(side: Optional[torch.cuda.Stream], *tensors: Optional[torch.Tensor]) -> None:
+    """A call on `side` uses these tensors, and the caller the results on the current stream: the
+    memory of one that is dropped is not handed out again before both have come past this point."""
+    if side is None:
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(side)
+            t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
@@ -100,17 +131,20 @@ def sparse_mla_decode(q: torch.Tensor, kv_cache: torch.Tensor, indices: torch.Te
     """Whole decode step.  Returns (out bf16 [B, H, 448], lse fp32 [B, H])."""
     p = _params_from(q, kv_cache, indices, softmax_scale)
     B, H = p.batch, p.num_heads
-    if out is None:
-        out = torch.empty((B, H, NOPE), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
     need = smla_workspace_size(p, num_splits)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    side = _side(stream, q.device)
+    with _memory_of(side):
+        if out is None:
+            out = torch.empty((B, H, NOPE), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     lib = _lib.load()
     st = lib.sparse_mla_decode(_ptr(q), _ptr(kv_cache), _ptr(indices), _ptr(out), _ptr(lse),
                                ctypes.byref(p), num_splits, _ptr(workspace),
                                workspace.numel() * workspace.element_size(), _stream(stream))
+    _keep(side, q, kv_cache, indices, out, lse, workspace)
     _check(st, "sparse_mla_decode")
     return out, lse
 
@@ -124,13 +158,16 @@ def sparse_mla_decode_split(q: torch.Tensor, kv_cache: torch.Tensor, indices: to
     """Split kernel alone.  Returns (o_part fp32 [B, H, S, 448], lse_part fp32 [B, H, S])."""
     p = _params_from(q, kv_cache, indices, softmax_scale)
     B, H, S = p.batch, p.num_heads, num_splits
-    if o_part is None:
-        o_part = torch.empty((B, H, S, NOPE), dtype=torch.float32, device=q.device)
-    if lse_part is None:
-        lse_part = torch.empty((B, H, S), dtype=torch.float32, device=q.device)
+    side = _side(stream, q.device)
+    with _memory_of(side):
+        if o_part is None:
+            o_part = torch.empty((B, H, S, NOPE), dtype=torch.float32, device=q.device)
+        if lse_part is None:
+            lse_part = torch.empty((B, H, S), dtype=torch.float32, device=q.device)
     lib = _lib.load()
     st = lib.sparse_mla_decode_split(_ptr(q), _ptr(kv_cache), _ptr(indices), ctypes.byref(p), S,
                                      _ptr(o_part), _ptr(lse_part), _stream(stream))
+    _keep(side, q, kv_cache, indices, o_part, lse_part)
     _check(st, "sparse_mla_decode_split")
     return o_part, lse_part
 
@@ -147,13 +184,16 @@ def sparse_mla_combine(o_part: torch.Tensor, lse_part: torch.Tensor,
     if not (o_part.is_contiguous() and lse_part.is_contiguous()):
         raise ValueError("partials must be contiguous")
     B, H, S, _ = o_part.shape
-    if out is None:
-        out = torch.empty((B, H, NOPE), dtype=torch.bfloat16, device=o_part.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=o_part.device)
+    side = _side(stream, o_part.device)
+    with _memory_of(side):
+        if out is None:
+            out = torch.empty((B, H, NOPE), dtype=torch.bfloat16, device=o_part.device)
+        if lse is None:
+            lse = torch.empty((B, H), dtype=torch.float32, device=o_part.device)
     lib = _lib.load()
     st = lib.sparse_mla_combine(_ptr(o_part), _ptr(lse_part), B, H, S, _ptr(out), _ptr(lse),
                                 _stream(stream))
+    _keep(side, o_part, lse_part, out, lse)
     _check(st, "sparse_mla_combine")
     return out, lse
 
@@ -168,13 +208,16 @@ def sparse_mla_decode_noalloc(q: torch.Tensor, kv_cache: torch.Tensor, indices: 
     (no workspace argument; the C function allocates nothing).  Pass `out` and `lse`
     to keep the call itself free of allocations."""
     p = _params_from(q, kv_cache, indices, softmax_scale)
-    if out is None:
-        out = torch.empty((p.batch, p.num_heads, NOPE), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((p.batch, p.num_heads), dtype=torch.float32, device=q.device)
+    side = _side(stream, q.device)
+    with _memory_of(side):
+        if out is None:
+            out = torch.empty((p.batch, p.num_heads, NOPE), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((p.batch, p.num_heads), dtype=torch.float32, device=q.device)
     st = _lib.load().sparse_mla_decode_noalloc(_ptr(q), _ptr(kv_cache), _ptr(indices), _ptr(out),
                                                _ptr(lse), ctypes.byref(p), num_splits,
                                                _stream(stream))
+    _keep(side, q, kv_cache, indices, out, lse)
     _check(st, "sparse_mla_decode_noalloc")
     return out, lse
 
@@ -201,17 +244,20 @@ def sparse_mla_decode_paged(q: torch.Tensor, kv_pages: torch.Tensor, block_table
             or block_table.shape[0] != p.batch or not block_table.is_contiguous()
             or not block_table.is_cuda):
         raise ValueError("block_table must be a contiguous CUDA int32 [B, max_pages] tensor")
-    if out is None:
-        out = torch.empty((p.batch, p.num_heads, NOPE), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((p.batch, p.num_heads), dtype=torch.float32, device=q.device)
     need = smla_paged_workspace_size(p, num_splits)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    side = _side(stream, q.device)
+    with _memory_of(side):
+        if out is None:
+            out = torch.empty((p.batch, p.num_heads, NOPE), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((p.batch, p.num_heads), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     st = _lib.load().sparse_mla_decode_paged(
         _ptr(q), _ptr(kv_pages), _ptr(block_table), block_table.shape[1], page_size,
         _ptr(indices), _ptr(out), _ptr(lse), ctypes.byref(p), num_splits, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
+    _keep(side, q, kv_pages, block_table, indices, out, lse, workspace)
     _check(st, "sparse_mla_decode_paged")
     return out, lse
 
@@ -225,12 +271,15 @@ def sparse_mla_decode_simt(q: torch.Tensor, kv_cache: torch.Tensor, indices: tor
     """The per-head fp32 SIMT form of the decode step (a reference point for the
     tensor-core path).  Returns (out bf16 [B, H, 448], lse fp32 [B, H])."""
     p = _params_from(q, kv_cache, indices, softmax_scale)
-    if out is None:
-        out = torch.empty((p.batch, p.num_heads, NOPE), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((p.batch, p.num_heads), dtype=torch.float32, device=q.device)
+    side = _side(stream, q.device)
+    with _memory_of(side):
+        if out is None:
+            out = torch.empty((p.batch, p.num_heads, NOPE), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((p.batch, p.num_heads), dtype=torch.float32, device=q.device)
     st = _lib.load().sparse_mla_decode_simt(_ptr(q), _ptr(kv_cache), _ptr(indices), _ptr(out),
                                             _ptr(lse), ctypes.byref(p), _stream(stream))
+    _keep(side, q, kv_cache, indices, out, lse)
     _check(st, "sparse_mla_decode_simt")
     return out, lse
 
@@ -273,9 +322,6 @@ def _on(device: torch.device):
     return _SAME if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
-_SAME = contextlib.nullcontext()
-
-
 def _row_stride(kv_pages: torch.Tensor) -> int:
     """Bytes between rows (a single row has no neighbour: any stride will do)."""
     return kv_pages.stride(0) if kv_pages.shape[0] > 1 else ROW_BYTES
@@ -299,10 +345,11 @@ def _cache_bytes(num_pages: int, num_seqs: int) -> int:
     return smla_cache_workspace_size(make_cache_params(num_pages, 1, num_seqs, 1))
 
 
-def _cache_workspace(p: _lib.SmlaCacheParams, workspace: Optional[torch.Tensor],
-                     device: torch.device) -> torch.Tensor:
+def _cache_workspace(p: _lib.SmlaCacheParams, workspace: Optional[torch.Tensor], device: torch.device,
+                     side: Optional[torch.cuda.Stream]) -> torch.Tensor:
     if workspace is None:
-        return torch.empty(_cache_bytes(p.num_pages, p.num_seqs), dtype=torch.uint8, device=device)
+        with _memory_of(side):
+            return torch.empty(_cache_bytes(p.num_pages, p.num_seqs), dtype=torch.uint8, device=device)
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace
@@ -330,10 +377,12 @@ def smla_cache_append(kv: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
     p = make_cache_params(kv_pages.shape[0] // page_size, page_size, B, block_table.shape[1],
                           _row_stride(kv_pages))
     stride = kv.stride(0) if kv.shape[0] > 1 else QK
+    side = _side(stream, dev)
     with _on(dev):
         st = _lib.load().smla_cache_append(_adr(kv), stride, kv.shape[0], _adr(kv_pages), _adr(block_table),
                                            _adr(cu_q), _adr(kv_lens), ctypes.byref(p),
                                            _stream_on(stream, dev))
+    _keep(side, kv, kv_pages, block_table, cu_q, kv_lens)
     _check(st, "smla_cache_append")
 
 
@@ -348,10 +397,12 @@ def smla_cache_reserve(page_size: int, ref_count: torch.Tensor, block_table: tor
     if not ref_count.is_cuda or target_lens.shape[0] != block_table.shape[0]:
         raise ValueError("target_lens must be [B] for a block_table of B rows, on a CUDA device")
     p = make_cache_params(ref_count.shape[0], page_size, block_table.shape[0], block_table.shape[1])
-    ws = _cache_workspace(p, workspace, dev)
+    side = _side(stream, dev)
+    ws = _cache_workspace(p, workspace, dev, side)
     with _on(dev):
         st = _lib.load().smla_cache_reserve(_adr(ref_count), _adr(block_table), _adr(target_lens),
                                             ctypes.byref(p), _adr(ws), _bytes(ws), _stream_on(stream, dev))
+    _keep(side, ref_count, block_table, target_lens, ws)
     _check(st, "smla_cache_reserve")
 
 
@@ -380,11 +431,13 @@ def smla_cache_fork(kv_pages: torch.Tensor, page_size: int, ref_count: torch.Ten
     _ints("children", children, 1, dev)
     if kv_lens.shape[0] != block_table.shape[0] or parents.shape != children.shape:
         raise ValueError("kv_lens must be [B], and parents and children equally long")
-    ws = _cache_workspace(p, workspace, dev)
+    side = _side(stream, dev)
+    ws = _cache_workspace(p, workspace, dev, side)
     with _on(dev):
         st = _lib.load().smla_cache_fork(_adr(kv_pages), _adr(ref_count), _adr(block_table), _adr(kv_lens),
                                          _adr(parents), _adr(children), parents.shape[0], ctypes.byref(p),
                                          _adr(ws), _bytes(ws), _stream_on(stream, dev))
+    _keep(side, kv_pages, ref_count, block_table, kv_lens, parents, children, ws)
     _check(st, "smla_cache_fork")
 
 
@@ -399,9 +452,11 @@ def smla_cache_free(ref_count: torch.Tensor, block_table: torch.Tensor, kv_lens:
     if not ref_count.is_cuda or kv_lens.shape[0] != block_table.shape[0]:
         raise ValueError("kv_lens must be [B] for a block_table of B rows, on a CUDA device")
     p = make_cache_params(ref_count.shape[0], 1, block_table.shape[0], block_table.shape[1])
+    side = _side(stream, dev)
     with _on(dev):
         st = _lib.load().smla_cache_free(_adr(ref_count), _adr(block_table), _adr(kv_lens), _adr(rows),
                                          rows.shape[0], ctypes.byref(p), _stream_on(stream, dev))
+    _keep(side, ref_count, block_table, kv_lens, rows)
     _check(st, "smla_cache_free")
 
 
@@ -420,16 +475,19 @@ def smla_cache_compact(kv_pages: torch.Tensor, page_size: int, ref_count: torch.
     _ints("block_table_out", table_out, 2, dev)
     if ref_out.shape != ref_count.shape or table_out.shape != block_table.shape:
         raise ValueError("the outputs must have the shapes of ref_count and block_table")
+    side = _side(stream, dev)
     if info is None:
-        info = torch.empty(2, dtype=torch.int32, device=dev)
+        with _memory_of(side):
+            info = torch.empty(2, dtype=torch.int32, device=dev)
     _ints("info", info, 1, dev)
     if info.shape[0] != 2:
         raise ValueError("info must be int32 [2]")
-    ws = _cache_workspace(p, workspace, dev)
+    ws = _cache_workspace(p, workspace, dev, side)
     with _on(dev):
         st = _lib.load().smla_cache_compact(_adr(kv_pages), _adr(ref_count), _adr(block_table), _adr(ref_out),
                                             _adr(table_out), _adr(info), ctypes.byref(p), _adr(ws),
                                             _bytes(ws), _stream_on(stream, dev))
+    _keep(side, kv_pages, ref_count, block_table, ref_out, table_out, info, ws)
     _check(st, "smla_cache_compact")
     return info
 
@@ -489,12 +547,15 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
     if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (H,)
                                or not slopes.is_contiguous() or slopes.device != dev):
         raise ValueError(f"slopes must be contiguous fp32 [H] on {dev}")
+    side = _side(stream, dev)
     if out is None:
-        out = torch.empty((T, H, NOPE), dtype=torch.bfloat16, device=dev)
+        with _memory_of(side):
+            out = torch.empty((T, H, NOPE), dtype=torch.bfloat16, device=dev)
     elif out.shape != (T, H, NOPE) or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be contiguous bf16 [{T}, {H}, {NOPE}] on {dev}")
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        with _memory_of(side):
+            lse = torch.empty((T, H), dtype=torch.float32, device=dev)
     elif lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
         raise ValueError(f"lse must be contiguous fp32 [{T}, {H}] on {dev}")
     if max_kv_tokens is None:
@@ -502,7 +563,8 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
     p = make_chunk_params(B, H, T, page_size, max_pages, kv_pages.shape[0], _row_stride(kv_pages),
                           max_kv_tokens, softmax_scale, logit_cap)
     if workspace is None:
-        workspace = torch.empty(_chunk_bytes(B, H, T, max_kv_tokens), dtype=torch.uint8, device=dev)
+        with _memory_of(side):
+            workspace = torch.empty(_chunk_bytes(B, H, T, max_kv_tokens), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     with _on(dev):
@@ -510,6 +572,7 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
             _adr(q), _adr(kv_pages), _adr(block_table), _adr(cu_q), _adr(kv_lens), _adr(vis_begin),
             _adr(vis_end), _adr(slopes), _adr(out), _adr(lse), ctypes.byref(p), _adr(workspace),
             _bytes(workspace), _stream_on(stream, dev))
+    _keep(side, q, kv_pages, block_table, cu_q, kv_lens, slopes, vis_begin, vis_end, out, lse, workspace)
     _check(st, "smla_chunk_attention")
     return out, lse
 
