@@ -72,8 +72,9 @@ __device__ __forceinline__ Sequence sequence(const ChunkArgs& a, int b) {
   s.len = max(a.kv_lens[b], 0);
   s.first = min(max(c0, 0), a.T);
   s.n = min(max(c1, s.first), a.T) - s.first;
-  // one without cached tokens keeps one block (of zeros) for its tiles to read
-  if (s.n > 0) s.blocks = max(1, (s.len + kChunkBlk - 1) / kChunkBlk);
+  // one without cached tokens keeps one block (of zeros) for its tiles to read; a length may be
+  // as large as its type allows (seq_len below cuts it to the copy)
+  if (s.n > 0) s.blocks = max(1, s.len / kChunkBlk + (s.len % kChunkBlk != 0 ? 1 : 0));
   return s;
 }
 // Its first block in the expanded copy, given the blocks before it, and how many positions

@@ -1,0 +1,62 @@
+"""Chunk attention at the edges of what its arguments allow: masks, lengths and offsets at the
+ends of their type, caps far below the scale, values next to bf16's largest, tables that can
+hold more than a call is told of.  Tolerances are derived in _cache_helpers, or beside the test."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_mla_decode_03_gb300 as m
+
+from _cache_helpers import ROW, SCALE, check_chunk, chunk_reference, dev, pack_rows, random_pool, tables
+
+pytestmark = pytest.mark.gpu
+
+LOW, HIGH = -2 ** 31, 2 ** 31 - 1
+
+
+def _case(lens, n, H, page, seed):
+    """A batch whose sequences bring n tokens each: 1 to 3 of 64 heads go to single SMs, 140 to
+    pairs."""
+    num_pages = sum(-(-L // page) for L in lens) + 2
+    pool, table = random_pool(num_pages, page, seed), tables(lens, page, num_pages, seed)
+    cu = (np.arange(len(lens) + 1) * n).astype(np.int32)
+    q = torch.randn(int(cu[-1]), H, 512, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16).cuda()
+    return q, pool, table, cu, np.array(lens, np.int32)
+
+
+def _call(q, pool, table, page, cu, lens, status=0, **kw):
+    m.smla_device_status(clear=True)
+    kw = {k: dev(v) if isinstance(v, np.ndarray) else v for k, v in kw.items()}
+    kw.setdefault("softmax_scale", SCALE)
+    got = m.smla_chunk_attention(q, pool, dev(table), page, dev(cu), dev(lens), **kw)
+    assert m.smla_device_status(clear=True) == status
+    return got
+
+
+@pytest.mark.parametrize("n", [1, 140])
+@pytest.mark.parametrize("first", [True, False])
+def test_lengths_as_large_as_their_type(n, first):
+    """A length of 2^31 - 1 counts 2^25 blocks: cut to what the bound on the tokens leaves (9 blocks
+    here, 7 behind the other sequence's 2) and reported; the sequence behind it finds no room."""
+    page, H = 64, 64
+    q, pool, table, cu, _ = _case([576, 100] if first else [100, 576], n, H, page, 3)
+    lens = np.array([HIGH, 100] if first else [100, HIGH], np.int32)
+    got = _call(q, pool, table, page, cu, lens, status=-7, max_kv_tokens=448)
+    seen = np.array([576, 100] if first else [100, 448], np.int32)
+    end = np.full(2 * n, HIGH, np.int32)
+    if first:
+        table[1] = -1
+    else:
+        end[:n] = 100 - n + 1 + np.arange(n)
+    check_chunk(got, chunk_reference(q, pool, table, page, cu, seen, begin=np.zeros(2 * n, np.int32), end=end))
+
+
+@pytest.mark.parametrize("n", [1, 140])
+def test_lengths_below_zero_count_as_none(n):
+    page, H = 64, 64
+    q, pool, table, cu, lens = _case([300, 200], n, H, page, 4)
+    for low in (-1, LOW):
+        lens[0] = low
+        got = _call(q, pool, table, page, cu, lens)
+        assert not got[0][:n].any() and torch.isneginf(got[1][:n]).all()
+        check_chunk(got, chunk_reference(q, pool, table, page, cu, np.maximum(lens, 0)))
