@@ -69,11 +69,12 @@ __device__ __forceinline__ int find_last_le(const int32_t* a, int n, int x) {   
 }
 
 // Visible positions [lo, hi) of token t of sequence b (hi <= lo: none), its position in
-// *pos.  len: positions of the sequence that can be seen.
+// *pos.  len: positions of the sequence that can be seen.  Neither is below 0, so that their
+// distance to a block's first position is an int, whatever the masks hold.
 __device__ __forceinline__ void visible(const ChunkArgs& a, int b, int t, int len, int* lo, int* hi, int* pos) {
   *pos = a.kv_lens[b] - (a.cu_q[b + 1] - t);
   *lo = a.vis_begin != nullptr ? max(0, a.vis_begin[t]) : 0;
-  *hi = min(len, a.vis_end != nullptr ? a.vis_end[t] : *pos + 1);
+  *hi = max(0, min(len, a.vis_end != nullptr ? a.vis_end[t] : *pos + 1));
 }
 
 // Pair kernel: tiles of 256 rows on pairs of SMs, over the expanded copy.

@@ -60,3 +60,16 @@ def test_lengths_below_zero_count_as_none(n):
         got = _call(q, pool, table, page, cu, lens)
         assert not got[0][:n].any() and torch.isneginf(got[1][:n]).all()
         check_chunk(got, chunk_reference(q, pool, table, page, cu, np.maximum(lens, 0)))
+
+
+@pytest.mark.parametrize("n,H", [(3, 64), (140, 64), (15, 16), (130, 128)])
+def test_masks_at_the_ends_of_their_type(n, H):
+    """Tokens that see nothing, or everything, by the least and largest numbers there are, in one
+    tile with tokens that see an ordinary part of blocks past the first."""
+    L, page = 520, 64
+    q, pool, table, cu, lens = _case([L], n, H, page, 7 + H)
+    pick = [(0, LOW), (200, 500), (HIGH, HIGH), (LOW, HIGH), (HIGH, LOW), (LOW, LOW), (130, 131)]
+    begin = np.array([pick[j % 7][0] for j in range(n)], np.int32)
+    end = np.array([pick[j % 7][1] for j in range(n)], np.int32)
+    got = _call(q, pool, table, page, cu, lens, vis_begin=begin, vis_end=end)
+    check_chunk(got, chunk_reference(q, pool, table, page, cu, lens, begin=begin, end=end))
