@@ -365,9 +365,9 @@ int smla_cache_compact(void* kv_pages, const int32_t* ref_count, const int32_t* 
  * result divided by the sum of the rounded ones); everything else is held in 32 bits.  The
  * same call gives the same bits every time.
  *
- * cu_q is nondecreasing; one that lists more query rows than q has, and a call with more than
- * 2^30 blocks to go through (64 positions times 64 or 256 query rows each: hours of work),
- * writes nothing and is reported (SMLA_ERR_INDEX_RANGE, SMLA_ERR_UNSUPPORTED_SHAPE).
+ * cu_q is nondecreasing, within 0 .. total_q; with any other (SMLA_ERR_INDEX_RANGE), and with
+ * more than 2^30 blocks to go through (64 positions times 64 or 256 query rows each: hours of
+ * work; SMLA_ERR_UNSUPPORTED_SHAPE), the call writes no result and is reported.
  *
  * Two kernels.  From 256 query rows (tokens times heads) a sequence on average, pairs of SMs
  * work on 256 rows each over a bf16 copy of the cached rows, which the call makes in the

@@ -61,14 +61,17 @@ __device__ long long block_sum(long long v, long long* total, long long* warp_su
   return s - v + (warp > 0 ? warp_sums[warp - 1] : 0);
 }
 
-// What a sequence brings: its entries of q, clamped to it, and its blocks.
+// What a sequence brings: its entries of q, clamped to it, and its blocks.  wrong: its offsets
+// decrease or are not q's, so that its entries may be another's too, or its positions astray.
 struct Sequence {
   int first, n, len, blocks;
+  bool wrong;
 };
 __device__ __forceinline__ Sequence sequence(const ChunkArgs& a, int b) {
-  Sequence s = {0, 0, 0, 0};
+  Sequence s = {0, 0, 0, 0, false};
   if (b >= a.B) return s;
   const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
+  s.wrong = c0 < 0 || c1 < c0 || c1 > a.T;
   s.len = max(a.kv_lens[b], 0);
   s.first = min(max(c0, 0), a.T);
   s.n = min(max(c1, s.first), a.T) - s.first;
@@ -102,9 +105,11 @@ __device__ void make_plan(const ChunkArgs& a, const ChunkPlan& p, int tile_rows,
                           PlanShared& sh) {
   const bool few = a.B <= kPlanSeqs;
   long long tiles = 0, blocks = 0;
+  bool wrong = false;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + static_cast<int>(threadIdx.x);
     const Sequence s = sequence(a, b);
+    wrong |= s.wrong;
     const int nt = (s.n * a.H + tile_rows - 1) / tile_rows;      // total_q * H < 2^30
     long long t_all, b_all;
     const long long t0 = tiles + block_sum(nt, &t_all, sh.sums);
@@ -130,9 +135,9 @@ __device__ void make_plan(const ChunkArgs& a, const ChunkPlan& p, int tile_rows,
     p.seq_base[a.B] = seq_base(p, blocks);
     if (few) sh.tile[a.B] = static_cast<int>(tiles);
   }
-  __syncthreads();
-  // a cu_q that decreases somewhere may list more tiles than the workspace has room for
-  if (tiles > (static_cast<long long>(a.T) * a.H + tile_rows - 1) / tile_rows + a.B) {
+  // Offsets in order and within q give each entry to one sequence at most, and no more tiles than
+  // the workspace has room for; with others the call does nothing.
+  if (__syncthreads_or(wrong)) {
     tiles = 0;
     if (threadIdx.x == 0) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
   }

@@ -73,3 +73,31 @@ def test_masks_at_the_ends_of_their_type(n, H):
     end = np.array([pick[j % 7][1] for j in range(n)], np.int32)
     got = _call(q, pool, table, page, cu, lens, vis_begin=begin, vis_end=end)
     check_chunk(got, chunk_reference(q, pool, table, page, cu, lens, begin=begin, end=end))
+
+
+@pytest.mark.parametrize("T", [2, 140])
+@pytest.mark.parametrize("offsets", [lambda T: [0, T + 10], lambda T: [-3, T], [0, 1, HIGH], [LOW, 0, 1],
+                                     lambda T: [0, T, 0, T], lambda T: [0, T + 1, T], lambda T: [1, 0, T],
+                                     lambda T: [T + 1, T + 1]])
+def test_offsets_out_of_order_or_not_of_q_write_nothing(T, offsets):
+    """Also those few enough to fit the workspace's room for tiles."""
+    H, page, L = 64, 16, 300
+    cu = np.array(offsets(T) if callable(offsets) else offsets, np.int32)
+    B = len(cu) - 1
+    q, pool, table, _, lens = _case([L] * B, T, H, page, 61)
+    q = q[:T].contiguous()
+    out = torch.full((T, H, 448), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, H), 7.0, dtype=torch.float32, device="cuda")
+    _call(q, pool, table, page, cu, lens, status=-7, out=out, lse=lse)
+    assert bool((out == 7).all()) and bool((lse == 7).all())
+
+
+@pytest.mark.parametrize("T", [3, 140])
+def test_offsets_at_the_ends_of_q_are_in_order(T):
+    """Empty sequences before the first entry and behind the last one."""
+    H, page = 64, 16
+    q, pool, table, _, lens = _case([300, 200, 100, 50], T, H, page, 62)
+    q = q[:T].contiguous()
+    cu = np.array([0, 0, T, T, T], np.int32)
+    got = _call(q, pool, table, page, cu, lens)
+    check_chunk(got, chunk_reference(q, pool, table, page, cu, lens))
