@@ -523,12 +523,14 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   const int used = cluster_share(make_int2(total, 0), 0, &low, &sh).x;
   // Holes are the free pages below `used`, movers the pages in use at or past it.  With r
   // pages in use below page p, p - r free ones are: a hole's rank; a mover's is r less the
-  // pages in use below `used`, which the second share counts.
+  // pages in use below `used`, which the second share counts.  rank_of tells the table's entries
+  // apart: the rank of a mover, -1 of a page that nobody owns, 0 of one that stays.
   int r = low.x + rank, kept_here = 0;
   each_page(a.ref, pp, [&](int p, int c) {
     if (p < used) {
       if (c <= 0) a.holes[p - r] = p;
       else ++kept_here;
+      a.rank_of[p] = c > 0 ? 0 : -1;
     } else {
       a.rank_of[p] = c > 0 ? r : -1;
     }
@@ -570,10 +572,10 @@ __global__ void __launch_bounds__(256) compact_move_kernel(const CompactArgs a) 
     int v = a.table[i];
     if (v >= a.num_pages) {
       report(a.status, SMLA_ERR_INDEX_RANGE);
-    } else if (v >= used) {
+    } else if (v >= 0) {
       const int r = a.rank_of[v];
-      if (r >= 0) v = a.holes[r - kept];
-      else report(a.status, SMLA_ERR_INDEX_RANGE);
+      if (r < 0) report(a.status, SMLA_ERR_INDEX_RANGE);
+      else if (v >= used) v = a.holes[r - kept];
     }
     a.table_out[i] = v;
   }
