@@ -66,23 +66,25 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
 // cap tanh(z), z = scale x / cap: up to |z| = 1/4 by tanh's series up to z^9 (the next term is
 // 9e-9 of the first), past it 1 - 2 / (1 + e^(2 z)), whose difference would lose small values'
 // digits (a lse of a few positions was off by 5e-6).  Usual scores are far below the cap, and then
-// only the series is worked out, in x^2 with the powers of scale / cap in its coefficients, two scores
-// an instruction (the mixed batch of 16 heads: 59 us; 72 with one, 58.5 by the exponential form).
+// only the series is worked out, two scores an instruction (the mixed batch of 16 heads: 59.3 us; 71.8
+// with one, 58.5 by the exponential form).  It is one in z itself: with the powers of scale / cap in
+// its coefficients, a product less, they overflow for a cap far below the scale (0 times infinity
+// where the score is 0) and vanish for one far above.  The product costs half a microsecond of that batch.
 struct ScoreMods {
-  float scale2, cap2, inner, most;     // scale, cap, 2 scale / cap, and the x of z = 1/4; cap2 0: none
-  float c3, c5, c7, c9;                // of the series
+  float scale2, cap2, z1, inner, most;     // scale, cap, scale / cap, 2 z1, and the x of z = 1/4; cap2 0: none
   __device__ __forceinline__ explicit ScoreMods(const ChunkArgs& a)
-      : scale2(a.scale * kLog2e), cap2(a.cap * kLog2e), inner(a.cap > 0.f ? 2.f * a.scale * kLog2e / a.cap : 0.f),
-        most(0.25f * a.cap / a.scale) {
-    const float z = a.cap > 0.f ? a.scale / a.cap : 0.f, u = z * z;
-    c3 = -1.f / 3.f * u;
-    c5 = 2.f / 15.f * u * u;
-    c7 = -17.f / 315.f * u * u * u;
-    c9 = 62.f / 2835.f * u * u * u * u;
+      : scale2(a.scale * kLog2e), cap2(0.f), z1(0.f), inner(0.f), most(0.f) {
+    if (a.cap > 0.f) {
+      constexpr float kMost = 3.402823466e38f;      // what passes it stays finite: 0 times it is 0
+      cap2 = fminf(a.cap * kLog2e, 0.5f * kMost);
+      z1 = fminf(a.scale / a.cap, kMost);
+      inner = fminf(2.f * kLog2e * z1, kMost);
+      most = 0.25f / z1;
+    }
   }
   __device__ __forceinline__ void series(float* x, float* y) const {
-    const Two v(*x, *y), u = v * v, s = v * Two(scale2);
-    const Two p = fma2(fma2(fma2(u, Two(c9), Two(c7)), u, Two(c5)), u, Two(c3));
+    const Two v(*x, *y), z = v * Two(z1), u = z * z, s = v * Two(scale2);
+    const Two p = fma2(fma2(fma2(u, Two(62.f / 2835.f), Two(-17.f / 315.f)), u, Two(2.f / 15.f)), u, Two(-1.f / 3.f));
     fma2(s * u, p, s).get(x, y);
   }
   // The scores v of a thread; away(c): slope and distance of score c.

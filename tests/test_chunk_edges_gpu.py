@@ -101,3 +101,44 @@ def test_offsets_at_the_ends_of_q_are_in_order(T):
     cu = np.array([0, 0, T, T, T], np.int32)
     got = _call(q, pool, table, page, cu, lens)
     check_chunk(got, chunk_reference(q, pool, table, page, cu, lens))
+
+
+@pytest.mark.parametrize("scale,cap", [(1.0, 1e-30), (1.0, 1e-7), (1.0, 1e30), (2.0 ** 33, 5.0), (2.0 ** 33, 30.0),
+                                       (2.0 ** 33, 1e-7), (2.0 ** -33, 5.0), (2.0 ** 60, 1e-3), (2.0 ** -40, 1e4)])
+@pytest.mark.parametrize("B,n", [(64, 1), (2, 32)])
+def test_caps_far_from_the_scale(B, n, scale, cap):
+    """Tokens that see one position, whose score is one exact product (the scales are powers of two):
+    lse is the capped score, also where the score is 0 and where scale / cap has no eighth power in
+    32 bits.  Relative error: past z = 1/4 the exponential form, 1 - 2 / (1 + e): two steps of 2^-23
+    each of the exponential and of the quotient, which are 0.47 e and 0.75 there, over tanh(1/4) =
+    0.245: 5 * 2^-22; the series 9e-9; a dozen 32-bit roundings of 2^-24 and the conversions to and
+    from log2: below 2^-19 together."""
+    H, page = 16, 4
+    rows = torch.zeros((B * page, ROW), dtype=torch.uint8, device="cuda")
+    rows[:, 448:455] = 127
+    rows[:, 0] = 0x38                                       # e4m3 1.0
+    lens = np.full(B, n, np.int32)
+    table = np.arange(B, dtype=np.int32)[:, None].repeat(-(-n // page), axis=1)
+    cu = (np.arange(B + 1) * n).astype(np.int32)
+    half = torch.logspace(-3, 2, B * n * H // 2, dtype=torch.float64) * (cap / scale)
+    x = torch.cat([half, -half])
+    x[::5] = 0
+    x = x[torch.randperm(x.numel(), generator=torch.Generator().manual_seed(1))]
+    q = torch.zeros((B * n, H, 512), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = x.view(B * n, H).to(torch.bfloat16).cuda()
+    out, lse = _call(q, rows, table, page, cu, lens, softmax_scale=scale, logit_cap=cap,
+                     vis_begin=np.zeros(B * n, np.int32), vis_end=np.ones(B * n, np.int32))
+    want = cap * torch.tanh(q[:, :, 0].double() * scale / cap)
+    assert ((lse.double() - want).abs() <= 2.0 ** -19 * want.abs()).all()
+    assert torch.equal(out[:, :, 0].float(), torch.ones_like(lse)) and not out[:, :, 1:].any()
+
+
+@pytest.mark.parametrize("cap", [1e-7, 3e38])
+@pytest.mark.parametrize("n", [1, 140])
+def test_the_least_and_the_largest_caps(n, cap):
+    """All positions weigh the same, or the cap does nothing; a query of zeros among the others."""
+    q, pool, table, cu, lens = _case([400], n, 64, 64, 17)
+    q[0, 5] = 0
+    got = _call(q, pool, table, 64, cu, lens, logit_cap=cap)
+    ref = chunk_reference(q, pool, table, 64, cu, lens, SCALE, 1e-7 if cap < 1 else 0.0)
+    check_chunk(got, ref)
