@@ -359,9 +359,11 @@ int smla_cache_compact(void* kv_pages, const int32_t* ref_count, const int32_t* 
  * (SMLA_ERR_INDEX_RANGE).  out and lse of entries outside [cu_q[0], cu_q[batch]) are left
  * as they were.
  *
- * A cached row with a NaN, an infinite rope value or a scale byte above 246 (values past
- * bf16) counts as not finite: tokens that see it get NaN in out and lse, all others are not
- * touched by it.  The attention weights are rounded to bf16 for the value product (and the
+ * A cached row with a NaN, an infinite rope value or a nope value that times its scale passes
+ * bf16's largest counts as not finite: tokens that see it get NaN in out and lse, all others
+ * are not touched by it.  The value sums are held in 32 bits before they are divided by the
+ * weights', which go up to 2^8 each: cached values within a few powers of two of bf16's largest
+ * may overflow them.  The attention weights are rounded to bf16 for the value product (and the
  * result divided by the sum of the rounded ones); everything else is held in 32 bits.  The
  * same call gives the same bits every time.
  *

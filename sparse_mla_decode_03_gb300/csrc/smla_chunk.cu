@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
             o[2 * k + 1] = in[j][k].y;
           }
         }
-        bool bad = lane < 28 && sc[j] > kMaxScaleByte;
+        bool bad = false;      // a NaN (a scale byte of 255 makes NaN), or past bf16's largest value
 #pragma unroll
         for (int k = 0; k < 8; ++k) bad |= not_finite(o[k]);
         if (__any_sync(0xffffffffu, bad)) {

@@ -12,9 +12,6 @@
 namespace smla {
 
 constexpr int kChunkBlk = 64;     // positions of a block
-// Largest scale byte of a cached row whose values bf16 holds (448 * 2^119): rows past it
-// count as not finite.
-constexpr int kMaxScaleByte = 246;
 
 struct ChunkArgs {
   const uint16_t* q;

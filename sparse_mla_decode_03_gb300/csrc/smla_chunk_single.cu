@@ -483,11 +483,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < kRows; ++j) {
             const uint2 wa = again(j, 8 * lane), wb = again(j, 256 + 8 * lane), wc = again(j, 512 + 8 * min(lane, 8));
             const uint32_t sx = __shfl_sync(0xffffffffu, wb.x, 24), sy = __shfl_sync(0xffffffffu, wb.y, 24);
-            const uint32_t s = max((sx >> sh) & 0xffu, lane < 24 ? (sy >> sh) & 0xffu : 0u);
-            const bool bad = ((nan_bits(wa.x) | nan_bits(wa.y)) & 0x80808080u) |
-                             ((((wb.x & mb) + ab) | ((wb.y & mb) + ab)) & tb) |
-                             ((rope_bits(wc.x) | rope_bits(wc.y)) & 0x80008000u) | (s > kMaxScaleByte ? 1u : 0u);
-            dropped |= __any_sync(0xffffffffu, bad) ? 1u << j : 0u;
+            // a NaN (a scale byte of 255 makes NaN), or past bf16's largest value: seen in the results
+            const uint4 oa = expand8_any(wa, (sx >> sh) & 0xffu);
+            const uint4 ob = lane < 24 ? expand8_any(wb, (sy >> sh) & 0xffu)
+                                       : lane > 24 ? make_uint4(wb.x, wb.y, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t bad = rope_bits(oa.x) | rope_bits(oa.y) | rope_bits(oa.z) | rope_bits(oa.w) | rope_bits(ob.x) |
+                                 rope_bits(ob.y) | rope_bits(ob.z) | rope_bits(ob.w) | rope_bits(wc.x) | rope_bits(wc.y);
+            dropped |= __any_sync(0xffffffffu, (bad & 0x80008000u) != 0) ? 1u << j : 0u;
           }
         }
         const uint32_t parity = ((n >> 1) - 1) & 1;

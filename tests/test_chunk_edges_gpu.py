@@ -133,6 +133,42 @@ def test_caps_far_from_the_scale(B, n, scale, cap):
     assert torch.equal(out[:, :, 0].float(), torch.ones_like(lse)) and not out[:, :, 1:].any()
 
 
+@pytest.mark.parametrize("n,H", [(2, 64), (40, 64), (15, 16)])
+def test_values_next_to_the_largest_of_bf16(n, H):
+    """1.8 * 2^127 in a group is stored with the scale byte 247, and values up to 240 * 2^120 are
+    numbers: rows of any scale byte count as finite while all their values are.  One block, so that
+    no weight passes 1, and one such row a group, so that the sums stay below 2^128."""
+    L, page = 50, 64
+    q, pool, table, cu, lens = _case([L], n, H, page, 23)
+    q[:, :, 64:320] = 0
+    x = torch.randn(L, 512, generator=torch.Generator().manual_seed(4))
+    x[:, 64:320] = 0
+    x[7, 70], x[9, 130] = 1.8 * 2.0 ** 127, -1.85 * 2.0 ** 127
+    rows = pack_rows(x.to(torch.bfloat16))
+    assert rows[7, 449] == 247 and rows[9, 450] == 247
+    rows[11, 451], rows[11, 192:256] = 254, 0x3F                # 1.875 * 2^127
+    rows[11, 200:230] = 0
+    rows[12, 452] = 254                                         # zeros with the largest scale
+    at = torch.as_tensor(table[0].astype(np.int64)[np.arange(L) // page] * page + np.arange(L) % page, device="cuda")
+    pool[at] = dev(rows)
+    got = _call(q, pool, table, page, cu, lens)
+    check_chunk(got, chunk_reference(q, pool, table, page, cu, lens))
+    # one step more, and the row is not finite: who sees it gets NaN
+    begin, end = np.arange(n, dtype=np.int32), np.full(n, L, np.int32)
+    for row, col, group, byte, code in ((7, 70, 449, 247, 0x78), (12, 256, 452, 254, 0x40), (12, 257, 452, 248, 0x70)):
+        bad = rows.copy()
+        bad[row, col], bad[row, group] = code, byte
+        pool[at] = dev(bad)
+        out, lse = _call(q, pool, table, page, cu, lens, vis_begin=begin, vis_end=end)
+        sees = torch.arange(n, device="cuda") <= row
+        assert torch.isnan(out[sees].float()).all() and torch.isnan(lse[sees]).all()
+        clean = pool.clone()
+        clean[at[row]] = 0
+        ref = chunk_reference(q, clean, table, page, cu, lens, begin=begin, end=end)
+        ref[0][sees] = ref[1][sees] = float("nan")              # (not compared)
+        check_chunk((out, lse), ref)
+
+
 @pytest.mark.parametrize("cap", [1e-7, 3e38])
 @pytest.mark.parametrize("n", [1, 140])
 def test_the_least_and_the_largest_caps(n, cap):
