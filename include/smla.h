@@ -277,7 +277,8 @@ typedef struct smla_cache_params {
  * integer with a <= 448 * 2^e (byte e + 127, kept in 1 .. 254; 127 where a = 0), and the
  * values x * 2^-e rounded to e4m3 (to nearest, ties to even); the padding byte is 0 and
  * the rope is copied.  Infinities and NaN become e4m3 NaN, the scale is that of the
- * group's finite values, and SMLA_ERR_RANGE is recorded.  A token whose position is
+ * group's finite values, and SMLA_ERR_RANGE is recorded; so it is for values that round to
+ * 2^128 (from 1.9375 * 2^127 on), which are stored as that.  A token whose position is
  * negative, past the table, or on an unmapped page is not written
  * (SMLA_ERR_INDEX_RANGE).  Entries of kv outside [cu_q[0], cu_q[num_seqs]) are ignored,
  * as are rows that no token lands on.  No two tokens of a call may share a position's

@@ -117,6 +117,8 @@ __device__ __forceinline__ void write_row(const AppendArgs& a, uint8_t* dst, con
   // and whether its mantissa exceeds 1.75: exact, no logarithm.
   int byte = static_cast<int>(top >> 7) - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
   byte = top == 0 ? 127 : min(max(byte, 1), 254);
+  // from 1.9375 * 2^127 on (halfway from 240 to 256 in the scale 2^120) the stored value is 2^128
+  if (top >= 0x7f78u && lane < 28) report(a.status, SMLA_ERR_RANGE);
   // 2^(127 - byte) as a float (byte 254: the subnormal 2^-127)
   const float inv = __uint_as_float(byte < 254 ? static_cast<uint32_t>(254 - byte) << 23 : 0x00400000u);
   if (lane < 28) {

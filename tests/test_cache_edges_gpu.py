@@ -5,7 +5,7 @@ import torch
 
 import sparse_mla_decode_03_gb300 as m
 
-from _cache_helpers import PageModel, check_pages, dev, random_pool
+from _cache_helpers import PageModel, ROW, check_pages, dev, pack_rows, random_pool
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,23 @@ def test_compact_copies_and_reports_entries_that_name_no_page_in_use(num_pages, 
     assert m.smla_device_status(clear=True) == (0 if stale is None else -7)
     assert info.cpu().tolist() == [n, k]
     check_pages(model, outs.get("ref_count_out", r), outs.get("block_table_out", t), None)
+
+
+@pytest.mark.parametrize("bits,status", [(0x7F77, 0), (0x7F78, -8), (0x7F7F, -8), (0x7F60, 0), (0x7F61, 0)])
+@pytest.mark.parametrize("sign", [0, 0x8000])
+@pytest.mark.parametrize("col", [0, 63, 100, 447, 448, 511])
+def test_append_reports_values_that_round_past_the_largest(bits, status, sign, col):
+    """1.9375 * 2^127 (bf16 0x7f78) is halfway between 240 and 256 in the scale 2^120 and rounds to
+    the even 256: 2^128.  A rope value is copied, and never out of range."""
+    kv = torch.randn(3, 512, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    kv[1].view(torch.int16)[col] = (bits | sign) - (65536 if sign else 0)
+    pool = torch.zeros((4, ROW), dtype=torch.uint8, device="cuda")
+    m.smla_device_status(clear=True)
+    m.smla_cache_append(kv.cuda(), pool, dev(np.zeros((1, 1), np.int32)), 4, dev(np.array([0, 3], np.int32)),
+                        dev(np.array([3], np.int32)))
+    assert m.smla_device_status(clear=True) == (status if col < 448 else 0)
+    want = pack_rows(kv)
+    assert np.array_equal(pool[:3].cpu().numpy(), want) and not pool[3].any()
+    if col < 448:
+        top = want[1, col] & 0x7F
+        assert (top >= 0x78) == (status != 0) if want[1, 448 + col // 64] == 247 else status == 0
