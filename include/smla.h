@@ -374,7 +374,7 @@ int smla_cache_compact(void* kv_pages, const int32_t* ref_count, const int32_t* 
  *
  * Two kernels.  From 256 query rows (tokens times heads) a sequence on average, pairs of SMs
  * work on 256 rows each over a bf16 copy of the cached rows, which the call makes in the
- * workspace (1,040 bytes a token of max_kv_tokens); below, single SMs work on 64 rows each and
+ * workspace (1,025 bytes a token of max_kv_tokens); below, single SMs work on 64 rows each and
  * expand the rows themselves.  Either way the work is cut evenly over the GPU and partial
  * results are joined.  Calls whose kernels may overlap (two streams, two graphs) need a
  * workspace each; calls that follow one another in a stream may share one.  As with the

@@ -24,6 +24,7 @@ DEFAULT_SCALE = 1.0 / math.sqrt(512)
 NOPE = 448
 QK = 512
 ROW_BYTES = 584
+MAX_KV_TOKENS = 1 << 30      # the largest bound that smla_chunk_attention takes
 
 
 class SmlaError(RuntimeError):
@@ -526,8 +527,9 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
     """Attention of the chunk's tokens q bf16 [T, H, 512] (sequence b's are
     q[cu_q[b]:cu_q[b + 1]], the last ones of its kv_lens[b] cached tokens) over the paged
     cache, causal unless vis_begin / vis_end say otherwise.  max_kv_tokens bounds the sum of
-    kv_lens (default: what the table can hold) and sizes the workspace.  Returns (out bf16
-    [T, H, 448], lse fp32 [T, H])."""
+    kv_lens (default: what the table can hold, 2^30 at most); from 256 rows of q (tokens times
+    heads) a sequence on it sizes the workspace, 1,025 bytes a token, so a caller with a wide
+    table gives the bound that it knows.  Returns (out bf16 [T, H, 448], lse fp32 [T, H])."""
     _pool(kv_pages, page_size)
     dev = kv_pages.device
     if q.dim() != 3 or q.shape[2] != QK or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.device != dev:
@@ -559,7 +561,7 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
     elif lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
         raise ValueError(f"lse must be contiguous fp32 [{T}, {H}] on {dev}")
     if max_kv_tokens is None:
-        max_kv_tokens = B * max_pages * page_size
+        max_kv_tokens = min(B * max_pages * page_size, MAX_KV_TOKENS)
     p = make_chunk_params(B, H, T, page_size, max_pages, kv_pages.shape[0], _row_stride(kv_pages),
                           max_kv_tokens, softmax_scale, logit_cap)
     if workspace is None:

@@ -133,6 +133,18 @@ def test_caps_far_from_the_scale(B, n, scale, cap):
     assert torch.equal(out[:, :, 0].float(), torch.ones_like(lse)) and not out[:, :, 1:].any()
 
 
+@pytest.mark.parametrize("H", [16, 64])
+def test_tables_that_hold_more_than_the_largest_bound(H):
+    """The default bound is what the table can hold, kept within what the call takes."""
+    page, L = 4096, [5000, 300]
+    q, pool, table, cu, lens = _case(L, 1, H, page, 71)
+    wide = np.full((2, (1 << 17) + 1), -1, np.int32)          # 2 * 131,073 pages of 4,096: 2^30 and 8,192
+    wide[:, :table.shape[1]] = table
+    assert wide.size * page > 1 << 30
+    got = _call(q, pool, wide, page, cu, lens)
+    check_chunk(got, chunk_reference(q, pool, table, page, cu, lens))
+
+
 @pytest.mark.parametrize("n,H", [(2, 64), (40, 64), (15, 16)])
 def test_values_next_to_the_largest_of_bf16(n, H):
     """1.8 * 2^127 in a group is stored with the scale byte 247, and values up to 240 * 2^120 are
