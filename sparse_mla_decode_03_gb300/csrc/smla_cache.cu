@@ -227,31 +227,31 @@ __device__ int2 cluster_share(int2 mine, int slot, int2* before, PlanShared* sh)
 }
 
 // This CTA's part [first, last) of n things, and within it the thread's part, a run of a
-// multiple of 4: ranks then need one block-wide sum, whatever the length.
+// multiple of 4: ranks then need one block-wide sum, whatever the length.  Unsigned, since the ends
+// of a part of nearly 2^31 things are rounded up past it.
 struct Part {
-  int first, last, run0, run1;
+  uint32_t run0, run1;
 };
-__device__ __forceinline__ Part part_of(int n) {
-  const int rank = static_cast<int>(cg::this_cluster().block_rank());
-  const int per = ((n + kPlanCtas - 1) / kPlanCtas + 3) & ~3;
+__device__ __forceinline__ Part part_of(uint32_t n) {
+  const uint32_t rank = cg::this_cluster().block_rank();
+  const uint32_t per = ((n + kPlanCtas - 1) / kPlanCtas + 3) & ~3u;
+  const uint32_t first = min(n, rank * per), last = min(n, first + per);
+  const uint32_t run = ((last - first + kPlanThreads - 1) / kPlanThreads + 3) & ~3u;
   Part p;
-  p.first = static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(rank) * per));
-  p.last = min(n, p.first + per);
-  const int run = ((p.last - p.first + kPlanThreads - 1) / kPlanThreads + 3) & ~3;
-  p.run0 = min(p.last, p.first + static_cast<int>(threadIdx.x) * run);
-  p.run1 = min(p.last, p.run0 + run);
+  p.run0 = min(last, first + threadIdx.x * run);
+  p.run1 = min(last, p.run0 + run);
   return p;
 }
 // f(page, count) for the pages of the thread's run.
 template <class F>
 __device__ __forceinline__ void each_page(const int32_t* ref, const Part& p, F f) {
-  for (int q = p.run0; q < p.run1; q += 4) {
+  for (uint32_t q = p.run0; q < p.run1; q += 4) {
     int c[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) c[k] = q + k < p.run1 ? __ldcg(ref + q + k) : 0;
+    for (uint32_t k = 0; k < 4; ++k) c[k] = q + k < p.run1 ? __ldcg(ref + q + k) : 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (q + k < p.run1) f(q + k, c[k]);
+    for (uint32_t k = 0; k < 4; ++k)
+      if (q + k < p.run1) f(static_cast<int>(q + k), c[k]);
   }
 }
 __device__ __forceinline__ int count_free(const int32_t* ref, const Part& p) {
@@ -371,7 +371,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   const Part ip = part_of(a.n), pp = part_of(a.num_pages);
   int free_total, need_total, mine = 0;
   const int free_rank = block_rank(count_free(a.ref, pp), &free_total, &sh);
-  for (int i = ip.run0; i < ip.run1; ++i) {
+  for (int i = static_cast<int>(ip.run0); i < static_cast<int>(ip.run1); ++i) {
     mine += fork_takes(a, i, fork_length(a, i));
   }
   const int need_rank = block_rank(mine, &need_total, &sh);
@@ -381,7 +381,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   take_free(a.ref, pp, low.y + free_rank, got, a.list);
   cg::this_cluster().sync();
   int k = low.x + need_rank;
-  for (int i = ip.run0; i < ip.run1; ++i) {
+  for (int i = static_cast<int>(ip.run0); i < static_cast<int>(ip.run1); ++i) {
     const int len = fork_length(a, i);
     int f = len < 0 ? kSkip : kNotNeeded;
     if (fork_takes(a, i, len)) {

@@ -58,3 +58,23 @@ def test_append_reports_values_that_round_past_the_largest(bits, status, sign, c
     if col < 448:
         top = want[1, col] & 0x7F
         assert (top >= 0x78) == (status != 0) if want[1, 448 + col // 64] == 247 else status == 0
+
+
+@pytest.mark.parametrize("short", [0, 6, 7, 2000])
+def test_reserve_from_as_many_pages_as_an_int_counts(short):
+    """2^31 - 1 pages: the parts of the counts that the blocks and threads of the plan take end
+    next to the largest int."""
+    n = 2 ** 31 - 1 - short
+    ref = torch.ones(n, dtype=torch.int32, device="cuda")
+    free = [5, 2 ** 28 + 1, 2 ** 30 + 7, n - 1030, n - 2, n - 1]
+    ref[torch.tensor(free, device="cuda")] = 0
+    table = dev(np.full((2, 4), -1, np.int32))
+    m.smla_device_status(clear=True)
+    m.smla_cache_reserve(1, ref, table, dev(np.array([3, 2], np.int32)))
+    assert m.smla_device_status(clear=True) == 0
+    assert table.cpu().tolist() == [free[:3] + [-1], free[3:5] + [-1, -1]]
+    assert ref[-1].item() == 0 and ref[torch.tensor(free[:5], device="cuda")].tolist() == [1] * 5
+    m.smla_cache_reserve(1, ref, table, dev(np.array([4, 3], np.int32)))
+    assert m.smla_device_status(clear=True) == -11
+    assert table.cpu().tolist() == [free[:3] + [free[5]], free[3:5] + [-1, -1]]
+    assert int(ref.min()) == 1 and int(ref.max()) == 1
