@@ -296,8 +296,9 @@ int smla_cache_workspace_size(const smla_cache_params* c, size_t* bytes);
  * Maps pages until sequence r holds target_lens[r] tokens: every unmapped entry among
  * the first ceil(target_lens[r] / page_size) of row r gets the next free page (in the
  * order of the table, row by row) with count 1.  Mapped entries stay, kv_lens is not
- * touched.  A target past the table is cut to it (SMLA_ERR_INDEX_RANGE); entries that
- * find no free page stay unmapped (SMLA_ERR_POOL_EXHAUSTED).
+ * touched.  The table has fewer than 2^31 entries (SMLA_ERR_UNSUPPORTED_SHAPE).  A target past
+ * the table is cut to it (SMLA_ERR_INDEX_RANGE); entries that find no free page stay unmapped
+ * (SMLA_ERR_POOL_EXHAUSTED).
  */
 int smla_cache_reserve(int32_t* ref_count, int32_t* block_table, const int32_t* target_lens,
                        const smla_cache_params* c, void* workspace, size_t workspace_bytes,

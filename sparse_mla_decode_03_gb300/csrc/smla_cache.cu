@@ -670,6 +670,8 @@ int smla_cache_reserve(int32_t* ref_count, int32_t* block_table, const int32_t* 
   int st = check_cache(c);
   if (st != SMLA_OK) return st;
   if (!ints_ok(ref_count) || !ints_ok(block_table) || !ints_ok(target_lens)) return SMLA_ERR_INVALID_ARG;
+  // entries that want a page are counted in ints
+  if (static_cast<int64_t>(c->num_seqs) * c->max_pages >= (int64_t{1} << 31)) return SMLA_ERR_UNSUPPORTED_SHAPE;
   st = check_workspace(c, workspace, workspace_bytes);
   if (st != SMLA_OK) return st;
   int* status = nullptr;
