@@ -56,8 +56,8 @@ L2_TURNOVER = 3           # L2 capacities read between two reads of one layer
 # one ncu capture of the decode kernel on the batch-32 workload.  They describe the
 # kernel source they were taken on: with any other source the field is null.
 TRAFFIC_KERNEL_SRC = "sparse_mla_decode_03_gb300/csrc/smla_decode.cu"
-TRAFFIC_SRC_SHA256_16 = "d623f299c93b8b75"
-TRAFFIC_BYTES = 47548160 + 100352
+TRAFFIC_SRC_SHA256_16 = "09de9143f11ac394"
+TRAFFIC_BYTES = 47547904 + 69632
 FALLBACK_HBM_GBS = 6800.0
 FALLBACK_BF16_TFLOPS = 1900.0
 
