@@ -54,17 +54,18 @@ def _side(stream: Optional[torch.cuda.Stream], device: torch.device) -> Optional
     return stream
 
 
-def _memory_of(side: Optional[torch.cuda.Stream]):
-    """Where a call that runs on `side` allocates: there, so that its results and workspace are not
-    handed out, before or after it, to work of the current stream that does not wait for it."""
-    return _SAME if side is None else torch.cuda.stream(side)
+def _empty(side: Optional[torch.cuda.Stream], shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """What a call that runs on `side` allocates is that stream's memory: it is not handed out, before
+    or after the call, to work of the current stream that does not wait for it."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _keep(side: Optional[torch.cuda.Stream], *tensors: Optional[torch.Tensor]) -> None:
+def _keep(side: torch.cuda.Stream, *tensors: Optional[torch.Tensor]) -> None:
     """A call on `side` uses these tensors, and the caller the results on the current stream: the
     memory of one that is dropped is not handed out again before both have come past this point."""
-    if side is None:
-        return
     for t in tensors:
         if t is not None:
             t.record_stream(side)
@@ -134,18 +135,18 @@ def sparse_mla_decode(q: torch.Tensor, kv_cache: torch.Tensor, indices: torch.Te
     B, H = p.batch, p.num_heads
     need = smla_workspace_size(p, num_splits)
     side = _side(stream, q.device)
-    with _memory_of(side):
-        if out is None:
-            out = torch.empty((B, H, NOPE), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = _empty(side, (B, H, NOPE), torch.bfloat16, q.device)
+    if lse is None:
+        lse = _empty(side, (B, H), torch.float32, q.device)
+    if workspace is None:
+        workspace = _empty(side, need, torch.uint8, q.device)
     lib = _lib.load()
     st = lib.sparse_mla_decode(_ptr(q), _ptr(kv_cache), _ptr(indices), _ptr(out), _ptr(lse),
                                ctypes.byref(p), num_splits, _ptr(workspace),
                                workspace.numel() * workspace.element_size(), _stream(stream))
-    _keep(side, q, kv_cache, indices, out, lse, workspace)
+    if side is not None:
+        _keep(side, q, kv_cache, indices, out, lse, workspace)
     _check(st, "sparse_mla_decode")
     return out, lse
 
@@ -160,15 +161,15 @@ def sparse_mla_decode_split(q: torch.Tensor, kv_cache: torch.Tensor, indices: to
     p = _params_from(q, kv_cache, indices, softmax_scale)
     B, H, S = p.batch, p.num_heads, num_splits
     side = _side(stream, q.device)
-    with _memory_of(side):
-        if o_part is None:
-            o_part = torch.empty((B, H, S, NOPE), dtype=torch.float32, device=q.device)
-        if lse_part is None:
-            lse_part = torch.empty((B, H, S), dtype=torch.float32, device=q.device)
+    if o_part is None:
+        o_part = _empty(side, (B, H, S, NOPE), torch.float32, q.device)
+    if lse_part is None:
+        lse_part = _empty(side, (B, H, S), torch.float32, q.device)
     lib = _lib.load()
     st = lib.sparse_mla_decode_split(_ptr(q), _ptr(kv_cache), _ptr(indices), ctypes.byref(p), S,
                                      _ptr(o_part), _ptr(lse_part), _stream(stream))
-    _keep(side, q, kv_cache, indices, o_part, lse_part)
+    if side is not None:
+        _keep(side, q, kv_cache, indices, o_part, lse_part)
     _check(st, "sparse_mla_decode_split")
     return o_part, lse_part
 
@@ -186,15 +187,15 @@ def sparse_mla_combine(o_part: torch.Tensor, lse_part: torch.Tensor,
         raise ValueError("partials must be contiguous")
     B, H, S, _ = o_part.shape
     side = _side(stream, o_part.device)
-    with _memory_of(side):
-        if out is None:
-            out = torch.empty((B, H, NOPE), dtype=torch.bfloat16, device=o_part.device)
-        if lse is None:
-            lse = torch.empty((B, H), dtype=torch.float32, device=o_part.device)
+    if out is None:
+        out = _empty(side, (B, H, NOPE), torch.bfloat16, o_part.device)
+    if lse is None:
+        lse = _empty(side, (B, H), torch.float32, o_part.device)
     lib = _lib.load()
     st = lib.sparse_mla_combine(_ptr(o_part), _ptr(lse_part), B, H, S, _ptr(out), _ptr(lse),
                                 _stream(stream))
-    _keep(side, o_part, lse_part, out, lse)
+    if side is not None:
+        _keep(side, o_part, lse_part, out, lse)
     _check(st, "sparse_mla_combine")
     return out, lse
 
@@ -210,15 +211,15 @@ def sparse_mla_decode_noalloc(q: torch.Tensor, kv_cache: torch.Tensor, indices: 
     to keep the call itself free of allocations."""
     p = _params_from(q, kv_cache, indices, softmax_scale)
     side = _side(stream, q.device)
-    with _memory_of(side):
-        if out is None:
-            out = torch.empty((p.batch, p.num_heads, NOPE), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((p.batch, p.num_heads), dtype=torch.float32, device=q.device)
+    if out is None:
+        out = _empty(side, (p.batch, p.num_heads, NOPE), torch.bfloat16, q.device)
+    if lse is None:
+        lse = _empty(side, (p.batch, p.num_heads), torch.float32, q.device)
     st = _lib.load().sparse_mla_decode_noalloc(_ptr(q), _ptr(kv_cache), _ptr(indices), _ptr(out),
                                                _ptr(lse), ctypes.byref(p), num_splits,
                                                _stream(stream))
-    _keep(side, q, kv_cache, indices, out, lse)
+    if side is not None:
+        _keep(side, q, kv_cache, indices, out, lse)
     _check(st, "sparse_mla_decode_noalloc")
     return out, lse
 
@@ -247,18 +248,18 @@ def sparse_mla_decode_paged(q: torch.Tensor, kv_pages: torch.Tensor, block_table
         raise ValueError("block_table must be a contiguous CUDA int32 [B, max_pages] tensor")
     need = smla_paged_workspace_size(p, num_splits)
     side = _side(stream, q.device)
-    with _memory_of(side):
-        if out is None:
-            out = torch.empty((p.batch, p.num_heads, NOPE), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((p.batch, p.num_heads), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = _empty(side, (p.batch, p.num_heads, NOPE), torch.bfloat16, q.device)
+    if lse is None:
+        lse = _empty(side, (p.batch, p.num_heads), torch.float32, q.device)
+    if workspace is None:
+        workspace = _empty(side, need, torch.uint8, q.device)
     st = _lib.load().sparse_mla_decode_paged(
         _ptr(q), _ptr(kv_pages), _ptr(block_table), block_table.shape[1], page_size,
         _ptr(indices), _ptr(out), _ptr(lse), ctypes.byref(p), num_splits, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
-    _keep(side, q, kv_pages, block_table, indices, out, lse, workspace)
+    if side is not None:
+        _keep(side, q, kv_pages, block_table, indices, out, lse, workspace)
     _check(st, "sparse_mla_decode_paged")
     return out, lse
 
@@ -273,14 +274,14 @@ def sparse_mla_decode_simt(q: torch.Tensor, kv_cache: torch.Tensor, indices: tor
     tensor-core path).  Returns (out bf16 [B, H, 448], lse fp32 [B, H])."""
     p = _params_from(q, kv_cache, indices, softmax_scale)
     side = _side(stream, q.device)
-    with _memory_of(side):
-        if out is None:
-            out = torch.empty((p.batch, p.num_heads, NOPE), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((p.batch, p.num_heads), dtype=torch.float32, device=q.device)
+    if out is None:
+        out = _empty(side, (p.batch, p.num_heads, NOPE), torch.bfloat16, q.device)
+    if lse is None:
+        lse = _empty(side, (p.batch, p.num_heads), torch.float32, q.device)
     st = _lib.load().sparse_mla_decode_simt(_ptr(q), _ptr(kv_cache), _ptr(indices), _ptr(out),
                                             _ptr(lse), ctypes.byref(p), _stream(stream))
-    _keep(side, q, kv_cache, indices, out, lse)
+    if side is not None:
+        _keep(side, q, kv_cache, indices, out, lse)
     _check(st, "sparse_mla_decode_simt")
     return out, lse
 
@@ -349,8 +350,7 @@ def _cache_bytes(num_pages: int, num_seqs: int) -> int:
 def _cache_workspace(p: _lib.SmlaCacheParams, workspace: Optional[torch.Tensor], device: torch.device,
                      side: Optional[torch.cuda.Stream]) -> torch.Tensor:
     if workspace is None:
-        with _memory_of(side):
-            return torch.empty(_cache_bytes(p.num_pages, p.num_seqs), dtype=torch.uint8, device=device)
+        return _empty(side, _cache_bytes(p.num_pages, p.num_seqs), torch.uint8, device)
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace
@@ -383,7 +383,8 @@ def smla_cache_append(kv: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
         st = _lib.load().smla_cache_append(_adr(kv), stride, kv.shape[0], _adr(kv_pages), _adr(block_table),
                                            _adr(cu_q), _adr(kv_lens), ctypes.byref(p),
                                            _stream_on(stream, dev))
-    _keep(side, kv, kv_pages, block_table, cu_q, kv_lens)
+    if side is not None:
+        _keep(side, kv, kv_pages, block_table, cu_q, kv_lens)
     _check(st, "smla_cache_append")
 
 
@@ -403,7 +404,8 @@ def smla_cache_reserve(page_size: int, ref_count: torch.Tensor, block_table: tor
     with _on(dev):
         st = _lib.load().smla_cache_reserve(_adr(ref_count), _adr(block_table), _adr(target_lens),
                                             ctypes.byref(p), _adr(ws), _bytes(ws), _stream_on(stream, dev))
-    _keep(side, ref_count, block_table, target_lens, ws)
+    if side is not None:
+        _keep(side, ref_count, block_table, target_lens, ws)
     _check(st, "smla_cache_reserve")
 
 
@@ -438,7 +440,8 @@ def smla_cache_fork(kv_pages: torch.Tensor, page_size: int, ref_count: torch.Ten
         st = _lib.load().smla_cache_fork(_adr(kv_pages), _adr(ref_count), _adr(block_table), _adr(kv_lens),
                                          _adr(parents), _adr(children), parents.shape[0], ctypes.byref(p),
                                          _adr(ws), _bytes(ws), _stream_on(stream, dev))
-    _keep(side, kv_pages, ref_count, block_table, kv_lens, parents, children, ws)
+    if side is not None:
+        _keep(side, kv_pages, ref_count, block_table, kv_lens, parents, children, ws)
     _check(st, "smla_cache_fork")
 
 
@@ -457,7 +460,8 @@ def smla_cache_free(ref_count: torch.Tensor, block_table: torch.Tensor, kv_lens:
     with _on(dev):
         st = _lib.load().smla_cache_free(_adr(ref_count), _adr(block_table), _adr(kv_lens), _adr(rows),
                                          rows.shape[0], ctypes.byref(p), _stream_on(stream, dev))
-    _keep(side, ref_count, block_table, kv_lens, rows)
+    if side is not None:
+        _keep(side, ref_count, block_table, kv_lens, rows)
     _check(st, "smla_cache_free")
 
 
@@ -478,8 +482,7 @@ def smla_cache_compact(kv_pages: torch.Tensor, page_size: int, ref_count: torch.
         raise ValueError("the outputs must have the shapes of ref_count and block_table")
     side = _side(stream, dev)
     if info is None:
-        with _memory_of(side):
-            info = torch.empty(2, dtype=torch.int32, device=dev)
+        info = _empty(side, 2, torch.int32, dev)
     _ints("info", info, 1, dev)
     if info.shape[0] != 2:
         raise ValueError("info must be int32 [2]")
@@ -488,7 +491,8 @@ def smla_cache_compact(kv_pages: torch.Tensor, page_size: int, ref_count: torch.
         st = _lib.load().smla_cache_compact(_adr(kv_pages), _adr(ref_count), _adr(block_table), _adr(ref_out),
                                             _adr(table_out), _adr(info), ctypes.byref(p), _adr(ws),
                                             _bytes(ws), _stream_on(stream, dev))
-    _keep(side, kv_pages, ref_count, block_table, ref_out, table_out, info, ws)
+    if side is not None:
+        _keep(side, kv_pages, ref_count, block_table, ref_out, table_out, info, ws)
     _check(st, "smla_cache_compact")
     return info
 
@@ -551,13 +555,11 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
         raise ValueError(f"slopes must be contiguous fp32 [H] on {dev}")
     side = _side(stream, dev)
     if out is None:
-        with _memory_of(side):
-            out = torch.empty((T, H, NOPE), dtype=torch.bfloat16, device=dev)
+        out = _empty(side, (T, H, NOPE), torch.bfloat16, dev)
     elif out.shape != (T, H, NOPE) or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be contiguous bf16 [{T}, {H}, {NOPE}] on {dev}")
     if lse is None:
-        with _memory_of(side):
-            lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        lse = _empty(side, (T, H), torch.float32, dev)
     elif lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
         raise ValueError(f"lse must be contiguous fp32 [{T}, {H}] on {dev}")
     if max_kv_tokens is None:
@@ -565,8 +567,7 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
     p = make_chunk_params(B, H, T, page_size, max_pages, kv_pages.shape[0], _row_stride(kv_pages),
                           max_kv_tokens, softmax_scale, logit_cap)
     if workspace is None:
-        with _memory_of(side):
-            workspace = torch.empty(_chunk_bytes(B, H, T, max_kv_tokens), dtype=torch.uint8, device=dev)
+        workspace = _empty(side, _chunk_bytes(B, H, T, max_kv_tokens), torch.uint8, dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     with _on(dev):
@@ -574,7 +575,8 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
             _adr(q), _adr(kv_pages), _adr(block_table), _adr(cu_q), _adr(kv_lens), _adr(vis_begin),
             _adr(vis_end), _adr(slopes), _adr(out), _adr(lse), ctypes.byref(p), _adr(workspace),
             _bytes(workspace), _stream_on(stream, dev))
-    _keep(side, q, kv_pages, block_table, cu_q, kv_lens, slopes, vis_begin, vis_end, out, lse, workspace)
+    if side is not None:
+        _keep(side, q, kv_pages, block_table, cu_q, kv_lens, slopes, vis_begin, vis_end, out, lse, workspace)
     _check(st, "smla_chunk_attention")
     return out, lse
 
