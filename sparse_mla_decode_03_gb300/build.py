@@ -1,7 +1,8 @@
 """Builds libsmla.so (the C-ABI library) in-tree with nvcc for sm_103a, and its debug
 twin libsmla_debug.so (the same sources with SMLA_DEBUG: device-side bounds checks
-of every computed shared-memory address and gathered row, reported as
-SMLA_ERR_INTERNAL; no trap).
+of every computed shared-memory address and gathered row of the decode kernels,
+reported as SMLA_ERR_INTERNAL; no trap.  The cache and chunk kernels check their
+ids, rows and offsets in every build and have none besides).
 
 Each .cu file is compiled in parallel, then linked into a shared library next to
 this file.  Usage: ``python -m sparse_mla_decode_03_gb300.build [-v]``."""

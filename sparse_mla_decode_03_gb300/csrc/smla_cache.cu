@@ -7,8 +7,8 @@
 // one thread-block cluster of 8 CTAs (hardware cluster barriers between the phases, a
 // CTA's slice of the pages or table each), so a call is one launch, plus one wide launch
 // where rows of the cache move.  Page calls are bound by launches and by the trips to memory
-// and cluster barriers of a plan: free 4 us, fork 9 + 5 (512 children 9 + 8), reserve 6 (of
-// 576 rows and 32,768 pages 13), compaction's plan 7 (32,768 pages 10).
+// and cluster barriers of a plan: free 4 us, fork 10 + 5.5 (512 children 11 + 8), reserve 6 (of
+// 528 rows and 32,768 pages 12.5), compaction's plan 7.5 (32,768 pages 11).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -20,7 +20,7 @@ __device__ __forceinline__ float ue8m0_value(uint32_t e) {
 }
 
 // ---------------------------------------------------------------------------
-// Plan: one CTA, 6 us cold (a launch, three dependent loads, block-wide sums), within the
+// Plan: one CTA, 6 to 7 us cold (a launch, three dependent loads, block-wide sums), within the
 // expansion's launch where there is one.  Equal shares of the block line, whatever the lengths
 // and masks: no SM waits for the longest sequence.
 // ---------------------------------------------------------------------------
@@ -521,6 +521,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // Which kernel: pairs once a sequence brings a full tile of 256 rows on average.  Single against
 // pairs, 16 sequences of 16,000 and 64 heads: 1 token 90 and 184 us, 2 tokens 126 and 161, 4
 // tokens 214 and 160; 16 tokens of 16 heads over 8,000 93 and 88; 1 token of 128 heads 60 and 70.
+// All of batches whose sequences bring the same number of tokens; mixed ones are not measured.
 bool use_pairs(const smla_chunk_params* p) {
   return static_cast<int64_t>(p->total_q) * p->num_heads >= static_cast<int64_t>(kPairRows) * p->batch;
 }

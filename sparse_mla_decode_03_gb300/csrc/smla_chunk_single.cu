@@ -14,8 +14,8 @@
 // softmax about 800.  Expansion, scores, softmax and value product of a block follow one
 // another, and the scores and O fill tensor memory, so two blocks in two buffers overlap in
 // part only: about 5,100 cycles a block.  32 single tokens of 64 heads over 8,192 positions
-// take 76 us (153 MB: 2.0 TB/s, 30 % of the copy rate; tensor pipe 40 % busy, integer pipe
-// 53 %), with plan and merge 86 us; two tokens of 16 heads over 131,072 take 68 and 78 us.
+// take 77 us (153 MB: 2.0 TB/s, 29 % of the copy rate; tensor pipe 40 % busy, integer pipe
+// 53 %), with plan and merge 87 us; two tokens of 16 heads over 131,072 take 69 and 79 us.
 // Measured and not kept: f16 operands (96 us against 93 then), two sets of 8 expanding warps
 // (93..105), the next block's rows read before this one's expansion (110: spills), through
 // shared memory (92 against 85: past the carve-out step) or half a row earlier (87), one lane
