@@ -197,3 +197,33 @@ def test_decode_on_a_busy_stream_while_the_current_one_allocates():
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     del junk
+
+
+@pytest.mark.parametrize("ns", [[1, 3], [150, 60]])
+def test_calls_on_a_stream_that_a_capture_forks_into(ns):
+    """In a captured graph a call may run on a stream that was forked from the capture's, and
+    allocate there; the graph's replays, and calls beside them, are right."""
+    page, H = 64, 64
+    lens = [900, 500]
+    num_pages = sum(-(-L // page) for L in lens) + 2
+    pool, table = random_pool(num_pages, page, 5), tables(lens, page, num_pages, 5)
+    cu = np.concatenate([[0], np.cumsum(ns)]).astype(np.int32)
+    q = torch.randn(int(cu[-1]), H, 512, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    args = (q, pool, dev(table), page, dev(cu), dev(np.array(lens, np.int32)))
+    want = m.smla_chunk_attention(*args, softmax_scale=SCALE, max_kv_tokens=sum(lens))
+    check_chunk(want, chunk_reference(q, pool, table, page, cu, np.array(lens, np.int32)))
+    s = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.wait_stream(torch.cuda.current_stream())
+        here = m.smla_chunk_attention(*args, softmax_scale=SCALE, max_kv_tokens=sum(lens))
+        there = m.smla_chunk_attention(*args, softmax_scale=SCALE, max_kv_tokens=sum(lens), stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+    for _ in range(3):
+        for t in here + there:
+            t.fill_(float("nan"))
+        g.replay()
+        beside = m.smla_chunk_attention(*args, softmax_scale=SCALE, max_kv_tokens=sum(lens))
+        torch.cuda.synchronize()
+        for got in (here, there, beside):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
