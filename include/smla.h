@@ -26,6 +26,17 @@
  * the same quantities per split of the index list, and the combine merges them:
  *     lse = ln sum_s exp(lse_s),   out = sum_s exp(lse_s - lse) * out_s.
  *
+ * Rows of 4-bit values.  A cache whose rows are 368 .. 512 bytes apart (a multiple of 16) holds rows
+ * of 368 bytes; the paged-cache calls, smla_chunk_attention, sparse_mla_decode and
+ * sparse_mla_decode_paged take such caches (16-byte aligned) as they take the others:
+ *
+ *     [0,224)   e2m1 nope values (1 sign, 2 exponent, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), eight
+ *               to a little-endian 4-byte word: of word i, nibble p is column 8 i + 2 p and nibble
+ *               p + 4 column 8 i + 2 p + 1, p = 0 .. 3
+ *     [224,238) UE8M0 scale of each 32-column group: k_nope[c] = e2m1(c) * 2^(s[c/32]-127)
+ *     [238,240) padding (never used)
+ *     [240,368) 64 bf16 rope values
+ *
  * Conventions common to every entry point:
  *   - All tensor pointers are DEVICE pointers owned by the caller; the library keeps
  *     no pointer after a call returns and allocates no device or host memory.
@@ -89,9 +100,17 @@ typedef struct smla_params {
   int32_t topk;           /* k: index slots per query, 1 .. 65536                      */
   int32_t reserved;       /* must be 0                                                 */
   int64_t num_rows;       /* rows in kv_cache, >= 1                                    */
-  int64_t kv_row_stride;  /* bytes between consecutive rows, >= 584, multiple of 8      */
+  int64_t kv_row_stride;  /* bytes between consecutive rows, >= 584, multiple of 8; or
+                             368 .. 512, multiple of 16: rows of 4-bit values           */
   float softmax_scale;    /* multiplies q.k (e.g. 1/sqrt(512)), finite and > 0          */
 } smla_params;
+
+/* Rows of 4-bit values: sparse_mla_decode and sparse_mla_decode_paged with num_splits 0 and a
+ * workspace of smla_workspace_size(p, 0) (smla_paged_workspace_size(p, 0)) bytes; any other num_splits
+ * is SMLA_ERR_INVALID_ARG.  They run on the kernel of smla_chunk_attention for few query rows, so that
+ * what its comment says of roundings, of cached rows that are not finite and of workspaces holds, and
+ * values need only fit bf16.  The plan, split, no-alloc and SIMT entry points take 8-bit rows only
+ * (SMLA_ERR_UNSUPPORTED_SHAPE). */
 
 /* Number of splits the library would use for `p` on the current device (its plan:
  * enough CTAs to fill the device's SMs, splits aligned to 16 index slots).  */
@@ -124,7 +143,7 @@ int smla_decode_plan(const smla_params* p, int32_t num_splits, int32_t* splits, 
  * once via the runtime); a driver without it, or a cache or q the encoder rejects,
  * gives SMLA_ERR_CUDA and nothing is launched.
  *   q          bf16  [B, H, 512]  (448 nope | 64 rope), 16-byte aligned
- *   kv_cache   uint8 [num_rows, kv_row_stride], 16-byte aligned, rows as above
+ *   kv_cache   uint8 [num_rows, kv_row_stride], 16-byte aligned, rows as above (8- or 4-bit)
  *   indices    int32 [B, topk]    row ids; < 0 = masked slot (shared by all heads)
  *   out        bf16  [B, H, 448]  16-byte aligned
  *   lse        fp32  [B, H]       natural-log LSE of the scaled scores (-inf if empty)
@@ -263,7 +282,8 @@ typedef struct smla_cache_params {
   int32_t page_size;      /* rows per page, >= 1                                        */
   int32_t num_seqs;       /* rows of block_table, 1 .. 65535                            */
   int32_t max_pages;      /* columns of block_table, >= 1                               */
-  int64_t kv_row_stride;  /* bytes between consecutive rows, >= 584, multiple of 8      */
+  int64_t kv_row_stride;  /* bytes between consecutive rows, >= 584, multiple of 8; or
+                             368 .. 512, multiple of 16: rows of 4-bit values           */
 } smla_cache_params;
 
 /*
@@ -283,10 +303,55 @@ typedef struct smla_cache_params {
  * (SMLA_ERR_INDEX_RANGE).  Entries of kv outside [cu_q[0], cu_q[num_seqs]) are ignored,
  * as are rows that no token lands on.  No two tokens of a call may share a position's
  * row.  total_tokens 0 is allowed (nothing is launched).
+ *
+ * Rows of 4-bit values (by kv_row_stride; kv_pages 16-byte aligned): groups of 32, e the least integer
+ * with a <= 6 * 2^e, the values rounded to e2m1 (to nearest, ties to even).  A group with an infinity
+ * or a NaN is stored as zeros with the scale byte 255 (NaN; SMLA_ERR_RANGE); values from 1.75 * 2^127 on
+ * round to 2^128, are stored as that and reported too.
  */
 int smla_cache_append(const void* kv, int64_t kv_token_stride, int32_t total_tokens,
                       void* kv_pages, const int32_t* block_table, const int32_t* cu_q,
                       const int32_t* kv_lens, const smla_cache_params* c, smla_stream_t stream);
+
+/*
+ * The same with the position rotation on the way.  With (cos, sin) of pair i at the token's position
+ * pos = kv_lens[b] - n + j from the table, each pair (x, y) of the token's 64 rope columns becomes
+ *     (x cos - y sin, x sin + y cos)
+ * in 32 bits, rounded to bf16 once; pairs are columns (2 i, 2 i + 1) or (i, i + 32), i = 0 .. 31.  The
+ * token's row is then written as smla_cache_append writes it, and its queries' rope columns q_rope are
+ * rotated the same way into columns 448 .. 511 of q, whose other columns are not touched.
+ * A token whose position is negative or past the table of rotations is skipped, row and queries
+ * (SMLA_ERR_INDEX_RANGE); one whose position has no place in the cache has its queries rotated.
+ */
+enum smla_rotary_pairing { SMLA_ROTARY_NEIGHBOURS = 0, SMLA_ROTARY_HALVES = 1 };
+typedef struct smla_rotary_params {
+  const float* table;           /* fp32 [table_rows, 64]: cosines of the 32 pairs, then sines; device,
+                                   16-byte aligned                                      */
+  const void* q_rope;           /* bf16 [total_tokens, num_heads, 64], 16-byte aligned  */
+  void* q;                      /* bf16 [total_tokens, num_heads, 512], 16-byte aligned; q_rope and q
+                                   share no memory                                      */
+  int64_t table_rows;           /* >= 1                                                 */
+  int64_t q_rope_token_stride, q_rope_head_stride;  /* elements, >= 0, multiples of 8   */
+  int64_t q_token_stride, q_head_stride;            /* the same; no two (token, head) rows share memory */
+  int32_t num_heads;            /* >= 0; 0: no queries (q_rope and q may be NULL).
+                                   total_tokens * (1 + ceil(num_heads / 16)) < 2^31     */
+  int32_t pairing;              /* smla_rotary_pairing                                  */
+  int32_t reserved;             /* must be 0                                            */
+} smla_rotary_params;
+int smla_cache_append_rotary(const void* kv, int64_t kv_token_stride, int32_t total_tokens,
+                             void* kv_pages, const int32_t* block_table, const int32_t* cu_q,
+                             const int32_t* kv_lens, const smla_cache_params* c,
+                             const smla_rotary_params* r, smla_stream_t stream);
+
+/*
+ * Reads rows back: out bf16 [total_tokens, 512] (448 nope | 64 rope, out_token_stride elements apart,
+ * >= 512, a multiple of 8; 16-byte aligned) receives the values that the rows of the same tokens hold,
+ * rounded to bf16 (exact but for values past its range), addressed as smla_cache_append addresses them.  Tokens without a row
+ * (SMLA_ERR_INDEX_RANGE) and entries outside [cu_q[0], cu_q[num_seqs]) are left as they were.
+ */
+int smla_cache_read(const void* kv_pages, const int32_t* block_table, const int32_t* cu_q,
+                    const int32_t* kv_lens, void* out, int64_t out_token_stride, int32_t total_tokens,
+                    const smla_cache_params* c, smla_stream_t stream);
 
 /* Workspace bytes of smla_cache_reserve, _fork and _compact (256-byte aligned; contents
  * on entry do not matter; calls whose kernels may overlap need one each). */
@@ -345,6 +410,65 @@ int smla_cache_compact(void* kv_pages, const int32_t* ref_count, const int32_t* 
                        smla_stream_t stream);
 
 /*
+ * Reorders sequences by parents, in place: row r of the table goes on from what row parents[r]
+ * held when the call began.  parents int32 [num_seqs]; several rows may have the same parent, and a
+ * row may be a parent and another's child at once (beams that go on from a selection).
+ *   - The lowest child of a row takes it over as it is: table entries (those behind its length
+ *     too) and length.
+ *   - Its other children share the full pages (count + 1), get a copy of a last page that is partly
+ *     filled in the lowest free page (in the order of the rows), nothing behind it, and the length.
+ *     Entries that name no page of the pool are copied as they are (those past it:
+ *     SMLA_ERR_INDEX_RANGE).  A length outside the table counts as cut to it (SMLA_ERR_INDEX_RANGE).
+ *   - The pages of a row without a child go back first (count - 1 each, skipped and reported as in
+ *     smla_cache_free), so that copies may take them.  A child that finds no free page is left
+ *     empty (SMLA_ERR_POOL_EXHAUSTED).
+ *   - parents[r] < 0 leaves row r empty, as does one past the rows (SMLA_ERR_INDEX_RANGE).
+ * A row that is its own lowest child is not touched.  workspace: smla_cache_reorder_workspace_size
+ * bytes, 256-byte aligned; contents on entry do not matter; calls whose kernels may overlap need one each.
+ */
+int smla_cache_reorder_workspace_size(const smla_cache_params* c, size_t* bytes);
+int smla_cache_reorder(void* kv_pages, int32_t* ref_count, int32_t* block_table, int32_t* kv_lens,
+                       const int32_t* parents, const smla_cache_params* c, void* workspace,
+                       size_t workspace_bytes, smla_stream_t stream);
+
+/*
+ * Selection over beams and vocabulary.  Row r = g * beams + j holds the logits x of beam j of
+ * group g, whose score (sum of log-probabilities) is c = scores[g][j].  Token v of it has the value
+ *     c + (x[v] - M) - ln sum_u exp(x[u] - M),     M = max_u x[u],
+ * and the num_out largest values of each group are returned in descending order: the row that each goes
+ * on from (parents, r: what smla_cache_reorder takes when num_out = beams), its token and its value.
+ * Equal values: the lower beam first, then the lower token.  A beam with finished[r] != 0 has one
+ * candidate, (end_token, c), and its logits are not read.
+ * A logit of -infinity is no candidate, nor is any of a beam whose score is -infinity; where a group has
+ * fewer than num_out candidates, the rest are (-1, -1, -infinity).  A beam with a NaN or a +infinity
+ * among its logits, or a score that is NaN or +infinity, has none (SMLA_ERR_RANGE).
+ * Logits are compared as they are; sums are held in 32 bits and values in 64 (a value is off by about
+ * 1e-7 before it is rounded).  The same call gives the same bits every time.
+ */
+enum smla_logits_type { SMLA_FLOAT32 = 0, SMLA_BFLOAT16 = 1, SMLA_FLOAT16 = 2 };
+typedef struct smla_beam_params {
+  int32_t groups;         /* G >= 1, G * beams <= 65535                                 */
+  int32_t beams;          /* rows of a group, 1 .. 64                                   */
+  int32_t vocab;          /* V: logits of a row, 1 .. 2^24                              */
+  int32_t num_out;        /* 1 .. 64                                                    */
+  int64_t row_stride;     /* elements between rows, >= vocab; rows may begin anywhere   */
+  int32_t logits_type;    /* smla_logits_type                                           */
+  int32_t end_token;      /* 0 .. V - 1 (not read without finished)                     */
+  int32_t reserved;       /* must be 0                                                  */
+} smla_beam_params;
+int smla_beam_workspace_size(const smla_beam_params* p, size_t* bytes);
+
+/*   logits      [G * beams, V], aligned to its elements   scores     fp32 [G, beams]
+ *   finished    uint8 [G * beams] or NULL
+ *   parents, tokens  int32 [G, num_out]                   out_scores fp32 [G, num_out]
+ *   workspace   >= smla_beam_workspace_size(p) bytes, 256-byte aligned; contents on entry do not matter
+ * The results overlap no input.  Calls whose kernels may overlap need a workspace each.
+ */
+int smla_beam_select(const void* logits, const float* scores, const uint8_t* finished, int32_t* parents,
+                     int32_t* tokens, float* out_scores, const smla_beam_params* p, void* workspace,
+                     size_t workspace_bytes, smla_stream_t stream);
+
+/*
  * Attention of a chunk of new tokens over the paged cache (which already holds their
  * rows): prefill chunks, drafted tokens to verify, dense single-token decode, mixed in
  * one call.  Token t of sequence b (t in cu_q[b] .. cu_q[b + 1] - 1, position
@@ -361,7 +485,7 @@ int smla_cache_compact(void* kv_pages, const int32_t* ref_count, const int32_t* 
  * (SMLA_ERR_INDEX_RANGE).  out and lse of entries outside [cu_q[0], cu_q[batch]) are left
  * as they were.
  *
- * A cached row with a NaN, an infinite rope value or a nope value that times its scale passes
+ * A cached row with a NaN (a scale byte of 255 makes one), an infinite rope value or a nope value that times its scale passes
  * bf16's largest counts as not finite: tokens that see it get NaN in out and lse, all others
  * are not touched by it.  The value sums are held in 32 bits before they are divided by the
  * weights', which go up to 2^8 each: cached values within a few powers of two of bf16's largest
@@ -389,7 +513,8 @@ typedef struct smla_chunk_params {
   int32_t max_pages;      /* columns of block_table, >= 1                               */
   int32_t reserved;       /* must be 0                                                  */
   int64_t num_rows;       /* rows of the pool, 1 .. 2^31                                */
-  int64_t kv_row_stride;  /* bytes between rows, >= 584, multiple of 8, < 2^31          */
+  int64_t kv_row_stride;  /* bytes between rows, >= 584, multiple of 8, < 2^31; or 368 .. 512,
+                             multiple of 16: rows of 4-bit values                       */
   int64_t max_kv_tokens;  /* 1 .. 2^30: the caller's bound on the sum of kv_lens; it sizes the
                              workspace of pairs of SMs (see above).  Tokens past it are masked and reported
                              (SMLA_ERR_INDEX_RANGE)                                     */

@@ -41,6 +41,12 @@ EXPORTED = (
     "smla_cache_fork",
     "smla_cache_free",
     "smla_cache_compact",
+    "smla_cache_append_rotary",
+    "smla_cache_read",
+    "smla_cache_reorder_workspace_size",
+    "smla_cache_reorder",
+    "smla_beam_workspace_size",
+    "smla_beam_select",
     "smla_chunk_workspace_size",
     "smla_chunk_attention",
     "smla_status_string",
@@ -87,6 +93,35 @@ class SmlaChunkParams(ctypes.Structure):
     ]
 
 
+class SmlaRotaryParams(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("q_rope", ctypes.c_void_p),
+        ("q", ctypes.c_void_p),
+        ("table_rows", ctypes.c_int64),
+        ("q_rope_token_stride", ctypes.c_int64),
+        ("q_rope_head_stride", ctypes.c_int64),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("num_heads", ctypes.c_int32),
+        ("pairing", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class SmlaBeamParams(ctypes.Structure):
+    _fields_ = [
+        ("groups", ctypes.c_int32),
+        ("beams", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("num_out", ctypes.c_int32),
+        ("row_stride", ctypes.c_int64),
+        ("logits_type", ctypes.c_int32),
+        ("end_token", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 _lib = None
 _debug_lib = None
 
@@ -130,6 +165,13 @@ def _open(path: str) -> ctypes.CDLL:
     lib.smla_cache_fork.argtypes = [vp, vp, vp, vp, vp, vp, i32, C, vp, sz, vp]
     lib.smla_cache_free.argtypes = [vp, vp, vp, vp, i32, C, vp]
     lib.smla_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, C, vp, sz, vp]
+    R, S = ctypes.POINTER(SmlaRotaryParams), ctypes.POINTER(SmlaBeamParams)
+    lib.smla_cache_append_rotary.argtypes = [vp, i64, i32, vp, vp, vp, vp, C, R, vp]
+    lib.smla_cache_read.argtypes = [vp, vp, vp, vp, vp, i64, i32, C, vp]
+    lib.smla_cache_reorder_workspace_size.argtypes = [C, ctypes.POINTER(sz)]
+    lib.smla_cache_reorder.argtypes = [vp, vp, vp, vp, vp, C, vp, sz, vp]
+    lib.smla_beam_workspace_size.argtypes = [S, ctypes.POINTER(sz)]
+    lib.smla_beam_select.argtypes = [vp, vp, vp, vp, vp, vp, S, vp, sz, vp]
     lib.smla_chunk_workspace_size.argtypes = [K, ctypes.POINTER(sz)]
     lib.smla_chunk_attention.argtypes = [vp] * 10 + [K, vp, sz, vp]
     lib.smla_status_string.argtypes = [ctypes.c_int]

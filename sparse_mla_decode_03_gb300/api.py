@@ -24,6 +24,8 @@ DEFAULT_SCALE = 1.0 / math.sqrt(512)
 NOPE = 448
 QK = 512
 ROW_BYTES = 584
+ROW4_BYTES = 368             # rows of 4-bit values, at most MAX_ROW4_STRIDE apart
+MAX_ROW4_STRIDE = 512
 MAX_KV_TOKENS = 1 << 30      # the largest bound that smla_chunk_attention takes
 
 
@@ -87,6 +89,8 @@ def _params_from(q: torch.Tensor, kv_cache: torch.Tensor, indices: torch.Tensor,
         raise ValueError("q must be bf16 [B, H, 512]")
     if kv_cache.dim() != 2 or kv_cache.dtype != torch.uint8 or kv_cache.stride(1) != 1:
         raise ValueError("kv_cache must be uint8 [num_rows, stride>=584] with unit column stride")
+    if kv_cache.stride(0) <= MAX_ROW4_STRIDE and kv_cache.shape[1] < ROW4_BYTES:
+        raise ValueError("kv_cache rows of 4-bit values must hold 368 bytes")
     if indices.dim() != 2 or indices.dtype != torch.int32 or indices.shape[0] != q.shape[0]:
         raise ValueError("indices must be int32 [B, topk]")
     for name, t in (("q", q), ("indices", indices)):
@@ -130,7 +134,8 @@ def sparse_mla_decode(q: torch.Tensor, kv_cache: torch.Tensor, indices: torch.Te
                       workspace: Optional[torch.Tensor] = None,
                       stream: Optional[torch.cuda.Stream] = None
                       ) -> Tuple[torch.Tensor, torch.Tensor]:
-    """Whole decode step.  Returns (out bf16 [B, H, 448], lse fp32 [B, H])."""
+    """Whole decode step.  Returns (out bf16 [B, H, 448], lse fp32 [B, H]).  kv_cache: rows of 584
+    bytes, or of 368 (4-bit values; num_splits 0)."""
     p = _params_from(q, kv_cache, indices, softmax_scale)
     B, H = p.batch, p.num_heads
     need = smla_workspace_size(p, num_splits)
@@ -297,8 +302,9 @@ def _ints(name: str, t: torch.Tensor, dims: int, device: torch.device) -> None:
 def _pool(kv_pages: torch.Tensor, page_size: int) -> None:
     if kv_pages.dim() != 2 or kv_pages.dtype != torch.uint8 or kv_pages.stride(1) != 1:
         raise ValueError("kv_pages must be uint8 [num_rows, stride>=584] with unit column stride")
-    if kv_pages.shape[1] < ROW_BYTES:
-        raise ValueError("kv_pages rows must hold 584 bytes")
+    if kv_pages.shape[1] < ROW_BYTES and (kv_pages.shape[1] < ROW4_BYTES or kv_pages.shape[0] > 1
+                                          and kv_pages.stride(0) > MAX_ROW4_STRIDE):
+        raise ValueError("kv_pages rows must hold 584 bytes, or 368 at most 512 bytes apart (4-bit values)")
     if not kv_pages.is_cuda:
         raise ValueError("kv_pages must be a CUDA tensor")
     if page_size < 1 or kv_pages.shape[0] < page_size:
@@ -326,7 +332,9 @@ def _on(device: torch.device):
 
 def _row_stride(kv_pages: torch.Tensor) -> int:
     """Bytes between rows (a single row has no neighbour: any stride will do)."""
-    return kv_pages.stride(0) if kv_pages.shape[0] > 1 else ROW_BYTES
+    if kv_pages.shape[0] > 1:
+        return kv_pages.stride(0)
+    return ROW_BYTES if kv_pages.shape[1] >= ROW_BYTES else ROW4_BYTES
 
 
 def make_cache_params(num_pages: int, page_size: int, num_seqs: int, max_pages: int,
@@ -360,24 +368,35 @@ def _bytes(t: torch.Tensor) -> int:
     return t.numel() * t.element_size()
 
 
-def smla_cache_append(kv: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
-                      page_size: int, cu_q: torch.Tensor, kv_lens: torch.Tensor,
-                      stream: Optional[torch.cuda.Stream] = None) -> None:
-    """Quantises new tokens and writes their rows.  kv bf16 [T, 512]; sequence b's are
-    kv[cu_q[b]:cu_q[b + 1]], the last ones of its kv_lens[b] tokens."""
+def _token_rows(name: str, kv: torch.Tensor, device: torch.device) -> int:
+    """Checks bf16 [T, 512]; elements between its rows."""
+    if kv.dim() != 2 or kv.shape[1] != QK or kv.dtype != torch.bfloat16 or kv.stride(1) != 1 or kv.device != device:
+        raise ValueError(f"{name} must be bf16 [T, 512] with unit column stride on {device}")
+    return kv.stride(0) if kv.shape[0] > 1 else QK
+
+
+def _token_places(kv_pages: torch.Tensor, page_size: int, block_table: torch.Tensor, cu_q: torch.Tensor,
+                  kv_lens: torch.Tensor) -> _lib.SmlaCacheParams:
     _pool(kv_pages, page_size)
     dev = kv_pages.device
-    if kv.dim() != 2 or kv.shape[1] != QK or kv.dtype != torch.bfloat16 or kv.stride(1) != 1 or kv.device != dev:
-        raise ValueError(f"kv must be bf16 [T, 512] with unit column stride on {dev}")
     _ints("block_table", block_table, 2, dev)
     _ints("cu_q", cu_q, 1, dev)
     _ints("kv_lens", kv_lens, 1, dev)
     B = block_table.shape[0]
     if cu_q.shape[0] != B + 1 or kv_lens.shape[0] != B:
         raise ValueError("cu_q must be [B + 1] and kv_lens [B] for a block_table of B rows")
-    p = make_cache_params(kv_pages.shape[0] // page_size, page_size, B, block_table.shape[1],
-                          _row_stride(kv_pages))
-    stride = kv.stride(0) if kv.shape[0] > 1 else QK
+    return make_cache_params(kv_pages.shape[0] // page_size, page_size, B, block_table.shape[1],
+                             _row_stride(kv_pages))
+
+
+def smla_cache_append(kv: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
+                      page_size: int, cu_q: torch.Tensor, kv_lens: torch.Tensor,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantises new tokens and writes their rows (8- or 4-bit, as kv_pages has them).  kv bf16 [T, 512];
+    sequence b's are kv[cu_q[b]:cu_q[b + 1]], the last ones of its kv_lens[b] tokens."""
+    p = _token_places(kv_pages, page_size, block_table, cu_q, kv_lens)
+    dev = kv_pages.device
+    stride = _token_rows("kv", kv, dev)
     side = _side(stream, dev)
     with _on(dev):
         st = _lib.load().smla_cache_append(_adr(kv), stride, kv.shape[0], _adr(kv_pages), _adr(block_table),
@@ -386,6 +405,69 @@ def smla_cache_append(kv: torch.Tensor, kv_pages: torch.Tensor, block_table: tor
     if side is not None:
         _keep(side, kv, kv_pages, block_table, cu_q, kv_lens)
     _check(st, "smla_cache_append")
+
+
+def smla_cache_append_rotary(kv: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
+                             page_size: int, cu_q: torch.Tensor, kv_lens: torch.Tensor,
+                             rotary: torch.Tensor, interleaved: bool = True,
+                             q_rope: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                             stream: Optional[torch.cuda.Stream] = None) -> None:
+    """smla_cache_append with the position rotation on the way: the rope columns of kv by the token's
+    row of rotary fp32 [positions, 64] (cosines of the 32 pairs, then sines), pairs (2 i, 2 i + 1) if
+    interleaved, else (i, i + 32).  With q_rope bf16 [T, H, 64] the queries' rope columns are rotated
+    too, into q[:, :, 448:] of q bf16 [T, H, 512]."""
+    p = _token_places(kv_pages, page_size, block_table, cu_q, kv_lens)
+    dev = kv_pages.device
+    stride = _token_rows("kv", kv, dev)
+    if (rotary.dim() != 2 or rotary.shape[1] != QK - NOPE or rotary.dtype != torch.float32 or rotary.device != dev
+            or not rotary.is_contiguous()):
+        raise ValueError(f"rotary must be contiguous fp32 [positions, 64] on {dev}")
+    if (q_rope is None) != (q is None):
+        raise ValueError("q_rope and q come together")
+    T, H, strides = kv.shape[0], 0, (0, 0, 0, 0)
+    if q is not None:
+        for name, t, width in (("q_rope", q_rope, QK - NOPE), ("q", q, QK)):
+            if (t.dim() != 3 or t.shape[0] != T or t.shape[2] != width or t.dtype != torch.bfloat16
+                    or t.stride(2) != 1 or t.device != dev):
+                raise ValueError(f"{name} must be bf16 [{T}, H, {width}] with unit column stride on {dev}")
+        H = q.shape[1]
+        if q_rope.shape[1] != H:
+            raise ValueError("q_rope and q must have as many heads")
+        if (T > 1 and (q.stride(0) == 0 or abs(q.stride(0)) < QK)) or (H > 1 and q.stride(1) < QK):
+            raise ValueError("the rows of q must not overlap")
+        strides = tuple(t.stride(i) if t.shape[i] > 1 else 0 for t in (q_rope, q) for i in (0, 1))
+    r = _lib.SmlaRotaryParams(_adr(rotary), _adr(q_rope), _adr(q), rotary.shape[0], *strides, H,
+                              0 if interleaved else 1, 0)
+    side = _side(stream, dev)
+    with _on(dev):
+        st = _lib.load().smla_cache_append_rotary(_adr(kv), stride, T, _adr(kv_pages), _adr(block_table), _adr(cu_q),
+                                                  _adr(kv_lens), ctypes.byref(p), ctypes.byref(r),
+                                                  _stream_on(stream, dev))
+    if side is not None:
+        _keep(side, kv, kv_pages, block_table, cu_q, kv_lens, rotary, q_rope, q)
+    _check(st, "smla_cache_append_rotary")
+
+
+def smla_cache_read(kv_pages: torch.Tensor, block_table: torch.Tensor, page_size: int, cu_q: torch.Tensor,
+                    kv_lens: torch.Tensor, total_tokens: int, out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The values of the rows that smla_cache_append writes for the same cu_q and kv_lens: bf16
+    [total_tokens, 512].  Entries without a row are left as they were (in a new out: undefined)."""
+    p = _token_places(kv_pages, page_size, block_table, cu_q, kv_lens)
+    dev = kv_pages.device
+    side = _side(stream, dev)
+    if out is None:
+        out = _empty(side, (total_tokens, QK), torch.bfloat16, dev)
+    stride = _token_rows("out", out, dev)
+    if out.shape[0] != total_tokens:
+        raise ValueError(f"out must be bf16 [{total_tokens}, 512]")
+    with _on(dev):
+        st = _lib.load().smla_cache_read(_adr(kv_pages), _adr(block_table), _adr(cu_q), _adr(kv_lens), _adr(out), stride,
+                                         total_tokens, ctypes.byref(p), _stream_on(stream, dev))
+    if side is not None:
+        _keep(side, kv_pages, block_table, cu_q, kv_lens, out)
+    _check(st, "smla_cache_read")
+    return out
 
 
 def smla_cache_reserve(page_size: int, ref_count: torch.Tensor, block_table: torch.Tensor,
@@ -495,6 +577,114 @@ def smla_cache_compact(kv_pages: torch.Tensor, page_size: int, ref_count: torch.
         _keep(side, kv_pages, ref_count, block_table, ref_out, table_out, info, ws)
     _check(st, "smla_cache_compact")
     return info
+
+
+def smla_cache_reorder_workspace_size(params: _lib.SmlaCacheParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.load().smla_cache_reorder_workspace_size(ctypes.byref(params), ctypes.byref(n)),
+           "smla_cache_reorder_workspace_size")
+    return n.value
+
+
+@functools.lru_cache(maxsize=256)
+def _reorder_bytes(num_seqs: int, max_pages: int) -> int:
+    """What smla_cache_reorder_workspace_size says: a matter of these two sizes alone."""
+    return smla_cache_reorder_workspace_size(make_cache_params(1, 1, num_seqs, max_pages))
+
+
+def smla_cache_reorder(kv_pages: torch.Tensor, page_size: int, ref_count: torch.Tensor,
+                       block_table: torch.Tensor, kv_lens: torch.Tensor, parents: torch.Tensor,
+                       workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Row r of the table goes on from what row parents[r] held, in place: its lowest child takes a
+    row over, the others share full pages and copy a last one, and rows without a child are freed.
+    parents[r] < 0 empties row r."""
+    p = _page_state(kv_pages, page_size, ref_count, block_table)
+    dev = kv_pages.device
+    _ints("kv_lens", kv_lens, 1, dev)
+    _ints("parents", parents, 1, dev)
+    if kv_lens.shape[0] != block_table.shape[0] or parents.shape[0] != block_table.shape[0]:
+        raise ValueError("kv_lens and parents must be [B] for a block_table of B rows")
+    side = _side(stream, dev)
+    if workspace is None:
+        workspace = _empty(side, _reorder_bytes(p.num_seqs, p.max_pages), torch.uint8, dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    with _on(dev):
+        st = _lib.load().smla_cache_reorder(_adr(kv_pages), _adr(ref_count), _adr(block_table), _adr(kv_lens),
+                                            _adr(parents), ctypes.byref(p), _adr(workspace), _bytes(workspace),
+                                            _stream_on(stream, dev))
+    if side is not None:
+        _keep(side, kv_pages, ref_count, block_table, kv_lens, parents, workspace)
+    _check(st, "smla_cache_reorder")
+
+
+_LOGITS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def make_beam_params(groups: int, beams: int, vocab: int, num_out: int, row_stride: int = 0,
+                     logits_type: int = 0, end_token: int = 0) -> _lib.SmlaBeamParams:
+    return _lib.SmlaBeamParams(groups, beams, vocab, num_out, row_stride or vocab, logits_type, end_token, 0)
+
+
+def smla_beam_workspace_size(params: _lib.SmlaBeamParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.load().smla_beam_workspace_size(ctypes.byref(params), ctypes.byref(n)), "smla_beam_workspace_size")
+    return n.value
+
+
+@functools.lru_cache(maxsize=256)
+def _beam_bytes(groups: int, beams: int, vocab: int, num_out: int) -> int:
+    """What smla_beam_workspace_size says: a matter of these sizes alone."""
+    return smla_beam_workspace_size(make_beam_params(groups, beams, vocab, num_out))
+
+
+def smla_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: Optional[int] = None,
+                     finished: Optional[torch.Tensor] = None, end_token: int = 0,
+                     parents: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
+                     out_scores: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None
+                     ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The num_out (default: as many as beams) best continuations of each group by score +
+    log-softmax(logits): logits fp32, bf16 or fp16 [G * K, V] (rows any stride apart), scores fp32
+    [G, K].  Beams with finished (uint8 or bool [G * K]) keep their score and take end_token.  Returns
+    (parents int32 [G, num_out], rows of logits; tokens int32; scores fp32), best first."""
+    dev = logits.device
+    if logits.dim() != 2 or logits.dtype not in _LOGITS or logits.stride(1) != 1 or not logits.is_cuda:
+        raise ValueError("logits must be fp32, bf16 or fp16 [G * K, V] with unit column stride on a CUDA device")
+    if scores.dim() != 2 or scores.dtype != torch.float32 or not scores.is_contiguous() or scores.device != dev:
+        raise ValueError(f"scores must be contiguous fp32 [G, K] on {dev}")
+    G, K = scores.shape
+    V = logits.shape[1]
+    if logits.shape[0] != G * K:
+        raise ValueError("logits must have a row for each of scores")
+    if finished is not None and (finished.dtype not in (torch.uint8, torch.bool) or finished.shape != (G * K,)
+                                 or not finished.is_contiguous() or finished.device != dev):
+        raise ValueError(f"finished must be contiguous uint8 or bool [G * K] on {dev}")
+    n = K if num_out is None else num_out
+    stride = logits.stride(0) if logits.shape[0] > 1 else V
+    p = make_beam_params(G, K, V, n, stride, _LOGITS[logits.dtype], end_token)
+    side = _side(stream, dev)
+    got = []
+    for name, t, dtype in (("parents", parents, torch.int32), ("tokens", tokens, torch.int32),
+                           ("out_scores", out_scores, torch.float32)):
+        if t is None:
+            t = _empty(side, (G, max(n, 0)), dtype, dev)
+        elif t.shape != (G, n) or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be contiguous {dtype} [{G}, {n}] on {dev}")
+        got.append(t)
+    if workspace is None:
+        workspace = _empty(side, _beam_bytes(G, K, V, n), torch.uint8, dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    with _on(dev):
+        st = _lib.load().smla_beam_select(_adr(logits), _adr(scores), _adr(finished), _adr(got[0]), _adr(got[1]),
+                                          _adr(got[2]), ctypes.byref(p), _adr(workspace), _bytes(workspace),
+                                          _stream_on(stream, dev))
+    if side is not None:
+        _keep(side, logits, scores, finished, *got, workspace)
+    _check(st, "smla_beam_select")
+    return got[0], got[1], got[2]
 
 
 def make_chunk_params(batch: int, num_heads: int, total_q: int, page_size: int, max_pages: int,

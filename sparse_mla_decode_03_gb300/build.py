@@ -24,7 +24,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "-I", os.path.join(ROOT, "include")]
 SOURCES = ["smla_decode.cu", "smla_combine.cu", "smla_api.cu", "smla_noalloc.cu", "smla_simt.cu",
-           "smla_paged.cu", "smla_cache.cu", "smla_chunk.cu",
+           "smla_paged.cu", "smla_append.cu", "smla_cache.cu", "smla_reorder.cu", "smla_beam.cu", "smla_chunk.cu",
            "smla_chunk_pair.cu", "smla_chunk_single.cu"]
 
 

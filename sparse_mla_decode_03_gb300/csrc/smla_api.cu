@@ -45,8 +45,7 @@ int check_params(const smla_params* p) {
   if (p == nullptr) return SMLA_ERR_INVALID_ARG;
   if (p->batch < 1 || p->topk < 1 || p->topk > 65536 || p->num_rows < 1 || p->reserved != 0)
     return SMLA_ERR_INVALID_ARG;
-  if (p->kv_row_stride < smla::kRowBytes || (p->kv_row_stride % 8) != 0)
-    return SMLA_ERR_INVALID_ARG;
+  if (!smla::row_stride_ok(p->kv_row_stride)) return SMLA_ERR_INVALID_ARG;
   if (!(std::isfinite(p->softmax_scale) && p->softmax_scale > 0.f)) return SMLA_ERR_INVALID_ARG;
   if (p->num_heads != 16 && p->num_heads != 32 && p->num_heads != 64 && p->num_heads != 128)
     return SMLA_ERR_UNSUPPORTED_SHAPE;
@@ -54,6 +53,14 @@ int check_params(const smla_params* p) {
     return SMLA_ERR_UNSUPPORTED_SHAPE;
   if (p->batch > 65535) return SMLA_ERR_UNSUPPORTED_SHAPE;   // grid z of the decode kernels
   return SMLA_OK;
+}
+
+// Rows of 4-bit values: sparse_mla_decode and its paged form, whose work is not split by the caller.
+bool four(const smla_params* p) { return smla::is_row4(p->kv_row_stride); }
+// The calls that take 8-bit rows only.
+int check_params8(const smla_params* p) {
+  const int st = check_params(p);
+  return st == SMLA_OK && four(p) ? SMLA_ERR_UNSUPPORTED_SHAPE : st;
 }
 
 int max_splits(const smla_params* p) {
@@ -193,12 +200,24 @@ int check_tensors(const void* q, const void* kv, const int32_t* idx) {
   return SMLA_OK;
 }
 
+int decode4(const void* q, const void* kv, const int32_t* indices, const int32_t* block_table, int max_pages,
+            int page_size, void* out, float* lse, const smla_params* p, int32_t num_splits, void* workspace,
+            size_t workspace_bytes, smla_stream_t stream) {
+  if (num_splits != 0 || workspace == nullptr || !aligned(workspace, 256)) return SMLA_ERR_INVALID_ARG;
+  if (workspace_bytes < smla::sparse4_workspace(p)) return SMLA_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  const int st = current_device_sms(&sms);
+  if (st != SMLA_OK) return st;
+  return smla::launch_sparse4(q, kv, indices, block_table, max_pages, page_size, out, lse, p, workspace,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
 
 int smla_default_num_splits(const smla_params* p, int32_t* num_splits) {
-  int st = check_params(p);
+  int st = check_params8(p);
   if (st != SMLA_OK) return st;
   if (num_splits == nullptr) return SMLA_ERR_INVALID_ARG;
   int S = 0;
@@ -209,7 +228,7 @@ int smla_default_num_splits(const smla_params* p, int32_t* num_splits) {
 }
 
 int smla_decode_plan(const smla_params* p, int32_t num_splits, int32_t* splits, int32_t* fused) {
-  int st = check_params(p);
+  int st = check_params8(p);
   if (st != SMLA_OK) return st;
   if (splits == nullptr || fused == nullptr) return SMLA_ERR_INVALID_ARG;
   int S = 0;
@@ -227,6 +246,11 @@ int smla_workspace_size(const smla_params* p, int32_t num_splits, size_t* bytes)
   int st = check_params(p);
   if (st != SMLA_OK) return st;
   if (bytes == nullptr) return SMLA_ERR_INVALID_ARG;
+  if (four(p)) {
+    if (num_splits != 0) return SMLA_ERR_INVALID_ARG;
+    *bytes = smla::sparse4_workspace(p);
+    return SMLA_OK;
+  }
   int S = 0;
   st = resolve_splits(p, num_splits, &S);
   if (st != SMLA_OK) return st;
@@ -239,7 +263,7 @@ int smla_workspace_size(const smla_params* p, int32_t num_splits, size_t* bytes)
 int sparse_mla_decode_split(const void* q, const void* kv_cache, const int32_t* indices,
                             const smla_params* p, int32_t num_splits, float* o_part,
                             float* lse_part, smla_stream_t stream) {
-  int st = check_params(p);
+  int st = check_params8(p);
   if (st != SMLA_OK) return st;
   st = check_tensors(q, kv_cache, indices);
   if (st != SMLA_OK) return st;
@@ -284,6 +308,7 @@ int sparse_mla_decode(const void* q, const void* kv_cache, const int32_t* indice
   if (st != SMLA_OK) return st;
   if (out == nullptr || lse == nullptr || !aligned(out, 16) || !aligned(lse, 4))
     return SMLA_ERR_INVALID_ARG;
+  if (four(p)) return decode4(q, kv_cache, indices, nullptr, 0, 0, out, lse, p, num_splits, workspace, workspace_bytes, stream);
   int S = 0;
   st = resolve_splits(p, num_splits, &S);
   if (st != SMLA_OK) return st;
@@ -302,6 +327,10 @@ int smla_paged_workspace_size(const smla_params* p, int32_t num_splits, size_t* 
   size_t total = 0;
   const int st = smla_workspace_size(p, num_splits, &total);
   if (st != SMLA_OK) return st;
+  if (four(p)) {
+    *bytes = total;
+    return SMLA_OK;
+  }
   *bytes = total + round256(static_cast<size_t>(p->batch) * p->topk * sizeof(int32_t));
   return SMLA_OK;
 }
@@ -318,6 +347,9 @@ int sparse_mla_decode_paged(const void* q, const void* kv_pages, const int32_t* 
     return SMLA_ERR_INVALID_ARG;
   if (out == nullptr || lse == nullptr || !aligned(out, 16) || !aligned(lse, 4))
     return SMLA_ERR_INVALID_ARG;
+  if (four(p))
+    return decode4(q, kv_pages, indices, block_table, max_pages_per_seq, page_size, out, lse, p, num_splits, workspace,
+                   workspace_bytes, stream);
   if (workspace == nullptr || !aligned(workspace, 256)) return SMLA_ERR_INVALID_ARG;
   size_t total = 0, need = 0;
   st = smla_workspace_size(p, num_splits, &total);
@@ -339,7 +371,7 @@ int sparse_mla_decode_paged(const void* q, const void* kv_pages, const int32_t* 
 
 int sparse_mla_decode_simt(const void* q, const void* kv_cache, const int32_t* indices,
                            void* out, float* lse, const smla_params* p, smla_stream_t stream) {
-  int st = check_params(p);
+  int st = check_params8(p);
   if (st != SMLA_OK) return st;
   st = check_tensors(q, kv_cache, indices);
   if (st != SMLA_OK) return st;

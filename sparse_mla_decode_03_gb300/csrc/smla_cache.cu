@@ -1,6 +1,5 @@
-// The paged cache: quantising new tokens into its rows (smla_cache_append) and managing
-// its pages (smla_cache_reserve, _fork, _free, _compact).  Declared and documented in
-// include/smla.h.
+// The pages of the paged cache (smla_cache_reserve, _fork, _free, _compact).  Declared and
+// documented in include/smla.h.
 //
 // Page calls.  A page is free exactly when its count is 0, so no free list is kept: a
 // call scans the counts.  The scans and the rankings that depend on one another run as
@@ -9,270 +8,19 @@
 // where rows of the cache move.  Page calls are bound by launches and by the trips to memory
 // and cluster barriers of a plan: free 4 us, fork 10 + 5.5 (512 children 11 + 8), reserve 6 (of
 // 528 rows and 32,768 pages 12.5), compaction's plan 7.5 (32,768 pages 11).
-#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "../../include/smla.h"
+#include "smla_cache_host.h"
+#include "smla_cache_plan.cuh"
+#include "smla_cache_rows.cuh"
 #include "smla_internal.h"
 #include "smla_ptx.cuh"
 
-namespace cg = cooperative_groups;
-
 namespace smla {
 namespace {
-
-constexpr int kPlanCtas = 8;        // CTAs of the planning cluster (the portable size)
-constexpr int kPlanThreads = 1024;
-
-__device__ __forceinline__ void report(int* status, int code) { atomicCAS(status, 0, code); }
-
-// ---------------------------------------------------------------------------
-// Append
-// ---------------------------------------------------------------------------
-struct AppendArgs {
-  const uint4* kv;
-  int64_t token_units;    // 16-byte units between tokens
-  int total;
-  uint8_t* pool;
-  const int32_t *table, *cu_q, *kv_lens;
-  int B, max_pages, page_size, num_pages;
-  int64_t stride;
-  int* status;
-};
-
-// Sequence of token t: the warp narrows [0, B) 32-fold a step.  -1 outside every one.
-__device__ __forceinline__ int sequence_of(const int32_t* cu_q, int B, int t) {
-  if (t < __ldg(cu_q) || t >= __ldg(cu_q + B)) return -1;
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = B;     // cu_q[lo] <= t < cu_q[hi]
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int at = lo + (lane + 1) * step;
-    const bool below = at < hi && __ldg(cu_q + at) <= t;
-    const int k = __popc(__ballot_sync(0xffffffffu, below));
-    lo += k * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
-// The row of token t, or null (reported) if it has no place; null too outside every sequence.
-__device__ __forceinline__ uint8_t* row_of(const AppendArgs& a, int t) {
-  const int b = sequence_of(a.cu_q, a.B, t);
-  if (b < 0) return nullptr;
-  const int64_t pos = static_cast<int64_t>(__ldg(a.kv_lens + b)) - (__ldg(a.cu_q + b + 1) - t);
-  if (pos >= 0) {   // below 2^31: kv_lens is an int32
-    const uint32_t at = static_cast<uint32_t>(pos), page = at / static_cast<uint32_t>(a.page_size);
-    if (page < static_cast<uint32_t>(a.max_pages)) {
-      const int phys = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + page);
-      if (phys >= 0 && phys < a.num_pages)
-        return a.pool + (static_cast<int64_t>(phys) * a.page_size + (at - page * a.page_size)) * a.stride;
-    }
-  }
-  if ((threadIdx.x & 31) == 0) report(a.status, SMLA_ERR_INDEX_RANGE);
-  return nullptr;
-}
-
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// One token of a warp.  Lane l < 28 holds nope columns 16 l .. 16 l + 15 (four lanes a scale
-// group), lanes 28..31 the rope.  The row is put together in shared memory (stage: 73 words)
-// and leaves in consecutive words.
-__device__ __forceinline__ void write_row(const AppendArgs& a, uint8_t* dst, const uint4& u0, const uint4& u1,
-                                          uint2* stage) {
-  const int lane = threadIdx.x & 31;
-  uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-  // largest magnitude as bf16 bits, two columns at a time (magnitudes compare as integers)
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_u16x2(m, w[i] & 0x7fff7fffu);
-  uint32_t top = max(m >> 16, m & 0xffffu);
-  if (__any_sync(0xffffffffu, lane < 28 && top >= 0x7f80u)) {
-    // infinity and NaN are stored as NaN and do not count
-    top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t h[2] = {w[i] & 0xffffu, w[i] >> 16};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if ((h[k] & 0x7fffu) >= 0x7f80u) {
-          h[k] = 0x7fffu;
-          if (lane < 28) report(a.status, SMLA_ERR_RANGE);
-        } else {
-          top = max(top, h[k] & 0x7fffu);
-        }
-      }
-      w[i] = h[0] | h[1] << 16;
-    }
-  }
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // 448 = 1.75 * 2^8, so the least e with top <= 448 * 2^e follows from top's exponent
-  // and whether its mantissa exceeds 1.75: exact, no logarithm.
-  int byte = static_cast<int>(top >> 7) - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
-  byte = top == 0 ? 127 : min(max(byte, 1), 254);
-  // from 1.9375 * 2^127 on (halfway from 240 to 256 in the scale 2^120) the stored value is 2^128
-  if (top >= 0x7f78u && lane < 28) report(a.status, SMLA_ERR_RANGE);
-  // 2^(127 - byte) as a float (byte 254: the subnormal 2^-127)
-  const float inv = __uint_as_float(byte < 254 ? static_cast<uint32_t>(254 - byte) << 23 : 0x00400000u);
-  if (lane < 28) {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint16_t lo, hi;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-          : "=h"(lo)
-          : "f"(__uint_as_float(w[2 * i] & 0xffff0000u) * inv), "f"(__uint_as_float(w[2 * i] << 16) * inv));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-          : "=h"(hi)
-          : "f"(__uint_as_float(w[2 * i + 1] & 0xffff0000u) * inv), "f"(__uint_as_float(w[2 * i + 1] << 16) * inv));
-      o[i] = lo | (static_cast<uint32_t>(hi) << 16);
-    }
-    stage[2 * lane] = make_uint2(o[0], o[1]);
-    stage[2 * lane + 1] = make_uint2(o[2], o[3]);
-    if ((lane & 3) == 0) reinterpret_cast<uint8_t*>(stage)[kNope + lane / 4] = static_cast<uint8_t>(byte);
-  } else {
-    uint2* d = stage + 57 + 4 * (lane - 28);
-    d[0] = make_uint2(u0.x, u0.y);
-    d[1] = make_uint2(u0.z, u0.w);
-    d[2] = make_uint2(u1.x, u1.y);
-    d[3] = make_uint2(u1.z, u1.w);
-    if (lane == 28) reinterpret_cast<uint8_t*>(stage)[kNope + 7] = 0;      // the padding
-  }
-  __syncwarp();
-  uint2* d = reinterpret_cast<uint2*>(dst);
-  d[lane] = stage[lane];
-  d[lane + 32] = stage[lane + 32];
-  if (lane < 9) d[lane + 64] = stage[lane + 64];
-  __syncwarp();
-}
-
-// Bound by memory: 1,024 bytes in and 584 out a token.  One token a warp: 38 us for 131,072 tokens
-// (5.55 TB/s, 82 % of the measured copy rate; issue 73 %, integer pipe 59 % busy); two or four
-// tokens' loads at once measured 41.0 and 44.1 us.  A decode step's call (96 tokens) is a launch
-// and two trips to memory, 5 us.
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
-  __shared__ uint2 stage[8][76];
-  grid_dep_wait();
-  grid_dep_launch();
-  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= a.total) return;
-  const uint4* src = a.kv + t * a.token_units + 2 * (threadIdx.x & 31);
-  const uint4 u0 = __ldcs(src), u1 = __ldcs(src + 1);
-  uint8_t* dst = row_of(a, t);
-  if (dst != nullptr) write_row(a, dst, u0, u1, stage[threadIdx.x >> 5]);
-}
-
-// ---------------------------------------------------------------------------
-// Ranking across the planning cluster
-// ---------------------------------------------------------------------------
-struct PlanShared {
-  int warp[32];
-  int2 counts[2][kPlanCtas];   // counts of every CTA of the cluster, two slots in turn
-};
-
-// Exclusive sum of v over the CTA's threads; *total gets the sum.  All threads call.
-__device__ int block_rank(int v, int* total, PlanShared* sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += u;
-  }
-  __syncthreads();            // the previous call's readers are done with warp[]
-  if (lane == 31) sh->warp[warp] = s;
-  __syncthreads();
-  if (warp == 0) {
-    int w = sh->warp[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    sh->warp[lane] = w;
-  }
-  __syncthreads();
-  *total = sh->warp[31];
-  return s - v + (warp > 0 ? sh->warp[warp - 1] : 0);
-}
-
-// Shares this CTA's two counts with the cluster (a slot may be used again after another
-// share): *before = sums of the lower ranks', returns the sums of all.  Orders the
-// cluster's memory accesses as a barrier does.
-__device__ int2 cluster_share(int2 mine, int slot, int2* before, PlanShared* sh) {
-  cg::cluster_group cl = cg::this_cluster();
-  const int rank = static_cast<int>(cl.block_rank());
-  if (threadIdx.x < kPlanCtas) cl.map_shared_rank(sh, threadIdx.x)->counts[slot][rank] = mine;
-  cl.sync();
-  int2 all = make_int2(0, 0), low = make_int2(0, 0);
-#pragma unroll
-  for (int r = 0; r < kPlanCtas; ++r) {
-    const int2 c = sh->counts[slot][r];
-    all.x += c.x;
-    all.y += c.y;
-    if (r < rank) {
-      low.x += c.x;
-      low.y += c.y;
-    }
-  }
-  *before = low;
-  return all;
-}
-
-// This CTA's part [first, last) of n things, and within it the thread's part, a run of a
-// multiple of 4: ranks then need one block-wide sum, whatever the length.  Unsigned, since the ends
-// of a part of nearly 2^31 things are rounded up past it.
-struct Part {
-  uint32_t run0, run1;
-};
-__device__ __forceinline__ Part part_of(uint32_t n) {
-  const uint32_t rank = cg::this_cluster().block_rank();
-  const uint32_t per = ((n + kPlanCtas - 1) / kPlanCtas + 3) & ~3u;
-  const uint32_t first = min(n, rank * per), last = min(n, first + per);
-  const uint32_t run = ((last - first + kPlanThreads - 1) / kPlanThreads + 3) & ~3u;
-  Part p;
-  p.run0 = min(last, first + threadIdx.x * run);
-  p.run1 = min(last, p.run0 + run);
-  return p;
-}
-// f(page, count) for the pages of the thread's run.
-template <class F>
-__device__ __forceinline__ void each_page(const int32_t* ref, const Part& p, F f) {
-  for (uint32_t q = p.run0; q < p.run1; q += 4) {
-    int c[4];
-#pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) c[k] = q + k < p.run1 ? __ldcg(ref + q + k) : 0;
-#pragma unroll
-    for (uint32_t k = 0; k < 4; ++k)
-      if (q + k < p.run1) f(static_cast<int>(q + k), c[k]);
-  }
-}
-__device__ __forceinline__ int count_free(const int32_t* ref, const Part& p) {
-  int n = 0;
-  each_page(ref, p, [&](int, int c) { n += c <= 0; });
-  return n;
-}
-// Gives the `want` lowest free pages (or all) a count of 1 and lists them, ascending.
-// rank: free pages before the thread's run.
-__device__ __forceinline__ void take_free(int32_t* ref, const Part& p, int rank, int want, int32_t* list) {
-  if (rank >= want) return;
-  each_page(ref, p, [&](int page, int c) {
-    if (c <= 0) {
-      if (rank < want) {
-        list[rank] = page;
-        ref[page] = 1;
-      }
-      ++rank;
-    }
-  });
-}
 
 // ---------------------------------------------------------------------------
 // Reserve
@@ -391,44 +139,6 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     if (f == kSkip) report(a.status, SMLA_ERR_INDEX_RANGE);
     if (f == kNoPage) report(a.status, SMLA_ERR_POOL_EXHAUSTED);
     a.fresh[i] = f;
-  }
-}
-
-// Copies rows from .. from + rows - 1 of the pool to to .. by the CTA's threads.  Rows that
-// follow one another without a gap go as 16-byte words where both ends allow it, four of a
-// thread's in flight.
-__device__ __forceinline__ void copy_rows(uint8_t* pool, int64_t stride, int64_t from, int64_t to,
-                                          int rows) {
-  const uint8_t* s = pool + from * stride;
-  uint8_t* d = pool + to * stride;
-  if (stride == kRowBytes) {
-    // 16-byte aligned parts: both start on one, or both 8 bytes behind one
-    const bool same = ((reinterpret_cast<uintptr_t>(s) ^ reinterpret_cast<uintptr_t>(d)) & 8) == 0;
-    if (same) {
-      const int bytes = rows * kRowBytes;
-      const int head = static_cast<int>(reinterpret_cast<uintptr_t>(s) & 8);
-      const int units = (bytes - head) / 16, tail = bytes - head - 16 * units;
-      if (threadIdx.x == 0 && head) *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(s);
-      if (threadIdx.x == 1 && tail)
-        *reinterpret_cast<uint2*>(d + bytes - 8) = *reinterpret_cast<const uint2*>(s + bytes - 8);
-      const uint4* s4 = reinterpret_cast<const uint4*>(s + head);
-      uint4* d4 = reinterpret_cast<uint4*>(d + head);
-      const int step = blockDim.x;
-      for (int w = threadIdx.x; w < units; w += 4 * step) {
-        uint4 v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (w + k * step < units) v[k] = __ldcs(s4 + w + k * step);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (w + k * step < units) __stcs(d4 + w + k * step, v[k]);
-      }
-      return;
-    }
-  }
-  for (int w = threadIdx.x; w < rows * (kRowBytes / 8); w += blockDim.x) {
-    const int64_t off = (w / (kRowBytes / 8)) * stride + 8 * (w % (kRowBytes / 8));
-    *reinterpret_cast<uint2*>(d + off) = *reinterpret_cast<const uint2*>(s + off);
   }
 }
 
@@ -590,71 +300,12 @@ __global__ void __launch_bounds__(256) compact_move_kernel(const CompactArgs a) 
   }
 }
 
-// ---------------------------------------------------------------------------
-// Host side
-// ---------------------------------------------------------------------------
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-int check_cache(const smla_cache_params* c) {
-  if (c == nullptr || c->num_pages < 1 || c->page_size < 1 || c->num_seqs < 1 || c->max_pages < 1)
-    return SMLA_ERR_INVALID_ARG;
-  if (c->kv_row_stride < kRowBytes || c->kv_row_stride % 8 != 0) return SMLA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(c->num_pages) * c->page_size > (int64_t{1} << 31) || c->num_seqs > 65535)
-    return SMLA_ERR_UNSUPPORTED_SHAPE;
-  return SMLA_OK;
-}
-
-bool ints_ok(const void* p) { return p != nullptr && aligned(p, 4); }
-bool pool_ok(const void* p) { return p != nullptr && aligned(p, 8); }
-
-// Workspace: three lists of num_pages entries, one of num_seqs.
-size_t list_bytes(const smla_cache_params* c) { return round256(size_t{4} * c->num_pages); }
-
-int check_workspace(const smla_cache_params* c, const void* ws, size_t bytes) {
-  if (ws == nullptr || !aligned(ws, 256)) return SMLA_ERR_INVALID_ARG;
-  size_t need = 0;
-  const int st = smla_cache_workspace_size(c, &need);
-  if (st != SMLA_OK) return st;
-  return bytes < need ? SMLA_ERR_WORKSPACE_TOO_SMALL : SMLA_OK;
-}
-
-// The device check and the status word; the last step before a launch.
-int ready(int** status) {
-  const int st = check_device();
-  if (st != SMLA_OK) return st;
-  return status_word_address(status) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
-}
-
-int done(cudaError_t e) { return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA; }
-
 }  // namespace
 }  // namespace smla
 
 using namespace smla;   // NOLINT: the entry points below are this file's own
 
 extern "C" {
-
-int smla_cache_append(const void* kv, int64_t kv_token_stride, int32_t total_tokens, void* kv_pages,
-                      const int32_t* block_table, const int32_t* cu_q, const int32_t* kv_lens,
-                      const smla_cache_params* c, smla_stream_t stream) {
-  int st = check_cache(c);
-  if (st != SMLA_OK) return st;
-  if (total_tokens < 0 || kv_token_stride < kQkDim || kv_token_stride % 8 != 0)
-    return SMLA_ERR_INVALID_ARG;
-  if (!pool_ok(kv_pages) || !ints_ok(block_table) || !ints_ok(cu_q) || !ints_ok(kv_lens))
-    return SMLA_ERR_INVALID_ARG;
-  if (total_tokens == 0) return SMLA_OK;
-  if (kv == nullptr || !aligned(kv, 16)) return SMLA_ERR_INVALID_ARG;
-  int* status = nullptr;
-  st = ready(&status);
-  if (st != SMLA_OK) return st;
-  const AppendArgs a = {static_cast<const uint4*>(kv), kv_token_stride / 8, total_tokens,
-                        static_cast<uint8_t*>(kv_pages), block_table, cu_q, kv_lens, c->num_seqs,
-                        c->max_pages, c->page_size, c->num_pages, c->kv_row_stride, status};
-  return done(launch_programmatic(append_kernel, dim3((total_tokens - 1) / 8 + 1), dim3(256), 0,
-                                  reinterpret_cast<cudaStream_t>(stream), a));
-}
 
 int smla_cache_workspace_size(const smla_cache_params* c, size_t* bytes) {
   const int st = check_cache(c);
@@ -691,7 +342,7 @@ int smla_cache_fork(void* kv_pages, int32_t* ref_count, int32_t* block_table, in
   int st = check_cache(c);
   if (st != SMLA_OK) return st;
   if (n < 0 || n > c->num_seqs) return SMLA_ERR_INVALID_ARG;
-  if (!pool_ok(kv_pages) || !ints_ok(ref_count) || !ints_ok(block_table) || !ints_ok(kv_lens))
+  if (!pool_ok(kv_pages, c) || !ints_ok(ref_count) || !ints_ok(block_table) || !ints_ok(kv_lens))
     return SMLA_ERR_INVALID_ARG;
   st = check_workspace(c, workspace, workspace_bytes);
   if (st != SMLA_OK) return st;
@@ -732,7 +383,7 @@ int smla_cache_compact(void* kv_pages, const int32_t* ref_count, const int32_t* 
                        smla_stream_t stream) {
   int st = check_cache(c);
   if (st != SMLA_OK) return st;
-  if (!pool_ok(kv_pages) || !ints_ok(ref_count) || !ints_ok(block_table) || !ints_ok(ref_count_out) ||
+  if (!pool_ok(kv_pages, c) || !ints_ok(ref_count) || !ints_ok(block_table) || !ints_ok(ref_count_out) ||
       !ints_ok(block_table_out) || !ints_ok(info))
     return SMLA_ERR_INVALID_ARG;
   st = check_workspace(c, workspace, workspace_bytes);

@@ -8,16 +8,13 @@
 #include <cstdint>
 
 #include "../../include/smla.h"
+#include "smla_cache_rows.cuh"
 #include "smla_chunk.h"
 #include "smla_internal.h"
 #include "smla_ptx.cuh"
 
 namespace smla {
 namespace {
-
-__device__ __forceinline__ float ue8m0_value(uint32_t e) {
-  return __uint_as_float(e == 0u ? 0x00400000u : (e == 255u ? 0x7fffffffu : (e << 23)));
-}
 
 // ---------------------------------------------------------------------------
 // Plan: one CTA, 6 to 7 us cold (a launch, three dependent loads, block-wide sums), within the
@@ -70,6 +67,7 @@ struct Sequence {
 __device__ __forceinline__ Sequence sequence(const ChunkArgs& a, int b) {
   Sequence s = {0, 0, 0, 0, false};
   if (b >= a.B) return s;
+  if (a.listed > 0) return {b, 1, a.listed, (a.listed - 1) / kChunkBlk + 1, false};
   const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
   s.wrong = c0 < 0 || c1 < c0 || c1 > a.T;
   s.len = max(a.kv_lens[b], 0);
@@ -251,15 +249,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 // two of them; lane l < 28 holds columns 16 l .. 16 l + 15, lanes 28..31 the rope.  Bound by
 // the launch and one trip to memory: 7.5 us for 8,192 rows (1.6 KB each), 11 us for 21,007.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t expand_pair(uint32_t two, float scale) {
-  uint32_t h2;
-  const uint16_t in = static_cast<uint16_t>(two);
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(in));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y * scale), "f"(f.x * scale));
-  return r;
-}
 __device__ __forceinline__ bool not_finite(uint32_t bf16x2) {
   return (bf16x2 & 0x7f80u) == 0x7f80u || (bf16x2 & 0x7f800000u) == 0x7f800000u;
 }
@@ -267,6 +256,7 @@ __device__ __forceinline__ bool not_finite(uint32_t bf16x2) {
 // CTA 0 makes the plan meanwhile; the others find the sequences' places by themselves (the
 // same sums over the batch), so that one launch does both.
 constexpr int kExpandRows = 2;     // rows of a block that a warp expands at once: 32 warps, 64 rows
+template <bool ROW4>
 __global__ void __launch_bounds__(kPlanThreads, 1)
     expand_kernel(const ChunkArgs a, const ChunkPlan p, int tile_rows, int workers) {
   __shared__ PlanShared sh;
@@ -327,44 +317,16 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
       }
       const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
       uint32_t poison = 0;
-      uint2 in[kExpandRows][4];
-      uint32_t sc[kExpandRows];
+      RowLane in[kExpandRows];
 #pragma unroll
       for (int j = 0; j < kExpandRows; ++j) {
         const long long r = __shfl_sync(0xffffffffu, row, j);
-        in[j][0] = in[j][1] = in[j][2] = in[j][3] = make_uint2(0u, 0u);
-        sc[j] = 127;
-        if (r >= 0) {
-          const uint8_t* src = a.pool + r * a.stride;
-          const uint2* w = reinterpret_cast<const uint2*>(src + (lane < 28 ? 16 * lane : 456 + 32 * (lane - 28)));
-          in[j][0] = __ldg(w);
-          in[j][1] = __ldg(w + 1);
-          if (lane >= 28) {
-            in[j][2] = __ldg(w + 2);
-            in[j][3] = __ldg(w + 3);
-          } else {
-            sc[j] = __ldg(src + kNope + lane / 4);
-          }
-        }
+        load_row<ROW4>(r >= 0 ? a.pool + r * a.stride : nullptr, in[j]);
       }
 #pragma unroll
       for (int j = 0; j < kExpandRows; ++j) {
         uint32_t o[8];
-        if (lane < 28) {
-          const float f = ue8m0_value(sc[j]);
-          const uint32_t w[4] = {in[j][0].x, in[j][0].y, in[j][1].x, in[j][1].y};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            o[2 * k] = expand_pair(w[k] & 0xffffu, f);
-            o[2 * k + 1] = expand_pair(w[k] >> 16, f);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            o[2 * k] = in[j][k].x;
-            o[2 * k + 1] = in[j][k].y;
-          }
-        }
+        row_values<ROW4>(in[j], o);
         bool bad = false;      // a NaN (a scale byte of 255 makes NaN), or past bf16's largest value
 #pragma unroll
         for (int k = 0; k < 8; ++k) bad |= not_finite(o[k]);
@@ -502,7 +464,7 @@ int check_chunk(const smla_chunk_params* p) {
   if (p->batch < 1 || p->total_q < 1 || p->page_size < 1 || p->max_pages < 1 || p->num_rows < 1 ||
       p->max_kv_tokens < 1)
     return SMLA_ERR_INVALID_ARG;
-  if (p->kv_row_stride < kRowBytes || p->kv_row_stride % 8 != 0) return SMLA_ERR_INVALID_ARG;
+  if (!row_stride_ok(p->kv_row_stride)) return SMLA_ERR_INVALID_ARG;
   if (!(std::isfinite(p->softmax_scale) && p->softmax_scale > 0.f)) return SMLA_ERR_INVALID_ARG;
   if (!(std::isfinite(p->logit_cap) && p->logit_cap >= 0.f)) return SMLA_ERR_INVALID_ARG;
   if (p->num_heads != 16 && p->num_heads != 32 && p->num_heads != 64 && p->num_heads != 128)
@@ -574,7 +536,7 @@ cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_
   if (workers > kMaxPairs) workers = kMaxPairs;
   const int64_t blocks = p.cap_blocks + 1;
   const unsigned grid = 1 + static_cast<unsigned>(blocks < kMaxSms - 1 ? blocks : kMaxSms - 1);
-  e = launch_programmatic(expand_kernel, dim3(grid), dim3(kPlanThreads), 0, s, a, p, kPairRows, workers);
+  e = launch_programmatic(is_row4(a.stride) ? expand_kernel<true> : expand_kernel<false>, dim3(grid), dim3(kPlanThreads), 0, s, a, p, kPairRows, workers);
   if (e != cudaSuccess) return e;
   e = launch_chunk_pair(a, p, workers, s);
   return e == cudaSuccess ? launch_merge(a, p, kPairRows, workers, s) : e;
@@ -587,8 +549,34 @@ cudaError_t launch_single_path(const ChunkArgs& a, const ChunkPlan& p, cudaStrea
   return e == cudaSuccess ? launch_merge(a, p, kSingleRows, workers, s) : e;
 }
 
+// Sparse decode over 4-bit rows as a chunk of one token a sequence that sees topk listed rows.
+smla_chunk_params sparse_as_chunk(const smla_params* p) {
+  return {p->batch, p->num_heads, p->batch, 1, p->topk, 0, p->num_rows, p->kv_row_stride,
+          static_cast<int64_t>(p->batch) * (((p->topk - 1) / kChunkBlk + 1) * kChunkBlk), p->softmax_scale, 0.f};
+}
 
 }  // namespace
+
+size_t sparse4_workspace(const smla_params* p) {
+  const smla_chunk_params c = sparse_as_chunk(p);
+  ChunkPlan plan;
+  return lay_out(&c, nullptr, &plan);
+}
+
+int launch_sparse4(const void* q, const void* kv, const int32_t* indices, const int32_t* block_table, int max_pages,
+                   int page_size, void* out, float* lse, const smla_params* p, void* workspace, cudaStream_t stream) {
+  int* status = nullptr;
+  if (status_word_address(&status) != cudaSuccess) return SMLA_ERR_CUDA;
+  const smla_chunk_params c = sparse_as_chunk(p);
+  const ChunkArgs a = {static_cast<const uint16_t*>(q), static_cast<const uint8_t*>(kv), indices, nullptr, nullptr,
+                       nullptr, nullptr, nullptr, static_cast<__nv_bfloat16*>(out), lse, c.batch, c.num_heads,
+                       c.total_q, 1, c.max_pages, c.num_rows, c.kv_row_stride, c.softmax_scale, 0.f, status,
+                       fault_block(), p->topk, block_table, max_pages, page_size};
+  ChunkPlan plan;
+  lay_out(&c, static_cast<char*>(workspace), &plan);
+  return launch_single_path(a, plan, stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
 }  // namespace smla
 
 using namespace smla;   // NOLINT: the entry points below are this file's own
@@ -630,7 +618,7 @@ int smla_chunk_attention(const void* q, const void* kv_pages, const int32_t* blo
                        block_table, cu_q, kv_lens, vis_begin, vis_end, slopes,
                        static_cast<__nv_bfloat16*>(out), lse, p->batch, p->num_heads, p->total_q,
                        p->page_size, p->max_pages, p->num_rows, p->kv_row_stride, p->softmax_scale,
-                       p->logit_cap, status, fault_block()};
+                       p->logit_cap, status, fault_block(), 0, nullptr, 0, 0};
   ChunkPlan plan;
   lay_out(p, static_cast<char*>(workspace), &plan);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

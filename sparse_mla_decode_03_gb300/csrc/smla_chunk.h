@@ -8,6 +8,7 @@
 
 #include "../../include/smla.h"
 #include "smla_internal.h"
+#include "smla_ptx.cuh"
 
 namespace smla {
 
@@ -25,6 +26,11 @@ struct ChunkArgs {
   float scale, cap;
   int* status;
   int fault_block;       // test hook: the block of each share that one warp does not report (-1: none)
+  // Sparse decode: every sequence is one token that sees `listed` slots; `table` lists their rows (pages
+  // of one row), or, with `pages`, their positions in the sequence.  cu_q and kv_lens are not read.
+  int listed;            // 0: not sparse
+  const int32_t* pages;  // [B, max_listed_pages] or null
+  int max_listed_pages, listed_page_size;
 };
 
 // The plan of a call: the (token, head) rows of each sequence cut into tiles, each tile's
@@ -49,12 +55,6 @@ struct ChunkPlan {
   int64_t cap_blocks;    // blocks of the expanded copy, not counting one of zeros behind
 };
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 __device__ __forceinline__ int find_last_le(const int32_t* a, int n, int x) {   // a[0] <= x
   int lo = 0;
   for (int hi = n; hi - lo > 1;) {
@@ -69,6 +69,12 @@ __device__ __forceinline__ int find_last_le(const int32_t* a, int n, int x) {   
 // *pos.  len: positions of the sequence that can be seen.  Neither is below 0, so that their
 // distance to a block's first position is an int, whatever the masks hold.
 __device__ __forceinline__ void visible(const ChunkArgs& a, int b, int t, int len, int* lo, int* hi, int* pos) {
+  if (a.listed > 0) {
+    *pos = 0;
+    *lo = 0;
+    *hi = len;
+    return;
+  }
   *pos = a.kv_lens[b] - (a.cu_q[b + 1] - t);
   *lo = a.vis_begin != nullptr ? max(0, a.vis_begin[t]) : 0;
   *hi = max(0, min(len, a.vis_end != nullptr ? a.vis_end[t] : *pos + 1));

@@ -32,6 +32,7 @@
 // value products, 26 loads Q.  Every wait is bounded.
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "smla_chunk.h"
 #include "smla_chunk_rows.cuh"
@@ -184,6 +185,38 @@ constexpr int kTails = (kRows + 2) / 3;
 struct RowWords {
   uint2 a[kRows], b[kRows], c[kTails];
 };
+
+// 4-bit rows: lane l holds the 16-byte words l / 4 (a), 8 + l / 4 (b) and 16 + l / 4 (c; lanes 28 .. 31: word 22
+// once more) of row l % 4 of its warp.  Words 0..13 of a row are 32 nope columns each, one scale
+// group; 14 is the scales, 15..22 the rope.
+struct RowWords4 {
+  uint4 a, b, c;
+};
+__device__ __forceinline__ uint4 ldg16_once(const uint8_t* src) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src));
+  return v;
+}
+// Eight e2m1 nibbles (column 2 p in nibble p, 2 p + 1 in nibble p + 4) -> eight bf16.  A nibble's
+// sign at bit 15 and its exponent and mantissa at bits 8..6 are its value times 2^-126, subnormals
+// included, and one product by 2^(scale byte - 1) (m) puts both powers right, exactly.
+__device__ __forceinline__ uint4 expand_nibbles(uint32_t w, uint32_t m) {
+  constexpr uint32_t kSign = 0x80008000u, kMag = 0x01c001c0u;
+  return make_uint4(mul_bf16x2(((w << 12) & kSign) | ((w << 6) & kMag), m),
+                    mul_bf16x2(((w << 8) & kSign) | ((w << 2) & kMag), m),
+                    mul_bf16x2(((w << 4) & kSign) | ((w >> 2) & kMag), m),
+                    mul_bf16x2((w & kSign) | ((w >> 6) & kMag), m));
+}
+__device__ __forceinline__ uint4 mul4(uint4 v, uint32_t m) {
+  return make_uint4(mul_bf16x2(v.x, m), mul_bf16x2(v.y, m), mul_bf16x2(v.z, m), mul_bf16x2(v.w, m));
+}
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+// Nibbles that times 2^(s - 127) pass bf16's largest value, or a scale byte of 255.
+__device__ __forceinline__ bool past_bf16(const uint4& v, uint32_t s) {
+  const uint32_t w = s == 254 ? v.x | v.y | v.z | v.w : 0u;                          // 2 and above
+  const uint32_t u = s == 253 ? (v.x & (v.x << 1)) | (v.y & (v.y << 1)) | (v.z & (v.z << 1)) | (v.w & (v.w << 1)) : 0u;
+  return s == 255 || ((w | u) & 0x44444444u) != 0;                                   // 4 and 6
+}
 
 // Two rows a thread: the 16 rows of a quarter with 32 of their 64 scores of a block, as the
 // 16-lane tensor-memory load deals them out: lane 4 g + q has columns 8 j + 2 q and + 1 (of
@@ -352,7 +385,7 @@ __device__ __forceinline__ void drain() {
   while (clock64() - t0 < 2000000) {
   }
 }
-template <bool MODS>
+template <bool MODS, bool ROW4>
 __global__ void __launch_bounds__(kThreads, 1)
     single_kernel(const ChunkArgs a, const ChunkPlan plan, const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ uint8_t smem_raw[];
@@ -401,7 +434,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       // page id of the cursor's row, -1 = no row there
       auto lookup = [&](const Cursor& c) {
         if (c.x >= c.x1 || c.left <= 0) return -1;
-        if (c.page < a.max_pages) return __ldg(a.table + static_cast<int64_t>(c.b) * a.max_pages + c.page);
+        if (c.page < a.max_pages) {
+          const int id = __ldg(a.table + static_cast<int64_t>(c.b) * a.max_pages + c.page);
+          if (!ROW4 || a.pages == nullptr || id < 0) return id;
+          // a listed position: its page, then its row
+          const int page = id / a.listed_page_size;
+          if (page < a.max_listed_pages) {
+            const int phys = __ldg(a.pages + static_cast<int64_t>(c.b) * a.max_listed_pages + page);
+            if (phys < 0) return -1;
+            const long long r = static_cast<long long>(phys) * a.listed_page_size + (id - page * a.listed_page_size);
+            if (r < a.num_rows) return static_cast<int>(r);
+          }
+        }
         atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
         return -1;
       };
@@ -410,12 +454,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // matter (a row that is not finite is held as zeros).  Rows of a pool that fits the
       // GPU number far below 2^32.
       uint32_t row_now = 0;
-      auto fetch = [&](int id, int off, RowWords& d) {
+      auto fetch = [&](int id, int off, auto& d) {
         const long long r = static_cast<long long>(id) * a.page_size + off;
         const bool there = id >= 0 && r < a.num_rows;
         if (id >= 0 && !there) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
         const uint32_t have = __ballot_sync(0xffffffffu, there) & ((1u << kRows) - 1u);
         row_now = there ? static_cast<uint32_t>(r) : 0u;
+        if constexpr (ROW4) {
+          const uint8_t* src = a.pool + static_cast<uint64_t>(row_now) * stride + 16 * (lane >> 2);
+          d.a = ldg16_once(src);
+          d.b = ldg16_once(src + 128);
+          d.c = ldg16_once(src + (lane < 28 ? 256 : 240));
+          return have;
+        } else {
         const uint8_t* base = a.pool + 8 * lane;
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
@@ -429,18 +480,86 @@ __global__ void __launch_bounds__(kThreads, 1)
           d.c[k] = ldg_once(a.pool + static_cast<uint64_t>(__shfl_sync(0xffffffffu, row_now, j)) * stride + 512 + 8 * c_word);
         }
         return have;
+        }
       };
       Cursor at;                     // the block whose page ids are fetched next
       at.x = x0;
       at.x1 = x1;
       at.t = t_first;
       at.load(plan, mine, a.page_size);
-      RowWords d;
+      std::conditional_t<ROW4, RowWords4, RowWords> d;
       const int count = x1 - x0;
       uint32_t have = fetch(lookup(at), at.off, d);
       at.step(plan, mine, a.page_size, pages_step, rest);
       int id = lookup(at), off = at.off;
       bool ok = true;
+      if constexpr (ROW4) {
+        const int j = lane & 3, w = lane >> 2;
+        const uint32_t key = static_cast<uint32_t>((kRows * w16 + j) & 7);
+        const uint32_t row = sbase + kBufOff + (kRows * w16 + j) * 128;
+        // nope words w and 8 + w: four 16-byte units of slab w / 2 and 4 + w / 2; rope units w + 1 (word c) and
+        // 0 (word b of lanes 28 .. 31)
+        const uint32_t to = row + (w >> 1) * kSlab, rope = row + 7 * kSlab;
+        auto unit = [&](int u) { return ((static_cast<uint32_t>(u) ^ key) << 4); };
+        const bool nope_b = w < 6, rope_b = w == 7;
+        for (int n = 0; n < count; ++n) {
+          const int B = n & 1;
+          // the scale bytes of the lane's two words
+          const uint32_t s0 = __shfl_sync(0xffffffffu, d.b.x, 24 + j), s1 = __shfl_sync(0xffffffffu, d.b.y, 24 + j);
+          const uint32_t s2 = __shfl_sync(0xffffffffu, d.b.z, 24 + j), s3 = __shfl_sync(0xffffffffu, d.b.w, 24 + j);
+          const uint32_t sa = ((w < 4 ? s0 : s1) >> (8 * (w & 3))) & 0xffu;
+          const uint32_t sb = nope_b ? ((w < 4 ? s2 : s3) >> (8 * (w & 3))) & 0xffu : 0u;
+          // 2^(s - 1) as two bf16, in two factors past bf16's exponents
+          auto first = [](uint32_t s) { return (min(s, 128u) + 126u) * 0x00800080u; };
+          auto second = [](uint32_t s) { return (max(s, 128u) - 1u) * 0x00800080u; };
+          const bool large = __any_sync(0xffffffffu, max(sa, sb) > 128u);
+          // rows that are not finite are held as zeros
+          const uint32_t rc = rope_bits(d.c.x) | rope_bits(d.c.y) | rope_bits(d.c.z) | rope_bits(d.c.w);
+          const uint32_t rb = rope_b ? rope_bits(d.b.x) | rope_bits(d.b.y) | rope_bits(d.b.z) | rope_bits(d.b.w) : 0u;
+          uint32_t dropped = 0;
+          if (__any_sync(0xffffffffu, ((rc | rb) & 0x80008000u) != 0 || max(sa, sb) >= 253u)) {
+            const bool bad = ((rc | rb) & 0x80008000u) != 0 || past_bf16(d.a, sa) || (nope_b && past_bf16(d.b, sb));
+            const uint32_t who = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) dropped |= (who & (0x11111111u << i)) != 0 ? 1u << i : 0u;
+            if ((dropped >> j) & 1) {
+              const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+              d.a = d.b = d.c = zero;
+            }
+          }
+          const uint32_t parity = ((n >> 1) - 1) & 1;
+          if (n >= 2) ok = warp_wait(bar(EMPTY + 2 * B), parity, stop, a.status);
+          if (!ok) break;
+          auto words = [&](const uint4& v, uint32_t s, uint32_t at, bool mine) {
+            const uint32_t m1 = first(s), m2 = second(s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 o = expand_nibbles(word_of(v, i), m1);
+              if (large) o = mul4(o, m2);
+              sts_if(mine, at + unit(4 * (w & 1) + i), o);
+            }
+          };
+          words(d.a, sa, to + B * kBuf, true);
+          if (lane == 0) {
+            masks[B * 32 + w16] = static_cast<uint8_t>(have);
+            masks[B * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && !(n == a.fault_block && w16 == 0)) mbar_arrive(bar(FULL + 2 * B));
+          if (n >= 2) ok = warp_wait(bar(EMPTY + 2 * B + 1), parity, stop, a.status);
+          if (!ok) break;
+          words(d.b, sb, to + 4 * kSlab + B * kBuf, nope_b);
+          sts(rope + B * kBuf + unit(rope_b ? 0 : w + 1), rope_b ? d.b : d.c);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(FULL + 2 * B + 1));
+          have = fetch(id, off, d);
+          at.step(plan, mine, a.page_size, pages_step, rest);
+          id = lookup(at);
+          off = at.off;
+        }
+      } else {
       // word b of this lane: nope, scales (lane 24) or rope; how its NaN are found
       const uint32_t mb = lane < 24 ? 0x7f7f7f7fu : lane > 24 ? 0x7f807f80u : 0u;
       const uint32_t ab = lane < 24 ? 0x01010101u : 0x00800080u;
@@ -565,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         at.step(plan, mine, a.page_size, pages_step, rest);
         id = lookup(at);
         off = at.off;
+      }
       }
     }
   } else if (warp >= kMmaWarp) {
@@ -786,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 std::mutex g_mu;
 
-template <bool MODS>
+template <bool MODS, bool ROW4>
 cudaError_t launch(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStream_t stream) {
   static bool done[64] = {};
   int dev = 0;
@@ -796,12 +916,12 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStre
   {
     std::lock_guard<std::mutex> lock(g_mu);
     if (!done[dev]) {
-      e = cudaFuncSetAttribute(single_kernel<MODS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      e = cudaFuncSetAttribute(single_kernel<MODS, ROW4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
       // the register split assumes the launch's share: a build that differs is refused,
       // since its increase would never be granted
       cudaFuncAttributes fa;
-      e = cudaFuncGetAttributes(&fa, single_kernel<MODS>);
+      e = cudaFuncGetAttributes(&fa, single_kernel<MODS, ROW4>);
       if (e != cudaSuccess) return e;
       if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
       done[dev] = true;
@@ -811,14 +931,15 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStre
   std::memset(static_cast<void*>(&qmap), 0, sizeof(qmap));
   e = encode_rows(&qmap, a.q, static_cast<int64_t>(a.T) * a.H, kSingleRows);
   if (e != cudaSuccess) return e;
-  return launch_programmatic(single_kernel<MODS>, dim3(workers), dim3(kThreads), kSmem, stream, a, p, qmap);
+  return launch_programmatic(single_kernel<MODS, ROW4>, dim3(workers), dim3(kThreads), kSmem, stream, a, p, qmap);
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_single(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStream_t stream) {
-  return a.cap > 0.f || a.slopes != nullptr ? launch<true>(a, p, workers, stream)
-                                            : launch<false>(a, p, workers, stream);
+  const bool mods = a.cap > 0.f || a.slopes != nullptr;
+  if (is_row4(a.stride)) return mods ? launch<true, true>(a, p, workers, stream) : launch<false, true>(a, p, workers, stream);
+  return mods ? launch<true, false>(a, p, workers, stream) : launch<false, false>(a, p, workers, stream);
 }
 
 }  // namespace smla

@@ -11,7 +11,18 @@ namespace smla {
 
 constexpr int kQkDim = 512;     // q / k width: 448 nope + 64 rope
 constexpr int kNope = 448;      // value / output width
-constexpr int kRowBytes = 584;  // packed KV row
+constexpr int kRowBytes = 584;  // packed KV row, 8-bit values
+// Rows of 4-bit values: 448 e2m1 nibbles, 14 scale bytes (one for 32 columns), 2 of padding, the
+// rope.  A pool's row stride tells which rows it holds.
+constexpr int kRow4Bytes = 368;
+constexpr int kRow4Scales = 224;
+constexpr int kRow4Rope = 240;
+constexpr int kMaxRow4Stride = 512;
+
+__host__ __device__ constexpr bool is_row4(int64_t stride) { return stride <= kMaxRow4Stride; }
+constexpr bool row_stride_ok(int64_t stride) {
+  return is_row4(stride) ? stride >= kRow4Bytes && stride % 16 == 0 : stride >= kRowBytes && stride % 8 == 0;
+}
 constexpr int kMaxSplits = 256;
 constexpr int kMaxCombineSplits = 1024;
 
@@ -82,6 +93,12 @@ cudaError_t launch_simt(const void* q, const void* kv, const int32_t* indices, v
 cudaError_t launch_paged_rows(const int32_t* indices, const int32_t* block_table, int B, int topk,
                               int max_pages, int page_size, int64_t num_rows, int32_t* rows,
                               cudaStream_t stream);
+
+// Sparse decode over 4-bit rows (checked arguments): workspace bytes, and the launches.  block_table
+// null: indices are rows, else positions.  Returns an smla_status.
+size_t sparse4_workspace(const smla_params* p);
+int launch_sparse4(const void* q, const void* kv, const int32_t* indices, const int32_t* block_table, int max_pages,
+                   int page_size, void* out, float* lse, const smla_params* p, void* workspace, cudaStream_t stream);
 
 // SMLA_OK if the current device is a compute capability 10.3 GPU, else an
 // smla_status (SMLA_ERR_UNSUPPORTED_DEVICE or SMLA_ERR_CUDA).

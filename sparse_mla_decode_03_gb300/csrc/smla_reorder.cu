@@ -1,0 +1,219 @@
+// Reordering of the paged cache by parents (smla_cache_reorder): row r of the table goes on from
+// the row that parents[r] names, in place.  Declared and documented in include/smla.h.
+//
+// Two launches.  The first cluster of the plan finds the child that takes each row over (the lowest),
+// gives the pages of rows without a child back, and only then ranks the free pages for the last pages
+// that further children copy, so a beam that is dropped makes room for the one that is doubled.  Its other
+// clusters meanwhile copy the table and the lengths aside, since the second launch overwrites the rows
+// that others still read.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/smla.h"
+#include "smla_cache_host.h"
+#include "smla_cache_plan.cuh"
+#include "smla_cache_rows.cuh"
+#include "smla_internal.h"
+#include "smla_ptx.cuh"
+
+namespace smla {
+namespace {
+
+struct ReorderArgs {
+  uint8_t* pool;
+  int32_t *ref, *table, *kv_lens;
+  const int32_t* parents;
+  int32_t *old_table, *old_lens;      // workspace, as are the lists
+  int32_t *first, *list, *fresh;      // lowest child of each row; free pages taken; the new page of each child
+  int rows, max_pages, page_size, num_pages;
+  int64_t stride;
+  int* status;
+};
+constexpr int kNobody = 0x7fffffff;
+constexpr int kNoPage = -1, kNotNeeded = -2;
+
+// The length of row p that its further children see: within the table.
+__device__ __forceinline__ int parent_length(const ReorderArgs& a, const int32_t* lens, int p) {
+  const int64_t most = static_cast<int64_t>(a.max_pages) * a.page_size;
+  const int len = lens[p];
+  return len < 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(len), most));
+}
+__device__ __forceinline__ int parent_of(const ReorderArgs& a, int r) {
+  const int p = __ldg(a.parents + r);
+  return p < a.rows ? p : -1;
+}
+// Whether child r copies a last page that is partly filled and mapped.
+__device__ __forceinline__ bool takes_page(const ReorderArgs& a, int r) {
+  const int p = parent_of(a, r);
+  if (p < 0 || __ldcg(a.first + p) == r) return false;
+  const int len = parent_length(a, a.kv_lens, p);
+  if (len % a.page_size == 0) return false;
+  const int page = a.table[static_cast<int64_t>(p) * a.max_pages + len / a.page_size];
+  return page >= 0 && page < a.num_pages;
+}
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
+    reorder_plan_kernel(const ReorderArgs a) {
+  __shared__ PlanShared sh;
+  cg::this_cluster().sync();   // every CTA has started: its shared memory may be written
+  grid_dep_wait();
+  grid_dep_launch();
+  if (blockIdx.x >= kPlanCtas) {
+    const int64_t entries = static_cast<int64_t>(a.rows) * a.max_pages;
+    const int64_t step = static_cast<int64_t>(gridDim.x - kPlanCtas) * kPlanThreads;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x - kPlanCtas) * kPlanThreads + threadIdx.x;
+    for (int64_t i = i0; i < entries; i += step) a.old_table[i] = a.table[i];
+    for (int64_t i = i0; i < a.rows; i += step) a.old_lens[i] = a.kv_lens[i];
+    return;
+  }
+  const int me = static_cast<int>(blockIdx.x) * kPlanThreads + static_cast<int>(threadIdx.x);
+  constexpr int kAll = kPlanCtas * kPlanThreads;
+  for (int r = me; r < a.rows; r += kAll) a.first[r] = kNobody;
+  cg::this_cluster().sync();
+  for (int r = me; r < a.rows; r += kAll) {
+    const int p = __ldg(a.parents + r);
+    if (p >= a.rows) report(a.status, SMLA_ERR_INDEX_RANGE);
+    else if (p >= 0) atomicMin(a.first + p, r);
+  }
+  cg::this_cluster().sync();
+  // rows that nobody goes on from: a warp each
+  const int lane = threadIdx.x & 31;
+  for (int r = me / 32; r < a.rows; r += kAll / 32) {
+    if (__ldcg(a.first + r) != kNobody) continue;
+    const int32_t* e = a.table + static_cast<int64_t>(r) * a.max_pages;
+    for (int i = lane; i < a.max_pages; i += 32) {
+      const int page = e[i];
+      if (page >= a.num_pages) {
+        report(a.status, SMLA_ERR_INDEX_RANGE);
+      } else if (page >= 0 && atomicSub(a.ref + page, 1) <= 0) {
+        atomicAdd(a.ref + page, 1);
+        report(a.status, SMLA_ERR_INDEX_RANGE);
+      }
+    }
+  }
+  cg::this_cluster().sync();
+  const Part rp = part_of(a.rows), pp = part_of(a.num_pages);
+  int free_total, need_total, mine = 0;
+  const int free_rank = block_rank(count_free(a.ref, pp), &free_total, &sh);
+  for (int r = static_cast<int>(rp.run0); r < static_cast<int>(rp.run1); ++r) mine += takes_page(a, r);
+  const int need_rank = block_rank(mine, &need_total, &sh);
+  int2 low;
+  const int2 all = cluster_share(make_int2(need_total, free_total), 0, &low, &sh);
+  const int got = min(all.x, all.y);
+  take_free(a.ref, pp, low.y + free_rank, got, a.list);
+  cg::this_cluster().sync();
+  int k = low.x + need_rank;
+  for (int r = static_cast<int>(rp.run0); r < static_cast<int>(rp.run1); ++r) {
+    int f = kNotNeeded;
+    if (takes_page(a, r)) {
+      f = k < got ? __ldcg(a.list + k) : kNoPage;
+      ++k;
+      if (f == kNoPage) report(a.status, SMLA_ERR_POOL_EXHAUSTED);
+    }
+    a.fresh[r] = f;
+  }
+}
+
+constexpr int kCopyRows = 16;   // rows of a partial page that one CTA copies
+
+// Grid (rows, row groups of a page): group 0 also writes the row of the table.
+__global__ void __launch_bounds__(256) reorder_apply_kernel(const ReorderArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int r = blockIdx.x, p = parent_of(a, r);
+  int32_t* dst = a.table + static_cast<int64_t>(r) * a.max_pages;
+  const int fresh = a.fresh[r];
+  if (p < 0 || fresh == kNoPage) {
+    if (blockIdx.y != 0) return;
+    for (int e = threadIdx.x; e < a.max_pages; e += blockDim.x) dst[e] = -1;
+    if (threadIdx.x == 0) a.kv_lens[r] = 0;
+    return;
+  }
+  const int32_t* src = a.old_table + static_cast<int64_t>(p) * a.max_pages;
+  if (a.first[p] == r) {        // takes the row over as it is
+    if (p == r || blockIdx.y != 0) return;
+    for (int e = threadIdx.x; e < a.max_pages; e += blockDim.x) dst[e] = src[e];
+    if (threadIdx.x == 0) a.kv_lens[r] = a.old_lens[p];
+    return;
+  }
+  const int len = parent_length(a, a.old_lens, p), full = len / a.page_size, rem = len % a.page_size;
+  if (blockIdx.y == 0) {
+    for (int e = threadIdx.x; e < a.max_pages; e += blockDim.x) {
+      int v = -1;
+      if (e < full) v = src[e];
+      else if (e == full && rem > 0) v = fresh >= 0 ? fresh : src[e];
+      if (v >= a.num_pages) report(a.status, SMLA_ERR_INDEX_RANGE);
+      else if (v >= 0 && e < full) atomicAdd(a.ref + v, 1);
+      dst[e] = v;
+    }
+    if (threadIdx.x == 0) {
+      a.kv_lens[r] = len;
+      if (a.old_lens[p] != len) report(a.status, SMLA_ERR_INDEX_RANGE);
+    }
+  }
+  if (fresh < 0) return;
+  const int64_t from = static_cast<int64_t>(src[full]) * a.page_size, to = static_cast<int64_t>(fresh) * a.page_size;
+  for (int r0 = blockIdx.y * kCopyRows; r0 < rem; r0 += gridDim.y * kCopyRows)
+    copy_rows(a.pool, a.stride, from + r0, to + r0, min(kCopyRows, rem - r0));
+}
+
+// The workspace; base may be null to size it.
+size_t lay_out(const smla_cache_params* c, char* base, ReorderArgs* a) {
+  size_t at = 0;
+  auto take = [&](size_t ints) {
+    int32_t* p = reinterpret_cast<int32_t*>(base + at);
+    at += round256(4 * ints);
+    return p;
+  };
+  const size_t rows = static_cast<size_t>(c->num_seqs);
+  a->first = take(rows);
+  a->list = take(rows);
+  a->fresh = take(rows);
+  a->old_lens = take(rows);
+  a->old_table = take(rows * c->max_pages);
+  return at;
+}
+
+}  // namespace
+}  // namespace smla
+
+using namespace smla;   // NOLINT: the entry points below are this file's own
+
+extern "C" {
+
+int smla_cache_reorder_workspace_size(const smla_cache_params* c, size_t* bytes) {
+  const int st = check_cache(c);
+  if (st != SMLA_OK) return st;
+  if (bytes == nullptr) return SMLA_ERR_INVALID_ARG;
+  ReorderArgs a;
+  *bytes = lay_out(c, nullptr, &a);
+  return SMLA_OK;
+}
+
+int smla_cache_reorder(void* kv_pages, int32_t* ref_count, int32_t* block_table, int32_t* kv_lens,
+                       const int32_t* parents, const smla_cache_params* c, void* workspace,
+                       size_t workspace_bytes, smla_stream_t stream) {
+  int st = check_cache(c);
+  if (st != SMLA_OK) return st;
+  if (!pool_ok(kv_pages, c) || !ints_ok(ref_count) || !ints_ok(block_table) || !ints_ok(kv_lens) || !ints_ok(parents))
+    return SMLA_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256)) return SMLA_ERR_INVALID_ARG;
+  ReorderArgs a = {static_cast<uint8_t*>(kv_pages), ref_count, block_table, kv_lens, parents, nullptr, nullptr,
+                   nullptr, nullptr, nullptr, c->num_seqs, c->max_pages, c->page_size, c->num_pages,
+                   c->kv_row_stride, nullptr};
+  if (workspace_bytes < lay_out(c, static_cast<char*>(workspace), &a)) return SMLA_ERR_WORKSPACE_TOO_SMALL;
+  st = ready(&a.status);
+  if (st != SMLA_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // clusters that copy the table aside: eight entries a thread
+  const int64_t entries = static_cast<int64_t>(c->num_seqs) * c->max_pages;
+  const int64_t copies = (entries - 1) / (8 * kPlanCtas * kPlanThreads) + 1;
+  const unsigned clusters = 1 + static_cast<unsigned>(copies < 18 ? copies : 18);
+  st = done(launch_programmatic(reorder_plan_kernel, dim3(clusters * kPlanCtas), dim3(kPlanThreads), 0, s, a));
+  if (st != SMLA_OK) return st;
+  const int groups = (c->page_size - 1) / kCopyRows + 1;
+  return done(launch_programmatic(reorder_apply_kernel, dim3(c->num_seqs, groups < 64 ? groups : 64), dim3(256), 0, s, a));
+}
+
+}  // extern "C"
