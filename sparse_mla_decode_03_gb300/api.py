@@ -634,9 +634,9 @@ def smla_beam_workspace_size(params: _lib.SmlaBeamParams) -> int:
 
 
 @functools.lru_cache(maxsize=256)
-def _beam_bytes(groups: int, beams: int, vocab: int, num_out: int) -> int:
-    """What smla_beam_workspace_size says: a matter of these sizes alone."""
-    return smla_beam_workspace_size(make_beam_params(groups, beams, vocab, num_out))
+def _beam_bytes(groups: int, beams: int, vocab: int, num_out: int, logits_type: int) -> int:
+    """What smla_beam_workspace_size says: a matter of these sizes and the type alone."""
+    return smla_beam_workspace_size(make_beam_params(groups, beams, vocab, num_out, logits_type=logits_type))
 
 
 def smla_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: Optional[int] = None,
@@ -674,7 +674,7 @@ def smla_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: Option
             raise ValueError(f"{name} must be contiguous {dtype} [{G}, {n}] on {dev}")
         got.append(t)
     if workspace is None:
-        workspace = _empty(side, _beam_bytes(G, K, V, n), torch.uint8, dev)
+        workspace = _empty(side, _beam_bytes(G, K, V, n, _LOGITS[logits.dtype]), torch.uint8, dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     with _on(dev):

@@ -3,12 +3,11 @@
 //
 // For row r = group * beams + beam with logits x and score c, a candidate's value is
 //     c + (x - M) - ln sum exp(x - M),     M = max x,
-// and each group's num_out largest are wanted.  Two launches: segments of 8,192 logits each leave
-// their maximum, their sum of exponentials and their own num_out best; a CTA a group joins them.
-//
-// The logits are read once, into registers.  Best of a segment: the largest logits of 2 num_out (or
-// more) parts of it have a num_out-th largest, which at least num_out logits reach and few others
-// do, so those go to a list in shared memory that is ranked by counting.
+// and each group's num_out largest are wanted.  Two launches.  The first reads the logits once: warps
+// go over runs of them, 2 KB (a step) at a time, and leave each step's maximum and each run's sum of
+// exponentials; they meet nobody and keep no candidates.  The second, a CTA a group, finds a border from
+// the maxima that at least num_out candidates reach and few steps do, reads those few steps again, and
+// ranks what reaches the border by counting.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -23,13 +22,17 @@
 namespace smla {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;                     // of the CTA that joins a group
 constexpr int kWarps = kThreads / 32;
-constexpr int kEach = 32;                         // logits of a thread
-constexpr int kSegment = kThreads * kEach;
+constexpr int kRunWarps = 4;                      // of a CTA that goes over runs
+constexpr int kRegs = 16;                         // registers of a lane's logits
+template <class T>
+constexpr int kEach = 4 * kRegs / static_cast<int>(sizeof(T));        // logits of a lane: 16 or 32
+template <class T>
+constexpr int kStep = 32 * kEach<T>;              // of a warp
 constexpr int kMaxOut = 64;
-constexpr int kList = 1024;                       // candidates of a segment that are ranked by counting
-constexpr unsigned long long kNone = 0;           // no candidate: below every key
+constexpr int kList = 512;                        // candidates that are ranked by counting
+constexpr int kBlocks = 512;                      // steps that are read again
 
 struct BeamArgs {
   const void* logits;
@@ -38,10 +41,10 @@ struct BeamArgs {
   const uint8_t* finished;
   int32_t *parents, *tokens;
   float* out_scores;
-  // workspace: [row][segment] of maximum and sum, [row][segment][num_out] of keys, descending
+  // workspace: [row][run] of maximum and sum, [row][step] of maximum
   float2* stats;
-  unsigned long long* best;
-  int beams, vocab, num_out, segments, end_token;
+  float* maxima;
+  int rows, beams, vocab, num_out, steps, runs, end_token;      // steps of a row, and its runs
   int* status;
 };
 
@@ -60,25 +63,26 @@ __device__ __forceinline__ unsigned long long key_of(float x, int token) {
 __device__ __forceinline__ float key_value(unsigned long long k) { return unsortable(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ int key_token(unsigned long long k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
 
-// The largest key of the warp, in every lane.
-__device__ __forceinline__ unsigned long long warp_max(unsigned long long k) {
-  const uint32_t hi = static_cast<uint32_t>(k >> 32), top = __reduce_max_sync(0xffffffffu, hi);
-  const uint32_t lo = __reduce_max_sync(0xffffffffu, hi == top ? static_cast<uint32_t>(k) : 0u);
-  return static_cast<unsigned long long>(top) << 32 | lo;
+// Lanes of a part, so that there are at least four times as many parts of a CTA as results.
+__device__ __forceinline__ int part_lanes(int num_out) { return num_out <= 8 ? 16 : num_out <= 16 ? 8 : num_out <= 32 ? 4 : 2; }
+// The num_out-th largest maximum of the CTA's parts, given each thread's; -infinity counts.  All threads call;
+// the answer is in *least after a barrier.
+__device__ __forceinline__ void part_maximum(float mine, int lanes, float* part) {
+  for (int o = 1; o < lanes; o <<= 1) mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, o));
+  if (threadIdx.x % lanes == 0) part[threadIdx.x / lanes] = mine;
 }
-
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+__device__ __forceinline__ void rank_parts(const float* part, int lanes, int num_out, float* least) {
+  const int parts = kThreads / lanes, t = threadIdx.x;
+  if (t >= parts) return;
+  const float p = part[t];
+  int rank = 0;
+  for (int j = 0; j < parts; j += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(part + j);
+    rank += (v.x > p || (v.x == p && j < t)) + (v.y > p || (v.y == p && j + 1 < t)) + (v.z > p || (v.z == p && j + 2 < t)) +
+            (v.w > p || (v.w == p && j + 3 < t));
+  }
+  if (rank == num_out - 1) *least = p;
 }
-// e^d for d <= 0: log2(e) in two parts, since the first alone is off by 1.3e-8 and every term of a sum
-// by 1e-7 in the same direction.
-__device__ __forceinline__ float exp_of(float d) { return exp2_fast(fmaf(d, 1.44269502162933349609f, d * 1.92596299e-8f)); }
 
 // Words of 16, 4 or 2 bytes.
 template <int BYTES>
@@ -90,121 +94,174 @@ struct Word<4> { using type = unsigned int; };
 template <>
 struct Word<2> { using type = unsigned short; };
 
-// BYTES: of a load, what the start of every row is aligned to.  Which thread adds which logits goes by
+// A thread's logits as they lie in memory, two of 16 bits to a register, and the maxima of its quarters.
+template <class T>
+struct Held;
+template <>
+struct Held<float> {
+  static constexpr uint32_t kNothing = 0xff800000u;      // -infinity
+  uint32_t w[kRegs];
+  __device__ __forceinline__ float at(int i) const { return __uint_as_float(w[i]); }
+  __device__ __forceinline__ float top(int quarter) const {
+    float m = at(quarter * kRegs / 4);
+#pragma unroll
+    for (int i = 1; i < kRegs / 4; ++i) m = fmaxf(m, at(quarter * kRegs / 4 + i));
+    return m;
+  }
+};
+template <class T>
+struct Held16 {
+  uint32_t w[kRegs];
+  __device__ __forceinline__ float at(int i) const { return i % 2 ? T::high(w[i / 2]) : T::low(w[i / 2]); }
+  __device__ __forceinline__ float top(int quarter) const {
+    uint32_t m = w[quarter * kRegs / 4];
+#pragma unroll
+    for (int i = 1; i < kRegs / 4; ++i) m = T::max(m, w[quarter * kRegs / 4 + i]);
+    return fmaxf(T::low(m), T::high(m));
+  }
+};
+struct Bf16 {
+  static __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+};
+struct Fp16 {
+  static __device__ __forceinline__ float low(uint32_t w) { return __half2float(__ushort_as_half(static_cast<unsigned short>(w))); }
+  static __device__ __forceinline__ float high(uint32_t w) { return __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16))); }
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+};
+template <>
+struct Held<__nv_bfloat16> : Held16<Bf16> {
+  static constexpr uint32_t kNothing = 0xff80u;
+};
+template <>
+struct Held<__half> : Held16<Fp16> {
+  static constexpr uint32_t kNothing = 0xfc00u;
+};
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+
+// log2(e) in two parts, since the first alone is off by 1.3e-8 and every term of a sum by 1e-7 in the same
+// direction.
+constexpr float kLog2e0 = 1.44269502162933349609f, kLog2e1 = 1.92596299e-8f;
+// e^d for two d <= 0
+__device__ __forceinline__ Two exp_of(Two d) {
+  float x, y;
+  fma2(d, Two(kLog2e0), d * Two(kLog2e1)).get(&x, &y);
+  return Two(exp2_fast(x), exp2_fast(y));
+}
+
+// The row's last logits, element by element; out of line, once a row.
+template <class T>
+__device__ __noinline__ uint4 load_last(const T* base, int at, int vocab) {
+  uint32_t v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      v[k] = at + k < vocab ? reinterpret_cast<const uint32_t*>(base)[at + k] : Held<T>::kNothing;
+    } else {
+      const unsigned short* half = reinterpret_cast<const unsigned short*>(base);
+      const uint32_t lo = at + 2 * k < vocab ? half[at + 2 * k] : Held<T>::kNothing;
+      const uint32_t hi = at + 2 * k + 1 < vocab ? half[at + 2 * k + 1] : Held<T>::kNothing;
+      v[k] = lo | hi << 16;
+    }
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <class T, int BYTES>
+__device__ __forceinline__ void load_step(const T* base, int first, int vocab, Held<T>& x) {
+  constexpr int kPer = BYTES / sizeof(T), kWords = kEach<T> / kPer;       // logits of a word; words a lane
+#pragma unroll
+  for (int j = 0; j < kWords; ++j) {
+    const int at = first + j * 32 * kPer;
+    const bool whole = at + kPer <= vocab;
+    const auto* from = reinterpret_cast<const typename Word<BYTES>::type*>(base + at);
+    constexpr uint32_t kNothing = Held<T>::kNothing, kTwo = sizeof(T) == 4 ? kNothing : kNothing * 0x10001u;
+    if constexpr (BYTES == 16) {
+      uint4 w = make_uint4(kTwo, kTwo, kTwo, kTwo);
+      if (whole) w = __ldcs(from);
+      else if (at < vocab) w = load_last(base, at, vocab);
+      x.w[4 * j] = w.x;
+      x.w[4 * j + 1] = w.y;
+      x.w[4 * j + 2] = w.z;
+      x.w[4 * j + 3] = w.w;
+    } else if constexpr (BYTES == 4) {
+      uint32_t w = kTwo;
+      if (whole) w = __ldcs(from);
+      else if (at < vocab) w = load_last(base, at, vocab).x;       // the first of two
+      x.w[j] = w;
+    } else {
+      const uint32_t w = whole ? __ldcs(from) : static_cast<unsigned short>(kNothing);
+      if (j % 2 == 0) x.w[j / 2] = w;
+      else x.w[j / 2] |= w << 16;
+    }
+  }
+}
+
+// BYTES: of a load, what the start of every row is aligned to.  Which lane adds which logits goes by
 // their place in the row alone, so that equal rows have equal sums, and ties are ties.
 template <class T, int BYTES>
-__global__ void __launch_bounds__(kThreads) segment_kernel(const BeamArgs a) {
-  constexpr int kPer = BYTES / sizeof(T), kVecs = kEach / kPer;       // logits of a word; words a thread
-  __shared__ float part[2 * kMaxOut], warp_top[kWarps], warp_sum[kWarps];
-  __shared__ float least;
-  __shared__ int count;
-  __shared__ unsigned long long list[kList];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int seg = blockIdx.x, row = blockIdx.y;
+__global__ void __launch_bounds__(kRunWarps * 32, 8) run_kernel(const BeamArgs a) {
+  constexpr int kPer = BYTES / sizeof(T);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dep_wait();
   grid_dep_launch();
-  if (a.finished != nullptr && a.finished[row] != 0) return;
-  if (tid == 0) {
-    count = 0;
-    least = INFINITY;
-  }
+  const int64_t slot = static_cast<int64_t>(blockIdx.x) * kRunWarps + warp;
+  const int row = static_cast<int>(slot / a.runs), run = static_cast<int>(slot % a.runs);
+  if (row >= a.rows || (a.finished != nullptr && a.finished[row] != 0)) return;
   const T* base = static_cast<const T*>(a.logits) + row * a.row_stride;
-  const int first = seg * kSegment + tid * kPer;            // of word 0
-  float x[kEach];
+  const int step0 = static_cast<int>(static_cast<int64_t>(run) * a.steps / a.runs);
+  const int step1 = static_cast<int>(static_cast<int64_t>(run + 1) * a.steps / a.runs);
+  auto begin = [&](int step) { return step * kStep<T> + lane * kPer; };            // of the lane's word 0
+  float* maxima = a.maxima + static_cast<int64_t>(row) * a.steps;
+  float top = -INFINITY, sum = 0.f;
+  Held<T> x, next;
+  load_step<T, BYTES>(base, begin(step0), a.vocab, next);
+  for (int step = step0; step < step1; ++step) {
+    x = next;
+    // the next step's logits are on their way meanwhile
+    if (step + 1 < step1) load_step<T, BYTES>(base, begin(step + 1), a.vocab, next);
+    float m = fmaxf(fmaxf(x.top(0), x.top(1)), fmaxf(x.top(2), x.top(3)));
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    const int at = first + j * kThreads * kPer;
-    if (at + kPer <= a.vocab) {
-      const auto w = __ldcs(reinterpret_cast<const typename Word<BYTES>::type*>(base + at));
-      const T* v = reinterpret_cast<const T*>(&w);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) maxima[step] = m;
+    if (m > top) {               // the same in all lanes
+      float f, none;
+      exp_of(Two(top - m, 0.f)).get(&f, &none);
+      sum *= f;                  // 0 while the maximum is -infinity
+      top = m;
+    }
+    if (top == -INFINITY) {      // nothing but -infinity, or NaN, which a maximum drops
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) x[j * kPer + e] = to_float(v[e]);
+      for (int i = 0; i < kEach<T>; ++i)
+        if (const float v = x.at(i); v != v) sum = v;
     } else {
+      Two sum0(0.f), sum1(0.f);
+      const Two shift(-top);
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) x[j * kPer + e] = at + e < a.vocab ? to_float(base[at + e]) : -INFINITY;
-    }
-  }
-  auto token = [&](int i) { return first + (i / kPer) * kThreads * kPer + i % kPer; };
-  float mine = x[0];
-#pragma unroll
-  for (int i = 1; i < kEach; ++i) mine = fmaxf(mine, x[i]);
-  // maxima of the parts: 16, 32, 64 or 128 of them
-  const int lanes = a.num_out <= 8 ? 16 : a.num_out <= 16 ? 8 : a.num_out <= 32 ? 4 : 2, parts = kThreads / lanes;
-  float top = mine;
-  for (int o = 1; o < 32; o <<= 1) {
-    if (o == lanes && lane % lanes == 0) part[tid / lanes] = top;
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  }
-  if (lane == 0) warp_top[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, warp_top[w]);
-  if (tid < parts) {
-    const float p = part[tid];
-    int rank = 0;
-    for (int j = 0; j < parts; ++j) rank += part[j] > p || (part[j] == p && j < tid);
-    if (rank == a.num_out - 1) least = fmaxf(p, -3.402823466e38f);   // -infinity is no candidate
-  }
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  if (top == -INFINITY) {        // nothing but -infinity, or NaN, which a maximum drops
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (x[i] != x[i]) sum[0] = x[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) sum[i % 4] += exp_of(x[i] - top);
-  }
-  float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) warp_sum[warp] = s;
-  __syncthreads();
-  if (mine >= least) {
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (x[i] >= least) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kList) list[at] = key_of(x[i], token(i));
+      for (int i = 0; i < kEach<T>; i += 4) {
+        sum0 = sum0 + exp_of(Two(x.at(i), x.at(i + 1)) + shift);
+        sum1 = sum1 + exp_of(Two(x.at(i + 2), x.at(i + 3)) + shift);
       }
-  }
-  const int64_t slot = static_cast<int64_t>(row) * a.segments + seg;
-  if (tid == 0) {
-    float all = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) all += warp_sum[w];
-    a.stats[slot] = make_float2(top, all);        // a NaN or +infinity leaves a sum that is not finite
-  }
-  __syncthreads();
-  unsigned long long* out = a.best + slot * a.num_out;
-  const int n = count;
-  if (n <= kList) {
-    for (int i = tid; i < n; i += kThreads) {
-      const unsigned long long k = list[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += list[j] > k;
-      if (rank < a.num_out) out[rank] = k;
+      float s0, s1;
+      (sum0 + sum1).get(&s0, &s1);
+      sum += s0 + s1;
     }
-    for (int i = n + tid; i < a.num_out; i += kThreads) out[i] = kNone;
-    return;
   }
-  // more equal logits than the list holds: one after the other, each the largest below the last
-  unsigned long long last = ~0ull;
-  for (int i = 0; i < a.num_out; ++i) {
-    unsigned long long k = kNone;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const unsigned long long c = x[j] >= least ? key_of(x[j], token(j)) : kNone;
-      if (c < last && c > k) k = c;
-    }
-    k = warp_max(k);
-    __syncthreads();
-    if (lane == 0) list[warp] = k;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) k = list[w] > k ? list[w] : k;
-    if (tid == 0) out[i] = k;
-    last = k;
-  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) a.stats[slot] = make_float2(top, sum);        // a NaN or +infinity leaves a sum that is not finite
 }
 
 // ln x for x >= 1, in 64 bits where 32 would round the whole: the power of two apart, the rest in
@@ -223,121 +280,234 @@ __device__ __forceinline__ unsigned long long sortable64(double x) {
   return (b >> 63) ? ~b : b | 0x8000000000000000ull;
 }
 
-constexpr int kHeld = 16;          // keys of a lane while a beam's lists are joined
+// A beam of a group: what its keys' values are made of.  kDead: no candidates; kDone: one, the end.
+enum BeamState : int { kDead, kDone, kLive };
+struct Beam {
+  double score, top, log_sum;
+  float near;             // score - log_sum in 32 bits
+  int state;
+};
 
-// A CTA a group.  A warp joins the segments of a beam, beam after beam; then one warp takes the
-// group's best, one at a time, from the heads of the beams' lists.
+// A candidate of a group: larger values first, then the lower beam, then the lower token.
+struct Candidate {
+  unsigned long long value;        // sortable; 0: none
+  unsigned long long place;        // beam and token
+};
+__device__ __forceinline__ bool before(const Candidate& a, const Candidate& b) {
+  return a.value > b.value || (a.value == b.value && a.place < b.place);
+}
+
+// A CTA a group.
+template <class T, int BYTES>
 __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
-  extern __shared__ unsigned long long lists[];          // [beams][num_out] keys
-  __shared__ double base[kMaxOut], shift[kMaxOut], log_sum[kMaxOut];       // of a beam: score, M, ln sum
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int group = blockIdx.x, n = a.num_out;
+  constexpr int kPer = BYTES / sizeof(T);
+  __shared__ Beam beam[kMaxOut];
+  __shared__ float4 part4[kThreads / 8];
+  __shared__ float least;
+  __shared__ int count, blocks;
+  __shared__ int block[kBlocks];                 // step * beams + beam
+  __shared__ Candidate list[kStep<__half> + kMaxOut];
+  __shared__ Candidate best[kMaxOut];
+  static_assert(kList <= kStep<__half> + kMaxOut, "one list for both paths");
+  float* part = reinterpret_cast<float*>(part4);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = blockIdx.x, n = a.num_out, row0 = group * a.beams;
   grid_dep_wait();
   grid_dep_launch();
+  if (tid == 0) {
+    count = blocks = 0;
+    least = INFINITY;
+  }
   for (int b = warp; b < a.beams; b += kWarps) {
-    const int row = group * a.beams + b;
-    const float score = a.scores[row];
-    unsigned long long* mine = lists + b * n;
-    if (a.finished != nullptr && a.finished[row] != 0) {
-      const bool fine = fabsf(score) < INFINITY;
-      for (int i = lane; i < n; i += 32) mine[i] = i == 0 && fine ? key_of(0.f, a.end_token) : kNone;
-      if (lane == 0) {
-        base[b] = score;
-        shift[b] = log_sum[b] = 0.0;
-        if (!fine && score != -INFINITY) report_range(a.status);
+    const float score = a.scores[row0 + b];
+    Beam m = {score, 0.0, 0.0, score, kDead};
+    bool bad = !(fabsf(score) < INFINITY) && score != -INFINITY;
+    if (a.finished != nullptr && a.finished[row0 + b] != 0) {
+      m.state = kDone;
+    } else {
+      const float2* stats = a.stats + static_cast<int64_t>(row0 + b) * a.runs;
+      float top = -INFINITY, sum = 0.f;
+      bool odd = false;
+      for (int s = lane; s < a.runs; s += 32) {
+        const float2 t = stats[s];
+        top = fmaxf(top, t.x);
+        odd |= !(t.y < INFINITY);
       }
-      continue;
-    }
-    const float2* stats = a.stats + static_cast<int64_t>(row) * a.segments;
-    float top = -INFINITY;
-    bool bad = false;
-    for (int s = lane; s < a.segments; s += 32) {
-      const float2 t = stats[s];
-      top = fmaxf(top, t.x);
-      bad |= !(t.y < INFINITY);
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float sum = 0.f;
-    for (int s = lane; s < a.segments; s += 32) {
-      const float2 t = stats[s];
-      if (t.y > 0.f) sum = fmaf(t.y, exp_of(t.x - top), sum);
-    }
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int s = lane; s < a.runs; s += 32) {
+        const float2 t = stats[s];
+        float w, none;
+        exp_of(Two(t.x - top, 0.f)).get(&w, &none);
+        if (t.y > 0.f) sum = fmaf(t.y, w, sum);
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    bad = __any_sync(0xffffffffu, bad) || (!(fabsf(score) < INFINITY) && score != -INFINITY);
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      bad |= __any_sync(0xffffffffu, odd);
+      if (!bad && top > -INFINITY) {
+        m.top = top;
+        m.log_sum = log_of(sum);
+        m.near = static_cast<float>(m.score - m.log_sum);
+        m.state = kLive;
+      }
+    }
+    if (bad || score == -INFINITY) m.state = kDead;
     if (bad && lane == 0) report_range(a.status);
-    const bool empty = bad || top == -INFINITY || score == -INFINITY;
-    if (lane == 0) {
-      base[b] = score;
-      shift[b] = top;
-      log_sum[b] = empty ? 0.0 : log_of(sum);
-    }
-    // the n largest of segments * n keys: the best so far and the next ones, kHeld a lane at a time
-    const unsigned long long* best = a.best + static_cast<int64_t>(row) * a.segments * n;
-    const int64_t total = empty ? 0 : static_cast<int64_t>(a.segments) * n;
-    for (int i = lane; i < n; i += 32) mine[i] = kNone;
-    __syncwarp();
-    for (int64_t at = 0; at < total; at += 32 * (kHeld - 2)) {
-      unsigned long long held[kHeld];
-#pragma unroll
-      for (int i = 0; i < kHeld - 2; ++i) {
-        const int64_t j = at + i * 32 + lane;
-        held[i] = j < total ? best[j] : kNone;
-      }
-      held[kHeld - 2] = lane < n ? mine[lane] : kNone;
-      held[kHeld - 1] = lane + 32 < n ? mine[lane + 32] : kNone;
-      __syncwarp();
-      for (int i = 0; i < n; ++i) {
-        unsigned long long k = held[0];
-#pragma unroll
-        for (int j = 1; j < kHeld; ++j) k = held[j] > k ? held[j] : k;
-        k = warp_max(k);
-#pragma unroll
-        for (int j = 0; j < kHeld; ++j) held[j] = held[j] == k ? kNone : held[j];
-        if (lane == 0) mine[i] = k;
-      }
-      __syncwarp();
-    }
+    if (lane == 0) beam[b] = m;
   }
   __syncthreads();
-  if (warp != 0) return;
   // x - M first: logits of any size keep their differences; the logarithm last: what is equal but for
   // rounding in beams of equal sums stays equal
-  auto value = [&](int b, unsigned long long k) {
-    return (base[b] + (static_cast<double>(key_value(k)) - shift[b])) - log_sum[b];
+  auto candidate = [&](float x, int token, int b) {
+    const Beam& m = beam[b];
+    Candidate c;
+    c.value = sortable64((m.score + (static_cast<double>(x == 0.f ? 0.f : x) - m.top)) - m.log_sum);      // -0 is 0
+    c.place = static_cast<unsigned long long>(b) << 32 | static_cast<uint32_t>(token);
+    return c;
   };
-  // the heads of beams lane and lane + 32
-  int at[2] = {0, 0};
-  auto head = [&](int i) {
-    const int b = lane + 32 * i;
-    const unsigned long long k = b < a.beams && at[i] < n ? lists[b * n + at[i]] : kNone;
-    return k == kNone ? 0ull : sortable64(value(b, k));
+  // In 32 bits the value of logit x is off by less than `off`: *low and the result are below and above it.
+  auto nearly = [&](float x, int b, float* low) {
+    const float near = beam[b].near, d = x - static_cast<float>(beam[b].top);
+    const float v = near + d, off = 0x1p-21f * (fabsf(near) + fabsf(d));
+    *low = v - off;
+    return v + off;
   };
-  unsigned long long h[2] = {head(0), head(1)};
-  for (int i = 0; i < n; ++i) {
-    const int own = h[1] > h[0] ? 1 : 0;              // equal: the lower beam
-    const unsigned long long v = own ? h[1] : h[0], k = warp_max(v);
-    const int beam = static_cast<int>(__reduce_min_sync(0xffffffffu, v == k ? lane + 32 * own : 0x7fffffffu));
-    const int64_t o = static_cast<int64_t>(group) * n + i;
-    if (k == 0) {
-      if (lane == 0) {
-        a.parents[o] = a.tokens[o] = -1;
-        a.out_scores[o] = -INFINITY;
-      }
-      continue;
-    }
-    if (beam % 32 == lane) {
-      const int w = beam / 32;
-      const unsigned long long c = lists[beam * n + at[w]];
-      a.parents[o] = group * a.beams + beam;
-      a.tokens[o] = key_token(c);
-      a.out_scores[o] = static_cast<float>(value(beam, c));
-      ++at[w];
-      h[w] = head(w);
-    }
-    __syncwarp();
+  // The largest logit of a step of a beam; of a finished one the first step has one candidate, as a logit of 0.
+  auto maximum = [&](int step, int b) {
+    if (beam[b].state == kLive) return a.maxima[static_cast<int64_t>(row0 + b) * a.steps + step];
+    return beam[b].state == kDone && step == 0 ? 0.f : -INFINITY;
+  };
+  const int lanes = part_lanes(n), all = a.beams * a.steps;
+  float mine = -INFINITY;
+  for (int i = tid; i < all; i += kThreads) {
+    // neighbours are of different beams: a part's maximum is then seldom that of a beam far behind
+    const int b = i % a.beams;
+    const float x = maximum(i / a.beams, b);
+    float low;
+    nearly(x, b, &low);
+    if (x > -INFINITY) mine = fmaxf(mine, low);
   }
+  part_maximum(mine, lanes, part);
+  __syncthreads();
+  rank_parts(part, lanes, n, &least);
+  __syncthreads();
+  for (int i = tid; i < all; i += kThreads) {
+    const int b = i % a.beams;
+    const float x = maximum(i / a.beams, b);
+    float low;
+    if (x == -INFINITY || nearly(x, b, &low) < least) continue;
+    const int at = atomicAdd(&blocks, 1);
+    if (at < kBlocks) block[at] = i;
+  }
+  __syncthreads();
+  // f(beam, held logits, token of the lane's word 0) for the warp's blocks
+  auto each_block = [&](auto f) {
+    for (int j = warp; j < min(blocks, kBlocks); j += kWarps) {
+      const int b = block[j] % a.beams, first = block[j] / a.beams * kStep<T> + lane * kPer;
+      Held<T> x;
+      if (beam[b].state == kLive)
+        load_step<T, BYTES>(static_cast<const T*>(a.logits) + (row0 + b) * a.row_stride, first, a.vocab, x);
+      f(b, x, first);
+    }
+  };
+  float border = least;
+  if (border == -INFINITY) {
+    // fewer steps than results: the border from the logits themselves
+    __syncthreads();
+    mine = -INFINITY;
+    each_block([&](int b, const Held<T>& x, int) {
+      if (beam[b].state != kLive) return;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float low;
+        nearly(x.top(k), b, &low);
+        if (x.top(k) > -INFINITY) mine = fmaxf(mine, low);
+      }
+    });
+    part_maximum(mine, lanes, part);
+    __syncthreads();
+    rank_parts(part, lanes, n, &least);
+    __syncthreads();
+    border = least;
+  }
+  each_block([&](int b, const Held<T>& x, int first) {
+    if (beam[b].state == kDone) {
+      float low;
+      if (lane == 0 && nearly(0.f, b, &low) >= border) {
+        const int at = atomicAdd(&count, 1);
+        if (at < kList) list[at] = {key_of(0.f, a.end_token), static_cast<unsigned long long>(b)};
+      }
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float low;
+      if (x.top(k) == -INFINITY || nearly(x.top(k), b, &low) < border) continue;
+#pragma unroll
+      for (int i = k * (kEach<T> / 4); i < (k + 1) * (kEach<T> / 4); ++i) {
+        const float v = x.at(i);
+        if (v == -INFINITY || nearly(v, b, &low) < border) continue;
+        const int at = atomicAdd(&count, 1);
+        // the logit and its place; made a candidate below
+        if (at < kList) list[at] = {key_of(v, first + (i / kPer) * 32 * kPer + i % kPer), static_cast<unsigned long long>(b)};
+      }
+    }
+  });
+  __syncthreads();
+  auto put = [&](int i, const Candidate& c) {
+    const int64_t o = static_cast<int64_t>(group) * n + i;
+    const int b = static_cast<int>(c.place >> 32);
+    a.parents[o] = c.value == 0 ? -1 : row0 + b;
+    a.tokens[o] = c.value == 0 ? -1 : static_cast<int>(static_cast<uint32_t>(c.place));
+    const unsigned long long v = c.value;
+    a.out_scores[o] = v == 0 ? -INFINITY
+                             : static_cast<float>(__longlong_as_double(static_cast<long long>((v >> 63) ? v & ~(1ull << 63) : ~v)));
+  };
+  const Candidate none = {0, 0};
+  // ranks list[0 .. found) and gives f(rank, candidate) the first n
+  auto ranked = [&](int found, auto f) {
+    for (int i = tid; i < found; i += kThreads) {
+      const Candidate c = list[i];
+      int rank = 0;
+      for (int j = 0; j < found; ++j) rank += before(list[j], c);
+      if (rank < n) f(rank, c);
+    }
+  };
+  const int found = count;
+  if (blocks <= kBlocks && found <= kList) {
+    for (int i = tid; i < found; i += kThreads) {
+      list[i] = candidate(key_value(list[i].value), key_token(list[i].value), static_cast<int>(list[i].place));
+    }
+    __syncthreads();
+    ranked(found, put);
+    for (int i = found + tid; i < n; i += kThreads) put(i, none);
+    return;
+  }
+  // Many equal ones: all steps in turn, against the n best so far.
+  int kept = 0;
+  for (int i = 0; i < all; ++i) {
+    const int b = i / a.steps, step = i % a.steps;
+    if (maximum(step, b) == -INFINITY) continue;
+    __syncthreads();
+    if (tid == 0) count = kept;
+    if (tid < kept) list[tid] = best[tid];
+    __syncthreads();
+    const bool done = beam[b].state == kDone;
+    const T* base = static_cast<const T*>(a.logits) + (row0 + b) * a.row_stride;
+    for (int v = step * kStep<T> + tid; v < min(a.vocab, (step + 1) * kStep<T>); v += kThreads) {
+      const float x = done ? 0.f : to_float(base[v]);
+      if (x == -INFINITY || (done && v > 0)) continue;
+      const Candidate c = candidate(x, done ? a.end_token : v, b);
+      if (kept < n || before(c, best[n - 1])) list[atomicAdd(&count, 1)] = c;
+    }
+    __syncthreads();
+    const int here = count;
+    if (here == kept) continue;
+    ranked(here, [&](int rank, const Candidate& c) { best[rank] = c; });
+    kept = min(here, n);
+    __syncthreads();
+  }
+  for (int i = tid; i < n; i += kThreads) put(i, i < kept ? best[i] : none);
 }
 
 int check_beam(const smla_beam_params* p) {
@@ -350,25 +520,53 @@ int check_beam(const smla_beam_params* p) {
     return SMLA_ERR_UNSUPPORTED_SHAPE;
   return SMLA_OK;
 }
-int segments_of(const smla_beam_params* p) { return (p->vocab - 1) / kSegment + 1; }
+int steps_of(const smla_beam_params* p) {
+  return (p->vocab - 1) / (p->logits_type == SMLA_FLOAT32 ? kStep<float> : kStep<__half>) + 1;
+}
 
-// The widest load that every row's start allows.
-template <class T>
-auto segment_of(const void* logits, int64_t row_stride) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(logits) | static_cast<uintptr_t>(row_stride) * sizeof(T);
-  if (at % 16 == 0) return segment_kernel<T, 16>;
-  if constexpr (sizeof(T) == 2) {
-    if (at % 4 != 0) return segment_kernel<T, 2>;
+// Runs of a row: the split of least modelled time, in steps: those of a run and two for its start, times
+// the waves of warps (32 an SM).
+int runs_of(const smla_beam_params* p) {
+  const int steps = steps_of(p), rows = p->groups * p->beams;
+  constexpr int64_t kSlots = 152 * 32;
+  int best = steps;
+  int64_t least = INT64_MAX;
+  for (const int each : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+    const int runs = (steps + each - 1) / each;
+    const int64_t cost = (static_cast<int64_t>(rows) * runs + kSlots - 1) / kSlots * (each + 2);
+    if (cost < least) {
+      least = cost;
+      best = runs;
+    }
   }
-  return segment_kernel<T, 4>;
+  return best;
+}
+
+template <class T, int BYTES>
+int launch(const BeamArgs& a, cudaStream_t s) {
+  const int64_t warps = static_cast<int64_t>(a.rows) * a.runs;
+  const int st = done(launch_programmatic(run_kernel<T, BYTES>, dim3(static_cast<unsigned>((warps - 1) / kRunWarps + 1)),
+                                          dim3(kRunWarps * 32), 0, s, a));
+  if (st != SMLA_OK) return st;
+  return done(launch_programmatic(join_kernel<T, BYTES>, dim3(a.rows / a.beams), dim3(kThreads), 0, s, a));
+}
+// With the widest load that every row's start allows.
+template <class T>
+int launch(const BeamArgs& a, cudaStream_t s) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits) | static_cast<uintptr_t>(a.row_stride) * sizeof(T);
+  if (at % 16 == 0) return launch<T, 16>(a, s);
+  if constexpr (sizeof(T) == 2) {
+    if (at % 4 != 0) return launch<T, 2>(a, s);
+  }
+  return launch<T, 4>(a, s);
 }
 
 size_t lay_out(const smla_beam_params* p, char* base, BeamArgs* a) {
-  const size_t slots = static_cast<size_t>(p->groups) * p->beams * segments_of(p);
+  const size_t rows = static_cast<size_t>(p->groups) * p->beams;
   a->stats = reinterpret_cast<float2*>(base);
-  const size_t at = round256(slots * sizeof(float2));
-  a->best = reinterpret_cast<unsigned long long*>(base + at);
-  return at + round256(slots * p->num_out * sizeof(unsigned long long));
+  const size_t at = round256(rows * runs_of(p) * sizeof(float2));
+  a->maxima = reinterpret_cast<float*>(base + at);
+  return at + round256(rows * steps_of(p) * sizeof(float));
 }
 
 }  // namespace
@@ -398,19 +596,13 @@ int smla_beam_select(const void* logits, const float* scores, const uint8_t* fin
       !ints_ok(tokens) || out_scores == nullptr || !aligned(out_scores, 4) || workspace == nullptr || !aligned(workspace, 256))
     return SMLA_ERR_INVALID_ARG;
   BeamArgs a = {logits, p->row_stride, scores, finished, parents, tokens, out_scores, nullptr, nullptr,
-                p->beams, p->vocab, p->num_out, segments_of(p), p->end_token, nullptr};
+                p->groups * p->beams, p->beams, p->vocab, p->num_out, steps_of(p), runs_of(p), p->end_token, nullptr};
   if (workspace_bytes < lay_out(p, static_cast<char*>(workspace), &a)) return SMLA_ERR_WORKSPACE_TOO_SMALL;
   st = ready(&a.status);
   if (st != SMLA_OK) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid(a.segments, p->groups * p->beams);
-  const auto segment = p->logits_type == SMLA_FLOAT32    ? segment_of<float>(logits, p->row_stride)
-                       : p->logits_type == SMLA_BFLOAT16 ? segment_of<__nv_bfloat16>(logits, p->row_stride)
-                                                         : segment_of<__half>(logits, p->row_stride);
-  st = done(launch_programmatic(segment, grid, dim3(kThreads), 0, s, a));
-  if (st != SMLA_OK) return st;
-  const size_t lists = sizeof(unsigned long long) * p->beams * p->num_out;      // 32 KB at most
-  return done(launch_programmatic(join_kernel, dim3(p->groups), dim3(kThreads), lists, s, a));
+  if (p->logits_type == SMLA_FLOAT32) return launch<float>(a, s);
+  return p->logits_type == SMLA_BFLOAT16 ? launch<__nv_bfloat16>(a, s) : launch<__half>(a, s);
 }
 
 }  // extern "C"

@@ -16,12 +16,6 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kHeadroom = 8.f;
 constexpr long long kWaitLimit = 2000000000ll;     // SM clocks, ~1 s
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // A wait that gives up on its limit or when another role has.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* stop, int* status) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -39,25 +33,6 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
 // The same for a whole warp: one verdict for its lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop, int* status) {
   return __all_sync(0xffffffffu, wait(bar, parity, stop, status));
-}
-
-// Two 32-bit products or sums of products an instruction.
-struct Two {
-  unsigned long long v;
-  __device__ __forceinline__ Two() {}
-  __device__ __forceinline__ Two(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
-  __device__ __forceinline__ explicit Two(float x) : Two(x, x) {}
-  __device__ __forceinline__ void get(float* x, float* y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(v)); }
-};
-__device__ __forceinline__ Two operator*(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
 }
 
 // What may be done to a score x = q . k besides the scale: a cap and a distance bias (both
