@@ -22,15 +22,13 @@ namespace {
 // and masks: no SM waits for the longest sequence.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
-// Least blocks of a share, which pays for its query tile and its partial result: 4 x 4 tokens of
+// kMinShare, the least blocks of a share, pays for its query tile and its partial result: 4 x 4 tokens of
 // 1,001: 33.0, 29.3, 31.6 and 35.9 us with 1, 2, 4 and 8.
-constexpr int kMinShare = 2;
-// A border within this many blocks of a tile's end moves there (by a quarter of a share at
+// A border within kSnap blocks of a tile's end moves there (by a quarter of a share at
 // most): a piece of a tile costs its 256 rows of Q and 458 KB of partial results, which leave an SM
 // at 28 bytes a cycle, as much as four blocks.  Seven ragged sequences of 16 heads: 68.0, 65.3,
 // 59.5, 59.4 and 59.5 us with 0, 1, 2, 3 and 6; three of 700 tokens in a window 156, 153, 151,
 // 147 and 146; single tokens do not mind.
-constexpr int kSnap = 3;
 
 // Exclusive sum over the CTA; *total gets the sum.
 __device__ long long block_sum(long long v, long long* total, long long* warp_sums) {
@@ -67,7 +65,6 @@ struct Sequence {
 __device__ __forceinline__ Sequence sequence(const ChunkArgs& a, int b) {
   Sequence s = {0, 0, 0, 0, false};
   if (b >= a.B) return s;
-  if (a.listed > 0) return {b, 1, a.listed, (a.listed - 1) / kChunkBlk + 1, false};
   const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
   s.wrong = c0 < 0 || c1 < c0 || c1 > a.T;
   s.len = max(a.kv_lens[b], 0);
@@ -388,9 +385,20 @@ __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const Chu
   __shared__ float weight[8];
   grid_dep_wait();
   grid_dep_launch();
-  const int cuts = p.head[2];
-  const int4 cut = p.cut[blockIdx.y];     // first row of the tile, rows, first and last worker
-  if (static_cast<int>(blockIdx.y) >= cuts) return;
+  int4 cut;                               // first row of the tile, rows, first and last worker
+  if (is_even<true>(p)) {
+    // the border of shares y and y + 1, if it is the first inside a tile
+    const int c = static_cast<int>(blockIdx.y) + 1, x = plan_begin<true>(p, c), t = x / p.even.blocks;
+    if (x >= p.even.line || x == t * p.even.blocks || plan_begin<true>(p, c - 1) > t * p.even.blocks) return;
+    const int4 tile = plan_tile<true>(p, t);
+    int last = c;
+    while (last + 1 < static_cast<int>(gridDim.y) + 1 && plan_begin<true>(p, last + 1) < (t + 1) * p.even.blocks) ++last;
+    cut = make_int4(tile.y, tile.z, c - 1, last);
+  } else {
+    const int cuts = p.head[2];
+    cut = p.cut[blockIdx.y];
+    if (static_cast<int>(blockIdx.y) >= cuts) return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x * kRows + warp / ROW_WARPS;
   if (static_cast<int>(blockIdx.x) * kRows >= cut.y) return;
@@ -491,6 +499,7 @@ bool use_pairs(const smla_chunk_params* p) {
 // The workspace of a call; base may be null to size it.
 size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
   size_t at = 0;
+  plan->even = {};
   auto take = [&](size_t bytes) {
     char* q = base + at;
     at += round256(bytes);
@@ -523,7 +532,7 @@ cudaError_t launch_merge(const ChunkArgs& a, const ChunkPlan& p, int rows, int w
   if (workers < 2) return cudaSuccess;
   // few tiles: many partial results a row (see the kernel)
   const int64_t tiles = (static_cast<int64_t>(a.T) * a.H + rows - 1) / rows + a.B;
-  const unsigned cuts = static_cast<unsigned>(tiles < workers - 1 ? tiles : workers - 1);
+  const unsigned cuts = static_cast<unsigned>(tiles < workers - 1 && p.even.blocks == 0 ? tiles : workers - 1);
   if (tiles * 4 <= workers)
     return launch_programmatic(merge_kernel<8>, dim3(rows, cuts), dim3(256), 0, s, a, p, rows);
   return launch_programmatic(merge_kernel<1>, dim3(rows / 8, cuts), dim3(256), 0, s, a, p, rows);
@@ -544,7 +553,9 @@ cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_
 
 cudaError_t launch_single_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_t s) {
   const int workers = kMaxSms;
-  cudaError_t e = launch_programmatic(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, p, kSingleRows, workers);
+  cudaError_t e = cudaSuccess;
+  if (p.even.blocks == 0)
+    e = launch_programmatic(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, p, kSingleRows, workers);
   if (e == cudaSuccess) e = launch_chunk_single(a, p, workers, s);
   return e == cudaSuccess ? launch_merge(a, p, kSingleRows, workers, s) : e;
 }
@@ -574,6 +585,10 @@ int launch_sparse4(const void* q, const void* kv, const int32_t* indices, const 
                        fault_block(), p->topk, block_table, max_pages, page_size};
   ChunkPlan plan;
   lay_out(&c, static_cast<char*>(workspace), &plan);
+  const int blocks = (p->topk - 1) / kChunkBlk + 1, tiles = (p->num_heads - 1) / kSingleRows + 1;
+  const int line = p->batch * tiles * blocks, share = (line + kMaxSms - 1) / kMaxSms;      // 65,535 * 2 * 1,024 at most
+  const int per = share > kMinShare ? share : kMinShare;
+  plan.even = {blocks, tiles, p->num_heads, per, line, per / 4 < kSnap ? per / 4 : kSnap};
   return launch_single_path(a, plan, stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 

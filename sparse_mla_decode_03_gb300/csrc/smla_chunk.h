@@ -53,7 +53,45 @@ struct ChunkPlan {
                          // of them whose row has a value that is not finite
   uint16_t* kv;          // [blocks][64][512] bf16: the expanded copy
   int64_t cap_blocks;    // blocks of the expanded copy, not counting one of zeros behind
+  // Sparse decode: every tile has as many blocks, so that the plan follows from its number (blocks 0: it
+  // lies in memory, above).
+  struct Even {
+    int blocks, tiles, heads, per, line, snap;      // of a tile; of a sequence; share and line as make_plan has them
+  } even;
 };
+
+// Blocks of a share, and how far a border moves to a tile's end (see make_plan).
+constexpr int kMinShare = 2, kSnap = 3;
+
+// The plan's parts, of sparse decode where EVEN allows for it.
+template <bool EVEN>
+__device__ __forceinline__ bool is_even(const ChunkPlan& p) {
+  return EVEN && p.even.blocks > 0;
+}
+template <bool EVEN>
+__device__ __forceinline__ int plan_begin(const ChunkPlan& p, int worker) {
+  if (!is_even<EVEN>(p)) return p.begin[worker];
+  const int n = p.even.blocks, x = min(worker * p.even.per, p.even.line), rest = x % n;
+  return rest <= p.even.snap ? x - rest : n - rest <= p.even.snap ? x + n - rest : x;
+}
+template <bool EVEN>
+__device__ __forceinline__ int plan_start(const ChunkPlan& p, int worker, int begin) {
+  return is_even<EVEN>(p) ? begin / p.even.blocks : p.start[worker];
+}
+template <bool EVEN>
+__device__ __forceinline__ int plan_cum(const ChunkPlan& p, int tile) {
+  return is_even<EVEN>(p) ? tile * p.even.blocks : p.cum[tile];
+}
+template <bool EVEN>
+__device__ __forceinline__ int4 plan_tile(const ChunkPlan& p, int tile) {
+  if (!is_even<EVEN>(p)) return p.tile[tile];
+  const int b = tile / p.even.tiles, row = (tile - b * p.even.tiles) * 64;
+  return make_int4(b, b * p.even.heads + row, min(64, p.even.heads - row), 0);
+}
+template <bool EVEN>
+__device__ __forceinline__ int plan_len(const ChunkArgs& a, const ChunkPlan& p, int b) {
+  return is_even<EVEN>(p) ? a.listed : p.seq_len[b];
+}
 
 __device__ __forceinline__ int find_last_le(const int32_t* a, int n, int x) {   // a[0] <= x
   int lo = 0;

@@ -85,21 +85,23 @@ struct Cursor {
   int x, x1, t, next;     // next: where tile t ends
   int b, left;            // sequence, and its positions from the row's on
   int page, off;
-  __device__ __forceinline__ void load(const ChunkPlan& p, int row, int page_size) {
-    const int4 tile = p.tile[t];
-    next = p.cum[t + 1];
+  template <bool EVEN>
+  __device__ __forceinline__ void load(const ChunkArgs& a, const ChunkPlan& p, int row, int page_size) {
+    const int4 tile = plan_tile<EVEN>(p, t);
+    next = plan_cum<EVEN>(p, t + 1);
     b = tile.x;
-    const int pos = (tile.w + (min(x1, next) - 1 - p.cum[t])) * kChunkBlk + row;
-    left = p.seq_len[b] - pos;
+    const int pos = (tile.w + (min(x1, next) - 1 - plan_cum<EVEN>(p, t))) * kChunkBlk + row;
+    left = plan_len<EVEN>(a, p, b) - pos;
     page = pos / page_size;
     off = pos - page * page_size;
   }
   // pages, rest: 64 / page_size and 64 % page_size
-  __device__ __forceinline__ void step(const ChunkPlan& p, int row, int page_size, int pages, int rest) {
+  template <bool EVEN>
+  __device__ __forceinline__ void step(const ChunkArgs& a, const ChunkPlan& p, int row, int page_size, int pages, int rest) {
     ++x;
     if (x == next && x < x1) {
       ++t;
-      load(p, row, page_size);
+      load<EVEN>(a, p, row, page_size);
       return;
     }
     left += kChunkBlk;
@@ -222,7 +224,7 @@ __device__ __forceinline__ bool past_bf16(const uint4& v, uint32_t s) {
 // 16-lane tensor-memory load deals them out: lane 4 g + q has columns 8 j + 2 q and + 1 (of
 // the warp's half) of rows g (v[4 j], v[4 j + 1]) and g + 8 (v[4 j + 2], v[4 j + 3]).  Sums
 // stay per thread until the end; the maximum is the row's, of both halves.
-template <bool MODS>
+template <bool MODS, bool EVEN>
 struct TwoRows {
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
   int lo[2] = {0, 0}, hi[2] = {0, 0}, pos[2] = {0, 0};
@@ -236,7 +238,7 @@ struct TwoRows {
       const int row = row0 + 8 * i;
       if (row >= tile.z) continue;
       const int tok = (tile.y + row) / a.H;
-      visible(a, tile.x, tok, plan.seq_len[tile.x], &lo[i], &hi[i], &pos[i]);
+      visible(a, tile.x, tok, plan_len<EVEN>(a, plan, tile.x), &lo[i], &hi[i], &pos[i]);
       if (MODS && a.slopes != nullptr) slope2[i] = a.slopes[tile.y + row - tok * a.H] * kLog2e;
     }
   }
@@ -416,7 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   grid_dep_launch();
 
-  const int t_first = plan.start[worker], x0 = plan.begin[worker], x1 = plan.begin[worker + 1];
+  constexpr bool EVEN = ROW4 && !MODS;     // may be a sparse call
+  const int x0 = plan_begin<EVEN>(plan, worker), x1 = plan_begin<EVEN>(plan, worker + 1), t_first = plan_start<EVEN>(plan, worker, x0);
 
   if (warp >= kExpandWarp0 && warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsExpand) : "memory");
@@ -486,11 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       at.x = x0;
       at.x1 = x1;
       at.t = t_first;
-      at.load(plan, mine, a.page_size);
+      at.load<EVEN>(a, plan, mine, a.page_size);
       std::conditional_t<ROW4, RowWords4, RowWords> d;
       const int count = x1 - x0;
       uint32_t have = fetch(lookup(at), at.off, d);
-      at.step(plan, mine, a.page_size, pages_step, rest);
+      at.step<EVEN>(a, plan, mine, a.page_size, pages_step, rest);
       int id = lookup(at), off = at.off;
       bool ok = true;
       if constexpr (ROW4) {
@@ -555,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(FULL + 2 * B + 1));
           have = fetch(id, off, d);
-          at.step(plan, mine, a.page_size, pages_step, rest);
+          at.step<EVEN>(a, plan, mine, a.page_size, pages_step, rest);
           id = lookup(at);
           off = at.off;
         }
@@ -681,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(FULL + 2 * B + 1));
         // the next block's bytes, and the page ids of the one after it
         have = fetch(id, off, d);
-        at.step(plan, mine, a.page_size, pages_step, rest);
+        at.step<EVEN>(a, plan, mine, a.page_size, pages_step, rest);
         id = lookup(at);
         off = at.off;
       }
@@ -701,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 0, k = 0;               // blocks and tiles so far
       bool ok = true;
       for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
-        const int end = min(x1, plan.cum[t + 1]);
+        const int end = min(x1, plan_cum<EVEN>(plan, t + 1));
         ok = warp_wait(bar(QFULL), k & 1, stop, a.status);
         for (; ok && x < end; ++x, ++n) {
           if (n > 0) ok = warp_wait(bar(SEMPTY), (n - 1) & 1, stop, a.status);
@@ -734,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 0, k = 0;
       bool ok = true;
       for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
-        const int end = min(x1, plan.cum[t + 1]);
+        const int end = min(x1, plan_cum<EVEN>(plan, t + 1));
         uint32_t old = 0;                  // the tile's first product overwrites O
         for (; ok && x < end; ++x, ++n, old = 1) {
           ok = warp_wait(bar(PFULL + (n & 1)), (n >> 1) & 1, stop, a.status);
@@ -768,10 +771,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           mbar_arrive_expect_tx(bar(QFULL), 8 * kSlab);
           for (int c = 0; c < 8; ++c)
-            tma_load_2d(sbase + kQOff + c * kSlab, &qmap, 64 * c, plan.tile[t].y, bar(QFULL));
+            tma_load_2d(sbase + kQOff + c * kSlab, &qmap, 64 * c, plan_tile<EVEN>(plan, t).y, bar(QFULL));
         }
         __syncwarp();
-        x = min(x1, plan.cum[t + 1]);
+        x = min(x1, plan_cum<EVEN>(plan, t + 1));
       }
       // the last copy has landed before the CTA may end
       if (k > 0) warp_wait(bar(QFULL), (k - 1) & 1, stop, a.status);
@@ -793,12 +796,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int x = x0, t = t_first, i = 0, held = 0;
     bool ok = true;
     for (; ok && x < x1; ++t) {
-      const int4 tile = plan.tile[t];
-      const int begin = plan.cum[t], after = plan.cum[t + 1], end = min(x1, after);
+      const int4 tile = plan_tile<EVEN>(plan, t);
+      const int begin = plan_cum<EVEN>(plan, t), after = plan_cum<EVEN>(plan, t + 1), end = min(x1, after);
       const int nb = end - x, blk = tile.w + (end - 1 - begin);     // the first block
       // rows past the tile stay whatever they are (a product's rows do not mix), so a warp
       // without rows only keeps step
-      TwoRows<MODS> st(a, plan, tile, 16 * quarter + g);
+      TwoRows<MODS, EVEN> st(a, plan, tile, 16 * quarter + g);
       const bool idle = 16 * quarter >= tile.z;
       for (i = 0; ok && i < nb; ++i, ++n) {
         ok = warp_wait(bar(FULL + 2 * (n & 1)), (n >> 1) & 1, stop, a.status);     // the masks' writers
@@ -890,8 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // meetings of the schedule, one a block and three a tile, so that neither waits for good.
     if (!ok)
       for (; x < x1; ++t, i = 0, held = 0) {
-        const int end = min(x1, plan.cum[t + 1]);
-        if (16 * quarter < plan.tile[t].z)
+        const int end = min(x1, plan_cum<EVEN>(plan, t + 1));
+        if (16 * quarter < plan_tile<EVEN>(plan, t).z)
           for (int k = end - x + 3 - i - held; k > 0; --k) asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
         x = end;
       }
