@@ -43,19 +43,54 @@ __device__ __forceinline__ int parent_of(const ReorderArgs& a, int r) {
   const int p = __ldg(a.parents + r);
   return p < a.rows ? p : -1;
 }
-// Whether child r copies a last page that is partly filled and mapped.
-__device__ __forceinline__ bool takes_page(const ReorderArgs& a, int r) {
-  const int p = parent_of(a, r);
-  if (p < 0 || __ldcg(a.first + p) == r) return false;
+// Whether child r, which does not take row p over, copies a last page that is partly filled and mapped.
+__device__ __forceinline__ bool takes_page(const ReorderArgs& a, int p) {
   const int len = parent_length(a, a.kv_lens, p);
   if (len % a.page_size == 0) return false;
   const int page = a.table[static_cast<int64_t>(p) * a.max_pages + len / a.page_size];
   return page >= 0 && page < a.num_pages;
 }
 
+// Exclusive sums of two counts over the CTA's threads; *total gets the sums.  All threads call.
+__device__ __forceinline__ int2 block_rank2(int2 v, int2* total, int2* warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int2 s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, s.x, o), y = __shfl_up_sync(0xffffffffu, s.y, o);
+    if (lane >= o) {
+      s.x += x;
+      s.y += y;
+    }
+  }
+  if (lane == 31) warps[warp] = s;
+  __syncthreads();
+  int2 w = warps[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, w.x, o), y = __shfl_up_sync(0xffffffffu, w.y, o);
+    if (lane >= o) {
+      w.x += x;
+      w.y += y;
+    }
+  }
+  *total = make_int2(__shfl_sync(0xffffffffu, w.x, 31), __shfl_sync(0xffffffffu, w.y, 31));
+  const int from = warp > 0 ? warp - 1 : 0;
+  const int bx = __shfl_sync(0xffffffffu, w.x, from), by = __shfl_sync(0xffffffffu, w.y, from);
+  return make_int2(s.x - v.x + (warp > 0 ? bx : 0), s.y - v.y + (warp > 0 ? by : 0));
+}
+
+// Rows whose lowest children every CTA of the plan finds for itself, in shared memory; more: together, in the
+// workspace, which takes two cluster barriers.
+constexpr int kOwnRows = 8192;
+
+// Bound by latency: a launch, four trips to memory one after the other (parents, lengths, table; counts) and three
+// cluster barriers.
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
     reorder_plan_kernel(const ReorderArgs a) {
   __shared__ PlanShared sh;
+  __shared__ int2 warps[32];
+  __shared__ int own[kOwnRows];
   cg::this_cluster().sync();   // every CTA has started: its shared memory may be written
   grid_dep_wait();
   grid_dep_launch();
@@ -67,20 +102,41 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     for (int64_t i = i0; i < a.rows; i += step) a.old_lens[i] = a.kv_lens[i];
     return;
   }
-  const int me = static_cast<int>(blockIdx.x) * kPlanThreads + static_cast<int>(threadIdx.x);
+  const bool few = a.rows <= kOwnRows;
+  const int tid = static_cast<int>(threadIdx.x), cta = static_cast<int>(blockIdx.x);
   constexpr int kAll = kPlanCtas * kPlanThreads;
-  for (int r = me; r < a.rows; r += kAll) a.first[r] = kNobody;
-  cg::this_cluster().sync();
-  for (int r = me; r < a.rows; r += kAll) {
-    const int p = __ldg(a.parents + r);
-    if (p >= a.rows) report(a.status, SMLA_ERR_INDEX_RANGE);
-    else if (p >= 0) atomicMin(a.first + p, r);
+  {
+    int* first = few ? own : a.first;
+    const int r0 = few ? tid : cta * kPlanThreads + tid, step = few ? kPlanThreads : kAll;
+    for (int r = r0; r < a.rows; r += step) first[r] = kNobody;
+    if (few) __syncthreads();
+    else cg::this_cluster().sync();
+    for (int r = r0; r < a.rows; r += step) {
+      const int p = __ldg(a.parents + r);
+      if (p >= a.rows) report(a.status, SMLA_ERR_INDEX_RANGE);
+      else if (p >= 0) atomicMin(first + p, r);
+    }
+    if (few) __syncthreads();
+    else cg::this_cluster().sync();
   }
-  cg::this_cluster().sync();
-  // rows that nobody goes on from: a warp each
-  const int lane = threadIdx.x & 31;
-  for (int r = me / 32; r < a.rows; r += kAll / 32) {
-    if (__ldcg(a.first + r) != kNobody) continue;
+  auto first_of = [&](int p) { return few ? own[p] : __ldcg(a.first + p); };
+  // this CTA's rows, each thread a run of them: who copies a page
+  const int per = (a.rows + kPlanCtas - 1) / kPlanCtas, row0 = min(a.rows, cta * per), row1 = min(a.rows, row0 + per);
+  const int run = (row1 - row0 + kPlanThreads - 1) / kPlanThreads;
+  const int r0 = min(row1, row0 + tid * run), r1 = min(row1, r0 + run);
+  auto copies = [&](int r) {
+    const int p = parent_of(a, r);
+    return p >= 0 && first_of(p) != r && takes_page(a, p);
+  };
+  uint32_t who = 0;               // run <= 8: 65,535 rows on 8,192 threads
+  for (int r = r0; r < r1; ++r) {
+    if (few) a.first[r] = own[r];         // for the next launch
+    who |= copies(r) ? 1u << (r - r0) : 0u;
+  }
+  // rows that nobody goes on from give their pages back: a warp each
+  const int lane = tid & 31;
+  for (int r = (cta * kPlanThreads + tid) / 32; r < a.rows; r += kAll / 32) {
+    if (first_of(r) != kNobody) continue;
     const int32_t* e = a.table + static_cast<int64_t>(r) * a.max_pages;
     for (int i = lane; i < a.max_pages; i += 32) {
       const int page = e[i];
@@ -93,20 +149,17 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     }
   }
   cg::this_cluster().sync();
-  const Part rp = part_of(a.rows), pp = part_of(a.num_pages);
-  int free_total, need_total, mine = 0;
-  const int free_rank = block_rank(count_free(a.ref, pp), &free_total, &sh);
-  for (int r = static_cast<int>(rp.run0); r < static_cast<int>(rp.run1); ++r) mine += takes_page(a, r);
-  const int need_rank = block_rank(mine, &need_total, &sh);
-  int2 low;
-  const int2 all = cluster_share(make_int2(need_total, free_total), 0, &low, &sh);
+  const Part pp = part_of(a.num_pages);
+  int2 total, low;
+  const int2 rank = block_rank2(make_int2(__popc(who), count_free(a.ref, pp)), &total, warps);
+  const int2 all = cluster_share(total, 0, &low, &sh);
   const int got = min(all.x, all.y);
-  take_free(a.ref, pp, low.y + free_rank, got, a.list);
+  take_free(a.ref, pp, low.y + rank.y, got, a.list);
   cg::this_cluster().sync();
-  int k = low.x + need_rank;
-  for (int r = static_cast<int>(rp.run0); r < static_cast<int>(rp.run1); ++r) {
+  int k = low.x + rank.x;
+  for (int r = r0; r < r1; ++r) {
     int f = kNotNeeded;
-    if (takes_page(a, r)) {
+    if ((who >> (r - r0)) & 1) {
       f = k < got ? __ldcg(a.list + k) : kNoPage;
       ++k;
       if (f == kNoPage) report(a.status, SMLA_ERR_POOL_EXHAUSTED);
