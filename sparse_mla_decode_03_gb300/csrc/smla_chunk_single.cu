@@ -30,7 +30,6 @@
 // Warps of a CTA: 0..7 softmax and results (64 rows lie in 16 tensor-memory lanes of each
 // quarter, which two warps share by columns), 8..23 expand, 24 issues the scores, 25 the
 // value products, 26 loads Q.  Every wait is bounded.
-#include <cstring>
 #include <mutex>
 #include <type_traits>
 
@@ -47,7 +46,6 @@ constexpr int kExpandWarps = 16;
 constexpr int kRows = 64 / kExpandWarps;   // of a block, a warp
 constexpr int kMmaWarp = 24;
 constexpr int kPvWarp = 25;
-constexpr int kQWarp = 26;
 constexpr int kThreads = 28 * 32;
 // Registers (setmaxnreg): what the launch gives is split among the warpgroups.
 constexpr int kLaunchRegs = 72;
@@ -56,26 +54,52 @@ static_assert(kRegsSoft * 256 + kRegsExpand * 512 + kRegsMma * 128 <= kLaunchReg
 static_assert(kRegsSoft >= kLaunchRegs && kRegsExpand >= kLaunchRegs && kRegsMma <= kLaunchRegs,
               "the direction that each role's setmaxnreg takes");
 constexpr int kSlab = 64 * 128;            // 64 columns of 64 rows
-constexpr int kBuf = 8 * kSlab;            // an expanded block
-constexpr int kQOff = 0;
-constexpr int kBufOff = 8 * kSlab;
-// P of a block takes the place of its rope, which the scores are done with; the buffer is
-// filled again only after the value product.  Without 8 KB for P the CTA stays below the
-// 196 KB step of the shared-memory carve-out, which leaves the loads 60 KB of L1, not 28 (93 ->
-// 85 us).
-constexpr int kPOff = kBufOff + 7 * kSlab;     // + kBuf for the second buffer
-constexpr int kBarOff = kBufOff + 2 * kBuf;
-constexpr int kMaskOff = kBarOff + 256;    // [2 buffers][mapped, not finite][16 half bytes]
-constexpr int kMaxOff = kMaskOff + 64;      // float [2 blocks][2 halves][64 rows]: largest scores; later sums
+constexpr int kHalf = 4 * kSlab;           // columns 0..255 or 256..511 of an expanded block
+// Half blocks are expanded into a ring of places, a block's two one after the other: three blocks, so that
+// expansion, scores and value product need not wait for one another's ends.  With Q in tensor memory the CTA
+// stays below the 196 KB step of the shared-memory carve-out, which leaves the loads 60 KB of L1, not 28.
+constexpr int kPlaces = 6;
+// P of a block takes the place of its rope, the last slab of its second half, which the scores are done
+// with; the place is filled again only after the value product.
+constexpr int kPOff = 3 * kSlab;
+constexpr int kBarOff = kPlaces * kHalf;
+constexpr int kMasks = 3;                  // blocks whose masks are held: a block is expanded again only after its weights
+constexpr int kMaskOff = kBarOff + 256;    // [3 blocks][mapped, not finite][16 half bytes]
+constexpr int kMaxOff = kMaskOff + 128;    // float [2 blocks][2 halves][64 rows]: largest scores; later sums
 constexpr int kSmem = kMaxOff + 1024 + 1024;
 static_assert(kSmem <= 195 * 1024, "the carve-out step, less what the system takes");
-constexpr uint32_t kColS = 448;
 
-// FULL / EMPTY: half of a block buffer (columns 0..255, the rest) filled / its value product
-// done, two buffers; QFULL / QEMPTY: Q loaded / its last scores done; SFULL / SEMPTY: scores
-// in tensor memory / taken by the softmax; PFULL: weights written (one for each buffer: a
-// quarter may be a block ahead of another); OEMPTY: results taken.
-enum Bar : int { FULL = 0, EMPTY = 4, PFULL = 8, QFULL = 10, QEMPTY, SFULL, SEMPTY, OEMPTY, kBars };
+// Tensor memory.  64 rows of a product lie in 16 lanes of each quarter, the lower ones or the upper, so
+// that 512 columns hold twice as much.  Lower: Q (two bf16 a column), the scores of two blocks, columns 384..447 of
+// O.  Upper: columns 0..383 of O.  (Q as a product's first operand lies in the lanes of its result.)
+constexpr uint32_t kColS = 256, kColTail = 384, kUpper = 16u << 16;
+__device__ __forceinline__ uint32_t o_column(uint32_t tmem, int c) {
+  return tmem + static_cast<uint32_t>(c) + (c < static_cast<int>(kColTail) ? kUpper : 0u);
+}
+
+// FULL / EMPTY: a place of the ring filled / its value product done; PFULL: weights written (one for each of
+// two blocks: a quarter may be a block ahead of another); QFULL: a tile's Q in tensor memory; SFULL /
+// SEMPTY: scores of a block in tensor memory / taken by the softmax, two in turn; OEMPTY: results taken.
+enum Bar : int { FULL = 0, EMPTY = kPlaces, PFULL = 2 * kPlaces, QFULL = PFULL + 2, SFULL, SEMPTY = SFULL + 2, OEMPTY = SEMPTY + 2, kBars };
+
+// A place of the ring, and the parity of its uses.
+struct Place {
+  uint32_t at = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kPlaces) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+  // of half block i (without a state to keep: registers of the softmax)
+  static __device__ __forceinline__ Place of(uint32_t i) {
+    Place p;
+    const uint32_t use = i / kPlaces;
+    p.at = i - use * kPlaces;
+    p.phase = use & 1;
+    return p;
+  }
+};
 
 // A row of the blocks on the line, walked tile by tile and each tile's share from its last
 // block to its first (scores that a distance bias shapes then fall along the way, and the
@@ -336,7 +360,7 @@ __device__ __forceinline__ void store_result(const ChunkArgs& a, const ChunkPlan
 #pragma unroll 1
   for (int c = 224 * half; c < 224 * half + 224; c += 32) {
     float o[16];
-    tmem_ld_16x32(tO + c, o);
+    tmem_ld_16x32(o_column(tO, c), o);
     tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -360,12 +384,44 @@ __device__ __forceinline__ void store_result(const ChunkArgs& a, const ChunkPlan
   }
 }
 
-// x[0] of lane 4 g for row g < 8, x[1] for row g + 8, to lane = row.
-__device__ __forceinline__ float to_row(const float (&x)[2]) {
-  const int src = (threadIdx.x & 7) * 4;
-  const float a = __shfl_sync(0xffffffffu, x[0], src), b = __shfl_sync(0xffffffffu, x[1], src);
-  return (threadIdx.x & 8) ? b : a;
+// A warp's half of the columns of O, times alpha of its two rows; seldom, so out of line.
+__device__ __noinline__ void rescale_half(uint32_t tO, float alpha0, float alpha1, int half) {
+#pragma unroll 1
+  for (int c = 224 * half; c < 224 * half + 224; c += 32) {
+    float o[16];
+    tmem_ld_16x32(o_column(tO, c), o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] *= k % 4 < 2 ? alpha0 : alpha1;
+    tmem_st_16x32(o_column(tO, c), o);
+  }
+  tmem_wait_st();
 }
+
+// A warp's half of the columns of its 16 rows of the tile's Q into tensor memory, as the 16-lane store takes them:
+// lane 4 g + q has columns (pairs of bf16) 8 j + 2 q and + 1 of rows g and g + 8.  Rows past the tile are zeros.
+__device__ __forceinline__ void load_q(const ChunkArgs& a, const int4& tile, uint32_t tQ, int quarter, int half) {
+  const int lane = threadIdx.x & 31, row = 16 * quarter + (lane >> 2);
+  const uint16_t* src = a.q + (static_cast<int64_t>(tile.y) + row) * kQkDim + 256 * half + 4 * (lane & 3);
+  const bool in0 = row < tile.z, in1 = row + 8 < tile.z;
+#pragma unroll 2
+  for (int c = 0; c < 4; ++c) {
+    float r[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint2 none = make_uint2(0u, 0u);
+      const uint2 u = in0 ? __ldg(reinterpret_cast<const uint2*>(src + 64 * c + 16 * j)) : none;
+      const uint2 v = in1 ? __ldg(reinterpret_cast<const uint2*>(src + 8 * kQkDim + 64 * c + 16 * j)) : none;
+      r[4 * j] = __uint_as_float(u.x);
+      r[4 * j + 1] = __uint_as_float(u.y);
+      r[4 * j + 2] = __uint_as_float(v.x);
+      r[4 * j + 3] = __uint_as_float(v.y);
+    }
+    tmem_st_16x32(tQ + 128 * half + 32 * c, r);
+  }
+  tmem_wait_st();
+}
+
 __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
@@ -389,7 +445,7 @@ __device__ __forceinline__ void drain() {
 }
 template <bool MODS, bool ROW4>
 __global__ void __launch_bounds__(kThreads, 1)
-    single_kernel(const ChunkArgs a, const ChunkPlan plan, const __grid_constant__ CUtensorMap qmap) {
+    single_kernel(const ChunkArgs a, const ChunkPlan plan) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -403,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i)
-      mbar_init(bar(i), i < EMPTY ? kExpandWarps : i == SEMPTY || i == PFULL || i == PFULL + 1 || i == OEMPTY ? kSoftWarps : 1);
+      mbar_init(bar(i), i < EMPTY ? kExpandWarps : i < PFULL || i == SFULL || i == SFULL + 1 ? 1 : kSoftWarps);
     *stop = 0;
     fence_mbar_init();
   }
@@ -499,14 +555,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (ROW4) {
         const int j = lane & 3, w = lane >> 2;
         const uint32_t key = static_cast<uint32_t>((kRows * w16 + j) & 7);
-        const uint32_t row = sbase + kBufOff + (kRows * w16 + j) * 128;
-        // nope words w and 8 + w: four 16-byte units of slab w / 2 and 4 + w / 2; rope units w + 1 (word c) and
-        // 0 (word b of lanes 28 .. 31)
-        const uint32_t to = row + (w >> 1) * kSlab, rope = row + 7 * kSlab;
+        const uint32_t row = sbase + (kRows * w16 + j) * 128;
+        // nope words w and 8 + w: four 16-byte units of slab w / 2 of the first and the second half; rope
+        // units w + 1 (word c) and 0 (word b of lanes 28 .. 31)
+        const uint32_t to = row + (w >> 1) * kSlab, rope = row + 3 * kSlab;
         auto unit = [&](int u) { return ((static_cast<uint32_t>(u) ^ key) << 4); };
         const bool nope_b = w < 6, rope_b = w == 7;
+        Place place;
+        int turn = 0;                // of the masks' three
         for (int n = 0; n < count; ++n) {
-          const int B = n & 1;
           // the scale bytes of the lane's two words
           const uint32_t s0 = __shfl_sync(0xffffffffu, d.b.x, 24 + j), s1 = __shfl_sync(0xffffffffu, d.b.y, 24 + j);
           const uint32_t s2 = __shfl_sync(0xffffffffu, d.b.z, 24 + j), s3 = __shfl_sync(0xffffffffu, d.b.w, 24 + j);
@@ -530,8 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               d.a = d.b = d.c = zero;
             }
           }
-          const uint32_t parity = ((n >> 1) - 1) & 1;
-          if (n >= 2) ok = warp_wait(bar(EMPTY + 2 * B), parity, stop, a.status);
+          if (n >= 3) ok = warp_wait(bar(EMPTY + place.at), place.phase ^ 1, stop, a.status);
           if (!ok) break;
           auto words = [&](const uint4& v, uint32_t s, uint32_t at, bool mine) {
             const uint32_t m1 = first(s), m2 = second(s);
@@ -542,21 +598,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               sts_if(mine, at + unit(4 * (w & 1) + i), o);
             }
           };
-          words(d.a, sa, to + B * kBuf, true);
+          words(d.a, sa, to + place.at * kHalf, true);
           if (lane == 0) {
-            masks[B * 32 + w16] = static_cast<uint8_t>(have);
-            masks[B * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
+            masks[turn * 32 + w16] = static_cast<uint8_t>(have);
+            masks[turn * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && !(n == a.fault_block && w16 == 0)) mbar_arrive(bar(FULL + 2 * B));
-          if (n >= 2) ok = warp_wait(bar(EMPTY + 2 * B + 1), parity, stop, a.status);
+          if (lane == 0 && !(n == a.fault_block && w16 == 0)) mbar_arrive(bar(FULL + place.at));
+          place.next();
+          if (n >= 3) ok = warp_wait(bar(EMPTY + place.at), place.phase ^ 1, stop, a.status);
           if (!ok) break;
-          words(d.b, sb, to + 4 * kSlab + B * kBuf, nope_b);
-          sts(rope + B * kBuf + unit(rope_b ? 0 : w + 1), rope_b ? d.b : d.c);
+          words(d.b, sb, to + place.at * kHalf, nope_b);
+          sts(rope + place.at * kHalf + unit(rope_b ? 0 : w + 1), rope_b ? d.b : d.c);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(FULL + 2 * B + 1));
+          if (lane == 0) mbar_arrive(bar(FULL + place.at));
+          place.next();
+          turn = turn + 1 == kMasks ? 0 : turn + 1;
           have = fetch(id, off, d);
           at.step<EVEN>(a, plan, mine, a.page_size, pages_step, rest);
           id = lookup(at);
@@ -570,9 +629,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int sh = 8 * (lane >> 3);
       const uint32_t pick = 0x4040u + 0x0101u * static_cast<uint32_t>(lane >> 3);   // (byte, 0, byte, 0)
       const uint32_t pick_b = lane < 24 ? pick : 0x4444u;
-      const uint32_t dst_nope = sbase + kBufOff + (lane >> 3) * kSlab;
+      const uint32_t dst_nope = sbase + (lane >> 3) * kSlab;
+      Place place;
+      int turn = 0;                  // of the masks' three
       for (int n = 0; n < count; ++n) {
-        const int B = n & 1;
         // 2^(s - 7) as two bf16 of this lane's groups (s: their scale bytes) of each row; lanes
         // 24 .. 31 have no second group
         auto power = [](uint32_t twice) { return twice * 128u + 0x3c003c00u; };
@@ -614,10 +674,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             dropped |= __any_sync(0xffffffffu, (bad & 0x80008000u) != 0) ? 1u << j : 0u;
           }
         }
-        const uint32_t parity = ((n >> 1) - 1) & 1;
-        if (n >= 2) ok = warp_wait(bar(EMPTY + 2 * B), parity, stop, a.status);
+        if (n >= 3) ok = warp_wait(bar(EMPTY + place.at), place.phase ^ 1, stop, a.status);
         if (!ok) break;
-        const uint32_t dn = dst_nope + kRows * w16 * 128 + B * kBuf;
+        uint32_t dn = dst_nope + kRows * w16 * 128 + place.at * kHalf;
         const int r7 = (kRows * w16) & 7;                 // the warp's first row modulo 8
         auto unit = [&](int j) { return j * 128 + (((lane & 7) ^ (r7 + j)) << 4); };    // the lane's unit of row j
         if (usual) {
@@ -640,16 +699,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (lane == 0) {
-          masks[B * 32 + w16] = static_cast<uint8_t>(have);
-          masks[B * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
+          masks[turn * 32 + w16] = static_cast<uint8_t>(have);
+          masks[turn * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && !(n == a.fault_block && w16 == 0)) mbar_arrive(bar(FULL + 2 * B));
-        if (n >= 2) ok = warp_wait(bar(EMPTY + 2 * B + 1), parity, stop, a.status);
+        if (lane == 0 && !(n == a.fault_block && w16 == 0)) mbar_arrive(bar(FULL + place.at));
+        place.next();
+        if (n >= 3) ok = warp_wait(bar(EMPTY + place.at), place.phase ^ 1, stop, a.status);
         if (!ok) break;
+        dn = dst_nope + kRows * w16 * 128 + place.at * kHalf;
         // the rope: word w of row j
-        const uint32_t dr = sbase + kBufOff + 7 * kSlab + kRows * w16 * 128 + B * kBuf;
+        const uint32_t dr = sbase + 3 * kSlab + kRows * w16 * 128 + place.at * kHalf;
         auto rope = [&](int j, int w) { return dr + j * 128 + (((w >> 1) ^ (r7 + j)) << 4) + 8 * (w & 1); };
         if (usual) {
 #pragma unroll
@@ -660,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               o[j] = expand8(d.b[j0 + j], mx[j0 + j]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              sts_if(lane < 24, dn + 4 * kSlab + unit(j0 + j), o[j]);
+              sts_if(lane < 24, dn + unit(j0 + j), o[j]);
               sts8_if(lane > 24, rope(j0 + j, (lane - 25) & 15), d.b[j0 + j]);
             }
           }
@@ -670,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint2 wb = again(j, 256 + 8 * lane);
             const uint32_t s = (again(j, kNope).y >> sh) & 0xffu;
             const bool drop = (dropped >> j) & 1;
-            sts_if(lane < 24, dn + 4 * kSlab + unit(j), drop ? make_uint4(0u, 0u, 0u, 0u) : expand8_any(wb, s));
+            sts_if(lane < 24, dn + unit(j), drop ? make_uint4(0u, 0u, 0u, 0u) : expand8_any(wb, s));
             sts8_if(lane > 24, rope(j, (lane - 25) & 15), drop ? make_uint2(0u, 0u) : wb);
           }
         }
@@ -681,7 +742,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(FULL + 2 * B + 1));
+        if (lane == 0) mbar_arrive(bar(FULL + place.at));
+        place.next();
+        turn = turn + 1 == kMasks ? 0 : turn + 1;
         // the next block's bytes, and the page ids of the one after it
         have = fetch(id, off, d);
         at.step<EVEN>(a, plan, mine, a.page_size, pages_step, rest);
@@ -700,41 +763,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) {
       // ---------------- scores ----------------
       constexpr uint32_t kIdQK = idesc_bf16(64, 64, false, false);
-      const uint32_t lq = static_cast<uint32_t>(d0), lk = lq + (kBufOff >> 4);
+      const uint32_t lk = static_cast<uint32_t>(d0);
       uint32_t n = 0, k = 0;               // blocks and tiles so far
+      Place place;
       bool ok = true;
       for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
         const int end = min(x1, plan_cum<EVEN>(plan, t + 1));
         ok = warp_wait(bar(QFULL), k & 1, stop, a.status);
         for (; ok && x < end; ++x, ++n) {
-          if (n > 0) ok = warp_wait(bar(SEMPTY), (n - 1) & 1, stop, a.status);
+          if (n >= 2) ok = warp_wait(bar(SEMPTY + (n & 1)), ((n >> 1) - 1) & 1, stop, a.status);
           for (int h = 0; ok && h < 2; ++h) {
-            ok = warp_wait(bar(FULL + 2 * (n & 1) + h), (n >> 1) & 1, stop, a.status);
+            ok = warp_wait(bar(FULL + place.at), place.phase, stop, a.status);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t la = lq + h * ((4 * kSlab) >> 4), lb = lk + (n & 1) * (kBuf >> 4) + h * ((4 * kSlab) >> 4);
+            const uint32_t q = tmem + 128 * h, lb = lk + place.at * (kHalf >> 4);
             if (elect_one()) {
 #pragma unroll 1
               for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  mma_f16_ss_hl(tmem + kColS, la + ((c * kSlab + i * 32) >> 4), hi, lb + ((c * kSlab + i * 32) >> 4), hi,
-                                kIdQK, c + i > 0 ? 1u : static_cast<uint32_t>(h));
-              if (h == 1) {
-                mma_commit(bar(SFULL));
-                if (x + 1 == end) mma_commit(bar(QEMPTY));
-              }
+                  mma_f16_ts_hl(tmem + kColS + 64 * (n & 1), q + 32 * c + 8 * i, lb + ((c * kSlab + i * 32) >> 4), hi, kIdQK,
+                                c + i > 0 ? 1u : static_cast<uint32_t>(h));
+              if (h == 1) mma_commit(bar(SFULL + (n & 1)));
             }
             __syncwarp();
+            place.next();
           }
         }
       }
       if (!ok) drain();
     } else if (warp == kPvWarp) {
       // ---------------- value products ----------------
-      constexpr uint32_t kIdV0 = idesc_bf16(64, 256, false, true), kIdV1 = idesc_bf16(64, 192, false, true);
-      const uint32_t lp = static_cast<uint32_t>(d0) + (kPOff >> 4), lv = static_cast<uint32_t>(dv) + (kBufOff >> 4);
+      constexpr uint32_t kId256 = idesc_bf16(64, 256, false, true), kId128 = idesc_bf16(64, 128, false, true),
+                         kId64 = idesc_bf16(64, 64, false, true);
+      const uint32_t lp = static_cast<uint32_t>(d0) + (kPOff >> 4), lv = static_cast<uint32_t>(dv);
       uint32_t n = 0, k = 0;
+      Place place;
       bool ok = true;
       for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
         const int end = min(x1, plan_cum<EVEN>(plan, t + 1));
@@ -744,40 +808,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && old == 0 && k > 0) ok = warp_wait(bar(OEMPTY), (k - 1) & 1, stop, a.status);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t lb = lv + (n & 1) * (kBuf >> 4);
+          const uint32_t first = place.at;
+          place.next();
+          const uint32_t l0 = lv + first * (kHalf >> 4), l1 = lv + place.at * (kHalf >> 4), lw = lp + place.at * (kHalf >> 4);
           if (elect_one()) {
-            // columns 0..255 first: the next block's may be written while 256..447 follow
+            // columns 0..255 first: their place may be filled again while 256..447 follow
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_f16_ss_hl(tmem, lp + (n & 1) * (kBuf >> 4) + ((i * 32) >> 4), hi, lb + ((i * 2048) >> 4), hi, kIdV0, i > 0 ? 1u : old);
-            mma_commit(bar(EMPTY + 2 * (n & 1)));
+              mma_f16_ss_hl(o_column(tmem, 0), lw + ((i * 32) >> 4), hi, l0 + ((i * 2048) >> 4), hi, kId256, i > 0 ? 1u : old);
+            mma_commit(bar(EMPTY + first));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_f16_ss_hl(tmem + 256, lp + (n & 1) * (kBuf >> 4) + ((i * 32) >> 4), hi, lb + ((4 * kSlab + i * 2048) >> 4), hi, kIdV1,
+              mma_f16_ss_hl(o_column(tmem, 256), lw + ((i * 32) >> 4), hi, l1 + ((i * 2048) >> 4), hi, kId128, i > 0 ? 1u : old);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_f16_ss_hl(o_column(tmem, kColTail), lw + ((i * 32) >> 4), hi, l1 + ((2 * kSlab + i * 2048) >> 4), hi, kId64,
                             i > 0 ? 1u : old);
-            mma_commit(bar(EMPTY + 2 * (n & 1) + 1));
+            mma_commit(bar(EMPTY + place.at));
           }
           __syncwarp();
+          place.next();
         }
       }
       if (!ok) drain();
-    } else if (warp == kQWarp) {
-      // ---------------- Q ----------------
-      bool ok = true;
-      uint32_t k = 0;
-      for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
-        if (k > 0) ok = warp_wait(bar(QEMPTY), (k - 1) & 1, stop, a.status);
-        if (!ok) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(bar(QFULL), 8 * kSlab);
-          for (int c = 0; c < 8; ++c)
-            tma_load_2d(sbase + kQOff + c * kSlab, &qmap, 64 * c, plan_tile<EVEN>(plan, t).y, bar(QFULL));
-        }
-        __syncwarp();
-        x = min(x1, plan_cum<EVEN>(plan, t + 1));
-      }
-      // the last copy has landed before the CTA may end
-      if (k > 0) warp_wait(bar(QFULL), (k - 1) & 1, stop, a.status);
     }
   } else if (warp < kExpandWarp0) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft) : "memory");
@@ -790,11 +843,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + kColS + 32 * half + lanes, tO = tmem + lanes;
     const int g = lane >> 2;
     volatile float* most = reinterpret_cast<volatile float*>(smem + kMaxOff);
+    auto give_q = [&](int t) {
+      load_q(a, plan_tile<EVEN>(plan, t), tmem + lanes, quarter, half);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(QFULL));
+    };
     // P: rows 16 quarter + g and + 8 (the same row modulo 8), columns 2 (lane % 4) .. of unit j
     const uint32_t p0 = sbase + kPOff + (16 * quarter + g) * 128 + 4 * (lane & 3), p1 = p0 + 8 * 128;
     uint32_t n = 0;
     int x = x0, t = t_first, i = 0, held = 0;
     bool ok = true;
+    if (x < x1) give_q(t);
     for (; ok && x < x1; ++t) {
       const int4 tile = plan_tile<EVEN>(plan, t);
       const int begin = plan_cum<EVEN>(plan, t), after = plan_cum<EVEN>(plan, t + 1), end = min(x1, after);
@@ -804,45 +864,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       TwoRows<MODS, EVEN> st(a, plan, tile, 16 * quarter + g);
       const bool idle = 16 * quarter >= tile.z;
       for (i = 0; ok && i < nb; ++i, ++n) {
-        ok = warp_wait(bar(FULL + 2 * (n & 1)), (n >> 1) & 1, stop, a.status);     // the masks' writers
+        ok = warp_wait(bar(FULL + Place::of(2 * n).at), Place::of(2 * n).phase, stop, a.status);     // the masks' writers
         if (!ok) break;
         const volatile unsigned long long* mk =
-            reinterpret_cast<const volatile unsigned long long*>(smem + kMaskOff + (n & 1) * 32);
+            reinterpret_cast<const volatile unsigned long long*>(smem + kMaskOff + (n % kMasks) * 32);
         const unsigned long long m0 = mk[0], m1 = mk[1], d0 = mk[2], d1 = mk[3];
         ulonglong2 rows = make_ulonglong2(~0ull, 0ull);
         if (__any_sync(0xffffffffu, (m0 & m1) != 0x0f0f0f0f0f0f0f0full || (d0 | d1) != 0))
           rows = make_ulonglong2(halves(m0, m1), halves(d0, d1));
-        ok = warp_wait(bar(SFULL), n & 1, stop, a.status);
+        ok = warp_wait(bar(SFULL + (n & 1)), (n >> 1) & 1, stop, a.status);
         if (!ok) break;
         if (idle) {
           if (lane == 0) {
-            mbar_arrive(bar(SEMPTY));
+            mbar_arrive(bar(SEMPTY + (n & 1)));
             mbar_arrive(bar(PFULL + (n & 1)));
           }
           continue;
         }
         tc_fence_after();
         float v[16];
-        tmem_ld_16x32(tS, v);
+        tmem_ld_16x32(tS + 64 * (n & 1), v);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(SEMPTY));
+        if (lane == 0) mbar_arrive(bar(SEMPTY + (n & 1)));
         uint32_t p[8];
         float alpha[2];
         st.weights(v, (blk - i) * kChunkBlk, rows, most + (n & 1) * 128, p, alpha);
         // O may be rescaled once the value product before this one is done
         if (i > 0 && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-          ok = warp_wait(bar(EMPTY + 2 * ((n - 1) & 1) + 1), ((n - 1) >> 1) & 1, stop, a.status);
+          ok = warp_wait(bar(EMPTY + Place::of(2 * n - 1).at), Place::of(2 * n - 1).phase, stop, a.status);
           if (!ok) {
             held = 1;
             break;
           }
           tc_fence_after();
-          const float f = to_row(alpha);
-          rescale_rows(tO, lane < 16 ? f : 1.f, 224 * half, 224);
+          rescale_half(tO, alpha[0], alpha[1], half);
         }
-        const uint32_t pb = (n & 1) * kBuf;
+        const uint32_t pb = Place::of(2 * n + 1).at * kHalf;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           sts4(p0 + pb + (((j + 4 * half) ^ g) << 4), p[2 * j]);
@@ -854,7 +913,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(PFULL + (n & 1)));
       }
       if (!ok) break;
-      ok = warp_wait(bar(EMPTY + 2 * ((n - 1) & 1) + 1), ((n - 1) >> 1) & 1, stop, a.status);
+      // all scores of the tile have been seen: the next one's Q may take this one's place
+      if (end < x1) give_q(t + 1);
+      ok = warp_wait(bar(EMPTY + Place::of(2 * n - 1).at), Place::of(2 * n - 1).phase, stop, a.status);
       if (!ok) break;
       tc_fence_after();
       if (!idle) {
@@ -930,11 +991,7 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStre
       done[dev] = true;
     }
   }
-  CUtensorMap qmap;
-  std::memset(static_cast<void*>(&qmap), 0, sizeof(qmap));
-  e = encode_rows(&qmap, a.q, static_cast<int64_t>(a.T) * a.H, kSingleRows);
-  if (e != cudaSuccess) return e;
-  return launch_programmatic(single_kernel<MODS, ROW4>, dim3(workers), dim3(kThreads), kSmem, stream, a, p, qmap);
+  return launch_programmatic(single_kernel<MODS, ROW4>, dim3(workers), dim3(kThreads), kSmem, stream, a, p);
 }
 
 }  // namespace
