@@ -43,7 +43,10 @@ namespace {
 constexpr int kSoftWarps = 8;              // two for each quarter of tensor memory
 constexpr int kExpandWarp0 = 8;
 constexpr int kExpandWarps = 16;
-constexpr int kRows = 64 / kExpandWarps;   // of a block, a warp
+// Warps that expand a block together.  4-bit rows: two sets of 8 take the blocks in turn, since a warp's way through
+// a block (its loads, two waits, two proxy fences) is mostly latency.
+template <bool ROW4>
+constexpr int kSetWarps = ROW4 ? 8 : kExpandWarps;
 constexpr int kMmaWarp = 24;
 constexpr int kPvWarp = 25;
 constexpr int kThreads = 28 * 32;
@@ -161,6 +164,15 @@ __device__ __forceinline__ uint4 expand8(uint2 w, uint32_t m) {
 }
 // Bits 15 and 31: an infinite or NaN bf16.
 __device__ __forceinline__ uint32_t rope_bits(uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; }
+// The largest magnitudes (signs aside; NaN wins).
+__device__ __forceinline__ uint32_t largest_bf16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t largest_of(const uint4& v) {
+  return largest_bf16(largest_bf16(v.x, v.y), largest_bf16(v.z, v.w));
+}
 // Any e4m3 NaN among four bytes: a byte of 0x7f carries into its bit 7.
 __device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
 
@@ -207,16 +219,16 @@ __device__ __forceinline__ uint2 ldg_once(const uint8_t* src) {
 // The 8-byte words of its warp's rows that a lane l holds.  Words 0..55 of a row are the nope
 // part (word w: columns 8 (w % 8) .. + 7 of group w / 8), 56 the scales, 57..72 the rope.
 // a[j], b[j]: words l and l + 32 of row j; c[k]: word 64 + l % 9 of row 3 k + l / 9.
-constexpr int kTails = (kRows + 2) / 3;
+constexpr int kRows8 = 64 / kSetWarps<false>, kTails = (kRows8 + 2) / 3;
 struct RowWords {
-  uint2 a[kRows], b[kRows], c[kTails];
+  uint2 a[kRows8], b[kRows8], c[kTails];
 };
 
-// 4-bit rows: lane l holds the 16-byte words l / 4 (a), 8 + l / 4 (b) and 16 + l / 4 (c; lanes 28 .. 31: word 22
-// once more) of row l % 4 of its warp.  Words 0..13 of a row are 32 nope columns each, one scale
-// group; 14 is the scales, 15..22 the rope.
+// 4-bit rows: lane l holds the 16-byte words 4 k + l / 8 (w[k]; k = 5 of lanes 24 .. 31: word 22 once more) of
+// row l % 8 of its warp.  Words 0..13 of a row are 32 nope columns each, one scale group; 14 is the
+// scales, 15..22 the rope.
 struct RowWords4 {
-  uint4 a, b, c;
+  uint4 w[6];
 };
 __device__ __forceinline__ uint4 ldg16_once(const uint8_t* src) {
   uint4 v;
@@ -321,30 +333,32 @@ struct TwoRows {
       m[i] = raise ? top[i] : m[i];
       shift[i] = m[i] == -INFINITY ? 0.f : m[i];
     }
-    float sum[4] = {0.f, 0.f, 0.f, 0.f}, rsum[4] = {0.f, 0.f, 0.f, 0.f};
+    // two scores, weights or sums an instruction: the columns of a row side by side
+    Two sum[2] = {Two(0.f), Two(0.f)}, rsum[2] = {Two(0.f), Two(0.f)};
+    const Two by(MODS ? 1.f : scale2);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float e[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x = v[4 * j + k];
-        e[k] = exp2_fast(MODS ? x - shift[k / 2] : fmaf(x, scale2, -shift[k / 2]));
-        sum[k] += e[k];
-      }
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        p[2 * j + i] = pack_bf16(e[2 * i], e[2 * i + 1]);
-        rsum[2 * i] += __uint_as_float(p[2 * j + i] << 16);
-        rsum[2 * i + 1] += __uint_as_float(p[2 * j + i] & 0xffff0000u);
+        const Two x(v[4 * j + 2 * i], v[4 * j + 2 * i + 1]), away(-shift[i]);
+        float e0, e1;
+        (MODS ? x + away : fma2(x, by, away)).get(&e0, &e1);
+        e0 = exp2_fast(e0);
+        e1 = exp2_fast(e1);
+        sum[i] = sum[i] + Two(e0, e1);
+        p[2 * j + i] = pack_bf16(e0, e1);
+        rsum[i] = rsum[i] + Two(__uint_as_float(p[2 * j + i] << 16), __uint_as_float(p[2 * j + i] & 0xffff0000u));
       }
-    }
     // a row of the cache that is not finite is held as zeros; who sees it becomes NaN
     const bool odd0 = (seen0 & rows.y) != 0, odd1 = (seen1 & rows.y) != 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const bool odd = i == 0 ? odd0 : odd1;
-      l[i] = odd ? __uint_as_float(0x7fffffffu) : fmaf(l[i], alpha[i], sum[2 * i] + sum[2 * i + 1]);
-      lr[i] = odd ? __uint_as_float(0x7fffffffu) : fmaf(lr[i], alpha[i], rsum[2 * i] + rsum[2 * i + 1]);
+      float s0, s1, r0, r1;
+      sum[i].get(&s0, &s1);
+      rsum[i].get(&r0, &r1);
+      l[i] = odd ? __uint_as_float(0x7fffffffu) : fmaf(l[i], alpha[i], s0 + s1);
+      lr[i] = odd ? __uint_as_float(0x7fffffffu) : fmaf(lr[i], alpha[i], r0 + r1);
     }
   }
 };
@@ -459,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i)
-      mbar_init(bar(i), i < EMPTY ? kExpandWarps : i < PFULL || i == SFULL || i == SFULL + 1 ? 1 : kSoftWarps);
+      mbar_init(bar(i), i < EMPTY ? kSetWarps<ROW4> : i < PFULL || i == SFULL || i == SFULL + 1 ? 1 : kSoftWarps);
     *stop = 0;
     fence_mbar_init();
   }
@@ -484,10 +498,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // reads a row at once, 256 consecutive bytes a load.  All warps expand a block together,
     // since that lies between a value product and the scores of the block after next; the
     // next block's bytes are on their way meanwhile.
-    const int w16 = warp - kExpandWarp0;
+    constexpr int kRows = 64 / kSetWarps<ROW4>, kSets = kExpandWarps / kSetWarps<ROW4>;      // kRows: of a block, a warp
+    const int w16 = (warp - kExpandWarp0) % kSetWarps<ROW4>, set = kSets > 1 ? (warp - kExpandWarp0) / kSetWarps<ROW4> : 0;
     const int mine = kRows * w16 + (lane & (kRows - 1));
     const int c_row = lane / 9, c_word = lane % 9;       // of words c
-    if (x0 < x1) {
+    if (x0 + set < x1) {
       const int pages_step = kChunkBlk / a.page_size, rest = kChunkBlk % a.page_size;
       const uint32_t stride = static_cast<uint32_t>(a.stride);
       // page id of the cursor's row, -1 = no row there
@@ -520,10 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t have = __ballot_sync(0xffffffffu, there) & ((1u << kRows) - 1u);
         row_now = there ? static_cast<uint32_t>(r) : 0u;
         if constexpr (ROW4) {
-          const uint8_t* src = a.pool + static_cast<uint64_t>(row_now) * stride + 16 * (lane >> 2);
-          d.a = ldg16_once(src);
-          d.b = ldg16_once(src + 128);
-          d.c = ldg16_once(src + (lane < 28 ? 256 : 240));
+          const uint8_t* src = a.pool + static_cast<uint64_t>(row_now) * stride + 16 * (lane >> 3);
+#pragma unroll
+          for (int k = 0; k < 5; ++k) d.w[k] = ldg16_once(src + 64 * k);
+          d.w[5] = ldg16_once(src + (lane < 24 ? 320 : 304));
           return have;
         } else {
         const uint8_t* base = a.pool + 8 * lane;
@@ -546,78 +561,92 @@ __global__ void __launch_bounds__(kThreads, 1)
       at.x1 = x1;
       at.t = t_first;
       at.load<EVEN>(a, plan, mine, a.page_size);
+      auto advance = [&](int blocks) {
+#pragma unroll
+        for (int i = 0; i < blocks; ++i) at.step<EVEN>(a, plan, mine, a.page_size, pages_step, rest);
+      };
+      if (kSets > 1 && set > 0) advance(1);
       std::conditional_t<ROW4, RowWords4, RowWords> d;
       const int count = x1 - x0;
       uint32_t have = fetch(lookup(at), at.off, d);
-      at.step<EVEN>(a, plan, mine, a.page_size, pages_step, rest);
+      advance(kSets);
       int id = lookup(at), off = at.off;
       bool ok = true;
       if constexpr (ROW4) {
-        const int j = lane & 3, w = lane >> 2;
-        const uint32_t key = static_cast<uint32_t>((kRows * w16 + j) & 7);
+        const int j = lane & 7, w = lane >> 3;
+        const uint32_t key = static_cast<uint32_t>(j);               // of the swizzle: the row modulo 8
         const uint32_t row = sbase + (kRows * w16 + j) * 128;
-        // nope words w and 8 + w: four 16-byte units of slab w / 2 of the first and the second half; rope
-        // units w + 1 (word c) and 0 (word b of lanes 28 .. 31)
-        const uint32_t to = row + (w >> 1) * kSlab, rope = row + 3 * kSlab;
-        auto unit = [&](int u) { return ((static_cast<uint32_t>(u) ^ key) << 4); };
-        const bool nope_b = w < 6, rope_b = w == 7;
-        Place place;
-        int turn = 0;                // of the masks' three
-        for (int n = 0; n < count; ++n) {
-          // the scale bytes of the lane's two words
-          const uint32_t s0 = __shfl_sync(0xffffffffu, d.b.x, 24 + j), s1 = __shfl_sync(0xffffffffu, d.b.y, 24 + j);
-          const uint32_t s2 = __shfl_sync(0xffffffffu, d.b.z, 24 + j), s3 = __shfl_sync(0xffffffffu, d.b.w, 24 + j);
-          const uint32_t sa = ((w < 4 ? s0 : s1) >> (8 * (w & 3))) & 0xffu;
-          const uint32_t sb = nope_b ? ((w < 4 ? s2 : s3) >> (8 * (w & 3))) & 0xffu : 0u;
-          // 2^(s - 1) as two bf16, in two factors past bf16's exponents
-          auto first = [](uint32_t s) { return (min(s, 128u) + 126u) * 0x00800080u; };
-          auto second = [](uint32_t s) { return (max(s, 128u) - 1u) * 0x00800080u; };
-          const bool large = __any_sync(0xffffffffu, max(sa, sb) > 128u);
+        auto unit = [&](uint32_t u) { return (u ^ key) << 4; };
+        // 2^(s - 1) as two bf16, in two factors past bf16's exponents
+        auto first = [](uint32_t s) { return (min(s, 128u) + 126u) * 0x00800080u; };
+        auto second = [](uint32_t s) { return (max(s, 128u) - 1u) * 0x00800080u; };
+        for (int n = set; n < count; n += kSets) {
+          // the scale bytes of the lane's four nope words (the fourth: words 12 and 13, lanes below 16)
+          uint32_t s[4];
+          {
+            const int from = 16 + j;
+            const uint32_t sx = __shfl_sync(0xffffffffu, d.w[3].x, from), sy = __shfl_sync(0xffffffffu, d.w[3].y, from);
+            const uint32_t sz = __shfl_sync(0xffffffffu, d.w[3].z, from), sw = __shfl_sync(0xffffffffu, d.w[3].w, from);
+            s[0] = (sx >> (8 * w)) & 0xffu;
+            s[1] = (sy >> (8 * w)) & 0xffu;
+            s[2] = (sz >> (8 * w)) & 0xffu;
+            s[3] = w < 2 ? (sw >> (8 * w)) & 0xffu : 0u;
+          }
+          const uint32_t most_s = max(max(s[0], s[1]), max(s[2], s[3]));
+          const bool large = __any_sync(0xffffffffu, most_s > 128u);
           // rows that are not finite are held as zeros
-          const uint32_t rc = rope_bits(d.c.x) | rope_bits(d.c.y) | rope_bits(d.c.z) | rope_bits(d.c.w);
-          const uint32_t rb = rope_b ? rope_bits(d.b.x) | rope_bits(d.b.y) | rope_bits(d.b.z) | rope_bits(d.b.w) : 0u;
+          uint32_t largest = largest_bf16(largest_of(d.w[4]), largest_of(d.w[5]));
+          if (w == 3) largest = largest_bf16(largest, largest_of(d.w[3]));
+          const bool rope_odd = (rope_bits(largest) & 0x80008000u) != 0;
           uint32_t dropped = 0;
-          if (__any_sync(0xffffffffu, ((rc | rb) & 0x80008000u) != 0 || max(sa, sb) >= 253u)) {
-            const bool bad = ((rc | rb) & 0x80008000u) != 0 || past_bf16(d.a, sa) || (nope_b && past_bf16(d.b, sb));
-            const uint32_t who = __ballot_sync(0xffffffffu, bad);
+          if (__any_sync(0xffffffffu, rope_odd || most_s >= 253u)) {
+            bool bad = rope_odd || (w < 2 && past_bf16(d.w[3], s[3]));
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) dropped |= (who & (0x11111111u << i)) != 0 ? 1u << i : 0u;
+            for (int k = 0; k < 3; ++k) bad |= past_bf16(d.w[k], s[k]);
+            const uint32_t who = __ballot_sync(0xffffffffu, bad);
+            dropped = (who | who >> 8 | who >> 16 | who >> 24) & 0xffu;
             if ((dropped >> j) & 1) {
-              const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-              d.a = d.b = d.c = zero;
+#pragma unroll
+              for (int k = 0; k < 6; ++k) d.w[k] = make_uint4(0u, 0u, 0u, 0u);
             }
           }
-          if (n >= 3) ok = warp_wait(bar(EMPTY + place.at), place.phase ^ 1, stop, a.status);
-          if (!ok) break;
-          auto words = [&](const uint4& v, uint32_t s, uint32_t at, bool mine) {
-            const uint32_t m1 = first(s), m2 = second(s);
+          // word 4 k + w of the nope part: four 16-byte units of a slab, two words to one
+          auto word = [&](const uint4& v, uint32_t scale, uint32_t at) {
+            const uint32_t m1 = first(scale), m2 = second(scale);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint4 o = expand_nibbles(word_of(v, i), m1);
               if (large) o = mul4(o, m2);
-              sts_if(mine, at + unit(4 * (w & 1) + i), o);
+              sts(at + unit(4 * (w & 1) + i), o);
             }
           };
-          words(d.a, sa, to + place.at * kHalf, true);
+          const Place p0 = Place::of(2 * n), p1 = Place::of(2 * n + 1);
+          uint32_t to = row + p0.at * kHalf + (w >> 1) * kSlab;
+          if (n >= 3) ok = warp_wait(bar(EMPTY + p0.at), p0.phase ^ 1, stop, a.status);
+          if (!ok) break;
+          word(d.w[0], s[0], to);
+          word(d.w[1], s[1], to + 2 * kSlab);
           if (lane == 0) {
-            masks[turn * 32 + w16] = static_cast<uint8_t>(have);
-            masks[turn * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
+            masks[(n % kMasks) * 32 + w16] = static_cast<uint8_t>(have);
+            masks[(n % kMasks) * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && !(n == a.fault_block && w16 == 0)) mbar_arrive(bar(FULL + place.at));
-          place.next();
-          if (n >= 3) ok = warp_wait(bar(EMPTY + place.at), place.phase ^ 1, stop, a.status);
+          if (lane == 0 && !(n == a.fault_block && w16 == 0)) mbar_arrive(bar(FULL + p0.at));
+          if (n >= 3) ok = warp_wait(bar(EMPTY + p1.at), p1.phase ^ 1, stop, a.status);
           if (!ok) break;
-          words(d.b, sb, to + place.at * kHalf, nope_b);
-          sts(rope + place.at * kHalf + unit(rope_b ? 0 : w + 1), rope_b ? d.b : d.c);
+          to = row + p1.at * kHalf + (w >> 1) * kSlab;
+          word(d.w[2], s[2], to);
+          if (w < 2) word(d.w[3], s[3], to + 2 * kSlab);
+          // the rope: its unit 0 is word 15, 1 + w word 16 + w, 5 + w word 20 + w
+          const uint32_t rope = row + p1.at * kHalf + 3 * kSlab;
+          sts(rope + unit(1 + w), d.w[4]);
+          sts(rope + unit(w == 3 ? 0 : 5 + w), w == 3 ? d.w[3] : d.w[5]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(FULL + place.at));
-          place.next();
-          turn = turn + 1 == kMasks ? 0 : turn + 1;
+          if (lane == 0) mbar_arrive(bar(FULL + p1.at));
           have = fetch(id, off, d);
-          at.step<EVEN>(a, plan, mine, a.page_size, pages_step, rest);
+          advance(kSets);
           id = lookup(at);
           off = at.off;
         }
@@ -868,10 +897,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const volatile unsigned long long* mk =
             reinterpret_cast<const volatile unsigned long long*>(smem + kMaskOff + (n % kMasks) * 32);
-        const unsigned long long m0 = mk[0], m1 = mk[1], d0 = mk[2], d1 = mk[3];
         ulonglong2 rows = make_ulonglong2(~0ull, 0ull);
-        if (__any_sync(0xffffffffu, (m0 & m1) != 0x0f0f0f0f0f0f0f0full || (d0 | d1) != 0))
-          rows = make_ulonglong2(halves(m0, m1), halves(d0, d1));
+        if constexpr (ROW4) {        // a byte a warp: 8 rows
+          rows = make_ulonglong2(mk[0], mk[2]);
+        } else {
+          const unsigned long long m0 = mk[0], m1 = mk[1], d0 = mk[2], d1 = mk[3];
+          if (__any_sync(0xffffffffu, (m0 & m1) != 0x0f0f0f0f0f0f0f0full || (d0 | d1) != 0))
+            rows = make_ulonglong2(halves(m0, m1), halves(d0, d1));
+        }
         ok = warp_wait(bar(SFULL + (n & 1)), (n >> 1) & 1, stop, a.status);
         if (!ok) break;
         if (idle) {
