@@ -588,7 +588,14 @@ int launch_sparse4(const void* q, const void* kv, const int32_t* indices, const 
   const int blocks = (p->topk - 1) / kChunkBlk + 1, tiles = (p->num_heads - 1) / kSingleRows + 1;
   const int line = p->batch * tiles * blocks, share = (line + kMaxSms - 1) / kMaxSms;      // 65,535 * 2 * 1,024 at most
   const int per = share > kMinShare ? share : kMinShare;
-  plan.even = {blocks, tiles, p->num_heads, per, line, per / 4 < kSnap ? per / 4 : kSnap};
+  // Shares that end with their tiles, some SMs left over, or shares along the line, whose change of tile costs as
+  // much as kTileChange blocks (13,000 cycles: Q, and results that the next tile's scores wait for).  32 queries
+  // of 2,048 and 64 heads: 4 shares of 8 blocks each, or 152 of 7; 96 of 999 and 16 heads: one of 16, or 152 of 11.
+  constexpr int kTileChange = 4;
+  int pieces = p->batch * tiles <= kMaxSms ? kMaxSms / (p->batch * tiles) : 0;
+  if (pieces > (blocks + 1) / kMinShare) pieces = (blocks + 1) / kMinShare;
+  if (pieces > 0 && (blocks - 1) / pieces + 1 > per + kTileChange) pieces = 0;
+  plan.even = {blocks, tiles, p->num_heads, pieces, per, line, per / 4 < kSnap ? per / 4 : kSnap};
   return launch_single_path(a, plan, stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 

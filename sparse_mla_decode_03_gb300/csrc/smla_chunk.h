@@ -56,7 +56,9 @@ struct ChunkPlan {
   // Sparse decode: every tile has as many blocks, so that the plan follows from its number (blocks 0: it
   // lies in memory, above).
   struct Even {
-    int blocks, tiles, heads, per, line, snap;      // of a tile; of a sequence; share and line as make_plan has them
+    int blocks, tiles, heads;      // of a tile; of a sequence
+    int pieces;                    // shares of a tile, if whole shares make up each; else 0, and
+    int per, line, snap;           // shares along the line as make_plan has them
   } even;
 };
 
@@ -71,6 +73,10 @@ __device__ __forceinline__ bool is_even(const ChunkPlan& p) {
 template <bool EVEN>
 __device__ __forceinline__ int plan_begin(const ChunkPlan& p, int worker) {
   if (!is_even<EVEN>(p)) return p.begin[worker];
+  if (p.even.pieces > 0) {
+    const int t = worker / p.even.pieces;
+    return min(p.even.line, t * p.even.blocks + (worker - t * p.even.pieces) * p.even.blocks / p.even.pieces);
+  }
   const int n = p.even.blocks, x = min(worker * p.even.per, p.even.line), rest = x % n;
   return rest <= p.even.snap ? x - rest : n - rest <= p.even.snap ? x + n - rest : x;
 }
