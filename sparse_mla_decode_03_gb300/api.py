@@ -375,6 +375,15 @@ def _token_rows(name: str, kv: torch.Tensor, device: torch.device) -> int:
     return kv.stride(0) if kv.shape[0] > 1 else QK
 
 
+def _rows_of_heads(name: str, t: torch.Tensor, tokens: int, width: int, device: torch.device) -> Tuple[int, ...]:
+    """Checks bf16 [tokens, H, width]; its strides."""
+    stride = t.stride()
+    if (len(stride) != 3 or stride[2] != 1 or t.shape[2] != width or t.shape[0] != tokens or t.dtype != torch.bfloat16
+            or t.device != device):
+        raise ValueError(f"{name} must be bf16 [{tokens}, H, {width}] with unit column stride on {device}")
+    return stride
+
+
 def _token_places(kv_pages: torch.Tensor, page_size: int, block_table: torch.Tensor, cu_q: torch.Tensor,
                   kv_lens: torch.Tensor) -> _lib.SmlaCacheParams:
     _pool(kv_pages, page_size)
@@ -424,19 +433,21 @@ def smla_cache_append_rotary(kv: torch.Tensor, kv_pages: torch.Tensor, block_tab
         raise ValueError(f"rotary must be contiguous fp32 [positions, 64] on {dev}")
     if (q_rope is None) != (q is None):
         raise ValueError("q_rope and q come together")
-    T, H, strides = kv.shape[0], 0, (0, 0, 0, 0)
+    T, H, q0, q1, r0, r1 = kv.shape[0], 0, 0, 0, 0, 0
     if q is not None:
-        for name, t, width in (("q_rope", q_rope, QK - NOPE), ("q", q, QK)):
-            if (t.dim() != 3 or t.shape[0] != T or t.shape[2] != width or t.dtype != torch.bfloat16
-                    or t.stride(2) != 1 or t.device != dev):
-                raise ValueError(f"{name} must be bf16 [{T}, H, {width}] with unit column stride on {dev}")
+        q0, q1, _ = _rows_of_heads("q", q, T, QK, dev)
+        r0, r1, _ = _rows_of_heads("q_rope", q_rope, T, QK - NOPE, dev)
         H = q.shape[1]
         if q_rope.shape[1] != H:
             raise ValueError("q_rope and q must have as many heads")
-        if (T > 1 and (q.stride(0) == 0 or abs(q.stride(0)) < QK)) or (H > 1 and q.stride(1) < QK):
+        if (T > 1 and q0 < QK) or (H > 1 and q1 < QK) or (
+                T > 1 and H > 1 and q0 < (H - 1) * q1 + QK and q1 < (T - 1) * q0 + QK):
             raise ValueError("the rows of q must not overlap")
-        strides = tuple(t.stride(i) if t.shape[i] > 1 else 0 for t in (q_rope, q) for i in (0, 1))
-    r = _lib.SmlaRotaryParams(_adr(rotary), _adr(q_rope), _adr(q), rotary.shape[0], *strides, H,
+        if T <= 1:
+            q0 = r0 = 0
+        if H <= 1:
+            q1 = r1 = 0
+    r = _lib.SmlaRotaryParams(_adr(rotary), _adr(q_rope), _adr(q), rotary.shape[0], r0, r1, q0, q1, H,
                               0 if interleaved else 1, 0)
     side = _side(stream, dev)
     with _on(dev):
@@ -622,9 +633,10 @@ def smla_cache_reorder(kv_pages: torch.Tensor, page_size: int, ref_count: torch.
 _LOGITS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
-def make_beam_params(groups: int, beams: int, vocab: int, num_out: int, row_stride: int = 0,
+def make_beam_params(groups: int, beams: int, vocab: int, num_out: int, row_stride: Optional[int] = None,
                      logits_type: int = 0, end_token: int = 0) -> _lib.SmlaBeamParams:
-    return _lib.SmlaBeamParams(groups, beams, vocab, num_out, row_stride or vocab, logits_type, end_token, 0)
+    return _lib.SmlaBeamParams(groups, beams, vocab, num_out, vocab if row_stride is None else row_stride,
+                               logits_type, end_token, 0)
 
 
 def smla_beam_workspace_size(params: _lib.SmlaBeamParams) -> int:
@@ -646,7 +658,7 @@ def smla_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: Option
                      stream: Optional[torch.cuda.Stream] = None
                      ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """The num_out (default: as many as beams) best continuations of each group by score +
-    log-softmax(logits): logits fp32, bf16 or fp16 [G * K, V] (rows any stride apart), scores fp32
+    log-softmax(logits): logits fp32, bf16 or fp16 [G * K, V] (rows at least V elements apart), scores fp32
     [G, K].  Beams with finished (uint8 or bool [G * K]) keep their score and take end_token.  Returns
     (parents int32 [G, num_out], rows of logits; tokens int32; scores fp32), best first."""
     dev = logits.device
