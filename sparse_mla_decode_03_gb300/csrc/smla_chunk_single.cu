@@ -80,10 +80,11 @@ __device__ __forceinline__ uint32_t o_column(uint32_t tmem, int c) {
   return tmem + static_cast<uint32_t>(c) + (c < static_cast<int>(kColTail) ? kUpper : 0u);
 }
 
-// FULL / EMPTY: a place of the ring filled / its value product done; PFULL: weights written (one for each of
-// two blocks: a quarter may be a block ahead of another); QFULL: a tile's Q in tensor memory; SFULL /
+// FULL / EMPTY: a place of the ring filled / its value product done; PFULL: weights written (one for each block of
+// the ring: a quarter may be two blocks ahead of another, and no more, since a third one's place waits for the
+// value product that the other holds up); QFULL: a tile's Q in tensor memory; SFULL /
 // SEMPTY: scores of a block in tensor memory / taken by the softmax, two in turn; OEMPTY: results taken.
-enum Bar : int { FULL = 0, EMPTY = kPlaces, PFULL = 2 * kPlaces, QFULL = PFULL + 2, SFULL, SEMPTY = SFULL + 2, OEMPTY = SEMPTY + 2, kBars };
+enum Bar : int { FULL = 0, EMPTY = kPlaces, PFULL = 2 * kPlaces, QFULL = PFULL + kPlaces / 2, SFULL, SEMPTY = SFULL + 2, OEMPTY = SEMPTY + 2, kBars };
 
 // A place of the ring, and the parity of its uses.
 struct Place {
@@ -494,9 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kExpandWarp0 && warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsExpand) : "memory");
     // ---------------- expand ----------------
-    // Rows 4 w .. + 3 of a block are warp w's; lane j's cursor follows row j % 4; the warp
-    // reads a row at once, 256 consecutive bytes a load.  All warps expand a block together,
-    // since that lies between a value product and the scores of the block after next; the
+    // Rows kRows w .. of a block are warp w's of a set; lane j's cursor follows row j % kRows.  8-bit rows: all
+    // 16 warps expand a block together, and a warp reads a row at once, 256 consecutive bytes a load.  4-bit
+    // rows: two sets of 8 warps take the blocks in turn, and a load is 64 bytes of each of a warp's 8 rows.  The
     // next block's bytes are on their way meanwhile.
     constexpr int kRows = 64 / kSetWarps<ROW4>, kSets = kExpandWarps / kSetWarps<ROW4>;      // kRows: of a block, a warp
     const int w16 = (warp - kExpandWarp0) % kSetWarps<ROW4>, set = kSets > 1 ? (warp - kExpandWarp0) / kSetWarps<ROW4> : 0;
@@ -826,14 +827,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kId256 = idesc_bf16(64, 256, false, true), kId128 = idesc_bf16(64, 128, false, true),
                          kId64 = idesc_bf16(64, 64, false, true);
       const uint32_t lp = static_cast<uint32_t>(d0) + (kPOff >> 4), lv = static_cast<uint32_t>(dv);
-      uint32_t n = 0, k = 0;
+      uint32_t k = 0;                      // tiles so far
       Place place;
       bool ok = true;
       for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
         const int end = min(x1, plan_cum<EVEN>(plan, t + 1));
         uint32_t old = 0;                  // the tile's first product overwrites O
-        for (; ok && x < end; ++x, ++n, old = 1) {
-          ok = warp_wait(bar(PFULL + (n & 1)), (n >> 1) & 1, stop, a.status);
+        for (; ok && x < end; ++x, old = 1) {
+          ok = warp_wait(bar(PFULL + (place.at >> 1)), place.phase, stop, a.status);
           if (ok && old == 0 && k > 0) ok = warp_wait(bar(OEMPTY), (k - 1) & 1, stop, a.status);
           if (!ok) break;
           tc_fence_after();
@@ -910,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (idle) {
           if (lane == 0) {
             mbar_arrive(bar(SEMPTY + (n & 1)));
-            mbar_arrive(bar(PFULL + (n & 1)));
+            mbar_arrive(bar(PFULL + (Place::of(2 * n).at >> 1)));
           }
           continue;
         }
@@ -943,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(PFULL + (n & 1)));
+        if (lane == 0) mbar_arrive(bar(PFULL + (Place::of(2 * n).at >> 1)));
       }
       if (!ok) break;
       // all scores of the tile have been seen: the next one's Q may take this one's place
