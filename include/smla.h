@@ -328,8 +328,9 @@ typedef struct smla_rotary_params {
   const float* table;           /* fp32 [table_rows, 64]: cosines of the 32 pairs, then sines; device,
                                    16-byte aligned                                      */
   const void* q_rope;           /* bf16 [total_tokens, num_heads, 64], 16-byte aligned  */
-  void* q;                      /* bf16 [total_tokens, num_heads, 512], 16-byte aligned; q_rope and q
-                                   share no memory                                      */
+  void* q;                      /* bf16 [total_tokens, num_heads, 512], 16-byte aligned; q_rope is
+                                   q's own columns 448 .. 511 (with q's strides) or shares no
+                                   memory with q                                        */
   int64_t table_rows;           /* >= 1                                                 */
   int64_t q_rope_token_stride, q_rope_head_stride;  /* elements, >= 0, multiples of 8   */
   int64_t q_token_stride, q_head_stride;            /* the same; no two (token, head) rows share memory */
@@ -462,7 +463,8 @@ int smla_beam_workspace_size(const smla_beam_params* p, size_t* bytes);
  *   finished    uint8 [G * beams] or NULL
  *   parents, tokens  int32 [G, num_out]                   out_scores fp32 [G, num_out]
  *   workspace   >= smla_beam_workspace_size(p) bytes, 256-byte aligned; contents on entry do not matter
- * The results overlap no input.  Calls whose kernels may overlap need a workspace each.
+ * The results overlap no input, but out_scores may be scores (num_out = beams).  Calls whose kernels may
+ * overlap need a workspace each.
  */
 int smla_beam_select(const void* logits, const float* scores, const uint8_t* finished, int32_t* parents,
                      int32_t* tokens, float* out_scores, const smla_beam_params* p, void* workspace,

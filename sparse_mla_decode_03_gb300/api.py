@@ -424,7 +424,7 @@ def smla_cache_append_rotary(kv: torch.Tensor, kv_pages: torch.Tensor, block_tab
     """smla_cache_append with the position rotation on the way: the rope columns of kv by the token's
     row of rotary fp32 [positions, 64] (cosines of the 32 pairs, then sines), pairs (2 i, 2 i + 1) if
     interleaved, else (i, i + 32).  With q_rope bf16 [T, H, 64] the queries' rope columns are rotated
-    too, into q[:, :, 448:] of q bf16 [T, H, 512]."""
+    too, into q[:, :, 448:] of q bf16 [T, H, 512] (which may be q_rope itself)."""
     p = _token_places(kv_pages, page_size, block_table, cu_q, kv_lens)
     dev = kv_pages.device
     stride = _token_rows("kv", kv, dev)
@@ -659,8 +659,8 @@ def smla_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: Option
                      ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """The num_out (default: as many as beams) best continuations of each group by score +
     log-softmax(logits): logits fp32, bf16 or fp16 [G * K, V] (rows at least V elements apart), scores fp32
-    [G, K].  Beams with finished (uint8 or bool [G * K]) keep their score and take end_token.  Returns
-    (parents int32 [G, num_out], rows of logits; tokens int32; scores fp32), best first."""
+    [G, K].  Beams with finished (uint8 or bool [G * K]) keep their score and take end_token.  out_scores may
+    be scores.  Returns (parents int32 [G, num_out], rows of logits; tokens int32; scores fp32), best first."""
     dev = logits.device
     if logits.dim() != 2 or logits.dtype not in _LOGITS or logits.stride(1) != 1 or not logits.is_cuda:
         raise ValueError("logits must be fp32, bf16 or fp16 [G * K, V] with unit column stride on a CUDA device")

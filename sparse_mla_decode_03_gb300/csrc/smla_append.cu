@@ -93,8 +93,8 @@ __device__ __forceinline__ uint4 shfl_xor(const uint4& x, int mask) {
                     __shfl_xor_sync(0xffffffffu, x.z, mask), __shfl_xor_sync(0xffffffffu, x.w, mask));
 }
 
-// A warp takes a token's row, or the rope columns of kHeads of its queries (8 lanes a head, 16
-// bytes a lane).
+// A warp takes a token's row, or the rope columns of kHeads of its queries (8 lanes a head, 16 bytes a lane,
+// each of which a lane reads before it writes there, and no other lane: q_rope may be q's own columns).
 template <bool ROW4, bool NEIGHBOURS>
 __global__ void __launch_bounds__(256) append_rotary_kernel(const AppendArgs a, const RotaryArgs r) {
   __shared__ uint4 stage[8][38];

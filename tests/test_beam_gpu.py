@@ -258,3 +258,11 @@ def test_a_beam_searched_run(row):
     # every page is counted as often as it is listed
     counts = torch.bincount(table[table >= 0].long(), minlength=num_pages)
     assert torch.equal(counts.int(), ref)
+
+
+def test_scores_that_are_replaced_where_they_lie():
+    logits, scores = _logits(40, 8, 5000, 5)
+    want = select_reference(logits, scores, 8)
+    got = m.smla_beam_select(logits, scores, out_scores=scores)
+    assert got[2] is scores
+    _same(got, want)

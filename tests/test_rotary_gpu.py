@@ -144,3 +144,17 @@ def test_strided_queries_and_replay():
         pos = torch.as_tensor(np.concatenate([np.arange(L - 3, L) for L in new]), device="cuda")
         _near(q[:, :, 448:], *rotate64(q_rope, turn[pos][:, None], False))
         assert (store[:, :, :456] == 0).all() and (store[:, :, 520:] == 0).all()
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_queries_rotated_where_they_lie(interleaved):
+    pool = random_pool4(8, 16, 3)
+    turn = rotary_table(128)
+    q = torch.randn(5, 33, 512, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    before = q.clone()
+    lens = [40, 77]
+    m.smla_cache_append_rotary(q.new_zeros(5, 512), pool, dev(tables(lens, 16, 8, 3)), 16, _ints([0, 2, 5]), _ints(lens), turn,
+                               interleaved=interleaved, q_rope=q[:, :, 448:], q=q)
+    at = torch.tensor([38, 39, 74, 75, 76], device="cuda")
+    _near(q[:, :, 448:], *rotate64(before[:, :, 448:], turn[at][:, None], interleaved))
+    assert torch.equal(q[:, :, :448], before[:, :, :448])
