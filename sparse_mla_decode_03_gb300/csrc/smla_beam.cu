@@ -6,8 +6,10 @@
 // and each group's num_out largest are wanted.  Two launches.  The first reads the logits once: warps
 // go over runs of them, 2 KB (a step) at a time, and leave each step's maximum and each run's sum of
 // exponentials; they meet nobody and keep no candidates.  The second, a CTA a group, finds a border from
-// the maxima that at least num_out candidates reach and few steps do, reads those few steps again, and
-// ranks what reaches the border by counting.
+// the maxima that at least num_out candidates reach and few steps do (bit by bit, a count of the CTA's
+// threads a bit), reads those few steps again, and ranks what reaches the border by counting.  Where too many
+// logits reach it (few steps, beams far apart), the border comes from those steps' logits; where too many are
+// equal, the steps that may hold something better are gone through one by one.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -63,25 +65,18 @@ __device__ __forceinline__ unsigned long long key_of(float x, int token) {
 __device__ __forceinline__ float key_value(unsigned long long k) { return unsortable(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ int key_token(unsigned long long k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
 
-// Lanes of a part, so that there are at least four times as many parts of a CTA as results.
-__device__ __forceinline__ int part_lanes(int num_out) { return num_out <= 8 ? 16 : num_out <= 16 ? 8 : num_out <= 32 ? 4 : 2; }
-// The num_out-th largest maximum of the CTA's parts, given each thread's; -infinity counts.  All threads call;
-// the answer is in *least after a barrier.
-__device__ __forceinline__ void part_maximum(float mine, int lanes, float* part) {
-  for (int o = 1; o < lanes; o <<= 1) mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, o));
-  if (threadIdx.x % lanes == 0) part[threadIdx.x / lanes] = mine;
-}
-__device__ __forceinline__ void rank_parts(const float* part, int lanes, int num_out, float* least) {
-  const int parts = kThreads / lanes, t = threadIdx.x;
-  if (t >= parts) return;
-  const float p = part[t];
-  int rank = 0;
-  for (int j = 0; j < parts; j += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(part + j);
-    rank += (v.x > p || (v.x == p && j < t)) + (v.y > p || (v.y == p && j + 1 < t)) + (v.z > p || (v.z == p && j + 2 < t)) +
-            (v.w > p || (v.w == p && j + 3 < t));
+// The largest t >= t0 of which count(t) (the same in all threads, falling in t) is `least` at least, from bit `bit`
+// on, above which it is t0; any of which it is `most` at most will do.
+template <class F>
+__device__ __forceinline__ uint32_t border_of(uint32_t t, uint32_t bit, int least, int most, F count) {
+  for (; bit != 0; bit >>= 1) {
+    const int c = count(t | bit);
+    if (c >= least) {
+      t |= bit;
+      if (c <= most) break;
+    }
   }
-  if (rank == num_out - 1) *least = p;
+  return t;
 }
 
 // Words of 16, 4 or 2 bytes.
@@ -302,22 +297,19 @@ template <class T, int BYTES>
 __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   constexpr int kPer = BYTES / sizeof(T);
   __shared__ Beam beam[kMaxOut];
-  __shared__ float4 part4[kThreads / 8];
-  __shared__ float least;
-  __shared__ int count, blocks;
+  __shared__ int count, blocks, next;
+  __shared__ uint32_t top_key;
+  __shared__ int counts[32];                     // of the border's bits
   __shared__ int block[kBlocks];                 // step * beams + beam
   __shared__ Candidate list[kStep<__half> + kMaxOut];
   __shared__ Candidate best[kMaxOut];
   static_assert(kList <= kStep<__half> + kMaxOut, "one list for both paths");
-  float* part = reinterpret_cast<float*>(part4);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = blockIdx.x, n = a.num_out, row0 = group * a.beams;
   grid_dep_wait();
   grid_dep_launch();
-  if (tid == 0) {
-    count = blocks = 0;
-    least = INFINITY;
-  }
+  if (tid == 0) count = blocks = top_key = 0;
+  if (tid < 32) counts[tid] = 0;
   for (int b = warp; b < a.beams; b += kWarps) {
     const float score = a.scores[row0 + b];
     Beam m = {score, 0.0, 0.0, score, kDead};
@@ -377,25 +369,25 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
     if (beam[b].state == kLive) return a.maxima[static_cast<int64_t>(row0 + b) * a.steps + step];
     return beam[b].state == kDone && step == 0 ? 0.f : -INFINITY;
   };
-  const int lanes = part_lanes(n), all = a.beams * a.steps;
+  const int all = a.beams * a.steps;
   float mine = -INFINITY;
   for (int i = tid; i < all; i += kThreads) {
-    // neighbours are of different beams: a part's maximum is then seldom that of a beam far behind
+    // neighbours are of different beams: a thread's maximum is then seldom that of a beam far behind
     const int b = i % a.beams;
     const float x = maximum(i / a.beams, b);
     float low;
     nearly(x, b, &low);
     if (x > -INFINITY) mine = fmaxf(mine, low);
   }
-  part_maximum(mine, lanes, part);
-  __syncthreads();
-  rank_parts(part, lanes, n, &least);
-  __syncthreads();
+  const uint32_t key = sortable(mine);
+  const uint32_t most = __reduce_max_sync(0xffffffffu, key);
+  if (lane == 0) atomicMax(&top_key, most);
+  float border = unsortable(border_of(0u, 1u << 31, n, n, [&](uint32_t t) { return __syncthreads_count(key >= t); }));
   for (int i = tid; i < all; i += kThreads) {
     const int b = i % a.beams;
     const float x = maximum(i / a.beams, b);
     float low;
-    if (x == -INFINITY || nearly(x, b, &low) < least) continue;
+    if (x == -INFINITY || nearly(x, b, &low) < border) continue;
     const int at = atomicAdd(&blocks, 1);
     if (at < kBlocks) block[at] = i;
   }
@@ -410,50 +402,61 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
       f(b, x, first);
     }
   };
-  float border = least;
-  if (border == -INFINITY) {
-    // fewer steps than results: the border from the logits themselves
-    __syncthreads();
-    mine = -INFINITY;
-    each_block([&](int b, const Held<T>& x, int) {
-      if (beam[b].state != kLive) return;
+  auto gather = [&] {
+    each_block([&](int b, const Held<T>& x, int first) {
+      if (beam[b].state == kDone) {
+        float low;
+        if (lane == 0 && nearly(0.f, b, &low) >= border) {
+          const int at = atomicAdd(&count, 1);
+          if (at < kList) list[at] = {key_of(0.f, a.end_token), static_cast<unsigned long long>(b)};
+        }
+        return;
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float low;
-        nearly(x.top(k), b, &low);
-        if (x.top(k) > -INFINITY) mine = fmaxf(mine, low);
+        if (x.top(k) == -INFINITY || nearly(x.top(k), b, &low) < border || *const_cast<volatile int*>(&count) > kList) continue;
+#pragma unroll
+        for (int i = k * (kEach<T> / 4); i < (k + 1) * (kEach<T> / 4); ++i) {
+          const float v = x.at(i);
+          if (v == -INFINITY || nearly(v, b, &low) < border) continue;
+          const int at = atomicAdd(&count, 1);
+          // the logit and its place; made a candidate below
+          if (at < kList) list[at] = {key_of(v, first + (i / kPer) * 32 * kPer + i % kPer), static_cast<unsigned long long>(b)};
+        }
       }
     });
-    part_maximum(mine, lanes, part);
     __syncthreads();
-    rank_parts(part, lanes, n, &least);
+  };
+  gather();
+  if (blocks <= kBlocks && count > kList) {
+    // Few steps (a small vocabulary), or a beam far ahead that has few: the border from the logits themselves.
     __syncthreads();
-    border = least;
+    if (tid == 0) count = 0;
+    int pass = 0;
+    const uint32_t low = sortable(border), apart = low ^ top_key;
+    const uint32_t bit = apart != 0 ? 1u << (31 - __clz(apart)) : 0u;
+    border = unsortable(border_of(bit != 0 ? low & ~(2 * bit - 1) : low, bit, n, kList / 4, [&](uint32_t t) {
+      const float value = unsortable(t);
+      int c = 0;
+      each_block([&](int b, const Held<T>& x, int) {
+        // logits from `least` on have values from `value` on, whatever was rounded
+        const float near = beam[b].near, top = static_cast<float>(beam[b].top);
+        const float least = top + (value - near) + 0x1p-21f * (fabsf(top) + fabsf(value) + fabsf(near));
+        if (beam[b].state == kDone) {
+          c += lane == 0 && 0.f >= least;
+          return;
+        }
+#pragma unroll
+        for (int i = 0; i < kEach<T>; ++i) c += x.at(i) >= least;
+      });
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0 && c > 0) atomicAdd(counts + pass, c);
+      __syncthreads();
+      return counts[pass++];
+    }));
+    gather();
   }
-  each_block([&](int b, const Held<T>& x, int first) {
-    if (beam[b].state == kDone) {
-      float low;
-      if (lane == 0 && nearly(0.f, b, &low) >= border) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kList) list[at] = {key_of(0.f, a.end_token), static_cast<unsigned long long>(b)};
-      }
-      return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float low;
-      if (x.top(k) == -INFINITY || nearly(x.top(k), b, &low) < border) continue;
-#pragma unroll
-      for (int i = k * (kEach<T> / 4); i < (k + 1) * (kEach<T> / 4); ++i) {
-        const float v = x.at(i);
-        if (v == -INFINITY || nearly(v, b, &low) < border) continue;
-        const int at = atomicAdd(&count, 1);
-        // the logit and its place; made a candidate below
-        if (at < kList) list[at] = {key_of(v, first + (i / kPer) * 32 * kPer + i % kPer), static_cast<unsigned long long>(b)};
-      }
-    }
-  });
-  __syncthreads();
   auto put = [&](int i, const Candidate& c) {
     const int64_t o = static_cast<int64_t>(group) * n + i;
     const int b = static_cast<int>(c.place >> 32);
@@ -483,9 +486,24 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
     for (int i = found + tid; i < n; i += kThreads) put(i, none);
     return;
   }
-  // Many equal ones: all steps in turn, against the n best so far.
+  // Many equal ones: in turn the steps that may have something better than the n best so far, each by what its
+  // largest logit would be as its first.
   int kept = 0;
   for (int i = 0; i < all; ++i) {
+    if (kept == n) {
+      if (tid == 0) next = all;
+      __syncthreads();
+      for (int j = i + tid; j < all; j += kThreads) {
+        const int b = j / a.steps, step = j - b * a.steps;
+        const float x = maximum(step, b);
+        if (x == -INFINITY || !before(candidate(x, beam[b].state == kDone ? a.end_token : step * kStep<T>, b), best[n - 1])) continue;
+        atomicMin(&next, j);
+        break;
+      }
+      __syncthreads();
+      i = next;
+      if (i >= all) break;
+    }
     const int b = i / a.steps, step = i % a.steps;
     if (maximum(step, b) == -INFINITY) continue;
     __syncthreads();

@@ -266,3 +266,27 @@ def test_scores_that_are_replaced_where_they_lie():
     got = m.smla_beam_select(logits, scores, out_scores=scores)
     assert got[2] is scores
     _same(got, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("G,K,n,V", [(5, 8, 16, 11306), (4, 9, 18, 1054), (3, 7, 7, 1850), (2, 10, 10, 112), (2, 64, 64, 600), (1, 3, 6, 224)])
+def test_few_steps_and_beams_far_apart(G, K, n, V, dtype):
+    """The best come from one or two beams, whose steps are fewer than the results."""
+    logits, scores = _logits(G, K, V, V, dtype)
+    _check(logits, scores * 4, n)
+    done = torch.zeros(G * K, dtype=torch.uint8, device="cuda")
+    done[::3] = 1
+    _check(logits, scores * 4, n, done, 2)
+
+
+def test_more_equal_steps_than_are_read_again():
+    logits = torch.full((24, 60000), -1.5, device="cuda")
+    logits[5, 59999] = 3.0
+    logits[17, 1024] = 2.0
+    scores = torch.zeros(2, 12, device="cuda")
+    scores[1] -= torch.arange(12, device="cuda") * 0.5
+    _check(logits, scores, 24)
+    lowest = torch.finfo(torch.bfloat16).min
+    logits = torch.full((16, 70000), lowest, dtype=torch.bfloat16, device="cuda")
+    logits[:, 69000:69003] = 1.0
+    _check(logits, torch.zeros(2, 8, device="cuda"), 40)
