@@ -387,13 +387,22 @@ __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const Chu
   grid_dep_launch();
   int4 cut;                               // first row of the tile, rows, first and last worker
   if (is_even<true>(p)) {
-    // the border of shares y and y + 1, if it is the first inside a tile
-    const int c = static_cast<int>(blockIdx.y) + 1, x = plan_begin<true>(p, c), t = x / p.even.blocks;
-    if (x >= p.even.line || x == t * p.even.blocks || plan_begin<true>(p, c - 1) > t * p.even.blocks) return;
+    // tile y, or, of more tiles than borders, the one that border y + 1 is the first inside
+    const int n = p.even.blocks, y = blockIdx.y;
+    const bool by_tile = a.B * p.even.tiles < kMaxSms;
+    const int t = by_tile ? y : plan_begin<true>(p, y + 1) / n, from = t * n;
+    if (!by_tile && (plan_begin<true>(p, y + 1) >= p.even.line || plan_begin<true>(p, y + 1) == from || plan_begin<true>(p, y) > from))
+      return;
+    auto share = [&](int x) {        // the last that begins at block x or before: a border moves by less than a share
+      int c = p.even.pieces > 0 ? x / n * p.even.pieces : x / p.even.per;
+      while (c > 0 && plan_begin<true>(p, c) > x) --c;
+      while (c + 1 < kMaxSms && plan_begin<true>(p, c + 1) <= x) ++c;
+      return c;
+    };
+    const int first = by_tile ? share(from) : y, last = p.even.pieces > 0 ? first + p.even.pieces - 1 : share(from + n - 1);
+    if (first == last) return;
     const int4 tile = plan_tile<true>(p, t);
-    int last = c;
-    while (last + 1 < static_cast<int>(gridDim.y) + 1 && plan_begin<true>(p, last + 1) < (t + 1) * p.even.blocks) ++last;
-    cut = make_int4(tile.y, tile.z, c - 1, last);
+    cut = make_int4(tile.y, tile.z, first, last);
   } else {
     const int cuts = p.head[2];
     cut = p.cut[blockIdx.y];
@@ -483,8 +492,6 @@ int check_chunk(const smla_chunk_params* p) {
   return SMLA_OK;
 }
 
-// SMs of the GPU that this library is for: the workers that a workspace has room for.
-constexpr int kMaxSms = 152;
 constexpr int kMaxPairs = kMaxSms / 2;
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -532,7 +539,8 @@ cudaError_t launch_merge(const ChunkArgs& a, const ChunkPlan& p, int rows, int w
   if (workers < 2) return cudaSuccess;
   // few tiles: many partial results a row (see the kernel)
   const int64_t tiles = (static_cast<int64_t>(a.T) * a.H + rows - 1) / rows + a.B;
-  const unsigned cuts = static_cast<unsigned>(tiles < workers - 1 && p.even.blocks == 0 ? tiles : workers - 1);
+  const int64_t even = static_cast<int64_t>(a.B) * p.even.tiles, most = p.even.blocks > 0 ? even : tiles;
+  const unsigned cuts = static_cast<unsigned>(most < workers - 1 ? most : workers - 1);
   if (tiles * 4 <= workers)
     return launch_programmatic(merge_kernel<8>, dim3(rows, cuts), dim3(256), 0, s, a, p, rows);
   return launch_programmatic(merge_kernel<1>, dim3(rows / 8, cuts), dim3(256), 0, s, a, p, rows);

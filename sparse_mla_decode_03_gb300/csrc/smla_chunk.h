@@ -13,6 +13,7 @@
 namespace smla {
 
 constexpr int kChunkBlk = 64;     // positions of a block
+constexpr int kMaxSms = 152;      // SMs of the GPU that this library is for: the workers that a workspace has room for
 
 struct ChunkArgs {
   const uint16_t* q;
