@@ -429,14 +429,32 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
     __syncthreads();
   };
   gather();
-  if (blocks <= kBlocks && count > kList) {
-    // Few steps (a small vocabulary), or a beam far ahead that has few: the border from the logits themselves.
+  // Few steps (a small vocabulary), or a beam far ahead that has few: the border from the lanes' shares of them,
+  auto again = [&] {
+    const bool many = blocks <= kBlocks && count > kList;
     __syncthreads();
-    if (tid == 0) count = 0;
+    if (many && tid == 0) count = 0;
+    return many;
+  };
+  if (again()) {
+    mine = -INFINITY;
+    each_block([&](int b, const Held<T>& x, int) {
+      float m = 0.f, low;
+      if (beam[b].state == kLive) m = fmaxf(fmaxf(x.top(0), x.top(1)), fmaxf(x.top(2), x.top(3)));
+      else if (lane != 0) m = -INFINITY;
+      nearly(m, b, &low);
+      if (m > -INFINITY) mine = fmaxf(mine, low);
+    });
+    const uint32_t key = sortable(mine);
+    border = unsortable(border_of(0u, 1u << 31, n, n, [&](uint32_t t) { return __syncthreads_count(key >= t); }));
+    gather();
+  }
+  if (again()) {
+    // or from the logits themselves
     int pass = 0;
     const uint32_t low = sortable(border), apart = low ^ top_key;
     const uint32_t bit = apart != 0 ? 1u << (31 - __clz(apart)) : 0u;
-    border = unsortable(border_of(bit != 0 ? low & ~(2 * bit - 1) : low, bit, n, kList / 4, [&](uint32_t t) {
+    border = unsortable(border_of(bit != 0 ? low & ~(2 * bit - 1) : low, bit, n, kList / 2, [&](uint32_t t) {
       const float value = unsortable(t);
       int c = 0;
       each_block([&](int b, const Held<T>& x, int) {
@@ -472,16 +490,29 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
     for (int i = tid; i < found; i += kThreads) {
       const Candidate c = list[i];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < found; ++j) rank += before(list[j], c);
       if (rank < n) f(rank, c);
     }
   };
-  const int found = count;
+  int found = count;
   if (blocks <= kBlocks && found <= kList) {
-    for (int i = tid; i < found; i += kThreads) {
-      list[i] = candidate(key_value(list[i].value), key_token(list[i].value), static_cast<int>(list[i].place));
+    static_assert(kList <= kThreads, "a candidate a thread");
+    Candidate mine = none;
+    if (tid < found) mine = candidate(key_value(list[tid].value), key_token(list[tid].value), static_cast<int>(list[tid].place));
+    // ranking compares all with all: first drop those whose upper half is not among the n largest
+    const uint32_t upper = static_cast<uint32_t>(mine.value >> 32);
+    bool in = tid < found;
+    if (found > 2 * n) {
+      const uint32_t t = border_of(0u, 1u << 31, n, n + n / 2, [&](uint32_t t) { return __syncthreads_count(upper >= t); });
+      in = in && upper >= t;
     }
     __syncthreads();
+    if (tid == 0) count = 0;
+    __syncthreads();
+    if (in) list[atomicAdd(&count, 1)] = mine;
+    __syncthreads();
+    found = count;
     ranked(found, put);
     for (int i = found + tid; i < n; i += kThreads) put(i, none);
     return;
