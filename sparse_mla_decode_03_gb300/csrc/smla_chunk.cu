@@ -56,35 +56,6 @@ __device__ long long block_sum(long long v, long long* total, long long* warp_su
   return s - v + (warp > 0 ? warp_sums[warp - 1] : 0);
 }
 
-// What a sequence brings: its entries of q, clamped to it, and its blocks.  wrong: its offsets
-// decrease or are not q's, so that its entries may be another's too, or its positions astray.
-struct Sequence {
-  int first, n, len, blocks;
-  bool wrong;
-};
-__device__ __forceinline__ Sequence sequence(const ChunkArgs& a, int b) {
-  Sequence s = {0, 0, 0, 0, false};
-  if (b >= a.B) return s;
-  const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
-  s.wrong = c0 < 0 || c1 < c0 || c1 > a.T;
-  s.len = max(a.kv_lens[b], 0);
-  s.first = min(max(c0, 0), a.T);
-  s.n = min(max(c1, s.first), a.T) - s.first;
-  // one without cached tokens keeps one block (of zeros) for its tiles to read; a length may be
-  // as large as its type allows (seq_len below cuts it to the copy)
-  if (s.n > 0) s.blocks = max(1, s.len / kChunkBlk + (s.len % kChunkBlk != 0 ? 1 : 0));
-  return s;
-}
-// Its first block in the expanded copy, given the blocks before it, and how many positions
-// of it find room there.
-__device__ __forceinline__ int seq_base(const ChunkPlan& p, long long before) {
-  return static_cast<int>(min(before, static_cast<long long>(p.cap_blocks)));
-}
-__device__ __forceinline__ int seq_len(const ChunkPlan& p, const Sequence& s, long long before) {
-  const long long left = p.cap_blocks - before;
-  return s.blocks <= left ? s.len : left > 0 ? static_cast<int>(left) * kChunkBlk : 0;
-}
-
 constexpr int kPlanSeqs = 1024;    // sequences and tiles whose plan fits in shared memory
 constexpr int kPlanTiles = 2048;
 struct PlanShared {
@@ -160,17 +131,8 @@ __device__ void make_plan(const ChunkArgs& a, const ChunkPlan& p, int tile_rows,
       }
       const int row = first * a.H + (t - base) * tile_rows;
       const int rows = min(tile_rows, last * a.H - row);
-      int low = 0x7fffffff, high = 0;
-      for (int tok = row / a.H; tok <= (row + rows - 1) / a.H; ++tok) {
-        int lo, hi, pos;
-        visible(a, b, tok, len, &lo, &hi, &pos);
-        if (hi > lo) {
-          low = min(low, lo);
-          high = max(high, hi);
-        }
-      }
-      const int blk = high > 0 ? low / kChunkBlk : 0;
-      n = high > 0 ? (high - 1) / kChunkBlk + 1 - blk : 1;
+      int blk;
+      tile_blocks(a, b, row, rows, len, &blk, &n);
       tile = make_int4(b, row, rows, blk);
     }
     long long all;
@@ -507,6 +469,10 @@ bool use_pairs(const smla_chunk_params* p) {
 size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
   size_t at = 0;
   plan->even = {};
+  // the tiles of sequences that all end inside one: no less than there are
+  plan->few = !use_pairs(p) && p->batch <= kFewTiles &&
+              (static_cast<int64_t>(p->total_q) * p->num_heads +
+               static_cast<int64_t>(p->batch) * (p->num_heads < kSingleRows ? kSingleRows - p->num_heads : 0)) / kSingleRows <= kFewTiles;
   auto take = [&](size_t bytes) {
     char* q = base + at;
     at += round256(bytes);
@@ -562,7 +528,7 @@ cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_
 cudaError_t launch_single_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_t s) {
   const int workers = kMaxSms;
   cudaError_t e = cudaSuccess;
-  if (p.even.blocks == 0)
+  if (p.even.blocks == 0 && !p.few)
     e = launch_programmatic(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, p, kSingleRows, workers);
   if (e == cudaSuccess) e = launch_chunk_single(a, p, workers, s);
   return e == cudaSuccess ? launch_merge(a, p, kSingleRows, workers, s) : e;

@@ -54,6 +54,9 @@ struct ChunkPlan {
                          // of them whose row has a value that is not finite
   uint16_t* kv;          // [blocks][64][512] bf16: the expanded copy
   int64_t cap_blocks;    // blocks of the expanded copy, not counting one of zeros behind
+  // Single kernel: 32 sequences and tiles at most, so that a warp of each CTA works the plan out for itself, into
+  // shared memory, and the first one what the merge needs
+  bool few;
   // Sparse decode: every tile has as many blocks, so that the plan follows from its number (blocks 0: it
   // lies in memory, above).
   struct Even {
@@ -125,6 +128,50 @@ __device__ __forceinline__ void visible(const ChunkArgs& a, int b, int t, int le
   *hi = max(0, min(len, a.vis_end != nullptr ? a.vis_end[t] : *pos + 1));
 }
 
+// What a sequence brings: its entries of q, clamped to it, and its blocks.  wrong: its offsets
+// decrease or are not q's, so that its entries may be another's too, or its positions astray.
+struct Sequence {
+  int first, n, len, blocks;
+  bool wrong;
+};
+__device__ __forceinline__ Sequence sequence(const ChunkArgs& a, int b) {
+  Sequence s = {0, 0, 0, 0, false};
+  if (b >= a.B) return s;
+  const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
+  s.wrong = c0 < 0 || c1 < c0 || c1 > a.T;
+  s.len = max(a.kv_lens[b], 0);
+  s.first = min(max(c0, 0), a.T);
+  s.n = min(max(c1, s.first), a.T) - s.first;
+  // one without cached tokens keeps one block (of zeros) for its tiles to read; a length may be
+  // as large as its type allows (seq_len below cuts it to the copy)
+  if (s.n > 0) s.blocks = max(1, s.len / kChunkBlk + (s.len % kChunkBlk != 0 ? 1 : 0));
+  return s;
+}
+// Its first block in the expanded copy, given the blocks before it, and how many positions
+// of it find room there.
+__device__ __forceinline__ int seq_base(const ChunkPlan& p, long long before) {
+  return static_cast<int>(min(before, static_cast<long long>(p.cap_blocks)));
+}
+__device__ __forceinline__ int seq_len(const ChunkPlan& p, const Sequence& s, long long before) {
+  const long long left = p.cap_blocks - before;
+  return s.blocks <= left ? s.len : left > 0 ? static_cast<int>(left) * kChunkBlk : 0;
+}
+
+// The first block that rows row .. row + rows - 1 of sequence b see, and how many (one at least).
+__device__ __forceinline__ void tile_blocks(const ChunkArgs& a, int b, int row, int rows, int len, int* first, int* n) {
+  int low = 0x7fffffff, high = 0;
+  for (int tok = row / a.H; tok <= (row + rows - 1) / a.H; ++tok) {
+    int lo, hi, pos;
+    visible(a, b, tok, len, &lo, &hi, &pos);
+    if (hi > lo) {
+      low = min(low, lo);
+      high = max(high, hi);
+    }
+  }
+  *first = high > 0 ? low / kChunkBlk : 0;
+  *n = high > 0 ? (high - 1) / kChunkBlk + 1 - *first : 1;
+}
+
 // Pair kernel: tiles of 256 rows on pairs of SMs, over the expanded copy.
 constexpr int kPairRows = 256;
 cudaError_t pair_workers(int* workers);
@@ -132,6 +179,7 @@ cudaError_t launch_chunk_pair(const ChunkArgs& a, const ChunkPlan& p, int worker
 
 // Single kernel: tiles of 64 rows on one SM each, which expands the rows itself.
 constexpr int kSingleRows = 64;
+constexpr int kFewTiles = 32;      // a lane each
 cudaError_t launch_chunk_single(const ChunkArgs& a, const ChunkPlan& p, int workers, cudaStream_t stream);
 
 // The tensor map of `rows` rows of 512 bf16, in boxes of 64 columns, 128-byte swizzle.

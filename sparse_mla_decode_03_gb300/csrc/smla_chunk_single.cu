@@ -49,6 +49,7 @@ template <bool ROW4>
 constexpr int kSetWarps = ROW4 ? 8 : kExpandWarps;
 constexpr int kMmaWarp = 24;
 constexpr int kPvWarp = 25;
+constexpr int kPlanWarp = 26;
 constexpr int kThreads = 28 * 32;
 // Registers (setmaxnreg): what the launch gives is split among the warpgroups.
 constexpr int kLaunchRegs = 72;
@@ -67,9 +68,12 @@ constexpr int kPlaces = 6;
 constexpr int kPOff = 3 * kSlab;
 constexpr int kBarOff = kPlaces * kHalf;
 constexpr int kMasks = 3;                  // blocks whose masks are held: a block is expanded again only after its weights
-constexpr int kMaskOff = kBarOff + 256;    // [3 blocks][mapped, not finite][16 half bytes]
-constexpr int kMaxOff = kMaskOff + 128;    // float [2 blocks][2 halves][64 rows]: largest scores; later sums
-constexpr int kSmem = kMaxOff + 1024 + 1024;
+constexpr int kMaskOff = kBarOff + 192;    // [3 blocks][mapped, not finite][16 half bytes]
+constexpr int kMaxOff = kMaskOff + 96;     // float [2 blocks][2 halves][64 rows]: largest scores; later sums
+// The plan of few tiles: int4 [tiles] sequence + 256 rows, first row, positions of the sequence, first block;
+// int [tiles + 1] where each begins on the line; the share's begin, end and first tile.
+constexpr int kPlanOff = kMaxOff + 1024, kPlanCum = kPlanOff + 16 * kFewTiles, kPlanShare = kPlanCum + 4 * (kFewTiles + 1);
+constexpr int kSmem = kPlanShare + 12 + 1024;
 static_assert(kSmem <= 195 * 1024, "the carve-out step, less what the system takes");
 
 // Tensor memory.  64 rows of a product lie in 16 lanes of each quarter, the lower ones or the upper, so
@@ -105,6 +109,38 @@ struct Place {
   }
 };
 
+__device__ __forceinline__ int lds4(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ int4 lds16(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// The plan as a worker reads it: worked out from a tile's number, in shared memory, or in the workspace.
+template <bool EVEN>
+struct Plan {
+  const ChunkArgs& a;
+  const ChunkPlan& p;
+  uint32_t smem;
+  __device__ __forceinline__ bool few() const { return !is_even<EVEN>(p) && p.few; }
+  __device__ __forceinline__ int begin(int worker) const { return few() ? lds4(smem + kPlanShare) : plan_begin<EVEN>(p, worker); }
+  __device__ __forceinline__ int end(int worker) const { return few() ? lds4(smem + kPlanShare + 4) : plan_begin<EVEN>(p, worker + 1); }
+  __device__ __forceinline__ int start(int worker, int x) const { return few() ? lds4(smem + kPlanShare + 8) : plan_start<EVEN>(p, worker, x); }
+  __device__ __forceinline__ int cum(int t) const { return few() ? lds4(smem + kPlanCum + 4 * t) : plan_cum<EVEN>(p, t); }
+  // sequence, first row, rows, first block
+  __device__ __forceinline__ int4 tile(int t) const {
+    if (!few()) return plan_tile<EVEN>(p, t);
+    const int4 v = lds16(smem + kPlanOff + 16 * t);
+    return make_int4(v.x & 255, v.y, v.x >> 8, v.w);
+  }
+  // positions of tile t's sequence b
+  __device__ __forceinline__ int len(int t, int b) const { return few() ? lds4(smem + kPlanOff + 16 * t + 8) : plan_len<EVEN>(a, p, b); }
+};
+
 // A row of the blocks on the line, walked tile by tile and each tile's share from its last
 // block to its first (scores that a distance bias shapes then fall along the way, and the
 // running maximum seldom rises): page and row in it follow by subtractions, divided out at a
@@ -114,22 +150,22 @@ struct Cursor {
   int b, left;            // sequence, and its positions from the row's on
   int page, off;
   template <bool EVEN>
-  __device__ __forceinline__ void load(const ChunkArgs& a, const ChunkPlan& p, int row, int page_size) {
-    const int4 tile = plan_tile<EVEN>(p, t);
-    next = plan_cum<EVEN>(p, t + 1);
+  __device__ __forceinline__ void load(const Plan<EVEN>& p, int row, int page_size) {
+    const int4 tile = p.tile(t);
+    next = p.cum(t + 1);
     b = tile.x;
-    const int pos = (tile.w + (min(x1, next) - 1 - plan_cum<EVEN>(p, t))) * kChunkBlk + row;
-    left = plan_len<EVEN>(a, p, b) - pos;
+    const int pos = (tile.w + (min(x1, next) - 1 - p.cum(t))) * kChunkBlk + row;
+    left = p.len(t, b) - pos;
     page = pos / page_size;
     off = pos - page * page_size;
   }
   // pages, rest: 64 / page_size and 64 % page_size
   template <bool EVEN>
-  __device__ __forceinline__ void step(const ChunkArgs& a, const ChunkPlan& p, int row, int page_size, int pages, int rest) {
+  __device__ __forceinline__ void step(const Plan<EVEN>& p, int row, int page_size, int pages, int rest) {
     ++x;
     if (x == next && x < x1) {
       ++t;
-      load<EVEN>(a, p, row, page_size);
+      load(p, row, page_size);
       return;
     }
     left += kChunkBlk;
@@ -261,21 +297,21 @@ __device__ __forceinline__ bool past_bf16(const uint4& v, uint32_t s) {
 // 16-lane tensor-memory load deals them out: lane 4 g + q has columns 8 j + 2 q and + 1 (of
 // the warp's half) of rows g (v[4 j], v[4 j + 1]) and g + 8 (v[4 j + 2], v[4 j + 3]).  Sums
 // stay per thread until the end; the maximum is the row's, of both halves.
-template <bool MODS, bool EVEN>
+template <bool MODS>
 struct TwoRows {
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
   int lo[2] = {0, 0}, hi[2] = {0, 0}, pos[2] = {0, 0};
   float slope2[2] = {0.f, 0.f};
   ScoreMods mods;
 
-  __device__ __forceinline__ TwoRows(const ChunkArgs& a, const ChunkPlan& plan, const int4& tile, int row0)
+  __device__ __forceinline__ TwoRows(const ChunkArgs& a, const int4& tile, int len, int row0)
       : mods(a) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = row0 + 8 * i;
       if (row >= tile.z) continue;
       const int tok = (tile.y + row) / a.H;
-      visible(a, tile.x, tok, plan_len<EVEN>(a, plan, tile.x), &lo[i], &hi[i], &pos[i]);
+      visible(a, tile.x, tok, len, &lo[i], &hi[i], &pos[i]);
       if (MODS && a.slopes != nullptr) slope2[i] = a.slopes[tile.y + row - tok * a.H] * kLog2e;
     }
   }
@@ -458,6 +494,100 @@ __device__ __forceinline__ void drain() {
   while (clock64() - t0 < 2000000) {
   }
 }
+
+// The plan of 32 sequences and tiles at most, by one warp: what make_plan does, a lane a sequence and then a lane a
+// tile.  Every CTA needs its own share; the first one leaves the cut tiles for the merge.
+__device__ __forceinline__ int lanes_before(int v, int* total) {
+  const int lane = threadIdx.x & 31;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  return s - v;
+}
+__device__ __forceinline__ void plan_few(const ChunkArgs& a, const ChunkPlan& p, uint32_t smem, int worker) {
+  const int lane = threadIdx.x & 31, workers = gridDim.x;
+  const Sequence s = sequence(a, lane);        // nothing past the last
+  int tiles, blocks;
+  const int t0 = lanes_before((s.n * a.H + kSingleRows - 1) / kSingleRows, &tiles);
+  const int b0 = lanes_before(s.blocks, &blocks);      // 32 * 2^25 at most
+  const int held = seq_len(p, s, b0);
+  bool report = held != s.len && lane < a.B;
+  if (__any_sync(0xffffffffu, s.wrong)) {
+    tiles = 0;
+    report = true;
+  }
+  int b = 0;
+  for (int i = 0; i < a.B; ++i)
+    if (__shfl_sync(0xffffffffu, t0, i) <= lane) b = i;
+  const int first = __shfl_sync(0xffffffffu, s.first, b), last = first + __shfl_sync(0xffffffffu, s.n, b);
+  const int len = __shfl_sync(0xffffffffu, held, b), base = __shfl_sync(0xffffffffu, t0, b);
+  int row = 0, rows = 0, blk = 0, n = 0;
+  if (lane < tiles) {
+    row = first * a.H + (lane - base) * kSingleRows;
+    rows = min(kSingleRows, last * a.H - row);
+    tile_blocks(a, b, row, rows, len, &blk, &n);
+  }
+  int line;
+  const int at = lanes_before(n, &line);       // 2^30 at most
+  if (report && worker == 0) atomicCAS(a.status, 0, SMLA_ERR_INDEX_RANGE);
+  auto put = [&](uint32_t to, int v) { sts4(smem + to, static_cast<uint32_t>(v)); };
+  if (lane < tiles) {
+    sts(smem + kPlanOff + 16 * lane, make_uint4(static_cast<uint32_t>(b | rows << 8), static_cast<uint32_t>(row),
+                                                static_cast<uint32_t>(len), static_cast<uint32_t>(blk)));
+    put(kPlanCum + 4 * lane, at);
+  }
+  if (lane == 0) put(kPlanCum + 4 * tiles, line);
+  __syncwarp();
+  const int per = max(kMinShare, (line + workers - 1) / workers), snap = min(kSnap, per / 4);
+  auto cum = [&](int t) { return lds4(smem + kPlanCum + 4 * t); };
+  // where share c begins, and the tile there (-1 behind the line)
+  auto border = [&](int c, int* t) {
+    int x = min(c * per, line);                // 152 * (2^30 / 152 + 2) at most
+    *t = -1;
+    if (x == line) return x;
+    int lo = 0;
+    for (int hi = tiles; hi - lo > 1;) {
+      const int mid = (lo + hi) >> 1;
+      if (cum(mid) <= x) lo = mid;
+      else hi = mid;
+    }
+    if (x - cum(lo) <= snap) x = cum(lo);
+    else if (cum(lo + 1) - x <= snap) x = cum(++lo);
+    if (x < line) *t = lo;
+    return x;
+  };
+  if (lane < 2) {
+    int t;
+    const int x = border(worker + lane, &t);
+    put(kPlanShare + 4 * lane, x);
+    if (lane == 0) put(kPlanShare + 8, t);
+  }
+  if (worker != 0) return;
+  // tiles that a border lies inside: the last shares that begin at the tile's start or before, and before its end
+  int c0 = 0, c1 = 0;
+  if (lane < tiles) {
+    auto share = [&](int x) {
+      int t, c = min(x / per, workers - 1);
+      while (c > 0 && border(c, &t) > x) --c;
+      while (c + 1 < workers && border(c + 1, &t) <= x) ++c;
+      return c;
+    };
+    c0 = share(at);
+    c1 = share(at + n - 1);
+  }
+  const uint32_t cuts = __ballot_sync(0xffffffffu, c0 != c1);
+  if (c0 != c1) p.cut[__popc(cuts & ((1u << lane) - 1))] = make_int4(row, rows, c0, c1);
+  if (lane == 0) p.head[2] = __popc(cuts);
+}
+
+__device__ __noinline__ void plan_few_apart(const ChunkArgs& a, const ChunkPlan& p, uint32_t smem, int worker) {
+  plan_few(a, p, smem, worker);
+}
+
 template <bool MODS, bool ROW4>
 __global__ void __launch_bounds__(kThreads, 1)
     single_kernel(const ChunkArgs a, const ChunkPlan plan) {
@@ -490,7 +620,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch();
 
   constexpr bool EVEN = ROW4 && !MODS;     // may be a sparse call
-  const int x0 = plan_begin<EVEN>(plan, worker), x1 = plan_begin<EVEN>(plan, worker + 1), t_first = plan_start<EVEN>(plan, worker, x0);
+  const Plan<EVEN> line = {a, plan, sbase};
+  if (line.few()) {
+    if (warp == kPlanWarp) {      // out of line where the other roles would spill
+      if constexpr (EVEN) plan_few_apart(a, plan, sbase, worker);
+      else plan_few(a, plan, sbase, worker);
+    }
+    __syncthreads();
+  }
+  const int x0 = line.begin(worker), x1 = line.end(worker), t_first = line.start(worker, x0);
 
   if (warp >= kExpandWarp0 && warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsExpand) : "memory");
@@ -561,10 +699,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       at.x = x0;
       at.x1 = x1;
       at.t = t_first;
-      at.load<EVEN>(a, plan, mine, a.page_size);
+      at.load(line, mine, a.page_size);
       auto advance = [&](int blocks) {
 #pragma unroll
-        for (int i = 0; i < blocks; ++i) at.step<EVEN>(a, plan, mine, a.page_size, pages_step, rest);
+        for (int i = 0; i < blocks; ++i) at.step(line, mine, a.page_size, pages_step, rest);
       };
       if (kSets > 1 && set > 0) advance(1);
       std::conditional_t<ROW4, RowWords4, RowWords> d;
@@ -777,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         turn = turn + 1 == kMasks ? 0 : turn + 1;
         // the next block's bytes, and the page ids of the one after it
         have = fetch(id, off, d);
-        at.step<EVEN>(a, plan, mine, a.page_size, pages_step, rest);
+        at.step(line, mine, a.page_size, pages_step, rest);
         id = lookup(at);
         off = at.off;
       }
@@ -798,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Place place;
       bool ok = true;
       for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
-        const int end = min(x1, plan_cum<EVEN>(plan, t + 1));
+        const int end = min(x1, line.cum(t + 1));
         ok = warp_wait(bar(QFULL), k & 1, stop, a.status);
         for (; ok && x < end; ++x, ++n) {
           if (n >= 2) ok = warp_wait(bar(SEMPTY + (n & 1)), ((n >> 1) - 1) & 1, stop, a.status);
@@ -831,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Place place;
       bool ok = true;
       for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
-        const int end = min(x1, plan_cum<EVEN>(plan, t + 1));
+        const int end = min(x1, line.cum(t + 1));
         uint32_t old = 0;                  // the tile's first product overwrites O
         for (; ok && x < end; ++x, old = 1) {
           ok = warp_wait(bar(PFULL + (place.at >> 1)), place.phase, stop, a.status);
@@ -874,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = lane >> 2;
     volatile float* most = reinterpret_cast<volatile float*>(smem + kMaxOff);
     auto give_q = [&](int t) {
-      load_q(a, plan_tile<EVEN>(plan, t), tmem + lanes, quarter, half);
+      load_q(a, line.tile(t), tmem + lanes, quarter, half);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(QFULL));
@@ -886,12 +1024,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     if (x < x1) give_q(t);
     for (; ok && x < x1; ++t) {
-      const int4 tile = plan_tile<EVEN>(plan, t);
-      const int begin = plan_cum<EVEN>(plan, t), after = plan_cum<EVEN>(plan, t + 1), end = min(x1, after);
+      const int4 tile = line.tile(t);
+      const int begin = line.cum(t), after = line.cum(t + 1), end = min(x1, after);
       const int nb = end - x, blk = tile.w + (end - 1 - begin);     // the first block
       // rows past the tile stay whatever they are (a product's rows do not mix), so a warp
       // without rows only keeps step
-      TwoRows<MODS, EVEN> st(a, plan, tile, 16 * quarter + g);
+      TwoRows<MODS> st(a, tile, line.len(t, tile.x), 16 * quarter + g);
       const bool idle = 16 * quarter >= tile.z;
       for (i = 0; ok && i < nb; ++i, ++n) {
         ok = warp_wait(bar(FULL + Place::of(2 * n).at), Place::of(2 * n).phase, stop, a.status);     // the masks' writers
@@ -988,8 +1126,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // meetings of the schedule, one a block and three a tile, so that neither waits for good.
     if (!ok)
       for (; x < x1; ++t, i = 0, held = 0) {
-        const int end = min(x1, plan_cum<EVEN>(plan, t + 1));
-        if (16 * quarter < plan_tile<EVEN>(plan, t).z)
+        const int end = min(x1, line.cum(t + 1));
+        if (16 * quarter < line.tile(t).z)
           for (int k = end - x + 3 - i - held; k > 0; --k) asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
         x = end;
       }

@@ -7,7 +7,7 @@ import torch
 
 import sparse_mla_decode_03_gb300 as m
 
-from _cache_helpers import (PageModel, ROW, SCALE, check_chunk, check_pages, dev, pack_rows, random_pool, tables)
+from _cache_helpers import (PageModel, ROW, SCALE, check_chunk, check_pages, chunk_reference, dev, pack_rows, random_pool, tables)
 from _rows4_helpers import ROW4, chunk_reference4, dequantize4, pack_rows4, random_pool4
 
 pytestmark = pytest.mark.gpu
@@ -411,3 +411,54 @@ def test_rows_past_32_bits_of_offset():
     got = m.sparse_mla_decode(q, pool, dev(idx), SCALE)
     want = m.sparse_mla_decode(q, last, dev(np.arange(64)[None].astype(np.int32)), SCALE)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("H,lens,ns", [
+    (64, [700 + 331 * i for i in range(32)], [1] * 32),
+    (16, [1 + 97 * i for i in range(32)], [1] * 32),
+    (128, [9000, 3, 64, 65, 0, 2000], [2, 3, 1, 2, 0, 3]),
+    (32, [40000], [5]),
+    (64, [0] * 32, [1] * 32),
+])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_an_empty_sequence_more_changes_no_bit(bits, H, lens, ns):
+    """The plan that each SM works out for up to 32 sequences and tiles is the one that a kernel makes for more."""
+    page = 64
+    num_pages = sum(-(-L // page) for L in lens) + 2
+    pool = (random_pool if bits == 8 else random_pool4)(num_pages, page, 5)
+    table = tables(lens, page, num_pages, 5)
+    T = sum(ns)
+    cu = np.concatenate([[0], np.cumsum(ns)]).astype(np.int32)
+    q = torch.randn(T, H, 512, generator=torch.Generator().manual_seed(T)).to(torch.bfloat16).cuda()
+    begin = torch.arange(T, dtype=torch.int32, device="cuda") * 13
+    end = torch.full((T,), 30000, dtype=torch.int32, device="cuda")
+    more = 33 - len(lens)
+    for kw in ({}, {"vis_begin": begin, "vis_end": end}):
+        few = m.smla_chunk_attention(q, pool, dev(table), page, dev(cu), dev(np.array(lens, np.int32)), softmax_scale=SCALE,
+                                     max_kv_tokens=sum(lens) + 1, **kw)
+        many = m.smla_chunk_attention(q, pool, dev(np.concatenate([table, np.full((more, table.shape[1]), -1, np.int32)])), page,
+                                      dev(np.concatenate([cu, np.full(more, T, np.int32)])),
+                                      dev(np.array(lens + [0] * more, np.int32)), softmax_scale=SCALE,
+                                     max_kv_tokens=sum(lens) + 1, **kw)
+        # One warp of the merge adds up a row's parts, or eight where 4 * (T H / 64 + sequences) is within the 152 SMs: six
+        # sequences of 11 tokens of 128 heads are, 33 of them are not.  The order of a sum then differs, the plan does not.
+        tiles = (T * H + 63) // 64
+        if (4 * (tiles + len(lens)) <= 152) == (4 * (tiles + 33) <= 152):
+            assert torch.equal(few[0].view(torch.int16), many[0].view(torch.int16))
+            assert torch.equal(few[1], many[1])
+        else:
+            masks = {"begin": kw["vis_begin"].cpu().numpy(), "end": kw["vis_end"].cpu().numpy()} if kw else {}
+            want = (chunk_reference4 if bits == 4 else chunk_reference)(q, pool, table, page, cu, np.array(lens), **masks)
+            check_chunk(few, want)
+            check_chunk(many, want)
+
+
+@pytest.mark.parametrize("cu", [[0, 3, 2, 5], [0, 2, 4, 9], [-1, 2, 4, 5]])
+def test_offsets_that_are_wrong_write_nothing(cu):
+    pool, table = random_pool4(9, 64, 2), tables([100, 100, 100], 64, 9, 2)
+    q = torch.randn(5, 64, 512).to(torch.bfloat16).cuda()
+    out, lse = torch.full((5, 64, 448), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((5, 64), 7.0, device="cuda")
+    m.smla_device_status(clear=True)
+    m.smla_chunk_attention(q, pool, dev(table), 64, dev(np.array(cu, np.int32)), dev(np.array([100] * 3, np.int32)), out=out, lse=lse)
+    assert m.smla_device_status(clear=True) == m._lib.SMLA_ERR_INDEX_RANGE
+    assert (out == 7).all() and (lse == 7).all()
