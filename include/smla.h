@@ -347,8 +347,9 @@ int smla_cache_append_rotary(const void* kv, int64_t kv_token_stride, int32_t to
 /*
  * Reads rows back: out bf16 [total_tokens, 512] (448 nope | 64 rope, out_token_stride elements apart,
  * >= 512, a multiple of 8; 16-byte aligned) receives the values that the rows of the same tokens hold,
- * rounded to bf16 (exact but for values past its range), addressed as smla_cache_append addresses them.  Tokens without a row
- * (SMLA_ERR_INDEX_RANGE) and entries outside [cu_q[0], cu_q[num_seqs]) are left as they were.
+ * rounded to bf16 (exact but for values past its range), addressed as smla_cache_append addresses them.
+ * Tokens without a row (SMLA_ERR_INDEX_RANGE) and entries outside [cu_q[0], cu_q[num_seqs]) are left as
+ * they were.
  */
 int smla_cache_read(const void* kv_pages, const int32_t* block_table, const int32_t* cu_q,
                     const int32_t* kv_lens, void* out, int64_t out_token_stride, int32_t total_tokens,
@@ -487,8 +488,8 @@ int smla_beam_select(const void* logits, const float* scores, const uint8_t* fin
  * (SMLA_ERR_INDEX_RANGE).  out and lse of entries outside [cu_q[0], cu_q[batch]) are left
  * as they were.
  *
- * A cached row with a NaN (a scale byte of 255 makes one), an infinite rope value or a nope value that times its scale passes
- * bf16's largest counts as not finite: tokens that see it get NaN in out and lse, all others
+ * A cached row with a NaN (a scale byte of 255 makes one), an infinite rope value or a nope value
+ * that times its scale passes bf16's largest counts as not finite: tokens that see it get NaN in out and lse, all others
  * are not touched by it.  The value sums are held in 32 bits before they are divided by the
  * weights', which go up to 2^8 each: cached values within a few powers of two of bf16's largest
  * may overflow them.  The attention weights are rounded to bf16 for the value product (and the
@@ -499,9 +500,9 @@ int smla_beam_select(const void* logits, const float* scores, const uint8_t* fin
  * more than 2^30 blocks to go through (64 positions times 64 or 256 query rows each: hours of
  * work; SMLA_ERR_UNSUPPORTED_SHAPE), the call writes no result and is reported.
  *
- * Two kernels.  From 256 query rows (tokens times heads) a sequence on average, pairs of SMs
- * work on 256 rows each over a bf16 copy of the cached rows, which the call makes in the
- * workspace (1,025 bytes a token of max_kv_tokens); below, single SMs work on 64 rows each and
+ * Two kernels.  From 256 query rows (tokens times heads) a sequence on average (over 4-bit rows:
+ * past 256), pairs of SMs work on 256 rows each over a bf16 copy of the cached rows, which the
+ * call makes in the workspace (1,025 bytes a token of max_kv_tokens); below, single SMs work on 64 rows each and
  * expand the rows themselves.  Either way the work is cut evenly over the GPU and partial
  * results are joined.  Calls whose kernels may overlap (two streams, two graphs) need a
  * workspace each; calls that follow one another in a stream may share one.  As with the

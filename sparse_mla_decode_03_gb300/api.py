@@ -715,9 +715,9 @@ def smla_chunk_workspace_size(params: _lib.SmlaChunkParams) -> int:
 
 
 @functools.lru_cache(maxsize=1024)
-def _chunk_bytes(batch: int, num_heads: int, total_q: int, max_kv_tokens: int) -> int:
-    """What smla_chunk_workspace_size says: a matter of these sizes alone."""
-    return smla_chunk_workspace_size(make_chunk_params(batch, num_heads, total_q, 1, 1, 1, ROW_BYTES, max_kv_tokens))
+def _chunk_bytes(batch: int, num_heads: int, total_q: int, row_bytes: int, max_kv_tokens: int) -> int:
+    """What smla_chunk_workspace_size says: a matter of these sizes and of the kind of rows alone."""
+    return smla_chunk_workspace_size(make_chunk_params(batch, num_heads, total_q, 1, 1, 1, row_bytes, max_kv_tokens))
 
 
 def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
@@ -769,7 +769,7 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
     p = make_chunk_params(B, H, T, page_size, max_pages, kv_pages.shape[0], _row_stride(kv_pages),
                           max_kv_tokens, softmax_scale, logit_cap)
     if workspace is None:
-        workspace = _empty(side, _chunk_bytes(B, H, T, max_kv_tokens), torch.uint8, dev)
+        workspace = _empty(side, _chunk_bytes(B, H, T, p.kv_row_stride, max_kv_tokens), torch.uint8, dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     with _on(dev):

@@ -94,7 +94,11 @@ __device__ __forceinline__ uint4 shfl_xor(const uint4& x, int mask) {
 }
 
 // A warp takes a token's row, or the rope columns of kHeads of its queries (8 lanes a head, 16 bytes a lane,
-// each of which a lane reads before it writes there, and no other lane: q_rope may be q's own columns).
+// each of which a lane reads before it writes there, and no other lane: q_rope may be q's own columns).  Bound by
+// memory: 16 heads a token are 2,048 bytes in and out beside the row's 1,608; 65,536 tokens take 62 us (374 MB, 6.0
+// TB/s, 89 % of the measured copy rate).  Products and sums in 32 bits, one rounding to bf16, so that a rotation by
+// nothing changes no bit.  A step's call (96 tokens of 64 heads) is a launch and three trips to memory (offsets,
+// lengths, then the table's row), 5 us.
 template <bool ROW4, bool NEIGHBOURS>
 __global__ void __launch_bounds__(256) append_rotary_kernel(const AppendArgs a, const RotaryArgs r) {
   __shared__ uint4 stage[8][38];
@@ -147,6 +151,8 @@ __global__ void __launch_bounds__(256) append_rotary_kernel(const AppendArgs a, 
 // ---------------------------------------------------------------------------
 // Reading back
 // ---------------------------------------------------------------------------
+// A token a warp, 368 or 584 bytes in and 1,024 out; the products are exact, but at the ends of bf16's
+// range.  10,005 tokens of 4-bit rows: 7.5 us (14 MB), a launch and three trips to memory.
 template <bool ROW4>
 __global__ void __launch_bounds__(256) read_kernel(const AppendArgs a, uint4* out, int64_t out_units) {
   grid_dep_wait();

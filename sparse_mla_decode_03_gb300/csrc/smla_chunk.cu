@@ -460,9 +460,13 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // Which kernel: pairs once a sequence brings a full tile of 256 rows on average.  Single against
 // pairs, 16 sequences of 16,000 and 64 heads: 1 token 90 and 184 us, 2 tokens 126 and 161, 4
 // tokens 214 and 160; 16 tokens of 16 heads over 8,000 93 and 88; 1 token of 128 heads 60 and 70.
+// Over 4-bit rows, which cost the single kernel less, from more than a full tile: of 64 heads, 4 x 4 tokens of 1,001
+// 24.7 and 26.8, 16 x 4 of 16,000 183 and 199, 32 x 4 of 500 39.1 and 34.8; 4 x 5 of 1,001 30.8 and 28.7, 3 x 5 of
+// 19,717 70 and 81, 8 x 8 of 4,000 67 and 60; 16 x 16 of 16 heads and 8,000 106 and 116.
 // All of batches whose sequences bring the same number of tokens; mixed ones are not measured.
 bool use_pairs(const smla_chunk_params* p) {
-  return static_cast<int64_t>(p->total_q) * p->num_heads >= static_cast<int64_t>(kPairRows) * p->batch;
+  const int64_t rows = static_cast<int64_t>(p->total_q) * p->num_heads, full = static_cast<int64_t>(kPairRows) * p->batch;
+  return is_row4(p->kv_row_stride) ? rows > full : rows >= full;
 }
 
 // The workspace of a call; base may be null to size it.

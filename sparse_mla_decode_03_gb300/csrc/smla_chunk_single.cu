@@ -7,29 +7,30 @@
 // 512 a block of 64 positions), O += P V (64 x 448 x 64), K and V from one expanded block in
 // shared memory.
 //
-// What bounds it: the chain that each block goes through, not one unit.  64 positions are 37 KB
-// of the cache, 1,630 cycles at the copy rate with all SMs reading.  The products take 2,350
-// (32 of 64 x 64 x 16 at their measured minimum of 45 cycles; the value product runs at half
-// of the tensor rate with 64 rows: 900), the expansion about 1,600 of the integer pipe, the
-// softmax about 800.  Expansion, scores, softmax and value product of a block follow one
-// another, and the scores and O fill tensor memory, so two blocks in two buffers overlap in
-// part only: about 5,100 cycles a block.  32 single tokens of 64 heads over 8,192 positions
-// take 77 us (153 MB: 2.0 TB/s, 29 % of the copy rate; tensor pipe 40 % busy, integer pipe
-// 53 %), with plan and merge 87 us; two tokens of 16 heads over 131,072 take 69 and 79 us.
-// Measured and not kept: f16 operands (96 us against 93 then), two sets of 8 expanding warps
-// (93..105), the next block's rows read before this one's expansion (110: spills), through
+// What bounds it: the chain that each block goes through, not one unit.  64 positions of 8-bit rows are 37 KB of
+// the cache, 1,630 cycles at the copy rate with all SMs reading (24 KB and 1,030 of 4-bit rows).  The products take
+// 2,000 (32 of 64 x 64 x 16 by way of tensor memory 1,060, the value product 940: 64 rows run at half the tensor
+// rate), the expansion about 1,600 of the integer pipe (700 of 4-bit rows), the softmax about 800.  Expansion,
+// scores, softmax and value product of a block follow one another, 4,500 cycles alone, so three blocks are on their
+// way: the scores of one beside the expansion of the next and the value product of the one before.  32 single tokens
+// of 64 heads over 8,192 positions take 75 us of 8-bit rows (153 MB: 2.0 TB/s, 30 % of the copy rate) and 54 of 4-bit
+// rows (tensor pipe 37 % of the time, issue slots 52 %, integer pipe 42 % of the active cycles).
+// Measured and not kept, two blocks and Q in shared memory: f16 operands (96 us against 93 then), two sets of 8
+// expanding warps (93..105), the next block's rows read before this one's expansion (110: spills), through
 // shared memory (92 against 85: past the carve-out step) or half a row earlier (87), one lane
-// polling for its warp (107).
+// polling for its warp (107).  4-bit rows, three blocks: a block more on its way to registers 65 against 62, one proxy
+// fence a block 59 against 57.5, a ring of 5 half blocks past the carve-out step 68 against 64.
 //
 // Expansion without conversions: an e4m3 byte's exponent and mantissa, shifted into bf16's
 // fields, are its value times 2^-120 (subnormals included), and one bf16 product by
 // 2^(scale byte - 7) puts both powers right, exactly.  The shifts act on four bytes at
 // once: the integer pipe is the expansion's bound.  Rows with NaN or with scale bytes past
-// 134 take a slower path.
+// 134 take a slower path.  4-bit rows the same way (expand_nibbles); any scale byte, in two products where one
+// power of two is not enough.
 //
-// Warps of a CTA: 0..7 softmax and results (64 rows lie in 16 tensor-memory lanes of each
+// Warps of a CTA: 0..7 softmax, Q and results (64 rows lie in 16 tensor-memory lanes of each
 // quarter, which two warps share by columns), 8..23 expand, 24 issues the scores, 25 the
-// value products, 26 loads Q.  Every wait is bounded.
+// value products, 26 makes the plan of few tiles.  Every wait is bounded.
 #include <mutex>
 #include <type_traits>
 
@@ -680,19 +681,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           d.w[5] = ldg16_once(src + (lane < 24 ? 320 : 304));
           return have;
         } else {
-        const uint8_t* base = a.pool + 8 * lane;
+          const uint8_t* base = a.pool + 8 * lane;
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-          const uint8_t* src = base + static_cast<uint64_t>(__shfl_sync(0xffffffffu, row_now, j)) * stride;
-          d.a[j] = ldg_once(src);
-          d.b[j] = ldg_once(src + 256);
-        }
+          for (int j = 0; j < kRows; ++j) {
+            const uint8_t* src = base + static_cast<uint64_t>(__shfl_sync(0xffffffffu, row_now, j)) * stride;
+            d.a[j] = ldg_once(src);
+            d.b[j] = ldg_once(src + 256);
+          }
 #pragma unroll
-        for (int k = 0; k < kTails; ++k) {
-          const int j = min(3 * k + c_row, kRows - 1);        // lanes with no such row: any
-          d.c[k] = ldg_once(a.pool + static_cast<uint64_t>(__shfl_sync(0xffffffffu, row_now, j)) * stride + 512 + 8 * c_word);
-        }
-        return have;
+          for (int k = 0; k < kTails; ++k) {
+            const int j = min(3 * k + c_row, kRows - 1);        // lanes with no such row: any
+            d.c[k] = ldg_once(a.pool + static_cast<uint64_t>(__shfl_sync(0xffffffffu, row_now, j)) * stride + 512 + 8 * c_word);
+          }
+          return have;
         }
       };
       Cursor at;                     // the block whose page ids are fetched next
@@ -790,135 +791,135 @@ __global__ void __launch_bounds__(kThreads, 1)
           off = at.off;
         }
       } else {
-      // word b of this lane: nope, scales (lane 24) or rope; how its NaN are found
-      const uint32_t mb = lane < 24 ? 0x7f7f7f7fu : lane > 24 ? 0x7f807f80u : 0u;
-      const uint32_t ab = lane < 24 ? 0x01010101u : 0x00800080u;
-      const uint32_t tb = lane < 24 ? 0x80808080u : 0x80008000u;
-      const int sh = 8 * (lane >> 3);
-      const uint32_t pick = 0x4040u + 0x0101u * static_cast<uint32_t>(lane >> 3);   // (byte, 0, byte, 0)
-      const uint32_t pick_b = lane < 24 ? pick : 0x4444u;
-      const uint32_t dst_nope = sbase + (lane >> 3) * kSlab;
-      Place place;
-      int turn = 0;                  // of the masks' three
-      for (int n = 0; n < count; ++n) {
-        // 2^(s - 7) as two bf16 of this lane's groups (s: their scale bytes) of each row; lanes
-        // 24 .. 31 have no second group
-        auto power = [](uint32_t twice) { return twice * 128u + 0x3c003c00u; };
-        uint32_t ma[kRows], mx[kRows];
-        // anything that the fast path does not cover: NaN, infinite rope values, scale bytes
-        // past 134
-        uint32_t na = 0, nb = 0, nc = 0, top = 0;
+        // word b of this lane: nope, scales (lane 24) or rope; how its NaN are found
+        const uint32_t mb = lane < 24 ? 0x7f7f7f7fu : lane > 24 ? 0x7f807f80u : 0u;
+        const uint32_t ab = lane < 24 ? 0x01010101u : 0x00800080u;
+        const uint32_t tb = lane < 24 ? 0x80808080u : 0x80008000u;
+        const int sh = 8 * (lane >> 3);
+        const uint32_t pick = 0x4040u + 0x0101u * static_cast<uint32_t>(lane >> 3);   // (byte, 0, byte, 0)
+        const uint32_t pick_b = lane < 24 ? pick : 0x4444u;
+        const uint32_t dst_nope = sbase + (lane >> 3) * kSlab;
+        Place place;
+        int turn = 0;                  // of the masks' three
+        for (int n = 0; n < count; ++n) {
+          // 2^(s - 7) as two bf16 of this lane's groups (s: their scale bytes) of each row; lanes
+          // 24 .. 31 have no second group
+          auto power = [](uint32_t twice) { return twice * 128u + 0x3c003c00u; };
+          uint32_t ma[kRows], mx[kRows];
+          // anything that the fast path does not cover: NaN, infinite rope values, scale bytes
+          // past 134
+          uint32_t na = 0, nb = 0, nc = 0, top = 0;
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-          na |= nan_bits(d.a[j].x) | nan_bits(d.a[j].y);
-          nb |= ((d.b[j].x & mb) + ab) | ((d.b[j].y & mb) + ab);
-          const uint32_t sa = prmt(__shfl_sync(0xffffffffu, d.b[j].x, 24), 0, pick);
-          const uint32_t sb = prmt(__shfl_sync(0xffffffffu, d.b[j].y, 24), 0, pick_b);
-          top = max(top, max(sa, sb));
-          ma[j] = power(sa);
-          mx[j] = power(sb);
-        }
-#pragma unroll
-        for (int k = 0; k < kTails; ++k) nc |= rope_bits(d.c[k].x) | rope_bits(d.c[k].y);
-        const bool odd = (na & 0x80808080u) | (nb & tb) | (nc & 0x80008000u) | (top > 0x00860086u ? 1u : 0u);
-        const bool usual = !__any_sync(0xffffffffu, odd);
-        uint32_t dropped = 0;        // rows that are not finite: held as zeros
-        // The unusual path reads its rows again, one by one: kept in registers for it, they
-        // would make the usual path spill.
-        auto again = [&](int j, int byte) {      // 8 bytes of row j
-          return ldg_once(a.pool + static_cast<uint64_t>(__shfl_sync(0xffffffffu, row_now, j)) * stride + byte);
-        };
-        if (!usual) {
-#pragma unroll 1
           for (int j = 0; j < kRows; ++j) {
-            const uint2 wa = again(j, 8 * lane), wb = again(j, 256 + 8 * lane), wc = again(j, 512 + 8 * min(lane, 8));
-            const uint32_t sx = __shfl_sync(0xffffffffu, wb.x, 24), sy = __shfl_sync(0xffffffffu, wb.y, 24);
-            // a NaN (a scale byte of 255 makes NaN), or past bf16's largest value: seen in the results
-            const uint4 oa = expand8_any(wa, (sx >> sh) & 0xffu);
-            const uint4 ob = lane < 24 ? expand8_any(wb, (sy >> sh) & 0xffu)
-                                       : lane > 24 ? make_uint4(wb.x, wb.y, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t bad = rope_bits(oa.x) | rope_bits(oa.y) | rope_bits(oa.z) | rope_bits(oa.w) | rope_bits(ob.x) |
-                                 rope_bits(ob.y) | rope_bits(ob.z) | rope_bits(ob.w) | rope_bits(wc.x) | rope_bits(wc.y);
-            dropped |= __any_sync(0xffffffffu, (bad & 0x80008000u) != 0) ? 1u << j : 0u;
+            na |= nan_bits(d.a[j].x) | nan_bits(d.a[j].y);
+            nb |= ((d.b[j].x & mb) + ab) | ((d.b[j].y & mb) + ab);
+            const uint32_t sa = prmt(__shfl_sync(0xffffffffu, d.b[j].x, 24), 0, pick);
+            const uint32_t sb = prmt(__shfl_sync(0xffffffffu, d.b[j].y, 24), 0, pick_b);
+            top = max(top, max(sa, sb));
+            ma[j] = power(sa);
+            mx[j] = power(sb);
           }
-        }
-        if (n >= 3) ok = warp_wait(bar(EMPTY + place.at), place.phase ^ 1, stop, a.status);
-        if (!ok) break;
-        uint32_t dn = dst_nope + kRows * w16 * 128 + place.at * kHalf;
-        const int r7 = (kRows * w16) & 7;                 // the warp's first row modulo 8
-        auto unit = [&](int j) { return j * 128 + (((lane & 7) ^ (r7 + j)) << 4); };    // the lane's unit of row j
-        if (usual) {
-          // two rows at a time, their conversions interleaved; times 2^(s - 7) as two bf16
 #pragma unroll
-          for (int j0 = 0; j0 < kRows; j0 += 2) {
-            uint4 o[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              o[j] = expand8(d.a[j0 + j], ma[j0 + j]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) sts(dn + unit(j0 + j), o[j]);
-          }
-        } else {
+          for (int k = 0; k < kTails; ++k) nc |= rope_bits(d.c[k].x) | rope_bits(d.c[k].y);
+          const bool odd = (na & 0x80808080u) | (nb & tb) | (nc & 0x80008000u) | (top > 0x00860086u ? 1u : 0u);
+          const bool usual = !__any_sync(0xffffffffu, odd);
+          uint32_t dropped = 0;        // rows that are not finite: held as zeros
+          // The unusual path reads its rows again, one by one: kept in registers for it, they
+          // would make the usual path spill.
+          auto again = [&](int j, int byte) {      // 8 bytes of row j
+            return ldg_once(a.pool + static_cast<uint64_t>(__shfl_sync(0xffffffffu, row_now, j)) * stride + byte);
+          };
+          if (!usual) {
 #pragma unroll 1
-          for (int j = 0; j < kRows; ++j) {
-            const uint2 wa = again(j, 8 * lane);
-            const uint32_t s = (again(j, kNope).x >> sh) & 0xffu;
-            sts(dn + unit(j), (dropped >> j) & 1 ? make_uint4(0u, 0u, 0u, 0u) : expand8_any(wa, s));
-          }
-        }
-        if (lane == 0) {
-          masks[turn * 32 + w16] = static_cast<uint8_t>(have);
-          masks[turn * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && !(n == a.fault_block && w16 == 0)) mbar_arrive(bar(FULL + place.at));
-        place.next();
-        if (n >= 3) ok = warp_wait(bar(EMPTY + place.at), place.phase ^ 1, stop, a.status);
-        if (!ok) break;
-        dn = dst_nope + kRows * w16 * 128 + place.at * kHalf;
-        // the rope: word w of row j
-        const uint32_t dr = sbase + 3 * kSlab + kRows * w16 * 128 + place.at * kHalf;
-        auto rope = [&](int j, int w) { return dr + j * 128 + (((w >> 1) ^ (r7 + j)) << 4) + 8 * (w & 1); };
-        if (usual) {
-#pragma unroll
-          for (int j0 = 0; j0 < kRows; j0 += 2) {
-            uint4 o[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              o[j] = expand8(d.b[j0 + j], mx[j0 + j]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              sts_if(lane < 24, dn + unit(j0 + j), o[j]);
-              sts8_if(lane > 24, rope(j0 + j, (lane - 25) & 15), d.b[j0 + j]);
+            for (int j = 0; j < kRows; ++j) {
+              const uint2 wa = again(j, 8 * lane), wb = again(j, 256 + 8 * lane), wc = again(j, 512 + 8 * min(lane, 8));
+              const uint32_t sx = __shfl_sync(0xffffffffu, wb.x, 24), sy = __shfl_sync(0xffffffffu, wb.y, 24);
+              // a NaN (a scale byte of 255 makes NaN), or past bf16's largest value: seen in the results
+              const uint4 oa = expand8_any(wa, (sx >> sh) & 0xffu);
+              const uint4 ob = lane < 24 ? expand8_any(wb, (sy >> sh) & 0xffu)
+                                         : lane > 24 ? make_uint4(wb.x, wb.y, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t bad = rope_bits(oa.x) | rope_bits(oa.y) | rope_bits(oa.z) | rope_bits(oa.w) | rope_bits(ob.x) |
+                                   rope_bits(ob.y) | rope_bits(ob.z) | rope_bits(ob.w) | rope_bits(wc.x) | rope_bits(wc.y);
+              dropped |= __any_sync(0xffffffffu, (bad & 0x80008000u) != 0) ? 1u << j : 0u;
             }
           }
-        } else {
-#pragma unroll 1
-          for (int j = 0; j < kRows; ++j) {
-            const uint2 wb = again(j, 256 + 8 * lane);
-            const uint32_t s = (again(j, kNope).y >> sh) & 0xffu;
-            const bool drop = (dropped >> j) & 1;
-            sts_if(lane < 24, dn + unit(j), drop ? make_uint4(0u, 0u, 0u, 0u) : expand8_any(wb, s));
-            sts8_if(lane > 24, rope(j, (lane - 25) & 15), drop ? make_uint2(0u, 0u) : wb);
-          }
-        }
+          if (n >= 3) ok = warp_wait(bar(EMPTY + place.at), place.phase ^ 1, stop, a.status);
+          if (!ok) break;
+          uint32_t dn = dst_nope + kRows * w16 * 128 + place.at * kHalf;
+          const int r7 = (kRows * w16) & 7;                 // the warp's first row modulo 8
+          auto unit = [&](int j) { return j * 128 + (((lane & 7) ^ (r7 + j)) << 4); };    // the lane's unit of row j
+          if (usual) {
+            // two rows at a time, their conversions interleaved; times 2^(s - 7) as two bf16
 #pragma unroll
-        for (int k = 0; k < kTails; ++k) {
-          const int j = 3 * k + c_row;
-          sts8_if(j < kRows && lane < 27, rope(j & (kRows - 1), 7 + c_word), (dropped >> j) & 1 ? make_uint2(0u, 0u) : d.c[k]);
+            for (int j0 = 0; j0 < kRows; j0 += 2) {
+              uint4 o[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                o[j] = expand8(d.a[j0 + j], ma[j0 + j]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) sts(dn + unit(j0 + j), o[j]);
+            }
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < kRows; ++j) {
+              const uint2 wa = again(j, 8 * lane);
+              const uint32_t s = (again(j, kNope).x >> sh) & 0xffu;
+              sts(dn + unit(j), (dropped >> j) & 1 ? make_uint4(0u, 0u, 0u, 0u) : expand8_any(wa, s));
+            }
+          }
+          if (lane == 0) {
+            masks[turn * 32 + w16] = static_cast<uint8_t>(have);
+            masks[turn * 32 + 16 + w16] = static_cast<uint8_t>(dropped);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && !(n == a.fault_block && w16 == 0)) mbar_arrive(bar(FULL + place.at));
+          place.next();
+          if (n >= 3) ok = warp_wait(bar(EMPTY + place.at), place.phase ^ 1, stop, a.status);
+          if (!ok) break;
+          dn = dst_nope + kRows * w16 * 128 + place.at * kHalf;
+          // the rope: word w of row j
+          const uint32_t dr = sbase + 3 * kSlab + kRows * w16 * 128 + place.at * kHalf;
+          auto rope = [&](int j, int w) { return dr + j * 128 + (((w >> 1) ^ (r7 + j)) << 4) + 8 * (w & 1); };
+          if (usual) {
+#pragma unroll
+            for (int j0 = 0; j0 < kRows; j0 += 2) {
+              uint4 o[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                o[j] = expand8(d.b[j0 + j], mx[j0 + j]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                sts_if(lane < 24, dn + unit(j0 + j), o[j]);
+                sts8_if(lane > 24, rope(j0 + j, (lane - 25) & 15), d.b[j0 + j]);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < kRows; ++j) {
+              const uint2 wb = again(j, 256 + 8 * lane);
+              const uint32_t s = (again(j, kNope).y >> sh) & 0xffu;
+              const bool drop = (dropped >> j) & 1;
+              sts_if(lane < 24, dn + unit(j), drop ? make_uint4(0u, 0u, 0u, 0u) : expand8_any(wb, s));
+              sts8_if(lane > 24, rope(j, (lane - 25) & 15), drop ? make_uint2(0u, 0u) : wb);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kTails; ++k) {
+            const int j = 3 * k + c_row;
+            sts8_if(j < kRows && lane < 27, rope(j & (kRows - 1), 7 + c_word), (dropped >> j) & 1 ? make_uint2(0u, 0u) : d.c[k]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(FULL + place.at));
+          place.next();
+          turn = turn + 1 == kMasks ? 0 : turn + 1;
+          // the next block's bytes, and the page ids of the one after it
+          have = fetch(id, off, d);
+          at.step(line, mine, a.page_size, pages_step, rest);
+          id = lookup(at);
+          off = at.off;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(FULL + place.at));
-        place.next();
-        turn = turn + 1 == kMasks ? 0 : turn + 1;
-        // the next block's bytes, and the page ids of the one after it
-        have = fetch(id, off, d);
-        at.step(line, mine, a.page_size, pages_step, rest);
-        id = lookup(at);
-        off = at.off;
-      }
       }
     }
   } else if (warp >= kMmaWarp) {

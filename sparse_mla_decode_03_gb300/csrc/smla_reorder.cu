@@ -85,7 +85,8 @@ __device__ __forceinline__ int2 block_rank2(int2 v, int2* total, int2* warps) {
 constexpr int kOwnRows = 8192;
 
 // Bound by latency: a launch, four trips to memory one after the other (parents, lengths, table; counts) and three
-// cluster barriers.
+// cluster barriers: 10.5 us for 8 rows and 8,192 pages, 12 for 512 rows and 32,768 (19 when the lowest children went
+// through the workspace there too).
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
     reorder_plan_kernel(const ReorderArgs a) {
   __shared__ PlanShared sh;
@@ -170,7 +171,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 
 constexpr int kCopyRows = 16;   // rows of a partial page that one CTA copies
 
-// Grid (rows, row groups of a page): group 0 also writes the row of the table.
+// Grid (rows, row groups of a page): group 0 also writes the row of the table.  A launch, two trips to memory and the
+// copies: 4.6 us for 8 rows, 7 for 512 of which half copy 56 rows.
 __global__ void __launch_bounds__(256) reorder_apply_kernel(const ReorderArgs a) {
   grid_dep_wait();
   grid_dep_launch();
