@@ -11,10 +11,10 @@
 // the cache, 1,630 cycles at the copy rate with all SMs reading (24 KB and 1,030 of 4-bit rows).  The products take
 // 2,000 (32 of 64 x 64 x 16 by way of tensor memory 1,060, the value product 940: 64 rows run at half the tensor
 // rate), the expansion about 1,600 of the integer pipe (700 of 4-bit rows), the softmax about 800.  Expansion,
-// scores, softmax and value product of a block follow one another, 4,500 cycles alone, so three blocks are on their
-// way: the scores of one beside the expansion of the next and the value product of the one before.  32 single tokens
-// of 64 heads over 8,192 positions take 75 us of 8-bit rows (153 MB: 2.0 TB/s, 30 % of the copy rate) and 54 of 4-bit
-// rows (tensor pipe 37 % of the time, issue slots 52 %, integer pipe 42 % of the active cycles).
+// scores, softmax and value product of a block follow one another, so three blocks are on their way: the scores of
+// one beside the expansion of the next and the value product of the one before.  32 single tokens
+// of 64 heads over 8,192 positions take 75 us of 8-bit rows (153 MB: 2.0 TB/s, 30 % of the copy rate; 5,300 cycles a block) and 54 of 4-bit
+// rows (3,800; tensor pipe 37 % of the time, issue slots 52 %, integer pipe 42 % of the active cycles).
 // Measured and not kept, two blocks and Q in shared memory: f16 operands (96 us against 93 then), two sets of 8
 // expanding warps (93..105), the next block's rows read before this one's expansion (110: spills), through
 // shared memory (92 against 85: past the carve-out step) or half a row earlier (87), one lane
