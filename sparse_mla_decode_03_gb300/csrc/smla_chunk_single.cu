@@ -5,21 +5,24 @@
 // Tiles of 64 (token, head) rows; shares of the block line (see smla_chunk.h) spread a
 // long context over all SMs.  A CTA expands the packed rows itself: S = Q K^T (64 x 64 x
 // 512 a block of 64 positions), O += P V (64 x 448 x 64), K and V from one expanded block in
-// shared memory.
+// shared memory, Q and P from tensor memory.
 //
 // What bounds it: the chain that each block goes through, not one unit.  64 positions of 8-bit rows are 37 KB of
 // the cache, 1,630 cycles at the copy rate with all SMs reading (24 KB and 1,030 of 4-bit rows).  The products take
 // 2,000 (32 of 64 x 64 x 16 by way of tensor memory 1,060, the value product 940: 64 rows run at half the tensor
 // rate), the expansion about 1,600 of the integer pipe (700 of 4-bit rows), the softmax about 800.  Expansion,
 // scores, softmax and value product of a block follow one another, so three blocks are on their way: the scores of
-// one beside the expansion of the next and the value product of the one before.  32 single tokens
-// of 64 heads over 8,192 positions take 75 us of 8-bit rows (153 MB: 2.0 TB/s, 30 % of the copy rate; 5,300 cycles a block) and 54 of 4-bit
-// rows (3,800; tensor pipe 37 % of the time, issue slots 52 %, integer pipe 42 % of the active cycles).
+// one beside the expansion of the next and the value product of the one before.  From the release of a block's places
+// to that of the same places again are 8,900 cycles: expansion 2,700, scores 2,200 beside the other products, softmax
+// 2,100 beside the expanding warps, value product.  32 single tokens of 64 heads over 8,192 positions take 74 us of
+// 8-bit rows (153 MB: 2.1 TB/s, 30 % of the copy rate) and 52 of 4-bit rows (tensor pipe 37 % of the time, issue
+// slots 52 %, integer pipe 42 % of the active cycles).
 // Measured and not kept, two blocks and Q in shared memory: f16 operands (96 us against 93 then), two sets of 8
 // expanding warps (93..105), the next block's rows read before this one's expansion (110: spills), through
 // shared memory (92 against 85: past the carve-out step) or half a row earlier (87), one lane
 // polling for its warp (107).  4-bit rows, three blocks: a block more on its way to registers 65 against 62, one proxy
-// fence a block 59 against 57.5, a ring of 5 half blocks past the carve-out step 68 against 64.
+// fence a block 59 against 57.5, a ring of 7 half blocks past the carve-out step 66 against 55, a set of expanding
+// warps for each half of a block 57 against 55.
 //
 // Expansion without conversions: an e4m3 byte's exponent and mantissa, shifted into bf16's
 // fields, are its value times 2^-120 (subnormals included), and one bf16 product by
@@ -64,9 +67,6 @@ constexpr int kHalf = 4 * kSlab;           // columns 0..255 or 256..511 of an e
 // expansion, scores and value product need not wait for one another's ends.  With Q in tensor memory the CTA
 // stays below the 196 KB step of the shared-memory carve-out, which leaves the loads 60 KB of L1, not 28.
 constexpr int kPlaces = 6;
-// P of a block takes the place of its rope, the last slab of its second half, which the scores are done
-// with; the place is filled again only after the value product.
-constexpr int kPOff = 3 * kSlab;
 constexpr int kBarOff = kPlaces * kHalf;
 constexpr int kMasks = 3;                  // blocks whose masks are held: a block is expanded again only after its weights
 constexpr int kMaskOff = kBarOff + 192;    // [3 blocks][mapped, not finite][16 half bytes]
@@ -79,17 +79,19 @@ static_assert(kSmem <= 195 * 1024, "the carve-out step, less what the system tak
 
 // Tensor memory.  64 rows of a product lie in 16 lanes of each quarter, the lower ones or the upper, so
 // that 512 columns hold twice as much.  Lower: Q (two bf16 a column), the scores of two blocks, columns 384..447 of
-// O.  Upper: columns 0..383 of O.  (Q as a product's first operand lies in the lanes of its result.)
-constexpr uint32_t kColS = 256, kColTail = 384, kUpper = 16u << 16;
+// O, the weights of two blocks (two bf16 a column).  Upper: columns 0..383 of O, and the weights once more.  (A
+// product's first operand lies in the lanes of its result.)  Weights by way of shared memory, with its fence, took
+// 54.8 us against 53.0 (32 single tokens, 4-bit rows; 79.4 and 78.4 of 8-bit rows).
+constexpr uint32_t kColS = 256, kColTail = 384, kColP = 448, kUpper = 16u << 16;
 __device__ __forceinline__ uint32_t o_column(uint32_t tmem, int c) {
   return tmem + static_cast<uint32_t>(c) + (c < static_cast<int>(kColTail) ? kUpper : 0u);
 }
 
-// FULL / EMPTY: a place of the ring filled / its value product done; PFULL: weights written (one for each block of
-// the ring: a quarter may be two blocks ahead of another, and no more, since a third one's place waits for the
-// value product that the other holds up); QFULL: a tile's Q in tensor memory; SFULL /
+// FULL / EMPTY: a place of the ring filled / its value product done; PFULL: weights in tensor memory, two blocks in
+// turn (a quarter may be a block ahead of another, and no more, since the third one's weights wait for the value
+// product that the other holds up); QFULL: a tile's Q in tensor memory; SFULL /
 // SEMPTY: scores of a block in tensor memory / taken by the softmax, two in turn; OEMPTY: results taken.
-enum Bar : int { FULL = 0, EMPTY = kPlaces, PFULL = 2 * kPlaces, QFULL = PFULL + kPlaces / 2, SFULL, SEMPTY = SFULL + 2, OEMPTY = SEMPTY + 2, kBars };
+enum Bar : int { FULL = 0, EMPTY = kPlaces, PFULL = 2 * kPlaces, QFULL = PFULL + 2, SFULL, SEMPTY = SFULL + 2, OEMPTY = SEMPTY + 2, kBars };
 
 // A place of the ring, and the parity of its uses.
 struct Place {
@@ -235,6 +237,12 @@ __device__ __forceinline__ void sts(uint32_t addr, uint4 v) {
 }
 __device__ __forceinline__ void sts4(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// The store of 16 lanes x 16 columns: lane 4 g + q of the warp gives columns 4 j + q of lanes g (v[2 j]) and g + 8.
+__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 // Predicated forms, so that lanes with and without a word do not part ways.
 __device__ __forceinline__ void sts_if(bool p, uint32_t addr, uint4 v) {
@@ -585,10 +593,6 @@ __device__ __forceinline__ void plan_few(const ChunkArgs& a, const ChunkPlan& p,
   if (lane == 0) p.head[2] = __popc(cuts);
 }
 
-__device__ __noinline__ void plan_few_apart(const ChunkArgs& a, const ChunkPlan& p, uint32_t smem, int worker) {
-  plan_few(a, p, smem, worker);
-}
-
 template <bool MODS, bool ROW4>
 __global__ void __launch_bounds__(kThreads, 1)
     single_kernel(const ChunkArgs a, const ChunkPlan plan) {
@@ -623,10 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool EVEN = ROW4 && !MODS;     // may be a sparse call
   const Plan<EVEN> line = {a, plan, sbase};
   if (line.few()) {
-    if (warp == kPlanWarp) {      // out of line where the other roles would spill
-      if constexpr (EVEN) plan_few_apart(a, plan, sbase, worker);
-      else plan_few(a, plan, sbase, worker);
-    }
+    if (warp == kPlanWarp) plan_few(a, plan, sbase, worker);
     __syncthreads();
   }
   const int x0 = line.begin(worker), x1 = line.end(worker), t_first = line.start(worker, x0);
@@ -965,33 +966,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- value products ----------------
       constexpr uint32_t kId256 = idesc_bf16(64, 256, false, true), kId128 = idesc_bf16(64, 128, false, true),
                          kId64 = idesc_bf16(64, 64, false, true);
-      const uint32_t lp = static_cast<uint32_t>(d0) + (kPOff >> 4), lv = static_cast<uint32_t>(dv);
-      uint32_t k = 0;                      // tiles so far
+      const uint32_t lv = static_cast<uint32_t>(dv);
+      uint32_t n = 0, k = 0;               // blocks and tiles so far
       Place place;
       bool ok = true;
       for (int x = x0, t = t_first; ok && x < x1; ++t, ++k) {
         const int end = min(x1, line.cum(t + 1));
         uint32_t old = 0;                  // the tile's first product overwrites O
-        for (; ok && x < end; ++x, old = 1) {
-          ok = warp_wait(bar(PFULL + (place.at >> 1)), place.phase, stop, a.status);
+        for (; ok && x < end; ++x, ++n, old = 1) {
+          ok = warp_wait(bar(PFULL + (n & 1)), (n >> 1) & 1, stop, a.status);
           if (ok && old == 0 && k > 0) ok = warp_wait(bar(OEMPTY), (k - 1) & 1, stop, a.status);
           if (!ok) break;
           tc_fence_after();
           const uint32_t first = place.at;
           place.next();
-          const uint32_t l0 = lv + first * (kHalf >> 4), l1 = lv + place.at * (kHalf >> 4), lw = lp + place.at * (kHalf >> 4);
+          const uint32_t l0 = lv + first * (kHalf >> 4), l1 = lv + place.at * (kHalf >> 4);
+          const uint32_t tail = tmem + kColP + 32 * (n & 1), p = tail + kUpper;
           if (elect_one()) {
             // columns 0..255 first: their place may be filled again while 256..447 follow
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_f16_ss_hl(o_column(tmem, 0), lw + ((i * 32) >> 4), hi, l0 + ((i * 2048) >> 4), hi, kId256, i > 0 ? 1u : old);
+              mma_f16_ts_hl(o_column(tmem, 0), p + 8 * i, l0 + ((i * 2048) >> 4), hi, kId256, i > 0 ? 1u : old);
             mma_commit(bar(EMPTY + first));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_f16_ss_hl(o_column(tmem, 256), lw + ((i * 32) >> 4), hi, l1 + ((i * 2048) >> 4), hi, kId128, i > 0 ? 1u : old);
+              mma_f16_ts_hl(o_column(tmem, 256), p + 8 * i, l1 + ((i * 2048) >> 4), hi, kId128, i > 0 ? 1u : old);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_f16_ss_hl(o_column(tmem, kColTail), lw + ((i * 32) >> 4), hi, l1 + ((2 * kSlab + i * 2048) >> 4), hi, kId64,
+              mma_f16_ts_hl(o_column(tmem, kColTail), tail + 8 * i, l1 + ((2 * kSlab + i * 2048) >> 4), hi, kId64,
                             i > 0 ? 1u : old);
             mma_commit(bar(EMPTY + place.at));
           }
@@ -1018,8 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(QFULL));
     };
-    // P: rows 16 quarter + g and + 8 (the same row modulo 8), columns 2 (lane % 4) .. of unit j
-    const uint32_t p0 = sbase + kPOff + (16 * quarter + g) * 128 + 4 * (lane & 3), p1 = p0 + 8 * 128;
+    const uint32_t tP = tmem + kColP + 16 * half + lanes;
     uint32_t n = 0;
     int x = x0, t = t_first, i = 0, held = 0;
     bool ok = true;
@@ -1045,12 +1046,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__any_sync(0xffffffffu, (m0 & m1) != 0x0f0f0f0f0f0f0f0full || (d0 | d1) != 0))
             rows = make_ulonglong2(halves(m0, m1), halves(d0, d1));
         }
-        ok = warp_wait(bar(SFULL + (n & 1)), (n >> 1) & 1, stop, a.status);
+        // the value product before the last is done with its weights, in whose place this block's will be
+        if (n >= 2) ok = warp_wait(bar(EMPTY + Place::of(2 * n - 3).at), Place::of(2 * n - 3).phase, stop, a.status);
+        if (ok) ok = warp_wait(bar(SFULL + (n & 1)), (n >> 1) & 1, stop, a.status);
         if (!ok) break;
         if (idle) {
           if (lane == 0) {
             mbar_arrive(bar(SEMPTY + (n & 1)));
-            mbar_arrive(bar(PFULL + (Place::of(2 * n).at >> 1)));
+            mbar_arrive(bar(PFULL + (n & 1)));
           }
           continue;
         }
@@ -1074,16 +1077,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           rescale_half(tO, alpha[0], alpha[1], half);
         }
-        const uint32_t pb = Place::of(2 * n + 1).at * kHalf;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sts4(p0 + pb + (((j + 4 * half) ^ g) << 4), p[2 * j]);
-          sts4(p1 + pb + (((j + 4 * half) ^ g) << 4), p[2 * j + 1]);
-        }
-        fence_proxy_async_smem();
+        tmem_st_16x16(tP + 32 * (n & 1), p);
+        tmem_st_16x16(tP + 32 * (n & 1) + kUpper, p);
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(PFULL + (Place::of(2 * n).at >> 1)));
+        if (lane == 0) mbar_arrive(bar(PFULL + (n & 1)));
       }
       if (!ok) break;
       // all scores of the tile have been seen: the next one's Q may take this one's place
