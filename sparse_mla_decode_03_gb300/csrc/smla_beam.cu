@@ -322,21 +322,29 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
       m.state = kDone;
     } else {
       const float2* stats = a.stats + static_cast<int64_t>(row0 + b) * a.runs;
+      // the sums of runs in turn, at the maximum so far
       float top = -INFINITY, sum = 0.f;
       bool odd = false;
       for (int s = lane; s < a.runs; s += 32) {
         const float2 t = stats[s];
-        top = fmaxf(top, t.x);
         odd |= !(t.y < INFINITY);
+        const float most = fmaxf(top, t.x);
+        if (t.y > 0.f) {               // most is finite
+          float was, is;
+          exp_of(Two(top - most, t.x - most)).get(&was, &is);
+          sum = fmaf(t.y, is, sum * was);
+          top = most;
+        }
       }
+      float most = top;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      for (int s = lane; s < a.runs; s += 32) {
-        const float2 t = stats[s];
+      for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      if (sum > 0.f) {
         float w, none;
-        exp_of(Two(t.x - top, 0.f)).get(&w, &none);
-        if (t.y > 0.f) sum = fmaf(t.y, w, sum);
+        exp_of(Two(top - most, 0.f)).get(&w, &none);
+        sum *= w;
       }
+      top = most;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       bad |= __any_sync(0xffffffffu, odd);
@@ -386,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   const uint32_t key = sortable(mine);
   const uint32_t most = __reduce_max_sync(0xffffffffu, key);
   if (lane == 0) atomicMax(&top_key, most);
-  float border = unsortable(border_of(0u, 1u << 31, n, n, [&](uint32_t t) { return __syncthreads_count(key >= t); }));
+  float border = unsortable(border_of(0u, 1u << 31, n, n + n / 2, [&](uint32_t t) { return __syncthreads_count(key >= t); }));
   for (int i = tid; i < all; i += kThreads) {
     const int b = i % a.beams;
     const float x = maximum(i / a.beams, b);
@@ -452,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
       if (m > -INFINITY) mine = fmaxf(mine, low);
     });
     const uint32_t key = sortable(mine);
-    border = unsortable(border_of(0u, 1u << 31, n, n, [&](uint32_t t) { return __syncthreads_count(key >= t); }));
+    border = unsortable(border_of(0u, 1u << 31, n, n + n / 2, [&](uint32_t t) { return __syncthreads_count(key >= t); }));
     gather();
   }
   if (again()) {
