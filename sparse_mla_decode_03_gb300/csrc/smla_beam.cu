@@ -125,8 +125,10 @@ struct Bf16 {
   }
 };
 struct Fp16 {
-  static __device__ __forceinline__ float low(uint32_t w) { return __half2float(__ushort_as_half(static_cast<unsigned short>(w))); }
-  static __device__ __forceinline__ float high(uint32_t w) { return __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16))); }
+  static __device__ __forceinline__ float low(uint32_t w) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
+  }
+  static __device__ __forceinline__ float high(uint32_t w) { return low(w >> 16); }
   static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -492,9 +494,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
     const int b = static_cast<int>(c.place >> 32);
     a.parents[o] = c.value == 0 ? -1 : row0 + b;
     a.tokens[o] = c.value == 0 ? -1 : static_cast<int>(static_cast<uint32_t>(c.place));
-    const unsigned long long v = c.value;
-    a.out_scores[o] = v == 0 ? -INFINITY
-                             : static_cast<float>(__longlong_as_double(static_cast<long long>((v >> 63) ? v & ~(1ull << 63) : ~v)));
+    const unsigned long long bits = (c.value >> 63) ? c.value & ~(1ull << 63) : ~c.value;
+    a.out_scores[o] = c.value == 0 ? -INFINITY : static_cast<float>(__longlong_as_double(static_cast<long long>(bits)));
   };
   const Candidate none = {0, 0};
   // ranks list[0 .. found) and gives f(rank, candidate) the first n
@@ -511,7 +512,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   if (blocks <= kBlocks && found <= kList) {
     static_assert(kList <= kThreads, "a candidate a thread");
     Candidate mine = none;
-    if (tid < found) mine = candidate(key_value(list[tid].value), key_token(list[tid].value), static_cast<int>(list[tid].place));
+    if (tid < found)
+      mine = candidate(key_value(list[tid].value), key_token(list[tid].value), static_cast<int>(list[tid].place));
     // ranking compares all with all: first drop those whose upper half is not among the n largest
     const uint32_t upper = static_cast<uint32_t>(mine.value >> 32);
     bool in = tid < found;
@@ -539,7 +541,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
       for (int j = i + tid; j < all; j += kThreads) {
         const int b = j / a.steps, step = j - b * a.steps;
         const float x = maximum(step, b);
-        if (x == -INFINITY || !before(candidate(x, beam[b].state == kDone ? a.end_token : step * kStep<T>, b), best[n - 1])) continue;
+        const int token = beam[b].state == kDone ? a.end_token : step * kStep<T>;
+        if (x == -INFINITY || !before(candidate(x, token, b), best[n - 1])) continue;
         atomicMin(&next, j);
         break;
       }
@@ -596,7 +599,8 @@ int runs_of(const smla_beam_params* p) {
   double least = 1e300;
   for (const int each : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
     const int runs = (steps + each - 1) / each;
-    const double waves = static_cast<double>(rows) * runs / kSlots, cost = (2 * each + 1) * (waves > 1. ? waves : 1.) + each + runs / 24.;
+    const double waves = static_cast<double>(rows) * runs / kSlots;
+    const double cost = (2 * each + 1) * (waves > 1. ? waves : 1.) + each + runs / 24.;
     if (cost < least) {
       least = cost;
       best = runs;

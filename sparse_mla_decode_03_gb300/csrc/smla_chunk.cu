@@ -353,8 +353,10 @@ __global__ void __launch_bounds__(256) merge_kernel(const ChunkArgs a, const Chu
     const int n = p.even.blocks, y = blockIdx.y;
     const bool by_tile = a.B * p.even.tiles < kMaxSms;
     const int t = by_tile ? y : plan_begin<true>(p, y + 1) / n, from = t * n;
-    if (!by_tile && (plan_begin<true>(p, y + 1) >= p.even.line || plan_begin<true>(p, y + 1) == from || plan_begin<true>(p, y) > from))
-      return;
+    if (!by_tile) {
+      const int border = plan_begin<true>(p, y + 1);
+      if (border >= p.even.line || border == from || plan_begin<true>(p, y) > from) return;
+    }
     auto share = [&](int x) {        // the last that begins at block x or before: a border moves by less than a share
       int c = p.even.pieces > 0 ? x / n * p.even.pieces : x / p.even.per;
       while (c > 0 && plan_begin<true>(p, c) > x) --c;
@@ -476,7 +478,8 @@ size_t lay_out(const smla_chunk_params* p, char* base, ChunkPlan* plan) {
   // the tiles of sequences that all end inside one: no less than there are
   plan->few = !use_pairs(p) && p->batch <= kFewTiles &&
               (static_cast<int64_t>(p->total_q) * p->num_heads +
-               static_cast<int64_t>(p->batch) * (p->num_heads < kSingleRows ? kSingleRows - p->num_heads : 0)) / kSingleRows <= kFewTiles;
+               static_cast<int64_t>(p->batch) * (p->num_heads < kSingleRows ? kSingleRows - p->num_heads : 0)) /
+                      kSingleRows <= kFewTiles;
   auto take = [&](size_t bytes) {
     char* q = base + at;
     at += round256(bytes);
@@ -523,7 +526,8 @@ cudaError_t launch_pair_path(const ChunkArgs& a, const ChunkPlan& p, cudaStream_
   if (workers > kMaxPairs) workers = kMaxPairs;
   const int64_t blocks = p.cap_blocks + 1;
   const unsigned grid = 1 + static_cast<unsigned>(blocks < kMaxSms - 1 ? blocks : kMaxSms - 1);
-  e = launch_programmatic(is_row4(a.stride) ? expand_kernel<true> : expand_kernel<false>, dim3(grid), dim3(kPlanThreads), 0, s, a, p, kPairRows, workers);
+  e = launch_programmatic(is_row4(a.stride) ? expand_kernel<true> : expand_kernel<false>, dim3(grid), dim3(kPlanThreads), 0,
+                          s, a, p, kPairRows, workers);
   if (e != cudaSuccess) return e;
   e = launch_chunk_pair(a, p, workers, s);
   return e == cudaSuccess ? launch_merge(a, p, kPairRows, workers, s) : e;

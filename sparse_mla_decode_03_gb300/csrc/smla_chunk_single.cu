@@ -91,7 +91,9 @@ __device__ __forceinline__ uint32_t o_column(uint32_t tmem, int c) {
 // turn (a quarter may be a block ahead of another, and no more, since the third one's weights wait for the value
 // product that the other holds up); QFULL: a tile's Q in tensor memory; SFULL /
 // SEMPTY: scores of a block in tensor memory / taken by the softmax, two in turn; OEMPTY: results taken.
-enum Bar : int { FULL = 0, EMPTY = kPlaces, PFULL = 2 * kPlaces, QFULL = PFULL + 2, SFULL, SEMPTY = SFULL + 2, OEMPTY = SEMPTY + 2, kBars };
+enum Bar : int {
+  FULL = 0, EMPTY = kPlaces, PFULL = 2 * kPlaces, QFULL = PFULL + 2, SFULL, SEMPTY = SFULL + 2, OEMPTY = SEMPTY + 2, kBars
+};
 
 // A place of the ring, and the parity of its uses.
 struct Place {
@@ -130,9 +132,12 @@ struct Plan {
   const ChunkPlan& p;
   uint32_t smem;
   __device__ __forceinline__ bool few() const { return !is_even<EVEN>(p) && p.few; }
-  __device__ __forceinline__ int begin(int worker) const { return few() ? lds4(smem + kPlanShare) : plan_begin<EVEN>(p, worker); }
-  __device__ __forceinline__ int end(int worker) const { return few() ? lds4(smem + kPlanShare + 4) : plan_begin<EVEN>(p, worker + 1); }
-  __device__ __forceinline__ int start(int worker, int x) const { return few() ? lds4(smem + kPlanShare + 8) : plan_start<EVEN>(p, worker, x); }
+  // a worker's share and its first tile
+  __device__ __forceinline__ int begin(int w) const { return few() ? lds4(smem + kPlanShare) : plan_begin<EVEN>(p, w); }
+  __device__ __forceinline__ int end(int w) const { return few() ? lds4(smem + kPlanShare + 4) : plan_begin<EVEN>(p, w + 1); }
+  __device__ __forceinline__ int start(int w, int x) const {
+    return few() ? lds4(smem + kPlanShare + 8) : plan_start<EVEN>(p, w, x);
+  }
   __device__ __forceinline__ int cum(int t) const { return few() ? lds4(smem + kPlanCum + 4 * t) : plan_cum<EVEN>(p, t); }
   // sequence, first row, rows, first block
   __device__ __forceinline__ int4 tile(int t) const {
@@ -141,7 +146,9 @@ struct Plan {
     return make_int4(v.x & 255, v.y, v.x >> 8, v.w);
   }
   // positions of tile t's sequence b
-  __device__ __forceinline__ int len(int t, int b) const { return few() ? lds4(smem + kPlanOff + 16 * t + 8) : plan_len<EVEN>(a, p, b); }
+  __device__ __forceinline__ int len(int t, int b) const {
+    return few() ? lds4(smem + kPlanOff + 16 * t + 8) : plan_len<EVEN>(a, p, b);
+  }
 };
 
 // A row of the blocks on the line, walked tile by tile and each tile's share from its last
