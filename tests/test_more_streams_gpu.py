@@ -247,3 +247,33 @@ def test_refusals_of_tensors_on_the_gpu():
             except error:
                 continue
             pytest.fail(f"{error.__name__}: call {i} was taken")
+
+
+def test_calls_on_two_streams_at_once():
+    """Each call has a workspace of its own, so that calls in flight together do not meet."""
+    page, lens = 64, [5000, 12000, 700]
+    num_pages = sum(-(-L // page) for L in lens) + 4
+    pool, table = random_pool4(num_pages, page, 8), dev(tables(lens, page, num_pages, 8))
+    l, cu1, cu40 = dev(np.array(lens, np.int32)), dev(np.arange(4).astype(np.int32)), dev(40 * np.arange(4).astype(np.int32))
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q1, q40 = (torch.randn(n, 64, 512, generator=g, device="cuda").to(torch.bfloat16) for n in (3, 120))
+    idx = torch.randint(-1, pool.shape[0], (20, 1500), generator=g, device="cuda", dtype=torch.int32)
+    qs = torch.randn(20, 64, 512, generator=g, device="cuda").to(torch.bfloat16)
+    logits, scores = torch.randn(48, 60001, generator=g, device="cuda"), torch.randn(6, 8, generator=g, device="cuda")
+    jobs = [lambda: m.smla_chunk_attention(q1, pool, table, page, cu1, l, softmax_scale=SCALE, max_kv_tokens=sum(lens)),
+            lambda: m.smla_chunk_attention(q40, pool, table, page, cu40, l, softmax_scale=SCALE, max_kv_tokens=sum(lens)),
+            lambda: m.sparse_mla_decode(qs, pool, idx), lambda: m.smla_beam_select(logits, scores),
+            lambda: (m.smla_cache_read(pool, table, page, cu40, l, 120),)]
+    want = [[t.clone() for t in job()] for job in jobs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(6):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append([(i, jobs[i]()) for i in (range(len(jobs)) if k == 0 else reversed(range(len(jobs))))])
+    torch.cuda.synchronize()
+    for results in got:
+        for i, r in results:
+            for a, b in zip(r, want[i]):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
