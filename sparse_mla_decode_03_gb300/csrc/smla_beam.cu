@@ -449,7 +449,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   auto again = [&] {
     const bool many = blocks <= kBlocks && count > kList;
     __syncthreads();
-    if (many && tid == 0) count = 0;
+    if (many) {                    // the same in all threads
+      if (tid == 0) count = 0;
+      __syncthreads();             // before anyone counts again, whatever lies between
+    }
     return many;
   };
   if (again()) {
