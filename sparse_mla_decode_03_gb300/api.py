@@ -83,14 +83,31 @@ def make_params(batch: int, num_heads: int, topk: int, num_rows: int, kv_row_str
     return _lib.SmlaParams(batch, num_heads, topk, 0, num_rows, kv_row_stride, softmax_scale)
 
 
+def _row_stride(rows: torch.Tensor) -> int:
+    """Bytes between rows (a single row has no neighbour: any stride will do)."""
+    if rows.shape[0] > 1:
+        return rows.stride(0)
+    return ROW_BYTES if rows.shape[1] >= ROW_BYTES else ROW4_BYTES
+
+
+def _check_rows(name: str, rows: torch.Tensor) -> int:
+    """Checks a cache of rows, of 8- or 4-bit values by the bytes between them, which it returns.  Rows
+    that do not hold what their distance says, or reach into the next ones, would be read past their ends
+    or as the other kind."""
+    if rows.dim() != 2 or rows.dtype != torch.uint8 or rows.stride(1) != 1:
+        raise ValueError(f"{name} must be uint8 [num_rows, stride>=584] with unit column stride")
+    stride, width = _row_stride(rows), rows.shape[1]
+    if width < ROW4_BYTES or (stride > MAX_ROW4_STRIDE and width < ROW_BYTES) or (stride <= MAX_ROW4_STRIDE and
+                                                                                  rows.shape[0] > 1 and width > stride):
+        raise ValueError(f"{name} rows must hold 584 bytes, or 368 at most 512 bytes apart (4-bit values)")
+    return stride
+
+
 def _params_from(q: torch.Tensor, kv_cache: torch.Tensor, indices: torch.Tensor,
                  softmax_scale: float) -> _lib.SmlaParams:
     if q.dim() != 3 or q.shape[2] != QK or q.dtype != torch.bfloat16:
         raise ValueError("q must be bf16 [B, H, 512]")
-    if kv_cache.dim() != 2 or kv_cache.dtype != torch.uint8 or kv_cache.stride(1) != 1:
-        raise ValueError("kv_cache must be uint8 [num_rows, stride>=584] with unit column stride")
-    if kv_cache.stride(0) <= MAX_ROW4_STRIDE and kv_cache.shape[1] < ROW4_BYTES:
-        raise ValueError("kv_cache rows of 4-bit values must hold 368 bytes")
+    stride = _check_rows("kv_cache", kv_cache)
     if indices.dim() != 2 or indices.dtype != torch.int32 or indices.shape[0] != q.shape[0]:
         raise ValueError("indices must be int32 [B, topk]")
     for name, t in (("q", q), ("indices", indices)):
@@ -99,8 +116,7 @@ def _params_from(q: torch.Tensor, kv_cache: torch.Tensor, indices: torch.Tensor,
     if not (q.is_cuda and kv_cache.is_cuda and indices.is_cuda):
         raise ValueError("q, kv_cache and indices must be CUDA tensors")
     B, H, _ = q.shape
-    return make_params(B, H, indices.shape[1], kv_cache.shape[0], kv_cache.stride(0),
-                       softmax_scale)
+    return make_params(B, H, indices.shape[1], kv_cache.shape[0], stride, softmax_scale)
 
 
 def smla_default_num_splits(params: _lib.SmlaParams) -> int:
@@ -300,11 +316,7 @@ def _ints(name: str, t: torch.Tensor, dims: int, device: torch.device) -> None:
 
 
 def _pool(kv_pages: torch.Tensor, page_size: int) -> None:
-    if kv_pages.dim() != 2 or kv_pages.dtype != torch.uint8 or kv_pages.stride(1) != 1:
-        raise ValueError("kv_pages must be uint8 [num_rows, stride>=584] with unit column stride")
-    if kv_pages.shape[1] < ROW_BYTES and (kv_pages.shape[1] < ROW4_BYTES or kv_pages.shape[0] > 1
-                                          and kv_pages.stride(0) > MAX_ROW4_STRIDE):
-        raise ValueError("kv_pages rows must hold 584 bytes, or 368 at most 512 bytes apart (4-bit values)")
+    _check_rows("kv_pages", kv_pages)
     if not kv_pages.is_cuda:
         raise ValueError("kv_pages must be a CUDA tensor")
     if page_size < 1 or kv_pages.shape[0] < page_size:
@@ -328,13 +340,6 @@ def _adr(t: Optional[torch.Tensor]) -> int:
 def _on(device: torch.device):
     """The device as the current one for a call (no switch where it is already)."""
     return _SAME if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _row_stride(kv_pages: torch.Tensor) -> int:
-    """Bytes between rows (a single row has no neighbour: any stride will do)."""
-    if kv_pages.shape[0] > 1:
-        return kv_pages.stride(0)
-    return ROW_BYTES if kv_pages.shape[1] >= ROW_BYTES else ROW4_BYTES
 
 
 def make_cache_params(num_pages: int, page_size: int, num_seqs: int, max_pages: int,
