@@ -1057,6 +1057,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n >= 2) ok = warp_wait(bar(EMPTY + Place::of(2 * n - 3).at), Place::of(2 * n - 3).phase, stop, a.status);
         if (ok) ok = warp_wait(bar(SFULL + (n & 1)), (n >> 1) & 1, stop, a.status);
         if (!ok) break;
+        // also of a warp without rows: the tile's last scores are worked out before the next Q takes its place
+        tc_fence_after();
         if (idle) {
           if (lane == 0) {
             mbar_arrive(bar(SEMPTY + (n & 1)));
@@ -1064,7 +1066,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           continue;
         }
-        tc_fence_after();
         float v[16];
         tmem_ld_16x32(tS + 64 * (n & 1), v);
         tmem_wait_ld();
