@@ -327,6 +327,7 @@ int smla_paged_workspace_size(const smla_params* p, int32_t num_splits, size_t* 
   size_t total = 0;
   const int st = smla_workspace_size(p, num_splits, &total);
   if (st != SMLA_OK) return st;
+  if (bytes == nullptr) return SMLA_ERR_INVALID_ARG;
   if (four(p)) {
     *bytes = total;
     return SMLA_OK;

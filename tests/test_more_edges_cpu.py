@@ -1,8 +1,14 @@
 """Calls that need no GPU to be refused: pools whose rows cannot be what their distance says."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import sparse_mla_decode_03_gb300 as m
+
+from test_cache_cpu import lib  # noqa: F401
 
 
 def _pools():
@@ -49,3 +55,16 @@ def test_pools_of_one_row():
         with pytest.raises(ValueError, match="CUDA"):
             api._params_from(q, pool, i2, 1.0)
         assert api._row_stride(pool) == stride
+
+
+@pytest.mark.parametrize("stride,splits", [(368, 0), (584, 2)])
+def test_no_place_for_a_workspace_size(lib, stride, splits):  # noqa: F811
+    """A null pointer for the bytes is an error of the argument (in a process of its own)."""
+    code = f"""
+from ctypes import byref
+import sparse_mla_decode_03_gb300 as m
+from sparse_mla_decode_03_gb300 import _lib
+p = byref(m.make_params(2, 64, 128, 1000, {stride}))
+assert _lib.load().smla_paged_workspace_size(p, {splits}, None) == _lib.SMLA_ERR_INVALID_ARG"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    assert subprocess.run([sys.executable, "-c", code], cwd=root).returncode == 0
