@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(256) fork_apply_kernel(const ForkArgs a) {
   const int32_t* src = a.table + static_cast<int64_t>(p) * a.max_pages;
   if (blockIdx.y == 0) {
     int32_t* dst = a.table + static_cast<int64_t>(c) * a.max_pages;
-    for (int e = threadIdx.x; e < a.max_pages; e += blockDim.x) {
+    each_entry(a.max_pages, [&](int e) {
       int v = -1;
       if (e < full) {
         v = src[e];
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(256) fork_apply_kernel(const ForkArgs a) {
       if (v >= a.num_pages) report(a.status, SMLA_ERR_INDEX_RANGE);
       else if (v >= 0 && e < full) atomicAdd(a.ref + v, 1);
       dst[e] = v;
-    }
+    });
     if (threadIdx.x == 0) a.kv_lens[c] = len;
   }
   if (fresh < 0 || rem == 0) return;
@@ -193,17 +193,17 @@ __global__ void __launch_bounds__(256)
     return;
   }
   int32_t* e = table + static_cast<int64_t>(r) * max_pages;
-  for (int i = threadIdx.x; i < max_pages; i += blockDim.x) {
-    if (e[i] < 0) continue;
+  each_entry(max_pages, [&](int i) {
+    if (e[i] < 0) return;
     const int p = atomicExch(e + i, -1);   // a row listed twice gives its pages back once
-    if (p < 0) continue;
+    if (p < 0) return;
     if (p >= num_pages) {
       report(status, SMLA_ERR_INDEX_RANGE);
     } else if (atomicSub(ref + p, 1) <= 0) {
       atomicAdd(ref + p, 1);
       report(status, SMLA_ERR_INDEX_RANGE);
     }
-  }
+  });
   if (threadIdx.x == 0) kv_lens[r] = 0;
 }
 

@@ -121,6 +121,13 @@ __device__ __forceinline__ void take_free(int32_t* ref, const Part& p, int rank,
   });
 }
 
+// f(entry) for the entries of a row of the table, by the CTA's threads.  Unsigned, since the count behind
+// the last of nearly 2^31 entries is past an int.
+template <class F>
+__device__ __forceinline__ void each_entry(int max_pages, F f) {
+  for (uint32_t e = threadIdx.x; e < static_cast<uint32_t>(max_pages); e += blockDim.x) f(static_cast<int>(e));
+}
+
 // Copies rows from .. from + rows - 1 of the pool to to .. by the CTA's threads.  Rows that
 // follow one another without a gap go as 16-byte words where both ends allow it, four of a
 // thread's in flight.

@@ -188,27 +188,27 @@ __global__ void __launch_bounds__(256) reorder_apply_kernel(const ReorderArgs a)
   const int fresh = a.fresh[r];
   if (p < 0 || fresh == kNoPage) {
     if (blockIdx.y != 0) return;
-    for (int e = threadIdx.x; e < a.max_pages; e += blockDim.x) dst[e] = -1;
+    each_entry(a.max_pages, [&](int e) { dst[e] = -1; });
     if (threadIdx.x == 0) a.kv_lens[r] = 0;
     return;
   }
   const int32_t* src = a.old_table + static_cast<int64_t>(p) * a.max_pages;
   if (a.first[p] == r) {        // takes the row over as it is
     if (p == r || blockIdx.y != 0) return;
-    for (int e = threadIdx.x; e < a.max_pages; e += blockDim.x) dst[e] = src[e];
+    each_entry(a.max_pages, [&](int e) { dst[e] = src[e]; });
     if (threadIdx.x == 0) a.kv_lens[r] = a.old_lens[p];
     return;
   }
   const int len = parent_length(a, a.old_lens, p), full = len / a.page_size, rem = len % a.page_size;
   if (blockIdx.y == 0) {
-    for (int e = threadIdx.x; e < a.max_pages; e += blockDim.x) {
+    each_entry(a.max_pages, [&](int e) {
       int v = -1;
       if (e < full) v = src[e];
       else if (e == full && rem > 0) v = fresh >= 0 ? fresh : src[e];
       if (v >= a.num_pages) report(a.status, SMLA_ERR_INDEX_RANGE);
       else if (v >= 0 && e < full) atomicAdd(a.ref + v, 1);
       dst[e] = v;
-    }
+    });
     if (threadIdx.x == 0) {
       a.kv_lens[r] = len;
       if (a.old_lens[p] != len) report(a.status, SMLA_ERR_INDEX_RANGE);
