@@ -8,8 +8,9 @@
 // exponentials; they meet nobody and keep no candidates.  The second, a CTA a group, finds a border from
 // the maxima that at least num_out candidates reach and few steps do (bit by bit, a count of the CTA's
 // threads a bit), reads those few steps again, and ranks what reaches the border by counting.  Where too many
-// logits reach it (few steps, beams far apart), the border comes from those steps' logits; where too many are
-// equal, the steps that may hold something better are gone through one by one.
+// steps reach it (wide groups, of which few beams lead), the border comes from the steps' maxima themselves; where
+// too many logits do (few steps, beams far apart), from those steps' logits; and where too many are equal, the
+// steps that may hold something better are gone through one by one.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   __shared__ Beam beam[kMaxOut];
   __shared__ int count, blocks, next;
   __shared__ uint32_t top_key;
-  __shared__ int counts[32];                     // of the border's bits
+  __shared__ int counts[2][32];                  // of the border's bits: from the steps, from the logits
   __shared__ int block[kBlocks];                 // step * beams + beam
   __shared__ Candidate list[kStep<__half> + kMaxOut];
   __shared__ Candidate best[kMaxOut];
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   if (tid == 0) count = blocks = top_key = 0;
-  if (tid < 32) counts[tid] = 0;
+  if (tid < 64) counts[tid / 32][tid % 32] = 0;
   for (int b = warp; b < a.beams; b += kWarps) {
     const float score = a.scores[row0 + b];
     Beam m = {score, 0.0, 0.0, score, kDead};
@@ -397,15 +398,53 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   const uint32_t most = __reduce_max_sync(0xffffffffu, key);
   if (lane == 0) atomicMax(&top_key, most);
   float border = unsortable(border_of(0u, 1u << 31, n, n + n / 2, [&](uint32_t t) { return __syncthreads_count(key >= t); }));
-  for (int i = tid; i < all; i += kThreads) {
-    const int b = i % a.beams;
-    const float x = maximum(i / a.beams, b);
-    float low;
-    if (x == -INFINITY || nearly(x, b, &low) < border) continue;
-    const int at = atomicAdd(&blocks, 1);
-    if (at < kBlocks) block[at] = i;
+  auto list_steps = [&] {
+    for (int i = tid; i < all; i += kThreads) {
+      const int b = i % a.beams;
+      const float x = maximum(i / a.beams, b);
+      float low;
+      if (x == -INFINITY || nearly(x, b, &low) < border) continue;
+      const int at = atomicAdd(&blocks, 1);
+      if (at < kBlocks) block[at] = i;
+    }
+    __syncthreads();
+  };
+  list_steps();
+  // The bits in which the border and the best key are apart: t0, the ones above, and the first of them.
+  auto bits_apart = [&](uint32_t* t0) {
+    const uint32_t low = sortable(border), apart = low ^ top_key, bit = apart != 0 ? 1u << (31 - __clz(apart)) : 0u;
+    *t0 = bit != 0 ? low & ~(2 * bit - 1) : low;
+    return bit;
+  };
+  if (blocks > kBlocks) {
+    // Few threads hold the best (of many beams each thread has one beam's steps, so that the best beams' maxima are
+    // few), or fewer than n anything at all: the border from the steps themselves.  64 results of 4 groups of 64 beams
+    // far apart, 131,072 bf16 logits: 133 us, and 6,700 step by step; of 64 beams of which one is alive, 2^19 fp32
+    // logits: 450 and 6,300.
+    uint32_t t0;
+    int pass = 0;
+    const uint32_t bit = bits_apart(&t0);
+    border = unsortable(border_of(t0, bit, n, n + n / 2, [&](uint32_t t) {
+      int c = 0;
+      for (int i = tid; i < all; i += kThreads) {
+        const int b = i % a.beams;
+        const float x = maximum(i / a.beams, b);
+        float low;
+        nearly(x, b, &low);
+        c += x > -INFINITY && sortable(low) >= t;
+      }
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0 && c > 0) atomicAdd(&counts[0][pass], c);
+      __syncthreads();
+      return counts[0][pass++];
+    }));
+    if (bit != 0) {
+      __syncthreads();
+      if (tid == 0) blocks = 0;
+      __syncthreads();
+      list_steps();
+    }
   }
-  __syncthreads();
   // f(beam, held logits, token of the lane's word 0) for the warp's blocks
   auto each_block = [&](auto f) {
     for (int j = warp; j < min(blocks, kBlocks); j += kWarps) {
@@ -471,9 +510,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   if (again()) {
     // or from the logits themselves
     int pass = 0;
-    const uint32_t low = sortable(border), apart = low ^ top_key;
-    const uint32_t bit = apart != 0 ? 1u << (31 - __clz(apart)) : 0u;
-    border = unsortable(border_of(bit != 0 ? low & ~(2 * bit - 1) : low, bit, n, kList / 2, [&](uint32_t t) {
+    uint32_t t0;
+    const uint32_t bit = bits_apart(&t0);
+    border = unsortable(border_of(t0, bit, n, kList / 2, [&](uint32_t t) {
       const float value = unsortable(t);
       int c = 0;
       each_block([&](int b, const Held<T>& x, int) {
@@ -486,9 +525,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
         for (int i = 0; i < kEach<T>; ++i) c += x.at(i) >= least;
       });
       c = __reduce_add_sync(0xffffffffu, c);
-      if (lane == 0 && c > 0) atomicAdd(counts + pass, c);
+      if (lane == 0 && c > 0) atomicAdd(&counts[1][pass], c);
       __syncthreads();
-      return counts[pass++];
+      return counts[1][pass++];
     }));
     gather();
   }

@@ -1,11 +1,14 @@
-"""smla_beam_select where many candidates are equal, against the definition in 64 bits (tolerances:
-_rows4_helpers).  Sums are whole numbers here, and powers of two, so that ties are exact."""
+"""smla_beam_select where many candidates are equal, and over wide groups, against the definition in 64
+bits (tolerances: _rows4_helpers).  Where candidates are equal, sums are whole numbers and powers of two,
+so that ties are exact."""
 import math
 
 import pytest
 import torch
 
-from test_beam_gpu import _check
+import sparse_mla_decode_03_gb300 as m
+
+from test_beam_gpu import _check, _logits
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +41,51 @@ def test_constant_rows_beside_finished_beams(dtype):
     scores = torch.where(done == 1, -math.log(V), 0.0).float()
     for n in (2, 24, 64):
         _check(logits, scores, n, done.view(-1), 7)
+
+
+@pytest.mark.parametrize("G,K,n,V,dtype", [
+    (2, 64, 64, 131072, torch.bfloat16), (2, 32, 64, 131072, torch.float32), (1, 64, 64, 131072, torch.float16),
+    (2, 48, 33, 100001, torch.float32), (3, 16, 64, 262143, torch.float32),
+])
+def test_wide_groups_whose_beams_are_far_apart(G, K, n, V, dtype):
+    """The best come from a few beams, nearly all of whose steps reach a border that few threads' maxima
+    make."""
+    logits, scores = _logits(G, K, V, V + K, dtype)
+    _check(logits, scores * 4, n)
+    done = torch.zeros(G, K, dtype=torch.uint8, device="cuda")
+    done[:, 5::9] = 1
+    _check(logits, scores * 4, n, done.view(-1), 3)
+
+
+@pytest.mark.parametrize("V,dtype", [(1 << 19, torch.float32), (1 << 20, torch.bfloat16), ((1 << 18) + 513, torch.float32)])
+@pytest.mark.parametrize("K,alive", [(64, 0), (64, 63), (32, 7)])
+def test_the_first_step_of_a_wide_group(K, alive, V, dtype):
+    """One beam is alive, so that fewer threads than results hold anything."""
+    logits, scores = _logits(1, K, V, V + K, dtype)
+    scores = torch.full_like(scores, -math.inf)
+    scores[0, alive] = -0.5
+    _check(logits, scores, 64)
+    up = torch.linspace(-9, 9, V, device="cuda").to(dtype)
+    logits[alive] = up
+    _check(logits, scores, 64)
+    logits[alive] = up.flip(0)
+    _check(logits, scores, 64)
+
+
+@pytest.mark.parametrize("K,V,dtype", [(64, 131072, torch.bfloat16), (32, 131072, torch.float32)])
+def test_wide_groups_are_not_gone_through_step_by_step(K, V, dtype):
+    """Beams far apart cost no more than five times what beams side by side do (it was a hundred)."""
+    logits, scores = _logits(4, K, V, K, dtype)
+
+    def least(c):
+        times = []
+        for _ in range(6):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            m.smla_beam_select(logits, c, 64)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    assert least(scores * 4) < 5 * least(scores * 0.05)
