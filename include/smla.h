@@ -444,8 +444,10 @@ int smla_cache_reorder(void* kv_pages, int32_t* ref_count, int32_t* block_table,
  * A logit of -infinity is no candidate, nor is any of a beam whose score is -infinity; where a group has
  * fewer than num_out candidates, the rest are (-1, -1, -infinity).  A beam with a NaN or a +infinity
  * among its logits, or a score that is NaN or +infinity, has none (SMLA_ERR_RANGE).
- * Logits are compared as they are; sums are held in 32 bits and values in 64 (a value is off by about
- * 1e-7 before it is rounded).  The same call gives the same bits every time.
+ * Logits are compared as they are; sums are held in 32 bits and values in 64.  A beam's logarithm, and
+ * with it all of its values alike, is off by 1e-7 to 3e-7 as a rule and by less than 2^-14 whatever the
+ * logits are: candidates of different beams whose values are closer than that may change places, those
+ * of one beam do not.  The same call gives the same bits every time.
  */
 enum smla_logits_type { SMLA_FLOAT32 = 0, SMLA_BFLOAT16 = 1, SMLA_FLOAT16 = 2 };
 typedef struct smla_beam_params {
