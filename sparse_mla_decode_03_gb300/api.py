@@ -83,22 +83,16 @@ def make_params(batch: int, num_heads: int, topk: int, num_rows: int, kv_row_str
     return _lib.SmlaParams(batch, num_heads, topk, 0, num_rows, kv_row_stride, softmax_scale)
 
 
-def _row_stride(rows: torch.Tensor) -> int:
-    """Bytes between rows (a single row has no neighbour: any stride will do)."""
-    if rows.shape[0] > 1:
-        return rows.stride(0)
-    return ROW_BYTES if rows.shape[1] >= ROW_BYTES else ROW4_BYTES
-
-
 def _check_rows(name: str, rows: torch.Tensor) -> int:
-    """Checks a cache of rows, of 8- or 4-bit values by the bytes between them, which it returns.  Rows
-    that do not hold what their distance says, or reach into the next ones, would be read past their ends
-    or as the other kind."""
-    if rows.dim() != 2 or rows.dtype != torch.uint8 or rows.stride(1) != 1:
+    """Checks a cache of rows, of 8- or 4-bit values by the bytes between them, which it returns (a
+    single row has no neighbour: its width tells).  Rows that do not hold what their distance says, or reach
+    into the next ones, would be read past their ends or as the other kind."""
+    shape, strides = rows.shape, rows.stride()
+    if len(shape) != 2 or rows.dtype != torch.uint8 or strides[1] != 1:
         raise ValueError(f"{name} must be uint8 [num_rows, stride>=584] with unit column stride")
-    stride, width = _row_stride(rows), rows.shape[1]
-    if width < ROW4_BYTES or (stride > MAX_ROW4_STRIDE and width < ROW_BYTES) or (stride <= MAX_ROW4_STRIDE and
-                                                                                  rows.shape[0] > 1 and width > stride):
+    num, width = shape
+    stride = strides[0] if num > 1 else ROW_BYTES if width >= ROW_BYTES else ROW4_BYTES
+    if width < ROW4_BYTES or (width < ROW_BYTES if stride > MAX_ROW4_STRIDE else num > 1 and width > stride):
         raise ValueError(f"{name} rows must hold 584 bytes, or 368 at most 512 bytes apart (4-bit values)")
     return stride
 
@@ -315,12 +309,14 @@ def _ints(name: str, t: torch.Tensor, dims: int, device: torch.device) -> None:
         raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} dimension(s) on {device}")
 
 
-def _pool(kv_pages: torch.Tensor, page_size: int) -> None:
-    _check_rows("kv_pages", kv_pages)
+def _pool(kv_pages: torch.Tensor, page_size: int) -> int:
+    """Checks a pool of pages; the bytes between its rows."""
+    stride = _check_rows("kv_pages", kv_pages)
     if not kv_pages.is_cuda:
         raise ValueError("kv_pages must be a CUDA tensor")
     if page_size < 1 or kv_pages.shape[0] < page_size:
         raise ValueError("kv_pages must hold a page of page_size >= 1 rows")
+    return stride
 
 
 def _stream_on(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
@@ -391,7 +387,7 @@ def _rows_of_heads(name: str, t: torch.Tensor, tokens: int, width: int, device: 
 
 def _token_places(kv_pages: torch.Tensor, page_size: int, block_table: torch.Tensor, cu_q: torch.Tensor,
                   kv_lens: torch.Tensor) -> _lib.SmlaCacheParams:
-    _pool(kv_pages, page_size)
+    row_stride = _pool(kv_pages, page_size)
     dev = kv_pages.device
     _ints("block_table", block_table, 2, dev)
     _ints("cu_q", cu_q, 1, dev)
@@ -400,7 +396,7 @@ def _token_places(kv_pages: torch.Tensor, page_size: int, block_table: torch.Ten
     if cu_q.shape[0] != B + 1 or kv_lens.shape[0] != B:
         raise ValueError("cu_q must be [B + 1] and kv_lens [B] for a block_table of B rows")
     return make_cache_params(kv_pages.shape[0] // page_size, page_size, B, block_table.shape[1],
-                             _row_stride(kv_pages))
+                             row_stride)
 
 
 def smla_cache_append(kv: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor,
@@ -509,14 +505,14 @@ def smla_cache_reserve(page_size: int, ref_count: torch.Tensor, block_table: tor
 
 def _page_state(kv_pages: torch.Tensor, page_size: int, ref_count: torch.Tensor,
                 block_table: torch.Tensor) -> _lib.SmlaCacheParams:
-    _pool(kv_pages, page_size)
+    row_stride = _pool(kv_pages, page_size)
     dev = kv_pages.device
     _ints("ref_count", ref_count, 1, dev)
     _ints("block_table", block_table, 2, dev)
     if ref_count.shape[0] * page_size > kv_pages.shape[0]:
         raise ValueError("ref_count has more pages than kv_pages")
     return make_cache_params(ref_count.shape[0], page_size, block_table.shape[0], block_table.shape[1],
-                             _row_stride(kv_pages))
+                             row_stride)
 
 
 def smla_cache_fork(kv_pages: torch.Tensor, page_size: int, ref_count: torch.Tensor,
@@ -741,7 +737,7 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
     kv_lens (default: what the table can hold, 2^30 at most); from 256 rows of q (tokens times
     heads) a sequence on it sizes the workspace, 1,025 bytes a token, so a caller with a wide
     table gives the bound that it knows.  Returns (out bf16 [T, H, 448], lse fp32 [T, H])."""
-    _pool(kv_pages, page_size)
+    row_stride = _pool(kv_pages, page_size)
     dev = kv_pages.device
     if q.dim() != 3 or q.shape[2] != QK or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.device != dev:
         raise ValueError(f"q must be contiguous bf16 [T, H, 512] on {dev}")
@@ -771,7 +767,7 @@ def smla_chunk_attention(q: torch.Tensor, kv_pages: torch.Tensor, block_table: t
         raise ValueError(f"lse must be contiguous fp32 [{T}, {H}] on {dev}")
     if max_kv_tokens is None:
         max_kv_tokens = min(B * max_pages * page_size, MAX_KV_TOKENS)
-    p = make_chunk_params(B, H, T, page_size, max_pages, kv_pages.shape[0], _row_stride(kv_pages),
+    p = make_chunk_params(B, H, T, page_size, max_pages, kv_pages.shape[0], row_stride,
                           max_kv_tokens, softmax_scale, logit_cap)
     if workspace is None:
         workspace = _empty(side, _chunk_bytes(B, H, T, p.kv_row_stride, max_kv_tokens), torch.uint8, dev)

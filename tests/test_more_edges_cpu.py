@@ -54,7 +54,7 @@ def test_pools_of_one_row():
                          (torch.zeros(2000, dtype=torch.uint8).as_strided((1, 584), (16, 1)), 584)):
         with pytest.raises(ValueError, match="CUDA"):
             api._params_from(q, pool, i2, 1.0)
-        assert api._row_stride(pool) == stride
+        assert api._check_rows("pool", pool) == stride
 
 
 @pytest.mark.parametrize("stride,splits", [(368, 0), (584, 2)])
