@@ -97,7 +97,7 @@ __device__ __forceinline__ uint4 shfl_xor(const uint4& x, int mask) {
 // each of which a lane reads before it writes there, and no other lane: q_rope may be q's own columns).  Bound by
 // memory: 16 heads a token are 2,048 bytes in and out beside the row's 1,608; 65,536 tokens take 62 us (374 MB, 6.0
 // TB/s, 89 % of the measured copy rate).  Products and sums in 32 bits, one rounding to bf16, so that a rotation by
-// nothing changes no bit.  A step's call (96 tokens of 64 heads) is a launch and three trips to memory (offsets,
+// nothing changes no finite value but a zero's sign (beside a partner below 0).  A step's call (96 tokens of 64 heads) is a launch and three trips to memory (offsets,
 // lengths, then the table's row), 5 us.
 template <bool ROW4, bool NEIGHBOURS>
 __global__ void __launch_bounds__(256) append_rotary_kernel(const AppendArgs a, const RotaryArgs r) {

@@ -209,9 +209,9 @@ __device__ __forceinline__ void load_step(const T* base, int first, int vocab, H
 
 // BYTES: of a load, what the start of every row is aligned to.  Which lane adds which logits goes by
 // their place in the row alone, so that equal rows have equal sums, and ties are ties.
-// Bound by memory: 2 KB a warp is on its way, 54 KB an SM.  Nine tenths of 512 rows of 131,072 bf16 logits (the others
-// have ended; 121 MB): 26 us, 4.6 TB/s, with the start (issue slots 60 %, exponentials 31 % of their pipe).
-// 256 rows: 32 us with both launches at 16 bytes a load, 34 at 4 and 40 at 2.
+// Bound by memory: 2 KB a warp is on its way, 56 KB an SM (28 warps of 64 at work).  Nine tenths of 512 rows of 131,072
+// bf16 logits (the others have ended; 121 MB): 24.8 us, 4.9 TB/s, with the start (issue slots 60 %, exponentials 31 % of
+// their pipe).  256 rows: 25.5 us with both launches at 16 bytes a load, 29.9 at 4 and 34.1 at 2 (replayed graphs).
 template <class T, int BYTES>
 __global__ void __launch_bounds__(kRunWarps * 32, 8) run_kernel(const BeamArgs a) {
   constexpr int kPer = BYTES / sizeof(T);
@@ -299,7 +299,7 @@ __device__ __forceinline__ bool before(const Candidate& a, const Candidate& b) {
 }
 
 // A CTA a group.  Bound by latency: sums, logarithm, maxima, the border's bits (a barrier each), steps, ranks, each
-// waiting for the one before: 11 us for 4 beams of 32,000, 15 for 64 groups of 8 of 131,072.
+// waiting for the one before: 9.7 us for 4 beams of 32,000, 12.4 for 64 groups of 8 of 131,072.
 template <class T, int BYTES>
 __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   constexpr int kPer = BYTES / sizeof(T);

@@ -465,6 +465,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // Over 4-bit rows, which cost the single kernel less, from more than a full tile: of 64 heads, 4 x 4 tokens of 1,001
 // 24.7 and 26.8, 16 x 4 of 16,000 183 and 199, 32 x 4 of 500 39.1 and 34.8; 4 x 5 of 1,001 30.8 and 28.7, 3 x 5 of
 // 19,717 70 and 81, 8 x 8 of 4,000 67 and 60; 16 x 16 of 16 heads and 8,000 106 and 116.
+// The length decides too, which the rule does not look at: 3 x 5 of 19,717 and 32 x 4 of 500 are on their slower side.
 // All of batches whose sequences bring the same number of tokens; mixed ones are not measured.
 bool use_pairs(const smla_chunk_params* p) {
   const int64_t rows = static_cast<int64_t>(p->total_q) * p->num_heads, full = static_cast<int64_t>(kPairRows) * p->batch;
@@ -572,7 +573,8 @@ int launch_sparse4(const void* q, const void* kv, const int32_t* indices, const 
   const int per = share > kMinShare ? share : kMinShare;
   // Shares that end with their tiles, some SMs left over, or shares along the line, whose change of tile costs as
   // much as kTileChange blocks (13,000 cycles: Q, and results that the next tile's scores wait for).  32 queries
-  // of 2,048 and 64 heads: 4 shares of 8 blocks each, or 152 of 7; 96 of 999 and 16 heads: one of 16, or 152 of 11.
+  // of 2,048 and 64 heads: 4 shares of 8 blocks each (taken: 29.6 us, 32.7 along the line), or 147 of 7; 96 of 999 and 16
+  // heads: one of 16, or 140 of 11 (taken: 16 is more than 11 + 4; the other is not measured).
   constexpr int kTileChange = 4;
   int pieces = p->batch * tiles <= kMaxSms ? kMaxSms / (p->batch * tiles) : 0;
   if (pieces > (blocks + 1) / kMinShare) pieces = (blocks + 1) / kMinShare;
